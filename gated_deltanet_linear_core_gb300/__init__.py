@@ -27,7 +27,7 @@ __all__ = [
     "gdn_layer_prefill_host", "gdn_decode_step", "gdn_decode_verify", "gdn_layer_prefill",
     "gdn_layer_prefill_workspace_size", "gdn_layer_prefill_launches", "gdn_chunk_prefill_norm",
     "HeadShard", "head_shard",
-    "gdn_layer_decode",
+    "gdn_layer_decode", "gdn_kv_append", "gdn_attn_decode", "gdn_attn_decode_workspace_size", "gdn_draft_accept",
     "library_path",
 ]
 
@@ -527,6 +527,135 @@ def gdn_layer_decode(x, z, a, b, conv_w, A_log, dt_bias, norm_w, dims, state, co
     y = gdn_conv1d_update(x, conv_w, conv_state, dims, True, stream=stream)
     o = gdn_recurrent_decode(y, state, dims, a, b, A_log, dt_bias, scale=scale, stream=stream)
     return gdn_rmsnorm_gated(o, z, norm_w, dims, stream=stream)
+
+
+def _one_device(first, *rest):
+    """The device of the tensors (None among them is skipped); they must share it."""
+    dev = first.device
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices ({dev} and {t.device})")
+    return dev
+
+
+def _call_on(dev, stream, body):
+    """body(raw stream) with `dev` current and, where the caller names a stream,
+    that stream current too, so that outputs and workspaces allocated in body
+    belong to the stream that uses them."""
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be CUDA tensors (got {dev})")
+    if stream is None and torch.cuda.current_device() == dev.index:
+        return body(torch.cuda.current_stream(dev).cuda_stream)
+    with torch.cuda.device(dev):
+        if stream is None:
+            return body(torch.cuda.current_stream(dev).cuda_stream)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), dev) if int(stream) else torch.cuda.default_stream(dev)
+        with torch.cuda.stream(stream):
+            return body(stream.cuda_stream)
+
+
+def _cache_dims(k_cache, v_cache, page_table, seq_lens):
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache, v_cache: expected [n_pages, H_kv, page_size, D], both alike")
+    if page_table.dim() != 2 or seq_lens.dim() != 1 or seq_lens.shape[0] != page_table.shape[0]:
+        raise ValueError("page_table: expected [B, max_pages]; seq_lens: [B]")
+    return tuple(k_cache.shape) + tuple(page_table.shape)
+
+
+def gdn_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, stream=None):
+    """Writes new tokens' keys and values k, v [T, H_kv, D] into the pages of
+    k_cache, v_cache [n_pages, H_kv, page_size, D] (in place).  The L_b new tokens
+    of sequence b (cu_seqlens int32 [B + 1], or T / B each) end at position
+    seq_lens[b] (int32 [B], new tokens counted); page_table int32 [B, max_pages].
+    Returns (k_cache, v_cache)."""
+    dt = k.dtype
+    n_pages, H, ps, D, B, mp = _cache_dims(k_cache, v_cache, page_table, seq_lens)
+    if k.dim() != 3:
+        raise ValueError("k: expected [T, H_kv, D]")
+    T = int(k.shape[0])
+    if cu_seqlens is not None and tuple(cu_seqlens.shape) != (B + 1,):
+        raise ValueError(f"cu_seqlens: shape {tuple(cu_seqlens.shape)}, expected {(B + 1,)}")
+    dev = _one_device(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens)
+    st = _call_on(dev, stream, lambda s: _lib.load().gdn_kv_append(
+        _ptr(k, "k", dt, (T, H, D)), _ptr(v, "v", dt, (T, H, D)), _ptr(k_cache, "k_cache", dt),
+        _ptr(v_cache, "v_cache", dt), _ptr(page_table, "page_table", torch.int32),
+        _ptr(seq_lens, "seq_lens", torch.int32), _ptr(cu_seqlens, "cu_seqlens", torch.int32), B, T, H, D, ps,
+        n_pages, mp, _dtype_code(k), s))
+    _lib.check(st, "gdn_kv_append")
+    return k_cache, v_cache
+
+
+def gdn_attn_decode_workspace_size(B: int, K: int, H_q: int, H_kv: int, D: int, page_size: int, dtype) -> int:
+    code = _lib.GDN_BF16 if dtype == torch.bfloat16 else _lib.GDN_F32
+    return int(_lib.load().gdn_attn_decode_workspace_size(int(B), int(K), int(H_q), int(H_kv), int(D),
+                                                          int(page_size), code))
+
+
+def gdn_attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=0.0, gate=None, out=None, lse=None,
+                    return_lse=False, workspace=None, stream=None):
+    """Softmax attention of the K newest tokens (q [B, K, H_q, D], causal among
+    themselves) over the paged cache, their own keys and values included
+    (gdn_kv_append); K = 1 is a decode step, K up to 16 a verification pass.
+    gate [B, K, H_q, D]: out = attention * sigmoid(gate).  Returns out
+    [B, K, H_q, D], with return_lse also lse [B, K, H_q] f32."""
+    dt = q.dtype
+    n_pages, H, ps, D, B, mp = _cache_dims(k_cache, v_cache, page_table, seq_lens)
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [{B}, K, H_q, {D}]")
+    K, H_q = int(q.shape[1]), int(q.shape[2])
+    shape = (B, K, H_q, D)
+    dev = _one_device(q, k_cache, v_cache, page_table, seq_lens, gate, out, lse, workspace)
+    lib, code = _lib.load(), _dtype_code(q)
+
+    def body(s):
+        o = torch.empty_like(q) if out is None else out
+        e = torch.empty(shape[:3], dtype=torch.float32, device=dev) if lse is None and return_lse else lse
+        ws = workspace
+        if ws is None:
+            need = lib.gdn_attn_decode_workspace_size(B, K, H_q, H, D, ps, code)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        st = lib.gdn_attn_decode(
+            _ptr(q, "q", dt), _ptr(k_cache, "k_cache", dt), _ptr(v_cache, "v_cache", dt),
+            _ptr(page_table, "page_table", torch.int32), _ptr(seq_lens, "seq_lens", torch.int32), float(scale),
+            _ptr(gate, "gate", dt, shape), _ptr(o, "out", dt, shape), _ptr(e, "lse", torch.float32, shape[:3]),
+            B, K, H_q, H, D, ps, n_pages, mp, _ptr(ws, "workspace"), ws.numel() * ws.element_size(), code, s)
+        _lib.check(st, "gdn_attn_decode")
+        return (o, e) if return_lse else o
+
+    return _call_on(dev, stream, body)
+
+
+def gdn_draft_accept(target_probs, draft_probs, draft_tokens, uniforms, n_draft=None, slots=None, n_accept=None,
+                     tokens=None, next_slot=None, stream=None):
+    """Speculative sampling from given uniforms [B, K + 1]: which of the drafted
+    tokens [B, K] hold under target_probs [B, K + 1, V] and draft_probs [B, K, V]
+    (None: drafts that were not sampled), and the token after them.  n_draft [B]:
+    drafts per sequence (None: K).  slots [B, K + 2]: the slots of the
+    gdn_decode_verify call over the K + 1 tokens.  Returns (n_accept [B], tokens
+    [B, K + 1]: held drafts, next token, then -1; next_slot [B]: slots[b, n + 1],
+    None without slots), all int32."""
+    dt = target_probs.dtype
+    if target_probs.dim() != 3 or target_probs.shape[1] < 1:
+        raise ValueError("target_probs: expected [B, K + 1, V]")
+    B, K, V = int(target_probs.shape[0]), int(target_probs.shape[1]) - 1, int(target_probs.shape[2])
+    dev = _one_device(target_probs, draft_probs, draft_tokens, uniforms, n_draft, slots, n_accept, tokens, next_slot)
+
+    def body(s):
+        i32 = torch.int32
+        n = torch.empty(B, dtype=i32, device=dev) if n_accept is None else n_accept
+        tk = torch.empty((B, K + 1), dtype=i32, device=dev) if tokens is None else tokens
+        ns = torch.empty(B, dtype=i32, device=dev) if next_slot is None and slots is not None else next_slot
+        st = _lib.load().gdn_draft_accept(
+            _ptr(target_probs, "target_probs", dt), _ptr(draft_probs, "draft_probs", dt, (B, K, V)),
+            _ptr(draft_tokens, "draft_tokens", i32, (B, K)), _ptr(uniforms, "uniforms", torch.float32, (B, K + 1)),
+            _ptr(n_draft, "n_draft", i32, (B,)), _ptr(slots, "slots", i32, (B, K + 2)), B, K, V,
+            _ptr(n, "n_accept", i32, (B,)), _ptr(tk, "tokens", i32, (B, K + 1)), _ptr(ns, "next_slot", i32, (B,)),
+            _dtype_code(target_probs), s)
+        _lib.check(st, "gdn_draft_accept")
+        return n, tk, ns
+
+    return _call_on(dev, stream, body)
 
 
 @dataclass(frozen=True)

@@ -75,6 +75,10 @@ SIGNATURES = {
     "gdn_decode_step": (ST, [P, P, P, P, P, P, P, P, P, P, F32, P, I32, F32, U32, P, Dims, ST, P]),
     "gdn_decode_verify": (ST, [P, P, P, P, P, P, P, P, P, P, F32, P, I32, I32, F32, U32, P, Dims, ST,
                                P]),
+    "gdn_kv_append": (ST, [P, P, P, P, P, P, P, I32, I64, I32, I32, I32, I32, I32, ST, P]),
+    "gdn_attn_decode_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32, ST]),
+    "gdn_attn_decode": (ST, [P, P, P, P, P, F32, P, P, P, I32, I32, I32, I32, I32, I32, I32, I32, P, SZ, ST, P]),
+    "gdn_draft_accept": (ST, [P, P, P, P, P, P, I32, I32, I32, P, P, P, ST, P]),
 }
 
 _lock = threading.Lock()

@@ -1,0 +1,153 @@
+// Work division shared by the paged-cache attention kernels (attn_ffma.cu,
+// attn_tc.cu) and the kernel that joins their partial results.
+//
+// An item is (sequence b, key-value head h, row block rb): a block of the
+// sequence's K*G query rows that share h (G = H_q / H_kv; row r is new token
+// r / G, query head h*G + r % G).  An item's units are its tiles of `tile`
+// cached tokens, at least one (an empty sequence still has rows to write).
+// All units of a call, item after item, are cut into equal contiguous ranges,
+// one per CTA, whatever the lengths are: the lengths stay on the device, so
+// the host never waits for them and a captured graph follows them.  A CTA that
+// covers an item whole writes its rows; otherwise it leaves the running
+// maximum, sum and unnormalised output in one of its two workspace slots
+// (its range starts inside an item: slot 2c; ends inside another: 2c + 1),
+// and attn_join_kernel combines the slots in CTA order.
+#pragma once
+
+#include <math.h>
+
+#include "gdn_common.cuh"
+#include "gdn_launch.h"
+
+namespace gdn {
+namespace attn {
+
+__device__ __forceinline__ int clamped_len(const AttnArgs& a, int b) {
+    const int64_t cap = (int64_t)a.max_pages * a.page_size;
+    const int n = a.lens[b];
+    return n < 0 ? 0 : (n > cap ? (int)cap : n);
+}
+__device__ __forceinline__ int units_of(int len, int tile) { return len <= tile ? 1 : (len - 1) / tile + 1; }
+
+// First unit of CTA c of n.
+__host__ __device__ __forceinline__ int64_t cta_begin(int64_t total, int c, int n) { return total * c / n; }
+// The CTA whose range holds unit u.
+__device__ __forceinline__ int cta_of(int64_t total, int64_t u, int n) { return (int)(((u + 1) * n - 1) / total); }
+
+struct Place {
+    int64_t total;  // units of the whole call
+    int64_t first;  // first unit of sequence b's items
+    int b, len;     // the sequence that holds the unit asked for, its clamped length
+};
+
+// Units of the call and the sequence that holds the first unit of CTA c of the
+// n that take part (n is capped so that a CTA has at least min_units).  All
+// NT threads call it; `sh` holds NT + 4 values.
+template <int NT>
+__device__ __forceinline__ Place find_place(const AttnArgs& a, int tile, int c, int& n, int64_t* sh) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = (a.B + NT - 1) / NT;
+    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    const int64_t mult = (int64_t)a.H_kv * a.n_rb;
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += units_of(clamped_len(a, b), tile);
+    int64_t inc = mine;  // inclusive scan over the threads
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) sh[warp] = inc;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        const int64_t v = sh[w];
+        if (w < warp) before += v;
+        all += v;
+    }
+    inc += before;
+    Place p;
+    p.total = all * mult;
+    const int64_t most = (p.total + a.min_units - 1) / a.min_units;
+    if (n > most) n = (int)most;
+    __syncthreads();
+    if (c < n) {
+        const int64_t want = cta_begin(p.total, c, n);
+        int64_t lo = (inc - mine) * mult;
+        if (want >= lo && want < inc * mult) {
+            int b = b0;
+            int len = clamped_len(a, b);
+            for (;;) {
+                const int64_t next = lo + units_of(len, tile) * mult;
+                if (want < next) break;
+                lo = next;
+                len = clamped_len(a, ++b);
+            }
+            sh[0] = lo;
+            sh[1] = ((int64_t)len << 32) | (uint32_t)b;
+        }
+    }
+    __syncthreads();
+    p.first = sh[0];
+    p.b = (int)(uint32_t)(sh[1] & 0xffffffff);
+    p.len = (int)(sh[1] >> 32);
+    __syncthreads();
+    return p;
+}
+
+// The segments (parts of items) of one CTA's unit range, in order.
+struct Segment {
+    int b, h, rb, len;   // item
+    int tile0, tile1;    // its tiles [tile0, tile1) of this segment
+    int tiles;           // tiles of the whole item
+    bool first;          // starts where the CTA's range starts
+};
+struct Walk {
+    int64_t at, end, begin, item0;  // units; item0: first unit of sequence b's items
+    int b, len;
+    __device__ __forceinline__ Walk(const Place& p, int64_t lo, int64_t hi)
+        : at(lo), end(hi), begin(lo), item0(p.first), b(p.b), len(p.len) {}
+    __device__ __forceinline__ bool next(const AttnArgs& a, int tile, Segment& s) {
+        if (at >= end) return false;
+        int units = units_of(len, tile);
+        while (at >= item0 + (int64_t)units * a.H_kv * a.n_rb) {
+            item0 += (int64_t)units * a.H_kv * a.n_rb;
+            len = clamped_len(a, ++b);
+            units = units_of(len, tile);
+        }
+        const int64_t off = at - item0;
+        const int item = (int)(off / units);
+        s.tile0 = (int)(off - (int64_t)item * units);
+        const int64_t left = end - at;
+        s.tile1 = left < units - s.tile0 ? s.tile0 + (int)left : units;
+        s.tiles = units;
+        s.h = item / a.n_rb;
+        s.rb = item - s.h * a.n_rb;
+        s.b = b;
+        s.len = len;
+        s.first = at == begin;
+        at += s.tile1 - s.tile0;
+        return true;
+    }
+};
+
+// Rows of row block rb.
+__device__ __forceinline__ int block_rows(const AttnArgs& a, int rb) { return min(a.rb_rows, a.rows - rb * a.rb_rows); }
+// Cached tokens row r of a sequence of len tokens sees.
+__device__ __forceinline__ int visible(const AttnArgs& a, int len, int r) { return len - (a.K - 1 - r / a.group); }
+// Index of row r of (b, h) among the [B, K, H_q] rows.
+__device__ __forceinline__ int64_t row_index(const AttnArgs& a, int b, int h, int r) {
+    const int i = r / a.group;
+    return ((int64_t)b * a.K + i) * a.H_q + h * a.group + (r - i * a.group);
+}
+
+// A workspace slot: maxima (log2 domain) and sums of its rows, then their
+// unnormalised outputs.
+__device__ __forceinline__ float* slot_ptr(const AttnArgs& a, int slot) { return a.ws + (int64_t)slot * a.slot_floats; }
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+}  // namespace attn
+}  // namespace gdn

@@ -1,0 +1,33 @@
+// gdn_attn_decode: how a call is cut up, and which kernel runs it.
+#include "attn_common.cuh"
+
+namespace gdn {
+
+namespace {
+constexpr int kFfmaRows = 16;  // rows of a block, at most
+
+int attn_ctas() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+    return n < kAttnMaxCtas ? n : kAttnMaxCtas;
+}
+}  // namespace
+
+size_t attn_plan(AttnArgs& a, gdn_dtype_t) {
+    a.group = a.H_q / a.H_kv;
+    a.rows = a.K * a.group;
+    a.n_rb = (a.rows + kFfmaRows - 1) / kFfmaRows;
+    a.rb_rows = (a.rows + a.n_rb - 1) / a.n_rb;
+    a.min_units = 1;
+    a.stat_floats = (2 * a.rb_rows + 3) & ~3;
+    a.slot_floats = a.stat_floats + (int64_t)a.rb_rows * a.D;
+    return (size_t)2 * kAttnMaxCtas * a.slot_floats * sizeof(float);
+}
+
+cudaError_t launch_attn_decode(const AttnArgs& a, gdn_dtype_t dt, cudaStream_t s) {
+    if (a.B == 0 || a.K == 0) return cudaSuccess;
+    return launch_attn_ffma(a, attn_ctas(), dt, s);
+}
+
+}  // namespace gdn

@@ -93,7 +93,7 @@ const char* gdn_status_string(gdn_status_t s) {
 
 int gdn_last_cuda_error(void) { return g_last_cuda_error; }
 
-int gdn_version(void) { return (1 << 16) | 0; }
+int gdn_version(void) { return (1 << 16) | 1; }
 
 int64_t gdn_ckpt_count(const int32_t* cu, int32_t n_seq, int32_t every) {
     if (cu == nullptr || n_seq < 1 || every < 0) return -1;
@@ -614,6 +614,110 @@ gdn_status_t gdn_rmsnorm_gated(const void* o, const void* z, const void* w, floa
     if (!aligned16(o) || !aligned16(z) || !aligned16(w) || !aligned16(out)) return GDN_ERR_ALIGN;
     return cuda_status(gdn::launch_rmsnorm_gated(o, z, w, eps, T, dims.H_v, dims.d_v, out, dtype,
                                                  (cudaStream_t)stream));
+}
+
+// ---------------------------------------------------------------- paged cache, drafted tokens
+namespace {
+gdn_status_t check_cache(int32_t H_kv, int32_t D, int32_t page_size, int32_t n_pages, int32_t max_pages,
+                         gdn_dtype_t dt) {
+    if (dt != GDN_F32 && dt != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (H_kv <= 0 || D <= 0 || page_size <= 0 || n_pages <= 0 || max_pages <= 0) return GDN_ERR_INVALID_ARG;
+    if (D % 8 != 0 || D > 256 || H_kv > 65536) return GDN_ERR_UNSUPPORTED;
+    // positions fit 32 bits with room for a tile, rows of a page fit 31
+    if ((int64_t)max_pages * page_size > (1 << 30) || (int64_t)H_kv * page_size > (1 << 30))
+        return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+
+gdn_status_t fill_attn(gdn::AttnArgs& a, int32_t B, int32_t K, int32_t H_q, int32_t H_kv, int32_t D,
+                       int32_t page_size, int32_t n_pages, int32_t max_pages, gdn_dtype_t dt) {
+    memset(&a, 0, sizeof(a));
+    const gdn_status_t st = check_cache(H_kv, D, page_size, n_pages, max_pages, dt);
+    if (st != GDN_OK) return st;
+    if (B < 0 || B > (1 << 24) || K < 0 || K > gdn::kAttnMaxK || H_q <= 0 || H_q % H_kv != 0)
+        return GDN_ERR_INVALID_ARG;
+    if (H_q > 65536) return GDN_ERR_UNSUPPORTED;
+    a.B = B; a.K = K; a.H_q = H_q; a.H_kv = H_kv; a.D = D;
+    a.page_size = page_size; a.n_pages = n_pages; a.max_pages = max_pages;
+    return GDN_OK;
+}
+}  // namespace
+
+gdn_status_t gdn_kv_append(const void* k, const void* v, void* k_cache, void* v_cache, const int32_t* page_table,
+                           const int32_t* seq_lens, const int32_t* cu_seqlens, int32_t B, int64_t T_tot,
+                           int32_t H_kv, int32_t D, int32_t page_size, int32_t n_pages, int32_t max_pages,
+                           gdn_dtype_t dtype, void* stream) {
+    const gdn_status_t st = check_cache(H_kv, D, page_size, n_pages, max_pages, dtype);
+    if (st != GDN_OK) return st;
+    if (B < 0 || B > (1 << 24) || T_tot < 0 || T_tot > (int64_t)INT32_MAX) return GDN_ERR_INVALID_ARG;
+    if ((int64_t)D * elem_size(dtype) % 16 != 0) return GDN_ERR_UNSUPPORTED;
+    if (T_tot == 0) return GDN_OK;
+    if (B == 0 || (cu_seqlens == nullptr && T_tot % B != 0)) return GDN_ERR_INVALID_ARG;
+    if (k == nullptr || v == nullptr || k_cache == nullptr || v_cache == nullptr || page_table == nullptr ||
+        seq_lens == nullptr)
+        return GDN_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned_n(page_table, 4) ||
+        !aligned_n(seq_lens, 4) || !aligned_n(cu_seqlens, 4))
+        return GDN_ERR_ALIGN;
+    gdn::KvAppendArgs a;
+    memset(&a, 0, sizeof(a));
+    a.k = k; a.v = v; a.k_cache = k_cache; a.v_cache = v_cache;
+    a.table = page_table; a.lens = seq_lens; a.cu = cu_seqlens;
+    a.T = T_tot; a.B = B; a.H_kv = H_kv; a.row_bytes = (int)(D * elem_size(dtype));
+    a.page_size = page_size; a.n_pages = n_pages; a.max_pages = max_pages;
+    return cuda_status(gdn::launch_kv_append(a, (cudaStream_t)stream));
+}
+
+size_t gdn_attn_decode_workspace_size(int32_t B, int32_t K, int32_t H_q, int32_t H_kv, int32_t D,
+                                      int32_t page_size, gdn_dtype_t dtype) {
+    gdn::AttnArgs a;
+    if (fill_attn(a, B, K, H_q, H_kv, D, page_size, 1, 1, dtype) != GDN_OK || B == 0 || K == 0) return 0;
+    return gdn::attn_plan(a, dtype);
+}
+
+gdn_status_t gdn_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                             const int32_t* seq_lens, float scale, const void* gate, void* out, float* lse,
+                             int32_t B, int32_t K, int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size,
+                             int32_t n_pages, int32_t max_pages, void* workspace, size_t ws_bytes,
+                             gdn_dtype_t dtype, void* stream) {
+    gdn::AttnArgs a;
+    const gdn_status_t st = fill_attn(a, B, K, H_q, H_kv, D, page_size, n_pages, max_pages, dtype);
+    if (st != GDN_OK) return st;
+    if (!isfinite(scale) || scale < 0.f) return GDN_ERR_INVALID_ARG;
+    if (B == 0 || K == 0) return GDN_OK;
+    if (q == nullptr || k_cache == nullptr || v_cache == nullptr || page_table == nullptr || seq_lens == nullptr ||
+        out == nullptr)
+        return GDN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned_n(page_table, 4) ||
+        !aligned_n(seq_lens, 4) || !aligned16(gate) || !aligned16(out) || !aligned_n(lse, 4) || !aligned16(workspace))
+        return GDN_ERR_ALIGN;
+    a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.table = page_table; a.lens = seq_lens;
+    a.gate = gate; a.out = out; a.lse = lse;
+    a.ws = static_cast<float*>(workspace);
+    a.scale_log2 = (scale == 0.f ? 1.0f / sqrtf((float)D) : scale) * 1.4426950408889634f;
+    const size_t need = gdn::attn_plan(a, dtype);
+    if (workspace == nullptr || ws_bytes < need) return GDN_ERR_WORKSPACE;
+    return cuda_status(gdn::launch_attn_decode(a, dtype, (cudaStream_t)stream));
+}
+
+gdn_status_t gdn_draft_accept(const void* p, const void* q, const int32_t* draft, const float* u,
+                              const int32_t* n_draft, const int32_t* slots, int32_t B, int32_t K, int32_t V,
+                              int32_t* n_accept, int32_t* tokens, int32_t* next_slot, gdn_dtype_t dtype,
+                              void* stream) {
+    if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (B < 0 || B > (1 << 24) || K < 0 || K > gdn::kAcceptMaxK || V <= 0 || V > (1 << 24)) return GDN_ERR_INVALID_ARG;
+    if (B == 0) return GDN_OK;
+    if (p == nullptr || (K > 0 && draft == nullptr) || u == nullptr || n_accept == nullptr || tokens == nullptr ||
+        (slots == nullptr) != (next_slot == nullptr))
+        return GDN_ERR_INVALID_ARG;
+    if (!aligned16(p) || !aligned16(q) || !aligned_n(draft, 4) || !aligned_n(u, 4) || !aligned_n(n_draft, 4) ||
+        !aligned_n(slots, 4) || !aligned_n(n_accept, 4) || !aligned_n(tokens, 4) || !aligned_n(next_slot, 4))
+        return GDN_ERR_ALIGN;
+    gdn::DraftAcceptArgs a;
+    memset(&a, 0, sizeof(a));
+    a.p = p; a.q = q; a.draft = draft; a.u = u; a.n_draft = n_draft; a.slots = slots;
+    a.B = B; a.K = K; a.V = V; a.n_accept = n_accept; a.tokens = tokens; a.next_slot = next_slot;
+    return cuda_status(gdn::launch_draft_accept(a, dtype, (cudaStream_t)stream));
 }
 
 }  // extern "C"

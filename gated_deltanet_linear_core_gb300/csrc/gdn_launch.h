@@ -151,6 +151,57 @@ cudaError_t read_and_clear_conv_error(cudaStream_t s, int* flags);
 cudaError_t launch_rmsnorm_gated(const void* o, const void* z, const void* w, float eps, int64_t T,
                                  int H, int D, void* out, gdn_dtype_t dt, cudaStream_t s);
 
+// Attention of the K newest tokens of B sequences over the paged cache
+// (gdn_attn_decode): arguments, and how the call is cut up (attn_common.cuh).
+struct AttnArgs {
+    const void* q;         // [B, K, H_q, D]
+    const void *k_cache, *v_cache;  // [n_pages, H_kv, page_size, D]
+    const int32_t* table;  // [B, max_pages]
+    const int32_t* lens;   // [B]
+    const void* gate;      // [B, K, H_q, D] or null
+    void* out;             // [B, K, H_q, D]
+    float* lse;            // [B, K, H_q] or null
+    float* ws;             // slots of partial results
+    int64_t slot_floats;   // floats per slot
+    int stat_floats;       // of which maxima and sums come first
+    int B, K, H_q, H_kv, D;
+    int page_size, max_pages, n_pages;
+    float scale_log2;      // score scale times log2 e
+    int group, rows;       // H_q / H_kv, K * group
+    int rb_rows, n_rb;     // rows per row block, row blocks
+    int min_units;         // least tiles per CTA
+};
+constexpr int kAttnMaxK = 16;
+constexpr int kAttnMaxCtas = 152;  // CTAs of a call, at most: one per SM
+// Fills the derived fields from the sizes; returns the workspace bytes.
+size_t attn_plan(AttnArgs& a, gdn_dtype_t dt);
+cudaError_t launch_attn_decode(const AttnArgs& a, gdn_dtype_t dt, cudaStream_t s);
+cudaError_t launch_attn_ffma(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaStream_t s);
+cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, int tile, gdn_dtype_t dt, cudaStream_t s);
+
+// New keys and values into their pages (gdn_kv_append).
+struct KvAppendArgs {
+    const void *k, *v;     // [T, H_kv, D]
+    void *k_cache, *v_cache;
+    const int32_t *table, *lens;
+    const int32_t* cu;     // [B + 1] or null: T / B tokens each
+    int64_t T;
+    int B, H_kv, row_bytes, page_size, max_pages, n_pages;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t s);
+
+// Acceptance of drafted tokens (gdn_draft_accept).
+struct DraftAcceptArgs {
+    const void *p, *q;     // [B, K + 1, V], [B, K, V] or null
+    const int32_t* draft;  // [B, K]
+    const float* u;        // [B, K + 1]
+    const int32_t *n_draft, *slots;  // [B] or null, [B, K + 2] or null
+    int B, K, V;
+    int32_t *n_accept, *tokens, *next_slot;  // [B], [B, K + 1], [B] or null
+};
+constexpr int kAcceptMaxK = 15;
+cudaError_t launch_draft_accept(const DraftAcceptArgs& a, gdn_dtype_t dt, cudaStream_t s);
+
 // The layer core for one sequence streamed from page-locked host memory
 // (gdn_layer_prefill_host).
 struct HostLayerArgs {

@@ -483,6 +483,98 @@ gdn_status_t gdn_layer_prefill(const void* x, const void* z, const void* a, cons
 gdn_status_t gdn_rmsnorm_gated(const void* o, const void* z, const void* w, float eps, int64_t T,
                                void* out, gdn_dims_t dims, gdn_dtype_t dtype, void* stream);
 
+/*
+ * The serving side of a speculative step around gdn_decode_verify: the paged
+ * key-value cache of a hybrid model's softmax-attention layers, the attention of
+ * the newest tokens that reads it, and the acceptance of the drafted tokens.  The
+ * pages name the parts (NxD-Inference Qwen3.6-27B PR, Summary: attention KV cache
+ * beside the GDN state checkpoints; GQA softmax layers of head_dim 256 with an
+ * output gate; "Known limitations": multi-token speculative decoding is missing)
+ * and define none of them; the definitions below are the textbook ones.
+ *
+ * A cache of n_pages pages is [n_pages, H_kv, page_size, D] (dtype), one array for
+ * keys and one for values.  Position t of sequence b lies in page
+ * page_table[b][t / page_size] at t % page_size; page_table (device) is
+ * [B, max_pages] int32, of which only the entries that positions below the length
+ * reach are used.  D is a multiple of 8 up to 256, any page_size >= 1 (the tensor-
+ * core path: bf16 and page_size a multiple of 4).  max_pages * page_size and
+ * H_kv * page_size are at most 2^30; offsets into the caches are 64-bit.
+ * seq_lens (device) [B] int32 counts the new tokens too, and is clamped to
+ * [0, max_pages * page_size].  A page outside [0, n_pages) is never accessed.
+ */
+
+/*
+ * Writes new tokens into the cache: token j of the L_b new tokens of sequence b
+ * goes to position seq_lens[b] - L_b + j (bit copies; all other rows keep their
+ * values).  Tokens whose position or page does not exist are left out.
+ *   k, v       (device) [T_tot, H_kv, D] dtype, sequence after sequence
+ *   k_cache, v_cache (device) written in place
+ *   cu_seqlens (device) [B + 1] int32, or NULL: T_tot / B tokens per sequence
+ *              (T_tot a multiple of B).  Tokens outside every sequence are left out.
+ * Two tokens of one call must not go to the same place.
+ */
+gdn_status_t gdn_kv_append(const void* k, const void* v, void* k_cache, void* v_cache, const int32_t* page_table,
+                           const int32_t* seq_lens, const int32_t* cu_seqlens, int32_t B, int64_t T_tot,
+                           int32_t H_kv, int32_t D, int32_t page_size, int32_t n_pages, int32_t max_pages,
+                           gdn_dtype_t dtype, void* stream);
+
+/*
+ * Attention of the K newest tokens of B sequences over the cache, which holds
+ * their keys and values already (gdn_kv_append).  K = 1 is a decode step; K > 1 is
+ * the verification pass (causal among the new tokens).  New token i of sequence b
+ * sees the n = seq_lens[b] - (K - 1 - i) first positions; query head h reads
+ * key-value head h / (H_q / H_kv):
+ *   s_t = scale q . k_t,  out = sum_{t<n} e^{s_t} v_t / sum_{t<n} e^{s_t}
+ *   [* sigmoid(gate)],    lse = log sum_{t<n} e^{s_t}
+ * and with n <= 0: out = 0, lse = -inf.  What hidden positions hold, NaN and
+ * infinities included, does not matter.
+ *   q          (device) [B, K, H_q, D] dtype;  H_q a multiple of H_kv
+ *   scale      0 means D^-1/2, else positive
+ *   gate       (device) [B, K, H_q, D] dtype, or NULL
+ *   out        (device) [B, K, H_q, D] dtype, no other argument's memory
+ *   lse        (device) [B, K, H_q] f32, or NULL
+ *   workspace  (device) >= gdn_attn_decode_workspace_size bytes; calls that may
+ *              run at the same time need one each.  Its contents do not matter.
+ * 0 <= K <= 16.  The lengths are read on the device: nothing synchronises, and a
+ * captured call follows them.  Results do not depend on timing.
+ */
+size_t gdn_attn_decode_workspace_size(int32_t B, int32_t K, int32_t H_q, int32_t H_kv, int32_t D,
+                                      int32_t page_size, gdn_dtype_t dtype);
+gdn_status_t gdn_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                             const int32_t* seq_lens, float scale, const void* gate, void* out, float* lse,
+                             int32_t B, int32_t K, int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size,
+                             int32_t n_pages, int32_t max_pages, void* workspace, size_t ws_bytes,
+                             gdn_dtype_t dtype, void* stream);
+
+/*
+ * Which of K drafted tokens hold, and the token after them, from given uniforms
+ * (speculative sampling; the tokens emitted are distributed as the target's own):
+ * draft t holds if u[b][t] q_t(d_t) < p_t(d_t) and every draft before it holds;
+ * n = drafts that hold; r(v) = max(p_n(v) - q_n(v), 0) if draft n failed, else
+ * p_n(v); the next token is the first v with r(v) > 0 whose running sum of r
+ * passes u[b][K] times the whole sum.  Both borders are decided to about twice
+ * f32's precision.  A row r without a positive value falls back to p_n, and to
+ * token 0 if that has none.
+ *   p          (device) [B, K + 1, V] dtype: the target's probabilities after the
+ *              last sampled token and after each draft (finite; need not add up to 1)
+ *   q          (device) [B, K, V] dtype: the draft model's, or NULL for drafts that
+ *              were not sampled (q_t is 1 at d_t)
+ *   draft      (device) [B, K] int32; a token outside [0, V) never holds
+ *   u          (device) [B, K + 1] f32 in [0, 1); u[b][K] picks the next token
+ *   n_draft    (device) [B] int32 drafts that sequence b has (clamped to [0, K]), or NULL: K
+ *   slots      (device) [B, K + 2] int32, the slots row of the gdn_decode_verify call
+ *              over the K + 1 tokens (last sampled, drafts), or NULL
+ *   n_accept   (device) [B] int32 out: n
+ *   tokens     (device) [B, K + 1] int32 out: the n drafts, the next token, then -1
+ *   next_slot  (device) [B] int32 out: slots[b][n + 1], the slot to continue from
+ *              (NULL exactly when slots is)
+ * 0 <= K <= 15, V <= 2^24.
+ */
+gdn_status_t gdn_draft_accept(const void* p, const void* q, const int32_t* draft, const float* u,
+                              const int32_t* n_draft, const int32_t* slots, int32_t B, int32_t K, int32_t V,
+                              int32_t* n_accept, int32_t* tokens, int32_t* next_slot, gdn_dtype_t dtype,
+                              void* stream);
+
 #ifdef __cplusplus
 }
 #endif
