@@ -4,7 +4,7 @@
 namespace gdn {
 
 namespace {
-constexpr int kFfmaRows = 16;  // rows of a block, at most
+constexpr int kFfmaRows = 16, kTcRows = 128;  // rows of a block, at most
 
 int attn_ctas() {
     int dev = 0, n = 0;
@@ -14,10 +14,11 @@ int attn_ctas() {
 }
 }  // namespace
 
-size_t attn_plan(AttnArgs& a, gdn_dtype_t) {
+size_t attn_plan(AttnArgs& a, gdn_dtype_t dt) {
+    const int most = attn_tc_takes(a, dt) ? kTcRows : kFfmaRows;
     a.group = a.H_q / a.H_kv;
     a.rows = a.K * a.group;
-    a.n_rb = (a.rows + kFfmaRows - 1) / kFfmaRows;
+    a.n_rb = (a.rows + most - 1) / most;
     a.rb_rows = (a.rows + a.n_rb - 1) / a.n_rb;
     a.min_units = 1;
     a.stat_floats = (2 * a.rb_rows + 3) & ~3;
@@ -27,7 +28,7 @@ size_t attn_plan(AttnArgs& a, gdn_dtype_t) {
 
 cudaError_t launch_attn_decode(const AttnArgs& a, gdn_dtype_t dt, cudaStream_t s) {
     if (a.B == 0 || a.K == 0) return cudaSuccess;
-    return launch_attn_ffma(a, attn_ctas(), dt, s);
+    return attn_tc_takes(a, dt) ? launch_attn_tc(a, attn_ctas(), s) : launch_attn_ffma(a, attn_ctas(), dt, s);
 }
 
 }  // namespace gdn

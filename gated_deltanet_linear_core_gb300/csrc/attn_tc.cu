@@ -1,0 +1,649 @@
+// Attention of the newest tokens over the paged cache on tcgen05 tensor cores
+// (bf16).
+//
+// With at most 128 query rows per key-value head the work is bound by reading
+// the cache once, so the products are laid out for the cache tiles as they
+// arrive: a tile is 128 tokens, and the tokens (then the head dims) are the
+// M = 128 side of the MMAs, the query rows the N side:
+//   S^T [128 tokens x N rows] = K Q^T        (A = K tile, B = Q; both K-major)
+//   O^T [128 dims x N rows]  += V^T P^T      (A = V tile, B = P; both MN-major)
+// No tile is transposed or copied, and an MMA of few rows costs what reading
+// its A operand from shared memory costs (128 B/clock, five times the HBM rate
+// per SM).  K and V tiles land by TMA, one box per page piece, in slots of 128
+// tokens x 128 dims, so a tile of head dim 256 is four slots of a ring.
+//
+// Softmax: a thread owns one token (TMEM lane) and CPT rows (columns).  The
+// running maximum of a row is moved only when a score exceeds it by 2^8 (P then
+// stays below 2^8, harmless in f32 sums), so most tiles need one vote and no
+// rescaling of O.  P is handed to the MMA as two bf16 (the value cut to 8 bits
+// and the rounded rest, 16 bits in all): one bf16 alone would add an error of
+// the size of the output's own rounding, and the second MMA is free, since the
+// kernel waits for HBM.  Sums are kept per thread in f32 and joined at the end.
+//
+// Warps: 0 loads, 1 issues the MMAs, the others are the softmax.  The MMA warp
+// runs S of the next tile ahead of P V of this one.  Every wait is bounded
+// (1 s): on a timeout the roles run out without waiting, the copies in flight
+// land, TMEM is freed and the error word is set.
+#include <cuda.h>
+
+#include "attn_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace gdn {
+
+__device__ int g_attn_error;  // bit 0: a bounded wait gave up
+
+namespace {
+
+using namespace attn;
+using namespace tc;
+
+constexpr int TILE = 128;
+constexpr int SLAB = TILE * 128;      // bytes of 128 tokens x 64 dims
+constexpr int SLOT = 2 * SLAB;        // ... x 128 dims
+constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr float kNone = -3.0e38f;     // running maximum of a row that saw nothing yet
+constexpr float kSlack = 8.0f;        // how far (log2) scores may exceed the running maximum
+constexpr int kSmemMax = 232448;
+
+template <int N, int NDB>
+struct Layout {
+    static constexpr int CPT = N < 32 ? N : 32;   // columns (rows of Q) per softmax thread
+    static constexpr int NWG = N / CPT;           // softmax warpgroups
+    static constexpr int NSW = 4 * NWG;           // softmax warps
+    static constexpr int NT = 64 + 32 * NSW;
+    static constexpr int PBUF = N <= 64 ? 2 : 1;  // buffers of P
+    // P of a tile: 128-byte rows of 64 columns.  N = 16: both buffers' [hi | lo] side by side in one
+    // block; N = 32: [hi | lo] in one block per buffer; else hi and lo in blocks of their own.
+    static constexpr int P_BYTES = N == 16 ? SLAB : N == 32 ? 2 * SLAB : PBUF * 2 * ((N + 63) / 64) * SLAB;
+    static constexpr int Q_BYTES = 2 * NDB * N * 128;
+    static constexpr int SCR = N <= 64 ? 4 * N * 4 : 0;  // scratch of its own (N = 128: in P, free by then)
+    static constexpr int BARS = 256;
+    static constexpr int SMALL = BARS + 256 + N * (4 + 4 + 4 + 8) + SCR;
+    static constexpr int FIT = (kSmemMax - P_BYTES - Q_BYTES - SMALL) / SLOT;
+    static constexpr int NS = FIT < 6 ? FIT : 6;
+    // S of the next tile runs ahead of P V where the ring holds that tile's K slots beside the V slots
+    static constexpr bool AHEAD = NS >= 2 * NDB;
+    static constexpr int O_Q = NS * SLOT;
+    static constexpr int O_P = O_Q + Q_BYTES;
+    static constexpr int O_BAR = O_P + P_BYTES;
+    static constexpr int O_SH = O_BAR + BARS;
+    static constexpr int O_OFF = O_SH + 256;
+    static constexpr int O_M = O_OFF + N * 8;
+    static constexpr int O_F = O_M + N * 4;
+    static constexpr int O_VIS = O_F + N * 4;
+    static constexpr int O_SCR = N <= 64 ? O_VIS + N * 4 : O_P;
+    static constexpr int SMEM = O_BAR + SMALL;
+    static constexpr int T_S = 0, T_O = 2 * N;
+    static constexpr int T_USED = (2 + NDB) * N;
+    static constexpr int T_COLS = T_USED <= 64 ? 64 : T_USED <= 128 ? 128 : T_USED <= 256 ? 256 : 512;
+    static_assert(SMEM <= kSmemMax && NS >= 3, "shared memory");
+    static_assert((5 + 2 * 6 + 2) * 8 + 16 <= BARS, "barriers");
+
+    // byte offset of P's column block (16-byte chunk j of 8 columns) of token t
+    __device__ static __forceinline__ uint32_t p_off(int buf, int lo, int chunk, int t) {
+        uint32_t base = 0;
+        int c = chunk;
+        if constexpr (N == 16) c = buf * 4 + lo * 2 + chunk;
+        else if constexpr (N == 32) { base = buf * SLAB; c = lo * 4 + chunk; }
+        else {
+            base = ((buf * 2 + lo) * ((N + 63) / 64) + (chunk >> 3)) * SLAB;
+            c = chunk & 7;
+        }
+        return base + t * 128 + ((c ^ (t & 7)) << 4);
+    }
+    // start of P's operand (first token, first column) for the MMA descriptor
+    __device__ static __forceinline__ uint32_t p_start(int buf, int lo) {
+        if constexpr (N == 16) return buf * 64 + lo * 32;
+        else if constexpr (N == 32) return buf * SLAB + lo * 64;
+        else return (buf * 2 + lo) * ((N + 63) / 64) * SLAB;
+    }
+};
+
+// Bounded wait; returns at once when another role has given up.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    if (mbar_test(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_test(bar, parity)) return true;
+        if ((it & 31) == 0) {
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 > kWaitNs) {
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+template <int NTHR>
+__device__ __forceinline__ void softmax_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
+}
+template <int NTHR>
+__device__ __forceinline__ bool softmax_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "n"(NTHR)
+        : "memory");
+    return r != 0;
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
+    if constexpr (N == 16) tmem_ld16(taddr, v); else tmem_ld32(taddr, v);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[N]) {
+    if constexpr (N == 16) tmem_st16(taddr, v); else tmem_st32(taddr, v);
+}
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ bool finite_bf16x8(uint4 u) {
+    bool ok = true;
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ok = ok && (w[i] & 0x7f80u) != 0x7f80u && (w[i] & 0x7f800000u) != 0x7f800000u;
+    return ok;
+}
+__device__ __forceinline__ uint32_t zero_non_finite(uint32_t w) {
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+    return w;
+}
+
+template <int N, int NDB>
+__global__ void __launch_bounds__(Layout<N, NDB>::NT, 1)
+attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a,
+               int piece) {
+    using L = Layout<N, NDB>;
+    constexpr int CPT = L::CPT, NS = L::NS, NSOFT = 32 * L::NSW;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::O_BAR);
+    uint64_t* full = bars;            // [6] slot landed (TMA)
+    uint64_t* empty = bars + 6;       // [6] slot consumed (commit)
+    uint64_t* s_full = bars + 12;     // [2] S of a tile done
+    uint64_t* p_full = bars + 14;     // [2] P of a tile written, V tail mended (softmax warps)
+    uint64_t* pv_done = bars + 16;    // [2] P V of a tile done
+    uint64_t* q_full = bars + 18;     // a segment's Q written (softmax warps)
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 19);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+    volatile int* odd_v = reinterpret_cast<volatile int*>(tslot + 2);  // a new token's value is not finite
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < 6; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], L::NSW);
+            mbar_init(&pv_done[i], 1);
+        }
+        mbar_init(q_full, L::NSW);
+        *abort_flag = 0;
+        *odd_v = 0;
+        fence_mbar_init();
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+    }
+    if (warp == 1) {
+        tmem_alloc(tslot, L::T_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = *tslot;
+    pdl_wait();
+    pdl_trigger();
+
+    int n_cta = gridDim.x;
+    const Place place = find_place<L::NT>(a, TILE, blockIdx.x, n_cta, reinterpret_cast<int64_t*>(sm + L::O_SH));
+    const bool works = (int)blockIdx.x < n_cta;
+    const int64_t u0 = works ? cta_begin(place.total, blockIdx.x, n_cta) : 0;
+    const int64_t u1 = works ? cta_begin(place.total, blockIdx.x + 1, n_cta) : 0;
+    Walk walk(place, u0, u1);
+    Segment s;
+    const int nslab = (a.D + 63) / 64;
+
+    if (warp == 0) {
+        // ------------------------------------------------ loads: lane p takes piece p of a tile
+        const int np = TILE / piece;
+        int sl = 0;  // slots filled
+        bool ok = true;
+        while (ok && walk.next(a, TILE, s)) {
+            if (s.len == 0) continue;
+            const int32_t* table = a.table + (int64_t)s.b * a.max_pages;
+            auto look_up = [&](int tile, int& y, int& z) {
+                const int t = tile * TILE + lane * piece;
+                z = a.n_pages;  // reads as zeros
+                y = 0;
+                if (lane < np && t < s.len) {
+                    const int pg = t / a.page_size;
+                    const int page = table[pg];
+                    if (page >= 0 && page < a.n_pages) z = page;
+                    y = s.h * a.page_size + (t - pg * a.page_size);
+                }
+            };
+            int y, z;
+            look_up(s.tile0, y, z);
+            for (int j = s.tile0; ok && j < s.tile1; ++j) {
+                const int left = s.len - j * TILE;
+                const int have = left >= TILE ? np : (left + piece - 1) / piece;  // pieces with tokens
+                int yn = 0, zn = 0;
+                if (j + 1 < s.tile1) look_up(j + 1, yn, zn);
+                for (int part = 0; ok && part < 2 * NDB; ++part, ++sl) {
+                    const int st = sl % NS, db = part % NDB;
+                    if (sl >= NS) {
+                        ok = __all_sync(0xffffffffu, wait_or_abort(&empty[st], (uint32_t)((sl / NS - 1) & 1), abort_flag));
+                        if (!ok) break;
+                    }
+                    const int slabs = nslab - 2 * db < 2 ? nslab - 2 * db : 2;
+                    if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(have * piece * 128 * slabs));
+                    __syncwarp();
+                    if (lane < have) {
+                        const CUtensorMap* map = part < NDB ? &kmap : &vmap;
+                        const uint32_t dst = smem_u32(sm) + st * SLOT + lane * piece * 128;
+                        for (int i = 0; i < slabs; ++i)
+                            tma_load_3d(dst + i * SLAB, map, &full[st], (2 * db + i) * 64, y, z);
+                    }
+                }
+                y = yn;
+                z = zn;
+            }
+        }
+        // on abort: let the copies in flight land before the CTA exits
+        if (*abort_flag)
+            for (int k = sl > NS ? sl - NS : 0; k < sl; ++k) mbar_wait(&full[k % NS], (uint32_t)((k / NS) & 1), kWaitNs);
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMAs (lane 0)
+        if (lane == 0) {
+            const uint32_t base = smem_u32(sm);
+            const int ksteps = (a.D + 15) / 16;
+            int it = 0, seg = 0;        // tiles and segments done
+            uint64_t* last = nullptr;   // the last commit, for the drain on abort
+            uint32_t last_parity = 0;
+            auto issue_s = [&](int t) -> bool {  // S of the CTA's tile t
+                for (int db = 0; db < NDB; ++db) {
+                    const int k = t * 2 * NDB + db;
+                    if (!wait_or_abort(&full[k % NS], (uint32_t)((k / NS) & 1), abort_flag)) return false;
+                }
+                tc_fence_after();
+                for (int q = 0; q < ksteps; ++q) {
+                    const int k = t * 2 * NDB + q / 8;
+                    const uint32_t ka = base + (k % NS) * SLOT + ((q >> 2) & 1) * SLAB + (q & 3) * 32;
+                    const uint32_t qa = base + L::O_Q + (q >> 2) * (N * 128) + (q & 3) * 32;
+                    mma_bf16(tb + L::T_S + (t & 1) * N, sdesc_sw128(ka, 16, 1024), sdesc_sw128(qa, 16, 1024),
+                             idesc_bf16_f32(128, N, 0, 0), q > 0);
+                }
+                for (int db = 0; db < NDB; ++db) mma_commit(&empty[(t * 2 * NDB + db) % NS]);
+                mma_commit(&s_full[t & 1]);
+                last = &s_full[t & 1];
+                last_parity = (uint32_t)((t >> 1) & 1);
+                return true;
+            };
+            bool ok = true;
+            while (ok && walk.next(a, TILE, s)) {
+                if (s.len == 0) continue;
+                ok = wait_or_abort(q_full, (uint32_t)(seg & 1), abort_flag);
+                ++seg;
+                ok = ok && issue_s(it);
+                for (int j = s.tile0; ok && j < s.tile1; ++j, ++it) {
+                    if (L::AHEAD && j + 1 < s.tile1 && !issue_s(it + 1)) { ok = false; break; }
+                    ok = wait_or_abort(&p_full[it & 1], (uint32_t)((it >> 1) & 1), abort_flag);
+                    if (!ok) break;
+                    const int left = s.len - j * TILE;
+                    const int pk = left >= TILE ? 8 : (left + 15) / 16;  // 16-token steps with tokens
+                    const int buf = L::PBUF == 2 ? it & 1 : 0;
+                    for (int db = 0; db < NDB; ++db) {
+                        const int k = it * 2 * NDB + NDB + db;
+                        if (!wait_or_abort(&full[k % NS], (uint32_t)((k / NS) & 1), abort_flag)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t va = base + (k % NS) * SLOT;
+                        for (int lo = 0; lo < 2; ++lo) {
+                            const uint32_t pa = base + L::O_P + L::p_start(buf, lo);
+                            for (int q = 0; q < pk; ++q)
+                                mma_bf16(tb + L::T_O + db * N, sdesc_sw128(va + q * 2048, SLAB, 1024),
+                                         sdesc_sw128(pa + q * 2048, SLAB, 1024), idesc_bf16_f32(128, N, 1, 1),
+                                         j > s.tile0 || lo > 0 || q > 0);
+                        }
+                        mma_commit(&empty[k % NS]);
+                    }
+                    if (!ok) break;
+                    mma_commit(&pv_done[it & 1]);
+                    last = &pv_done[it & 1];
+                    last_parity = (uint32_t)((it >> 1) & 1);
+                    if (!L::AHEAD && j + 1 < s.tile1 && !issue_s(it + 1)) { ok = false; break; }
+                }
+            }
+            if (*abort_flag && last != nullptr) mbar_wait(last, last_parity, kWaitNs);
+        }
+    } else {
+        // ------------------------------------------------ softmax and outputs
+        const int st = tid - 64;                 // softmax thread
+        const int quad = warp & 3;               // its TMEM lanes: 32 quad ..
+        const int row = quad * 32 + lane;        // token of a tile, head dim of an output block
+        const int c0 = ((warp - 2) >> 2) * CPT;  // its columns: c0 ..
+        const uint32_t tq = tb + ((uint32_t)(quad * 32) << 16) + c0;
+        float* m_s = reinterpret_cast<float*>(sm + L::O_M);      // running maxima
+        float* f_s = reinterpret_cast<float*>(sm + L::O_F);      // factors of a rescaling, 1 / l at the end
+        int* vis_s = reinterpret_cast<int*>(sm + L::O_VIS);      // tokens a row sees
+        int64_t* off_s = reinterpret_cast<int64_t*>(sm + L::O_OFF);  // element offset of a row in q, gate, out
+        float* scr = reinterpret_cast<float*>(sm + L::O_SCR);    // [4 lane quarters][N]
+        int it = 0;
+        bool live = true;  // no wait gave up: outputs are written only then
+        auto wait = [&](uint64_t* bar, int k) {
+            live = __all_sync(0xffffffffu, live && wait_or_abort(bar, (uint32_t)(k & 1), abort_flag));
+        };
+        while (walk.next(a, TILE, s)) {
+            const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
+            const bool whole = s.tile1 - s.tile0 == s.tiles;
+            softmax_sync<NSOFT>();  // everyone is done with the previous segment's arrays
+            for (int c = st; c < N; c += NSOFT) {
+                m_s[c] = kNone;
+                vis_s[c] = c < nr ? visible(a, s.len, r0 + c) : 0;
+                off_s[c] = c < nr ? row_index(a, s.b, s.h, r0 + c) * a.D : 0;
+            }
+            if (st == 0) *odd_v = 0;
+            softmax_sync<NSOFT>();
+            if (s.len == 0) {  // nothing to see: the rows are zeros
+                for (int e = st; e < nr * a.D; e += NSOFT) {
+                    const int r = e / a.D, d = e - r * a.D;
+                    static_cast<bf16*>(a.out)[off_s[r] + d] = from_f<bf16>(0.f);
+                    if (d == 0 && a.lse != nullptr) a.lse[off_s[r] / a.D] = -INFINITY;
+                }
+                continue;
+            }
+            // Q rows, zero beyond the block's rows and the head dim
+            for (int e = st; e < N * 16 * NDB; e += NSOFT) {
+                const int r = e / (16 * NDB), ch = e % (16 * NDB);
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (r < nr && ch * 8 < a.D)
+                    x = __ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) + off_s[r] + ch * 8));
+                *reinterpret_cast<uint4*>(sm + L::O_Q + (ch >> 3) * (N * 128) + sw128_off((uint32_t)r, (uint32_t)(ch & 7) * 8)) = x;
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+
+            float l[CPT];
+#pragma unroll
+            for (int c = 0; c < CPT; ++c) l[c] = 0.f;
+            const int least = visible(a, s.len, r0);  // what the block's first row sees
+            for (int j = s.tile0; j < s.tile1; ++j, ++it) {
+                const int t0 = j * TILE;
+                float x[CPT];
+                wait(&s_full[it & 1], it >> 1);
+                tc_fence_after();
+                tmem_ld<CPT>(tq + L::T_S + (it & 1) * N, x);
+                tmem_wait_ld();
+                const bool tail = t0 + TILE > least;
+                bool over = false;
+#pragma unroll
+                for (int c = 0; c < CPT; c += 4) {
+                    const float4 m4 = *reinterpret_cast<const float4*>(m_s + c0 + c);
+                    const float m[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[c + i] *= a.scale_log2;
+                        if (tail && t0 + row >= vis_s[c0 + c + i]) x[c + i] = -INFINITY;
+                        over = over || x[c + i] > m[i] + kSlack;
+                    }
+                }
+                if (softmax_any<NSOFT>(over)) {
+                    // ---- new maxima; sums and outputs so far are scaled to them
+                    const bool first = j == s.tile0;
+                    if (!first) wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
+#pragma unroll
+                    for (int c = 0; c < CPT; ++c) {
+                        const float t = warp_max(x[c]);
+                        if (lane == 0) scr[quad * N + c0 + c] = t;
+                    }
+                    softmax_sync<NSOFT>();
+                    for (int c = st; c < N; c += NSOFT) {
+                        const float m0 = m_s[c];
+                        const float m1 = fmaxf(fmaxf(fmaxf(scr[c], scr[N + c]), fmaxf(scr[2 * N + c], scr[3 * N + c])), m0);
+                        m_s[c] = m1;
+                        f_s[c] = ex2_approx(m0 - m1);
+                    }
+                    softmax_sync<NSOFT>();
+                    if (!first) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < CPT; ++c) l[c] *= f_s[c0 + c];
+#pragma unroll
+                        for (int db = 0; db < NDB; ++db) {
+                            float o[CPT];
+                            tmem_ld<CPT>(tq + L::T_O + db * N, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < CPT; ++c) o[c] *= f_s[c0 + c];
+                            tmem_st<CPT>(tq + L::T_O + db * N, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                const int buf = L::PBUF == 2 ? it & 1 : 0;
+                if (it >= L::PBUF) wait(&pv_done[(it - L::PBUF) & 1], (it - L::PBUF) >> 1);
+#pragma unroll
+                for (int c = 0; c < CPT; c += 8) {
+                    const float4 ma = *reinterpret_cast<const float4*>(m_s + c0 + c);
+                    const float4 mb = *reinterpret_cast<const float4*>(m_s + c0 + c + 4);
+                    const float m[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float p0 = ex2_approx(x[c + 2 * i] - m[2 * i]);
+                        const float p1 = ex2_approx(x[c + 2 * i + 1] - m[2 * i + 1]);
+                        l[c + 2 * i] += p0;
+                        l[c + 2 * i + 1] += p1;
+                        const uint32_t w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
+                        hi[i] = __byte_perm(w0, w1, 0x7632);  // the upper halves: cut, not rounded
+                        // the rest, at least p's last bit: a rest of 0 would turn an infinite value into NaN
+                        lo[i] = pack_bf16x2(__uint_as_float(w0 | 1u) - __uint_as_float(w0 & 0xffff0000u),
+                                            __uint_as_float(w1 | 1u) - __uint_as_float(w1 & 0xffff0000u));
+                    }
+                    *reinterpret_cast<uint4*>(sm + L::O_P + L::p_off(buf, 0, (c0 + c) >> 3, row)) =
+                        make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(sm + L::O_P + L::p_off(buf, 1, (c0 + c) >> 3, row)) =
+                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                if (tail) {
+                    // V rows behind the sequence's end that the MMA's last 16-token step reads become zeros
+                    // (whatever lies there times a weight of 0 could be NaN); so do non-finite values of the
+                    // new tokens that not all rows see -- the rows that do get them back at the end
+                    const int valid = min(TILE, s.len - t0);
+                    const int from = max(0, max(0, s.len - a.K + 1) - t0), upto = (valid + 15) & ~15;
+                    for (int db = 0; db < NDB; ++db) {
+                        const int k = it * 2 * NDB + NDB + db;
+                        wait(&full[k % NS], k / NS);
+                        const int slabs = nslab - 2 * db < 2 ? nslab - 2 * db : 2;
+                        for (int e = st; e < (upto - from) * slabs * 8; e += NSOFT) {
+                            const int t = from + e / (slabs * 8), rest = e % (slabs * 8);
+                            uint4* p = reinterpret_cast<uint4*>(sm + (k % NS) * SLOT + (rest >> 3) * SLAB + t * 128 + (rest & 7) * 16);
+                            if (t >= valid) {
+                                *p = make_uint4(0u, 0u, 0u, 0u);
+                            } else {
+                                const uint4 v = *p;
+                                if (!finite_bf16x8(v)) {
+                                    *odd_v = 1;
+                                    *p = make_uint4(zero_non_finite(v.x), zero_non_finite(v.y), zero_non_finite(v.z),
+                                                    zero_non_finite(v.w));
+                                }
+                            }
+                        }
+                    }
+                }
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[it & 1]);
+            }
+
+            // ---- sums over the tokens: lanes by a butterfly that halves the columns, then the warps
+            wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
+            tc_fence_after();
+#pragma unroll
+            for (int h = CPT / 2, o = 16; o >= 1; h /= 2, o /= 2) {
+                if (h >= 1) {
+#pragma unroll
+                    for (int c = 0; c < CPT / 2; ++c)
+                        if (c < h) {
+                            const float send = lane & o ? l[c] : l[c + h];
+                            const float keep = lane & o ? l[c + h] : l[c];
+                            l[c] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                        }
+                } else {
+                    l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+                }
+            }
+            // lane i now has column i (CPT = 32) or i / 2 (CPT = 16)
+            if (CPT == 32 || (lane & 1) == 0) scr[quad * N + c0 + (CPT == 32 ? lane : lane >> 1)] = l[0];
+            softmax_sync<NSOFT>();
+            float* slot = slot_ptr(a, 2 * blockIdx.x + (s.first ? 0 : 1));
+            for (int c = st; c < nr; c += NSOFT) {
+                const float sum = (scr[c] + scr[N + c]) + (scr[2 * N + c] + scr[3 * N + c]);
+                const float m = m_s[c];
+                f_s[c] = sum == 0.f ? 0.f : 1.0f / sum;
+                if (live) {
+                    if (whole) {
+                        if (a.lse != nullptr) a.lse[off_s[c] / a.D] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+                    } else {
+                        slot[c] = m == kNone ? -INFINITY : m;
+                        slot[a.rb_rows + c] = sum;
+                    }
+                }
+            }
+            softmax_sync<NSOFT>();
+            const bool odd = *odd_v != 0;
+            for (int db = 0; db < NDB; ++db) {
+                float o[CPT];
+                __syncwarp();
+                tmem_ld<CPT>(tq + L::T_O + db * N, o);
+                tmem_wait_ld();
+                const int d = db * 128 + row;
+                if (d >= a.D || !live) continue;
+                if (odd) {
+                    const int t1 = min(s.len, s.tile1 * TILE);
+                    for (int t = max(s.tile0 * TILE, s.len - a.K + 1); t < t1; ++t) {
+                        const int page = a.table[(int64_t)s.b * a.max_pages + t / a.page_size];
+                        if (page < 0 || page >= a.n_pages) continue;
+                        const float v = to_f(static_cast<const bf16*>(
+                            a.v_cache)[(((int64_t)page * a.H_kv + s.h) * a.page_size + t % a.page_size) * a.D + d]);
+                        if (!isfinite(v))
+#pragma unroll
+                            for (int c = 0; c < CPT; ++c)
+                                if (t < vis_s[c0 + c]) o[c] += v;
+                    }
+                }
+                if (whole) {
+#pragma unroll
+                    for (int c = 0; c < CPT; ++c)
+                        if (c0 + c < nr) {
+                            const int64_t at = off_s[c0 + c] + d;
+                            float y = o[c] * f_s[c0 + c];
+                            if (a.gate != nullptr) y *= sigmoid_f(to_f(static_cast<const bf16*>(a.gate)[at]));
+                            static_cast<bf16*>(a.out)[at] = from_f<bf16>(y);
+                        }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < CPT; ++c)
+                        if (c0 + c < nr) slot[a.stat_floats + (c0 + c) * a.D + d] = o[c];
+                }
+            }
+            tc_fence_before();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && *abort_flag) atomicOr(&g_attn_error, 1);
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tb, L::T_COLS);
+    }
+}
+
+bool encode_cache(CUtensorMap* map, const void* base, const AttnArgs& a, int piece) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensormap_encoder();
+    if (enc == nullptr) return false;
+    cuuint64_t dim[3] = {(cuuint64_t)a.D, (cuuint64_t)a.H_kv * a.page_size, (cuuint64_t)a.n_pages};
+    cuuint64_t str[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.D * 2 * a.H_kv * a.page_size};
+    cuuint32_t box[3] = {64, (cuuint32_t)piece, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dim, str, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int N, int NDB>
+cudaError_t launch_tc(const AttnArgs& a, int n_cta, int piece, cudaStream_t s) {
+    using L = Layout<N, NDB>;
+    CUtensorMap km, vm;
+    if (!encode_cache(&km, a.k_cache, a, piece) || !encode_cache(&vm, a.v_cache, a, piece)) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<N, NDB>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attn_tc_kernel<N, NDB>, dim3((unsigned)n_cta), dim3(L::NT), L::SMEM, s, km, vm, a, piece);
+}
+
+template <int NDB>
+cudaError_t launch_rows(const AttnArgs& a, int n_cta, int piece, cudaStream_t s) {
+    return a.rb_rows <= 16 ? launch_tc<16, NDB>(a, n_cta, piece, s)
+         : a.rb_rows <= 32 ? launch_tc<32, NDB>(a, n_cta, piece, s)
+         : a.rb_rows <= 64 ? launch_tc<64, NDB>(a, n_cta, piece, s) : launch_tc<128, NDB>(a, n_cta, piece, s);
+}
+
+// Rows of a page that one TMA box takes: the largest power of two that divides the page size, a tile at most.
+int page_piece(int page_size) {
+    const int p = page_size & -page_size;
+    return p < TILE ? p : TILE;
+}
+
+}  // namespace
+
+bool attn_tc_takes(const AttnArgs& a, gdn_dtype_t dt) {
+    // a lane loads one piece: 32 pieces of 4 tokens make a tile
+    return dt == GDN_BF16 && page_piece(a.page_size) >= TILE / 32;
+}
+
+cudaError_t launch_attn_tc(const AttnArgs& a, int n_cta, cudaStream_t s) {
+    const int piece = page_piece(a.page_size);
+    const cudaError_t e = a.D <= 128 ? launch_rows<1>(a, n_cta, piece, s) : launch_rows<2>(a, n_cta, piece, s);
+    return e != cudaSuccess ? e : launch_attn_join(a, n_cta, TILE, GDN_BF16, s);
+}
+
+cudaError_t read_and_clear_attn_error(cudaStream_t s, int* flags) {
+    int hf = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&hf, g_attn_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return e;
+    *flags = hf;
+    if (hf != 0) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbolAsync(g_attn_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    }
+    return e;
+}
+
+}  // namespace gdn

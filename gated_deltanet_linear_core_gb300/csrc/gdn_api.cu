@@ -120,11 +120,12 @@ gdn_status_t gdn_check_cu_seqlens(const int32_t* cu, int32_t n_seq, int64_t T, v
 }
 
 gdn_status_t gdn_sync_status(void* stream) {
-    int flags = 0, cflags = 0;
+    int flags = 0, cflags = 0, aflags = 0;
     cudaError_t e = gdn::read_and_clear_device_error((cudaStream_t)stream, &flags);
     if (e == cudaSuccess) e = gdn::read_and_clear_conv_error((cudaStream_t)stream, &cflags);
+    if (e == cudaSuccess) e = gdn::read_and_clear_attn_error((cudaStream_t)stream, &aflags);
     if (e != cudaSuccess) return cuda_status(e);
-    return ((flags | cflags) & 1) ? GDN_ERR_TIMEOUT : GDN_OK;
+    return ((flags | cflags | aflags) & 1) ? GDN_ERR_TIMEOUT : GDN_OK;
 }
 
 size_t gdn_layer_prefill_host_workspace_size(int64_t T, gdn_dims_t dims, gdn_dtype_t dtype) {

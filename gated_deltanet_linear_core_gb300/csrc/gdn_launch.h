@@ -177,6 +177,10 @@ constexpr int kAttnMaxCtas = 152;  // CTAs of a call, at most: one per SM
 size_t attn_plan(AttnArgs& a, gdn_dtype_t dt);
 cudaError_t launch_attn_decode(const AttnArgs& a, gdn_dtype_t dt, cudaStream_t s);
 cudaError_t launch_attn_ffma(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaStream_t s);
+// The tensor-core kernel: which calls it takes, and its launch with the join.
+bool attn_tc_takes(const AttnArgs& a, gdn_dtype_t dt);
+cudaError_t launch_attn_tc(const AttnArgs& a, int n_cta, cudaStream_t s);
+cudaError_t read_and_clear_attn_error(cudaStream_t s, int* flags);
 cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, int tile, gdn_dtype_t dt, cudaStream_t s);
 
 // New keys and values into their pages (gdn_kv_append).
