@@ -62,8 +62,10 @@ struct Layout {
     static constexpr int SMALL = BARS + 256 + N * (4 + 4 + 4 + 8) + SCR;
     static constexpr int FIT = (kSmemMax - P_BYTES - Q_BYTES - SMALL) / SLOT;
     static constexpr int NS = FIT < 6 ? FIT : 6;
-    // S of the next tile runs ahead of P V where the ring holds that tile's K slots beside the V slots
-    static constexpr bool AHEAD = NS >= 2 * NDB;
+    // Slots are filled and used in the order K(0), K(1), V(0), K(2), V(1), .. of a segment's n tiles
+    // (S of a tile runs ahead of P V of the one before): offsets from the segment's first slot.
+    __device__ static __forceinline__ int k_slot(int j) { return j == 0 ? 0 : NDB * (2 * j - 1); }
+    __device__ static __forceinline__ int v_slot(int j, int n) { return NDB * (j + 1 < n ? 2 * j + 2 : 2 * n - 1); }
     static constexpr int O_Q = NS * SLOT;
     static constexpr int O_P = O_Q + Q_BYTES;
     static constexpr int O_BAR = O_P + P_BYTES;
@@ -246,15 +248,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     y = s.h * a.page_size + (t - pg * a.page_size);
                 }
             };
-            int y, z;
-            look_up(s.tile0, y, z);
-            for (int j = s.tile0; ok && j < s.tile1; ++j) {
-                const int left = s.len - j * TILE;
+            // K(0), then K(j + 1) and V(j): the order the MMAs take them in
+            auto load = [&](const CUtensorMap* map, int tile, int y, int z) {
+                const int left = s.len - tile * TILE;
                 const int have = left >= TILE ? np : (left + piece - 1) / piece;  // pieces with tokens
-                int yn = 0, zn = 0;
-                if (j + 1 < s.tile1) look_up(j + 1, yn, zn);
-                for (int part = 0; ok && part < 2 * NDB; ++part, ++sl) {
-                    const int st = sl % NS, db = part % NDB;
+                for (int db = 0; ok && db < NDB; ++db, ++sl) {
+                    const int st = sl % NS;
                     if (sl >= NS) {
                         ok = __all_sync(0xffffffffu, wait_or_abort(&empty[st], (uint32_t)((sl / NS - 1) & 1), abort_flag));
                         if (!ok) break;
@@ -263,12 +262,21 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(have * piece * 128 * slabs));
                     __syncwarp();
                     if (lane < have) {
-                        const CUtensorMap* map = part < NDB ? &kmap : &vmap;
                         const uint32_t dst = smem_u32(sm) + st * SLOT + lane * piece * 128;
                         for (int i = 0; i < slabs; ++i)
                             tma_load_3d(dst + i * SLAB, map, &full[st], (2 * db + i) * 64, y, z);
                     }
                 }
+            };
+            int y, z, yn = 0, zn = 0;
+            look_up(s.tile0, y, z);
+            load(&kmap, s.tile0, y, z);
+            for (int j = s.tile0; ok && j < s.tile1; ++j) {
+                if (j + 1 < s.tile1) {
+                    look_up(j + 1, yn, zn);
+                    load(&kmap, j + 1, yn, zn);
+                }
+                load(&vmap, j, y, z);
                 y = yn;
                 z = zn;
             }
@@ -281,23 +289,23 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         if (lane == 0) {
             const uint32_t base = smem_u32(sm);
             const int ksteps = (a.D + 15) / 16;
-            int it = 0, seg = 0;        // tiles and segments done
-            uint64_t* last = nullptr;   // the last commit, for the drain on abort
+            int it = 0, seg = 0, sl0 = 0;  // tiles, segments and slots before
+            uint64_t* last = nullptr;      // the last commit, for the drain on abort
             uint32_t last_parity = 0;
-            auto issue_s = [&](int t) -> bool {  // S of the CTA's tile t
+            auto slot_full = [&](int k) { return wait_or_abort(&full[k % NS], (uint32_t)((k / NS) & 1), abort_flag); };
+            auto issue_s = [&](int t, int k0) -> bool {  // S of the CTA's tile t, its K from slot k0 on
                 for (int db = 0; db < NDB; ++db) {
-                    const int k = t * 2 * NDB + db;
-                    if (!wait_or_abort(&full[k % NS], (uint32_t)((k / NS) & 1), abort_flag)) return false;
+                    const int k = k0 + db;
+                    if (!slot_full(k)) return false;
+                    tc_fence_after();
+                    const int steps = ksteps - 8 * db < 8 ? ksteps - 8 * db : 8;
+                    const uint32_t ka = base + (k % NS) * SLOT, qa = base + L::O_Q + db * 2 * (N * 128);
+                    for (int q = 0; q < steps; ++q)
+                        mma_bf16(tb + L::T_S + (t & 1) * N, sdesc_sw128(ka + (q >> 2) * SLAB + (q & 3) * 32, 16, 1024),
+                                 sdesc_sw128(qa + (q >> 2) * (N * 128) + (q & 3) * 32, 16, 1024),
+                                 idesc_bf16_f32(128, N, 0, 0), db > 0 || q > 0);
+                    mma_commit(&empty[k % NS]);
                 }
-                tc_fence_after();
-                for (int q = 0; q < ksteps; ++q) {
-                    const int k = t * 2 * NDB + q / 8;
-                    const uint32_t ka = base + (k % NS) * SLOT + ((q >> 2) & 1) * SLAB + (q & 3) * 32;
-                    const uint32_t qa = base + L::O_Q + (q >> 2) * (N * 128) + (q & 3) * 32;
-                    mma_bf16(tb + L::T_S + (t & 1) * N, sdesc_sw128(ka, 16, 1024), sdesc_sw128(qa, 16, 1024),
-                             idesc_bf16_f32(128, N, 0, 0), q > 0);
-                }
-                for (int db = 0; db < NDB; ++db) mma_commit(&empty[(t * 2 * NDB + db) % NS]);
                 mma_commit(&s_full[t & 1]);
                 last = &s_full[t & 1];
                 last_parity = (uint32_t)((t >> 1) & 1);
@@ -306,19 +314,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             bool ok = true;
             while (ok && walk.next(a, TILE, s)) {
                 if (s.len == 0) continue;
+                const int n = s.tile1 - s.tile0;
                 ok = wait_or_abort(q_full, (uint32_t)(seg & 1), abort_flag);
                 ++seg;
-                ok = ok && issue_s(it);
-                for (int j = s.tile0; ok && j < s.tile1; ++j, ++it) {
-                    if (L::AHEAD && j + 1 < s.tile1 && !issue_s(it + 1)) { ok = false; break; }
+                ok = ok && issue_s(it, sl0);
+                for (int j = 0; ok && j < n; ++j, ++it) {
+                    if (j + 1 < n && !issue_s(it + 1, sl0 + L::k_slot(j + 1))) { ok = false; break; }
                     ok = wait_or_abort(&p_full[it & 1], (uint32_t)((it >> 1) & 1), abort_flag);
                     if (!ok) break;
-                    const int left = s.len - j * TILE;
+                    const int left = s.len - (s.tile0 + j) * TILE;
                     const int pk = left >= TILE ? 8 : (left + 15) / 16;  // 16-token steps with tokens
                     const int buf = L::PBUF == 2 ? it & 1 : 0;
                     for (int db = 0; db < NDB; ++db) {
-                        const int k = it * 2 * NDB + NDB + db;
-                        if (!wait_or_abort(&full[k % NS], (uint32_t)((k / NS) & 1), abort_flag)) { ok = false; break; }
+                        const int k = sl0 + L::v_slot(j, n) + db;
+                        if (!slot_full(k)) { ok = false; break; }
                         tc_fence_after();
                         const uint32_t va = base + (k % NS) * SLOT;
                         for (int lo = 0; lo < 2; ++lo) {
@@ -326,7 +335,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             for (int q = 0; q < pk; ++q)
                                 mma_bf16(tb + L::T_O + db * N, sdesc_sw128(va + q * 2048, SLAB, 1024),
                                          sdesc_sw128(pa + q * 2048, SLAB, 1024), idesc_bf16_f32(128, N, 1, 1),
-                                         j > s.tile0 || lo > 0 || q > 0);
+                                         j > 0 || lo > 0 || q > 0);
                         }
                         mma_commit(&empty[k % NS]);
                     }
@@ -334,8 +343,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     mma_commit(&pv_done[it & 1]);
                     last = &pv_done[it & 1];
                     last_parity = (uint32_t)((it >> 1) & 1);
-                    if (!L::AHEAD && j + 1 < s.tile1 && !issue_s(it + 1)) { ok = false; break; }
                 }
+                sl0 += 2 * NDB * n;
             }
             if (*abort_flag && last != nullptr) mbar_wait(last, last_parity, kWaitNs);
         }
@@ -351,7 +360,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         int* vis_s = reinterpret_cast<int*>(sm + L::O_VIS);      // tokens a row sees
         int64_t* off_s = reinterpret_cast<int64_t*>(sm + L::O_OFF);  // element offset of a row in q, gate, out
         float* scr = reinterpret_cast<float*>(sm + L::O_SCR);    // [4 lane quarters][N]
-        int it = 0;
+        int it = 0, sl0 = 0;  // tiles and slots before
         bool live = true;  // no wait gave up: outputs are written only then
         auto wait = [&](uint64_t* bar, int k) {
             live = __all_sync(0xffffffffu, live && wait_or_abort(bar, (uint32_t)(k & 1), abort_flag));
@@ -476,7 +485,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     const int valid = min(TILE, s.len - t0);
                     const int from = max(0, max(0, s.len - a.K + 1) - t0), upto = (valid + 15) & ~15;
                     for (int db = 0; db < NDB; ++db) {
-                        const int k = it * 2 * NDB + NDB + db;
+                        const int k = sl0 + L::v_slot(j - s.tile0, s.tile1 - s.tile0) + db;
                         wait(&full[k % NS], k / NS);
                         const int slabs = nslab - 2 * db < 2 ? nslab - 2 * db : 2;
                         for (int e = st; e < (upto - from) * slabs * 8; e += NSOFT) {
@@ -500,6 +509,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[it & 1]);
             }
+
+            sl0 += 2 * NDB * (s.tile1 - s.tile0);
 
             // ---- sums over the tokens: lanes by a butterfly that halves the columns, then the warps
             wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
