@@ -282,77 +282,94 @@ __global__ void __launch_bounds__(NT, 1) attn_ffma_kernel(AttnArgs a) {
     }
 }
 
-// Joins the parts of every item that more than one CTA worked on.  Block
-// (c - 1, y): the item that CTA c's range starts inside of, if c is the first
-// such CTA of it; rows y, y + gridDim.y, ...  The parts are added in CTA
-// order, so results do not depend on timing.
+// Joins the parts of every item that more than one CTA worked on.  The CTAs
+// whose ranges start inside an item (blockIdx.x + 1) share its rows, gridDim.y
+// blocks each.  A group of D / 4 threads takes a row, 4 columns per thread, and
+// runs through the parts in CTA order (with more than kSerial of them, the
+// groups of a block share one row's parts), keeping the running maximum, sum
+// and output as the tiles do; the order is fixed, so results do not depend on
+// timing.  Where the item lies is worked out before the wait for the kernel
+// that wrote the parts: the lengths are older than that kernel.
 constexpr int JT = 256;
+constexpr int kSerial = 8;
+struct Running {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    __device__ __forceinline__ void add(float m1, float l1, float4 x) {
+        const float top = fmaxf(m, m1);
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float f = exp2f(m - ref), w = exp2f(m1 - ref);
+        m = top;
+        l = l * f + l1 * w;
+        o.x = o.x * f + x.x * w; o.y = o.y * f + x.y * w; o.z = o.z * f + x.z * w; o.w = o.w * f + x.w * w;
+    }
+};
 template <typename T>
 __global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a, int n_cta, int tile) {
-    __shared__ int64_t sh[JT + 4];
-    __shared__ float acc_s[JT * 4];
-    __shared__ float w_s[kAttnMaxCtas];
-    __shared__ float ml[2];
+    __shared__ float4 o_s[JT];
+    __shared__ float2 ml_s[JT];
     const int tid = threadIdx.x, c = blockIdx.x + 1;
-    pdl_wait();
-    pdl_trigger();
-    const Place p = find_place<JT>(a, tile, c, n_cta, sh);
+    const Place p = find_place<JT>(a, tile, c, n_cta, reinterpret_cast<int64_t*>(o_s));
     if (c >= n_cta) return;
     Walk walk(p, cta_begin(p.total, c, n_cta), cta_begin(p.total, c + 1, n_cta));
     Segment s;
     const int64_t u = walk.at;
     if (!walk.next(a, tile, s) || s.tile0 == 0) return;  // the range starts with an item of its own
     const int64_t u0 = u - s.tile0, u1 = u0 + s.tiles;
-    const int c0 = cta_of(p.total, u0, n_cta);
-    if (c0 != c - 1) return;
-    const int c1 = cta_of(p.total, u1 - 1, n_cta);
+    const int c0 = cta_of(p.total, u0, n_cta), c1 = cta_of(p.total, u1 - 1, n_cta);
     const int first_slot = cta_begin(p.total, c0, n_cta) == u0 ? 2 * c0 : 2 * c0 + 1;
     const int n = c1 - c0 + 1;
-    const int D = a.D, ng = D / 4, nsplit = JT / ng, grp = tid % ng, split = tid / ng;
+    const int D = a.D, ng = D / 4, groups = JT / ng, grp = tid % ng, g = tid / ng;
     const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
-    auto part = [&](int i) { return slot_ptr(a, i == 0 ? first_slot : 2 * (c0 + i)); };
-    for (int r = blockIdx.y; r < nr; r += gridDim.y) {
-        if (tid < 32) {
-            float m = -INFINITY, l = 0.f;
-            for (int i = tid; i < n; i += 32) m = fmaxf(m, part(i)[r]);
+    const int workers = (n - 1) * gridDim.y, worker = (c - c0 - 1) * gridDim.y + blockIdx.y;
+    const int share = n > kSerial ? groups : 1;  // groups on one row
+    const int at_once = groups / share, sub = g % share;
+    pdl_wait();
+    pdl_trigger();
+    for (int first = worker * at_once; first < nr; first += workers * at_once) {
+        const int r = first + g / share;
+        const bool mine = g < groups && r < nr;
+        Running run;
+        if (mine) {
+            constexpr int U = 4;
+            for (int i = sub; i < n; i += U * share) {
+                float m[U], l[U];
+                float4 x[U];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float ref = m == -INFINITY ? 0.f : m;
-            for (int i = tid; i < n; i += 32) {
-                const float w = exp2f(part(i)[r] - ref);
-                w_s[i] = w;
-                l += w * part(i)[a.rb_rows + r];
-            }
-            l = warp_sum(l);
-            if (tid == 0) {
-                ml[0] = m;
-                ml[1] = l;
+                for (int k = 0; k < U; ++k) {
+                    const int part = i + k * share;
+                    if (part < n) {
+                        const float* slot = slot_ptr(a, part == 0 ? first_slot : 2 * (c0 + part));
+                        m[k] = slot[r];
+                        l[k] = slot[a.rb_rows + r];
+                        x[k] = *reinterpret_cast<const float4*>(slot + a.stat_floats + r * D + grp * 4);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+                    if (i + k * share < n) run.add(m[k], l[k], x[k]);
             }
         }
-        __syncthreads();
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (split < nsplit) {
-#pragma unroll 4
-            for (int i = split; i < n; i += nsplit) {
-                const float w = w_s[i];
-                const float4 x = *reinterpret_cast<const float4*>(part(i) + a.stat_floats + r * D + grp * 4);
-                // a part that saw nothing has weight 0 and outputs 0
-                o.x = fmaf(w, x.x, o.x); o.y = fmaf(w, x.y, o.y); o.z = fmaf(w, x.z, o.z); o.w = fmaf(w, x.w, o.w);
+        if (share > 1) {
+            o_s[tid] = run.o;
+            ml_s[tid] = make_float2(run.m, run.l);
+            __syncthreads();
+            if (mine && sub == 0)
+                for (int i = 1; i < share; ++i) run.add(ml_s[tid + i * ng].x, ml_s[tid + i * ng].y, o_s[tid + i * ng]);
+            __syncthreads();
+        }
+        if (mine && sub == 0) {
+            const int64_t row = row_index(a, s.b, s.h, r0 + r);
+            const int64_t at = row * D + grp * 4;
+            const float inv = run.l == 0.f ? 0.f : 1.0f / run.l;
+            float y[4] = {run.o.x * inv, run.o.y * inv, run.o.z * inv, run.o.w * inv};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (a.gate != nullptr) y[k] *= sigmoid_f(to_f(static_cast<const T*>(a.gate)[at + k]));
+                static_cast<T*>(a.out)[at + k] = from_f<T>(y[k]);
             }
-            *reinterpret_cast<float4*>(acc_s + (split * ng + grp) * 4) = o;
+            if (grp == 0 && a.lse != nullptr) a.lse[row] = run.l == 0.f ? -INFINITY : (run.m + log2f(run.l)) * kLn2;
         }
-        __syncthreads();
-        const int64_t row = row_index(a, s.b, s.h, r0 + r);
-        const float l = ml[1];
-        for (int d = tid; d < D; d += JT) {
-            float x = 0.f;
-            for (int sp = 0; sp < nsplit; ++sp) x += acc_s[sp * D + d];
-            x = l > 0.f ? x / l : (l == 0.f ? 0.f : x);
-            if (a.gate != nullptr) x *= sigmoid_f(to_f(static_cast<const T*>(a.gate)[row * D + d]));
-            static_cast<T*>(a.out)[row * D + d] = from_f<T>(x);
-        }
-        if (tid == 0 && a.lse != nullptr) a.lse[row] = l == 0.f ? -INFINITY : (ml[0] + log2f(l)) * kLn2;
-        __syncthreads();
     }
 }
 
@@ -378,7 +395,7 @@ cudaError_t launch_ffma_rows(const AttnArgs& a, int n_cta, cudaStream_t s) {
 
 cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, int tile, gdn_dtype_t dt, cudaStream_t s) {
     if (n_cta <= 1) return cudaSuccess;
-    const dim3 grid((unsigned)(n_cta - 1), (unsigned)(a.rb_rows < 16 ? a.rb_rows : 16));
+    const dim3 grid((unsigned)(n_cta - 1), (unsigned)((a.rb_rows + 15) / 16));
     return dt == GDN_BF16 ? launch_pdl(attn_join_kernel<bf16>, grid, dim3(JT), 0, s, a, n_cta, tile)
                           : launch_pdl(attn_join_kernel<float>, grid, dim3(JT), 0, s, a, n_cta, tile);
 }
