@@ -173,6 +173,20 @@ __device__ __forceinline__ uint32_t zero_non_finite(uint32_t w) {
     return w;
 }
 
+// Operand descriptors by their low words (address and lbo in units of 16 bytes); the high word is the same for
+// all (sbo 1024, version, 128-byte swizzle: sdesc_sw128).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+__device__ __forceinline__ void mma_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(hi)
+        : "memory");
+}
+
 template <int N, int NDB>
 __global__ void __launch_bounds__(Layout<N, NDB>::NT, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a,
@@ -292,18 +306,23 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             int it = 0, seg = 0, sl0 = 0;  // tiles, segments and slots before
             uint64_t* last = nullptr;      // the last commit, for the drain on abort
             uint32_t last_parity = 0;
+            // the issue loops are unrolled and step the descriptors by constants (their address field counts 16
+            // bytes): with descriptors built per MMA, one thread's issue rate, 60 ns each, was the tile's bound
             auto slot_full = [&](int k) { return wait_or_abort(&full[k % NS], (uint32_t)((k / NS) & 1), abort_flag); };
             auto issue_s = [&](int t, int k0) -> bool {  // S of the CTA's tile t, its K from slot k0 on
                 for (int db = 0; db < NDB; ++db) {
                     const int k = k0 + db;
                     if (!slot_full(k)) return false;
                     tc_fence_after();
-                    const int steps = ksteps - 8 * db < 8 ? ksteps - 8 * db : 8;
-                    const uint32_t ka = base + (k % NS) * SLOT, qa = base + L::O_Q + db * 2 * (N * 128);
-                    for (int q = 0; q < steps; ++q)
-                        mma_bf16(tb + L::T_S + (t & 1) * N, sdesc_sw128(ka + (q >> 2) * SLAB + (q & 3) * 32, 16, 1024),
-                                 sdesc_sw128(qa + (q >> 2) * (N * 128) + (q & 3) * 32, 16, 1024),
-                                 idesc_bf16_f32(128, N, 0, 0), db > 0 || q > 0);
+                    const int steps = ksteps - 8 * db;
+                    const uint32_t ka = desc_lo(base + (k % NS) * SLOT, 16);
+                    const uint32_t qa = desc_lo(base + L::O_Q + db * 2 * (N * 128), 16);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (q < steps)
+                            mma_lo(tb + L::T_S + (t & 1) * N, ka + (((q >> 2) * SLAB + (q & 3) * 32) >> 4),
+                                     qa + (((q >> 2) * (N * 128) + (q & 3) * 32) >> 4), idesc_bf16_f32(128, N, 0, 0),
+                                     db > 0 || q > 0);
                     mma_commit(&empty[k % NS]);
                 }
                 mma_commit(&s_full[t & 1]);
@@ -329,13 +348,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         const int k = sl0 + L::v_slot(j, n) + db;
                         if (!slot_full(k)) { ok = false; break; }
                         tc_fence_after();
-                        const uint32_t va = base + (k % NS) * SLOT;
+                        const uint32_t va = desc_lo(base + (k % NS) * SLOT, SLAB);
+#pragma unroll
                         for (int lo = 0; lo < 2; ++lo) {
-                            const uint32_t pa = base + L::O_P + L::p_start(buf, lo);
-                            for (int q = 0; q < pk; ++q)
-                                mma_bf16(tb + L::T_O + db * N, sdesc_sw128(va + q * 2048, SLAB, 1024),
-                                         sdesc_sw128(pa + q * 2048, SLAB, 1024), idesc_bf16_f32(128, N, 1, 1),
-                                         j > 0 || lo > 0 || q > 0);
+                            const uint32_t pa = desc_lo(base + L::O_P + L::p_start(buf, lo), SLAB);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                if (q < pk)
+                                    mma_lo(tb + L::T_O + db * N, va + q * (2048 >> 4), pa + q * (2048 >> 4),
+                                             idesc_bf16_f32(128, N, 1, 1), j > 0 || lo > 0 || q > 0);
                         }
                         mma_commit(&empty[k % NS]);
                     }
