@@ -14,6 +14,7 @@ g = -exp(A_log) softplus(a+dt_bias), beta = sigmoid(b) -> gated delta rule
 from __future__ import annotations
 
 from dataclasses import dataclass
+from functools import lru_cache
 
 import torch
 
@@ -529,23 +530,28 @@ def gdn_layer_decode(x, z, a, b, conv_w, A_log, dt_bias, norm_w, dims, state, co
     return gdn_rmsnorm_gated(o, z, norm_w, dims, stream=stream)
 
 
-def _one_device(first, *rest):
-    """The device of the tensors (None among them is skipped); they must share it."""
-    dev = first.device
-    for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices ({dev} and {t.device})")
-    return dev
+def _dptr(t, name, dev, dtype, shape=None):
+    """_ptr for a tensor that must lie on CUDA device number `dev`.  One pass of
+    cheap checks; what fails them goes through _ptr's for its message (a call's
+    tensors are looked at in about 0.3 us each, and a decode step has a dozen)."""
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and (dtype is None or t.dtype is dtype)
+            and t.is_contiguous() and (shape is None or t.shape == shape)):
+        return t.data_ptr() or None
+    if isinstance(t, torch.Tensor) and t.get_device() != dev:
+        raise ValueError(f"{name}: tensors on different devices (cuda:{dev} and {t.device})")
+    return _ptr(t, name, dtype, shape)
 
 
-def _call_on(dev, stream, body):
-    """body(raw stream) with `dev` current and, where the caller names a stream,
-    that stream current too, so that outputs and workspaces allocated in body
-    belong to the stream that uses them."""
-    if dev.type != "cuda":
-        raise ValueError(f"tensors must be CUDA tensors (got {dev})")
-    if stream is None and torch.cuda.current_device() == dev.index:
-        return body(torch.cuda.current_stream(dev).cuda_stream)
+def _on_stream(dev, stream, body):
+    """body(raw stream) with device number `dev` current and, where the caller
+    names a stream, that stream current too, so that outputs and workspaces
+    allocated in body belong to the stream that uses them."""
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    if stream is None and torch._C._cuda_getDevice() == dev:
+        return body(torch._C._cuda_getCurrentRawStream(dev))
     with torch.cuda.device(dev):
         if stream is None:
             return body(torch.cuda.current_stream(dev).cuda_stream)
@@ -556,11 +562,12 @@ def _call_on(dev, stream, body):
 
 
 def _cache_dims(k_cache, v_cache, page_table, seq_lens):
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    cs, ts = k_cache.shape, page_table.shape
+    if len(cs) != 4 or v_cache.shape != cs:
         raise ValueError("k_cache, v_cache: expected [n_pages, H_kv, page_size, D], both alike")
-    if page_table.dim() != 2 or seq_lens.dim() != 1 or seq_lens.shape[0] != page_table.shape[0]:
+    if len(ts) != 2 or seq_lens.shape != ts[:1]:
         raise ValueError("page_table: expected [B, max_pages]; seq_lens: [B]")
-    return tuple(k_cache.shape) + tuple(page_table.shape)
+    return (*cs, *ts)
 
 
 def gdn_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None, stream=None):
@@ -569,27 +576,33 @@ def gdn_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None,
     of sequence b (cu_seqlens int32 [B + 1], or T / B each) end at position
     seq_lens[b] (int32 [B], new tokens counted); page_table int32 [B, max_pages].
     Returns (k_cache, v_cache)."""
-    dt = k.dtype
+    dt, i32, dev = k.dtype, torch.int32, k.get_device()
     n_pages, H, ps, D, B, mp = _cache_dims(k_cache, v_cache, page_table, seq_lens)
     if k.dim() != 3:
         raise ValueError("k: expected [T, H_kv, D]")
-    T = int(k.shape[0])
-    if cu_seqlens is not None and tuple(cu_seqlens.shape) != (B + 1,):
-        raise ValueError(f"cu_seqlens: shape {tuple(cu_seqlens.shape)}, expected {(B + 1,)}")
-    dev = _one_device(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens)
-    st = _call_on(dev, stream, lambda s: _lib.load().gdn_kv_append(
-        _ptr(k, "k", dt, (T, H, D)), _ptr(v, "v", dt, (T, H, D)), _ptr(k_cache, "k_cache", dt),
-        _ptr(v_cache, "v_cache", dt), _ptr(page_table, "page_table", torch.int32),
-        _ptr(seq_lens, "seq_lens", torch.int32), _ptr(cu_seqlens, "cu_seqlens", torch.int32), B, T, H, D, ps,
-        n_pages, mp, _dtype_code(k), s))
-    _lib.check(st, "gdn_kv_append")
+    T = k.shape[0]
+
+    def body(s):
+        return _lib.load().gdn_kv_append(
+            _dptr(k, "k", dev, dt, (T, H, D)), _dptr(v, "v", dev, dt, (T, H, D)), _dptr(k_cache, "k_cache", dev, dt),
+            _dptr(v_cache, "v_cache", dev, dt), _dptr(page_table, "page_table", dev, i32),
+            _dptr(seq_lens, "seq_lens", dev, i32), _dptr(cu_seqlens, "cu_seqlens", dev, i32, (B + 1,)), B, T, H, D,
+            ps, n_pages, mp, _dtype_code(k), s)
+
+    st = _on_stream(dev, stream, body)
+    if st:
+        _lib.check(st, "gdn_kv_append")
     return k_cache, v_cache
 
 
+@lru_cache(maxsize=256)
+def _attn_workspace(B, K, H_q, H_kv, D, page_size, code):
+    return int(_lib.load().gdn_attn_decode_workspace_size(B, K, H_q, H_kv, D, page_size, code))
+
+
 def gdn_attn_decode_workspace_size(B: int, K: int, H_q: int, H_kv: int, D: int, page_size: int, dtype) -> int:
-    code = _lib.GDN_BF16 if dtype == torch.bfloat16 else _lib.GDN_F32
-    return int(_lib.load().gdn_attn_decode_workspace_size(int(B), int(K), int(H_q), int(H_kv), int(D),
-                                                          int(page_size), code))
+    return _attn_workspace(int(B), int(K), int(H_q), int(H_kv), int(D), int(page_size),
+                           _lib.GDN_BF16 if dtype == torch.bfloat16 else _lib.GDN_F32)
 
 
 def gdn_attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=0.0, gate=None, out=None, lse=None,
@@ -599,31 +612,32 @@ def gdn_attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=0.0, gate=N
     (gdn_kv_append); K = 1 is a decode step, K up to 16 a verification pass.
     gate [B, K, H_q, D]: out = attention * sigmoid(gate).  Returns out
     [B, K, H_q, D], with return_lse also lse [B, K, H_q] f32."""
-    dt = q.dtype
+    dt, i32, dev = q.dtype, torch.int32, q.get_device()
     n_pages, H, ps, D, B, mp = _cache_dims(k_cache, v_cache, page_table, seq_lens)
-    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D:
-        raise ValueError(f"q: shape {tuple(q.shape)}, expected [{B}, K, H_q, {D}]")
-    K, H_q = int(q.shape[1]), int(q.shape[2])
-    shape = (B, K, H_q, D)
-    dev = _one_device(q, k_cache, v_cache, page_table, seq_lens, gate, out, lse, workspace)
-    lib, code = _lib.load(), _dtype_code(q)
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or shape[3] != D:
+        raise ValueError(f"q: shape {tuple(shape)}, expected [{B}, K, H_q, {D}]")
+    K, H_q = shape[1], shape[2]
+    code = _dtype_code(q)
 
     def body(s):
         o = torch.empty_like(q) if out is None else out
-        e = torch.empty(shape[:3], dtype=torch.float32, device=dev) if lse is None and return_lse else lse
+        e = q.new_empty(shape[:3], dtype=torch.float32) if lse is None and return_lse else lse
+        # one batch size stands for all: the size goes by the head layout and K
         ws = workspace
         if ws is None:
-            need = lib.gdn_attn_decode_workspace_size(B, K, H_q, H, D, ps, code)
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        st = lib.gdn_attn_decode(
-            _ptr(q, "q", dt), _ptr(k_cache, "k_cache", dt), _ptr(v_cache, "v_cache", dt),
-            _ptr(page_table, "page_table", torch.int32), _ptr(seq_lens, "seq_lens", torch.int32), float(scale),
-            _ptr(gate, "gate", dt, shape), _ptr(o, "out", dt, shape), _ptr(e, "lse", torch.float32, shape[:3]),
-            B, K, H_q, H, D, ps, n_pages, mp, _ptr(ws, "workspace"), ws.numel() * ws.element_size(), code, s)
-        _lib.check(st, "gdn_attn_decode")
+            ws = q.new_empty(_attn_workspace(min(B, 1), K, H_q, H, D, ps, code), dtype=torch.uint8)
+        st = _lib.load().gdn_attn_decode(
+            _dptr(q, "q", dev, dt), _dptr(k_cache, "k_cache", dev, dt), _dptr(v_cache, "v_cache", dev, dt),
+            _dptr(page_table, "page_table", dev, i32), _dptr(seq_lens, "seq_lens", dev, i32), scale,
+            _dptr(gate, "gate", dev, dt, shape), _dptr(o, "out", dev, dt, shape),
+            _dptr(e, "lse", dev, torch.float32, shape[:3]), B, K, H_q, H, D, ps, n_pages, mp,
+            _dptr(ws, "workspace", dev, None), ws.numel() * ws.element_size(), code, s)
+        if st:
+            _lib.check(st, "gdn_attn_decode")
         return (o, e) if return_lse else o
 
-    return _call_on(dev, stream, body)
+    return _on_stream(dev, stream, body)
 
 
 def gdn_draft_accept(target_probs, draft_probs, draft_tokens, uniforms, n_draft=None, slots=None, n_accept=None,
@@ -635,27 +649,28 @@ def gdn_draft_accept(target_probs, draft_probs, draft_tokens, uniforms, n_draft=
     gdn_decode_verify call over the K + 1 tokens.  Returns (n_accept [B], tokens
     [B, K + 1]: held drafts, next token, then -1; next_slot [B]: slots[b, n + 1],
     None without slots), all int32."""
-    dt = target_probs.dtype
+    dt, i32, dev = target_probs.dtype, torch.int32, target_probs.get_device()
     if target_probs.dim() != 3 or target_probs.shape[1] < 1:
         raise ValueError("target_probs: expected [B, K + 1, V]")
-    B, K, V = int(target_probs.shape[0]), int(target_probs.shape[1]) - 1, int(target_probs.shape[2])
-    dev = _one_device(target_probs, draft_probs, draft_tokens, uniforms, n_draft, slots, n_accept, tokens, next_slot)
+    B, K1, V = target_probs.shape
+    K = K1 - 1
 
     def body(s):
-        i32 = torch.int32
-        n = torch.empty(B, dtype=i32, device=dev) if n_accept is None else n_accept
-        tk = torch.empty((B, K + 1), dtype=i32, device=dev) if tokens is None else tokens
-        ns = torch.empty(B, dtype=i32, device=dev) if next_slot is None and slots is not None else next_slot
+        n = uniforms.new_empty(B, dtype=i32) if n_accept is None else n_accept
+        tk = uniforms.new_empty((B, K1), dtype=i32) if tokens is None else tokens
+        ns = uniforms.new_empty(B, dtype=i32) if next_slot is None and slots is not None else next_slot
         st = _lib.load().gdn_draft_accept(
-            _ptr(target_probs, "target_probs", dt), _ptr(draft_probs, "draft_probs", dt, (B, K, V)),
-            _ptr(draft_tokens, "draft_tokens", i32, (B, K)), _ptr(uniforms, "uniforms", torch.float32, (B, K + 1)),
-            _ptr(n_draft, "n_draft", i32, (B,)), _ptr(slots, "slots", i32, (B, K + 2)), B, K, V,
-            _ptr(n, "n_accept", i32, (B,)), _ptr(tk, "tokens", i32, (B, K + 1)), _ptr(ns, "next_slot", i32, (B,)),
+            _dptr(target_probs, "target_probs", dev, dt), _dptr(draft_probs, "draft_probs", dev, dt, (B, K, V)),
+            _dptr(draft_tokens, "draft_tokens", dev, i32, (B, K)),
+            _dptr(uniforms, "uniforms", dev, torch.float32, (B, K1)), _dptr(n_draft, "n_draft", dev, i32, (B,)),
+            _dptr(slots, "slots", dev, i32, (B, K + 2)), B, K, V, _dptr(n, "n_accept", dev, i32, (B,)),
+            _dptr(tk, "tokens", dev, i32, (B, K1)), _dptr(ns, "next_slot", dev, i32, (B,)),
             _dtype_code(target_probs), s)
-        _lib.check(st, "gdn_draft_accept")
+        if st:
+            _lib.check(st, "gdn_draft_accept")
         return n, tk, ns
 
-    return _call_on(dev, stream, body)
+    return _on_stream(dev, stream, body)
 
 
 @dataclass(frozen=True)

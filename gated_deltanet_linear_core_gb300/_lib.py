@@ -89,6 +89,8 @@ def load() -> ctypes.CDLL:
     """Load libgdn.so (built in-tree by gated_deltanet_linear_core_gb300.build).
     Raises if it is missing: there is no fallback implementation."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
