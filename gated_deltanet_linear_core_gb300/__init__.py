@@ -622,11 +622,11 @@ def gdn_attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=0.0, gate=N
 
     def body(s):
         o = torch.empty_like(q) if out is None else out
-        e = q.new_empty(shape[:3], dtype=torch.float32) if lse is None and return_lse else lse
+        e = torch.empty(shape[:3], dtype=torch.float32, device=q.device) if lse is None and return_lse else lse
         # one batch size stands for all: the size goes by the head layout and K
         ws = workspace
         if ws is None:
-            ws = q.new_empty(_attn_workspace(min(B, 1), K, H_q, H, D, ps, code), dtype=torch.uint8)
+            ws = torch.empty(_attn_workspace(min(B, 1), K, H_q, H, D, ps, code), dtype=torch.uint8, device=q.device)
         st = _lib.load().gdn_attn_decode(
             _dptr(q, "q", dev, dt), _dptr(k_cache, "k_cache", dev, dt), _dptr(v_cache, "v_cache", dev, dt),
             _dptr(page_table, "page_table", dev, i32), _dptr(seq_lens, "seq_lens", dev, i32), scale,
@@ -653,12 +653,12 @@ def gdn_draft_accept(target_probs, draft_probs, draft_tokens, uniforms, n_draft=
     if target_probs.dim() != 3 or target_probs.shape[1] < 1:
         raise ValueError("target_probs: expected [B, K + 1, V]")
     B, K1, V = target_probs.shape
-    K = K1 - 1
+    K, on = K1 - 1, target_probs.device
 
     def body(s):
-        n = uniforms.new_empty(B, dtype=i32) if n_accept is None else n_accept
-        tk = uniforms.new_empty((B, K1), dtype=i32) if tokens is None else tokens
-        ns = uniforms.new_empty(B, dtype=i32) if next_slot is None and slots is not None else next_slot
+        n = torch.empty(B, dtype=i32, device=on) if n_accept is None else n_accept
+        tk = torch.empty((B, K1), dtype=i32, device=on) if tokens is None else tokens
+        ns = torch.empty(B, dtype=i32, device=on) if next_slot is None and slots is not None else next_slot
         st = _lib.load().gdn_draft_accept(
             _dptr(target_probs, "target_probs", dev, dt), _dptr(draft_probs, "draft_probs", dev, dt, (B, K, V)),
             _dptr(draft_tokens, "draft_tokens", dev, i32, (B, K)),

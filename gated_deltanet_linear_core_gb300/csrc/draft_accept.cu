@@ -8,12 +8,17 @@
 // emitted tokens are then distributed as the target's own samples.
 //
 // Borders are decided exactly: u q and p - q are formed without rounding and
-// the sums carry their rounding errors, so the pick does not depend on how the
-// row is split.  Only row n is read (and q's when a draft failed): one cluster
-// of kCluster CTAs per sequence, the row cut into segments of SEG values whose
-// sums stay in shared memory; the CTAs exchange their totals through
-// distributed shared memory, and the warp that owns the segment with the
-// border reads that one again.
+// the sums carry their rounding errors (two f32 per sum; f64 adds would take
+// longer than reading the row), so the pick does not depend on how the row is
+// split.
+//
+// Only row n is read (and q's when a draft failed), so a batch is bound by HBM
+// and a single sequence by latency: one cluster of kCluster CTAs per sequence,
+// the row cut into segments of SEG values whose sums stay in shared memory; each
+// CTA writes its total into the shared memory of all, and the warp that owns the
+// segment with the border reads that one again.  A warp takes 16 bytes per lane
+// and load, several loads in flight; rows that do not start on 16 bytes are
+// read value by value in the same order.
 #include <cooperative_groups.h>
 
 #include "gdn_common.cuh"
@@ -25,19 +30,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int NT = 512;
+constexpr int NT = 256;
 constexpr int kCluster = 8;
-constexpr int SEG = 1024;          // values per segment
-constexpr int PER = SEG / 32;      // per lane when a segment is searched
+constexpr int SEG = 1024;  // values per segment
 
-template <typename T>
-__device__ __forceinline__ float ldg_f(const T* p) { return to_f(__ldg(p)); }
-template <>
-__device__ __forceinline__ float ldg_f<bf16>(const bf16* p) {
-    return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p)) << 16);
-}
-
-// A row r(v) = (p(v) - q(v))+, q: a row, or `hot` at one index, or nothing.
+// A row r(v) = (p(v) - q(v))+, q: a row, or 1 at `hot`, or nothing.
 template <typename T>
 struct Row {
     const T *p, *q;
@@ -62,47 +59,40 @@ __device__ __forceinline__ void add_diff(Sum2& a, float p, float q) {
     const float e = (p - (d - b)) - (q + b);
     if (p > q) a.add(d, e);
 }
-__device__ __forceinline__ double diff_of(float p, float q) { return p > q ? (double)p - (double)q : 0.0; }
 
-// Sum of the segment's values [v0, v1) by one warp.
-// Reads 16 bytes at a time where VEC.
+// The 16 bytes of values at `at` on, those from V on 0.
 template <typename T, bool VEC>
-__device__ __forceinline__ double segment_sum(const Row<T>& r, int v0, int v1, int lane) {
-    Sum2 acc;
-    constexpr int N = VEC ? Vec16<T>::N : 1;
-    constexpr int U = VEC ? (SEG / 32 / N < 8 ? SEG / 32 / N : 8) : 8;  // loads in flight
-    for (int v = v0 + lane * N; v < v1; v += 32 * N * U) {
-        float p[U][N], q[U][N];
+__device__ __forceinline__ void load_row(const T* p, int at, int V, float (&x)[Vec16<T>::N]) {
+    constexpr int N = Vec16<T>::N;
+    if constexpr (VEC) {
+        if (at < V) {  // V is a multiple of N
+            unpack16<T>(__ldg(reinterpret_cast<const uint4*>(p + at)), x);
+        } else {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int at = v + i * 32 * N;
-            if constexpr (VEC) {
-                if (at < v1) {
-                    unpack16<T>(__ldg(reinterpret_cast<const uint4*>(r.p + at)), p[i]);
-                    if (r.q != nullptr) unpack16<T>(__ldg(reinterpret_cast<const uint4*>(r.q + at)), q[i]);
-                }
-            } else {
-                if (at < v1) {
-                    p[i][0] = ldg_f(r.p + at);
-                    if (r.q != nullptr) q[i][0] = ldg_f(r.q + at);
-                }
-            }
+            for (int j = 0; j < N; ++j) x[j] = 0.f;
         }
+    } else {
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const int at = v + i * 32 * N + j;
-                if (v + i * 32 * N >= v1) break;
-                add_diff(acc, p[i][j], r.q != nullptr ? q[i][j] : (at == r.hot ? 1.f : 0.f));
-            }
+        for (int j = 0; j < N; ++j) x[j] = at + j < V ? to_f(p[at + j]) : 0.f;
     }
-    double t = acc.total();
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_pq(const Row<T>& r, int at, int V, float (&p)[Vec16<T>::N],
+                                        float (&q)[Vec16<T>::N]) {
+    load_row<T, VEC>(r.p, at, V, p);
+    if (r.q != nullptr) {
+        load_row<T, VEC>(r.q, at, V, q);
+    } else {
+#pragma unroll
+        for (int j = 0; j < Vec16<T>::N; ++j) q[j] = at + j == r.hot ? 1.f : 0.f;
+    }
+}
+
+__device__ __forceinline__ double warp_total(double t) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     return t;
 }
-
 __device__ __forceinline__ double warp_scan(double x, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -112,10 +102,86 @@ __device__ __forceinline__ double warp_scan(double x, int lane) {
     return x;
 }
 
+// Sum of the segment from v0 on, by one warp.
 template <typename T, bool VEC>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(NT) draft_accept_kernel(DraftAcceptArgs a) {
-    extern __shared__ double seg_s[];  // sums of this CTA's segments
-    __shared__ double total_s;         // their sum
+__device__ __forceinline__ double segment_sum(const Row<T>& r, int v0, int V, int lane) {
+    constexpr int N = Vec16<T>::N, IT = SEG / 32 / N, U = N == 4 ? 4 : 2;
+    Sum2 acc;
+#pragma unroll 1
+    for (int i = 0; i < IT; i += U) {
+        float p[U][N], q[U][N];
+#pragma unroll
+        for (int k = 0; k < U; ++k) load_pq<T, VEC>(r, v0 + ((i + k) * 32 + lane) * N, V, p[k], q[k]);
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int j = 0; j < N; ++j) add_diff(acc, p[k][j], q[k][j]);
+    }
+    return warp_total(acc.total());
+}
+
+// The first value of the segment from v0 on at which the running sum, `run`
+// before the segment, passes the border (by one warp).
+template <typename T, bool VEC>
+__device__ __forceinline__ int pick(const Row<T>& r, int v0, int V, double run, double border, int lane) {
+    constexpr int N = Vec16<T>::N, IT = SEG / 32 / N;
+    double part[IT];
+    int last = -1;  // this lane's last value with weight
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        float p[N], q[N];
+        const int at = v0 + (i * 32 + lane) * N;
+        load_pq<T, VEC>(r, at, V, p, q);
+        Sum2 acc;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            add_diff(acc, p[j], q[j]);
+            if (p[j] > q[j]) last = at + j;
+        }
+        part[i] = acc.total();
+    }
+    int it = -1;
+    double mine = 0.0;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const double t = warp_total(part[i]);
+        if (it < 0) {
+            if (run + t > border) {
+                it = i;
+                mine = part[i];
+            } else {
+                run += t;
+            }
+        }
+    }
+    if (it >= 0) {
+        const double upto = run + warp_scan(mine, lane);
+        const uint32_t past = __ballot_sync(0xffffffffu, upto > border);
+        double before = __shfl_up_sync(0xffffffffu, upto, 1);
+        if (lane == 0) before = run;
+        int token = -1;
+        if (past != 0 && lane == __ffs(past) - 1) {
+            float p[N], q[N];
+            const int at = v0 + (it * 32 + lane) * N;
+            load_pq<T, VEC>(r, at, V, p, q);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                if (p[j] > q[j] && !(token >= 0 && before > border)) {
+                    before += (double)p[j] - (double)q[j];
+                    token = at + j;
+                }
+            }
+        }
+        if (past != 0) return __shfl_sync(0xffffffffu, token, __ffs(past) - 1);
+    }
+    // rounding left the border at the segment's very end: its last value with weight
+    return __reduce_max_sync(0xffffffffu, last);
+}
+
+template <typename T, bool VEC>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(NT, 4) draft_accept_kernel(DraftAcceptArgs a) {
+    extern __shared__ double seg_s[];         // running sums of this CTA's segments
+    __shared__ double total_s[2][kCluster];   // the CTAs' sums, one set per pass
     __shared__ int n_s, drafts_s;
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -123,22 +189,22 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(NT) draft_acc
     const int K = a.K, V = a.V;
     const T* p = static_cast<const T*>(a.p) + (int64_t)b * (K + 1) * V;
     const T* q = a.q == nullptr ? nullptr : static_cast<const T*>(a.q) + (int64_t)b * K * V;
+    cluster.barrier_arrive();  // waited for before the first write into another CTA's shared memory
     pdl_wait();
     pdl_trigger();
+    const double u = a.u[(int64_t)b * (K + 1) + K];
 
     if (warp == 0) {
-        int drafts = K;
-        if (a.n_draft != nullptr) {
-            drafts = a.n_draft[b];
-            drafts = drafts < 0 ? 0 : (drafts > K ? K : drafts);
-        }
+        int drafts = a.n_draft == nullptr ? K : a.n_draft[b];
+        drafts = drafts < 0 ? 0 : (drafts > K ? K : drafts);
         bool holds = false;
-        if (lane < drafts) {
+        if (lane < K) {
             const int d = a.draft[(int64_t)b * K + lane];
+            const double ut = a.u[(int64_t)b * (K + 1) + lane];
             if (d >= 0 && d < V) {
                 const double pd = to_f(p[(int64_t)lane * V + d]);
                 const double qd = q == nullptr ? 1.0 : (double)to_f(q[(int64_t)lane * V + d]);
-                holds = (double)a.u[(int64_t)b * (K + 1) + lane] * qd < pd;
+                holds = lane < drafts && ut * qd < pd;
             }
         }
         const uint32_t held = __ballot_sync(0xffffffffu, holds);
@@ -149,9 +215,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(NT) draft_acc
     }
     __syncthreads();
     const int n = n_s;
-    const bool failed = n < drafts_s;
     Row<T> row{p + (int64_t)n * V, nullptr, -1};
-    if (failed) {
+    if (n < drafts_s) {
         if (q != nullptr) row.q = q + (int64_t)n * V;
         else row.hot = a.draft[(int64_t)b * K + n];
     }
@@ -161,12 +226,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(NT) draft_acc
     // a row without a positive value falls back to p alone
     bool picked = false;
     for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
         for (int g = g0 + warp; g < g1; g += NT / 32) {
-            const double t = segment_sum<T, VEC>(row, g * SEG, min(V, (g + 1) * SEG), lane);
+            const double t = segment_sum<T, VEC>(row, g * SEG, V, lane);
             if (lane == 0) seg_s[g - g0] = t;
         }
         __syncthreads();
-        if (warp == 0) {  // running sums of the segments
+        if (pass == 0) cluster.barrier_wait();
+        if (warp == 0) {
             double carry = 0.0;
             for (int g = 0; g < g1 - g0; g += 32) {
                 double x = g + lane < g1 - g0 ? seg_s[g + lane] : 0.0;
@@ -174,18 +241,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(NT) draft_acc
                 if (g + lane < g1 - g0) seg_s[g + lane] = x;
                 carry = __shfl_sync(0xffffffffu, x, 31);
             }
-            if (lane == 0) total_s = carry;
+            if (lane < kCluster) *cluster.map_shared_rank(&total_s[pass][rank], lane) = carry;
         }
         cluster.sync();
-        double before = 0.0, sum = 0.0;
+        double before = 0.0, after = 0.0, sum = 0.0;
+#pragma unroll
         for (int i = 0; i < kCluster; ++i) {
             if (i == rank) before = sum;
-            sum += *cluster.map_shared_rank(&total_s, i);
+            sum += total_s[pass][i];
+            if (i == rank) after = sum;
         }
-        const double after = before + total_s;
         if (sum > 0.0 && isfinite(sum)) {
-            const double border =
-                fmin(fmax((double)a.u[(int64_t)b * (K + 1) + K] * sum, 0.0), sum * (1.0 - 0x1p-52));
+            const double border = fmin(fmax(u * sum, 0.0), sum * (1.0 - 0x1p-52));
             if (warp == 0 && border >= before && border < after) {
                 int g = 0;  // the first segment whose running sum passes the border
                 for (;; g += 32) {
@@ -200,53 +267,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(NT) draft_acc
                         break;
                     }
                 }
-                const double base = g == 0 ? before : before + seg_s[g - 1];
-                // PER consecutive values per lane, then one lane walks its own
-                const int v0 = (g0 + g) * SEG + lane * PER, v1 = min(min(V, (g0 + g + 1) * SEG), v0 + PER);
-                double mine = 0.0;
-                float pv[PER], qv[PER];
-#pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    pv[j] = qv[j] = 0.f;
-                    if (v0 + j < v1) {
-                        pv[j] = ldg_f(row.p + v0 + j);
-                        qv[j] = row.q != nullptr ? ldg_f(row.q + v0 + j) : (v0 + j == row.hot ? 1.f : 0.f);
-                    }
-                }
-                Sum2 s2;
-                int last = -1;
-#pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    add_diff(s2, pv[j], qv[j]);
-                    if (pv[j] > qv[j]) last = v0 + j;
-                }
-                mine = s2.total();
-                const double upto = base + warp_scan(mine, lane);
-                double run = __shfl_up_sync(0xffffffffu, upto, 1);
-                if (lane == 0) run = base;
-                const uint32_t m = __ballot_sync(0xffffffffu, last >= 0 && upto > border);
-                const uint32_t any = __ballot_sync(0xffffffffu, last >= 0);
-                // rounding may leave the border at the very end of the segment: its last positive value
-                const int at = m != 0 ? __ffs(m) - 1 : 31 - __clz(any);
-                int token = last;
-                if (m != 0 && lane == at) {
-#pragma unroll
-                    for (int j = 0; j < PER; ++j) {
-                        const double d = diff_of(pv[j], qv[j]);
-                        run += d;
-                        if (d > 0.0 && run > border) {
-                            token = v0 + j;
-                            break;
-                        }
-                    }
-                }
-                token = __shfl_sync(0xffffffffu, token, at & 31);
+                const int token =
+                    pick<T, VEC>(row, (g0 + g) * SEG, V, g == 0 ? before : before + seg_s[g - 1], border, lane);
                 if (lane == 0) a.tokens[(int64_t)b * (K + 1) + n] = token < 0 ? 0 : token;
             }
             picked = true;
+            break;
         }
-        cluster.sync();  // the totals have been read
-        if (picked) break;
         row.q = nullptr;
         row.hot = -1;
     }
