@@ -7,10 +7,11 @@
 // (with q null the draft's distribution is 1 at the drafted token).  The
 // emitted tokens are then distributed as the target's own samples.
 //
-// Borders are decided exactly: u q and p - q are formed without rounding and
-// the sums carry their rounding errors (two f32 per sum; f64 adds would take
-// longer than reading the row), so the pick does not depend on how the row is
-// split.
+// Borders are decided as good as exactly: u q and p - q are formed without
+// rounding, and every sum is a pair of f32, the sum and its rounding error
+// (46 bits and more), so the pick does not depend on how the row is split.
+// f64 sums would cost more: at 2 adds per clock and SM the scans alone took as
+// long as reading the rows.
 //
 // Only row n is read (and q's when a draft failed), so a batch is bound by HBM
 // and a single sequence by latency: one cluster of kCluster CTAs per sequence,
@@ -32,7 +33,7 @@ namespace cg = cooperative_groups;
 
 constexpr int NT = 256;
 constexpr int kCluster = 8;
-constexpr int SEG = 1024;  // values per segment
+constexpr int SEG = 512;  // values per segment
 
 // A row r(v) = (p(v) - q(v))+, q: a row, or 1 at `hot`, or nothing.
 template <typename T>
@@ -41,17 +42,38 @@ struct Row {
     int hot;  // index where 1 is taken off, -1: none
 };
 
-// sum + err = sum of the values added so far, to about twice f32's precision
+// A sum and what rounding left out of it.
 struct Sum2 {
     float s = 0.f, c = 0.f;
-    __device__ __forceinline__ void add(float d, float e) {
+    __device__ __forceinline__ void add(float d, float e) {  // the value d + e, |e| small beside d
         const float t = s + d;
         const float b = t - s;
         c += ((s - (t - b)) + (d - b)) + e;
         s = t;
     }
-    __device__ __forceinline__ double total() const { return (double)s + (double)c; }
+    __device__ __forceinline__ Sum2 folded() const {  // |c| at most half a step of s
+        Sum2 r;
+        r.s = s + c;
+        r.c = c - (r.s - s);
+        return r;
+    }
 };
+__device__ __forceinline__ Sum2 operator+(Sum2 a, Sum2 b) {
+    a.add(b.s, b.c);
+    return a.folded();
+}
+__device__ __forceinline__ bool operator>(Sum2 a, Sum2 b) { return (a.s - b.s) + (a.c - b.c) > 0.f; }
+__device__ __forceinline__ Sum2 operator*(float u, Sum2 a) {
+    Sum2 r;
+    r.s = __fmul_rn(u, a.s);
+    r.c = fmaf(u, a.c, fmaf(u, a.s, -r.s));
+    return r.folded();
+}
+__device__ __forceinline__ Sum2 shfl(Sum2 x, int lane) {
+    x.s = __shfl_sync(0xffffffffu, x.s, lane);
+    x.c = __shfl_sync(0xffffffffu, x.c, lane);
+    return x;
+}
 // adds (p - q)+ without rounding the difference
 __device__ __forceinline__ void add_diff(Sum2& a, float p, float q) {
     const float d = p - q;
@@ -88,23 +110,24 @@ __device__ __forceinline__ void load_pq(const Row<T>& r, int at, int V, float (&
     }
 }
 
-__device__ __forceinline__ double warp_total(double t) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    return t;
-}
-__device__ __forceinline__ double warp_scan(double x, int lane) {
+// Inclusive sum over the lanes.  Not inlined, like the loops below not unrolled:
+// a cluster runs most of this code once, and fetching it costs more than
+// running it (unrolled and inlined, the search took 6 us of a call's 13).
+__device__ __noinline__ Sum2 warp_scan(Sum2 x) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        Sum2 y;
+        y.s = __shfl_up_sync(0xffffffffu, x.s, o);
+        y.c = __shfl_up_sync(0xffffffffu, x.c, o);
+        if (lane >= o) x = y + x;
     }
     return x;
 }
 
 // Sum of the segment from v0 on, by one warp.
 template <typename T, bool VEC>
-__device__ __forceinline__ double segment_sum(const Row<T>& r, int v0, int V, int lane) {
+__device__ __forceinline__ Sum2 segment_sum(const Row<T>& r, int v0, int V, int lane) {
     constexpr int N = Vec16<T>::N, IT = SEG / 32 / N, U = N == 4 ? 4 : 2;
     Sum2 acc;
 #pragma unroll 1
@@ -117,20 +140,19 @@ __device__ __forceinline__ double segment_sum(const Row<T>& r, int v0, int V, in
 #pragma unroll
             for (int j = 0; j < N; ++j) add_diff(acc, p[k][j], q[k][j]);
     }
-    return warp_total(acc.total());
+    return shfl(warp_scan(acc.folded()), 31);
 }
 
 // The first value of the segment from v0 on at which the running sum, `run`
 // before the segment, passes the border (by one warp).
 template <typename T, bool VEC>
-__device__ __forceinline__ int pick(const Row<T>& r, int v0, int V, double run, double border, int lane) {
-    constexpr int N = Vec16<T>::N, IT = SEG / 32 / N;
-    double part[IT];
+__device__ __forceinline__ int pick(const Row<T>& r, int v0, int V, Sum2 run, Sum2 border, int lane) {
+    constexpr int N = Vec16<T>::N;
     int last = -1;  // this lane's last value with weight
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
+#pragma unroll 1
+    for (int v = v0; v < v0 + SEG && v < V; v += 32 * N) {
         float p[N], q[N];
-        const int at = v0 + (i * 32 + lane) * N;
+        const int at = v + lane * N;
         load_pq<T, VEC>(r, at, V, p, q);
         Sum2 acc;
 #pragma unroll
@@ -138,41 +160,23 @@ __device__ __forceinline__ int pick(const Row<T>& r, int v0, int V, double run, 
             add_diff(acc, p[j], q[j]);
             if (p[j] > q[j]) last = at + j;
         }
-        part[i] = acc.total();
-    }
-    int it = -1;
-    double mine = 0.0;
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const double t = warp_total(part[i]);
-        if (it < 0) {
-            if (run + t > border) {
-                it = i;
-                mine = part[i];
-            } else {
-                run += t;
-            }
-        }
-    }
-    if (it >= 0) {
-        const double upto = run + warp_scan(mine, lane);
-        const uint32_t past = __ballot_sync(0xffffffffu, upto > border);
-        double before = __shfl_up_sync(0xffffffffu, upto, 1);
-        if (lane == 0) before = run;
-        int token = -1;
-        if (past != 0 && lane == __ffs(past) - 1) {
-            float p[N], q[N];
-            const int at = v0 + (it * 32 + lane) * N;
-            load_pq<T, VEC>(r, at, V, p, q);
+        const Sum2 upto = run + warp_scan(acc.folded());
+        const uint32_t past = __ballot_sync(0xffffffffu, acc.s > 0.f && upto > border);
+        if (past != 0) {  // the lane that passes it walks its own values
+            Sum2 before = shfl(upto, lane > 0 ? lane - 1 : 0);
+            if (lane == 0) before = run;
+            int token = -1;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 if (p[j] > q[j] && !(token >= 0 && before > border)) {
-                    before += (double)p[j] - (double)q[j];
+                    add_diff(before, p[j], q[j]);
+                    before = before.folded();
                     token = at + j;
                 }
             }
+            return __shfl_sync(0xffffffffu, token, __ffs(past) - 1);
         }
-        if (past != 0) return __shfl_sync(0xffffffffu, token, __ffs(past) - 1);
+        run = shfl(upto, 31);
     }
     // rounding left the border at the segment's very end: its last value with weight
     return __reduce_max_sync(0xffffffffu, last);
@@ -180,8 +184,9 @@ __device__ __forceinline__ int pick(const Row<T>& r, int v0, int V, double run, 
 
 template <typename T, bool VEC>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(NT, 4) draft_accept_kernel(DraftAcceptArgs a) {
-    extern __shared__ double seg_s[];         // running sums of this CTA's segments
-    __shared__ double total_s[2][kCluster];   // the CTAs' sums, one set per pass
+    extern __shared__ Sum2 seg_s[];         // running sums of this CTA's segments
+    uint8_t* some_s = reinterpret_cast<uint8_t*>(seg_s + (a.V + SEG * kCluster - 1) / (SEG * kCluster));  // segment has weight
+    __shared__ Sum2 total_s[2][kCluster];   // the CTAs' sums, one set per pass
     __shared__ int n_s, drafts_s;
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -192,7 +197,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(NT, 4) draft_
     cluster.barrier_arrive();  // waited for before the first write into another CTA's shared memory
     pdl_wait();
     pdl_trigger();
-    const double u = a.u[(int64_t)b * (K + 1) + K];
+    const float u = a.u[(int64_t)b * (K + 1) + K];
 
     if (warp == 0) {
         int drafts = a.n_draft == nullptr ? K : a.n_draft[b];
@@ -228,44 +233,50 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(NT, 4) draft_
     for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
         for (int g = g0 + warp; g < g1; g += NT / 32) {
-            const double t = segment_sum<T, VEC>(row, g * SEG, V, lane);
+            const Sum2 t = segment_sum<T, VEC>(row, g * SEG, V, lane);
             if (lane == 0) seg_s[g - g0] = t;
         }
         __syncthreads();
         if (pass == 0) cluster.barrier_wait();
         if (warp == 0) {
-            double carry = 0.0;
+            Sum2 carry;
             for (int g = 0; g < g1 - g0; g += 32) {
-                double x = g + lane < g1 - g0 ? seg_s[g + lane] : 0.0;
-                x = carry + warp_scan(x, lane);
-                if (g + lane < g1 - g0) seg_s[g + lane] = x;
-                carry = __shfl_sync(0xffffffffu, x, 31);
+                Sum2 x;
+                if (g + lane < g1 - g0) x = seg_s[g + lane];
+                const bool some = x.s > 0.f;
+                x = carry + warp_scan(x);
+                if (g + lane < g1 - g0) {
+                    seg_s[g + lane] = x;
+                    some_s[g + lane] = some;
+                }
+                carry = shfl(x, 31);
             }
             if (lane < kCluster) *cluster.map_shared_rank(&total_s[pass][rank], lane) = carry;
         }
         cluster.sync();
-        double before = 0.0, after = 0.0, sum = 0.0;
-#pragma unroll
+        // the CTAs' ranges: one after the other, so that a CTA without weight has an empty one
+        Sum2 before, after, sum;
+#pragma unroll 1
         for (int i = 0; i < kCluster; ++i) {
             if (i == rank) before = sum;
-            sum += total_s[pass][i];
+            sum = sum + total_s[pass][i];
             if (i == rank) after = sum;
         }
-        if (sum > 0.0 && isfinite(sum)) {
-            const double border = fmin(fmax(u * sum, 0.0), sum * (1.0 - 0x1p-52));
-            if (warp == 0 && border >= before && border < after) {
-                int g = 0;  // the first segment whose running sum passes the border
-                for (;; g += 32) {
-                    const bool past = g + lane < g1 - g0 && before + seg_s[g + lane] > border;
-                    const uint32_t m = __ballot_sync(0xffffffffu, past);
-                    if (m != 0) {
-                        g += __ffs(m) - 1;
+        if (sum.s > 0.f && isfinite(sum.s + sum.c)) {
+            // u below 1 leaves a border below the sum; anything else is brought there
+            Sum2 border = (u > 0.f ? u : 0.f) * sum;
+            if (!(sum > border)) border = (1.f - 0x1p-24f) * sum;
+            if (warp == 0 && !(before > border) && after > border) {
+                int g = -1;  // the first segment with weight whose running sum passes the border, else the last
+                for (int i = 0; i < g1 - g0; i += 32) {
+                    const bool some = i + lane < g1 - g0 && some_s[i + lane] != 0;
+                    const uint32_t past = __ballot_sync(0xffffffffu, some && before + seg_s[i + lane] > border);
+                    const uint32_t any = __ballot_sync(0xffffffffu, some);
+                    if (past != 0) {
+                        g = i + __ffs(past) - 1;
                         break;
                     }
-                    if (g + 32 >= g1 - g0) {
-                        g = g1 - g0 - 1;
-                        break;
-                    }
+                    if (any != 0) g = i + 31 - __clz(any);
                 }
                 const int token =
                     pick<T, VEC>(row, (g0 + g) * SEG, V, g == 0 ? before : before + seg_s[g - 1], border, lane);
@@ -289,8 +300,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(NT, 4) draft_
 
 template <typename T>
 cudaError_t launch_t(const DraftAcceptArgs& a, cudaStream_t s) {
-    const int nseg = (a.V + SEG - 1) / SEG;
-    const size_t smem = (size_t)((nseg + kCluster - 1) / kCluster) * sizeof(double);
+    const int nseg = (a.V + SEG - 1) / SEG;  // at most 4096 per CTA: V <= 2^24
+    const size_t smem = (size_t)((nseg + kCluster - 1) / kCluster) * (sizeof(Sum2) + 1);
     const dim3 grid((unsigned)(a.B * kCluster));
     // whole 16-byte pieces only when every row starts on one
     const bool vec = (size_t)a.V * sizeof(T) % 16 == 0;
