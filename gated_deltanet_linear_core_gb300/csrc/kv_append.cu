@@ -12,6 +12,7 @@ namespace {
 
 constexpr int NT = 256;
 constexpr int kMaxTB = 64;
+constexpr int U = 4;  // pieces of K and of V in flight per thread
 
 __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int tb) {
     __shared__ int64_t row_s[kMaxTB];  // row of (page, head 0, position in page), -1: nowhere
@@ -53,15 +54,27 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int tb) {
     const uint4* v = static_cast<const uint4*>(a.v) + t0 * per_token;
     uint4* kc = static_cast<uint4*>(a.k_cache);
     uint4* vc = static_cast<uint4*>(a.v_cache);
-#pragma unroll 4
-    for (int e = threadIdx.x; e < all; e += NT) {
-        const int t = e / per_token, hc = e - t * per_token;
-        const int h = hc / chunks, c = hc - h * chunks;
-        const int64_t row = row_s[t];
-        if (row < 0) continue;
-        const int64_t dst = (row + (int64_t)h * a.page_size) * chunks + c;
-        kc[dst] = __ldcs(k + e);
-        vc[dst] = __ldcs(v + e);
+    for (int e0 = threadIdx.x; e0 < all; e0 += U * NT) {
+        uint4 x[U], y[U];
+        int64_t dst[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int e = e0 + i * NT;
+            dst[i] = -1;
+            if (e < all) {
+                const int t = e / per_token, hc = e - t * per_token;
+                const int h = hc / chunks, c = hc - h * chunks;
+                if (row_s[t] >= 0) dst[i] = (row_s[t] + (int64_t)h * a.page_size) * chunks + c;
+                x[i] = __ldcs(k + e);
+                y[i] = __ldcs(v + e);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (dst[i] >= 0) {
+                kc[dst[i]] = x[i];
+                vc[dst[i]] = y[i];
+            }
     }
 }
 
@@ -69,8 +82,8 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int tb) {
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t s) {
     if (a.T == 0) return cudaSuccess;
-    // enough blocks for the SMs first, then larger blocks
-    int64_t tb = a.T / (152 * 4);
+    // many small blocks, so that lookups overlap copies (32768 prompt tokens: 26.6 us, with 4 blocks per SM 29.4)
+    int64_t tb = a.T / (152 * 16);
     tb = tb < 1 ? 1 : (tb > kMaxTB ? kMaxTB : tb);
     return launch_pdl(kv_append_kernel, dim3((unsigned)((a.T + tb - 1) / tb)), dim3(NT), 0, s, a, (int)tb);
 }
