@@ -363,11 +363,15 @@ __global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a, int n_cta, in
             const int64_t at = row * D + grp * 4;
             const float inv = run.l == 0.f ? 0.f : 1.0f / run.l;
             float y[4] = {run.o.x * inv, run.o.y * inv, run.o.z * inv, run.o.w * inv};
+            if (a.gate != nullptr) {
+                float gt[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (a.gate != nullptr) y[k] *= sigmoid_f(to_f(static_cast<const T*>(a.gate)[at + k]));
-                static_cast<T*>(a.out)[at + k] = from_f<T>(y[k]);
+                for (int k = 0; k < 4; ++k) gt[k] = to_f(static_cast<const T*>(a.gate)[at + k]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] *= sigmoid_f(gt[k]);
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) static_cast<T*>(a.out)[at + k] = from_f<T>(y[k]);
             if (grp == 0 && a.lse != nullptr) a.lse[row] = run.l == 0.f ? -INFINITY : (run.m + log2f(run.l)) * kLn2;
         }
     }

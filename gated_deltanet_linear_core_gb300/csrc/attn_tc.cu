@@ -79,6 +79,7 @@ struct Layout {
     static constexpr int T_S = 0, T_O = 2 * N;
     static constexpr int T_USED = (2 + NDB) * N;
     static constexpr int T_COLS = T_USED <= 64 ? 64 : T_USED <= 128 ? 128 : T_USED <= 256 ? 256 : 512;
+    static_assert(N * 512 <= P_BYTES, "output rows");
     static_assert(SMEM <= kSmemMax && NS >= 3, "shared memory");
     static_assert((5 + 2 * 6 + 2) * 8 + 16 <= BARS, "barriers");
 
@@ -462,7 +463,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         tc_fence_after();
 #pragma unroll
                         for (int c = 0; c < CPT; ++c) l[c] *= f_s[c0 + c];
-#pragma unroll
+#pragma unroll 1
                         for (int db = 0; db < NDB; ++db) {
                             float o[CPT];
                             tmem_ld<CPT>(tq + L::T_O + db * N, o);
@@ -568,40 +569,53 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 }
             }
             softmax_sync<NSOFT>();
+            // ---- outputs, 128 head dims at a time: turned into rows in P's memory, then read back 8 dims at a time
+            // (one thread writing its dim of every row, unrolled, spent longer on fetching code than on the rest)
             const bool odd = *odd_v != 0;
+            float* o_s = reinterpret_cast<float*>(sm + L::O_P);  // [rows][128]
+#pragma unroll 1
             for (int db = 0; db < NDB; ++db) {
                 float o[CPT];
-                __syncwarp();
+                if (db > 0) softmax_sync<NSOFT>();
                 tmem_ld<CPT>(tq + L::T_O + db * N, o);
                 tmem_wait_ld();
-                const int d = db * 128 + row;
-                if (d >= a.D || !live) continue;
-                if (odd) {
+                if (odd && db * 128 + row < a.D) {
                     const int t1 = min(s.len, s.tile1 * TILE);
                     for (int t = max(s.tile0 * TILE, s.len - a.K + 1); t < t1; ++t) {
                         const int page = a.table[(int64_t)s.b * a.max_pages + t / a.page_size];
                         if (page < 0 || page >= a.n_pages) continue;
                         const float v = to_f(static_cast<const bf16*>(
-                            a.v_cache)[(((int64_t)page * a.H_kv + s.h) * a.page_size + t % a.page_size) * a.D + d]);
+                            a.v_cache)[(((int64_t)page * a.H_kv + s.h) * a.page_size + t % a.page_size) * a.D + db * 128 + row]);
                         if (!isfinite(v))
 #pragma unroll
                             for (int c = 0; c < CPT; ++c)
                                 if (t < vis_s[c0 + c]) o[c] += v;
                     }
                 }
-                if (whole) {
 #pragma unroll
-                    for (int c = 0; c < CPT; ++c)
-                        if (c0 + c < nr) {
-                            const int64_t at = off_s[c0 + c] + d;
-                            float y = o[c] * f_s[c0 + c];
-                            if (a.gate != nullptr) y *= sigmoid_f(to_f(static_cast<const bf16*>(a.gate)[at]));
-                            static_cast<bf16*>(a.out)[at] = from_f<bf16>(y);
+                for (int c = 0; c < CPT; ++c) o_s[(c0 + c) * 128 + row] = o[c];
+                softmax_sync<NSOFT>();
+#pragma unroll 1
+                for (int e = st; e < nr * 16; e += NSOFT) {
+                    const int r = e >> 4, dd = (e & 15) * 8, d = db * 128 + dd;
+                    if (d >= a.D || !live) continue;
+                    const float4 x0 = *reinterpret_cast<const float4*>(o_s + r * 128 + dd);
+                    const float4 x1 = *reinterpret_cast<const float4*>(o_s + r * 128 + dd + 4);
+                    if (whole) {
+                        float y[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w}, gt[8];
+                        const float inv = f_s[r];
+                        if (a.gate != nullptr) load16<bf16>(static_cast<const bf16*>(a.gate) + off_s[r] + d, gt);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            y[i] *= inv;
+                            if (a.gate != nullptr) y[i] *= sigmoid_f(gt[i]);
                         }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < CPT; ++c)
-                        if (c0 + c < nr) slot[a.stat_floats + (c0 + c) * a.D + d] = o[c];
+                        store16<bf16>(static_cast<bf16*>(a.out) + off_s[r] + d, y);
+                    } else {
+                        float* p = slot + a.stat_floats + r * a.D + d;
+                        *reinterpret_cast<float4*>(p) = x0;
+                        *reinterpret_cast<float4*>(p + 4) = x1;
+                    }
                 }
             }
             tc_fence_before();
