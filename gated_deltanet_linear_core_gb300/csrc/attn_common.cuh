@@ -41,58 +41,45 @@ struct Place {
 };
 
 // Units of the call and the sequence that holds the first unit of CTA c of the
-// n that take part (n is capped so that a CTA has at least min_units).  All
-// NT threads call it; `sh` holds NT + 4 values.
-template <int NT>
-__device__ __forceinline__ Place find_place(const AttnArgs& a, int tile, int c, int& n, int64_t* sh) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int per = (a.B + NT - 1) / NT;
-    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+// n that take part (n is capped so that a CTA has at least min_units).  Every
+// warp works it out for itself, all lanes together: a block-wide scan saves
+// loads but costs three barriers, which at the start of a call is longer.
+__device__ __forceinline__ Place find_place(const AttnArgs& a, int tile, int c, int& n) {
+    const int lane = threadIdx.x & 31;
     const int64_t mult = (int64_t)a.H_kv * a.n_rb;
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += units_of(clamped_len(a, b), tile);
-    int64_t inc = mine;  // inclusive scan over the threads
+    const int len0 = lane < a.B ? clamped_len(a, lane) : 0;  // kept: all of a small batch
+    int64_t all = lane < a.B ? units_of(len0, tile) : 0;
+    for (int b = lane + 32; b < a.B; b += 32) all += units_of(clamped_len(a, b), tile);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-    }
-    if (lane == 31) sh[warp] = inc;
-    __syncthreads();
-    int64_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-        const int64_t v = sh[w];
-        if (w < warp) before += v;
-        all += v;
-    }
-    inc += before;
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     Place p;
     p.total = all * mult;
+    p.first = 0;
+    p.b = p.len = 0;
     const int64_t most = (p.total + a.min_units - 1) / a.min_units;
     if (n > most) n = (int)most;
-    __syncthreads();
-    if (c < n) {
-        const int64_t want = cta_begin(p.total, c, n);
-        int64_t lo = (inc - mine) * mult;
-        if (want >= lo && want < inc * mult) {
-            int b = b0;
-            int len = clamped_len(a, b);
-            for (;;) {
-                const int64_t next = lo + units_of(len, tile) * mult;
-                if (want < next) break;
-                lo = next;
-                len = clamped_len(a, ++b);
-            }
-            sh[0] = lo;
-            sh[1] = ((int64_t)len << 32) | (uint32_t)b;
+    if (c >= n) return p;
+    const int64_t want = cta_begin(p.total, c, n);
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int b = b0 + lane;
+        const int len = b0 == 0 ? len0 : (b < a.B ? clamped_len(a, b) : 0);
+        int inc = b < a.B ? units_of(len, tile) : 0;  // inclusive scan: 32 sequences' units fit 31 bits
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
         }
+        const uint32_t past = __ballot_sync(0xffffffffu, want < p.first + inc * mult);
+        if (past != 0) {
+            const int l = __ffs(past) - 1;
+            const int before = __shfl_sync(0xffffffffu, inc, l > 0 ? l - 1 : 0);
+            p.b = b0 + l;
+            p.len = __shfl_sync(0xffffffffu, len, l);
+            if (l > 0) p.first += before * mult;
+            break;
+        }
+        p.first += __shfl_sync(0xffffffffu, inc, 31) * mult;
     }
-    __syncthreads();
-    p.first = sh[0];
-    p.b = (int)(uint32_t)(sh[1] & 0xffffffff);
-    p.len = (int)(sh[1] >> 32);
-    __syncthreads();
     return p;
 }
 

@@ -39,7 +39,6 @@ __device__ __forceinline__ float4 lds4(const bf16* p) {
 
 template <typename T, int R, int TT>
 struct FfmaSmem {
-    int64_t sh[NT + 4];
     int64_t rowoff[3][TT];  // element offset of the tile's rows in the caches, -1: no such token
     float s[R][TT];         // scores, then weights
     float m[R], l[R], f[R];
@@ -61,7 +60,7 @@ __global__ void __launch_bounds__(NT, 1) attn_ffma_kernel(AttnArgs a) {
     pdl_wait();
     pdl_trigger();
     int n_cta = gridDim.x;
-    const Place place = find_place<NT>(a, TT, blockIdx.x, n_cta, sm.sh);
+    const Place place = find_place(a, TT, blockIdx.x, n_cta);
     if ((int)blockIdx.x >= n_cta) return;
     Walk walk(place, cta_begin(place.total, blockIdx.x, n_cta), cta_begin(place.total, blockIdx.x + 1, n_cta));
 
@@ -309,7 +308,7 @@ __global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a, int n_cta, in
     __shared__ float4 o_s[JT];
     __shared__ float2 ml_s[JT];
     const int tid = threadIdx.x, c = blockIdx.x + 1;
-    const Place p = find_place<JT>(a, tile, c, n_cta, reinterpret_cast<int64_t*>(o_s));
+    const Place p = find_place(a, tile, c, n_cta);
     if (c >= n_cta) return;
     Walk walk(p, cta_begin(p.total, c, n_cta), cta_begin(p.total, c + 1, n_cta));
     Segment s;
@@ -319,16 +318,18 @@ __global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a, int n_cta, in
     const int c0 = cta_of(p.total, u0, n_cta), c1 = cta_of(p.total, u1 - 1, n_cta);
     const int first_slot = cta_begin(p.total, c0, n_cta) == u0 ? 2 * c0 : 2 * c0 + 1;
     const int n = c1 - c0 + 1;
-    const int D = a.D, ng = D / 4, groups = JT / ng, grp = tid % ng, g = tid / ng;
+    // many parts: a worker takes a quarter of a row, so that more groups share its parts
+    const int split = n > kSerial && a.D % 16 == 0 ? 4 : 1;
+    const int ng = a.D / 4 / split, groups = JT / ng, grp = tid % ng, g = tid / ng;
     const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
     const int workers = (n - 1) * gridDim.y, worker = (c - c0 - 1) * gridDim.y + blockIdx.y;
     const int share = n > kSerial ? groups : 1;  // groups on one row
     const int at_once = groups / share, sub = g % share;
     pdl_wait();
     pdl_trigger();
-    for (int first = worker * at_once; first < nr; first += workers * at_once) {
-        const int r = first + g / share;
-        const bool mine = g < groups && r < nr;
+    for (int first = worker * at_once; first < nr * split; first += workers * at_once) {
+        const int rq = first + g / share, r = rq / split, d = ((rq - r * split) * ng + grp) * 4;
+        const bool mine = g < groups && rq < nr * split;
         Running run;
         if (mine) {
             constexpr int U = 4;
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a, int n_cta, in
                         const float* slot = slot_ptr(a, part == 0 ? first_slot : 2 * (c0 + part));
                         m[k] = slot[r];
                         l[k] = slot[a.rb_rows + r];
-                        x[k] = *reinterpret_cast<const float4*>(slot + a.stat_floats + r * D + grp * 4);
+                        x[k] = *reinterpret_cast<const float4*>(slot + a.stat_floats + r * a.D + d);
                     }
                 }
 #pragma unroll
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a, int n_cta, in
         }
         if (mine && sub == 0) {
             const int64_t row = row_index(a, s.b, s.h, r0 + r);
-            const int64_t at = row * D + grp * 4;
+            const int64_t at = row * a.D + d;
             const float inv = run.l == 0.f ? 0.f : 1.0f / run.l;
             float y[4] = {run.o.x * inv, run.o.y * inv, run.o.z * inv, run.o.w * inv};
             if (a.gate != nullptr) {
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a, int n_cta, in
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) static_cast<T*>(a.out)[at + k] = from_f<T>(y[k]);
-            if (grp == 0 && a.lse != nullptr) a.lse[row] = run.l == 0.f ? -INFINITY : (run.m + log2f(run.l)) * kLn2;
+            if (d == 0 && a.lse != nullptr) a.lse[row] = run.l == 0.f ? -INFINITY : (run.m + log2f(run.l)) * kLn2;
         }
     }
 }

@@ -59,7 +59,7 @@ struct Layout {
     static constexpr int Q_BYTES = 2 * NDB * N * 128;
     static constexpr int SCR = N <= 64 ? 4 * N * 4 : 0;  // scratch of its own (N = 128: in P, free by then)
     static constexpr int BARS = 256;
-    static constexpr int SMALL = BARS + 256 + N * (4 + 4 + 4 + 8) + SCR;
+    static constexpr int SMALL = BARS + N * (4 + 4 + 4 + 8) + SCR;
     static constexpr int FIT = (kSmemMax - P_BYTES - Q_BYTES - SMALL) / SLOT;
     static constexpr int NS = FIT < 6 ? FIT : 6;
     // Slots are filled and used in the order K(0), K(1), V(0), K(2), V(1), .. of a segment's n tiles
@@ -69,8 +69,7 @@ struct Layout {
     static constexpr int O_Q = NS * SLOT;
     static constexpr int O_P = O_Q + Q_BYTES;
     static constexpr int O_BAR = O_P + P_BYTES;
-    static constexpr int O_SH = O_BAR + BARS;
-    static constexpr int O_OFF = O_SH + 256;
+    static constexpr int O_OFF = O_BAR + BARS;
     static constexpr int O_M = O_OFF + N * 8;
     static constexpr int O_F = O_M + N * 4;
     static constexpr int O_VIS = O_F + N * 4;
@@ -236,7 +235,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     pdl_trigger();
 
     int n_cta = gridDim.x;
-    const Place place = find_place<L::NT>(a, TILE, blockIdx.x, n_cta, reinterpret_cast<int64_t*>(sm + L::O_SH));
+    const Place place = find_place(a, TILE, blockIdx.x, n_cta);
     const bool works = (int)blockIdx.x < n_cta;
     const int64_t u0 = works ? cta_begin(place.total, blockIdx.x, n_cta) : 0;
     const int64_t u1 = works ? cta_begin(place.total, blockIdx.x + 1, n_cta) : 0;
@@ -337,9 +336,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 const int n = s.tile1 - s.tile0;
                 ok = wait_or_abort(q_full, (uint32_t)(seg & 1), abort_flag);
                 ++seg;
-                ok = ok && issue_s(it, sl0);
-                for (int j = 0; ok && j < n; ++j, ++it) {
-                    if (j + 1 < n && !issue_s(it + 1, sl0 + L::k_slot(j + 1))) { ok = false; break; }
+                for (int j = -1; ok && j < n; ++j) {  // S of tile j + 1, then P V of tile j
+                    if (j + 1 < n && !issue_s(it + (j < 0 ? 0 : 1), sl0 + L::k_slot(j + 1))) { ok = false; break; }
+                    if (j < 0) continue;
                     ok = wait_or_abort(&p_full[it & 1], (uint32_t)((it >> 1) & 1), abort_flag);
                     if (!ok) break;
                     const int left = s.len - (s.tile0 + j) * TILE;
@@ -365,6 +364,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     mma_commit(&pv_done[it & 1]);
                     last = &pv_done[it & 1];
                     last_parity = (uint32_t)((it >> 1) & 1);
+                    ++it;
                 }
                 sl0 += 2 * NDB * n;
             }
