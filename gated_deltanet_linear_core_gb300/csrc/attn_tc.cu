@@ -48,7 +48,8 @@ constexpr int kSmemMax = 232448;
 
 template <int N, int NDB>
 struct Layout {
-    static constexpr int CPT = N < 32 ? N : 32;   // columns (rows of Q) per softmax thread
+    static constexpr int CPT = N <= 32 ? N : N / 2;  // columns (rows of Q) per softmax thread
+    static constexpr int CH = CPT < 32 ? CPT : 32;   // columns per TMEM access
     static constexpr int NWG = N / CPT;           // softmax warpgroups
     static constexpr int NSW = 4 * NWG;           // softmax warps
     static constexpr int NT = 64 + 32 * NSW;
@@ -59,7 +60,7 @@ struct Layout {
     static constexpr int Q_BYTES = 2 * NDB * N * 128;
     static constexpr int SCR = N <= 64 ? 4 * N * 4 : 0;  // scratch of its own (N = 128: in P, free by then)
     static constexpr int BARS = 256;
-    static constexpr int SMALL = BARS + N * (4 + 4 + 4 + 8) + SCR;
+    static constexpr int SMALL = BARS + N * 4 * 5 + SCR;
     static constexpr int FIT = (kSmemMax - P_BYTES - Q_BYTES - SMALL) / SLOT;
     static constexpr int NS = FIT < 6 ? FIT : 6;
     // Slots are filled and used in the order K(0), K(1), V(0), K(2), V(1), .. of a segment's n tiles
@@ -69,18 +70,17 @@ struct Layout {
     static constexpr int O_Q = NS * SLOT;
     static constexpr int O_P = O_Q + Q_BYTES;
     static constexpr int O_BAR = O_P + P_BYTES;
-    static constexpr int O_OFF = O_BAR + BARS;
-    static constexpr int O_M = O_OFF + N * 8;
-    static constexpr int O_F = O_M + N * 4;
-    static constexpr int O_VIS = O_F + N * 4;
-    static constexpr int O_SCR = N <= 64 ? O_VIS + N * 4 : O_P;
+    static constexpr int O_M = O_BAR + BARS;    // [2 segments][N]
+    static constexpr int O_VIS = O_M + 2 * N * 4;  // [2 segments][N]
+    static constexpr int O_F = O_VIS + 2 * N * 4;
+    static constexpr int O_SCR = N <= 64 ? O_F + N * 4 : O_P;
     static constexpr int SMEM = O_BAR + SMALL;
     static constexpr int T_S = 0, T_O = 2 * N;
     static constexpr int T_USED = (2 + NDB) * N;
     static constexpr int T_COLS = T_USED <= 64 ? 64 : T_USED <= 128 ? 128 : T_USED <= 256 ? 256 : 512;
     static_assert(N * 512 <= P_BYTES, "output rows");
     static_assert(SMEM <= kSmemMax && NS >= 3, "shared memory");
-    static_assert((5 + 2 * 6 + 2) * 8 + 16 <= BARS, "barriers");
+    static_assert(20 * 8 + 16 <= BARS, "barriers");
 
     // byte offset of P's column block (16-byte chunk j of 8 columns) of token t
     __device__ static __forceinline__ uint32_t p_off(int buf, int lo, int chunk, int t) {
@@ -141,7 +141,7 @@ __device__ __forceinline__ bool softmax_any(bool x) {
     return r != 0;
 }
 template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
     if constexpr (N == 16) tmem_ld16(taddr, v); else tmem_ld32(taddr, v);
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
@@ -152,7 +152,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
         : "memory");
 }
 template <int N>
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[N]) {
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float* v) {
     if constexpr (N == 16) tmem_st16(taddr, v); else tmem_st32(taddr, v);
 }
 __device__ __forceinline__ float warp_max(float x) {
@@ -203,7 +203,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     uint64_t* q_full = bars + 18;     // a segment's Q written (softmax warps)
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 19);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-    volatile int* odd_v = reinterpret_cast<volatile int*>(tslot + 2);  // a new token's value is not finite
+    volatile int* odd_v = reinterpret_cast<volatile int*>(tslot + 2);  // [2 segments] a new token's value is not finite
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
@@ -218,7 +218,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         }
         mbar_init(q_full, L::NSW);
         *abort_flag = 0;
-        *odd_v = 0;
+        odd_v[0] = odd_v[1] = 0;
         fence_mbar_init();
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
@@ -241,7 +241,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     const int64_t u1 = works ? cta_begin(place.total, blockIdx.x + 1, n_cta) : 0;
     Walk walk(place, u0, u1);
     Segment s;
-    const int nslab = (a.D + 63) / 64;
+    const int nslab = (a.D + 63) / 64;  // 64-dim slabs of a cache row
 
     if (warp == 0) {
         // ------------------------------------------------ loads: lane p takes piece p of a tile
@@ -372,82 +372,107 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         }
     } else {
         // ------------------------------------------------ softmax and outputs
+        constexpr int CH = L::CH;
         const int st = tid - 64;                 // softmax thread
         const int quad = warp & 3;               // its TMEM lanes: 32 quad ..
         const int row = quad * 32 + lane;        // token of a tile, head dim of an output block
         const int c0 = ((warp - 2) >> 2) * CPT;  // its columns: c0 ..
         const uint32_t tq = tb + ((uint32_t)(quad * 32) << 16) + c0;
-        float* m_s = reinterpret_cast<float*>(sm + L::O_M);      // running maxima
-        float* f_s = reinterpret_cast<float*>(sm + L::O_F);      // factors of a rescaling, 1 / l at the end
-        int* vis_s = reinterpret_cast<int*>(sm + L::O_VIS);      // tokens a row sees
-        int64_t* off_s = reinterpret_cast<int64_t*>(sm + L::O_OFF);  // element offset of a row in q, gate, out
-        float* scr = reinterpret_cast<float*>(sm + L::O_SCR);    // [4 lane quarters][N]
+        float* f_s = reinterpret_cast<float*>(sm + L::O_F);    // factors of a rescaling, 1 / l at the end
+        float* scr = reinterpret_cast<float*>(sm + L::O_SCR);  // [4 lane quarters][N]
         int it = 0, sl0 = 0;  // tiles and slots before
-        bool live = true;  // no wait gave up: outputs are written only then
+        int par = 0;          // parity of the segment: which of the doubled arrays are its own
+        bool live = true;     // no wait gave up: outputs are written only then
         auto wait = [&](uint64_t* bar, int k) {
             live = __all_sync(0xffffffffu, live && wait_or_abort(bar, (uint32_t)(k & 1), abort_flag));
         };
-        while (walk.next(a, TILE, s)) {
-            const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
-            const bool whole = s.tile1 - s.tile0 == s.tiles;
-            softmax_sync<NSOFT>();  // everyone is done with the previous segment's arrays
-            for (int c = st; c < N; c += NSOFT) {
-                m_s[c] = kNone;
-                vis_s[c] = c < nr ? visible(a, s.len, r0 + c) : 0;
-                off_s[c] = c < nr ? row_index(a, s.b, s.h, r0 + c) * a.D : 0;
-            }
-            if (st == 0) *odd_v = 0;
-            softmax_sync<NSOFT>();
-            if (s.len == 0) {  // nothing to see: the rows are zeros
+        // The next segment with tokens (rows of empty sequences become zeros on the way), its running maxima,
+        // what its rows see, and its Q: all but the outputs of the segment before, so that S of its first tile
+        // runs beside them.  Q's memory is free once S of the last tile before is done.
+        auto start_segment = [&](Segment& g, int p) -> bool {
+            int r0, nr;
+            for (;;) {
+                if (!walk.next(a, TILE, g)) return false;
+                r0 = g.rb * a.rb_rows;
+                nr = block_rows(a, g.rb);
+                if (g.len > 0) break;
                 for (int e = st; e < nr * a.D; e += NSOFT) {
                     const int r = e / a.D, d = e - r * a.D;
-                    static_cast<bf16*>(a.out)[off_s[r] + d] = from_f<bf16>(0.f);
-                    if (d == 0 && a.lse != nullptr) a.lse[off_s[r] / a.D] = -INFINITY;
+                    const int64_t at = row_index(a, g.b, g.h, r0 + r);
+                    static_cast<bf16*>(a.out)[at * a.D + d] = from_f<bf16>(0.f);
+                    if (d == 0 && a.lse != nullptr) a.lse[at] = -INFINITY;
                 }
-                continue;
             }
-            // Q rows, zero beyond the block's rows and the head dim
+            float* m = reinterpret_cast<float*>(sm + L::O_M) + p * N;
+            int* vis = reinterpret_cast<int*>(sm + L::O_VIS) + p * N;
+            // rows beyond the block's and dims beyond the head's are zero
+#pragma unroll 4
             for (int e = st; e < N * 16 * NDB; e += NSOFT) {
                 const int r = e / (16 * NDB), ch = e % (16 * NDB);
                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
                 if (r < nr && ch * 8 < a.D)
-                    x = __ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) + off_s[r] + ch * 8));
+                    x = __ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) +
+                                                             row_index(a, g.b, g.h, r0 + r) * a.D + ch * 8));
                 *reinterpret_cast<uint4*>(sm + L::O_Q + (ch >> 3) * (N * 128) + sw128_off((uint32_t)r, (uint32_t)(ch & 7) * 8)) = x;
             }
+            for (int c = st; c < N; c += NSOFT) {
+                m[c] = kNone;
+                vis[c] = c < nr ? visible(a, g.len, r0 + c) : 0;
+            }
+            if (st == 0) odd_v[p] = 0;
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
-
+            return true;
+        };
+        Segment nx;
+        bool more = start_segment(s, par);
+        while (more) {
+            const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
+            const bool whole = s.tile1 - s.tile0 == s.tiles;
+            float* m_s = reinterpret_cast<float*>(sm + L::O_M) + par * N;    // running maxima
+            const int* vis_s = reinterpret_cast<int*>(sm + L::O_VIS) + par * N;  // tokens a row sees
+            softmax_sync<NSOFT>();  // they are written, and the outputs before are out of P's memory
             float l[CPT];
 #pragma unroll
             for (int c = 0; c < CPT; ++c) l[c] = 0.f;
             const int least = visible(a, s.len, r0);  // what the block's first row sees
             for (int j = s.tile0; j < s.tile1; ++j, ++it) {
                 const int t0 = j * TILE;
-                float x[CPT];
+                const bool tail = t0 + TILE > least;
+                float x[CPT];  // scores in the log2 domain, less the running maximum
                 wait(&s_full[it & 1], it >> 1);
                 tc_fence_after();
-                tmem_ld<CPT>(tq + L::T_S + (it & 1) * N, x);
+#pragma unroll
+                for (int c = 0; c < CPT; c += CH) tmem_ld<CH>(tq + L::T_S + (it & 1) * N + c, x + c);
                 tmem_wait_ld();
-                const bool tail = t0 + TILE > least;
-                bool over = false;
+                float top = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < CPT; c += 4) {
                     const float4 m4 = *reinterpret_cast<const float4*>(m_s + c0 + c);
                     const float m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[c + i] *= a.scale_log2;
-                        if (tail && t0 + row >= vis_s[c0 + c + i]) x[c + i] = -INFINITY;
-                        over = over || x[c + i] > m[i] + kSlack;
+                    for (int i = 0; i < 4; ++i) x[c + i] = fmaf(x[c + i], a.scale_log2, -m[i]);
+                    if (tail) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (t0 + row >= vis_s[c0 + c + i]) x[c + i] = -INFINITY;
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = fmaxf(top, x[c + i]);
                 }
-                if (softmax_any<NSOFT>(over)) {
+                if (softmax_any<NSOFT>(top > kSlack)) {
                     // ---- new maxima; sums and outputs so far are scaled to them
                     const bool first = j == s.tile0;
                     if (!first) wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < CPT; c += CH) tmem_ld<CH>(tq + L::T_S + (it & 1) * N + c, x + c);
+                    tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < CPT; ++c) {
+                        x[c] *= a.scale_log2;
+                        if (tail && t0 + row >= vis_s[c0 + c]) x[c] = -INFINITY;
                         const float t = warp_max(x[c]);
                         if (lane == 0) scr[quad * N + c0 + c] = t;
                     }
@@ -459,18 +484,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         f_s[c] = ex2_approx(m0 - m1);
                     }
                     softmax_sync<NSOFT>();
+#pragma unroll
+                    for (int c = 0; c < CPT; ++c) x[c] -= m_s[c0 + c];
                     if (!first) {
-                        tc_fence_after();
 #pragma unroll
                         for (int c = 0; c < CPT; ++c) l[c] *= f_s[c0 + c];
 #pragma unroll 1
-                        for (int db = 0; db < NDB; ++db) {
-                            float o[CPT];
-                            tmem_ld<CPT>(tq + L::T_O + db * N, o);
+                        for (int c1 = 0; c1 < NDB * CPT; c1 += CH) {
+                            const int db = c1 / CPT, c = c1 % CPT;
+                            float o[CH];
+                            tmem_ld<CH>(tq + L::T_O + db * N + c, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int c = 0; c < CPT; ++c) o[c] *= f_s[c0 + c];
-                            tmem_st<CPT>(tq + L::T_O + db * N, o);
+                            for (int i = 0; i < CH; ++i) o[i] *= f_s[c0 + c + i];
+                            tmem_st<CH>(tq + L::T_O + db * N + c, o);
                         }
                         tmem_wait_st();
                     }
@@ -479,14 +506,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 if (it >= L::PBUF) wait(&pv_done[(it - L::PBUF) & 1], (it - L::PBUF) >> 1);
 #pragma unroll
                 for (int c = 0; c < CPT; c += 8) {
-                    const float4 ma = *reinterpret_cast<const float4*>(m_s + c0 + c);
-                    const float4 mb = *reinterpret_cast<const float4*>(m_s + c0 + c + 4);
-                    const float m[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float p0 = ex2_approx(x[c + 2 * i] - m[2 * i]);
-                        const float p1 = ex2_approx(x[c + 2 * i + 1] - m[2 * i + 1]);
+                        const float p0 = ex2_approx(x[c + 2 * i]);
+                        const float p1 = ex2_approx(x[c + 2 * i + 1]);
                         l[c + 2 * i] += p0;
                         l[c + 2 * i + 1] += p1;
                         const uint32_t w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
@@ -506,6 +530,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     // new tokens that not all rows see -- the rows that do get them back at the end
                     const int valid = min(TILE, s.len - t0);
                     const int from = max(0, max(0, s.len - a.K + 1) - t0), upto = (valid + 15) & ~15;
+#pragma unroll 1
                     for (int db = 0; db < NDB; ++db) {
                         const int k = sl0 + L::v_slot(j - s.tile0, s.tile1 - s.tile0) + db;
                         wait(&full[k % NS], k / NS);
@@ -518,7 +543,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             } else {
                                 const uint4 v = *p;
                                 if (!finite_bf16x8(v)) {
-                                    *odd_v = 1;
+                                    odd_v[par] = 1;
                                     *p = make_uint4(zero_non_finite(v.x), zero_non_finite(v.y), zero_non_finite(v.z),
                                                     zero_non_finite(v.w));
                                 }
@@ -531,12 +556,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[it & 1]);
             }
-
             sl0 += 2 * NDB * (s.tile1 - s.tile0);
+            more = start_segment(nx, par ^ 1);
 
             // ---- sums over the tokens: lanes by a butterfly that halves the columns, then the warps
-            wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
-            tc_fence_after();
 #pragma unroll
             for (int h = CPT / 2, o = 16; o >= 1; h /= 2, o /= 2) {
                 if (h >= 1) {
@@ -551,8 +574,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
                 }
             }
-            // lane i now has column i (CPT = 32) or i / 2 (CPT = 16)
-            if (CPT == 32 || (lane & 1) == 0) scr[quad * N + c0 + (CPT == 32 ? lane : lane >> 1)] = l[0];
+            wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);  // O is done; P's memory is free
+            tc_fence_after();
+            // lane i now has columns 2 i and 2 i + 1 (CPT = 64), i (32) or i / 2 (16)
+            float* scr_w = scr + quad * N + c0;
+            if constexpr (CPT == 64) *reinterpret_cast<float2*>(scr_w + 2 * lane) = make_float2(l[0], l[1]);
+            else if (CPT == 32 || (lane & 1) == 0) scr_w[CPT == 32 ? lane : lane >> 1] = l[0];
             softmax_sync<NSOFT>();
             float* slot = slot_ptr(a, 2 * blockIdx.x + (s.first ? 0 : 1));
             for (int c = st; c < nr; c += NSOFT) {
@@ -561,7 +588,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 f_s[c] = sum == 0.f ? 0.f : 1.0f / sum;
                 if (live) {
                     if (whole) {
-                        if (a.lse != nullptr) a.lse[off_s[c] / a.D] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+                        if (a.lse != nullptr)
+                            a.lse[row_index(a, s.b, s.h, r0 + c)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
                     } else {
                         slot[c] = m == kNone ? -INFINITY : m;
                         slot[a.rb_rows + c] = sum;
@@ -571,29 +599,33 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             softmax_sync<NSOFT>();
             // ---- outputs, 128 head dims at a time: turned into rows in P's memory, then read back 8 dims at a time
             // (one thread writing its dim of every row, unrolled, spent longer on fetching code than on the rest)
-            const bool odd = *odd_v != 0;
+            const bool odd = odd_v[par] != 0;
             float* o_s = reinterpret_cast<float*>(sm + L::O_P);  // [rows][128]
 #pragma unroll 1
             for (int db = 0; db < NDB; ++db) {
-                float o[CPT];
                 if (db > 0) softmax_sync<NSOFT>();
-                tmem_ld<CPT>(tq + L::T_O + db * N, o);
-                tmem_wait_ld();
-                if (odd && db * 128 + row < a.D) {
-                    const int t1 = min(s.len, s.tile1 * TILE);
-                    for (int t = max(s.tile0 * TILE, s.len - a.K + 1); t < t1; ++t) {
-                        const int page = a.table[(int64_t)s.b * a.max_pages + t / a.page_size];
-                        if (page < 0 || page >= a.n_pages) continue;
-                        const float v = to_f(static_cast<const bf16*>(
-                            a.v_cache)[(((int64_t)page * a.H_kv + s.h) * a.page_size + t % a.page_size) * a.D + db * 128 + row]);
-                        if (!isfinite(v))
+#pragma unroll 1
+                for (int c = 0; c < CPT; c += CH) {
+                    float o[CH];
+                    tmem_ld<CH>(tq + L::T_O + db * N + c, o);
+                    tmem_wait_ld();
+                    if (odd && db * 128 + row < a.D) {
+                        const int t1 = min(s.len, s.tile1 * TILE);
+                        for (int t = max(s.tile0 * TILE, s.len - a.K + 1); t < t1; ++t) {
+                            const int page = a.table[(int64_t)s.b * a.max_pages + t / a.page_size];
+                            if (page < 0 || page >= a.n_pages) continue;
+                            const float v = to_f(static_cast<const bf16*>(
+                                a.v_cache)[(((int64_t)page * a.H_kv + s.h) * a.page_size + t % a.page_size) * a.D + db * 128 + row]);
+                            if (!isfinite(v))
 #pragma unroll
-                            for (int c = 0; c < CPT; ++c)
-                                if (t < vis_s[c0 + c]) o[c] += v;
+                                for (int i = 0; i < CH; ++i)
+                                    if (t < vis_s[c0 + c + i]) o[i] += v;
+                        }
                     }
-                }
+                    __syncwarp();
 #pragma unroll
-                for (int c = 0; c < CPT; ++c) o_s[(c0 + c) * 128 + row] = o[c];
+                    for (int i = 0; i < CH; ++i) o_s[(c0 + c + i) * 128 + row] = o[i];
+                }
                 softmax_sync<NSOFT>();
 #pragma unroll 1
                 for (int e = st; e < nr * 16; e += NSOFT) {
@@ -602,15 +634,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     const float4 x0 = *reinterpret_cast<const float4*>(o_s + r * 128 + dd);
                     const float4 x1 = *reinterpret_cast<const float4*>(o_s + r * 128 + dd + 4);
                     if (whole) {
+                        const int64_t at = row_index(a, s.b, s.h, r0 + r) * a.D + d;
                         float y[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w}, gt[8];
                         const float inv = f_s[r];
-                        if (a.gate != nullptr) load16<bf16>(static_cast<const bf16*>(a.gate) + off_s[r] + d, gt);
+                        if (a.gate != nullptr) load16<bf16>(static_cast<const bf16*>(a.gate) + at, gt);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             y[i] *= inv;
                             if (a.gate != nullptr) y[i] *= sigmoid_f(gt[i]);
                         }
-                        store16<bf16>(static_cast<bf16*>(a.out) + off_s[r] + d, y);
+                        store16<bf16>(static_cast<bf16*>(a.out) + at, y);
                     } else {
                         float* p = slot + a.stat_floats + r * a.D + d;
                         *reinterpret_cast<float4*>(p) = x0;
@@ -619,6 +652,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 }
             }
             tc_fence_before();
+            s = nx;
+            par ^= 1;
         }
     }
     tc_fence_before();
