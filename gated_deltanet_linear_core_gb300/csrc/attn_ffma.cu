@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(NT, 1) attn_ffma_kernel(AttnArgs a) {
 // Joins the parts of every item that more than one CTA worked on.  The CTAs
 // whose ranges start inside an item (blockIdx.x + 1) share its rows, gridDim.y
 // blocks each.  A group of D / 4 threads takes a row, 4 columns per thread, and
-// runs through the parts in CTA order (with more than kSerial of them, the
-// groups of a block share one row's parts), keeping the running maximum, sum
+// runs through the parts in CTA order (more than kSerial of them are
+// shared out to several groups), keeping the running maximum, sum
 // and output as the tiles do; the order is fixed, so results do not depend on
 // timing.  Where the item lies is worked out before the wait for the kernel
 // that wrote the parts: the lengths are older than that kernel.
@@ -318,18 +318,20 @@ __global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a, int n_cta, in
     const int c0 = cta_of(p.total, u0, n_cta), c1 = cta_of(p.total, u1 - 1, n_cta);
     const int first_slot = cta_begin(p.total, c0, n_cta) == u0 ? 2 * c0 : 2 * c0 + 1;
     const int n = c1 - c0 + 1;
-    // many parts: a worker takes a quarter of a row, so that more groups share its parts
-    const int split = n > kSerial && a.D % 16 == 0 ? 4 : 1;
+    // many parts: groups share a row's parts, about 4 each; where a block has too few groups for that, a worker
+    // takes a quarter of a row
+    const int need = n > kSerial ? (n + 3) / 4 : 1;
+    const int split = JT / (a.D / 4) < need && a.D % 16 == 0 ? 4 : 1;
     const int ng = a.D / 4 / split, groups = JT / ng, grp = tid % ng, g = tid / ng;
     const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
     const int workers = (n - 1) * gridDim.y, worker = (c - c0 - 1) * gridDim.y + blockIdx.y;
-    const int share = n > kSerial ? groups : 1;  // groups on one row
+    const int share = need < groups ? need : groups;  // groups on one row
     const int at_once = groups / share, sub = g % share;
     pdl_wait();
     pdl_trigger();
     for (int first = worker * at_once; first < nr * split; first += workers * at_once) {
         const int rq = first + g / share, r = rq / split, d = ((rq - r * split) * ng + grp) * 4;
-        const bool mine = g < groups && rq < nr * split;
+        const bool mine = g < at_once * share && rq < nr * split;  // whole shares only
         Running run;
         if (mine) {
             constexpr int U = 4;

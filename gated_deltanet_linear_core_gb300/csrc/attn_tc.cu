@@ -425,15 +425,118 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             if (lane == 0) mbar_arrive(q_full);
             return true;
         };
-        Segment nx;
-        bool more = start_segment(s, par);
-        while (more) {
+        // Sums and outputs of a segment whose last tile is handed to the MMA warp.
+        auto finish_segment = [&](const Segment& s, int p, float (&l)[CPT]) {
             const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
             const bool whole = s.tile1 - s.tile0 == s.tiles;
+            const float* m_s = reinterpret_cast<float*>(sm + L::O_M) + p * N;
+            const int* vis_s = reinterpret_cast<int*>(sm + L::O_VIS) + p * N;
+            // ---- sums over the tokens: lanes by a butterfly that halves the columns, then the warps
+#pragma unroll
+            for (int h = CPT / 2, o = 16; o >= 1; h /= 2, o /= 2) {
+                if (h >= 1) {
+#pragma unroll
+                    for (int c = 0; c < CPT / 2; ++c)
+                        if (c < h) {
+                            const float send = lane & o ? l[c] : l[c + h];
+                            const float keep = lane & o ? l[c + h] : l[c];
+                            l[c] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                        }
+                } else {
+                    l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+                }
+            }
+            wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);  // O is done; P's memory is free
+            tc_fence_after();
+            // lane i now has columns 2 i and 2 i + 1 (CPT = 64), i (32) or i / 2 (16)
+            float* scr_w = scr + quad * N + c0;
+            if constexpr (CPT == 64) *reinterpret_cast<float2*>(scr_w + 2 * lane) = make_float2(l[0], l[1]);
+            else if (CPT == 32 || (lane & 1) == 0) scr_w[CPT == 32 ? lane : lane >> 1] = l[0];
+            softmax_sync<NSOFT>();
+            float* slot = slot_ptr(a, 2 * blockIdx.x + (s.first ? 0 : 1));
+            for (int c = st; c < nr; c += NSOFT) {
+                const float sum = (scr[c] + scr[N + c]) + (scr[2 * N + c] + scr[3 * N + c]);
+                const float m = m_s[c];
+                f_s[c] = sum == 0.f ? 0.f : 1.0f / sum;
+                if (live) {
+                    if (whole) {
+                        if (a.lse != nullptr)
+                            a.lse[row_index(a, s.b, s.h, r0 + c)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+                    } else {
+                        slot[c] = m == kNone ? -INFINITY : m;
+                        slot[a.rb_rows + c] = sum;
+                    }
+                }
+            }
+            softmax_sync<NSOFT>();
+            // ---- outputs, 128 head dims at a time: turned into rows in P's memory, then read back 8 dims at a time
+            // (one thread writing its dim of every row, unrolled, spent longer on fetching code than on the rest)
+            const bool odd = odd_v[p] != 0;
+            float* o_s = reinterpret_cast<float*>(sm + L::O_P);  // [rows][128]
+#pragma unroll 1
+            for (int db = 0; db < NDB; ++db) {
+                if (db > 0) softmax_sync<NSOFT>();
+#pragma unroll 1
+                for (int c = 0; c < CPT; c += CH) {
+                    float o[CH];
+                    tmem_ld<CH>(tq + L::T_O + db * N + c, o);
+                    tmem_wait_ld();
+                    if (odd && db * 128 + row < a.D) {
+                        const int t1 = min(s.len, s.tile1 * TILE);
+                        for (int t = max(s.tile0 * TILE, s.len - a.K + 1); t < t1; ++t) {
+                            const int page = a.table[(int64_t)s.b * a.max_pages + t / a.page_size];
+                            if (page < 0 || page >= a.n_pages) continue;
+                            const float v = to_f(static_cast<const bf16*>(
+                                a.v_cache)[(((int64_t)page * a.H_kv + s.h) * a.page_size + t % a.page_size) * a.D + db * 128 + row]);
+                            if (!isfinite(v))
+#pragma unroll
+                                for (int i = 0; i < CH; ++i)
+                                    if (t < vis_s[c0 + c + i]) o[i] += v;
+                        }
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) o_s[(c0 + c + i) * 128 + row] = o[i];
+                }
+                softmax_sync<NSOFT>();
+#pragma unroll 1
+                for (int e = st; e < nr * 16; e += NSOFT) {
+                    const int r = e >> 4, dd = (e & 15) * 8, d = db * 128 + dd;
+                    if (d >= a.D || !live) continue;
+                    const float4 x0 = *reinterpret_cast<const float4*>(o_s + r * 128 + dd);
+                    const float4 x1 = *reinterpret_cast<const float4*>(o_s + r * 128 + dd + 4);
+                    if (whole) {
+                        const int64_t at = row_index(a, s.b, s.h, r0 + r) * a.D + d;
+                        float y[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w}, gt[8];
+                        const float inv = f_s[r];
+                        if (a.gate != nullptr) load16<bf16>(static_cast<const bf16*>(a.gate) + at, gt);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            y[i] *= inv;
+                            if (a.gate != nullptr) y[i] *= __fdividef(1.0f, 1.0f + __expf(-gt[i]));  // far below bf16's step
+                        }
+                        store16<bf16>(static_cast<bf16*>(a.out) + at, y);
+                    } else {
+                        float* to = slot + a.stat_floats + r * a.D + d;
+                        *reinterpret_cast<float4*>(to) = x0;
+                        *reinterpret_cast<float4*>(to + 4) = x1;
+                    }
+                }
+            }
+            tc_fence_before();
+        };
+        float l[CPT];  // this token's part of the rows' sums
+        for (;;) {
+            // one copy of each part: the next segment's start, the last one's outputs, the tiles
+            Segment nx;
+            const bool more = start_segment(nx, par);
+            if (it > 0) finish_segment(s, par ^ 1, l);
+            if (!more) break;
+            s = nx;
+            const int r0 = s.rb * a.rb_rows;
             float* m_s = reinterpret_cast<float*>(sm + L::O_M) + par * N;    // running maxima
             const int* vis_s = reinterpret_cast<int*>(sm + L::O_VIS) + par * N;  // tokens a row sees
             softmax_sync<NSOFT>();  // they are written, and the outputs before are out of P's memory
-            float l[CPT];
 #pragma unroll
             for (int c = 0; c < CPT; ++c) l[c] = 0.f;
             const int least = visible(a, s.len, r0);  // what the block's first row sees
@@ -557,102 +660,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 if (lane == 0) mbar_arrive(&p_full[it & 1]);
             }
             sl0 += 2 * NDB * (s.tile1 - s.tile0);
-            more = start_segment(nx, par ^ 1);
-
-            // ---- sums over the tokens: lanes by a butterfly that halves the columns, then the warps
-#pragma unroll
-            for (int h = CPT / 2, o = 16; o >= 1; h /= 2, o /= 2) {
-                if (h >= 1) {
-#pragma unroll
-                    for (int c = 0; c < CPT / 2; ++c)
-                        if (c < h) {
-                            const float send = lane & o ? l[c] : l[c + h];
-                            const float keep = lane & o ? l[c + h] : l[c];
-                            l[c] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-                        }
-                } else {
-                    l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
-                }
-            }
-            wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);  // O is done; P's memory is free
-            tc_fence_after();
-            // lane i now has columns 2 i and 2 i + 1 (CPT = 64), i (32) or i / 2 (16)
-            float* scr_w = scr + quad * N + c0;
-            if constexpr (CPT == 64) *reinterpret_cast<float2*>(scr_w + 2 * lane) = make_float2(l[0], l[1]);
-            else if (CPT == 32 || (lane & 1) == 0) scr_w[CPT == 32 ? lane : lane >> 1] = l[0];
-            softmax_sync<NSOFT>();
-            float* slot = slot_ptr(a, 2 * blockIdx.x + (s.first ? 0 : 1));
-            for (int c = st; c < nr; c += NSOFT) {
-                const float sum = (scr[c] + scr[N + c]) + (scr[2 * N + c] + scr[3 * N + c]);
-                const float m = m_s[c];
-                f_s[c] = sum == 0.f ? 0.f : 1.0f / sum;
-                if (live) {
-                    if (whole) {
-                        if (a.lse != nullptr)
-                            a.lse[row_index(a, s.b, s.h, r0 + c)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
-                    } else {
-                        slot[c] = m == kNone ? -INFINITY : m;
-                        slot[a.rb_rows + c] = sum;
-                    }
-                }
-            }
-            softmax_sync<NSOFT>();
-            // ---- outputs, 128 head dims at a time: turned into rows in P's memory, then read back 8 dims at a time
-            // (one thread writing its dim of every row, unrolled, spent longer on fetching code than on the rest)
-            const bool odd = odd_v[par] != 0;
-            float* o_s = reinterpret_cast<float*>(sm + L::O_P);  // [rows][128]
-#pragma unroll 1
-            for (int db = 0; db < NDB; ++db) {
-                if (db > 0) softmax_sync<NSOFT>();
-#pragma unroll 1
-                for (int c = 0; c < CPT; c += CH) {
-                    float o[CH];
-                    tmem_ld<CH>(tq + L::T_O + db * N + c, o);
-                    tmem_wait_ld();
-                    if (odd && db * 128 + row < a.D) {
-                        const int t1 = min(s.len, s.tile1 * TILE);
-                        for (int t = max(s.tile0 * TILE, s.len - a.K + 1); t < t1; ++t) {
-                            const int page = a.table[(int64_t)s.b * a.max_pages + t / a.page_size];
-                            if (page < 0 || page >= a.n_pages) continue;
-                            const float v = to_f(static_cast<const bf16*>(
-                                a.v_cache)[(((int64_t)page * a.H_kv + s.h) * a.page_size + t % a.page_size) * a.D + db * 128 + row]);
-                            if (!isfinite(v))
-#pragma unroll
-                                for (int i = 0; i < CH; ++i)
-                                    if (t < vis_s[c0 + c + i]) o[i] += v;
-                        }
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < CH; ++i) o_s[(c0 + c + i) * 128 + row] = o[i];
-                }
-                softmax_sync<NSOFT>();
-#pragma unroll 1
-                for (int e = st; e < nr * 16; e += NSOFT) {
-                    const int r = e >> 4, dd = (e & 15) * 8, d = db * 128 + dd;
-                    if (d >= a.D || !live) continue;
-                    const float4 x0 = *reinterpret_cast<const float4*>(o_s + r * 128 + dd);
-                    const float4 x1 = *reinterpret_cast<const float4*>(o_s + r * 128 + dd + 4);
-                    if (whole) {
-                        const int64_t at = row_index(a, s.b, s.h, r0 + r) * a.D + d;
-                        float y[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w}, gt[8];
-                        const float inv = f_s[r];
-                        if (a.gate != nullptr) load16<bf16>(static_cast<const bf16*>(a.gate) + at, gt);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            y[i] *= inv;
-                            if (a.gate != nullptr) y[i] *= sigmoid_f(gt[i]);
-                        }
-                        store16<bf16>(static_cast<bf16*>(a.out) + at, y);
-                    } else {
-                        float* p = slot + a.stat_floats + r * a.D + d;
-                        *reinterpret_cast<float4*>(p) = x0;
-                        *reinterpret_cast<float4*>(p + 4) = x1;
-                    }
-                }
-            }
-            tc_fence_before();
-            s = nx;
             par ^= 1;
         }
     }
