@@ -17,11 +17,15 @@
 // stays below 2^8, harmless in f32 sums), so most tiles need one vote and no
 // rescaling of O.  P is handed to the MMA as two bf16 (the value cut to 8 bits
 // and the rounded rest, 16 bits in all): one bf16 alone would add an error of
-// the size of the output's own rounding, and the second MMA is free, since the
-// kernel waits for HBM.  Sums are kept per thread in f32 and joined at the end.
+// the size of the output's own rounding.  Up to 64 rows both are columns of one
+// MMA (2 N columns, joined at the end): its time is that of reading V, so the
+// rest is free; two MMAs per step were bound by that (64 rows: 3.2 us per tile
+// of head dim 256 where HBM takes 2.9).  Sums are kept per thread in f32 and joined at the end.
 //
-// Warps: 0 loads, 1 issues the MMAs, the others are the softmax.  The MMA warp
-// runs S of the next tile ahead of P V of this one.  Every wait is bounded
+// Warps: 0 loads K and V, 1 issues the MMAs, 2 loads Q of the next segment as
+// soon as S of the last tile is done, the others are the softmax.  The MMA warp
+// runs S of the next tile ahead of P V of this one, across segments too, so
+// that only the outputs stand between two segments.  Every wait is bounded
 // (1 s): on a timeout the roles run out without waiting, the copies in flight
 // land, TMEM is freed and the error word is set.
 #include <cuda.h>
@@ -52,15 +56,15 @@ struct Layout {
     static constexpr int CH = CPT < 32 ? CPT : 32;   // columns per TMEM access
     static constexpr int NWG = N / CPT;           // softmax warpgroups
     static constexpr int NSW = 4 * NWG;           // softmax warps
-    static constexpr int NT = 64 + 32 * NSW;
+    static constexpr int NT = 96 + 32 * NSW;
     static constexpr int PBUF = N <= 64 ? 2 : 1;  // buffers of P
     // P of a tile: 128-byte rows of 64 columns.  N = 16: both buffers' [hi | lo] side by side in one
     // block; N = 32: [hi | lo] in one block per buffer; else hi and lo in blocks of their own.
     static constexpr int P_BYTES = N == 16 ? SLAB : N == 32 ? 2 * SLAB : PBUF * 2 * ((N + 63) / 64) * SLAB;
     static constexpr int Q_BYTES = 2 * NDB * N * 128;
-    static constexpr int SCR = N <= 64 ? 4 * N * 4 : 0;  // scratch of its own (N = 128: in P, free by then)
+    static constexpr int SCR = 4 * NWG * CH * 4;     // scratch: a value per lane quarter and column of one access
     static constexpr int BARS = 256;
-    static constexpr int SMALL = BARS + N * 4 * 5 + SCR;
+    static constexpr int SMALL = BARS + N * 4 * 3 + SCR;
     static constexpr int FIT = (kSmemMax - P_BYTES - Q_BYTES - SMALL) / SLOT;
     static constexpr int NS = FIT < 6 ? FIT : 6;
     // Slots are filled and used in the order K(0), K(1), V(0), K(2), V(1), .. of a segment's n tiles
@@ -70,17 +74,18 @@ struct Layout {
     static constexpr int O_Q = NS * SLOT;
     static constexpr int O_P = O_Q + Q_BYTES;
     static constexpr int O_BAR = O_P + P_BYTES;
-    static constexpr int O_M = O_BAR + BARS;    // [2 segments][N]
-    static constexpr int O_VIS = O_M + 2 * N * 4;  // [2 segments][N]
-    static constexpr int O_F = O_VIS + 2 * N * 4;
-    static constexpr int O_SCR = N <= 64 ? O_F + N * 4 : O_P;
+    static constexpr int O_M = O_BAR + BARS;
+    static constexpr int O_VIS = O_M + N * 4;
+    static constexpr int O_F = O_VIS + N * 4;
+    static constexpr int O_SCR = O_F + N * 4;
     static constexpr int SMEM = O_BAR + SMALL;
     static constexpr int T_S = 0, T_O = 2 * N;
-    static constexpr int T_USED = (2 + NDB) * N;
+    static constexpr int PARTS = N <= 64 ? 2 : 1;  // O of P's upper and lower halves side by side, or their sum
+    static constexpr int T_USED = (2 + NDB * PARTS) * N;
     static constexpr int T_COLS = T_USED <= 64 ? 64 : T_USED <= 128 ? 128 : T_USED <= 256 ? 256 : 512;
     static_assert(N * 512 <= P_BYTES, "output rows");
     static_assert(SMEM <= kSmemMax && NS >= 3, "shared memory");
-    static_assert(20 * 8 + 16 <= BARS, "barriers");
+    static_assert(21 * 8 + 16 <= BARS, "barriers");
 
     // byte offset of P's column block (16-byte chunk j of 8 columns) of token t
     __device__ static __forceinline__ uint32_t p_off(int buf, int lo, int chunk, int t) {
@@ -200,10 +205,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     uint64_t* s_full = bars + 12;     // [2] S of a tile done
     uint64_t* p_full = bars + 14;     // [2] P of a tile written, V tail mended (softmax warps)
     uint64_t* pv_done = bars + 16;    // [2] P V of a tile done
-    uint64_t* q_full = bars + 18;     // a segment's Q written (softmax warps)
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 19);
+    uint64_t* q_full = bars + 18;     // a segment's Q written (Q warp)
+    uint64_t* q_empty = bars + 19;    // S of a segment's last tile done
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 20);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-    volatile int* odd_v = reinterpret_cast<volatile int*>(tslot + 2);  // [2 segments] a new token's value is not finite
+    volatile int* odd_v = reinterpret_cast<volatile int*>(tslot + 2);  // a new token's value is not finite
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
@@ -216,9 +222,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             mbar_init(&p_full[i], L::NSW);
             mbar_init(&pv_done[i], 1);
         }
-        mbar_init(q_full, L::NSW);
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
         *abort_flag = 0;
-        odd_v[0] = odd_v[1] = 0;
+        *odd_v = 0;
         fence_mbar_init();
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
@@ -338,6 +345,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 ++seg;
                 for (int j = -1; ok && j < n; ++j) {  // S of tile j + 1, then P V of tile j
                     if (j + 1 < n && !issue_s(it + (j < 0 ? 0 : 1), sl0 + L::k_slot(j + 1))) { ok = false; break; }
+                    if (j + 2 == n) mma_commit(q_empty);
                     if (j < 0) continue;
                     ok = wait_or_abort(&p_full[it & 1], (uint32_t)((it >> 1) & 1), abort_flag);
                     if (!ok) break;
@@ -350,13 +358,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         tc_fence_after();
                         const uint32_t va = desc_lo(base + (k % NS) * SLOT, SLAB);
 #pragma unroll
-                        for (int lo = 0; lo < 2; ++lo) {
+                        for (int lo = 0; lo < (L::PARTS == 2 ? 1 : 2); ++lo) {
                             const uint32_t pa = desc_lo(base + L::O_P + L::p_start(buf, lo), SLAB);
 #pragma unroll
                             for (int q = 0; q < 8; ++q)
                                 if (q < pk)
-                                    mma_lo(tb + L::T_O + db * N, va + q * (2048 >> 4), pa + q * (2048 >> 4),
-                                             idesc_bf16_f32(128, N, 1, 1), j > 0 || lo > 0 || q > 0);
+                                    mma_lo(tb + L::T_O + db * L::PARTS * N, va + q * (2048 >> 4), pa + q * (2048 >> 4),
+                                           idesc_bf16_f32(128, L::PARTS * N, 1, 1), j > 0 || lo > 0 || q > 0);
                         }
                         mma_commit(&empty[k % NS]);
                     }
@@ -370,32 +378,55 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             }
             if (*abort_flag && last != nullptr) mbar_wait(last, last_parity, kWaitNs);
         }
+    } else if (warp == 2) {
+        // ------------------------------------------------ Q rows, zero beyond the block's rows and the head's dims
+        int seg = 0;
+        while (walk.next(a, TILE, s)) {
+            if (s.len == 0) continue;
+            const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
+            if (seg > 0 && !__all_sync(0xffffffffu, wait_or_abort(q_empty, (uint32_t)((seg - 1) & 1), abort_flag))) break;
+            const uint32_t qs = smem_u32(sm) + L::O_Q;
+#pragma unroll 1
+            for (int r = lane / (4 * NDB); r < N; r += 32 / (4 * NDB)) {  // 4 NDB lanes per row, 4 pieces each
+                const bf16* src = static_cast<const bf16*>(a.q) + (r < nr ? row_index(a, s.b, s.h, r0 + r) * a.D : 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int ch = lane % (4 * NDB) + i * 4 * NDB;  // 8 dims
+                    const bool real = r < nr && ch * 8 < a.D;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     qs + (ch >> 3) * (N * 128) + sw128_off((uint32_t)r, (uint32_t)(ch & 7) * 8)),
+                                 "l"(real ? src + ch * 8 : src), "r"(real ? 16 : 0)
+                                 : "memory");
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+            ++seg;
+        }
     } else {
         // ------------------------------------------------ softmax and outputs
         constexpr int CH = L::CH;
-        const int st = tid - 64;                 // softmax thread
+        const int st = tid - 96;                 // softmax thread
         const int quad = warp & 3;               // its TMEM lanes: 32 quad ..
         const int row = quad * 32 + lane;        // token of a tile, head dim of an output block
-        const int c0 = ((warp - 2) >> 2) * CPT;  // its columns: c0 ..
+        const int c0 = ((warp - 3) >> 2) * CPT;  // its columns: c0 ..
         const uint32_t tq = tb + ((uint32_t)(quad * 32) << 16) + c0;
-        float* f_s = reinterpret_cast<float*>(sm + L::O_F);    // factors of a rescaling, 1 / l at the end
-        float* scr = reinterpret_cast<float*>(sm + L::O_SCR);  // [4 lane quarters][N]
+        float* m_s = reinterpret_cast<float*>(sm + L::O_M);     // running maxima
+        int* vis_s = reinterpret_cast<int*>(sm + L::O_VIS);     // tokens a row sees
+        float* f_s = reinterpret_cast<float*>(sm + L::O_F);     // factors of a rescaling, 1 / l at the end
+        float* scr = reinterpret_cast<float*>(sm + L::O_SCR);   // [4 lane quarters][NWG * CH]
         int it = 0, sl0 = 0;  // tiles and slots before
-        int par = 0;          // parity of the segment: which of the doubled arrays are its own
         bool live = true;     // no wait gave up: outputs are written only then
         auto wait = [&](uint64_t* bar, int k) {
             live = __all_sync(0xffffffffu, live && wait_or_abort(bar, (uint32_t)(k & 1), abort_flag));
         };
-        // The next segment with tokens (rows of empty sequences become zeros on the way), its running maxima,
-        // what its rows see, and its Q: all but the outputs of the segment before, so that S of its first tile
-        // runs beside them.  Q's memory is free once S of the last tile before is done.
-        auto start_segment = [&](Segment& g, int p) -> bool {
-            int r0, nr;
-            for (;;) {
-                if (!walk.next(a, TILE, g)) return false;
-                r0 = g.rb * a.rb_rows;
-                nr = block_rows(a, g.rb);
-                if (g.len > 0) break;
+        // The next segment with tokens; rows of empty sequences become zeros on the way.
+        auto next_segment = [&](Segment& g) -> bool {
+            while (walk.next(a, TILE, g)) {
+                if (g.len > 0) return true;
+                const int r0 = g.rb * a.rb_rows, nr = block_rows(a, g.rb);
                 for (int e = st; e < nr * a.D; e += NSOFT) {
                     const int r = e / a.D, d = e - r * a.D;
                     const int64_t at = row_index(a, g.b, g.h, r0 + r);
@@ -403,35 +434,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     if (d == 0 && a.lse != nullptr) a.lse[at] = -INFINITY;
                 }
             }
-            float* m = reinterpret_cast<float*>(sm + L::O_M) + p * N;
-            int* vis = reinterpret_cast<int*>(sm + L::O_VIS) + p * N;
-            // rows beyond the block's and dims beyond the head's are zero
-#pragma unroll 4
-            for (int e = st; e < N * 16 * NDB; e += NSOFT) {
-                const int r = e / (16 * NDB), ch = e % (16 * NDB);
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (r < nr && ch * 8 < a.D)
-                    x = __ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) +
-                                                             row_index(a, g.b, g.h, r0 + r) * a.D + ch * 8));
-                *reinterpret_cast<uint4*>(sm + L::O_Q + (ch >> 3) * (N * 128) + sw128_off((uint32_t)r, (uint32_t)(ch & 7) * 8)) = x;
-            }
-            for (int c = st; c < N; c += NSOFT) {
-                m[c] = kNone;
-                vis[c] = c < nr ? visible(a, g.len, r0 + c) : 0;
-            }
-            if (st == 0) odd_v[p] = 0;
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
-            return true;
+            return false;
         };
         // Sums and outputs of a segment whose last tile is handed to the MMA warp.
-        auto finish_segment = [&](const Segment& s, int p, float (&l)[CPT]) {
+        auto finish_segment = [&](const Segment& s, float (&l)[CPT]) {
             const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
             const bool whole = s.tile1 - s.tile0 == s.tiles;
-            const float* m_s = reinterpret_cast<float*>(sm + L::O_M) + p * N;
-            const int* vis_s = reinterpret_cast<int*>(sm + L::O_VIS) + p * N;
-            // ---- sums over the tokens: lanes by a butterfly that halves the columns, then the warps
+            // sums over the tokens: lanes by a butterfly that halves the columns, then the warps
 #pragma unroll
             for (int h = CPT / 2, o = 16; o >= 1; h /= 2, o /= 2) {
                 if (h >= 1) {
@@ -449,13 +458,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);  // O is done; P's memory is free
             tc_fence_after();
             // lane i now has columns 2 i and 2 i + 1 (CPT = 64), i (32) or i / 2 (16)
-            float* scr_w = scr + quad * N + c0;
+            float* sum_s = CPT == CH ? scr : reinterpret_cast<float*>(sm + L::O_P);  // [4 lane quarters][N]
+            float* scr_w = sum_s + quad * N + c0;
             if constexpr (CPT == 64) *reinterpret_cast<float2*>(scr_w + 2 * lane) = make_float2(l[0], l[1]);
             else if (CPT == 32 || (lane & 1) == 0) scr_w[CPT == 32 ? lane : lane >> 1] = l[0];
             softmax_sync<NSOFT>();
             float* slot = slot_ptr(a, 2 * blockIdx.x + (s.first ? 0 : 1));
             for (int c = st; c < nr; c += NSOFT) {
-                const float sum = (scr[c] + scr[N + c]) + (scr[2 * N + c] + scr[3 * N + c]);
+                const float sum = (sum_s[c] + sum_s[N + c]) + (sum_s[2 * N + c] + sum_s[3 * N + c]);
                 const float m = m_s[c];
                 f_s[c] = sum == 0.f ? 0.f : 1.0f / sum;
                 if (live) {
@@ -469,9 +479,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 }
             }
             softmax_sync<NSOFT>();
-            // ---- outputs, 128 head dims at a time: turned into rows in P's memory, then read back 8 dims at a time
+            // outputs, 128 head dims at a time: turned into rows in P's memory, then read back 8 dims at a time
             // (one thread writing its dim of every row, unrolled, spent longer on fetching code than on the rest)
-            const bool odd = odd_v[p] != 0;
+            const bool odd = *odd_v != 0;
             float* o_s = reinterpret_cast<float*>(sm + L::O_P);  // [rows][128]
 #pragma unroll 1
             for (int db = 0; db < NDB; ++db) {
@@ -479,8 +489,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 #pragma unroll 1
                 for (int c = 0; c < CPT; c += CH) {
                     float o[CH];
-                    tmem_ld<CH>(tq + L::T_O + db * N + c, o);
-                    tmem_wait_ld();
+                    const uint32_t to = tq + L::T_O + db * L::PARTS * N + c;
+                    tmem_ld<CH>(to, o);
+                    if constexpr (L::PARTS == 2) {
+                        float o2[CH];
+                        tmem_ld<CH>(to + N, o2);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < CH; ++i) o[i] += o2[i];
+                    } else {
+                        tmem_wait_ld();
+                    }
                     if (odd && db * 128 + row < a.D) {
                         const int t1 = min(s.len, s.tile1 * TILE);
                         for (int t = max(s.tile0 * TILE, s.len - a.K + 1); t < t1; ++t) {
@@ -513,13 +532,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             y[i] *= inv;
-                            if (a.gate != nullptr) y[i] *= __fdividef(1.0f, 1.0f + __expf(-gt[i]));  // far below bf16's step
+                            // the approximate exponential and quotient: far below the step of bf16
+                            if (a.gate != nullptr) y[i] *= __fdividef(1.0f, 1.0f + __expf(-gt[i]));
                         }
                         store16<bf16>(static_cast<bf16*>(a.out) + at, y);
                     } else {
-                        float* to = slot + a.stat_floats + r * a.D + d;
-                        *reinterpret_cast<float4*>(to) = x0;
-                        *reinterpret_cast<float4*>(to + 4) = x1;
+                        float* p = slot + a.stat_floats + r * a.D + d;
+                        *reinterpret_cast<float4*>(p) = x0;
+                        *reinterpret_cast<float4*>(p + 4) = x1;
                     }
                 }
             }
@@ -527,105 +547,112 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         };
         float l[CPT];  // this token's part of the rows' sums
         for (;;) {
-            // one copy of each part: the next segment's start, the last one's outputs, the tiles
+            // one copy of each part: the next segment, the last one's outputs, the tiles
             Segment nx;
-            const bool more = start_segment(nx, par);
-            if (it > 0) finish_segment(s, par ^ 1, l);
+            const bool more = next_segment(nx);
+            if (it > 0) finish_segment(s, l);
             if (!more) break;
             s = nx;
-            const int r0 = s.rb * a.rb_rows;
-            float* m_s = reinterpret_cast<float*>(sm + L::O_M) + par * N;    // running maxima
-            const int* vis_s = reinterpret_cast<int*>(sm + L::O_VIS) + par * N;  // tokens a row sees
-            softmax_sync<NSOFT>();  // they are written, and the outputs before are out of P's memory
+            const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
+            softmax_sync<NSOFT>();  // the outputs before are out of P's memory and the arrays
+            for (int c = st; c < N; c += NSOFT) {
+                m_s[c] = kNone;
+                vis_s[c] = c < nr ? visible(a, s.len, r0 + c) : 0;
+            }
+            if (st == 0) *odd_v = 0;
+            softmax_sync<NSOFT>();
 #pragma unroll
             for (int c = 0; c < CPT; ++c) l[c] = 0.f;
             const int least = visible(a, s.len, r0);  // what the block's first row sees
             for (int j = s.tile0; j < s.tile1; ++j, ++it) {
                 const int t0 = j * TILE;
-                const bool tail = t0 + TILE > least;
-                float x[CPT];  // scores in the log2 domain, less the running maximum
+                const bool first = j == s.tile0, tail = t0 + TILE > least;
+                const int buf = L::PBUF == 2 ? it & 1 : 0;
                 wait(&s_full[it & 1], it >> 1);
                 tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < CPT; c += CH) tmem_ld<CH>(tq + L::T_S + (it & 1) * N + c, x + c);
-                tmem_wait_ld();
-                float top = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < CPT; c += 4) {
-                    const float4 m4 = *reinterpret_cast<const float4*>(m_s + c0 + c);
-                    const float m[4] = {m4.x, m4.y, m4.z, m4.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[c + i] = fmaf(x[c + i], a.scale_log2, -m[i]);
-                    if (tail) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (t0 + row >= vis_s[c0 + c + i]) x[c + i] = -INFINITY;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) top = fmaxf(top, x[c + i]);
-                }
-                if (softmax_any<NSOFT>(top > kSlack)) {
-                    // ---- new maxima; sums and outputs so far are scaled to them
-                    const bool first = j == s.tile0;
-                    if (!first) wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
-                    tc_fence_after();
-#pragma unroll
-                    for (int c = 0; c < CPT; c += CH) tmem_ld<CH>(tq + L::T_S + (it & 1) * N + c, x + c);
+                for (int c1 = 0; c1 < CPT; c1 += CH) {  // CH columns at a time
+                    const uint32_t ts = tq + L::T_S + (it & 1) * N + c1;
+                    float x[CH];  // scores in the log2 domain, less the running maximum
+                    tmem_ld<CH>(ts, x);
                     tmem_wait_ld();
+                    float top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < CPT; ++c) {
-                        x[c] *= a.scale_log2;
-                        if (tail && t0 + row >= vis_s[c0 + c]) x[c] = -INFINITY;
-                        const float t = warp_max(x[c]);
-                        if (lane == 0) scr[quad * N + c0 + c] = t;
-                    }
-                    softmax_sync<NSOFT>();
-                    for (int c = st; c < N; c += NSOFT) {
-                        const float m0 = m_s[c];
-                        const float m1 = fmaxf(fmaxf(fmaxf(scr[c], scr[N + c]), fmaxf(scr[2 * N + c], scr[3 * N + c])), m0);
-                        m_s[c] = m1;
-                        f_s[c] = ex2_approx(m0 - m1);
-                    }
-                    softmax_sync<NSOFT>();
+                    for (int c = 0; c < CH; c += 4) {
+                        const float4 m4 = *reinterpret_cast<const float4*>(m_s + c0 + c1 + c);
+                        const float m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
-                    for (int c = 0; c < CPT; ++c) x[c] -= m_s[c0 + c];
-                    if (!first) {
+                        for (int i = 0; i < 4; ++i) x[c + i] = fmaf(x[c + i], a.scale_log2, -m[i]);
+                        if (tail) {
 #pragma unroll
-                        for (int c = 0; c < CPT; ++c) l[c] *= f_s[c0 + c];
-#pragma unroll 1
-                        for (int c1 = 0; c1 < NDB * CPT; c1 += CH) {
-                            const int db = c1 / CPT, c = c1 % CPT;
-                            float o[CH];
-                            tmem_ld<CH>(tq + L::T_O + db * N + c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < CH; ++i) o[i] *= f_s[c0 + c + i];
-                            tmem_st<CH>(tq + L::T_O + db * N + c, o);
+                            for (int i = 0; i < 4; ++i)
+                                if (t0 + row >= vis_s[c0 + c1 + c + i]) x[c + i] = -INFINITY;
                         }
-                        tmem_wait_st();
-                    }
-                }
-                const int buf = L::PBUF == 2 ? it & 1 : 0;
-                if (it >= L::PBUF) wait(&pv_done[(it - L::PBUF) & 1], (it - L::PBUF) >> 1);
 #pragma unroll
-                for (int c = 0; c < CPT; c += 8) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float p0 = ex2_approx(x[c + 2 * i]);
-                        const float p1 = ex2_approx(x[c + 2 * i + 1]);
-                        l[c + 2 * i] += p0;
-                        l[c + 2 * i + 1] += p1;
-                        const uint32_t w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
-                        hi[i] = __byte_perm(w0, w1, 0x7632);  // the upper halves: cut, not rounded
-                        // the rest, at least p's last bit: a rest of 0 would turn an infinite value into NaN
-                        lo[i] = pack_bf16x2(__uint_as_float(w0 | 1u) - __uint_as_float(w0 & 0xffff0000u),
-                                            __uint_as_float(w1 | 1u) - __uint_as_float(w1 & 0xffff0000u));
+                        for (int i = 0; i < 4; ++i) top = fmaxf(top, x[c + i]);
                     }
-                    *reinterpret_cast<uint4*>(sm + L::O_P + L::p_off(buf, 0, (c0 + c) >> 3, row)) =
-                        make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(sm + L::O_P + L::p_off(buf, 1, (c0 + c) >> 3, row)) =
-                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    if (softmax_any<NSOFT>(top > kSlack)) {
+                        // ---- new maxima; sums and outputs so far are scaled to them
+                        if (!first) wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
+                        tc_fence_after();
+                        tmem_ld<CH>(ts, x);
+                        tmem_wait_ld();
+                        constexpr int W = L::NWG * CH;
+                        const int w0 = ((warp - 3) >> 2) * CH;
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            x[c] *= a.scale_log2;
+                            if (tail && t0 + row >= vis_s[c0 + c1 + c]) x[c] = -INFINITY;
+                            const float t = warp_max(x[c]);
+                            if (lane == 0) scr[quad * W + w0 + c] = t;
+                        }
+                        softmax_sync<NSOFT>();
+                        for (int i = st; i < W; i += NSOFT) {
+                            const int c = i / CH * CPT + c1 + i % CH;
+                            const float m0 = m_s[c];
+                            const float m1 = fmaxf(fmaxf(fmaxf(scr[i], scr[W + i]), fmaxf(scr[2 * W + i], scr[3 * W + i])), m0);
+                            m_s[c] = m1;
+                            f_s[c] = ex2_approx(m0 - m1);
+                        }
+                        softmax_sync<NSOFT>();
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) x[c] -= m_s[c0 + c1 + c];
+                        if (!first) {
+#pragma unroll
+                            for (int c = 0; c < CH; ++c) l[c1 + c] *= f_s[c0 + c1 + c];
+#pragma unroll 1
+                            for (int i = 0; i < NDB * L::PARTS; ++i) {
+                                float o[CH];
+                                tmem_ld<CH>(tq + L::T_O + i * N + c1, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int c = 0; c < CH; ++c) o[c] *= f_s[c0 + c1 + c];
+                                tmem_st<CH>(tq + L::T_O + i * N + c1, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    if (c1 == 0 && it >= L::PBUF) wait(&pv_done[(it - L::PBUF) & 1], (it - L::PBUF) >> 1);
+#pragma unroll
+                    for (int c = 0; c < CH; c += 8) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float p0 = ex2_approx(x[c + 2 * i]);
+                            const float p1 = ex2_approx(x[c + 2 * i + 1]);
+                            l[c1 + c + 2 * i] += p0;
+                            l[c1 + c + 2 * i + 1] += p1;
+                            const uint32_t w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
+                            hi[i] = __byte_perm(w0, w1, 0x7632);  // the upper halves: cut, not rounded
+                            // the rest, at least p's last bit: a rest of 0 would turn an infinite value into NaN
+                            lo[i] = pack_bf16x2(__uint_as_float(w0 | 1u) - __uint_as_float(w0 & 0xffff0000u),
+                                                __uint_as_float(w1 | 1u) - __uint_as_float(w1 & 0xffff0000u));
+                        }
+                        *reinterpret_cast<uint4*>(sm + L::O_P + L::p_off(buf, 0, (c0 + c1 + c) >> 3, row)) =
+                            make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(sm + L::O_P + L::p_off(buf, 1, (c0 + c1 + c) >> 3, row)) =
+                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
                 }
                 if (tail) {
                     // V rows behind the sequence's end that the MMA's last 16-token step reads become zeros
@@ -646,7 +673,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             } else {
                                 const uint4 v = *p;
                                 if (!finite_bf16x8(v)) {
-                                    odd_v[par] = 1;
+                                    *odd_v = 1;
                                     *p = make_uint4(zero_non_finite(v.x), zero_non_finite(v.y), zero_non_finite(v.z),
                                                     zero_non_finite(v.w));
                                 }
@@ -660,7 +687,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 if (lane == 0) mbar_arrive(&p_full[it & 1]);
             }
             sl0 += 2 * NDB * (s.tile1 - s.tile0);
-            par ^= 1;
         }
     }
     tc_fence_before();
