@@ -455,6 +455,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
                 }
             }
+            // the output loop below has this many rounds per 128 dims; the gate's values are loaded two rounds ahead
+            const int rounds = (nr * 16 + NSOFT - 1) / NSOFT;
+            const bool gated = whole && a.gate != nullptr;
+            // row_index of the block's row c, its new token taken from what the row sees
+            auto out_row = [&](int c) -> int64_t {
+                const int i = vis_s[c] - s.len + a.K - 1;
+                return ((int64_t)s.b * a.K + i) * a.H_q + s.h * a.group + (r0 + c - i * a.group);
+            };
+            auto gate_of = [&](int i) -> uint4 {
+                const int db = i >= rounds ? 1 : 0, e = st + (i - db * rounds) * NSOFT, d = db * 128 + (e & 15) * 8;
+                if (!gated || e >= nr * 16 || d >= a.D) return make_uint4(0u, 0u, 0u, 0u);
+                return __ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.gate) + out_row(e >> 4) * a.D + d));
+            };
+            uint4 g0 = gate_of(0), g1 = gate_of(1);
             wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);  // O is done; P's memory is free
             tc_fence_after();
             // lane i now has columns 2 i and 2 i + 1 (CPT = 64), i (32) or i / 2 (16)
@@ -471,7 +485,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 if (live) {
                     if (whole) {
                         if (a.lse != nullptr)
-                            a.lse[row_index(a, s.b, s.h, r0 + c)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+                            a.lse[out_row(c)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
                     } else {
                         slot[c] = m == kNone ? -INFINITY : m;
                         slot[a.rb_rows + c] = sum;
@@ -519,21 +533,24 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 }
                 softmax_sync<NSOFT>();
 #pragma unroll 1
-                for (int e = st; e < nr * 16; e += NSOFT) {
-                    const int r = e >> 4, dd = (e & 15) * 8, d = db * 128 + dd;
-                    if (d >= a.D || !live) continue;
+                for (int i = 0; i < rounds; ++i) {
+                    const uint4 gv = g0;
+                    g0 = g1;
+                    g1 = gate_of(db * rounds + i + 2);
+                    const int e = st + i * NSOFT, r = e >> 4, dd = (e & 15) * 8, d = db * 128 + dd;
+                    if (r >= nr || d >= a.D || !live) continue;
                     const float4 x0 = *reinterpret_cast<const float4*>(o_s + r * 128 + dd);
                     const float4 x1 = *reinterpret_cast<const float4*>(o_s + r * 128 + dd + 4);
                     if (whole) {
-                        const int64_t at = row_index(a, s.b, s.h, r0 + r) * a.D + d;
+                        const int64_t at = out_row(r) * a.D + d;
                         float y[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w}, gt[8];
                         const float inv = f_s[r];
-                        if (a.gate != nullptr) load16<bf16>(static_cast<const bf16*>(a.gate) + at, gt);
+                        unpack16<bf16>(gv, gt);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             y[i] *= inv;
                             // the approximate exponential and quotient: far below the step of bf16
-                            if (a.gate != nullptr) y[i] *= __fdividef(1.0f, 1.0f + __expf(-gt[i]));
+                            if (gated) y[i] *= __fdividef(1.0f, 1.0f + __expf(-gt[i]));
                         }
                         store16<bf16>(static_cast<bf16*>(a.out) + at, y);
                     } else {
