@@ -160,10 +160,25 @@ template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const float* v) {
     if constexpr (N == 16) tmem_st16(taddr, v); else tmem_st32(taddr, v);
 }
-__device__ __forceinline__ float warp_max(float x) {
-    float y;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-    return y;
+// Joins C columns over the warp's lanes, halving the columns a lane holds at
+// each step: v[0 .. C / 32) of lane i becomes columns (C / 32) i .. (C = 16: lane
+// i has column i / 2).  A reduction per column costs several times as much.
+template <int C, typename F>
+__device__ __forceinline__ void join_lanes(float* v, int lane, F f) {
+#pragma unroll
+    for (int h = C / 2, o = 16; o >= 1; h /= 2, o /= 2) {
+        if (h >= 1) {
+#pragma unroll
+            for (int c = 0; c < C / 2; ++c)
+                if (c < h) {
+                    const float send = lane & o ? v[c] : v[c + h];
+                    const float keep = lane & o ? v[c + h] : v[c];
+                    v[c] = f(keep, __shfl_xor_sync(0xffffffffu, send, o));
+                }
+        } else {
+            v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+        }
+    }
 }
 __device__ __forceinline__ bool finite_bf16x8(uint4 u) {
     bool ok = true;
@@ -440,21 +455,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         auto finish_segment = [&](const Segment& s, float (&l)[CPT]) {
             const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
             const bool whole = s.tile1 - s.tile0 == s.tiles;
-            // sums over the tokens: lanes by a butterfly that halves the columns, then the warps
-#pragma unroll
-            for (int h = CPT / 2, o = 16; o >= 1; h /= 2, o /= 2) {
-                if (h >= 1) {
-#pragma unroll
-                    for (int c = 0; c < CPT / 2; ++c)
-                        if (c < h) {
-                            const float send = lane & o ? l[c] : l[c + h];
-                            const float keep = lane & o ? l[c + h] : l[c];
-                            l[c] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-                        }
-                } else {
-                    l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
-                }
-            }
+            // sums over the tokens: the lanes, then the warps
+            join_lanes<CPT>(l, lane, [](float x, float y) { return x + y; });
             // the output loop below has this many rounds per 128 dims; the gate's values are loaded two rounds ahead
             const int rounds = (nr * 16 + NSOFT - 1) / NSOFT;
             const bool gated = whole && a.gate != nullptr;
@@ -620,9 +622,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         for (int c = 0; c < CH; ++c) {
                             x[c] *= a.scale_log2;
                             if (tail && t0 + row >= vis_s[c0 + c1 + c]) x[c] = -INFINITY;
-                            const float t = warp_max(x[c]);
-                            if (lane == 0) scr[quad * W + w0 + c] = t;
                         }
+                        float t[CH];
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) t[c] = x[c];
+                        join_lanes<CH>(t, lane, [](float p, float q) { return fmaxf(p, q); });
+                        if (CH == 32 || (lane & 1) == 0) scr[quad * W + w0 + (CH == 32 ? lane : lane >> 1)] = t[0];
                         softmax_sync<NSOFT>();
                         for (int i = st; i < W; i += NSOFT) {
                             const int c = i / CH * CPT + c1 + i % CH;
