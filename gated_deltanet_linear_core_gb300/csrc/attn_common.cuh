@@ -133,8 +133,30 @@ __device__ __forceinline__ int64_t row_index(const AttnArgs& a, int b, int h, in
 // unnormalised outputs.
 __device__ __forceinline__ float* slot_ptr(const AttnArgs& a, int slot) { return a.ws + (int64_t)slot * a.slot_floats; }
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNone = -3.0e38f;     // running maximum of a row that saw nothing yet
+constexpr float kSlack = 8.0f;        // how far (log2) scores may exceed the running maximum before it is moved
 constexpr float kLn2 = 0.6931471805599453f;
+
+// Joins C columns over the warp's lanes, halving the columns a lane holds at
+// each step: v[0 .. C / 32) of lane i becomes columns (C / 32) i .. (C = 16: lane
+// i has column i / 2).  A reduction per column costs several times as much.
+template <int C, typename F>
+__device__ __forceinline__ void join_lanes(float* v, int lane, F f) {
+#pragma unroll
+    for (int h = C / 2, o = 16; o >= 1; h /= 2, o /= 2) {
+        if (h >= 1) {
+#pragma unroll
+            for (int c = 0; c < C / 2; ++c)
+                if (c < h) {
+                    const float send = lane & o ? v[c] : v[c + h];
+                    const float keep = lane & o ? v[c + h] : v[c];
+                    v[c] = f(keep, __shfl_xor_sync(0xffffffffu, send, o));
+                }
+        } else {
+            v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+        }
+    }
+}
 
 }  // namespace attn
 }  // namespace gdn

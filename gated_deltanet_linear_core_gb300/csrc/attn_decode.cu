@@ -4,7 +4,7 @@
 namespace gdn {
 
 namespace {
-constexpr int kFfmaRows = 16, kTcRows = 128;  // rows of a block, at most
+constexpr int kTcRows = 128;  // rows of a block, at most
 
 int attn_ctas() {
     int dev = 0, n = 0;
@@ -15,7 +15,7 @@ int attn_ctas() {
 }  // namespace
 
 size_t attn_plan(AttnArgs& a, gdn_dtype_t dt) {
-    const int most = attn_tc_takes(a, dt) ? kTcRows : kFfmaRows;
+    const int most = attn_tc_takes(a, dt) ? kTcRows : attn_ffma_rows(a);
     a.group = a.H_q / a.H_kv;
     a.rows = a.K * a.group;
     a.n_rb = (a.rows + most - 1) / most;

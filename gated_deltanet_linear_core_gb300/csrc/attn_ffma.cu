@@ -8,10 +8,21 @@
 // plain softmax attention: with n = len - (K - 1 - i) for new token i,
 //   s_t = scale q . k_t,  out = sum_{t<n} e^{s_t} v_t / sum_{t<n} e^{s_t}
 //   [* sigmoid(gate)],    lse = log sum_{t<n} e^{s_t}
-// one pass over the tiles with the running maximum m, sum l and output O:
+// one pass over the tokens with the running maximum m, sum l and output O:
 //   m' = max(m, max s),  l <- l 2^(m-m') + sum 2^(s-m'),  O <- O 2^(m-m') + P V
-// (scores in the log2 domain, all statistics in f32).
+// (scores in the log2 domain, all statistics in f32; m is moved only when a
+// score exceeds it by 2^8, so O is rarely rescaled).
+//
+// Reading the cache is the bound up to about 8 rows per block, so every warp
+// works on its own, without shared memory or barriers between tokens: a lane
+// holds 4 (or 8) dims of the rows' Q and O, a warp takes T tokens at a time
+// straight into registers (K and V together, 8 KB in flight per warp), the T R
+// partial dot products are joined over the lanes by halving, which leaves each
+// lane a score, and the weights go back through a few words of shared memory.
+// The warps' results are joined at the end of a segment.
 #include "attn_common.cuh"
+
+#include "tc_ptx.cuh"
 
 namespace gdn {
 
@@ -19,43 +30,39 @@ namespace {
 
 using namespace attn;
 
-constexpr int NT = 256;   // threads
-constexpr int DQ = 8;     // lanes that share a token's dot product
+constexpr int TT = 64;  // tokens of a unit
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// four consecutive elements of shared memory as f32
-__device__ __forceinline__ float4 lds4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 lds4(const bf16* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
+// four consecutive elements as f32
+__device__ __forceinline__ float4 ld4(const float* p) { return __ldcs(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 ld4(const bf16* p) {
+    const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p));
     return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
                        __uint_as_float(u.y & 0xffff0000u));
 }
 
-template <typename T, int R, int TT>
-struct FfmaSmem {
-    int64_t rowoff[3][TT];  // element offset of the tile's rows in the caches, -1: no such token
-    float s[R][TT];         // scores, then weights
-    float m[R], l[R], f[R];
+// R rows per block (of which block_rows are real), NV x 4 dims per lane, T tokens at a time, NW warps.
+template <int R, int NV>
+struct Ffma {
+    static constexpr int T = NV == 1 && R <= 8 ? 8 : 4;
+    static constexpr int NW = R == 4 ? 16 : 8;
+    static constexpr int NT = NW * 32;
+    static constexpr int C = T * R;       // scores of T tokens
+    static constexpr int S = C / 32;      // scores per lane
+    static constexpr int PER = R / S;     // lanes per token
+    static_assert(C % 32 == 0 && PER * T == 32, "a lane holds whole scores");
 };
 
-// R rows (of which block_rows are real), tiles of TT tokens, NST stages of K and V rows.
-template <typename T, int R, int TT>
-__global__ void __launch_bounds__(NT, 1) attn_ffma_kernel(AttnArgs a) {
-    constexpr int NST = 3;
-    constexpr int TPT = TT * DQ / NT;  // tokens per thread in Q K^T
-    using Sm = FfmaSmem<T, R, TT>;
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
-    const int D = a.D;
-    float* q_s = reinterpret_cast<float*>(smem_raw + ((sizeof(Sm) + 15) & ~size_t(15)));  // [R][D]
-    T* stage = reinterpret_cast<T*>(q_s + R * D);                                          // [NST][K, V][TT][D]
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+template <typename E, int R, int NV>
+__global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs a) {
+    using G = Ffma<R, NV>;
+    constexpr int T = G::T, NW = G::NW, S = G::S, PER = G::PER;
+    extern __shared__ __align__(16) float sm[];
+    float* p_s = sm;                            // [NW][T][R] weights
+    float* m_s = p_s + NW * G::C;               // [NW][R]
+    float* l_s = m_s + NW * R;                  // [NW][R]
+    int* vis_s = reinterpret_cast<int*>(l_s + NW * R);  // [R] tokens a row sees
+    float* o_s = reinterpret_cast<float*>(vis_s + R);   // [NW][R][D]
+    const int D = a.D, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     pdl_wait();
     pdl_trigger();
@@ -63,217 +70,187 @@ __global__ void __launch_bounds__(NT, 1) attn_ffma_kernel(AttnArgs a) {
     const Place place = find_place(a, TT, blockIdx.x, n_cta);
     if ((int)blockIdx.x >= n_cta) return;
     Walk walk(place, cta_begin(place.total, blockIdx.x, n_cta), cta_begin(place.total, blockIdx.x + 1, n_cta));
-
-    const T* kc = static_cast<const T*>(a.k_cache);
-    const T* vc = static_cast<const T*>(a.v_cache);
-    const int ng = D / 4;             // groups of 4 output columns
-    const int nsplit = NT / ng;       // token splits of P V
-    const int grp = tid % ng, split = tid / ng;
-    const int chunks = D * (int)sizeof(T) / 16;  // 16-byte pieces of a row
+    const E* kc = static_cast<const E*>(a.k_cache);
+    const E* vc = static_cast<const E*>(a.v_cache);
+    const bool has[2] = {lane * 4 < D, NV > 1 && (lane + 32) * 4 < D};
+    float* p_w = p_s + warp * G::C;
+    const int my_t = lane / PER, my_r = lane % PER * S;  // token of the lane's scores, first row
 
     Segment s;
     while (walk.next(a, TT, s)) {
         const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
-        const int nt = s.tile1 - s.tile0;
-        // the query rows, scaled into the log2 domain
-        for (int e = tid; e < R * D; e += NT) {
-            const int r = e / D, d = e - r * D;
-            float x = 0.f;
-            if (r < nr) x = to_f(static_cast<const T*>(a.q)[row_index(a, s.b, s.h, r0 + r) * D + d]);
-            q_s[e] = x;
-        }
-        if (tid < R) {
-            sm.m[tid] = -INFINITY;
-            sm.l[tid] = 0.f;
-        }
-        const int32_t* table = a.table + (int64_t)s.b * a.max_pages;
-        auto place_rows = [&](int j) {  // where the rows of the segment's tile j are
-            if (tid >= TT) return;
-            const int t = (s.tile0 + j) * TT + tid;
-            int64_t off = -1;
-            if (j < nt && t < s.len) {
-                const int pg = t / a.page_size, page = table[pg];
-                if (page >= 0 && page < a.n_pages)
-                    off = (((int64_t)page * a.H_kv + s.h) * a.page_size + (t - pg * a.page_size)) * D;
-            }
-            sm.rowoff[j % 3][tid] = off;
-        };
-        auto load = [&](int j) {
-            if (j < nt) {
-                T* kd = stage + (int64_t)(j % NST) * 2 * TT * D;
-                for (int e = tid; e < TT * chunks; e += NT) {
-                    const int t = e / chunks, c = e - t * chunks;
-                    const int64_t off = sm.rowoff[j % 3][t];
-                    const int64_t src = (off < 0 ? 0 : off) + c * (16 / (int)sizeof(T));
-                    T* dst = kd + t * D + c * (16 / (int)sizeof(T));
-                    const int bytes = off < 0 ? 0 : 16;
-                    cp_async16((uint32_t)__cvta_generic_to_shared(dst), kc + src, bytes);
-                    cp_async16((uint32_t)__cvta_generic_to_shared(dst + TT * D), vc + src, bytes);
-                }
-            }
-            cp_async_commit();
-        };
-        place_rows(0);
-        place_rows(1);
-        place_rows(2);
-        __syncthreads();
-        load(0);
-        load(1);
-        float acc[R][4];
+        if (tid < R) vis_s[tid] = tid < nr ? visible(a, s.len, r0 + tid) : 0;
+        float4 q[R][NV], o[R][NV];
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
-
-        for (int j = 0; j < nt; ++j) {
-            cp_async_wait<1>();
-            __syncthreads();  // tile j landed; everyone is done with tile j - 1
-            load(j + 2);
-            const T* ks = stage + (int64_t)(j % NST) * 2 * TT * D;
-            const T* vs = ks + TT * D;
-            const int t0 = (s.tile0 + j) * TT;
-            // ---- scores: DQ lanes per token, each every 8th group of 4 dims
-            {
-                const int dq = tid % DQ, tk = tid / DQ;
-                float sc[TPT][R];
-#pragma unroll
-                for (int i = 0; i < TPT; ++i)
-#pragma unroll
-                    for (int r = 0; r < R; ++r) sc[i][r] = 0.f;
-                for (int d = dq * 4; d < D; d += DQ * 4) {
-                    float4 kv[TPT];
-#pragma unroll
-                    for (int i = 0; i < TPT; ++i) kv[i] = lds4(ks + (tk + i * (NT / DQ)) * D + d);
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const float4 qv = lds4(q_s + r * D + d);
-#pragma unroll
-                        for (int i = 0; i < TPT; ++i) {
-                            sc[i][r] = fmaf(kv[i].x, qv.x, sc[i][r]);
-                            sc[i][r] = fmaf(kv[i].y, qv.y, sc[i][r]);
-                            sc[i][r] = fmaf(kv[i].z, qv.z, sc[i][r]);
-                            sc[i][r] = fmaf(kv[i].w, qv.w, sc[i][r]);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < TPT; ++i)
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        float x = sc[i][r];
-#pragma unroll
-                        for (int o = DQ / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                        if (dq == r % DQ) sm.s[r][tk + i * (NT / DQ)] = x * a.scale_log2;
-                    }
-            }
-            __syncthreads();
-            // ---- running maximum and sum, one warp per row
-            for (int r = warp; r < R; r += NT / 32) {
-                const int vis = r < nr ? visible(a, s.len, r0 + r) - t0 : 0;
-                float x[TT / 32], top = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < TT / 32; ++i) {
-                    x[i] = lane + 32 * i < vis ? sm.s[r][lane + 32 * i] : -INFINITY;
-                    top = fmaxf(top, x[i]);
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const float m0 = sm.m[r], m1 = fmaxf(m0, top);
-                const float ref = m1 == -INFINITY ? 0.f : m1;
-                float sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < TT / 32; ++i) {
-                    const float p = exp2f(x[i] - ref);
-                    sm.s[r][lane + 32 * i] = p;
-                    sum += p;
-                }
-                sum = warp_sum(sum);
-                __syncwarp();
-                if (lane == 0) {
-                    const float f = exp2f(m0 - ref);
-                    sm.f[r] = f;
-                    sm.l[r] = sm.l[r] * f + sum;
-                    sm.m[r] = m1;
+            for (int v = 0; v < NV; ++v) {
+                o[r][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+                q[r][v] = o[r][v];
+                if (r < nr && has[v]) {
+                    const float4 x = ld4(static_cast<const E*>(a.q) + row_index(a, s.b, s.h, r0 + r) * D + (lane + 32 * v) * 4);
+                    q[r][v] = make_float4(x.x * a.scale_log2, x.y * a.scale_log2, x.z * a.scale_log2, x.w * a.scale_log2);
                 }
             }
-            place_rows(j + 3);
-            __syncthreads();
-            // ---- O = O f + P V: 4 columns per thread, groups of 4 tokens over the splits
-            if (split < nsplit) {
+        __syncthreads();
+        float m[S], l[S];
+        int vis[S];
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            m[i] = kNone;
+            l[i] = 0.f;
+            vis[i] = vis_s[my_r + i];
+        }
+        const int least = vis_s[0];
+        const int end = min(s.len, s.tile1 * TT);
+        const int32_t* table = a.table + (int64_t)s.b * a.max_pages;
+        auto place_of = [&](int t) -> int64_t {  // element offset of token t's row, -1: no such token
+            if (t >= end) return -1;
+            const int pg = t / a.page_size, page = table[pg];
+            if (page < 0 || page >= a.n_pages) return -1;
+            return (((int64_t)page * a.H_kv + s.h) * a.page_size + (t - pg * a.page_size)) * D;
+        };
+        int t0 = s.tile0 * TT + warp * T;
+        int64_t next = place_of(t0 + lane % T);  // lane i: token i of the T
+        for (; t0 < end; t0 += NW * T) {
+            const int64_t off = next;
+            float4 kv[T][NV], vv[T][NV];
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                const int64_t at = __shfl_sync(0xffffffffu, off, t);
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    kv[t][v] = vv[t][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (at >= 0 && has[v]) {
+                        kv[t][v] = ld4(kc + at + (lane + 32 * v) * 4);
+                        vv[t][v] = ld4(vc + at + (lane + 32 * v) * 4);
+                    }
+                }
+            }
+            next = place_of(t0 + NW * T + lane % T);
+            // ---- scores: partial dot products, joined over the lanes
+            float x[G::C];
+#pragma unroll
+            for (int t = 0; t < T; ++t)
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float f = sm.f[r];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[r][c] *= f;
+                    float2 d = __fmul2_rn(make_float2(kv[t][0].x, kv[t][0].y), make_float2(q[r][0].x, q[r][0].y));
+                    d = __ffma2_rn(make_float2(kv[t][0].z, kv[t][0].w), make_float2(q[r][0].z, q[r][0].w), d);
+                    if constexpr (NV > 1) {
+                        d = __ffma2_rn(make_float2(kv[t][NV - 1].x, kv[t][NV - 1].y),
+                                       make_float2(q[r][NV - 1].x, q[r][NV - 1].y), d);
+                        d = __ffma2_rn(make_float2(kv[t][NV - 1].z, kv[t][NV - 1].w),
+                                       make_float2(q[r][NV - 1].z, q[r][NV - 1].w), d);
+                    }
+                    x[t * R + r] = d.x + d.y;
                 }
-                // some rows see less than others at the end: a weight of zero must not meet their
-                // hidden values, which may be anything
-                const bool ragged = t0 + TT > visible(a, s.len, r0);
-                for (int tg = split * 4; tg < TT; tg += nsplit * 4) {
-                    float4 v[4];
+            join_lanes<G::C>(x, lane, [](float u, float w) { return u + w; });
+            const bool tail = t0 + T > least || t0 + T > end;
+            bool over = false;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = lds4(vs + (tg + i) * D + grp * 4);
-                    if (!ragged) {
+            for (int i = 0; i < S; ++i) {
+                if (tail && (t0 + my_t >= vis[i] || t0 + my_t >= end)) x[i] = -INFINITY;
+                over = over || x[i] - m[i] > kSlack;
+            }
+            if (__any_sync(0xffffffffu, over)) {  // new maxima; sums and outputs so far are scaled to them
+                float f[S];
 #pragma unroll
-                        for (int r = 0; r < R; ++r) {
-                            const float4 p = lds4(&sm.s[r][tg]);
-                            const float pp[4] = {p.x, p.y, p.z, p.w};
+                for (int i = 0; i < S; ++i) {
+                    float top = x[i];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                acc[r][0] = fmaf(pp[i], v[i].x, acc[r][0]);
-                                acc[r][1] = fmaf(pp[i], v[i].y, acc[r][1]);
-                                acc[r][2] = fmaf(pp[i], v[i].z, acc[r][2]);
-                                acc[r][3] = fmaf(pp[i], v[i].w, acc[r][3]);
-                            }
-                        }
-                    } else {
+                    for (int w = PER; w < 32; w *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                    if (!(top > m[i] + kSlack)) top = m[i];  // rows do not move with one another
+                    f[i] = tc::ex2_approx(m[i] - top);
+                    m[i] = top;
+                    l[i] *= f[i];
+                }
 #pragma unroll
-                        for (int r = 0; r < R; ++r) {
-                            const int vis = r < nr ? visible(a, s.len, r0 + r) - t0 - tg : 0;
-                            const float4 p = lds4(&sm.s[r][tg]);
-                            const float pp[4] = {p.x, p.y, p.z, p.w};
+                for (int r = 0; r < R; ++r) {
+                    const float g = __shfl_sync(0xffffffffu, f[r % S], r / S);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (i < vis) {
-                                    acc[r][0] = fmaf(pp[i], v[i].x, acc[r][0]);
-                                    acc[r][1] = fmaf(pp[i], v[i].y, acc[r][1]);
-                                    acc[r][2] = fmaf(pp[i], v[i].z, acc[r][2]);
-                                    acc[r][3] = fmaf(pp[i], v[i].w, acc[r][3]);
-                                }
-                        }
+                    for (int v = 0; v < NV; ++v) {
+                        o[r][v].x *= g; o[r][v].y *= g; o[r][v].z *= g; o[r][v].w *= g;
+                    }
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                const float p = tc::ex2_approx(x[i] - m[i]);
+                l[i] += p;
+                p_w[lane * S + i] = p;  // [token][row]
+            }
+            __syncwarp();
+            // ---- O += P V
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                float p[R];
+#pragma unroll
+                for (int r = 0; r < R; r += 4) {
+                    const float4 w = *reinterpret_cast<const float4*>(p_w + t * R + r);
+                    p[r] = w.x; p[r + 1] = w.y; p[r + 2] = w.z; p[r + 3] = w.w;
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    // a hidden value may be anything: a weight of 0 must not meet it
+                    if (tail && t0 + t >= vis_s[r]) continue;
+                    const float2 pp = make_float2(p[r], p[r]);
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                        float2* acc = reinterpret_cast<float2*>(&o[r][v]);
+                        acc[0] = __ffma2_rn(pp, make_float2(vv[t][v].x, vv[t][v].y), acc[0]);
+                        acc[1] = __ffma2_rn(pp, make_float2(vv[t][v].z, vv[t][v].w), acc[1]);
                     }
                 }
             }
         }
-        // ---- the splits' sums, then the rows (or this segment's part of them)
-        cp_async_wait<0>();
-        __syncthreads();
-        float* red = reinterpret_cast<float*>(stage);  // [nsplit][R][D]
-        if (split < nsplit)
+        // ---- the warps' parts, then the rows (or this segment's part of them)
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                *reinterpret_cast<float4*>(red + ((int64_t)split * R + r) * D + grp * 4) =
-                    make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+        for (int i = 0; i < S; ++i) {
+#pragma unroll
+            for (int w = PER; w < 32; w *= 2) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+            if (my_t == 0) {
+                m_s[warp * R + my_r + i] = m[i];
+                l_s[warp * R + my_r + i] = l[i];
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                if (has[v]) *reinterpret_cast<float4*>(o_s + (warp * R + r) * D + (lane + 32 * v) * 4) = o[r][v];
         __syncthreads();
-        const bool whole = nt == s.tiles;
+        const bool whole = s.tile1 - s.tile0 == s.tiles;
         float* slot = slot_ptr(a, 2 * blockIdx.x + (s.first ? 0 : 1));
-        for (int e = tid; e < nr * D; e += NT) {
-            const int r = e / D, d = e - r * D;
-            float o = 0.f;
-            for (int sp = 0; sp < nsplit; ++sp) o += red[((int64_t)sp * R + r) * D + d];
+        for (int e = tid; e < nr * (D / 4); e += G::NT) {
+            const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
+            float top = kNone, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) top = fmaxf(top, m_s[w * R + r]);
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int w = 0; w < NW; ++w) {
+                const float f = tc::ex2_approx(m_s[w * R + r] - top);
+                const float4 x = *reinterpret_cast<const float4*>(o_s + (w * R + r) * D + d);
+                sum = fmaf(f, l_s[w * R + r], sum);
+                y.x = fmaf(f, x.x, y.x); y.y = fmaf(f, x.y, y.y); y.z = fmaf(f, x.z, y.z); y.w = fmaf(f, x.w, y.w);
+            }
             if (whole) {
                 const int64_t row = row_index(a, s.b, s.h, r0 + r);
-                const float l = sm.l[r];
-                o = l > 0.f ? o / l : (l == 0.f ? 0.f : o);
-                if (a.gate != nullptr) o *= sigmoid_f(to_f(static_cast<const T*>(a.gate)[row * D + d]));
-                static_cast<T*>(a.out)[row * D + d] = from_f<T>(o);
-                if (d == 0 && a.lse != nullptr)
-                    a.lse[row] = l == 0.f ? -INFINITY : (sm.m[r] + log2f(l)) * kLn2;
+                const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+                float out[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
+                if (a.gate != nullptr) {
+                    const float4 g = ld4(static_cast<const E*>(a.gate) + row * D + d);
+                    out[0] *= sigmoid_f(g.x); out[1] *= sigmoid_f(g.y); out[2] *= sigmoid_f(g.z); out[3] *= sigmoid_f(g.w);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) static_cast<E*>(a.out)[row * D + d + i] = from_f<E>(out[i]);
+                if (d == 0 && a.lse != nullptr) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
             } else {
-                slot[a.stat_floats + r * D + d] = o;
+                *reinterpret_cast<float4*>(slot + a.stat_floats + r * D + d) = y;
                 if (d == 0) {
-                    slot[r] = sm.m[r];
-                    slot[a.rb_rows + r] = sm.l[r];
+                    slot[r] = top == kNone ? -INFINITY : top;
+                    slot[a.rb_rows + r] = sum;
                 }
             }
         }
@@ -380,22 +357,21 @@ __global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a, int n_cta, in
     }
 }
 
-template <typename T, int R, int TT>
+template <typename E, int R, int NV>
 cudaError_t launch_ffma(const AttnArgs& a, int n_cta, cudaStream_t s) {
-    // the stages' memory also holds the splits' sums at the end of a segment: at most NT * 4 columns
-    const size_t stages = (size_t)3 * 2 * TT * a.D * sizeof(T), sums = (size_t)NT * 4 * R * 4;
-    const size_t smem = ((sizeof(FfmaSmem<T, R, TT>) + 15) & ~size_t(15)) + (size_t)R * a.D * 4 +
-                        (stages > sums ? stages : sums);
-    cudaError_t e = cudaFuncSetAttribute(attn_ffma_kernel<T, R, TT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    using G = Ffma<R, NV>;
+    const size_t smem = sizeof(float) * (G::NW * (G::C + 2 * R + (size_t)R * a.D) + R);
+    const cudaError_t e = cudaFuncSetAttribute(attn_ffma_kernel<E, R, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_ffma_kernel<T, R, TT>, dim3((unsigned)n_cta), dim3(NT), smem, s, a);
+    return launch_pdl(attn_ffma_kernel<E, R, NV>, dim3((unsigned)n_cta), dim3(G::NT), smem, s, a);
 }
 
-template <typename T, int TT>
+template <typename E>
 cudaError_t launch_ffma_rows(const AttnArgs& a, int n_cta, cudaStream_t s) {
-    return a.rb_rows <= 4 ? launch_ffma<T, 4, TT>(a, n_cta, s)
-         : a.rb_rows <= 8 ? launch_ffma<T, 8, TT>(a, n_cta, s) : launch_ffma<T, 16, TT>(a, n_cta, s);
+    if (a.D > 128) return launch_ffma<E, 8, 2>(a, n_cta, s);
+    return a.rb_rows <= 4 ? launch_ffma<E, 4, 1>(a, n_cta, s)
+         : a.rb_rows <= 8 ? launch_ffma<E, 8, 1>(a, n_cta, s) : launch_ffma<E, 16, 1>(a, n_cta, s);
 }
 
 }  // namespace
@@ -407,15 +383,12 @@ cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, int tile, gdn_dtype_t
                           : launch_pdl(attn_join_kernel<float>, grid, dim3(JT), 0, s, a, n_cta, tile);
 }
 
+// Rows per block: Q and O of 8 dims per lane leave registers for 8.
+int attn_ffma_rows(const AttnArgs& a) { return a.D > 128 ? 8 : 16; }
+
 cudaError_t launch_attn_ffma(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaStream_t s) {
-    const bool small = a.D <= 128;
-    const int tile = small ? 64 : 32;
-    cudaError_t e;
-    if (dt == GDN_BF16)
-        e = small ? launch_ffma_rows<bf16, 64>(a, n_cta, s) : launch_ffma_rows<bf16, 32>(a, n_cta, s);
-    else
-        e = small ? launch_ffma_rows<float, 64>(a, n_cta, s) : launch_ffma_rows<float, 32>(a, n_cta, s);
-    return e != cudaSuccess ? e : launch_attn_join(a, n_cta, tile, dt, s);
+    const cudaError_t e = dt == GDN_BF16 ? launch_ffma_rows<bf16>(a, n_cta, s) : launch_ffma_rows<float>(a, n_cta, s);
+    return e != cudaSuccess ? e : launch_attn_join(a, n_cta, TT, dt, s);
 }
 
 }  // namespace gdn

@@ -46,8 +46,6 @@ constexpr int TILE = 128;
 constexpr int SLAB = TILE * 128;      // bytes of 128 tokens x 64 dims
 constexpr int SLOT = 2 * SLAB;        // ... x 128 dims
 constexpr uint64_t kWaitNs = 1000000000ull;
-constexpr float kNone = -3.0e38f;     // running maximum of a row that saw nothing yet
-constexpr float kSlack = 8.0f;        // how far (log2) scores may exceed the running maximum
 constexpr int kSmemMax = 232448;
 
 template <int N, int NDB>
@@ -159,26 +157,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const float* v) {
     if constexpr (N == 16) tmem_st16(taddr, v); else tmem_st32(taddr, v);
-}
-// Joins C columns over the warp's lanes, halving the columns a lane holds at
-// each step: v[0 .. C / 32) of lane i becomes columns (C / 32) i .. (C = 16: lane
-// i has column i / 2).  A reduction per column costs several times as much.
-template <int C, typename F>
-__device__ __forceinline__ void join_lanes(float* v, int lane, F f) {
-#pragma unroll
-    for (int h = C / 2, o = 16; o >= 1; h /= 2, o /= 2) {
-        if (h >= 1) {
-#pragma unroll
-            for (int c = 0; c < C / 2; ++c)
-                if (c < h) {
-                    const float send = lane & o ? v[c] : v[c + h];
-                    const float keep = lane & o ? v[c + h] : v[c];
-                    v[c] = f(keep, __shfl_xor_sync(0xffffffffu, send, o));
-                }
-        } else {
-            v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
-        }
-    }
 }
 __device__ __forceinline__ bool finite_bf16x8(uint4 u) {
     bool ok = true;
@@ -632,7 +610,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         for (int i = st; i < W; i += NSOFT) {
                             const int c = i / CH * CPT + c1 + i % CH;
                             const float m0 = m_s[c];
-                            const float m1 = fmaxf(fmaxf(fmaxf(scr[i], scr[W + i]), fmaxf(scr[2 * W + i], scr[3 * W + i])), m0);
+                            const float t1 = fmaxf(fmaxf(scr[i], scr[W + i]), fmaxf(scr[2 * W + i], scr[3 * W + i]));
+                            const float m1 = t1 > m0 + kSlack ? t1 : m0;  // rows do not move with one another
                             m_s[c] = m1;
                             f_s[c] = ex2_approx(m0 - m1);
                         }
