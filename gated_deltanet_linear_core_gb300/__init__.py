@@ -536,9 +536,12 @@ def _dptr(t, name, dev, dtype, shape=None):
     tensors are looked at in about 0.3 us each, and a decode step has a dozen)."""
     if t is None:
         return None
-    if (isinstance(t, torch.Tensor) and t.get_device() == dev and (dtype is None or t.dtype is dtype)
-            and t.is_contiguous() and (shape is None or t.shape == shape)):
-        return t.data_ptr() or None
+    try:
+        if (t.get_device() == dev and (t.dtype is dtype or dtype is None) and t.is_contiguous()
+                and (shape is None or t.shape == shape)):
+            return t.data_ptr()  # 0, that is NULL, without elements
+    except AttributeError:
+        pass
     if isinstance(t, torch.Tensor) and t.get_device() != dev:
         raise ValueError(f"{name}: tensors on different devices (cuda:{dev} and {t.device})")
     return _ptr(t, name, dtype, shape)

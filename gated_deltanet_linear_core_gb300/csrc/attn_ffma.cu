@@ -79,6 +79,16 @@ __global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs 
     Segment s;
     while (walk.next(a, TT, s)) {
         const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
+        const int end = min(s.len, s.tile1 * TT);
+        const int32_t* table = a.table + (int64_t)s.b * a.max_pages;
+        auto place_of = [&](int t) -> int64_t {  // element offset of token t's row, -1: no such token
+            if (t >= end) return -1;
+            const int pg = t / a.page_size, page = table[pg];
+            if (page < 0 || page >= a.n_pages) return -1;
+            return (((int64_t)page * a.H_kv + s.h) * a.page_size + (t - pg * a.page_size)) * D;
+        };
+        int t0 = s.tile0 * TT + warp * T;
+        int64_t next = place_of(t0 + lane % T);  // lane i: token i of the T
         if (tid < R) vis_s[tid] = tid < nr ? visible(a, s.len, r0 + tid) : 0;
         float4 q[R][NV], o[R][NV];
 #pragma unroll
@@ -87,10 +97,8 @@ __global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs 
             for (int v = 0; v < NV; ++v) {
                 o[r][v] = make_float4(0.f, 0.f, 0.f, 0.f);
                 q[r][v] = o[r][v];
-                if (r < nr && has[v]) {
-                    const float4 x = ld4(static_cast<const E*>(a.q) + row_index(a, s.b, s.h, r0 + r) * D + (lane + 32 * v) * 4);
-                    q[r][v] = make_float4(x.x * a.scale_log2, x.y * a.scale_log2, x.z * a.scale_log2, x.w * a.scale_log2);
-                }
+                if (r < nr && has[v])
+                    q[r][v] = ld4(static_cast<const E*>(a.q) + row_index(a, s.b, s.h, r0 + r) * D + (lane + 32 * v) * 4);
             }
         __syncthreads();
         float m[S], l[S];
@@ -102,16 +110,6 @@ __global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs 
             vis[i] = vis_s[my_r + i];
         }
         const int least = vis_s[0];
-        const int end = min(s.len, s.tile1 * TT);
-        const int32_t* table = a.table + (int64_t)s.b * a.max_pages;
-        auto place_of = [&](int t) -> int64_t {  // element offset of token t's row, -1: no such token
-            if (t >= end) return -1;
-            const int pg = t / a.page_size, page = table[pg];
-            if (page < 0 || page >= a.n_pages) return -1;
-            return (((int64_t)page * a.H_kv + s.h) * a.page_size + (t - pg * a.page_size)) * D;
-        };
-        int t0 = s.tile0 * TT + warp * T;
-        int64_t next = place_of(t0 + lane % T);  // lane i: token i of the T
         for (; t0 < end; t0 += NW * T) {
             const int64_t off = next;
             float4 kv[T][NV], vv[T][NV];
@@ -149,6 +147,7 @@ __global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs 
             bool over = false;
 #pragma unroll
             for (int i = 0; i < S; ++i) {
+                x[i] *= a.scale_log2;
                 if (tail && (t0 + my_t >= vis[i] || t0 + my_t >= end)) x[i] = -INFINITY;
                 over = over || x[i] - m[i] > kSlack;
             }
