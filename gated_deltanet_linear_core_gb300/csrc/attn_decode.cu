@@ -15,7 +15,7 @@ int attn_ctas() {
 }  // namespace
 
 size_t attn_plan(AttnArgs& a, gdn_dtype_t dt) {
-    const int most = attn_tc_takes(a, dt) ? kTcRows : attn_ffma_rows(a);
+    const int most = attn_tc_takes(a, dt) ? kTcRows : kAttnFfmaRows;
     a.group = a.H_q / a.H_kv;
     a.rows = a.K * a.group;
     a.n_rb = (a.rows + most - 1) / most;

@@ -13,12 +13,15 @@
 // (scores in the log2 domain, all statistics in f32; m is moved only when a
 // score exceeds it by 2^8, so O is rarely rescaled).
 //
-// Reading the cache is the bound up to about 8 rows per block, so every warp
+// Reading the cache is the bound of few rows (4 rows of head dim 128: 5.7 TB/s
+// once it runs), so every warp
 // works on its own, without shared memory or barriers between tokens: a lane
 // holds 4 (or 8) dims of the rows' Q and O, a warp takes T tokens at a time
 // straight into registers (K and V together, 8 KB in flight per warp), the T R
 // partial dot products are joined over the lanes by halving, which leaves each
 // lane a score, and the weights go back through a few words of shared memory.
+// Blocks have at most kAttnFfmaRows rows: 16 in one pass (registers for 8 warps
+// only) took longer than two passes of 8, of which the second reads from L2.
 // The warps' results are joined at the end of a segment.
 #include "attn_common.cuh"
 
@@ -43,8 +46,9 @@ __device__ __forceinline__ float4 ld4(const bf16* p) {
 // R rows per block (of which block_rows are real), NV x 4 dims per lane, T tokens at a time, NW warps.
 template <int R, int NV>
 struct Ffma {
-    static constexpr int T = NV == 1 && R <= 8 ? 8 : 4;
-    static constexpr int NW = R == 4 ? 16 : 8;
+    static constexpr int T = R == 4 ? 8 : 4;
+    // more warps beat more registers (8 rows, head dim 128: 50 us with 16 warps and a few spills, 70 with 8)
+    static constexpr int NW = NV == 1 ? 16 : 8;
     static constexpr int NT = NW * 32;
     static constexpr int C = T * R;       // scores of T tokens
     static constexpr int S = C / 32;      // scores per lane
@@ -368,9 +372,8 @@ cudaError_t launch_ffma(const AttnArgs& a, int n_cta, cudaStream_t s) {
 
 template <typename E>
 cudaError_t launch_ffma_rows(const AttnArgs& a, int n_cta, cudaStream_t s) {
-    if (a.D > 128) return launch_ffma<E, 8, 2>(a, n_cta, s);
-    return a.rb_rows <= 4 ? launch_ffma<E, 4, 1>(a, n_cta, s)
-         : a.rb_rows <= 8 ? launch_ffma<E, 8, 1>(a, n_cta, s) : launch_ffma<E, 16, 1>(a, n_cta, s);
+    if (a.D > 128) return a.rb_rows <= 4 ? launch_ffma<E, 4, 2>(a, n_cta, s) : launch_ffma<E, 8, 2>(a, n_cta, s);
+    return a.rb_rows <= 4 ? launch_ffma<E, 4, 1>(a, n_cta, s) : launch_ffma<E, 8, 1>(a, n_cta, s);
 }
 
 }  // namespace
@@ -381,9 +384,6 @@ cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, int tile, gdn_dtype_t
     return dt == GDN_BF16 ? launch_pdl(attn_join_kernel<bf16>, grid, dim3(JT), 0, s, a, n_cta, tile)
                           : launch_pdl(attn_join_kernel<float>, grid, dim3(JT), 0, s, a, n_cta, tile);
 }
-
-// Rows per block: Q and O of 8 dims per lane leave registers for 8.
-int attn_ffma_rows(const AttnArgs& a) { return a.D > 128 ? 8 : 16; }
 
 cudaError_t launch_attn_ffma(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaStream_t s) {
     const cudaError_t e = dt == GDN_BF16 ? launch_ffma_rows<bf16>(a, n_cta, s) : launch_ffma_rows<float>(a, n_cta, s);

@@ -176,7 +176,7 @@ constexpr int kAttnMaxCtas = 152;  // CTAs of a call, at most: one per SM
 // Fills the derived fields from the sizes; returns the workspace bytes.
 size_t attn_plan(AttnArgs& a, gdn_dtype_t dt);
 cudaError_t launch_attn_decode(const AttnArgs& a, gdn_dtype_t dt, cudaStream_t s);
-int attn_ffma_rows(const AttnArgs& a);  // rows per block, at most
+constexpr int kAttnFfmaRows = 8;  // rows per block of launch_attn_ffma, at most
 cudaError_t launch_attn_ffma(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaStream_t s);
 // The tensor-core kernel: which calls it takes, and its launch with the join.
 bool attn_tc_takes(const AttnArgs& a, gdn_dtype_t dt);
