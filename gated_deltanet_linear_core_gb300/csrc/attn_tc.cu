@@ -78,7 +78,7 @@ struct Layout {
     static constexpr int O_SCR = O_F + N * 4;
     static constexpr int SMEM = O_BAR + SMALL;
     static constexpr int T_S = 0, T_O = 2 * N;
-    static constexpr int PARTS = N <= 64 ? 2 : 1;  // O of P's upper and lower halves side by side, or their sum
+    static constexpr int PARTS = N <= 64 || NDB == 1 ? 2 : 1;  // O of P's upper and lower parts side by side, or their sum
     static constexpr int T_USED = (2 + NDB * PARTS) * N;
     static constexpr int T_COLS = T_USED <= 64 ? 64 : T_USED <= 128 ? 128 : T_USED <= 256 ? 256 : 512;
     static_assert(N * 512 <= P_BYTES, "output rows");
@@ -633,26 +633,25 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             tmem_wait_st();
                         }
                     }
+                    uint32_t hi[CH / 2], lo[CH / 2];
+#pragma unroll
+                    for (int i = 0; i < CH / 2; ++i) {
+                        const float p0 = ex2_approx(x[2 * i]), p1 = ex2_approx(x[2 * i + 1]);
+                        l[c1 + 2 * i] += p0;
+                        l[c1 + 2 * i + 1] += p1;
+                        const uint32_t w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
+                        hi[i] = __byte_perm(w0, w1, 0x7632);  // the upper halves: cut, not rounded
+                        // the rest, at least p's last bit: a rest of 0 would turn an infinite value into NaN
+                        lo[i] = pack_bf16x2(__uint_as_float(w0 | 1u) - __uint_as_float(w0 & 0xffff0000u),
+                                            __uint_as_float(w1 | 1u) - __uint_as_float(w1 & 0xffff0000u));
+                    }
                     if (c1 == 0 && it >= L::PBUF) wait(&pv_done[(it - L::PBUF) & 1], (it - L::PBUF) >> 1);
 #pragma unroll
                     for (int c = 0; c < CH; c += 8) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float p0 = ex2_approx(x[c + 2 * i]);
-                            const float p1 = ex2_approx(x[c + 2 * i + 1]);
-                            l[c1 + c + 2 * i] += p0;
-                            l[c1 + c + 2 * i + 1] += p1;
-                            const uint32_t w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
-                            hi[i] = __byte_perm(w0, w1, 0x7632);  // the upper halves: cut, not rounded
-                            // the rest, at least p's last bit: a rest of 0 would turn an infinite value into NaN
-                            lo[i] = pack_bf16x2(__uint_as_float(w0 | 1u) - __uint_as_float(w0 & 0xffff0000u),
-                                                __uint_as_float(w1 | 1u) - __uint_as_float(w1 & 0xffff0000u));
-                        }
                         *reinterpret_cast<uint4*>(sm + L::O_P + L::p_off(buf, 0, (c0 + c1 + c) >> 3, row)) =
-                            make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            make_uint4(hi[c / 2], hi[c / 2 + 1], hi[c / 2 + 2], hi[c / 2 + 3]);
                         *reinterpret_cast<uint4*>(sm + L::O_P + L::p_off(buf, 1, (c0 + c1 + c) >> 3, row)) =
-                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            make_uint4(lo[c / 2], lo[c / 2 + 1], lo[c / 2 + 2], lo[c / 2 + 3]);
                     }
                 }
                 if (tail) {
