@@ -11,7 +11,8 @@
 // covers an item whole writes its rows; otherwise it leaves the running
 // maximum, sum and unnormalised output in one of its two workspace slots
 // (its range starts inside an item: slot 2c; ends inside another: 2c + 1),
-// and attn_join_kernel combines the slots in CTA order.
+// and attn_join_kernel combines the slots in CTA order, told by the CTAs what to
+// join (JoinTask).
 #pragma once
 
 #include <math.h>
@@ -129,9 +130,42 @@ __device__ __forceinline__ int64_t row_index(const AttnArgs& a, int b, int h, in
     return ((int64_t)b * a.K + i) * a.H_q + h * a.group + (r - i * a.group);
 }
 
+// What to join where CTA c's range starts inside an item: the item, and the CTAs
+// that worked on it.  Written by CTA c (one thread), so that the join needs
+// neither the lengths nor any of the divisions here.
+struct alignas(16) JoinTask {
+    int n;           // CTAs that worked on the item (0: the range starts with an item of its own)
+    int c0;          // the first of them
+    int first_slot;  // where its part is; CTA c0 + i's is in slot 2 (c0 + i)
+    int b, h, rb;    // the item
+    int pad[2];
+};
+__device__ __forceinline__ JoinTask* join_task(const AttnArgs& a, int c) { return reinterpret_cast<JoinTask*>(a.ws) + c; }
+__device__ __forceinline__ void write_join_task(const AttnArgs& a, const Place& p, int c, int n, int tile) {
+    JoinTask t;
+    t.n = 0;
+    if (c < n) {
+        Walk walk(p, cta_begin(p.total, c, n), cta_begin(p.total, c + 1, n));
+        const int64_t u = walk.at;
+        Segment s;
+        if (walk.next(a, tile, s) && s.tile0 > 0) {
+            const int64_t u0 = u - s.tile0;
+            t.c0 = cta_of(p.total, u0, n);
+            t.n = cta_of(p.total, u0 + s.tiles - 1, n) - t.c0 + 1;
+            t.first_slot = cta_begin(p.total, t.c0, n) == u0 ? 2 * t.c0 : 2 * t.c0 + 1;
+            t.b = s.b;
+            t.h = s.h;
+            t.rb = s.rb;
+        }
+    }
+    *join_task(a, c) = t;
+}
+
 // A workspace slot: maxima (log2 domain) and sums of its rows, then their
 // unnormalised outputs.
-__device__ __forceinline__ float* slot_ptr(const AttnArgs& a, int slot) { return a.ws + (int64_t)slot * a.slot_floats; }
+__device__ __forceinline__ float* slot_ptr(const AttnArgs& a, int slot) {
+    return a.ws + kAttnMaxCtas * (sizeof(JoinTask) / 4) + (int64_t)slot * a.slot_floats;
+}
 
 constexpr float kNone = -3.0e38f;     // running maximum of a row that saw nothing yet
 constexpr float kSlack = 8.0f;        // how far (log2) scores may exceed the running maximum before it is moved

@@ -23,7 +23,7 @@ size_t attn_plan(AttnArgs& a, gdn_dtype_t dt) {
     a.min_units = 1;
     a.stat_floats = (2 * a.rb_rows + 3) & ~3;
     a.slot_floats = a.stat_floats + (int64_t)a.rb_rows * a.D;
-    return (size_t)2 * kAttnMaxCtas * a.slot_floats * sizeof(float);
+    return kAttnMaxCtas * (sizeof(attn::JoinTask) + 2 * (size_t)a.slot_floats * sizeof(float));
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& a, gdn_dtype_t dt, cudaStream_t s) {

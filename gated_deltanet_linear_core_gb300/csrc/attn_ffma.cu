@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs 
     pdl_trigger();
     int n_cta = gridDim.x;
     const Place place = find_place(a, TT, blockIdx.x, n_cta);
+    if (tid == G::NT - 32) write_join_task(a, place, blockIdx.x, n_cta, TT);
     if ((int)blockIdx.x >= n_cta) return;
     Walk walk(place, cta_begin(place.total, blockIdx.x, n_cta), cta_begin(place.total, blockIdx.x + 1, n_cta));
     const E* kc = static_cast<const E*>(a.k_cache);
@@ -267,8 +268,7 @@ __global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs 
 // runs through the parts in CTA order (more than kSerial of them are
 // shared out to several groups), keeping the running maximum, sum
 // and output as the tiles do; the order is fixed, so results do not depend on
-// timing.  Where the item lies is worked out before the wait for the kernel
-// that wrote the parts: the lengths are older than that kernel.
+// timing.
 constexpr int JT = 256;
 constexpr int kSerial = 8;
 struct Running {
@@ -284,31 +284,29 @@ struct Running {
     }
 };
 template <typename T>
-__global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a, int n_cta, int tile) {
+__global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a) {
     __shared__ float4 o_s[JT];
     __shared__ float2 ml_s[JT];
     const int tid = threadIdx.x, c = blockIdx.x + 1;
-    const Place p = find_place(a, tile, c, n_cta);
-    if (c >= n_cta) return;
-    Walk walk(p, cta_begin(p.total, c, n_cta), cta_begin(p.total, c + 1, n_cta));
-    Segment s;
-    const int64_t u = walk.at;
-    if (!walk.next(a, tile, s) || s.tile0 == 0) return;  // the range starts with an item of its own
-    const int64_t u0 = u - s.tile0, u1 = u0 + s.tiles;
-    const int c0 = cta_of(p.total, u0, n_cta), c1 = cta_of(p.total, u1 - 1, n_cta);
-    const int first_slot = cta_begin(p.total, c0, n_cta) == u0 ? 2 * c0 : 2 * c0 + 1;
-    const int n = c1 - c0 + 1;
+    pdl_wait();
+    pdl_trigger();
+    const JoinTask task = *join_task(a, c);
+    // (the bounds hold for every task of this call's; they keep calls that share a workspace against the rules
+    // from writing out of bounds)
+    if (task.n < 2 || (unsigned)task.b >= (unsigned)a.B || (unsigned)task.h >= (unsigned)a.H_kv ||
+        (unsigned)task.rb >= (unsigned)a.n_rb || (unsigned)task.c0 >= kAttnMaxCtas || task.c0 + task.n > kAttnMaxCtas ||
+        (unsigned)(task.first_slot - 2 * task.c0) > 1u)
+        return;
+    const int n = task.n, c0 = task.c0, first_slot = task.first_slot;
     // many parts: groups share a row's parts, about 4 each; where a block has too few groups for that, a worker
     // takes a quarter of a row
     const int need = n > kSerial ? (n + 3) / 4 : 1;
     const int split = JT / (a.D / 4) < need && a.D % 16 == 0 ? 4 : 1;
     const int ng = a.D / 4 / split, groups = JT / ng, grp = tid % ng, g = tid / ng;
-    const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
+    const int r0 = task.rb * a.rb_rows, nr = block_rows(a, task.rb);
     const int workers = (n - 1) * gridDim.y, worker = (c - c0 - 1) * gridDim.y + blockIdx.y;
     const int share = need < groups ? need : groups;  // groups on one row
     const int at_once = groups / share, sub = g % share;
-    pdl_wait();
-    pdl_trigger();
     for (int first = worker * at_once; first < nr * split; first += workers * at_once) {
         const int rq = first + g / share, r = rq / split, d = ((rq - r * split) * ng + grp) * 4;
         const bool mine = g < at_once * share && rq < nr * split;  // whole shares only
@@ -342,7 +340,7 @@ __global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a, int n_cta, in
             __syncthreads();
         }
         if (mine && sub == 0) {
-            const int64_t row = row_index(a, s.b, s.h, r0 + r);
+            const int64_t row = row_index(a, task.b, task.h, r0 + r);
             const int64_t at = row * a.D + d;
             const float inv = run.l == 0.f ? 0.f : 1.0f / run.l;
             float y[4] = {run.o.x * inv, run.o.y * inv, run.o.z * inv, run.o.w * inv};
@@ -378,16 +376,16 @@ cudaError_t launch_ffma_rows(const AttnArgs& a, int n_cta, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, int tile, gdn_dtype_t dt, cudaStream_t s) {
+cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaStream_t s) {
     if (n_cta <= 1) return cudaSuccess;
     const dim3 grid((unsigned)(n_cta - 1), (unsigned)((a.rb_rows + 15) / 16));
-    return dt == GDN_BF16 ? launch_pdl(attn_join_kernel<bf16>, grid, dim3(JT), 0, s, a, n_cta, tile)
-                          : launch_pdl(attn_join_kernel<float>, grid, dim3(JT), 0, s, a, n_cta, tile);
+    return dt == GDN_BF16 ? launch_pdl(attn_join_kernel<bf16>, grid, dim3(JT), 0, s, a)
+                          : launch_pdl(attn_join_kernel<float>, grid, dim3(JT), 0, s, a);
 }
 
 cudaError_t launch_attn_ffma(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaStream_t s) {
     const cudaError_t e = dt == GDN_BF16 ? launch_ffma_rows<bf16>(a, n_cta, s) : launch_ffma_rows<float>(a, n_cta, s);
-    return e != cudaSuccess ? e : launch_attn_join(a, n_cta, TT, dt, s);
+    return e != cudaSuccess ? e : launch_attn_join(a, n_cta, dt, s);
 }
 
 }  // namespace gdn

@@ -398,6 +398,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             if (lane == 0) mbar_arrive(q_full);
             ++seg;
         }
+        if (lane == 0) write_join_task(a, place, blockIdx.x, n_cta, TILE);
     } else {
         // ------------------------------------------------ softmax and outputs
         constexpr int CH = L::CH;
@@ -743,7 +744,7 @@ bool attn_tc_takes(const AttnArgs& a, gdn_dtype_t dt) {
 cudaError_t launch_attn_tc(const AttnArgs& a, int n_cta, cudaStream_t s) {
     const int piece = page_piece(a.page_size);
     const cudaError_t e = a.D <= 128 ? launch_rows<1>(a, n_cta, piece, s) : launch_rows<2>(a, n_cta, piece, s);
-    return e != cudaSuccess ? e : launch_attn_join(a, n_cta, TILE, GDN_BF16, s);
+    return e != cudaSuccess ? e : launch_attn_join(a, n_cta, GDN_BF16, s);
 }
 
 cudaError_t read_and_clear_attn_error(cudaStream_t s, int* flags) {

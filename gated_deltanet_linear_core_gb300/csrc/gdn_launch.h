@@ -161,7 +161,7 @@ struct AttnArgs {
     const void* gate;      // [B, K, H_q, D] or null
     void* out;             // [B, K, H_q, D]
     float* lse;            // [B, K, H_q] or null
-    float* ws;             // slots of partial results
+    float* ws;             // what to join per CTA, then slots of partial results
     int64_t slot_floats;   // floats per slot
     int stat_floats;       // of which maxima and sums come first
     int B, K, H_q, H_kv, D;
@@ -182,7 +182,7 @@ cudaError_t launch_attn_ffma(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaS
 bool attn_tc_takes(const AttnArgs& a, gdn_dtype_t dt);
 cudaError_t launch_attn_tc(const AttnArgs& a, int n_cta, cudaStream_t s);
 cudaError_t read_and_clear_attn_error(cudaStream_t s, int* flags);
-cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, int tile, gdn_dtype_t dt, cudaStream_t s);
+cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaStream_t s);
 
 // New keys and values into their pages (gdn_kv_append).
 struct KvAppendArgs {
