@@ -4,15 +4,16 @@
 // An item is (sequence b, key-value head h, row block rb): a block of the
 // sequence's K*G query rows that share h (G = H_q / H_kv; row r is new token
 // r / G, query head h*G + r % G).  An item's units are its tiles of `tile`
-// cached tokens, at least one (an empty sequence still has rows to write).
-// All units of a call, item after item, are cut into equal contiguous ranges,
-// one per CTA, whatever the lengths are: the lengths stay on the device, so
-// the host never waits for them and a captured graph follows them.  A CTA that
-// covers an item whole writes its rows; otherwise it leaves the running
-// maximum, sum and unnormalised output in one of its two workspace slots
-// (its range starts inside an item: slot 2c; ends inside another: 2c + 1),
-// and attn_join_kernel combines the slots in CTA order, told by the CTAs what to
-// join (JoinTask).
+// cached tokens, at least one (an empty sequence still has rows to write),
+// after `setup` units that stand for what starting an item costs: a CTA that
+// gets several short sequences gets fewer tiles.  All units of a call, item
+// after item, are cut into equal contiguous ranges, one per CTA, whatever the
+// lengths are: the lengths stay on the device, so the host never waits for them
+// and a captured graph follows them.  A CTA that covers an item's tiles whole
+// writes its rows; otherwise it leaves the running maximum, sum and unnormalised
+// output in one of its two workspace slots (its part starts inside the item's
+// tiles: slot 2c; at their start: 2c + 1), and attn_join_kernel combines the
+// slots in CTA order, told by the CTAs what to join (JoinTask).
 #pragma once
 
 #include <math.h>
@@ -28,7 +29,8 @@ __device__ __forceinline__ int clamped_len(const AttnArgs& a, int b) {
     const int n = a.lens[b];
     return n < 0 ? 0 : (n > cap ? (int)cap : n);
 }
-__device__ __forceinline__ int units_of(int len, int tile) { return len <= tile ? 1 : (len - 1) / tile + 1; }
+__device__ __forceinline__ int tiles_of(int len, int tile) { return len <= tile ? 1 : (len - 1) / tile + 1; }
+__device__ __forceinline__ int units_of(const AttnArgs& a, int len, int tile) { return a.setup + tiles_of(len, tile); }
 
 // First unit of CTA c of n.
 __host__ __device__ __forceinline__ int64_t cta_begin(int64_t total, int c, int n) { return total * c / n; }
@@ -49,8 +51,8 @@ __device__ __forceinline__ Place find_place(const AttnArgs& a, int tile, int c, 
     const int lane = threadIdx.x & 31;
     const int64_t mult = (int64_t)a.H_kv * a.n_rb;
     const int len0 = lane < a.B ? clamped_len(a, lane) : 0;  // kept: all of a small batch
-    int64_t all = lane < a.B ? units_of(len0, tile) : 0;
-    for (int b = lane + 32; b < a.B; b += 32) all += units_of(clamped_len(a, b), tile);
+    int64_t all = lane < a.B ? units_of(a, len0, tile) : 0;
+    for (int b = lane + 32; b < a.B; b += 32) all += units_of(a, clamped_len(a, b), tile);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     Place p;
@@ -64,7 +66,7 @@ __device__ __forceinline__ Place find_place(const AttnArgs& a, int tile, int c, 
     for (int b0 = 0; b0 < a.B; b0 += 32) {
         const int b = b0 + lane;
         const int len = b0 == 0 ? len0 : (b < a.B ? clamped_len(a, b) : 0);
-        int inc = b < a.B ? units_of(len, tile) : 0;  // inclusive scan: 32 sequences' units fit 31 bits
+        int inc = b < a.B ? units_of(a, len, tile) : 0;  // inclusive scan: 32 sequences' units fit 31 bits
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -89,34 +91,37 @@ struct Segment {
     int b, h, rb, len;   // item
     int tile0, tile1;    // its tiles [tile0, tile1) of this segment
     int tiles;           // tiles of the whole item
-    bool first;          // starts where the CTA's range starts
 };
 struct Walk {
-    int64_t at, end, begin, item0;  // units; item0: first unit of sequence b's items
+    int64_t at, end, item0;  // units; item0: first unit of sequence b's items
     int b, len;
     __device__ __forceinline__ Walk(const Place& p, int64_t lo, int64_t hi)
-        : at(lo), end(hi), begin(lo), item0(p.first), b(p.b), len(p.len) {}
+        : at(lo), end(hi), item0(p.first), b(p.b), len(p.len) {}
     __device__ __forceinline__ bool next(const AttnArgs& a, int tile, Segment& s) {
-        if (at >= end) return false;
-        int units = units_of(len, tile);
-        while (at >= item0 + (int64_t)units * a.H_kv * a.n_rb) {
-            item0 += (int64_t)units * a.H_kv * a.n_rb;
-            len = clamped_len(a, ++b);
-            units = units_of(len, tile);
+        while (at < end) {
+            int units = units_of(a, len, tile);
+            while (at >= item0 + (int64_t)units * a.H_kv * a.n_rb) {
+                item0 += (int64_t)units * a.H_kv * a.n_rb;
+                len = clamped_len(a, ++b);
+                units = units_of(a, len, tile);
+            }
+            const int64_t off = at - item0;
+            const int item = (int)(off / units);
+            const int from = (int)(off - (int64_t)item * units);
+            const int64_t left = end - at;
+            const int upto = left < units - from ? from + (int)left : units;
+            at += upto - from;
+            if (upto <= a.setup) continue;  // the range ends before the item's tiles
+            s.tile0 = from > a.setup ? from - a.setup : 0;
+            s.tile1 = upto - a.setup;
+            s.tiles = units - a.setup;
+            s.h = item / a.n_rb;
+            s.rb = item - s.h * a.n_rb;
+            s.b = b;
+            s.len = len;
+            return true;
         }
-        const int64_t off = at - item0;
-        const int item = (int)(off / units);
-        s.tile0 = (int)(off - (int64_t)item * units);
-        const int64_t left = end - at;
-        s.tile1 = left < units - s.tile0 ? s.tile0 + (int)left : units;
-        s.tiles = units;
-        s.h = item / a.n_rb;
-        s.rb = item - s.h * a.n_rb;
-        s.b = b;
-        s.len = len;
-        s.first = at == begin;
-        at += s.tile1 - s.tile0;
-        return true;
+        return false;
     }
 };
 
@@ -134,11 +139,10 @@ __device__ __forceinline__ int64_t row_index(const AttnArgs& a, int b, int h, in
 // that worked on it.  Written by CTA c (one thread), so that the join needs
 // neither the lengths nor any of the divisions here.
 struct alignas(16) JoinTask {
-    int n;           // CTAs that worked on the item (0: the range starts with an item of its own)
-    int c0;          // the first of them
-    int first_slot;  // where its part is; CTA c0 + i's is in slot 2 (c0 + i)
-    int b, h, rb;    // the item
-    int pad[2];
+    int n;         // CTAs that worked on the item (0: the range starts with an item of its own)
+    int c0;        // the first of them: its part is in slot 2 c0 + 1, that of CTA c0 + i in slot 2 (c0 + i)
+    int b, h, rb;  // the item
+    int pad[3];
 };
 __device__ __forceinline__ JoinTask* join_task(const AttnArgs& a, int c) { return reinterpret_cast<JoinTask*>(a.ws) + c; }
 __device__ __forceinline__ void write_join_task(const AttnArgs& a, const Place& p, int c, int n, int tile) {
@@ -146,13 +150,11 @@ __device__ __forceinline__ void write_join_task(const AttnArgs& a, const Place& 
     t.n = 0;
     if (c < n) {
         Walk walk(p, cta_begin(p.total, c, n), cta_begin(p.total, c + 1, n));
-        const int64_t u = walk.at;
         Segment s;
         if (walk.next(a, tile, s) && s.tile0 > 0) {
-            const int64_t u0 = u - s.tile0;
-            t.c0 = cta_of(p.total, u0, n);
-            t.n = cta_of(p.total, u0 + s.tiles - 1, n) - t.c0 + 1;
-            t.first_slot = cta_begin(p.total, t.c0, n) == u0 ? 2 * t.c0 : 2 * t.c0 + 1;
+            const int64_t first = walk.item0 + (int64_t)(s.h * a.n_rb + s.rb) * (a.setup + s.tiles) + a.setup;
+            t.c0 = cta_of(p.total, first, n);
+            t.n = cta_of(p.total, first + s.tiles - 1, n) - t.c0 + 1;
             t.b = s.b;
             t.h = s.h;
             t.rb = s.rb;
@@ -162,10 +164,11 @@ __device__ __forceinline__ void write_join_task(const AttnArgs& a, const Place& 
 }
 
 // A workspace slot: maxima (log2 domain) and sums of its rows, then their
-// unnormalised outputs.
+// unnormalised outputs; and the slot of a CTA's part of an item.
 __device__ __forceinline__ float* slot_ptr(const AttnArgs& a, int slot) {
     return a.ws + kAttnMaxCtas * (sizeof(JoinTask) / 4) + (int64_t)slot * a.slot_floats;
 }
+__device__ __forceinline__ int part_slot(const Segment& s) { return 2 * blockIdx.x + (s.tile0 > 0 ? 0 : 1); }
 
 constexpr float kNone = -3.0e38f;     // running maximum of a row that saw nothing yet
 constexpr float kSlack = 8.0f;        // how far (log2) scores may exceed the running maximum before it is moved

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs 
                 if (has[v]) *reinterpret_cast<float4*>(o_s + (warp * R + r) * D + (lane + 32 * v) * 4) = o[r][v];
         __syncthreads();
         const bool whole = s.tile1 - s.tile0 == s.tiles;
-        float* slot = slot_ptr(a, 2 * blockIdx.x + (s.first ? 0 : 1));
+        float* slot = slot_ptr(a, part_slot(s));
         for (int e = tid; e < nr * (D / 4); e += G::NT) {
             const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
             float top = kNone, sum = 0.f;
@@ -294,10 +294,9 @@ __global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a) {
     // (the bounds hold for every task of this call's; they keep calls that share a workspace against the rules
     // from writing out of bounds)
     if (task.n < 2 || (unsigned)task.b >= (unsigned)a.B || (unsigned)task.h >= (unsigned)a.H_kv ||
-        (unsigned)task.rb >= (unsigned)a.n_rb || (unsigned)task.c0 >= kAttnMaxCtas || task.c0 + task.n > kAttnMaxCtas ||
-        (unsigned)(task.first_slot - 2 * task.c0) > 1u)
+        (unsigned)task.rb >= (unsigned)a.n_rb || (unsigned)task.c0 >= kAttnMaxCtas || task.c0 + task.n > kAttnMaxCtas)
         return;
-    const int n = task.n, c0 = task.c0, first_slot = task.first_slot;
+    const int n = task.n, c0 = task.c0;
     // many parts: groups share a row's parts, about 4 each; where a block has too few groups for that, a worker
     // takes a quarter of a row
     const int need = n > kSerial ? (n + 3) / 4 : 1;
@@ -320,7 +319,7 @@ __global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a) {
                 for (int k = 0; k < U; ++k) {
                     const int part = i + k * share;
                     if (part < n) {
-                        const float* slot = slot_ptr(a, part == 0 ? first_slot : 2 * (c0 + part));
+                        const float* slot = slot_ptr(a, 2 * (c0 + part) + (part == 0 ? 1 : 0));
                         m[k] = slot[r];
                         l[k] = slot[a.rb_rows + r];
                         x[k] = *reinterpret_cast<const float4*>(slot + a.stat_floats + r * a.D + d);

@@ -458,7 +458,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             if constexpr (CPT == 64) *reinterpret_cast<float2*>(scr_w + 2 * lane) = make_float2(l[0], l[1]);
             else if (CPT == 32 || (lane & 1) == 0) scr_w[CPT == 32 ? lane : lane >> 1] = l[0];
             softmax_sync<NSOFT>();
-            float* slot = slot_ptr(a, 2 * blockIdx.x + (s.first ? 0 : 1));
+            float* slot = slot_ptr(a, part_slot(s));
             for (int c = st; c < nr; c += NSOFT) {
                 const float sum = (sum_s[c] + sum_s[N + c]) + (sum_s[2 * N + c] + sum_s[3 * N + c]);
                 const float m = m_s[c];

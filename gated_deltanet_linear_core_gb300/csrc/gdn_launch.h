@@ -169,7 +169,8 @@ struct AttnArgs {
     float scale_log2;      // score scale times log2 e
     int group, rows;       // H_q / H_kv, K * group
     int rb_rows, n_rb;     // rows per row block, row blocks
-    int min_units;         // least tiles per CTA
+    int setup;             // units that starting an item counts as, beside its tiles
+    int min_units;         // least units per CTA
 };
 constexpr int kAttnMaxK = 16;
 constexpr int kAttnMaxCtas = 152;  // CTAs of a call, at most: one per SM
