@@ -23,7 +23,11 @@
 // of head dim 256 where HBM takes 2.9).  Sums are kept per thread in f32 and joined at the end.
 //
 // Warps: 0 loads K and V, 1 issues the MMAs, 2 loads Q of the next segment as
-// soon as S of the last tile is done, the others are the softmax.  The MMA warp
+// soon as S of the last tile is done, the others are the softmax.  Where a box
+// has 16 tokens or less, warp 2 loads V: a TMA load takes its warp some 80
+// clocks, and a tile of head dim 256 is 64 of them at 16 tokens (64 ragged
+// sequences, pages of 8: 174 us with one warp, 111 with two; of 64: 103 and 105,
+// so there one has both).  The MMA warp
 // runs S of the next tile ahead of P V of this one, across segments too, so
 // that only the outputs stand between two segments.  Every wait is bounded
 // (1 s): on a timeout the roles run out without waiting, the copies in flight
@@ -83,7 +87,7 @@ struct Layout {
     static constexpr int T_COLS = T_USED <= 64 ? 64 : T_USED <= 128 ? 128 : T_USED <= 256 ? 256 : 512;
     static_assert(N * 512 <= P_BYTES, "output rows");
     static_assert(SMEM <= kSmemMax && NS >= 3, "shared memory");
-    static_assert(21 * 8 + 16 <= BARS, "barriers");
+    static_assert(22 * 8 + 6 * 4 <= BARS, "barriers");
 
     // byte offset of P's column block (16-byte chunk j of 8 columns) of token t
     __device__ static __forceinline__ uint32_t p_off(int buf, int lo, int chunk, int t) {
@@ -111,6 +115,22 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1;; ++it) {
         if (mbar_test(bar, parity)) return true;
+        if ((it & 31) == 0) {
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 > kWaitNs) {
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// The same for a slot's position counter to reach `pos`.
+__device__ __forceinline__ bool loaded_or_abort(volatile int* filled, int pos, volatile int* abort_flag) {
+    if (*filled >= pos) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (*filled >= pos) return true;
         if ((it & 31) == 0) {
             if (*abort_flag) return false;
             if (globaltimer_ns() - t0 > kWaitNs) {
@@ -202,6 +222,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     uint64_t* q_empty = bars + 19;    // S of a segment's last tile done
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 20);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+    volatile int* filled = reinterpret_cast<volatile int*>(bars + 22);  // [6] one more than the last position loaded into a slot
     volatile int* odd_v = reinterpret_cast<volatile int*>(tslot + 2);  // a new token's value is not finite
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -209,6 +230,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         for (int i = 0; i < 6; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
+            filled[i] = 0;
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
@@ -243,61 +265,64 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     Segment s;
     const int nslab = (a.D + 63) / 64;  // 64-dim slabs of a cache row
 
+    // Page pieces of a tile: lane p of a loading warp takes piece p.
+    const int np = TILE / piece;
+    const bool two = piece <= 16;  // V has a warp of its own
+    auto look_up = [&](const Segment& g, int tile, int& y, int& z) {
+        const int t = tile * TILE + lane * piece;
+        z = a.n_pages;  // reads as zeros
+        y = 0;
+        if (lane < np && t < g.len) {
+            const int pg = t / a.page_size;
+            const int page = a.table[(int64_t)g.b * a.max_pages + pg];
+            if (page >= 0 && page < a.n_pages) z = page;
+            y = g.h * a.page_size + (t - pg * a.page_size);
+        }
+    };
+    auto load = [&](const CUtensorMap* map, const Segment& g, int tile, int y, int z, int sl) -> bool {  // into slots sl ..
+        const int left = g.len - tile * TILE;
+        const int have = left >= TILE ? np : (left + piece - 1) / piece;  // pieces with tokens
+        for (int db = 0; db < NDB; ++db, ++sl) {
+            const int st = sl % NS;
+            // the slot's last load may be the other warp's, and still to come: until then the barrier's parity
+            // would speak of the load before it
+            if (sl >= NS && !__all_sync(0xffffffffu, loaded_or_abort(&filled[st], sl - NS + 1, abort_flag) &&
+                                                         wait_or_abort(&empty[st], (uint32_t)((sl / NS - 1) & 1), abort_flag)))
+                return false;
+            const int slabs = nslab - 2 * db < 2 ? nslab - 2 * db : 2;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&full[st], (uint32_t)(have * piece * 128 * slabs));
+                filled[st] = sl + 1;
+            }
+            __syncwarp();
+            if (lane < have) {
+                const uint32_t dst = smem_u32(sm) + st * SLOT + lane * piece * 128;
+                for (int i = 0; i < slabs; ++i) tma_load_3d(dst + i * SLAB, map, &full[st], (2 * db + i) * 64, y, z);
+            }
+        }
+        return true;
+    };
+
     if (warp == 0) {
-        // ------------------------------------------------ loads: lane p takes piece p of a tile
-        const int np = TILE / piece;
-        int sl = 0;  // slots filled
+        // ------------------------------------------------ K and V
+        int sl0 = 0;  // slots before
         bool ok = true;
         while (ok && walk.next(a, TILE, s)) {
             if (s.len == 0) continue;
-            const int32_t* table = a.table + (int64_t)s.b * a.max_pages;
-            auto look_up = [&](int tile, int& y, int& z) {
-                const int t = tile * TILE + lane * piece;
-                z = a.n_pages;  // reads as zeros
-                y = 0;
-                if (lane < np && t < s.len) {
-                    const int pg = t / a.page_size;
-                    const int page = table[pg];
-                    if (page >= 0 && page < a.n_pages) z = page;
-                    y = s.h * a.page_size + (t - pg * a.page_size);
-                }
-            };
-            // K(0), then K(j + 1) and V(j): the order the MMAs take them in
-            auto load = [&](const CUtensorMap* map, int tile, int y, int z) {
-                const int left = s.len - tile * TILE;
-                const int have = left >= TILE ? np : (left + piece - 1) / piece;  // pieces with tokens
-                for (int db = 0; ok && db < NDB; ++db, ++sl) {
-                    const int st = sl % NS;
-                    if (sl >= NS) {
-                        ok = __all_sync(0xffffffffu, wait_or_abort(&empty[st], (uint32_t)((sl / NS - 1) & 1), abort_flag));
-                        if (!ok) break;
-                    }
-                    const int slabs = nslab - 2 * db < 2 ? nslab - 2 * db : 2;
-                    if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(have * piece * 128 * slabs));
-                    __syncwarp();
-                    if (lane < have) {
-                        const uint32_t dst = smem_u32(sm) + st * SLOT + lane * piece * 128;
-                        for (int i = 0; i < slabs; ++i)
-                            tma_load_3d(dst + i * SLAB, map, &full[st], (2 * db + i) * 64, y, z);
-                    }
-                }
-            };
-            int y, z, yn = 0, zn = 0;
-            look_up(s.tile0, y, z);
-            load(&kmap, s.tile0, y, z);
-            for (int j = s.tile0; ok && j < s.tile1; ++j) {
-                if (j + 1 < s.tile1) {
-                    look_up(j + 1, yn, zn);
-                    load(&kmap, j + 1, yn, zn);
-                }
-                load(&vmap, j, y, z);
-                y = yn;
-                z = zn;
+            const int n = s.tile1 - s.tile0;
+            int yv = 0, zv = 0, yk, zk, yn = 0, zn = 0;  // pieces of tiles j, j + 1, and j + 2 looked up ahead
+            look_up(s, s.tile0, yk, zk);
+            for (int j = -1; ok && j < n; ++j) {  // K of tile j + 1, V of tile j
+                if (j + 2 < n) look_up(s, s.tile0 + j + 2, yn, zn);
+                if (j + 1 < n) ok = load(&kmap, s, s.tile0 + j + 1, yk, zk, sl0 + L::k_slot(j + 1));
+                if (j >= 0 && !two) ok = ok && load(&vmap, s, s.tile0 + j, yv, zv, sl0 + L::v_slot(j, n));
+                yv = yk;
+                zv = zk;
+                yk = yn;
+                zk = zn;
             }
+            sl0 += 2 * NDB * n;
         }
-        // on abort: let the copies in flight land before the CTA exits
-        if (*abort_flag)
-            for (int k = sl > NS ? sl - NS : 0; k < sl; ++k) mbar_wait(&full[k % NS], (uint32_t)((k / NS) & 1), kWaitNs);
     } else if (warp == 1) {
         // ------------------------------------------------ MMAs (lane 0)
         if (lane == 0) {
@@ -372,12 +397,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             if (*abort_flag && last != nullptr) mbar_wait(last, last_parity, kWaitNs);
         }
     } else if (warp == 2) {
-        // ------------------------------------------------ Q rows, zero beyond the block's rows and the head's dims
-        int seg = 0;
-        while (walk.next(a, TILE, s)) {
+        // ------------------------------------------------ Q rows (zero beyond the block's rows and the head's dims), V
+        int seg = 0, sl0 = 0;  // segments and slots before
+        bool ok = true;
+        while (ok && walk.next(a, TILE, s)) {
             if (s.len == 0) continue;
-            const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
-            if (seg > 0 && !__all_sync(0xffffffffu, wait_or_abort(q_empty, (uint32_t)((seg - 1) & 1), abort_flag))) break;
+            const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb), n = s.tile1 - s.tile0;
+            int y = 0, z = 0, yn = 0, zn = 0;
+            if (two) look_up(s, s.tile0, y, z);
+            if (seg > 0) ok = __all_sync(0xffffffffu, wait_or_abort(q_empty, (uint32_t)((seg - 1) & 1), abort_flag));
+            if (!ok) break;
             const uint32_t qs = smem_u32(sm) + L::O_Q;
 #pragma unroll 1
             for (int r = lane / (4 * NDB); r < N; r += 32 / (4 * NDB)) {  // 4 NDB lanes per row, 4 pieces each
@@ -397,6 +426,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
             ++seg;
+            for (int j = 0; two && ok && j < n; ++j) {
+                if (j + 1 < n) look_up(s, s.tile0 + j + 1, yn, zn);
+                ok = load(&vmap, s, s.tile0 + j, y, z, sl0 + L::v_slot(j, n));
+                y = yn;
+                z = zn;
+            }
+            sl0 += 2 * NDB * n;
         }
         if (lane == 0) write_join_task(a, place, blockIdx.x, n_cta, TILE);
     } else {
@@ -692,7 +728,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     }
     tc_fence_before();
     __syncthreads();
-    if (tid == 0 && *abort_flag) atomicOr(&g_attn_error, 1);
+    if (tid == 0 && *abort_flag) {
+        for (int st = 0; st < NS; ++st)  // let the copies in flight land before the CTA exits
+            if (filled[st] > 0) mbar_wait(&full[st], (uint32_t)(((filled[st] - 1) / NS) & 1), kWaitNs);
+        atomicOr(&g_attn_error, 1);
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tb, L::T_COLS);
