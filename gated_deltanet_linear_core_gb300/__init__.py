@@ -547,10 +547,11 @@ def _dptr(t, name, dev, dtype, shape=None):
     return _ptr(t, name, dtype, shape)
 
 
-def _on_stream(dev, stream, body):
+def _on_stream(dev, stream, body, used):
     """body(raw stream) with device number `dev` current and, where the caller
     names a stream, that stream current too, so that outputs and workspaces
-    allocated in body belong to the stream that uses them."""
+    allocated in body belong to the stream that uses them; the tensors `used`
+    are then marked as in use there, so that a caller may drop them at once."""
     if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
     if stream is None and torch._C._cuda_getDevice() == dev:
@@ -560,6 +561,9 @@ def _on_stream(dev, stream, body):
             return body(torch.cuda.current_stream(dev).cuda_stream)
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), dev) if int(stream) else torch.cuda.default_stream(dev)
+        for t in used:
+            if t is not None:
+                t.record_stream(stream)
         with torch.cuda.stream(stream):
             return body(stream.cuda_stream)
 
@@ -592,7 +596,7 @@ def gdn_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None,
             _dptr(seq_lens, "seq_lens", dev, i32), _dptr(cu_seqlens, "cu_seqlens", dev, i32, (B + 1,)), B, T, H, D,
             ps, n_pages, mp, _dtype_code(k), s)
 
-    st = _on_stream(dev, stream, body)
+    st = _on_stream(dev, stream, body, (k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens))
     if st:
         _lib.check(st, "gdn_kv_append")
     return k_cache, v_cache
@@ -640,7 +644,7 @@ def gdn_attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=0.0, gate=N
             _lib.check(st, "gdn_attn_decode")
         return (o, e) if return_lse else o
 
-    return _on_stream(dev, stream, body)
+    return _on_stream(dev, stream, body, (q, k_cache, v_cache, page_table, seq_lens, gate, out, lse, workspace))
 
 
 def gdn_draft_accept(target_probs, draft_probs, draft_tokens, uniforms, n_draft=None, slots=None, n_accept=None,
@@ -673,7 +677,8 @@ def gdn_draft_accept(target_probs, draft_probs, draft_tokens, uniforms, n_draft=
             _lib.check(st, "gdn_draft_accept")
         return n, tk, ns
 
-    return _on_stream(dev, stream, body)
+    return _on_stream(dev, stream, body, (target_probs, draft_probs, draft_tokens, uniforms, n_draft, slots, n_accept,
+                                          tokens, next_slot))
 
 
 @dataclass(frozen=True)

@@ -651,7 +651,6 @@ gdn_status_t gdn_kv_append(const void* k, const void* v, void* k_cache, void* v_
     const gdn_status_t st = check_cache(H_kv, D, page_size, n_pages, max_pages, dtype);
     if (st != GDN_OK) return st;
     if (B < 0 || B > (1 << 24) || T_tot < 0 || T_tot > (int64_t)INT32_MAX) return GDN_ERR_INVALID_ARG;
-    if ((int64_t)D * elem_size(dtype) % 16 != 0) return GDN_ERR_UNSUPPORTED;
     if (T_tot == 0) return GDN_OK;
     if (B == 0 || (cu_seqlens == nullptr && T_tot % B != 0)) return GDN_ERR_INVALID_ARG;
     if (k == nullptr || v == nullptr || k_cache == nullptr || v_cache == nullptr || page_table == nullptr ||

@@ -63,6 +63,12 @@ SHAPES = [
     ([5000], 1, 16, 2, 256, 64, True),
     ([9000, 17, 4000], 5, 16, 2, 256, 16, True),
     ([6001], 6, 6, 1, 192, 1, False),
+    ([3000, 250, 129, 5, 1200], 5, 16, 2, 256, 8, True),
+    ([2500, 40, 1111], 16, 16, 2, 256, 16, False),
+    ([2500, 40, 1111], 16, 16, 2, 128, 8, True),
+    ([900] * 40, 8, 8, 1, 256, 4, False),
+    ([130] * 300, 3, 8, 1, 256, 12, True),
+    ([4000, 4000], 2, 40, 4, 104, 40, True),
 ]
 
 
@@ -291,6 +297,15 @@ def test_acceptance_matches_its_definition(B, K, V, dtype):
     check_accept(p, None, draft, u, n_draft)
 
 
+def test_acceptance_over_the_largest_vocabulary():
+    """Sums over 2^24 values, of which the last ones decide."""
+    V = 1 << 24
+    p = torch.full((2, 1, V), 2.0 ** -24)
+    p[0, 0, :-3] = 0
+    u = torch.tensor([[0.999], [1 - 2.0 ** -24]])
+    check_accept(p, None, torch.zeros((2, 0), dtype=torch.int32), u)
+
+
 def test_acceptance_borders():
     V = 4100
     p, q, draft, u, slots = accept_inputs(6, 3, V, F, 12)
@@ -388,6 +403,27 @@ def test_other_streams_and_graphs():
         torch.cuda.synchronize()
         r = ref.attention(q, kc, vc, table, ln, gate=gt)
         ref.check_attention(got[0], got[1], r, BF)
+
+
+def test_inputs_dropped_after_a_call_on_another_stream():
+    """Inputs given up right after the call are not reused before the stream has run it."""
+    side = torch.cuda.Stream()
+    g = torch.Generator().manual_seed(52)
+    kc, vc, table, ln = ref.make_cache([2000, 1500], 16, 2, 256, BF, g, "cuda")
+    q0 = torch.randn((2, 1, 16, 256), generator=g).to(BF).cuda()
+    want = gdn.gdn_attn_decode(q0, kc, vc, table, ln)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        q = q0.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)
+        got = gdn.gdn_attn_decode(q, kc, vc, table, ln, stream=side)
+        del q
+        junk = [torch.full_like(q0, 3.0) for _ in range(4)]  # would land in q's memory
+        side.synchronize()
+        assert torch.equal(got, want)
+        del junk
 
 
 def test_two_calls_at_once():
