@@ -54,8 +54,11 @@ constexpr int kSmemMax = 232448;
 
 template <int N, int NDB>
 struct Layout {
-    static constexpr int CPT = N <= 32 ? N : N / 2;  // columns (rows of Q) per softmax thread
-    static constexpr int CH = CPT < 32 ? CPT : 32;   // columns per TMEM access
+    // Columns (rows of Q) per softmax thread and per TMEM access.  More warps with fewer columns hide more, until
+    // registers spill: 128 rows of head dim 256 take 222 us with 16 warps and 267 with 8, of head dim 128 (whose O
+    // has both parts of P) 164 and 144; 32 rows 165 and 166.
+    static constexpr int CPT = N <= 32 ? 16 : N == 64 || NDB == 2 ? 32 : 64;
+    static constexpr int CH = N == 128 && NDB == 2 ? 16 : CPT < 32 ? CPT : 32;
     static constexpr int NWG = N / CPT;           // softmax warpgroups
     static constexpr int NSW = 4 * NWG;           // softmax warps
     static constexpr int NT = 96 + 32 * NSW;
@@ -152,14 +155,15 @@ template <int NTHR>
 __device__ __forceinline__ void softmax_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
 }
-template <int NTHR>
-__device__ __forceinline__ bool softmax_any(bool x) {
+// The same for the warpgroup that shares columns (named barriers 2 ..).
+__device__ __forceinline__ void group_sync(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory"); }
+__device__ __forceinline__ bool group_any(int wg, bool x) {
     uint32_t r;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\t"
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)x), "n"(NTHR)
+        : "r"((uint32_t)x), "r"(2 + wg)
         : "memory");
     return r != 0;
 }
@@ -441,7 +445,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         const int st = tid - 96;                 // softmax thread
         const int quad = warp & 3;               // its TMEM lanes: 32 quad ..
         const int row = quad * 32 + lane;        // token of a tile, head dim of an output block
-        const int c0 = ((warp - 3) >> 2) * CPT;  // its columns: c0 ..
+        const int wg = (warp - 3) >> 2;
+        const int c0 = wg * CPT;                 // its columns: c0 ..
         const uint32_t tq = tb + ((uint32_t)(quad * 32) << 16) + c0;
         float* m_s = reinterpret_cast<float*>(sm + L::O_M);     // running maxima
         int* vis_s = reinterpret_cast<int*>(sm + L::O_VIS);     // tokens a row sees
@@ -625,14 +630,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 #pragma unroll
                         for (int i = 0; i < 4; ++i) top = fmaxf(top, x[c + i]);
                     }
-                    if (softmax_any<NSOFT>(top > kSlack)) {
+                    if (group_any(wg, top > kSlack)) {
                         // ---- new maxima; sums and outputs so far are scaled to them
                         if (!first) wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
                         tc_fence_after();
                         tmem_ld<CH>(ts, x);
                         tmem_wait_ld();
                         constexpr int W = L::NWG * CH;
-                        const int w0 = ((warp - 3) >> 2) * CH;
 #pragma unroll
                         for (int c = 0; c < CH; ++c) {
                             x[c] *= a.scale_log2;
@@ -642,17 +646,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 #pragma unroll
                         for (int c = 0; c < CH; ++c) t[c] = x[c];
                         join_lanes<CH>(t, lane, [](float p, float q) { return fmaxf(p, q); });
-                        if (CH == 32 || (lane & 1) == 0) scr[quad * W + w0 + (CH == 32 ? lane : lane >> 1)] = t[0];
-                        softmax_sync<NSOFT>();
-                        for (int i = st; i < W; i += NSOFT) {
-                            const int c = i / CH * CPT + c1 + i % CH;
+                        if (CH == 32 || (lane & 1) == 0) scr[quad * W + wg * CH + (CH == 32 ? lane : lane >> 1)] = t[0];
+                        group_sync(wg);
+                        if ((st & 127) < CH) {
+                            const int i = wg * CH + (st & 127), c = c0 + c1 + (st & 127);
                             const float m0 = m_s[c];
                             const float t1 = fmaxf(fmaxf(scr[i], scr[W + i]), fmaxf(scr[2 * W + i], scr[3 * W + i]));
                             const float m1 = t1 > m0 + kSlack ? t1 : m0;  // rows do not move with one another
                             m_s[c] = m1;
                             f_s[c] = ex2_approx(m0 - m1);
                         }
-                        softmax_sync<NSOFT>();
+                        group_sync(wg);
 #pragma unroll
                         for (int c = 0; c < CH; ++c) x[c] -= m_s[c0 + c1 + c];
                         if (!first) {
