@@ -448,7 +448,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         const int wg = (warp - 3) >> 2;
         const int c0 = wg * CPT;                 // its columns: c0 ..
         const uint32_t tq = tb + ((uint32_t)(quad * 32) << 16) + c0;
-        float* m_s = reinterpret_cast<float*>(sm + L::O_M);     // running maxima
+        float* n_s = reinterpret_cast<float*>(sm + L::O_M);     // running maxima, negative
         int* vis_s = reinterpret_cast<int*>(sm + L::O_VIS);     // tokens a row sees
         float* f_s = reinterpret_cast<float*>(sm + L::O_F);     // factors of a rescaling, 1 / l at the end
         float* scr = reinterpret_cast<float*>(sm + L::O_SCR);   // [4 lane quarters][NWG * CH]
@@ -502,7 +502,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             float* slot = slot_ptr(a, part_slot(s));
             for (int c = st; c < nr; c += NSOFT) {
                 const float sum = (sum_s[c] + sum_s[N + c]) + (sum_s[2 * N + c] + sum_s[3 * N + c]);
-                const float m = m_s[c];
+                const float m = -n_s[c];
                 f_s[c] = sum == 0.f ? 0.f : 1.0f / sum;
                 if (live) {
                     if (whole) {
@@ -584,7 +584,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             }
             tc_fence_before();
         };
-        float l[CPT];  // this token's part of the rows' sums
+        alignas(8) float l[CPT];  // this token's part of the rows' sums
         for (;;) {
             // one copy of each part: the next segment, the last one's outputs, the tiles
             Segment nx;
@@ -595,7 +595,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
             softmax_sync<NSOFT>();  // the outputs before are out of P's memory and the arrays
             for (int c = st; c < N; c += NSOFT) {
-                m_s[c] = kNone;
+                n_s[c] = -kNone;
                 vis_s[c] = c < nr ? visible(a, s.len, r0 + c) : 0;
             }
             if (st == 0) *odd_v = 0;
@@ -615,21 +615,22 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     float x[CH];  // scores in the log2 domain, less the running maximum
                     tmem_ld<CH>(ts, x);
                     tmem_wait_ld();
-                    float top = -INFINITY;
 #pragma unroll
                     for (int c = 0; c < CH; c += 4) {
-                        const float4 m4 = *reinterpret_cast<const float4*>(m_s + c0 + c1 + c);
-                        const float m[4] = {m4.x, m4.y, m4.z, m4.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[c + i] = fmaf(x[c + i], a.scale_log2, -m[i]);
-                        if (tail) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (t0 + row >= vis_s[c0 + c1 + c + i]) x[c + i] = -INFINITY;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) top = fmaxf(top, x[c + i]);
+                        const float4 n4 = *reinterpret_cast<const float4*>(n_s + c0 + c1 + c);
+                        const float2 sc = make_float2(a.scale_log2, a.scale_log2);
+                        const float2 u = __ffma2_rn(make_float2(x[c], x[c + 1]), sc, make_float2(n4.x, n4.y));
+                        const float2 v = __ffma2_rn(make_float2(x[c + 2], x[c + 3]), sc, make_float2(n4.z, n4.w));
+                        x[c] = u.x; x[c + 1] = u.y; x[c + 2] = v.x; x[c + 3] = v.y;
                     }
+                    if (tail) {
+#pragma unroll
+                        for (int c = 0; c < CH; ++c)
+                            if (t0 + row >= vis_s[c0 + c1 + c]) x[c] = -INFINITY;
+                    }
+                    float top = x[0];
+#pragma unroll
+                    for (int c = 1; c < CH; ++c) top = fmaxf(top, x[c]);
                     if (group_any(wg, top > kSlack)) {
                         // ---- new maxima; sums and outputs so far are scaled to them
                         if (!first) wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
@@ -650,15 +651,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         group_sync(wg);
                         if ((st & 127) < CH) {
                             const int i = wg * CH + (st & 127), c = c0 + c1 + (st & 127);
-                            const float m0 = m_s[c];
+                            const float m0 = -n_s[c];
                             const float t1 = fmaxf(fmaxf(scr[i], scr[W + i]), fmaxf(scr[2 * W + i], scr[3 * W + i]));
                             const float m1 = t1 > m0 + kSlack ? t1 : m0;  // rows do not move with one another
-                            m_s[c] = m1;
+                            n_s[c] = -m1;
                             f_s[c] = ex2_approx(m0 - m1);
                         }
                         group_sync(wg);
 #pragma unroll
-                        for (int c = 0; c < CH; ++c) x[c] -= m_s[c0 + c1 + c];
+                        for (int c = 0; c < CH; ++c) x[c] += n_s[c0 + c1 + c];
                         if (!first) {
 #pragma unroll
                             for (int c = 0; c < CH; ++c) l[c1 + c] *= f_s[c0 + c1 + c];
@@ -677,14 +678,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     uint32_t hi[CH / 2], lo[CH / 2];
 #pragma unroll
                     for (int i = 0; i < CH / 2; ++i) {
-                        const float p0 = ex2_approx(x[2 * i]), p1 = ex2_approx(x[2 * i + 1]);
-                        l[c1 + 2 * i] += p0;
-                        l[c1 + 2 * i + 1] += p1;
-                        const uint32_t w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
+                        const float2 p = make_float2(ex2_approx(x[2 * i]), ex2_approx(x[2 * i + 1]));
+                        float2* sum = reinterpret_cast<float2*>(l + c1 + 2 * i);
+                        *sum = __fadd2_rn(*sum, p);
+                        const uint32_t w0 = __float_as_uint(p.x), w1 = __float_as_uint(p.y);
                         hi[i] = __byte_perm(w0, w1, 0x7632);  // the upper halves: cut, not rounded
                         // the rest, at least p's last bit: a rest of 0 would turn an infinite value into NaN
-                        lo[i] = pack_bf16x2(__uint_as_float(w0 | 1u) - __uint_as_float(w0 & 0xffff0000u),
-                                            __uint_as_float(w1 | 1u) - __uint_as_float(w1 & 0xffff0000u));
+                        const float2 rest = __fadd2_rn(
+                            make_float2(__uint_as_float(w0 | 1u), __uint_as_float(w1 | 1u)),
+                            make_float2(__uint_as_float((w0 & 0xffff0000u) | 0x80000000u),
+                                        __uint_as_float((w1 & 0xffff0000u) | 0x80000000u)));
+                        lo[i] = pack_bf16x2(rest.x, rest.y);
                     }
                     if (c1 == 0 && it >= L::PBUF) wait(&pv_done[(it - L::PBUF) & 1], (it - L::PBUF) >> 1);
 #pragma unroll
