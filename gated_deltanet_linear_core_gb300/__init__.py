@@ -628,18 +628,27 @@ def gdn_attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=0.0, gate=N
     code = _dtype_code(q)
 
     def body(s):
-        o = torch.empty_like(q) if out is None else out
-        e = torch.empty(shape[:3], dtype=torch.float32, device=q.device) if lse is None and return_lse else lse
-        # one batch size stands for all: the size goes by the head layout and K
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(_attn_workspace(min(B, 1), K, H_q, H, D, ps, code), dtype=torch.uint8, device=q.device)
+        # what the caller passes is checked, what is allocated here is not
+        p_q = _dptr(q, "q", dev, dt)
+        if out is None:
+            o = torch.empty_like(q)
+            p_o = o.data_ptr()
+        else:
+            o, p_o = out, _dptr(out, "out", dev, dt, shape)
+        e, p_e = lse, _dptr(lse, "lse", dev, torch.float32, shape[:3])
+        if e is None and return_lse:
+            e = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
+            p_e = e.data_ptr()
+        if workspace is None:  # one batch size stands for all: the size goes by the head layout and K
+            nws = _attn_workspace(1 if B else 0, K, H_q, H, D, ps, code)
+            ws = torch.empty(nws, dtype=torch.uint8, device=q.device)
+            p_w = ws.data_ptr()
+        else:
+            p_w, nws = _dptr(workspace, "workspace", dev, None), workspace.numel() * workspace.element_size()
         st = _lib.load().gdn_attn_decode(
-            _dptr(q, "q", dev, dt), _dptr(k_cache, "k_cache", dev, dt), _dptr(v_cache, "v_cache", dev, dt),
+            p_q, _dptr(k_cache, "k_cache", dev, dt), _dptr(v_cache, "v_cache", dev, dt),
             _dptr(page_table, "page_table", dev, i32), _dptr(seq_lens, "seq_lens", dev, i32), scale,
-            _dptr(gate, "gate", dev, dt, shape), _dptr(o, "out", dev, dt, shape),
-            _dptr(e, "lse", dev, torch.float32, shape[:3]), B, K, H_q, H, D, ps, n_pages, mp,
-            _dptr(ws, "workspace", dev, None), ws.numel() * ws.element_size(), code, s)
+            _dptr(gate, "gate", dev, dt, shape), p_o, p_e, B, K, H_q, H, D, ps, n_pages, mp, p_w, nws, code, s)
         if st:
             _lib.check(st, "gdn_attn_decode")
         return (o, e) if return_lse else o
@@ -662,17 +671,21 @@ def gdn_draft_accept(target_probs, draft_probs, draft_tokens, uniforms, n_draft=
     B, K1, V = target_probs.shape
     K, on = K1 - 1, target_probs.device
 
+    def result(given, name, shape):  # (tensor, its address): the caller's, checked, or a new one
+        if given is None:
+            t = torch.empty(shape, dtype=i32, device=on)
+            return t, t.data_ptr()
+        return given, _dptr(given, name, dev, i32, shape)
+
     def body(s):
-        n = torch.empty(B, dtype=i32, device=on) if n_accept is None else n_accept
-        tk = torch.empty((B, K1), dtype=i32, device=on) if tokens is None else tokens
-        ns = torch.empty(B, dtype=i32, device=on) if next_slot is None and slots is not None else next_slot
+        n, p_n = result(n_accept, "n_accept", (B,))
+        tk, p_t = result(tokens, "tokens", (B, K1))
+        ns, p_s = (None, None) if next_slot is None and slots is None else result(next_slot, "next_slot", (B,))
         st = _lib.load().gdn_draft_accept(
             _dptr(target_probs, "target_probs", dev, dt), _dptr(draft_probs, "draft_probs", dev, dt, (B, K, V)),
             _dptr(draft_tokens, "draft_tokens", dev, i32, (B, K)),
             _dptr(uniforms, "uniforms", dev, torch.float32, (B, K1)), _dptr(n_draft, "n_draft", dev, i32, (B,)),
-            _dptr(slots, "slots", dev, i32, (B, K + 2)), B, K, V, _dptr(n, "n_accept", dev, i32, (B,)),
-            _dptr(tk, "tokens", dev, i32, (B, K1)), _dptr(ns, "next_slot", dev, i32, (B,)),
-            _dtype_code(target_probs), s)
+            _dptr(slots, "slots", dev, i32, (B, K + 2)), B, K, V, p_n, p_t, p_s, _dtype_code(target_probs), s)
         if st:
             _lib.check(st, "gdn_draft_accept")
         return n, tk, ns

@@ -277,7 +277,7 @@ struct Running {
     __device__ __forceinline__ void add(float m1, float l1, float4 x) {
         const float top = fmaxf(m, m1);
         const float ref = top == -INFINITY ? 0.f : top;
-        const float f = exp2f(m - ref), w = exp2f(m1 - ref);
+        const float f = tc::ex2_approx(m - ref), w = tc::ex2_approx(m1 - ref);
         m = top;
         l = l * f + l1 * w;
         o.x = o.x * f + x.x * w; o.y = o.y * f + x.y * w; o.z = o.z * f + x.z * w; o.w = o.w * f + x.w * w;
