@@ -412,9 +412,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             if (seg > 0) ok = __all_sync(0xffffffffu, wait_or_abort(q_empty, (uint32_t)((seg - 1) & 1), abort_flag));
             if (!ok) break;
             const uint32_t qs = smem_u32(sm) + L::O_Q;
-#pragma unroll 1
-            for (int r = lane / (4 * NDB); r < N; r += 32 / (4 * NDB)) {  // 4 NDB lanes per row, 4 pieces each
-                const bf16* src = static_cast<const bf16*>(a.q) + (r < nr ? row_index(a, s.b, s.h, r0 + r) * a.D : 0);
+            // 4 NDB lanes per row, 4 pieces each; a row's new token i and query head g are stepped, not divided out
+            constexpr int RS = 32 / (4 * NDB);
+            const int step_i = RS / a.group, step_g = RS - step_i * a.group;
+            int i0 = (r0 + lane / (4 * NDB)) / a.group, g0 = r0 + lane / (4 * NDB) - i0 * a.group;
+#pragma unroll 2
+            for (int r = lane / (4 * NDB); r < N; r += RS) {
+                const bf16* src = static_cast<const bf16*>(a.q) +
+                                  (r < nr ? (((int64_t)s.b * a.K + i0) * a.H_q + s.h * a.group + g0) * a.D : 0);
+                i0 += step_i;
+                g0 += step_g;
+                if (g0 >= a.group) {
+                    g0 -= a.group;
+                    ++i0;
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int ch = lane % (4 * NDB) + i * 4 * NDB;  // 8 dims
