@@ -44,44 +44,56 @@ struct Place {
 };
 
 // Units of the call and the sequence that holds the first unit of CTA c of the
-// n that take part (n is capped so that a CTA has at least min_units).  Every
-// warp works it out for itself, all lanes together: a block-wide scan saves
-// loads but costs three barriers, which at the start of a call is longer.
+// n that take part (n is capped so that a CTA has at least min_units), by one
+// warp: a lane adds up a 32nd of the sequences, then the warp searches the lane's
+// share that holds the unit.  (A block-wide scan saves loads but costs three
+// barriers, which at the start of a call is longer.)
 __device__ __forceinline__ Place find_place(const AttnArgs& a, int tile, int c, int& n) {
     const int lane = threadIdx.x & 31;
     const int64_t mult = (int64_t)a.H_kv * a.n_rb;
-    const int len0 = lane < a.B ? clamped_len(a, lane) : 0;  // kept: all of a small batch
-    int64_t all = lane < a.B ? units_of(a, len0, tile) : 0;
-    for (int b = lane + 32; b < a.B; b += 32) all += units_of(a, clamped_len(a, b), tile);
+    const int per = (a.B + 31) / 32;
+    int64_t inc = 0;
+#pragma unroll 4
+    for (int i = 0; i < per; ++i) {
+        const int b = lane * per + i;
+        if (b < a.B) inc += units_of(a, clamped_len(a, b), tile);
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
     Place p;
-    p.total = all * mult;
+    p.total = __shfl_sync(0xffffffffu, inc, 31) * mult;
     p.first = 0;
     p.b = p.len = 0;
     const int64_t most = (p.total + a.min_units - 1) / a.min_units;
     if (n > most) n = (int)most;
     if (c >= n) return p;
     const int64_t want = cta_begin(p.total, c, n);
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int owner = __ffs(__ballot_sync(0xffffffffu, want < inc * mult)) - 1;
+    const int64_t before = __shfl_sync(0xffffffffu, inc, owner > 0 ? owner - 1 : 0);
+    if (owner > 0) p.first = before * mult;
+    const int end = min(a.B, (owner + 1) * per);
+    for (int b0 = owner * per; b0 < end; b0 += 32) {
         const int b = b0 + lane;
-        const int len = b0 == 0 ? len0 : (b < a.B ? clamped_len(a, b) : 0);
-        int inc = b < a.B ? units_of(a, len, tile) : 0;  // inclusive scan: 32 sequences' units fit 31 bits
+        const int len = b < end ? clamped_len(a, b) : 0;
+        int sum = b < end ? units_of(a, len, tile) : 0;  // inclusive scan: 32 sequences' units fit 31 bits
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
         }
-        const uint32_t past = __ballot_sync(0xffffffffu, want < p.first + inc * mult);
+        const uint32_t past = __ballot_sync(0xffffffffu, want < p.first + sum * mult);
         if (past != 0) {
             const int l = __ffs(past) - 1;
-            const int before = __shfl_sync(0xffffffffu, inc, l > 0 ? l - 1 : 0);
+            const int less = __shfl_sync(0xffffffffu, sum, l > 0 ? l - 1 : 0);
             p.b = b0 + l;
             p.len = __shfl_sync(0xffffffffu, len, l);
-            if (l > 0) p.first += before * mult;
+            if (l > 0) p.first += less * mult;
             break;
         }
-        p.first += __shfl_sync(0xffffffffu, inc, 31) * mult;
+        p.first += __shfl_sync(0xffffffffu, sum, 31) * mult;
     }
     return p;
 }
@@ -145,20 +157,19 @@ struct alignas(16) JoinTask {
     int pad[3];
 };
 __device__ __forceinline__ JoinTask* join_task(const AttnArgs& a, int c) { return reinterpret_cast<JoinTask*>(a.ws) + c; }
-__device__ __forceinline__ void write_join_task(const AttnArgs& a, const Place& p, int c, int n, int tile) {
+// `first`: the CTA's first segment, just taken from its walk; null: it has none.
+__device__ __forceinline__ void write_join_task(const AttnArgs& a, const Place& p, const Walk& walk, const Segment* first,
+                                                int c, int n) {
     JoinTask t;
     t.n = 0;
-    if (c < n) {
-        Walk walk(p, cta_begin(p.total, c, n), cta_begin(p.total, c + 1, n));
-        Segment s;
-        if (walk.next(a, tile, s) && s.tile0 > 0) {
-            const int64_t first = walk.item0 + (int64_t)(s.h * a.n_rb + s.rb) * (a.setup + s.tiles) + a.setup;
-            t.c0 = cta_of(p.total, first, n);
-            t.n = cta_of(p.total, first + s.tiles - 1, n) - t.c0 + 1;
-            t.b = s.b;
-            t.h = s.h;
-            t.rb = s.rb;
-        }
+    if (first != nullptr && first->tile0 > 0) {
+        const Segment& s = *first;
+        const int64_t u = walk.item0 + (int64_t)(s.h * a.n_rb + s.rb) * (a.setup + s.tiles) + a.setup;
+        t.c0 = cta_of(p.total, u, n);
+        t.n = cta_of(p.total, u + s.tiles - 1, n) - t.c0 + 1;
+        t.b = s.b;
+        t.h = s.h;
+        t.rb = s.rb;
     }
     *join_task(a, c) = t;
 }

@@ -72,9 +72,9 @@ __global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs 
     pdl_trigger();
     int n_cta = gridDim.x;
     const Place place = find_place(a, TT, blockIdx.x, n_cta);
-    if (tid == G::NT - 32) write_join_task(a, place, blockIdx.x, n_cta, TT);
-    if ((int)blockIdx.x >= n_cta) return;
-    Walk walk(place, cta_begin(place.total, blockIdx.x, n_cta), cta_begin(place.total, blockIdx.x + 1, n_cta));
+    const int64_t u0 = (int)blockIdx.x < n_cta ? cta_begin(place.total, blockIdx.x, n_cta) : 0;
+    const int64_t u1 = (int)blockIdx.x < n_cta ? cta_begin(place.total, blockIdx.x + 1, n_cta) : 0;
+    Walk walk(place, u0, u1);
     const E* kc = static_cast<const E*>(a.k_cache);
     const E* vc = static_cast<const E*>(a.v_cache);
     const bool has[2] = {lane * 4 < D, NV > 1 && (lane + 32) * 4 < D};
@@ -82,7 +82,9 @@ __global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs 
     const int my_t = lane / PER, my_r = lane % PER * S;  // token of the lane's scores, first row
 
     Segment s;
-    while (walk.next(a, TT, s)) {
+    bool more = walk.next(a, TT, s);
+    if (tid == G::NT - 32) write_join_task(a, place, walk, more ? &s : nullptr, blockIdx.x, n_cta);
+    for (; more; more = walk.next(a, TT, s)) {
         const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
         const int end = min(s.len, s.tile1 * TT);
         const int32_t* table = a.table + (int64_t)s.b * a.max_pages;

@@ -68,8 +68,8 @@ struct Layout {
     static constexpr int P_BYTES = N == 16 ? SLAB : N == 32 ? 2 * SLAB : PBUF * 2 * ((N + 63) / 64) * SLAB;
     static constexpr int Q_BYTES = 2 * NDB * N * 128;
     static constexpr int SCR = 4 * NWG * CH * 4;     // scratch: a value per lane quarter and column of one access
-    static constexpr int BARS = 256;
-    static constexpr int SMALL = BARS + N * 4 * 3 + SCR;
+    static constexpr int BARS = 320, SEGS = 4;  // barriers; segments told ahead
+    static constexpr int SMALL = BARS + SEGS * 32 + N * 4 * 3 + SCR;
     static constexpr int FIT = (kSmemMax - P_BYTES - Q_BYTES - SMALL) / SLOT;
     static constexpr int NS = FIT < 6 ? FIT : 6;
     // Slots are filled and used in the order K(0), K(1), V(0), K(2), V(1), .. of a segment's n tiles
@@ -79,7 +79,8 @@ struct Layout {
     static constexpr int O_Q = NS * SLOT;
     static constexpr int O_P = O_Q + Q_BYTES;
     static constexpr int O_BAR = O_P + P_BYTES;
-    static constexpr int O_M = O_BAR + BARS;
+    static constexpr int O_SEG = O_BAR + BARS;
+    static constexpr int O_M = O_SEG + SEGS * 32;
     static constexpr int O_VIS = O_M + N * 4;
     static constexpr int O_F = O_VIS + N * 4;
     static constexpr int O_SCR = O_F + N * 4;
@@ -90,7 +91,7 @@ struct Layout {
     static constexpr int T_COLS = T_USED <= 64 ? 64 : T_USED <= 128 ? 128 : T_USED <= 256 ? 256 : 512;
     static_assert(N * 512 <= P_BYTES, "output rows");
     static_assert(SMEM <= kSmemMax && NS >= 3, "shared memory");
-    static_assert(22 * 8 + 6 * 4 <= BARS, "barriers");
+    static_assert(30 * 8 + 6 * 4 <= BARS, "barriers");
 
     // byte offset of P's column block (16-byte chunk j of 8 columns) of token t
     __device__ static __forceinline__ uint32_t p_off(int buf, int lo, int chunk, int t) {
@@ -111,6 +112,14 @@ struct Layout {
         else return (buf * 2 + lo) * ((N + 63) / 64) * SLAB;
     }
 };
+
+// What warp 0 tells the other roles of a segment: only it walks the range (the
+// walk's code and divisions in every role cost each of them more than the note).
+struct alignas(16) SegmentNote {
+    Segment s;
+    int more;  // 0: the range has ended
+};
+static_assert(sizeof(SegmentNote) == 32, "notes");
 
 // Bounded wait; returns at once when another role has given up.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
@@ -154,6 +163,17 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 template <int NTHR>
 __device__ __forceinline__ void softmax_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
+}
+template <int NTHR>
+__device__ __forceinline__ bool softmax_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "n"(NTHR)
+        : "memory");
+    return r != 0;
 }
 // The same for the warpgroup that shares columns (named barriers 2 ..).
 __device__ __forceinline__ void group_sync(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory"); }
@@ -224,9 +244,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     uint64_t* pv_done = bars + 16;    // [2] P V of a tile done
     uint64_t* q_full = bars + 18;     // a segment's Q written (Q warp)
     uint64_t* q_empty = bars + 19;    // S of a segment's last tile done
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 20);
+    uint64_t* seg_full = bars + 20;   // [4] a segment is told (warp 0)
+    uint64_t* seg_empty = bars + 24;  // [4] ... and taken note of (MMA warp, Q warp, softmax warps)
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 28);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-    volatile int* filled = reinterpret_cast<volatile int*>(bars + 22);  // [6] one more than the last position loaded into a slot
+    volatile int* filled = reinterpret_cast<volatile int*>(bars + 30);  // [6] one more than the last position loaded into a slot
     volatile int* odd_v = reinterpret_cast<volatile int*>(tslot + 2);  // a new token's value is not finite
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -243,6 +265,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
+        for (int i = 0; i < L::SEGS; ++i) {
+            mbar_init(&seg_full[i], 1);
+            mbar_init(&seg_empty[i], 2 + L::NSW);
+        }
         *abort_flag = 0;
         *odd_v = 0;
         fence_mbar_init();
@@ -260,13 +286,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     pdl_wait();
     pdl_trigger();
 
-    int n_cta = gridDim.x;
-    const Place place = find_place(a, TILE, blockIdx.x, n_cta);
-    const bool works = (int)blockIdx.x < n_cta;
-    const int64_t u0 = works ? cta_begin(place.total, blockIdx.x, n_cta) : 0;
-    const int64_t u1 = works ? cta_begin(place.total, blockIdx.x + 1, n_cta) : 0;
-    Walk walk(place, u0, u1);
     Segment s;
+    SegmentNote* notes = reinterpret_cast<SegmentNote*>(sm + L::O_SEG);
+    int sg = 0;  // segments told or taken note of
+    // The next segment, from warp 0: false at the end of the CTA's range.  `ok` turns false where the wait gave up.
+    auto heard = [&](bool& ok) -> bool {
+        const int e = sg % L::SEGS;
+        ok = wait_or_abort(&seg_full[e], (uint32_t)((sg / L::SEGS) & 1), abort_flag);
+        if (!ok) return false;
+        const SegmentNote n = notes[e];
+        s = n.s;
+        ++sg;
+        return n.more != 0;
+    };
+    auto took_note = [&] { mbar_arrive(&seg_empty[(sg - 1) % L::SEGS]); };  // one thread per role, after heard()
     const int nslab = (a.D + 63) / 64;  // 64-dim slabs of a cache row
 
     // Page pieces of a tile: lane p of a loading warp takes piece p.
@@ -309,14 +342,29 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 
     if (warp == 0) {
         // ------------------------------------------------ K and V
+        int n_cta = gridDim.x;
+        const Place place = find_place(a, TILE, blockIdx.x, n_cta);
+        const bool works = (int)blockIdx.x < n_cta;
+        Walk walk(place, works ? cta_begin(place.total, blockIdx.x, n_cta) : 0,
+                  works ? cta_begin(place.total, blockIdx.x + 1, n_cta) : 0);
         int sl0 = 0;  // slots before
-        bool ok = true;
-        while (ok && walk.next(a, TILE, s)) {
-            if (s.len == 0) continue;
-            const int n = s.tile1 - s.tile0;
-            int yv = 0, zv = 0, yk, zk, yn = 0, zn = 0;  // pieces of tiles j, j + 1, and j + 2 looked up ahead
-            look_up(s, s.tile0, yk, zk);
-            for (int j = -1; ok && j < n; ++j) {  // K of tile j + 1, V of tile j
+        bool ok = true, more = true;
+        while (ok && more) {
+            more = walk.next(a, TILE, s);
+            const int e = sg % L::SEGS;
+            if (sg >= L::SEGS)
+                ok = __all_sync(0xffffffffu, wait_or_abort(&seg_empty[e], (uint32_t)((sg / L::SEGS - 1) & 1), abort_flag));
+            if (!ok) break;
+            if (lane == 0) {
+                notes[e].s = s;
+                notes[e].more = more;
+                mbar_arrive(&seg_full[e]);
+            }
+            ++sg;
+            const int n = more && s.len > 0 ? s.tile1 - s.tile0 : 0;
+            int yv = 0, zv = 0, yk = 0, zk = 0, yn = 0, zn = 0;  // pieces of tiles j, j + 1, and j + 2 looked up ahead
+            if (n > 0) look_up(s, s.tile0, yk, zk);
+            for (int j = -1; ok && n > 0 && j < n; ++j) {  // K of tile j + 1, V of tile j
                 if (j + 2 < n) look_up(s, s.tile0 + j + 2, yn, zn);
                 if (j + 1 < n) ok = load(&kmap, s, s.tile0 + j + 1, yk, zk, sl0 + L::k_slot(j + 1));
                 if (j >= 0 && !two) ok = ok && load(&vmap, s, s.tile0 + j, yv, zv, sl0 + L::v_slot(j, n));
@@ -326,6 +374,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 zk = zn;
             }
             sl0 += 2 * NDB * n;
+            if (sg == 1 && lane == 0) write_join_task(a, place, walk, more ? &s : nullptr, blockIdx.x, n_cta);
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMAs (lane 0)
@@ -360,7 +409,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 return true;
             };
             bool ok = true;
-            while (ok && walk.next(a, TILE, s)) {
+            while (ok && heard(ok)) {
+                took_note();
                 if (s.len == 0) continue;
                 const int n = s.tile1 - s.tile0;
                 ok = wait_or_abort(q_full, (uint32_t)(seg & 1), abort_flag);
@@ -404,7 +454,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         // ------------------------------------------------ Q rows (zero beyond the block's rows and the head's dims), V
         int seg = 0, sl0 = 0;  // segments and slots before
         bool ok = true;
-        while (ok && walk.next(a, TILE, s)) {
+        for (;;) {
+            const bool more = heard(ok);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || !more) break;
+            if (lane == 0) took_note();
             if (s.len == 0) continue;
             const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb), n = s.tile1 - s.tile0;
             int y = 0, z = 0, yn = 0, zn = 0;
@@ -449,7 +503,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             }
             sl0 += 2 * NDB * n;
         }
-        if (lane == 0) write_join_task(a, place, blockIdx.x, n_cta, TILE);
     } else {
         // ------------------------------------------------ softmax and outputs
         constexpr int CH = L::CH;
@@ -468,19 +521,27 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         auto wait = [&](uint64_t* bar, int k) {
             live = __all_sync(0xffffffffu, live && wait_or_abort(bar, (uint32_t)(k & 1), abort_flag));
         };
-        // The next segment with tokens; rows of empty sequences become zeros on the way.
-        auto next_segment = [&](Segment& g) -> bool {
-            while (walk.next(a, TILE, g)) {
-                if (g.len > 0) return true;
-                const int r0 = g.rb * a.rb_rows, nr = block_rows(a, g.rb);
+        // The next segment with tokens, into s; rows of empty sequences become zeros on the way.  The warps agree
+        // on a wait that gave up (they meet at barriers).
+        auto next_segment = [&]() -> bool {
+            for (;;) {
+                bool ok;
+                const bool more = heard(ok);
+                if (softmax_any<NSOFT>(!ok)) {
+                    live = false;
+                    return false;
+                }
+                if (!more) return false;
+                if (lane == 0) took_note();
+                if (s.len > 0) return true;
+                const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
                 for (int e = st; e < nr * a.D; e += NSOFT) {
                     const int r = e / a.D, d = e - r * a.D;
-                    const int64_t at = row_index(a, g.b, g.h, r0 + r);
+                    const int64_t at = row_index(a, s.b, s.h, r0 + r);
                     static_cast<bf16*>(a.out)[at * a.D + d] = from_f<bf16>(0.f);
                     if (d == 0 && a.lse != nullptr) a.lse[at] = -INFINITY;
                 }
             }
-            return false;
         };
         // Sums and outputs of a segment whose last tile is handed to the MMA warp.
         auto finish_segment = [&](const Segment& s, float (&l)[CPT]) {
@@ -598,11 +659,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         alignas(8) float l[CPT];  // this token's part of the rows' sums
         for (;;) {
             // one copy of each part: the next segment, the last one's outputs, the tiles
-            Segment nx;
-            const bool more = next_segment(nx);
-            if (it > 0) finish_segment(s, l);
+            const Segment before = s;
+            const bool more = next_segment();
+            if (it > 0) finish_segment(before, l);
             if (!more) break;
-            s = nx;
             const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
             softmax_sync<NSOFT>();  // the outputs before are out of P's memory and the arrays
             for (int c = st; c < N; c += NSOFT) {
