@@ -581,7 +581,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         if (a.lse != nullptr)
                             a.lse[out_row(c)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
                     } else {
-                        slot[c] = m == kNone ? -INFINITY : m;
+                        slot[c] = sum == 0.f ? -INFINITY : m;
                         slot[a.rb_rows + c] = sum;
                     }
                 }
@@ -666,7 +666,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
             softmax_sync<NSOFT>();  // the outputs before are out of P's memory and the arrays
             for (int c = st; c < N; c += NSOFT) {
-                n_s[c] = -kNone;
+                n_s[c] = 0.f;
                 vis_s[c] = c < nr ? visible(a, s.len, r0 + c) : 0;
             }
             if (st == 0) *odd_v = 0;
@@ -702,18 +702,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     float top = x[0];
 #pragma unroll
                     for (int c = 1; c < CH; ++c) top = fmaxf(top, x[c]);
-                    if (group_any(wg, top > kSlack)) {
+                    if (first || group_any(wg, top > kSlack)) {
                         // ---- new maxima; sums and outputs so far are scaled to them
                         if (!first) wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
                         tc_fence_after();
-                        tmem_ld<CH>(ts, x);
-                        tmem_wait_ld();
                         constexpr int W = L::NWG * CH;
 #pragma unroll
-                        for (int c = 0; c < CH; ++c) {
-                            x[c] *= a.scale_log2;
-                            if (tail && t0 + row >= vis_s[c0 + c1 + c]) x[c] = -INFINITY;
-                        }
+                        for (int c = 0; c < CH; ++c) x[c] -= n_s[c0 + c1 + c];
                         float t[CH];
 #pragma unroll
                         for (int c = 0; c < CH; ++c) t[c] = x[c];
@@ -724,7 +719,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             const int i = wg * CH + (st & 127), c = c0 + c1 + (st & 127);
                             const float m0 = -n_s[c];
                             const float t1 = fmaxf(fmaxf(scr[i], scr[W + i]), fmaxf(scr[2 * W + i], scr[3 * W + i]));
-                            const float m1 = t1 > m0 + kSlack ? t1 : m0;  // rows do not move with one another
+                            // rows do not move with one another; one that sees nothing of a segment's first tile sees
+                            // nothing of it, and its maximum stays 0
+                            const float m1 = t1 > (first ? -INFINITY : m0 + kSlack) ? t1 : m0;
                             n_s[c] = -m1;
                             f_s[c] = ex2_approx(m0 - m1);
                         }
