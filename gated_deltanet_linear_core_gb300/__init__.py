@@ -547,25 +547,30 @@ def _dptr(t, name, dev, dtype, shape=None):
     return _ptr(t, name, dtype, shape)
 
 
-def _on_stream(dev, stream, body, used):
-    """body(raw stream) with device number `dev` current and, where the caller
-    names a stream, that stream current too, so that outputs and workspaces
-    allocated in body belong to the stream that uses them; the tensors `used`
-    are then marked as in use there, so that a caller may drop them at once."""
+def _elsewhere(dev, stream) -> bool:
+    """Whether a call on device number `dev` needs _on_stream: it names a stream,
+    or its device is not the current one (or no CUDA device)."""
+    return stream is not None or dev < 0 or torch._C._cuda_getDevice() != dev
+
+
+def _on_stream(dev, stream, used, body):
+    """body() with device number `dev` current and, where the caller names a
+    stream, that stream current too, so that outputs and workspaces allocated in
+    body belong to the stream that uses them; the tensors `used` are then marked as
+    in use there, so that a caller may drop them at once."""
     if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
-    if stream is None and torch._C._cuda_getDevice() == dev:
-        return body(torch._C._cuda_getCurrentRawStream(dev))
     with torch.cuda.device(dev):
         if stream is None:
-            return body(torch.cuda.current_stream(dev).cuda_stream)
+            return body()
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), dev) if int(stream) else torch.cuda.default_stream(dev)
+        with torch.cuda.stream(stream):
+            res = body()
         for t in used:
             if t is not None:
                 t.record_stream(stream)
-        with torch.cuda.stream(stream):
-            return body(stream.cuda_stream)
+        return res
 
 
 def _cache_dims(k_cache, v_cache, page_table, seq_lens):
@@ -584,19 +589,18 @@ def gdn_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None,
     seq_lens[b] (int32 [B], new tokens counted); page_table int32 [B, max_pages].
     Returns (k_cache, v_cache)."""
     dt, i32, dev = k.dtype, torch.int32, k.get_device()
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, (k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens),
+                          lambda: gdn_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens))
     n_pages, H, ps, D, B, mp = _cache_dims(k_cache, v_cache, page_table, seq_lens)
     if k.dim() != 3:
         raise ValueError("k: expected [T, H_kv, D]")
     T = k.shape[0]
-
-    def body(s):
-        return _lib.load().gdn_kv_append(
-            _dptr(k, "k", dev, dt, (T, H, D)), _dptr(v, "v", dev, dt, (T, H, D)), _dptr(k_cache, "k_cache", dev, dt),
-            _dptr(v_cache, "v_cache", dev, dt), _dptr(page_table, "page_table", dev, i32),
-            _dptr(seq_lens, "seq_lens", dev, i32), _dptr(cu_seqlens, "cu_seqlens", dev, i32, (B + 1,)), B, T, H, D,
-            ps, n_pages, mp, _dtype_code(k), s)
-
-    st = _on_stream(dev, stream, body, (k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens))
+    st = _lib.load().gdn_kv_append(
+        _dptr(k, "k", dev, dt, (T, H, D)), _dptr(v, "v", dev, dt, (T, H, D)), _dptr(k_cache, "k_cache", dev, dt),
+        _dptr(v_cache, "v_cache", dev, dt), _dptr(page_table, "page_table", dev, i32),
+        _dptr(seq_lens, "seq_lens", dev, i32), _dptr(cu_seqlens, "cu_seqlens", dev, i32, (B + 1,)), B, T, H, D, ps,
+        n_pages, mp, _dtype_code(k), torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _lib.check(st, "gdn_kv_append")
     return k_cache, v_cache
@@ -620,40 +624,42 @@ def gdn_attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=0.0, gate=N
     gate [B, K, H_q, D]: out = attention * sigmoid(gate).  Returns out
     [B, K, H_q, D], with return_lse also lse [B, K, H_q] f32."""
     dt, i32, dev = q.dtype, torch.int32, q.get_device()
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, (q, k_cache, v_cache, page_table, seq_lens, gate, out, lse, workspace),
+                          lambda: gdn_attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale, gate, out, lse,
+                                                  return_lse, workspace))
     n_pages, H, ps, D, B, mp = _cache_dims(k_cache, v_cache, page_table, seq_lens)
     shape = q.shape
     if len(shape) != 4 or shape[0] != B or shape[3] != D:
         raise ValueError(f"q: shape {tuple(shape)}, expected [{B}, K, H_q, {D}]")
     K, H_q = shape[1], shape[2]
     code = _dtype_code(q)
-
-    def body(s):
-        # what the caller passes is checked, what is allocated here is not
-        p_q = _dptr(q, "q", dev, dt)
-        if out is None:
-            o = torch.empty_like(q)
-            p_o = o.data_ptr()
-        else:
-            o, p_o = out, _dptr(out, "out", dev, dt, shape)
-        e, p_e = lse, _dptr(lse, "lse", dev, torch.float32, shape[:3])
-        if e is None and return_lse:
-            e = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
-            p_e = e.data_ptr()
-        if workspace is None:  # one batch size stands for all: the size goes by the head layout and K
-            nws = _attn_workspace(1 if B else 0, K, H_q, H, D, ps, code)
-            ws = torch.empty(nws, dtype=torch.uint8, device=q.device)
-            p_w = ws.data_ptr()
-        else:
-            p_w, nws = _dptr(workspace, "workspace", dev, None), workspace.numel() * workspace.element_size()
-        st = _lib.load().gdn_attn_decode(
-            p_q, _dptr(k_cache, "k_cache", dev, dt), _dptr(v_cache, "v_cache", dev, dt),
-            _dptr(page_table, "page_table", dev, i32), _dptr(seq_lens, "seq_lens", dev, i32), scale,
-            _dptr(gate, "gate", dev, dt, shape), p_o, p_e, B, K, H_q, H, D, ps, n_pages, mp, p_w, nws, code, s)
-        if st:
-            _lib.check(st, "gdn_attn_decode")
-        return (o, e) if return_lse else o
-
-    return _on_stream(dev, stream, body, (q, k_cache, v_cache, page_table, seq_lens, gate, out, lse, workspace))
+    # what the caller passes is checked, what is allocated here is not
+    p_q = _dptr(q, "q", dev, dt)
+    if out is None:
+        out = torch.empty_like(q)
+        p_o = out.data_ptr()
+    else:
+        p_o = _dptr(out, "out", dev, dt, shape)
+    if lse is None and return_lse:
+        lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
+        p_e = lse.data_ptr()
+    else:
+        p_e = _dptr(lse, "lse", dev, torch.float32, shape[:3])
+    if workspace is None:  # one batch size stands for all: the size goes by the head layout and K
+        nws = _attn_workspace(1 if B else 0, K, H_q, H, D, ps, code)
+        workspace = torch.empty(nws, dtype=torch.uint8, device=q.device)
+        p_w = workspace.data_ptr()
+    else:
+        p_w, nws = _dptr(workspace, "workspace", dev, None), workspace.numel() * workspace.element_size()
+    st = _lib.load().gdn_attn_decode(
+        p_q, _dptr(k_cache, "k_cache", dev, dt), _dptr(v_cache, "v_cache", dev, dt),
+        _dptr(page_table, "page_table", dev, i32), _dptr(seq_lens, "seq_lens", dev, i32), scale,
+        _dptr(gate, "gate", dev, dt, shape), p_o, p_e, B, K, H_q, H, D, ps, n_pages, mp, p_w, nws, code,
+        torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _lib.check(st, "gdn_attn_decode")
+    return (out, lse) if return_lse else out
 
 
 def gdn_draft_accept(target_probs, draft_probs, draft_tokens, uniforms, n_draft=None, slots=None, n_accept=None,
@@ -666,32 +672,39 @@ def gdn_draft_accept(target_probs, draft_probs, draft_tokens, uniforms, n_draft=
     [B, K + 1]: held drafts, next token, then -1; next_slot [B]: slots[b, n + 1],
     None without slots), all int32."""
     dt, i32, dev = target_probs.dtype, torch.int32, target_probs.get_device()
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, (target_probs, draft_probs, draft_tokens, uniforms, n_draft, slots, n_accept,
+                                        tokens, next_slot),
+                          lambda: gdn_draft_accept(target_probs, draft_probs, draft_tokens, uniforms, n_draft, slots,
+                                                   n_accept, tokens, next_slot))
     if target_probs.dim() != 3 or target_probs.shape[1] < 1:
         raise ValueError("target_probs: expected [B, K + 1, V]")
     B, K1, V = target_probs.shape
     K, on = K1 - 1, target_probs.device
-
-    def result(given, name, shape):  # (tensor, its address): the caller's, checked, or a new one
-        if given is None:
-            t = torch.empty(shape, dtype=i32, device=on)
-            return t, t.data_ptr()
-        return given, _dptr(given, name, dev, i32, shape)
-
-    def body(s):
-        n, p_n = result(n_accept, "n_accept", (B,))
-        tk, p_t = result(tokens, "tokens", (B, K1))
-        ns, p_s = (None, None) if next_slot is None and slots is None else result(next_slot, "next_slot", (B,))
-        st = _lib.load().gdn_draft_accept(
-            _dptr(target_probs, "target_probs", dev, dt), _dptr(draft_probs, "draft_probs", dev, dt, (B, K, V)),
-            _dptr(draft_tokens, "draft_tokens", dev, i32, (B, K)),
-            _dptr(uniforms, "uniforms", dev, torch.float32, (B, K1)), _dptr(n_draft, "n_draft", dev, i32, (B,)),
-            _dptr(slots, "slots", dev, i32, (B, K + 2)), B, K, V, p_n, p_t, p_s, _dtype_code(target_probs), s)
-        if st:
-            _lib.check(st, "gdn_draft_accept")
-        return n, tk, ns
-
-    return _on_stream(dev, stream, body, (target_probs, draft_probs, draft_tokens, uniforms, n_draft, slots, n_accept,
-                                          tokens, next_slot))
+    if n_accept is None:
+        n_accept = torch.empty((B,), dtype=i32, device=on)
+        p_n = n_accept.data_ptr()
+    else:
+        p_n = _dptr(n_accept, "n_accept", dev, i32, (B,))
+    if tokens is None:
+        tokens = torch.empty((B, K1), dtype=i32, device=on)
+        p_t = tokens.data_ptr()
+    else:
+        p_t = _dptr(tokens, "tokens", dev, i32, (B, K1))
+    if next_slot is None and slots is not None:
+        next_slot = torch.empty((B,), dtype=i32, device=on)
+        p_s = next_slot.data_ptr()
+    else:
+        p_s = _dptr(next_slot, "next_slot", dev, i32, (B,))
+    st = _lib.load().gdn_draft_accept(
+        _dptr(target_probs, "target_probs", dev, dt), _dptr(draft_probs, "draft_probs", dev, dt, (B, K, V)),
+        _dptr(draft_tokens, "draft_tokens", dev, i32, (B, K)),
+        _dptr(uniforms, "uniforms", dev, torch.float32, (B, K1)), _dptr(n_draft, "n_draft", dev, i32, (B,)),
+        _dptr(slots, "slots", dev, i32, (B, K + 2)), B, K, V, p_n, p_t, p_s, _dtype_code(target_probs),
+        torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _lib.check(st, "gdn_draft_accept")
+    return n_accept, tokens, next_slot
 
 
 @dataclass(frozen=True)
