@@ -707,8 +707,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         if (!first) wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
                         tc_fence_after();
                         constexpr int W = L::NWG * CH;
+                        if (!first) {
+                            // the scores again: less a maximum far from them, they have lost their digits
+                            uint32_t hidden = 0;
 #pragma unroll
-                        for (int c = 0; c < CH; ++c) x[c] -= n_s[c0 + c1 + c];
+                            for (int c = 0; c < CH; ++c) hidden |= (x[c] == -INFINITY ? 1u : 0u) << c;
+                            tmem_ld<CH>(ts, x);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < CH; ++c) x[c] = hidden >> c & 1 ? -INFINITY : x[c] * a.scale_log2;
+                        }
                         float t[CH];
 #pragma unroll
                         for (int c = 0; c < CH; ++c) t[c] = x[c];
@@ -719,9 +727,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             const int i = wg * CH + (st & 127), c = c0 + c1 + (st & 127);
                             const float m0 = -n_s[c];
                             const float t1 = fmaxf(fmaxf(scr[i], scr[W + i]), fmaxf(scr[2 * W + i], scr[3 * W + i]));
-                            // rows do not move with one another; one that sees nothing of a segment's first tile sees
-                            // nothing of it, and its maximum stays 0
-                            const float m1 = t1 > (first ? -INFINITY : m0 + kSlack) ? t1 : m0;
+                            // rows do not move with one another; scores of -inf only leave any later one above
+                            const float m1 = first ? fmaxf(t1, kNone) : t1 > m0 + kSlack ? t1 : m0;
                             n_s[c] = -m1;
                             f_s[c] = ex2_approx(m0 - m1);
                         }

@@ -499,8 +499,8 @@ gdn_status_t gdn_rmsnorm_gated(const void* o, const void* z, const void* w, floa
  * reach are used.  D is a multiple of 8 up to 256, any page_size >= 1 (the tensor-
  * core path: bf16 and page_size a multiple of 4).  max_pages * page_size and
  * H_kv * page_size are at most 2^30; offsets into the caches are 64-bit.
- * seq_lens (device) [B] int32 counts the new tokens too, and is clamped to
- * [0, max_pages * page_size].  A page outside [0, n_pages) is never accessed.
+ * seq_lens (device) [B] int32 counts the new tokens too.  A page outside
+ * [0, n_pages) is never accessed: nothing is written there, and it reads as zeros.
  */
 
 /*
@@ -535,8 +535,9 @@ gdn_status_t gdn_kv_append(const void* k, const void* v, void* k_cache, void* v_
  *   lse        (device) [B, K, H_q] f32, or NULL
  *   workspace  (device) >= gdn_attn_decode_workspace_size bytes; calls that may
  *              run at the same time need one each.  Its contents do not matter.
- * 0 <= K <= 16.  The lengths are read on the device: nothing synchronises, and a
- * captured call follows them.  Results do not depend on timing.
+ * 0 <= K <= 16.  seq_lens is clamped to [0, max_pages * page_size].  The lengths
+ * are read on the device: nothing synchronises, and a captured call follows them.
+ * Results do not depend on timing.
  */
 size_t gdn_attn_decode_workspace_size(int32_t B, int32_t K, int32_t H_q, int32_t H_kv, int32_t D,
                                       int32_t page_size, gdn_dtype_t dtype);

@@ -135,6 +135,23 @@ def test_scale_and_peaked_scores(dtype):
     check(x, dtype)
 
 
+@pytest.mark.parametrize("low", [-1e7, -3e38, -INF])
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_scores_far_below_the_others_change_nothing(dtype, low):
+    """Keys whose scores are lower than the others' by so much that their weights are 0: the outputs are
+    those over the other keys, to the same bound, wherever the low ones lie."""
+    page = 64
+    for B, K, hq, hkv, D, lo, hi in [(200, 1, 8, 2, 128, 0, 128), (100, 5, 16, 2, 256, 0, 256),
+                                     (100, 5, 16, 2, 256, 448, 576), (60, 16, 16, 2, 128, 0, 128)]:
+        x = attn_inputs([640] * B, K, hq, hkv, D, page, dtype, 51)
+        q, kc, vc, table, ln, _ = x
+        q[..., 0] = 1.0
+        kc[table[:, lo // page:hi // page].flatten().long(), :, :, 0] = low
+        out, lse = run_attn(x)
+        others = torch.cat([table[:, :lo // page], table[:, hi // page:]], 1)
+        ref.check_attention(out, lse, ref.attention(q, kc, vc, others, ln - (hi - lo)), dtype)
+
+
 def test_lengths_and_pages_are_clamped():
     """A length beyond the table, a negative one, and pages that do not exist."""
     x = attn_inputs([64, 64, 64], 1, 4, 2, 128, 16, BF, 3)
