@@ -181,7 +181,7 @@ __device__ __forceinline__ float* slot_ptr(const AttnArgs& a, int slot) {
 }
 __device__ __forceinline__ int part_slot(const Segment& s) { return 2 * blockIdx.x + (s.tile0 > 0 ? 0 : 1); }
 
-constexpr float kNone = -3.0e38f;     // running maximum of a row that saw nothing yet
+constexpr float kNone = -3.0e38f;     // running maximum of a row without a score above -inf yet
 constexpr float kSlack = 8.0f;        // how far (log2) scores may exceed the running maximum before it is moved
 constexpr float kLn2 = 0.6931471805599453f;
 

@@ -22,8 +22,8 @@ size_t attn_plan(AttnArgs& a, gdn_dtype_t dt) {
     a.rb_rows = (a.rows + a.n_rb - 1) / a.n_rb;
     a.min_units = 1;
     // about the tiles that HBM delivers while an item starts and ends (16 ragged sequences with 16 new tokens 100 -> 92 us,
-    // 8 in f32 30 -> 27)
-    a.setup = attn_tc_takes(a, dt) ? (a.rb_rows <= 32 ? 1 : a.rb_rows <= 64 ? 2 : 3) * (a.D <= 128 ? 2 : 1) : 2;
+    // 8 in f32 27 -> 24)
+    a.setup = (!attn_tc_takes(a, dt) ? 2 : a.rb_rows <= 32 ? 1 : a.rb_rows <= 64 ? 2 : 3) * (a.D <= 128 ? 2 : 1);
     a.stat_floats = (2 * a.rb_rows + 3) & ~3;
     a.slot_floats = a.stat_floats + (int64_t)a.rb_rows * a.D;
     return kAttnMaxCtas * (sizeof(attn::JoinTask) + 2 * (size_t)a.slot_floats * sizeof(float));

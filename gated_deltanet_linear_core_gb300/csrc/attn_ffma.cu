@@ -13,13 +13,16 @@
 // (scores in the log2 domain, all statistics in f32; m is moved only when a
 // score exceeds it by 2^8, so O is rarely rescaled).
 //
-// Reading the cache is the bound of few rows (4 rows of head dim 128: 5.7 TB/s
-// once it runs), so every warp
-// works on its own, without shared memory or barriers between tokens: a lane
-// holds 4 (or 8) dims of the rows' Q and O, a warp takes T tokens at a time
-// straight into registers (K and V together, 8 KB in flight per warp), the T R
-// partial dot products are joined over the lanes by halving, which leaves each
-// lane a score, and the weights go back through a few words of shared memory.
+// Reading the cache is the bound of few rows (64 ragged sequences of 512 to 8192
+// tokens in f32, 4 rows of head dim 128: 168 us, 6.5 TB/s; 8 rows are bound by
+// the instructions of the products: 227 us), so every warp works on its own,
+// without barriers between tokens: a lane holds 4 (or 8) dims of the rows' Q and
+// O, a warp takes T tokens at a time, and a lane copies its dims of the next T (or
+// 2 T) tokens' K and V into shared memory, where it alone reads them (cp.async; with
+// loads straight into registers, which overlap with no arithmetic of the warp,
+// 211 and 298 us).  The T R partial dot products are joined over the lanes by
+// halving, which leaves each lane a score, and the weights go back through a few
+// words of shared memory.
 // Blocks have at most kAttnFfmaRows rows: 16 in one pass (registers for 8 warps
 // only) took longer than two passes of 8, of which the second reads from L2.
 // The warps' results are joined at the end of a segment.
@@ -35,38 +38,61 @@ using namespace attn;
 
 constexpr int TT = 64;  // tokens of a unit
 
-// four consecutive elements as f32
-__device__ __forceinline__ float4 ld4(const float* p) { return __ldcs(reinterpret_cast<const float4*>(p)); }
-__device__ __forceinline__ float4 ld4(const bf16* p) {
-    const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p));
+// Copies 16 (or 8) bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy_async(float4* dst, const void* src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(real ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_async(uint2* dst, const void* src, bool real) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(real ? 8 : 0)
+                 : "memory");
+}
+// four consecutive elements, and as f32
+template <typename E> struct Four { using type = float4; };
+template <> struct Four<bf16> { using type = uint2; };
+__device__ __forceinline__ float4 as_f32(float4 u) { return u; }
+__device__ __forceinline__ float4 as_f32(uint2 u) {
     return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
                        __uint_as_float(u.y & 0xffff0000u));
 }
+__device__ __forceinline__ float4 ld4(const float* p) { return __ldcs(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 ld4(const bf16* p) { return as_f32(__ldcs(reinterpret_cast<const uint2*>(p))); }
 
-// R rows per block (of which block_rows are real), NV x 4 dims per lane, T tokens at a time, NW warps.
-template <int R, int NV>
+// R rows per block (of which block_rows are real), NV x 4 dims per lane, T tokens at a time, NW warps, ST stages.
+template <typename E, int R, int NV>
 struct Ffma {
     static constexpr int T = R == 4 ? 8 : 4;
-    // more warps beat more registers (8 rows, head dim 128: 50 us with 16 warps and a few spills, 70 with 8)
-    static constexpr int NW = NV == 1 ? 16 : 8;
+    // As many warps as registers allow, stages of 192 KB in all in f32 (4 rows of head dim 128: 8 warps with 3 stages
+    // 194 us, 12 with 2 168; 8 rows of head dim 256: 12 warps spill).  bf16 has room for more, but is bound by issue: more
+    // stages of it only cost at the start (4 rows: 16 warps with 2 stages 150 us, with 3 160, 12 with 4 184).
+    static constexpr int NW = R == 4 && sizeof(E) == 4 ? 12 / NV : 16 / NV;
+    static constexpr int ST = R == 4 ? 2 : 3;
+    static constexpr int STAGE = 2 * T * NV * 32;             // fours of a warp's stage: K, then V
     static constexpr int NT = NW * 32;
     static constexpr int C = T * R;       // scores of T tokens
     static constexpr int S = C / 32;      // scores per lane
     static constexpr int PER = R / S;     // lanes per token
+    // floats of all warps' stages, a warp's at least those of its outputs (R rows of NV x 128)
+    static constexpr int STAGE_FLOATS = NW * ST * STAGE * (int)sizeof(typename Four<E>::type) / 4;
     static_assert(C % 32 == 0 && PER * T == 32, "a lane holds whole scores");
+    static_assert(STAGE_FLOATS / NW >= R * NV * 128, "outputs fit the stages");
 };
 
 template <typename E, int R, int NV>
-__global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs a) {
-    using G = Ffma<R, NV>;
+__global__ void __launch_bounds__(Ffma<E, R, NV>::NT, 1) attn_ffma_kernel(AttnArgs a) {
+    using G = Ffma<E, R, NV>;
     constexpr int T = G::T, NW = G::NW, S = G::S, PER = G::PER;
+    using F = typename Four<E>::type;
     extern __shared__ __align__(16) float sm[];
-    float* p_s = sm;                            // [NW][T][R] weights
+    float* p_s = sm + G::STAGE_FLOATS;  // [NW][T][R] weights
     float* m_s = p_s + NW * G::C;               // [NW][R]
     float* l_s = m_s + NW * R;                  // [NW][R]
     int* vis_s = reinterpret_cast<int*>(l_s + NW * R);  // [R] tokens a row sees
-    float* o_s = reinterpret_cast<float*>(vis_s + R);   // [NW][R][D]
     const int D = a.D, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the warp's stages [ST][K, V][T][NV][32], of which a lane fills and reads its own; at the end its outputs [R][D]
+    F* stages = reinterpret_cast<F*>(sm) + warp * G::ST * G::STAGE + lane;
+    constexpr int O_STEP = G::STAGE_FLOATS / NW;
+    float* o_w = sm + warp * O_STEP;
 
     pdl_wait();
     pdl_trigger();
@@ -94,8 +120,30 @@ __global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs 
             if (page < 0 || page >= a.n_pages) return -1;
             return (((int64_t)page * a.H_kv + s.h) * a.page_size + (t - pg * a.page_size)) * D;
         };
+        auto issue = [&](int stage, int64_t off) {  // lane i: token i of the T
+            F* to = stages + stage * G::STAGE;
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                const int64_t at = __shfl_sync(0xffffffffu, off, t);
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const bool real = at >= 0 && has[v];
+                    const int64_t from = real ? at + (lane + 32 * v) * 4 : 0;
+                    copy_async(to + (t * NV + v) * 32, kc + from, real);
+                    copy_async(to + ((T + t) * NV + v) * 32, vc + from, real);
+                }
+            }
+        };
         int t0 = s.tile0 * TT + warp * T;
-        int64_t next = place_of(t0 + lane % T);  // lane i: token i of the T
+        int64_t next = place_of(t0 + lane % T);
+#pragma unroll 1
+        for (int i = 0; i < G::ST; ++i) {
+            const int64_t off = next;
+            next = place_of(t0 + (i + 1) * NW * T + lane % T);
+            issue(i, off);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        int stage = 0;
         if (tid < R) vis_s[tid] = tid < nr ? visible(a, s.len, r0 + tid) : 0;
         float4 q[R][NV], o[R][NV];
 #pragma unroll
@@ -118,37 +166,29 @@ __global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs 
         }
         const int least = vis_s[0];
         for (; t0 < end; t0 += NW * T) {
-            const int64_t off = next;
-            float4 kv[T][NV], vv[T][NV];
-#pragma unroll
-            for (int t = 0; t < T; ++t) {
-                const int64_t at = __shfl_sync(0xffffffffu, off, t);
-#pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    kv[t][v] = vv[t][v] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (at >= 0 && has[v]) {
-                        kv[t][v] = ld4(kc + at + (lane + 32 * v) * 4);
-                        vv[t][v] = ld4(vc + at + (lane + 32 * v) * 4);
-                    }
-                }
-            }
-            next = place_of(t0 + NW * T + lane % T);
+            asm volatile("cp.async.wait_group %0;" ::"n"(G::ST - 1) : "memory");
+            const F* k_s = stages + stage * G::STAGE;
+            const F* v_s = k_s + T * NV * 32;
             // ---- scores: partial dot products, joined over the lanes
             float x[G::C];
 #pragma unroll
-            for (int t = 0; t < T; ++t)
+            for (int t = 0; t < T; ++t) {
+                float4 kv[NV];
+#pragma unroll
+                for (int v = 0; v < NV; ++v) kv[v] = as_f32(k_s[(t * NV + v) * 32]);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    float2 d = __fmul2_rn(make_float2(kv[t][0].x, kv[t][0].y), make_float2(q[r][0].x, q[r][0].y));
-                    d = __ffma2_rn(make_float2(kv[t][0].z, kv[t][0].w), make_float2(q[r][0].z, q[r][0].w), d);
+                    float2 d = __fmul2_rn(make_float2(kv[0].x, kv[0].y), make_float2(q[r][0].x, q[r][0].y));
+                    d = __ffma2_rn(make_float2(kv[0].z, kv[0].w), make_float2(q[r][0].z, q[r][0].w), d);
                     if constexpr (NV > 1) {
-                        d = __ffma2_rn(make_float2(kv[t][NV - 1].x, kv[t][NV - 1].y),
+                        d = __ffma2_rn(make_float2(kv[NV - 1].x, kv[NV - 1].y),
                                        make_float2(q[r][NV - 1].x, q[r][NV - 1].y), d);
-                        d = __ffma2_rn(make_float2(kv[t][NV - 1].z, kv[t][NV - 1].w),
+                        d = __ffma2_rn(make_float2(kv[NV - 1].z, kv[NV - 1].w),
                                        make_float2(q[r][NV - 1].z, q[r][NV - 1].w), d);
                     }
                     x[t * R + r] = d.x + d.y;
                 }
+            }
             join_lanes<G::C>(x, lane, [](float u, float w) { return u + w; });
             const bool tail = t0 + T > least || t0 + T > end;
             bool over = false;
@@ -196,6 +236,9 @@ __global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs 
                     const float4 w = *reinterpret_cast<const float4*>(p_w + t * R + r);
                     p[r] = w.x; p[r + 1] = w.y; p[r + 2] = w.z; p[r + 3] = w.w;
                 }
+                float4 vv[NV];
+#pragma unroll
+                for (int v = 0; v < NV; ++v) vv[v] = as_f32(v_s[(t * NV + v) * 32]);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     // a hidden value may be anything: a weight of 0 must not meet it
@@ -204,12 +247,20 @@ __global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs 
 #pragma unroll
                     for (int v = 0; v < NV; ++v) {
                         float2* acc = reinterpret_cast<float2*>(&o[r][v]);
-                        acc[0] = __ffma2_rn(pp, make_float2(vv[t][v].x, vv[t][v].y), acc[0]);
-                        acc[1] = __ffma2_rn(pp, make_float2(vv[t][v].z, vv[t][v].w), acc[1]);
+                        acc[0] = __ffma2_rn(pp, make_float2(vv[v].x, vv[v].y), acc[0]);
+                        acc[1] = __ffma2_rn(pp, make_float2(vv[v].z, vv[v].w), acc[1]);
                     }
                 }
             }
+            __syncwarp();  // the reads of this stage come first
+            const int64_t off = next;
+            next = place_of(t0 + (G::ST + 1) * NW * T + lane % T);
+            issue(stage, off);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            stage = stage + 1 < G::ST ? stage + 1 : 0;
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
         // ---- the warps' parts, then the rows (or this segment's part of them)
 #pragma unroll
         for (int i = 0; i < S; ++i) {
@@ -224,7 +275,7 @@ __global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs 
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int v = 0; v < NV; ++v)
-                if (has[v]) *reinterpret_cast<float4*>(o_s + (warp * R + r) * D + (lane + 32 * v) * 4) = o[r][v];
+                if (has[v]) *reinterpret_cast<float4*>(o_w + r * D + (lane + 32 * v) * 4) = o[r][v];
         __syncthreads();
         const bool whole = s.tile1 - s.tile0 == s.tiles;
         float* slot = slot_ptr(a, part_slot(s));
@@ -237,7 +288,7 @@ __global__ void __launch_bounds__(Ffma<R, NV>::NT, 1) attn_ffma_kernel(AttnArgs 
 #pragma unroll 4
             for (int w = 0; w < NW; ++w) {
                 const float f = tc::ex2_approx(m_s[w * R + r] - top);
-                const float4 x = *reinterpret_cast<const float4*>(o_s + (w * R + r) * D + d);
+                const float4 x = *reinterpret_cast<const float4*>(sm + w * O_STEP + r * D + d);
                 sum = fmaf(f, l_s[w * R + r], sum);
                 y.x = fmaf(f, x.x, y.x); y.y = fmaf(f, x.y, y.y); y.z = fmaf(f, x.z, y.z); y.w = fmaf(f, x.w, y.w);
             }
@@ -361,8 +412,8 @@ __global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a) {
 
 template <typename E, int R, int NV>
 cudaError_t launch_ffma(const AttnArgs& a, int n_cta, cudaStream_t s) {
-    using G = Ffma<R, NV>;
-    const size_t smem = sizeof(float) * (G::NW * (G::C + 2 * R + (size_t)R * a.D) + R);
+    using G = Ffma<E, R, NV>;
+    const size_t smem = sizeof(float) * (G::STAGE_FLOATS + G::NW * (G::C + 2 * R) + R);
     const cudaError_t e = cudaFuncSetAttribute(attn_ffma_kernel<E, R, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem);
     if (e != cudaSuccess) return e;

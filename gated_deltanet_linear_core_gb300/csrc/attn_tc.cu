@@ -22,16 +22,17 @@
 // rest is free; two MMAs per step were bound by that (64 rows: 3.2 us per tile
 // of head dim 256 where HBM takes 2.9).  Sums are kept per thread in f32 and joined at the end.
 //
-// Warps: 0 loads K and V, 1 issues the MMAs, 2 loads Q of the next segment as
-// soon as S of the last tile is done, the others are the softmax.  Where a box
-// has 16 tokens or less, warp 2 loads V: a TMA load takes its warp some 80
-// clocks, and a tile of head dim 256 is 64 of them at 16 tokens (64 ragged
-// sequences, pages of 8: 174 us with one warp, 111 with two; of 64: 103 and 105,
-// so there one has both).  The MMA warp
-// runs S of the next tile ahead of P V of this one, across segments too, so
-// that only the outputs stand between two segments.  Every wait is bounded
-// (1 s): on a timeout the roles run out without waiting, the copies in flight
-// land, TMEM is freed and the error word is set.
+// Warps: 0 walks the CTA's range, tells the others its segments and loads K and V
+// (the walk in every role cost 600 short sequences with 5 new tokens 14 us of 116),
+// 1 issues the MMAs, 2 loads Q of the next segment as soon as S of the last tile
+// is done, the others are the softmax.  Where a box has 16 tokens or less, warp 2
+// loads V: a TMA load takes its warp some 80 clocks, and a tile of head dim 256 is
+// 64 of them at 16 tokens (64 ragged sequences, pages of 8: 174 us with one warp,
+// 111 with two; of 64: 103 and 105, so there one has both).  The MMA warp runs S
+// of the next tile ahead of P V of this one, across segments too, so that only
+// the outputs stand between two segments.  Every wait is bounded (1 s): on a
+// timeout the roles run out without waiting, the copies in flight land, TMEM is
+// freed and the error word is set.
 #include <cuda.h>
 
 #include "attn_common.cuh"
