@@ -56,8 +56,8 @@ constexpr int kSmemMax = 232448;
 template <int N, int NDB>
 struct Layout {
     // Columns (rows of Q) per softmax thread and per TMEM access.  More warps with fewer columns hide more, until
-    // registers spill: 128 rows of head dim 256 take 222 us with 16 warps and 267 with 8, of head dim 128 (whose O
-    // has both parts of P) 164 and 144; 32 rows 165 and 166.
+    // registers spill: 128 rows of head dim 256 took 222 us with 16 warps and 267 with 8; of head dim 128, whose O has
+    // both parts of P, 84 with 16 (16 columns at a time; 32 spill: 138) and 83 with 8; 32 rows 165 and 166.
     static constexpr int CPT = N <= 32 ? 16 : N == 64 || NDB == 2 ? 32 : 64;
     static constexpr int CH = N == 128 && NDB == 2 ? 16 : CPT < 32 ? CPT : 32;
     static constexpr int NWG = N / CPT;           // softmax warpgroups
