@@ -58,6 +58,11 @@ __device__ __forceinline__ float4 as_f32(uint2 u) {
 __device__ __forceinline__ float4 ld4(const float* p) { return __ldcs(reinterpret_cast<const float4*>(p)); }
 __device__ __forceinline__ float4 ld4(const bf16* p) { return as_f32(__ldcs(reinterpret_cast<const uint2*>(p))); }
 
+__device__ __forceinline__ void store4(float* p, float4 y) { *reinterpret_cast<float4*>(p) = y; }
+__device__ __forceinline__ void store4(bf16* p, float4 y) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+}
+
 // R rows per block (of which block_rows are real), NV x 4 dims per lane, T tokens at a time, NW warps, ST stages.
 template <typename E, int R, int NV>
 struct Ffma {
@@ -295,13 +300,12 @@ __global__ void __launch_bounds__(Ffma<E, R, NV>::NT, 1) attn_ffma_kernel(AttnAr
             if (whole) {
                 const int64_t row = row_index(a, s.b, s.h, r0 + r);
                 const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-                float out[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
+                y.x *= inv; y.y *= inv; y.z *= inv; y.w *= inv;
                 if (a.gate != nullptr) {
                     const float4 g = ld4(static_cast<const E*>(a.gate) + row * D + d);
-                    out[0] *= sigmoid_f(g.x); out[1] *= sigmoid_f(g.y); out[2] *= sigmoid_f(g.z); out[3] *= sigmoid_f(g.w);
+                    y.x *= sigmoid_f(g.x); y.y *= sigmoid_f(g.y); y.z *= sigmoid_f(g.z); y.w *= sigmoid_f(g.w);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) static_cast<E*>(a.out)[row * D + d + i] = from_f<E>(out[i]);
+                store4(static_cast<E*>(a.out) + row * D + d, y);
                 if (d == 0 && a.lse != nullptr) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
             } else {
                 *reinterpret_cast<float4*>(slot + a.stat_floats + r * D + d) = y;
@@ -317,30 +321,54 @@ __global__ void __launch_bounds__(Ffma<E, R, NV>::NT, 1) attn_ffma_kernel(AttnAr
 
 // Joins the parts of every item that more than one CTA worked on.  The CTAs
 // whose ranges start inside an item (blockIdx.x + 1) share its rows, gridDim.y
-// blocks each.  A group of D / 4 threads takes a row, 4 columns per thread, and
-// runs through the parts in CTA order (more than kSerial of them are
-// shared out to several groups), keeping the running maximum, sum
-// and output as the tiles do; the order is fixed, so results do not depend on
-// timing.
+// blocks each.  A group of threads (blockDim.x, 4 columns each) takes a row, or a
+// quarter of one, and runs through the parts in CTA order (more than kSerial of
+// them are shared out to several groups), keeping the running maximum, sum and
+// output as the tiles do; the order is fixed, so results do not depend on timing.
+// A block runs its code once, so fetching instructions is what it waits for: block
+// shapes are powers of two in place of divisions, and bf16 takes the approximate
+// exponential and quotient, far below the step of its rounding (16 sequences with
+// 16 new tokens 83 -> 79 us; one of 201 tokens 12.2 -> 9.7).
 constexpr int JT = 256;
 constexpr int kSerial = 8;
 struct Running {
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    __device__ __forceinline__ void add(float m1, float l1, float4 x) {
-        const float top = fmaxf(m, m1);
+    template <int U>
+    __device__ __forceinline__ void add(const float (&m1)[U], const float (&l1)[U], const float4 (&x)[U]) {
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < U; ++k) top = fmaxf(top, m1[k]);
         const float ref = top == -INFINITY ? 0.f : top;
-        const float f = tc::ex2_approx(m - ref), w = tc::ex2_approx(m1 - ref);
+        const float f = tc::ex2_approx(m - ref);
         m = top;
-        l = l * f + l1 * w;
-        o.x = o.x * f + x.x * w; o.y = o.y * f + x.y * w; o.z = o.z * f + x.z * w; o.w = o.w * f + x.w * w;
+        l *= f;
+        o.x *= f; o.y *= f; o.z *= f; o.w *= f;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const float w = tc::ex2_approx(m1[k] - ref);
+            l = fmaf(l1[k], w, l);
+            o.x = fmaf(x[k].x, w, o.x); o.y = fmaf(x[k].y, w, o.y);
+            o.z = fmaf(x[k].z, w, o.z); o.w = fmaf(x[k].w, w, o.w);
+        }
     }
 };
 template <typename T>
-__global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a) {
+__device__ __forceinline__ float gate_of(float g) {
+    return sizeof(T) == 2 ? __fdividef(1.0f, 1.0f + __expf(-g)) : sigmoid_f(g);
+}
+template <typename T>
+__device__ __forceinline__ float inverse(float x) {
+    return x == 0.f ? 0.f : sizeof(T) == 2 ? __fdividef(1.0f, x) : 1.0f / x;
+}
+// log_groups: log2 of blockDim.y; log_split: 2 where a group takes a quarter row, else 0.
+template <typename T>
+__global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a, int log_groups, int log_split) {
+    using Raw = typename Four<T>::type;
+    constexpr int U = 4;  // parts at once
     __shared__ float4 o_s[JT];
     __shared__ float2 ml_s[JT];
-    const int tid = threadIdx.x, c = blockIdx.x + 1;
+    const int c = blockIdx.x + 1, ng = blockDim.x, g = threadIdx.y, tid = g * ng + threadIdx.x;
     pdl_wait();
     pdl_trigger();
     const JoinTask task = *join_task(a, c);
@@ -349,62 +377,64 @@ __global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a) {
     if (task.n < 2 || (unsigned)task.b >= (unsigned)a.B || (unsigned)task.h >= (unsigned)a.H_kv ||
         (unsigned)task.rb >= (unsigned)a.n_rb || (unsigned)task.c0 >= kAttnMaxCtas || task.c0 + task.n > kAttnMaxCtas)
         return;
-    const int n = task.n, c0 = task.c0;
-    // many parts: groups share a row's parts, about 4 each; where a block has too few groups for that, a worker
-    // takes a quarter of a row
-    const int need = n > kSerial ? (n + 3) / 4 : 1;
-    const int split = JT / (a.D / 4) < need && a.D % 16 == 0 ? 4 : 1;
-    const int ng = a.D / 4 / split, groups = JT / ng, grp = tid % ng, g = tid / ng;
+    const int n = task.n;
+    const int sf = (int)a.slot_floats;  // 2 kAttnMaxCtas of them fit 31 bits
+    const float* slots = slot_ptr(a, 2 * task.c0);
     const int r0 = task.rb * a.rb_rows, nr = block_rows(a, task.rb);
-    const int workers = (n - 1) * gridDim.y, worker = (c - c0 - 1) * gridDim.y + blockIdx.y;
-    const int share = need < groups ? need : groups;  // groups on one row
-    const int at_once = groups / share, sub = g % share;
-    for (int first = worker * at_once; first < nr * split; first += workers * at_once) {
-        const int rq = first + g / share, r = rq / split, d = ((rq - r * split) * ng + grp) * 4;
-        const bool mine = g < at_once * share && rq < nr * split;  // whole shares only
+    // 2^log_share groups on one row: about 4 parts each where there are many
+    const int log_share = n > kSerial ? min(log_groups, 32 - __clz((n - 1) >> 2)) : 0;
+    const int sub = g & ((1 << log_share) - 1), at_once = 1 << (log_groups - log_share);
+    const int step = (n - 1) * gridDim.y * at_once;
+    for (int first = ((c - task.c0 - 1) * gridDim.y + blockIdx.y) * at_once; first < nr << log_split; first += step) {
+        const int rq = first + (g >> log_share), r = rq >> log_split;
+        const int d = ((rq - (r << log_split)) * ng + threadIdx.x) * 4;
+        const bool mine = r < nr, writes = mine && sub == 0;
+        const int64_t row = writes ? row_index(a, task.b, task.h, r0 + r) : 0, at = row * a.D + d;
+        Raw gate{};
+        if (writes && a.gate != nullptr) gate = *reinterpret_cast<const Raw*>(static_cast<const T*>(a.gate) + at);
         Running run;
         if (mine) {
-            constexpr int U = 4;
-            for (int i = sub; i < n; i += U * share) {
+#pragma unroll 1
+            for (int i = sub; i < n; i += U << log_share) {
                 float m[U], l[U];
                 float4 x[U];
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
-                    const int part = i + k * share;
+                    const int part = i + (k << log_share);
+                    m[k] = -INFINITY;
+                    l[k] = 0.f;
+                    x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (part < n) {
-                        const float* slot = slot_ptr(a, 2 * (c0 + part) + (part == 0 ? 1 : 0));
+                        const float* slot = slots + (part == 0 ? 1 : 2 * part) * sf;
                         m[k] = slot[r];
                         l[k] = slot[a.rb_rows + r];
                         x[k] = *reinterpret_cast<const float4*>(slot + a.stat_floats + r * a.D + d);
                     }
                 }
-#pragma unroll
-                for (int k = 0; k < U; ++k)
-                    if (i + k * share < n) run.add(m[k], l[k], x[k]);
+                run.add(m, l, x);
             }
         }
-        if (share > 1) {
+        if (log_share > 0) {
             o_s[tid] = run.o;
             ml_s[tid] = make_float2(run.m, run.l);
             __syncthreads();
-            if (mine && sub == 0)
-                for (int i = 1; i < share; ++i) run.add(ml_s[tid + i * ng].x, ml_s[tid + i * ng].y, o_s[tid + i * ng]);
+            if (writes)
+#pragma unroll 1
+                for (int i = 1; i < 1 << log_share; ++i) {
+                    const float m[1] = {ml_s[tid + i * ng].x}, l[1] = {ml_s[tid + i * ng].y};
+                    const float4 x[1] = {o_s[tid + i * ng]};
+                    run.add(m, l, x);
+                }
             __syncthreads();
         }
-        if (mine && sub == 0) {
-            const int64_t row = row_index(a, task.b, task.h, r0 + r);
-            const int64_t at = row * a.D + d;
-            const float inv = run.l == 0.f ? 0.f : 1.0f / run.l;
-            float y[4] = {run.o.x * inv, run.o.y * inv, run.o.z * inv, run.o.w * inv};
+        if (writes) {
+            const float inv = inverse<T>(run.l);
+            float4 y = make_float4(run.o.x * inv, run.o.y * inv, run.o.z * inv, run.o.w * inv);
             if (a.gate != nullptr) {
-                float gt[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) gt[k] = to_f(static_cast<const T*>(a.gate)[at + k]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] *= sigmoid_f(gt[k]);
+                const float4 gt = as_f32(gate);
+                y.x *= gate_of<T>(gt.x); y.y *= gate_of<T>(gt.y); y.z *= gate_of<T>(gt.z); y.w *= gate_of<T>(gt.w);
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) static_cast<T*>(a.out)[at + k] = from_f<T>(y[k]);
+            store4(static_cast<T*>(a.out) + at, y);
             if (d == 0 && a.lse != nullptr) a.lse[row] = run.l == 0.f ? -INFINITY : (run.m + log2f(run.l)) * kLn2;
         }
     }
@@ -430,9 +460,17 @@ cudaError_t launch_ffma_rows(const AttnArgs& a, int n_cta, cudaStream_t s) {
 
 cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaStream_t s) {
     if (n_cta <= 1) return cudaSuccess;
-    const dim3 grid((unsigned)(n_cta - 1), (unsigned)((a.rb_rows + 15) / 16));
-    return dt == GDN_BF16 ? launch_pdl(attn_join_kernel<bf16>, grid, dim3(JT), 0, s, a)
-                          : launch_pdl(attn_join_kernel<float>, grid, dim3(JT), 0, s, a);
+    // fewer items than a quarter of the CTAs: many parts each
+    const int log_split = a.D % 16 == 0 && (int64_t)a.B * a.H_kv * a.n_rb * 4 < n_cta ? 2 : 0;
+    const int ng = (a.D / 4) >> log_split;
+    int log_groups = 0;
+    while ((2 << log_groups) * ng <= JT) ++log_groups;
+    // enough blocks that an item of two parts takes one pass (5 new tokens, 40 rows: 114 us with a block per 16 rows,
+    // 110 so); items of many parts have many blocks anyhow
+    const int y = log_split != 0 ? (a.rb_rows + 15) / 16 : (a.rb_rows + (1 << log_groups) - 1) >> log_groups;
+    const dim3 grid((unsigned)(n_cta - 1), (unsigned)y), block((unsigned)ng, 1u << log_groups);
+    return dt == GDN_BF16 ? launch_pdl(attn_join_kernel<bf16>, grid, block, 0, s, a, log_groups, log_split)
+                          : launch_pdl(attn_join_kernel<float>, grid, block, 0, s, a, log_groups, log_split);
 }
 
 cudaError_t launch_attn_ffma(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaStream_t s) {
