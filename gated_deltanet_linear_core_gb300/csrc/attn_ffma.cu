@@ -466,8 +466,8 @@ cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaS
     int log_groups = 0;
     while ((2 << log_groups) * ng <= JT) ++log_groups;
     // enough blocks that an item of two parts takes one pass (5 new tokens, 40 rows: 114 us with a block per 16 rows,
-    // 110 so); items of many parts have many blocks anyhow
-    const int y = log_split != 0 ? (a.rb_rows + 15) / 16 : (a.rb_rows + (1 << log_groups) - 1) >> log_groups;
+    // 110 so; one of 201 tokens 11.1 and 9.7)
+    const int y = ((a.rb_rows << log_split) + (1 << log_groups) - 1) >> log_groups;
     const dim3 grid((unsigned)(n_cta - 1), (unsigned)y), block((unsigned)ng, 1u << log_groups);
     return dt == GDN_BF16 ? launch_pdl(attn_join_kernel<bf16>, grid, block, 0, s, a, log_groups, log_split)
                           : launch_pdl(attn_join_kernel<float>, grid, block, 0, s, a, log_groups, log_split);
