@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(Ffma<E, R, NV>::NT, 1) attn_ffma_kernel(AttnAr
 // A block runs its code once, so fetching instructions is what it waits for: block
 // shapes are powers of two in place of divisions, and bf16 takes the approximate
 // exponential and quotient, far below the step of its rounding (16 sequences with
-// 16 new tokens 83 -> 79 us; one of 201 tokens 12.2 -> 9.7).
+// 16 new tokens 83 -> 79 us; one of 201 tokens 12.2 -> 10.2).
 constexpr int JT = 256;
 constexpr int kSerial = 8;
 struct Running {
@@ -466,7 +466,7 @@ cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaS
     int log_groups = 0;
     while ((2 << log_groups) * ng <= JT) ++log_groups;
     // enough blocks that an item of two parts takes one pass (5 new tokens, 40 rows: 114 us with a block per 16 rows,
-    // 110 so; one of 201 tokens 11.1 and 9.7)
+    // 110 so; one of 201 tokens 11.1 and 10.2)
     const int y = ((a.rb_rows << log_split) + (1 << log_groups) - 1) >> log_groups;
     const dim3 grid((unsigned)(n_cta - 1), (unsigned)y), block((unsigned)ng, 1u << log_groups);
     return dt == GDN_BF16 ? launch_pdl(attn_join_kernel<bf16>, grid, block, 0, s, a, log_groups, log_split)
