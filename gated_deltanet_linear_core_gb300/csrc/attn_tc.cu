@@ -784,6 +784,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 #pragma unroll 1
                     for (int db = 0; db < NDB; ++db) {
                         const int k = sl0 + L::v_slot(j - s.tile0, s.tile1 - s.tile0) + db;
+                        // until the slot's load is issued its barrier's parity speaks of the load before last: in a tile
+                        // that is not the segment's last, the slot may still be taking in the load before (17 to 128
+                        // rows of head dims above 128)
+                        live = __all_sync(0xffffffffu, live && loaded_or_abort(&filled[k % NS], k + 1, abort_flag));
                         wait(&full[k % NS], k / NS);
                         const int slabs = nslab - 2 * db < 2 ? nslab - 2 * db : 2;
                         for (int e = st; e < (upto - from) * slabs * 8; e += NSOFT) {

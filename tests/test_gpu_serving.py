@@ -118,6 +118,57 @@ def test_a_non_finite_value_reaches_the_rows_that_see_it(dtype):
         assert torch.equal(hit, want)
 
 
+# K new tokens that lie on both sides of a border of 128 tokens, in sequences of several tiles, several per
+# SM: 24, 40, 64 and 128 rows per key-value head
+STRADDLING = [(3, 16, 2, 256, 8), (3, 16, 2, 256, 64), (5, 16, 2, 256, 16), (5, 16, 2, 256, 64), (8, 16, 2, 200, 64),
+              (16, 16, 2, 256, 8), (16, 16, 2, 256, 64), (16, 32, 4, 128, 16)]
+
+
+def straddling_inputs(K, hq, hkv, D, page, dtype):
+    lens = [128 * (3 + b % 4) + 1 + b // 4 % (K - 1) for b in range(120)]
+    return lens, attn_inputs(lens, K, hq, hkv, D, page, dtype, 700 + K + page)
+
+
+def new_token(table, lens, K, i, page):
+    """Page and place in it of every sequence's new token i."""
+    pos = torch.tensor(lens, device="cuda") - (K - i)
+    return table[torch.arange(len(lens), device="cuda"), pos // page].long(), pos % page
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("K,hq,hkv,D,page", STRADDLING)
+def test_new_tokens_across_a_tile_border_do_not_reach_the_rows_before_them(K, hq, hkv, D, page, dtype):
+    lens, (q, kc, vc, table, ln, _) = straddling_inputs(K, hq, hkv, D, page, dtype)
+    for i in range(1, K) if K <= 5 else (1, 2, K // 2, K - 1):
+        pg, at = new_token(table, lens, K, i, page)
+        old = kc[pg, :, at].clone(), vc[pg, :, at].clone()
+        got = []
+        for bad in (0.0, NAN, INF, -INF):
+            kc[pg, :, at] = bad
+            vc[pg, :, at] = bad
+            got.append([t[:, :i].clone() for t in run_attn((q, kc, vc, table, ln, None))])
+        for out, lse in got[1:]:
+            assert torch.equal(got[0][0], out) and torch.equal(got[0][1], lse), f"token {i}"
+        kc[pg, :, at], vc[pg, :, at] = old
+    gdn.gdn_sync_status()
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("K,hq,hkv,D,page", STRADDLING)
+def test_a_value_across_a_tile_border_reaches_the_rows_that_see_it(K, hq, hkv, D, page, dtype):
+    lens, (q, kc, vc, table, ln, _) = straddling_inputs(K, hq, hkv, D, page, dtype)
+    for i in range(K) if K <= 5 else (0, 1, K // 2, K - 1):
+        pg, at = new_token(table, lens, K, i, page)
+        old = vc[pg, 1, at].clone()
+        vc[pg, 1, at, 77] = -INF
+        hit = torch.isneginf(gdn.gdn_attn_decode(q, kc, vc, table, ln))
+        want = torch.zeros_like(hit)
+        want[:, i:, hq // hkv:2 * (hq // hkv), 77] = True
+        assert torch.equal(hit, want), f"token {i}"
+        vc[pg, 1, at] = old
+    check((q, kc, vc, table, ln, None), dtype)
+
+
 @pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
 def test_scale_and_peaked_scores(dtype):
     x = attn_inputs([700, 90], 2, 8, 2, 128, 16, dtype, 21)
