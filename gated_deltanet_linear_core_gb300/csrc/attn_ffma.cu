@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(Ffma<E, R, NV>::NT, 1) attn_ffma_kernel(AttnAr
                 const int64_t row = row_index(a, s.b, s.h, r0 + r);
                 const float inv = sum == 0.f ? 0.f : 1.0f / sum;
                 y.x *= inv; y.y *= inv; y.z *= inv; y.w *= inv;
-                if (a.gate != nullptr) {
+                if (a.gate != nullptr && sum != 0.f) {  // a row that sees nothing is 0 whatever its gate holds
                     const float4 g = ld4(static_cast<const E*>(a.gate) + row * D + d);
                     y.x *= sigmoid_f(g.x); y.y *= sigmoid_f(g.y); y.z *= sigmoid_f(g.z); y.w *= sigmoid_f(g.w);
                 }
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a, int log_group
         if (writes) {
             const float inv = inverse<T>(run.l);
             float4 y = make_float4(run.o.x * inv, run.o.y * inv, run.o.z * inv, run.o.w * inv);
-            if (a.gate != nullptr) {
+            if (a.gate != nullptr && run.l != 0.f) {
                 const float4 gt = as_f32(gate);
                 y.x *= gate_of<T>(gt.x); y.y *= gate_of<T>(gt.y); y.z *= gate_of<T>(gt.z); y.w *= gate_of<T>(gt.w);
             }

@@ -640,12 +640,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         const int64_t at = out_row(r) * a.D + d;
                         float y[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w}, gt[8];
                         const float inv = f_s[r];
+                        const bool gates = gated && inv != 0.f;  // a row that sees nothing is 0 whatever its gate holds
                         unpack16<bf16>(gv, gt);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             y[i] *= inv;
                             // the approximate exponential and quotient: far below the step of bf16
-                            if (gated) y[i] *= __fdividef(1.0f, 1.0f + __expf(-gt[i]));
+                            if (gates) y[i] *= __fdividef(1.0f, 1.0f + __expf(-gt[i]));
                         }
                         store16<bf16>(static_cast<bf16*>(a.out) + at, y);
                     } else {

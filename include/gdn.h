@@ -526,7 +526,7 @@ gdn_status_t gdn_kv_append(const void* k, const void* v, void* k_cache, void* v_
  * key-value head h / (H_q / H_kv):
  *   s_t = scale q . k_t,  out = sum_{t<n} e^{s_t} v_t / sum_{t<n} e^{s_t}
  *   [* sigmoid(gate)],    lse = log sum_{t<n} e^{s_t}
- * and with n <= 0: out = 0, lse = -inf.  What hidden positions hold, NaN and
+ * and with n <= 0: out = 0 (whatever gate holds), lse = -inf.  What hidden positions hold, NaN and
  * infinities included, does not matter.
  *   q          (device) [B, K, H_q, D] dtype;  H_q a multiple of H_kv
  *   scale      0 means D^-1/2, else positive

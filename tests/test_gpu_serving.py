@@ -169,6 +169,21 @@ def test_a_value_across_a_tile_border_reaches_the_rows_that_see_it(K, hq, hkv, D
     check((q, kc, vc, table, ln, None), dtype)
 
 
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_rows_that_see_nothing_are_zero_whatever_their_gate_holds(dtype, bad):
+    """Padding rows: out 0 and lse -inf, in sequences without a token and in those with fewer than the new ones."""
+    for lens, K, hq, hkv, D, page in [([0, 3, 1, 700, 2], 5, 16, 2, 256, 16), ([3], 8, 4, 1, 64, 16),
+                                      ([2, 0], 16, 16, 2, 128, 64), ([1, 2, 0], 3, 4, 2, 72, 7)]:
+        x = attn_inputs(lens, K, hq, hkv, D, page, dtype, 23, gate=True)
+        seen = torch.tensor([[n - (K - 1 - i) > 0 for i in range(K)] for n in lens], device="cuda")
+        want, lse0 = check(x, dtype)
+        x[5][~seen] = bad
+        out, lse = run_attn(x)
+        assert torch.equal(out, want) and torch.equal(lse, lse0)
+        assert (out[~seen] == 0).all() and torch.isneginf(lse[~seen]).all()
+
+
 @pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
 def test_scale_and_peaked_scores(dtype):
     x = attn_inputs([700, 90], 2, 8, 2, 128, 16, dtype, 21)
