@@ -63,10 +63,12 @@ __device__ __forceinline__ Sum2 operator+(Sum2 a, Sum2 b) {
     return a.folded();
 }
 __device__ __forceinline__ bool operator>(Sum2 a, Sum2 b) { return (a.s - b.s) + (a.c - b.c) > 0.f; }
+// Rounded down: sums of subnormal values are multiples of the smallest step, and a border between two
+// of them must not end on the upper one (a sum above it would not pass it, nor the whole sum).
 __device__ __forceinline__ Sum2 operator*(float u, Sum2 a) {
     Sum2 r;
-    r.s = __fmul_rn(u, a.s);
-    r.c = fmaf(u, a.c, fmaf(u, a.s, -r.s));
+    r.s = __fmul_rd(u, a.s);
+    r.c = __fmaf_rd(u, a.c, __fmaf_rd(u, a.s, -r.s));
     return r.folded();
 }
 __device__ __forceinline__ Sum2 shfl(Sum2 x, int lane) {

@@ -432,6 +432,30 @@ def test_acceptance_without_weight():
     assert ((t >= -1) & (t < V)).all() and ((n >= 0) & (n <= 2)).all()
 
 
+def test_acceptance_of_the_smallest_probabilities():
+    """Rows of subnormal values, whose sums times a uniform fall between two of them: the token is picked all the
+    same, as the definition in 64 bits has it."""
+    V = 3001
+    g = torch.Generator().manual_seed(14)
+    us = [0.0, 0.3, 0.4999, 0.5, 0.5001, 0.9, 0.999, 1 - 2.0 ** -24]
+    tiny = 2.0 ** -149
+    for steps in (1, 3, 40, 1 << 14):  # values of 0 to this many smallest steps
+        few = torch.randint(0, V, (len(us), 3), generator=g)
+        p = torch.zeros((len(us), 2, V))
+        p[:, 0] = (torch.randint(0, steps + 1, (len(us), V), generator=g).double() * tiny).float()
+        p[:, 1].scatter_(1, few, steps * tiny)
+        assert (p[:, 1] > 0).any(-1).all()
+        u = torch.tensor(us).view(-1, 1).repeat(1, 2)
+        draft = few[:, :1].to(torch.int32)
+        none = torch.zeros((len(us), 0), dtype=torch.int32)
+        for row in (0, 1):
+            check_accept(p[:, row:row + 1].contiguous(), None, none, u[:, :1].contiguous())
+        check_accept(p, None, draft, u)
+        q = p[:, :1] * 0.5  # what is left over after the draft fails is smaller still
+        q.scatter_(2, draft.long().view(-1, 1, 1), 1.0)
+        check_accept(p, q, draft, u)
+
+
 def test_acceptance_does_not_depend_on_the_split_of_a_row():
     """Values over many magnitudes: the running sums keep what f32 would lose."""
     V = 50000
