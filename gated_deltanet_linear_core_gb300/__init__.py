@@ -560,11 +560,14 @@ def _on_stream(dev, stream, used, body):
     in use there, so that a caller may drop them at once."""
     if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+        raise ValueError(f"stream: on {stream.device}, the tensors are on cuda:{dev}")
     with torch.cuda.device(dev):
         if stream is None:
             return body()
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), dev) if int(stream) else torch.cuda.default_stream(dev)
+        if not isinstance(stream, torch.cuda.Stream):
+            raw = int(getattr(stream, "cuda_stream", stream))
+            stream = torch.cuda.ExternalStream(raw, dev) if raw else torch.cuda.default_stream(dev)
         with torch.cuda.stream(stream):
             res = body()
         for t in used:

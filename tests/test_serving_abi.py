@@ -108,3 +108,15 @@ def test_binding_refuses_host_tensors():
         gdn.gdn_kv_append(z[0], z[0], c, c, i, i[:, 0])
     with pytest.raises(ValueError, match="CUDA"):
         gdn.gdn_draft_accept(torch.zeros((1, 2, 9)), None, torch.zeros((1, 1), dtype=torch.int32), torch.zeros((1, 2)))
+
+
+def test_binding_refuses_a_stream_of_another_device(monkeypatch):
+    """It would run on the tensors' device's current stream, not on the one named."""
+    class Stream:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0x1234
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    ran = []
+    with pytest.raises(ValueError, match="stream: on cuda:1, the tensors are on cuda:0"):
+        gdn._on_stream(0, Stream(), (), lambda: ran.append(1))
+    assert not ran
