@@ -92,7 +92,7 @@ struct Layout {
     static constexpr int T_COLS = T_USED <= 64 ? 64 : T_USED <= 128 ? 128 : T_USED <= 256 ? 256 : 512;
     static_assert(N * 512 <= P_BYTES, "output rows");
     static_assert(SMEM <= kSmemMax && NS >= 3, "shared memory");
-    static_assert(30 * 8 + 6 * 4 <= BARS, "barriers");
+    static_assert(35 * 8 <= BARS, "barriers");
 
     // byte offset of P's column block (16-byte chunk j of 8 columns) of token t
     __device__ static __forceinline__ uint32_t p_off(int buf, int lo, int chunk, int t) {
@@ -250,6 +250,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 28);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     volatile int* filled = reinterpret_cast<volatile int*>(bars + 30);  // [6] one more than the last position loaded into a slot
+    uint64_t* drained = bars + 34;    // every MMA issued is done (abort)
     volatile int* odd_v = reinterpret_cast<volatile int*>(tslot + 2);  // a new token's value is not finite
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -266,6 +267,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
+        mbar_init(drained, 1);
         for (int i = 0; i < L::SEGS; ++i) {
             mbar_init(&seg_full[i], 1);
             mbar_init(&seg_empty[i], 2 + L::NSW);
@@ -383,8 +385,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             const uint32_t base = smem_u32(sm);
             const int ksteps = (a.D + 15) / 16;
             int it = 0, seg = 0, sl0 = 0;  // tiles, segments and slots before
-            uint64_t* last = nullptr;      // the last commit, for the drain on abort
-            uint32_t last_parity = 0;
             // the issue loops are unrolled and step the descriptors by constants (their address field counts 16
             // bytes): with descriptors built per MMA, one thread's issue rate, 60 ns each, was the tile's bound
             auto slot_full = [&](int k) { return wait_or_abort(&full[k % NS], (uint32_t)((k / NS) & 1), abort_flag); };
@@ -405,8 +405,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     mma_commit(&empty[k % NS]);
                 }
                 mma_commit(&s_full[t & 1]);
-                last = &s_full[t & 1];
-                last_parity = (uint32_t)((t >> 1) & 1);
                 return true;
             };
             bool ok = true;
@@ -420,6 +418,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     if (j + 1 < n && !issue_s(it + (j < 0 ? 0 : 1), sl0 + L::k_slot(j + 1))) { ok = false; break; }
                     if (j + 2 == n) mma_commit(q_empty);
                     if (j < 0) continue;
+                    ok = it != a.stop_at;
+                    if (!ok) break;
                     ok = wait_or_abort(&p_full[it & 1], (uint32_t)((it >> 1) & 1), abort_flag);
                     if (!ok) break;
                     const int left = s.len - (s.tile0 + j) * TILE;
@@ -443,13 +443,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     }
                     if (!ok) break;
                     mma_commit(&pv_done[it & 1]);
-                    last = &pv_done[it & 1];
-                    last_parity = (uint32_t)((it >> 1) & 1);
                     ++it;
                 }
                 sl0 += 2 * NDB * n;
             }
-            if (*abort_flag && last != nullptr) mbar_wait(last, last_parity, kWaitNs);
+            if (!ok) {  // MMAs that no commit above speaks of are waited for too
+                mma_commit(drained);
+                mbar_wait(drained, 0, kWaitNs);
+            }
         }
     } else if (warp == 2) {
         // ------------------------------------------------ Q rows (zero beyond the block's rows and the head's dims), V

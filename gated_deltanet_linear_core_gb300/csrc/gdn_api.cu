@@ -93,7 +93,7 @@ const char* gdn_status_string(gdn_status_t s) {
 
 int gdn_last_cuda_error(void) { return g_last_cuda_error; }
 
-int gdn_version(void) { return (1 << 16) | 1; }
+int gdn_version(void) { return (1 << 16) | 2; }
 
 int64_t gdn_ckpt_count(const int32_t* cu, int32_t n_seq, int32_t every) {
     if (cu == nullptr || n_seq < 1 || every < 0) return -1;
@@ -640,7 +640,34 @@ gdn_status_t fill_attn(gdn::AttnArgs& a, int32_t B, int32_t K, int32_t H_q, int3
     if (H_q > 65536) return GDN_ERR_UNSUPPORTED;
     a.B = B; a.K = K; a.H_q = H_q; a.H_kv = H_kv; a.D = D;
     a.page_size = page_size; a.n_pages = n_pages; a.max_pages = max_pages;
+    a.stop_at = -1;
     return GDN_OK;
+}
+
+gdn_status_t attn_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                         const int32_t* seq_lens, float scale, const void* gate, void* out, float* lse, int32_t B,
+                         int32_t K, int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size, int32_t n_pages,
+                         int32_t max_pages, void* workspace, size_t ws_bytes, gdn_dtype_t dtype, int32_t stop_at,
+                         void* stream) {
+    gdn::AttnArgs a;
+    const gdn_status_t st = fill_attn(a, B, K, H_q, H_kv, D, page_size, n_pages, max_pages, dtype);
+    if (st != GDN_OK) return st;
+    if (!isfinite(scale) || scale < 0.f) return GDN_ERR_INVALID_ARG;
+    if (B == 0 || K == 0) return GDN_OK;
+    if (q == nullptr || k_cache == nullptr || v_cache == nullptr || page_table == nullptr || seq_lens == nullptr ||
+        out == nullptr)
+        return GDN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned_n(page_table, 4) ||
+        !aligned_n(seq_lens, 4) || !aligned16(gate) || !aligned16(out) || !aligned_n(lse, 4) || !aligned16(workspace))
+        return GDN_ERR_ALIGN;
+    a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.table = page_table; a.lens = seq_lens;
+    a.gate = gate; a.out = out; a.lse = lse;
+    a.ws = static_cast<float*>(workspace);
+    a.stop_at = stop_at;
+    a.scale_log2 = (scale == 0.f ? 1.0f / sqrtf((float)D) : scale) * 1.4426950408889634f;
+    const size_t need = gdn::attn_plan(a, dtype);
+    if (workspace == nullptr || ws_bytes < need) return GDN_ERR_WORKSPACE;
+    return cuda_status(gdn::launch_attn_decode(a, dtype, (cudaStream_t)stream));
 }
 }  // namespace
 
@@ -680,24 +707,19 @@ gdn_status_t gdn_attn_decode(const void* q, const void* k_cache, const void* v_c
                              int32_t B, int32_t K, int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size,
                              int32_t n_pages, int32_t max_pages, void* workspace, size_t ws_bytes,
                              gdn_dtype_t dtype, void* stream) {
-    gdn::AttnArgs a;
-    const gdn_status_t st = fill_attn(a, B, K, H_q, H_kv, D, page_size, n_pages, max_pages, dtype);
-    if (st != GDN_OK) return st;
-    if (!isfinite(scale) || scale < 0.f) return GDN_ERR_INVALID_ARG;
-    if (B == 0 || K == 0) return GDN_OK;
-    if (q == nullptr || k_cache == nullptr || v_cache == nullptr || page_table == nullptr || seq_lens == nullptr ||
-        out == nullptr)
-        return GDN_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned_n(page_table, 4) ||
-        !aligned_n(seq_lens, 4) || !aligned16(gate) || !aligned16(out) || !aligned_n(lse, 4) || !aligned16(workspace))
-        return GDN_ERR_ALIGN;
-    a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.table = page_table; a.lens = seq_lens;
-    a.gate = gate; a.out = out; a.lse = lse;
-    a.ws = static_cast<float*>(workspace);
-    a.scale_log2 = (scale == 0.f ? 1.0f / sqrtf((float)D) : scale) * 1.4426950408889634f;
-    const size_t need = gdn::attn_plan(a, dtype);
-    if (workspace == nullptr || ws_bytes < need) return GDN_ERR_WORKSPACE;
-    return cuda_status(gdn::launch_attn_decode(a, dtype, (cudaStream_t)stream));
+    return attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale, gate, out, lse, B, K, H_q, H_kv, D, page_size,
+                       n_pages, max_pages, workspace, ws_bytes, dtype, -1, stream);
+}
+
+gdn_status_t gdn_selftest_attn_decode(const void* q, const void* k_cache, const void* v_cache,
+                                      const int32_t* page_table, const int32_t* seq_lens, void* out, int32_t B,
+                                      int32_t K, int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size,
+                                      int32_t n_pages, int32_t max_pages, void* workspace, size_t ws_bytes,
+                                      int32_t stop_at, void* stream) {
+    if (stop_at < 0) return GDN_ERR_INVALID_ARG;
+    if (page_size % 4 != 0) return GDN_ERR_UNSUPPORTED;  // the CUDA-core kernel waits for nothing
+    return attn_decode(q, k_cache, v_cache, page_table, seq_lens, 0.f, nullptr, out, nullptr, B, K, H_q, H_kv, D,
+                       page_size, n_pages, max_pages, workspace, ws_bytes, GDN_BF16, stop_at, stream);
 }
 
 gdn_status_t gdn_draft_accept(const void* p, const void* q, const int32_t* draft, const float* u,

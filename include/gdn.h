@@ -235,6 +235,19 @@ gdn_status_t gdn_layer_prefill_host(const void* h_qkv, const void* h_z, const vo
 gdn_status_t gdn_selftest_bounded_wait(int64_t limit_ns, void* stream);
 
 /*
+ * The same for the attention over the paged cache (bf16, page_size a multiple of
+ * 4; arguments as for gdn_attn_decode): the CTAs' MMAs stop at their tile number
+ * stop_at >= 0, so the waits of the other warps run out after 1 s, they finish
+ * without waiting, and the device error word is set.  `out` is then undefined.  A
+ * call of which no CTA has that many tiles runs as usual.
+ */
+gdn_status_t gdn_selftest_attn_decode(const void* q, const void* k_cache, const void* v_cache,
+                                      const int32_t* page_table, const int32_t* seq_lens, void* out, int32_t B,
+                                      int32_t K, int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size,
+                                      int32_t n_pages, int32_t max_pages, void* workspace, size_t ws_bytes,
+                                      int32_t stop_at, void* stream);
+
+/*
  * Number of kernel launches one gdn_chunk_prefill call with these sizes and
  * flags issues (for profiling and launch accounting; the library has no paper
  * counterpart for it): on the tensor-core path, a chunk-offsets kernel when

@@ -545,6 +545,37 @@ def test_two_calls_at_once():
             assert torch.equal(w[0], g[0]) and torch.equal(w[1], g[1])
 
 
+# ------------------------------------------------------------------ a wait that runs out
+@pytest.mark.parametrize("stop_at", [0, 1, 4])
+@pytest.mark.parametrize("K,hq,hkv,D,page", [(1, 16, 2, 256, 16), (5, 16, 2, 256, 64), (16, 16, 2, 256, 16),
+                                             (16, 32, 4, 128, 64)])
+def test_waits_that_run_out_are_reported_and_the_next_call_is_right(K, hq, hkv, D, page, stop_at):
+    """The MMAs of every CTA that has so many tiles stop: the call returns, gdn_sync_status reports it once,
+    and the context goes on."""
+    lens = [900 + 17 * b for b in range(90)]
+    x = attn_inputs(lens, K, hq, hkv, D, page, BF, 65)
+    q, kc, vc, table, ln, _ = x
+    want, _ = run_attn(x)
+    gdn.gdn_sync_status()
+    lib, out = gdn._lib.load(), torch.empty_like(q)
+    ws = torch.zeros(gdn.gdn_attn_decode_workspace_size(len(lens), K, hq, hkv, D, page, BF), dtype=torch.uint8,
+                     device="cuda")
+
+    def stopped(at):
+        return lib.gdn_selftest_attn_decode(q.data_ptr(), kc.data_ptr(), vc.data_ptr(), table.data_ptr(), ln.data_ptr(),
+                                            out.data_ptr(), len(lens), K, hq, hkv, D, page, kc.shape[0], table.shape[1],
+                                            ws.data_ptr(), ws.numel(), at, torch.cuda.current_stream().cuda_stream)
+
+    assert stopped(stop_at) == 0
+    with pytest.raises(gdn.GDNError, match="TIMEOUT"):
+        gdn.gdn_sync_status()
+    gdn.gdn_sync_status()  # cleared
+    assert stopped(10 ** 6) == 0  # no CTA has that many
+    gdn.gdn_sync_status()
+    assert torch.equal(out, want)
+    assert torch.equal(run_attn(x)[0], want)
+
+
 # ------------------------------------------------------------------ refusals
 def test_refusals():
     q, kc, vc, table, ln, _ = attn_inputs([64, 64], 2, 4, 2, 128, 16, BF, 70)

@@ -47,6 +47,15 @@ def test_attention_refusals(lib):
     assert attn(lib, B=0) == E.GDN_OK and attn(lib, K=0, q=None) == E.GDN_OK
 
 
+@no_gpu
+def test_selftest_refusals(lib):
+    def call(stop_at, page, ws):
+        return lib.gdn_selftest_attn_decode(A, A, A, A, A, A, 2, 1, 16, 2, 256, page, 100, 50, ws, 1 << 40, stop_at, None)
+    assert call(-1, 16, A) == E.GDN_ERR_INVALID_ARG
+    assert call(0, 6, A) == E.GDN_ERR_UNSUPPORTED
+    assert call(0, 16, None) == E.GDN_ERR_WORKSPACE
+
+
 def test_workspace_sizes(lib):
     f = gdn.gdn_attn_decode_workspace_size
     assert f(0, 1, 16, 2, 256, 16, torch.bfloat16) == 0 and f(1, 17, 16, 2, 256, 16, torch.bfloat16) == 0
