@@ -95,6 +95,27 @@ def check_attention(out, lse, ref, dtype):
             assert bool((e <= lim).all()), f"lse off by {e.max().item():.2e}"
 
 
+def weight_error(q, k_cache, table, lens, scale=None):
+    """[B, K, H_q] f64: by how much a weight of a row may be off, relatively, where nothing is held in fewer
+    than 32 bits; the log of a row's sum may then be off by as much.
+
+    The score's error as in attention(); five exponentials of 2^-21 each that multiply into a weight (its own,
+    one move of the running maximum, and the joins of warps, of groups of parts and of parts); the sum over
+    tiles at most (n / 128 + 256) 2^-24."""
+    B, K, hq, D = q.shape
+    hkv, page = k_cache.shape[1:3]
+    G = hq // hkv
+    scale = D ** -0.5 if scale is None else scale
+    err = torch.zeros((B, K, hq), dtype=torch.float64, device=q.device)
+    for b, n in enumerate(lens.tolist()):
+        ids = table[b, :-(-n // page)].long()
+        for h in range(hkv):
+            far = k_cache[ids, h].reshape(-1, D)[:n].double().norm(dim=-1).max()
+            d_s = (D + 2) * EPS_F32 * scale * q[b, :, h * G:(h + 1) * G].double().norm(dim=-1) * far
+            err[b, :, h * G:(h + 1) * G] = d_s + 5 * 2.0 ** -21 + (n / 128 + 256) * EPS_F32
+    return err
+
+
 def append(k, v, k_cache, v_cache, table, lens, cu):
     """Token by token; returns new caches."""
     kc, vc = k_cache.clone(), v_cache.clone()

@@ -218,6 +218,45 @@ def test_scores_far_below_the_others_change_nothing(dtype, low):
         ref.check_attention(out, lse, ref.attention(q, kc, vc, others, ln - (hi - lo)), dtype)
 
 
+# lengths, K, H_q, H_kv, D, page, gate
+DIGITS = [([5000], 1, 16, 2, 256, 64, True), ([3000, 2501, 1201], 5, 16, 2, 256, 16, True),
+          ([900 + b for b in range(40)], 1, 4, 4, 16, 32, False), ([20000], 1, 8, 1, 64, 16, False),
+          ([2500, 1111], 16, 16, 2, 128, 8, True), ([1500] * 8, 2, 6, 2, 72, 7, False)]
+
+
+@pytest.mark.parametrize("i", range(len(DIGITS)))
+def test_f32_is_held_in_32_bits(i):
+    """Elementwise to the bound without any rounding to fewer bits, and in the mean: the errors of the weights are
+    independent and mostly of 2^-22 or less (scores, exponentials), so rel-L2 stays below 2^-19; weights cut to 16
+    bits would leave 2^-18 (2^-16 of uniform error, less by sqrt(12) in the mean)."""
+    lens, K, hq, hkv, D, page, gate = DIGITS[i]
+    x = attn_inputs(lens, K, hq, hkv, D, page, F, 300 + i, gate)
+    q, kc, vc, table, ln, gt = x
+    out, _ = run_attn(x)
+    r_out, _, _ = ref.attention(q, kc, vc, table, ln, gate=gt)
+    # the largest value of any position in use: pages hold NaN elsewhere
+    top = torch.nan_to_num(vc, nan=0.0).abs().max().double()
+    tol = 2.0 ** -20 * r_out.abs() + 2 * ref.weight_error(q, kc, table, ln).unsqueeze(-1) * top
+    err = (out.double() - r_out).abs()
+    assert bool((err <= tol).all()), f"{(err / tol).max().item():.2f} times its bound off"
+    rel = (err.norm() / r_out.norm()).item()
+    assert rel <= 2.0 ** -19, f"rel-L2 {rel:.2e}"
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("i", range(len(DIGITS)))
+def test_lse_is_held_in_32_bits(i, dtype):
+    """To the error of the weights (sums are f32 whatever the type), and three roundings on the way out."""
+    lens, K, hq, hkv, D, page, _ = DIGITS[i]
+    x = attn_inputs(lens, K, hq, hkv, D, page, dtype, 400 + i)
+    q, kc, vc, table, ln, _ = x
+    _, lse = run_attn(x)
+    _, r_lse, _ = ref.attention(q, kc, vc, table, ln)
+    err = (lse.double() - r_lse).abs()
+    tol = ref.weight_error(q, kc, table, ln) + 2.0 ** -21 * (1 + r_lse.abs())
+    assert bool((err <= tol).all()), f"{(err / tol).max().item():.2f} times its bound off"
+
+
 def test_lengths_and_pages_are_clamped():
     """A length beyond the table, a negative one, and pages that do not exist."""
     x = attn_inputs([64, 64, 64], 1, 4, 2, 128, 16, BF, 3)
