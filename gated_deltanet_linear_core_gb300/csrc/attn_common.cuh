@@ -44,8 +44,7 @@ struct Place {
 };
 
 // Units of the call and the sequence that holds the first unit of CTA c of the
-// n that take part (n is capped so that a CTA has at least min_units), by one
-// warp: a lane adds up a 32nd of the sequences, then the warp searches the lane's
+// n that take part (at most one per unit), by one warp: a lane adds up a 32nd of the sequences, then the warp searches the lane's
 // share that holds the unit.  (A block-wide scan saves loads but costs three
 // barriers, which at the start of a call is longer.)
 __device__ __forceinline__ Place find_place(const AttnArgs& a, int tile, int c, int& n) {
@@ -67,8 +66,7 @@ __device__ __forceinline__ Place find_place(const AttnArgs& a, int tile, int c, 
     p.total = __shfl_sync(0xffffffffu, inc, 31) * mult;
     p.first = 0;
     p.b = p.len = 0;
-    const int64_t most = (p.total + a.min_units - 1) / a.min_units;
-    if (n > most) n = (int)most;
+    if (n > p.total) n = (int)p.total;
     if (c >= n) return p;
     const int64_t want = cta_begin(p.total, c, n);
     const int owner = __ffs(__ballot_sync(0xffffffffu, want < inc * mult)) - 1;

@@ -20,9 +20,9 @@ size_t attn_plan(AttnArgs& a, gdn_dtype_t dt) {
     a.rows = a.K * a.group;
     a.n_rb = (a.rows + most - 1) / most;
     a.rb_rows = (a.rows + a.n_rb - 1) / a.n_rb;
-    a.min_units = 1;
-    // about the tiles that HBM delivers while an item starts and ends (16 ragged sequences with 16 new tokens 100 -> 92 us,
-    // 8 in f32 27 -> 24)
+    // about the tiles that HBM delivers while an item starts and ends, twice as many where they are half as large (us with
+    // 0, without the doubling, and so: 16 ragged sequences with 16 new tokens 87.5, 79.2, 79.9; 8 in f32 27.3, 24.6, 23.4;
+    // 64 with 5 new tokens, head dim 256, 119.1 and 109.3)
     a.setup = (!attn_tc_takes(a, dt) ? 2 : a.rb_rows <= 32 ? 1 : a.rb_rows <= 64 ? 2 : 3) * (a.D <= 128 ? 2 : 1);
     a.stat_floats = (2 * a.rb_rows + 3) & ~3;
     a.slot_floats = a.stat_floats + (int64_t)a.rb_rows * a.D;

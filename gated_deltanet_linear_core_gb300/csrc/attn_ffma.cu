@@ -11,7 +11,9 @@
 // one pass over the tokens with the running maximum m, sum l and output O:
 //   m' = max(m, max s),  l <- l 2^(m-m') + sum 2^(s-m'),  O <- O 2^(m-m') + P V
 // (scores in the log2 domain, all statistics in f32; m is moved only when a
-// score exceeds it by 2^8, so O is rarely rescaled).
+// score exceeds it by 2^8, so O is rarely rescaled).  2^x is the hardware's
+// approximate form throughout, for weights and for the joins' factors, in f32
+// too: within 2^-22, some steps of f32, and 0 below 2^-126.
 //
 // Reading the cache is the bound of few rows (64 ragged sequences of 512 to 8192
 // tokens in f32, 4 rows of head dim 128: 168 us, 6.5 TB/s; 8 rows are bound by

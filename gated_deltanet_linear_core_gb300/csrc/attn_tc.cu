@@ -17,10 +17,12 @@
 // stays below 2^8, harmless in f32 sums), so most tiles need one vote and no
 // rescaling of O.  P is handed to the MMA as two bf16 (the value cut to 8 bits
 // and the rounded rest, 16 bits in all): one bf16 alone would add an error of
-// the size of the output's own rounding.  Up to 64 rows both are columns of one
-// MMA (2 N columns, joined at the end): its time is that of reading V, so the
-// rest is free; two MMAs per step were bound by that (64 rows: 3.2 us per tile
-// of head dim 256 where HBM takes 2.9).  Sums are kept per thread in f32 and joined at the end.
+// the size of the output's own rounding.  Both are columns of one MMA (2 N
+// columns, joined at the end): its time is that of reading V, so the rest is
+// free; two MMAs per step were bound by that (64 rows: 3.2 us per tile of head
+// dim 256 where HBM takes 2.9).  Only 128 rows of head dims above 128 take two,
+// which add up: O in two parts has no room in tensor memory there.
+// Sums are kept per thread in f32 and joined at the end.
 //
 // Warps: 0 walks the CTA's range, tells the others its segments and loads K and V
 // (the walk in every role cost 600 short sequences with 5 new tokens 14 us of 116),
@@ -55,9 +57,9 @@ constexpr int kSmemMax = 232448;
 
 template <int N, int NDB>
 struct Layout {
-    // Columns (rows of Q) per softmax thread and per TMEM access.  More warps with fewer columns hide more, until
-    // registers spill: 128 rows of head dim 256 took 222 us with 16 warps and 267 with 8; of head dim 128, whose O has
-    // both parts of P, 84 with 16 (16 columns at a time; 32 spill: 138) and 83 with 8; 32 rows 165 and 166.
+    // Columns (rows of Q) per softmax thread and per TMEM access, chosen by time: 128 rows of head dim 256 took 222 us
+    // with 16 warps and 267 with 8; of head dim 128, whose O has both parts of P, 84 with 16 (16 columns at a time; 138
+    // with 32, most of whose registers spill) and 83 with 8; 32 rows 165 and 166.  Both forms of 128 rows spill 44 bytes.
     static constexpr int CPT = N <= 32 ? 16 : N == 64 || NDB == 2 ? 32 : 64;
     static constexpr int CH = N == 128 && NDB == 2 ? 16 : CPT < 32 ? CPT : 32;
     static constexpr int NWG = N / CPT;           // softmax warpgroups

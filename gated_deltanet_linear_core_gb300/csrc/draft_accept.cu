@@ -16,8 +16,8 @@
 // Only row n is read (and q's when a draft failed), so a batch is bound by HBM
 // and a single sequence by latency: one cluster of kCluster CTAs per sequence,
 // the row cut into segments of SEG values whose sums stay in shared memory; each
-// CTA writes its total into the shared memory of all, and the warp that owns the
-// segment with the border reads that one again.  A warp takes 16 bytes per lane
+// CTA writes its total into the shared memory of all, and the first warp of the
+// CTA that has the border finds its segment and reads that one again.  A warp takes 16 bytes per lane
 // and load, several loads in flight; rows that do not start on 16 bytes are
 // read value by value in the same order.
 #include <cooperative_groups.h>

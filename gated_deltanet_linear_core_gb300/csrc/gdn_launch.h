@@ -170,7 +170,6 @@ struct AttnArgs {
     int group, rows;       // H_q / H_kv, K * group
     int rb_rows, n_rb;     // rows per row block, row blocks
     int setup;             // units that starting an item counts as, beside its tiles
-    int min_units;         // least units per CTA
     int stop_at;           // self-test: the MMAs stop at a CTA's tile of this number (-1: never)
 };
 constexpr int kAttnMaxK = 16;

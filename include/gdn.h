@@ -570,7 +570,7 @@ gdn_status_t gdn_attn_decode(const void* q, const void* k_cache, const void* v_c
  * f32's precision.  A row r without a positive value falls back to p_n, and to
  * token 0 if that has none.
  *   p          (device) [B, K + 1, V] dtype: the target's probabilities after the
- *              last sampled token and after each draft (finite; need not add up to 1)
+ *              last sampled token and after each draft (finite, as their sum is; need not add up to 1)
  *   q          (device) [B, K, V] dtype: the draft model's, or NULL for drafts that
  *              were not sampled (q_t is 1 at d_t)
  *   draft      (device) [B, K] int32; a token outside [0, V) never holds
