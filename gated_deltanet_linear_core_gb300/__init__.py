@@ -28,7 +28,7 @@ __all__ = [
     "gdn_layer_prefill_host", "gdn_decode_step", "gdn_decode_verify", "gdn_layer_prefill",
     "gdn_layer_prefill_workspace_size", "gdn_layer_prefill_launches", "gdn_chunk_prefill_norm",
     "HeadShard", "head_shard",
-    "gdn_layer_decode", "gdn_kv_append", "gdn_attn_decode", "gdn_attn_decode_workspace_size", "gdn_draft_accept",
+    "gdn_layer_decode", "gdn_kv_append", "gdn_rope", "gdn_rope_kv_append", "gdn_attn_decode", "gdn_attn_decode_workspace_size", "gdn_draft_accept",
     "library_path",
 ]
 
@@ -607,6 +607,110 @@ def gdn_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_seqlens=None,
     if st:
         _lib.check(st, "gdn_kv_append")
     return k_cache, v_cache
+
+
+def _rows(t, name, dev, dtype, T, D, H=None):
+    """Pointer and strides (tokens, heads) of a [T, H, D] tensor on CUDA device number
+    `dev` whose heads' dims are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != D or (H is not None and shape[1] != H):
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [{T}, {'H' if H is None else H}, {D}]")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensors on different devices (cuda:{dev} and {t.device})")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    token, head, dim = t.stride()
+    if dim != 1:
+        raise ValueError(f"{name}: the dims of a head must be contiguous")
+    return t.data_ptr(), token, head
+
+
+def _rotation(inv_freq, positions, axes, T, D, dev):
+    """Checked pointers of a rotation: (positions, n_axes, axes, inv_freq, R)."""
+    if inv_freq.dim() != 1 or not 1 <= inv_freq.shape[0] <= D // 2:
+        raise ValueError(f"inv_freq: shape {tuple(inv_freq.shape)}, expected [R / 2] with 2 <= R <= {D}")
+    half, n_axes = inv_freq.shape[0], 1
+    if positions is not None:
+        if positions.dim() not in (1, 2) or positions.shape[-1] != T:
+            raise ValueError(f"positions: shape {tuple(positions.shape)}, expected [{T}] or [n_axes, {T}]")
+        n_axes = positions.shape[0] if positions.dim() == 2 else 1
+    return (_dptr(positions, "positions", dev, torch.int32), n_axes, _dptr(axes, "axes", dev, torch.int32, (half,)),
+            _dptr(inv_freq, "inv_freq", dev, torch.float32), 2 * half)
+
+
+def gdn_rope(x, inv_freq, positions, axes=None, norm_w=None, norm_eps=RMSNORM_EPS, mscale=1.0, interleaved=False,
+             out=None, stream=None):
+    """Rotary positions of x [T, H, D] (strided between tokens and heads at will, as a
+    slice of a fused projection is): the pairs (j, j + R/2) of a head's first R dims,
+    with interleaved (2j, 2j + 1), turn by positions[axes[j]][t] * inv_freq[j].
+    inv_freq f32 [R/2]; positions int32 [T] or [n_axes, T]; axes int32 [R/2] (None:
+    axis 0).  norm_w f32 [D]: the head's RMS norm with that weight comes first.
+    mscale multiplies the rotated dims.  Returns out (dense unless given; x for in place)."""
+    dt, dev = x.dtype, x.get_device()
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, (x, inv_freq, positions, axes, norm_w, out),
+                          lambda: gdn_rope(x, inv_freq, positions, axes, norm_w, norm_eps, mscale, interleaved, out))
+    if x.dim() != 3:
+        raise ValueError("x: expected [T, H, D]")
+    if positions is None:
+        raise ValueError("positions: needed")
+    T, H, D = x.shape
+    code = _dtype_code(x)
+    p_x, x_tok, x_head = _rows(x, "x", dev, dt, T, D, H)
+    p_pos, n_axes, p_axes, p_freq, R = _rotation(inv_freq, positions, axes, T, D, dev)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=dt, device=x.device)
+    p_out, o_tok, o_head = _rows(out, "out", dev, dt, T, D, H)
+    st = _lib.load().gdn_rope(
+        p_x, x_tok, x_head, p_pos, n_axes, p_axes, p_freq, _dptr(norm_w, "norm_w", dev, torch.float32, (D,)), norm_eps,
+        mscale, _lib.GDN_ROPE_INTERLEAVED if interleaved else 0, p_out, o_tok, o_head, T, H, D, R, code,
+        torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _lib.check(st, "gdn_rope")
+    return out
+
+
+def gdn_rope_kv_append(q, k, v, k_cache, v_cache, page_table, seq_lens, inv_freq, positions=None, axes=None,
+                       q_norm_w=None, k_norm_w=None, norm_eps=RMSNORM_EPS, mscale=1.0, interleaved=False,
+                       cu_seqlens=None, q_out=None, stream=None):
+    """gdn_rope of the new tokens' queries q [T, H_q, D] and keys k [T, H_kv, D], and
+    gdn_kv_append of the keys and the values v, in one pass.  positions None: each
+    token's place in its sequence.  q, k, v may be slices of a fused projection (see
+    gdn_rope); the other arguments as gdn_rope's and gdn_kv_append's.  Returns q_out
+    [T, H_q, D] (dense; may be q); the caches are written in place."""
+    dt, i32, f32, dev = q.dtype, torch.int32, torch.float32, q.get_device()
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, (q, k, v, k_cache, v_cache, page_table, seq_lens, inv_freq, positions, axes,
+                                        q_norm_w, k_norm_w, cu_seqlens, q_out),
+                          lambda: gdn_rope_kv_append(q, k, v, k_cache, v_cache, page_table, seq_lens, inv_freq, positions,
+                                                     axes, q_norm_w, k_norm_w, norm_eps, mscale, interleaved, cu_seqlens,
+                                                     q_out))
+    n_pages, H, ps, D, B, mp = _cache_dims(k_cache, v_cache, page_table, seq_lens)
+    if q.dim() != 3:
+        raise ValueError("q: expected [T, H_q, D]")
+    T, H_q = q.shape[0], q.shape[1]
+    code = _dtype_code(q)
+    p_q, q_tok, q_head = _rows(q, "q", dev, dt, T, D)
+    p_k, k_tok, k_head = _rows(k, "k", dev, dt, T, D, H)
+    p_v, v_tok, v_head = _rows(v, "v", dev, dt, T, D, H)
+    p_pos, n_axes, p_axes, p_freq, R = _rotation(inv_freq, positions, axes, T, D, dev)
+    if q_out is None:
+        q_out = torch.empty((T, H_q, D), dtype=dt, device=q.device)
+        p_o = q_out.data_ptr()
+    else:
+        p_o = _dptr(q_out, "q_out", dev, dt, (T, H_q, D))
+    st = _lib.load().gdn_rope_kv_append(
+        p_q, q_tok, q_head, p_k, k_tok, k_head, p_v, v_tok, v_head, p_o, _dptr(k_cache, "k_cache", dev, dt),
+        _dptr(v_cache, "v_cache", dev, dt), _dptr(page_table, "page_table", dev, i32),
+        _dptr(seq_lens, "seq_lens", dev, i32), _dptr(cu_seqlens, "cu_seqlens", dev, i32, (B + 1,)), p_pos, n_axes, p_axes,
+        p_freq, _dptr(q_norm_w, "q_norm_w", dev, f32, (D,)), _dptr(k_norm_w, "k_norm_w", dev, f32, (D,)), norm_eps, mscale,
+        _lib.GDN_ROPE_INTERLEAVED if interleaved else 0, B, T, H_q, H, D, R, ps, n_pages, mp, code,
+        torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _lib.check(st, "gdn_rope_kv_append")
+    return q_out
 
 
 @lru_cache(maxsize=256)

@@ -22,6 +22,7 @@ GDN_F32 = 0
 GDN_BF16 = 1
 GDN_QK_L2NORM = 1
 GDN_SOLVE_NEUMANN = 2
+GDN_ROPE_INTERLEAVED = 1
 
 
 def GDN_CHUNK(c: int) -> int:
@@ -76,6 +77,9 @@ SIGNATURES = {
     "gdn_decode_verify": (ST, [P, P, P, P, P, P, P, P, P, P, F32, P, I32, I32, F32, U32, P, Dims, ST,
                                P]),
     "gdn_kv_append": (ST, [P, P, P, P, P, P, P, I32, I64, I32, I32, I32, I32, I32, ST, P]),
+    "gdn_rope": (ST, [P, I64, I64, P, I32, P, P, P, F32, F32, U32, P, I64, I64, I64, I32, I32, I32, ST, P]),
+    "gdn_rope_kv_append": (ST, [P, I64, I64, P, I64, I64, P, I64, I64, P, P, P, P, P, P, P, I32, P, P, P, P, F32, F32,
+                                U32, I32, I64, I32, I32, I32, I32, I32, I32, I32, ST, P]),
     "gdn_attn_decode_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32, ST]),
     "gdn_attn_decode": (ST, [P, P, P, P, P, F32, P, P, P, I32, I32, I32, I32, I32, I32, I32, I32, P, SZ, ST, P]),
     "gdn_selftest_attn_decode": (ST, [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, I32, P, SZ, I32, P]),

@@ -93,7 +93,7 @@ const char* gdn_status_string(gdn_status_t s) {
 
 int gdn_last_cuda_error(void) { return g_last_cuda_error; }
 
-int gdn_version(void) { return (1 << 16) | 2; }
+int gdn_version(void) { return (1 << 16) | 3; }
 
 int64_t gdn_ckpt_count(const int32_t* cu, int32_t n_seq, int32_t every) {
     if (cu == nullptr || n_seq < 1 || every < 0) return -1;
@@ -693,6 +693,106 @@ gdn_status_t gdn_kv_append(const void* k, const void* v, void* k_cache, void* v_
     a.T = T_tot; a.B = B; a.H_kv = H_kv; a.row_bytes = (int)(D * elem_size(dtype));
     a.page_size = page_size; a.n_pages = n_pages; a.max_pages = max_pages;
     return cuda_status(gdn::launch_kv_append(a, (cudaStream_t)stream));
+}
+
+namespace {
+// Strides of a [T, H, D] tensor of rows of D contiguous elements.
+gdn_status_t check_rows(int64_t tok, int64_t head, int64_t T, int32_t H, gdn_dtype_t dt) {
+    const int64_t per16 = 16 / (int64_t)elem_size(dt);
+    if ((T > 1 && tok < 0) || (H > 1 && head < 0)) return GDN_ERR_INVALID_ARG;
+    if ((T > 1 && tok > INT64_MAX / 16 / T) || (H > 1 && head > INT64_MAX / 16 / H)) return GDN_ERR_INVALID_ARG;
+    if ((T > 1 && tok % per16 != 0) || (H > 1 && head % per16 != 0)) return GDN_ERR_ALIGN;
+    return GDN_OK;
+}
+
+gdn_status_t check_rotation(int32_t n_axes, const int32_t* axes, const float* inv_freq, const float* w0, const float* w1,
+                            float eps, float mscale, uint32_t flags, int64_t T, int32_t H, int32_t D, int32_t R,
+                            gdn_dtype_t dt) {
+    if (dt != GDN_F32 && dt != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (T < 0 || T > (int64_t)INT32_MAX || H <= 0 || D <= 0 || R < 2 || R > D || R % 2 != 0 || n_axes < 1 ||
+        (flags & ~GDN_ROPE_INTERLEAVED) != 0 || !isfinite(mscale))
+        return GDN_ERR_INVALID_ARG;
+    if ((w0 != nullptr || w1 != nullptr) && (!(eps > 0.f) || !isfinite(eps))) return GDN_ERR_INVALID_ARG;
+    if (D % 8 != 0 || D > 256 || H > 65536 || n_axes > 16) return GDN_ERR_UNSUPPORTED;
+    if (T > 0 && inv_freq == nullptr) return GDN_ERR_INVALID_ARG;
+    if (!aligned_n(axes, 4) || !aligned_n(inv_freq, 4) || !aligned_n(w0, 4) || !aligned_n(w1, 4)) return GDN_ERR_ALIGN;
+    return GDN_OK;
+}
+
+void fill_rotation(gdn::RopeArgs& a, const int32_t* positions, int32_t n_axes, const int32_t* axes, const float* inv_freq,
+                   const float* q_w, const float* k_w, float eps, float mscale, uint32_t flags, int64_t T, int32_t D,
+                   int32_t R) {
+    memset(&a, 0, sizeof(a));
+    a.positions = positions; a.axes = axes; a.inv_freq = inv_freq; a.n_axes = n_axes;
+    a.q_w = q_w; a.k_w = k_w; a.eps = eps; a.mscale = mscale;
+    a.neighbours = (flags & GDN_ROPE_INTERLEAVED) != 0;
+    a.T = T; a.D = D; a.R = R;
+}
+}  // namespace
+
+gdn_status_t gdn_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions,
+                      int32_t n_axes, const int32_t* axes, const float* inv_freq, const float* norm_w, float norm_eps,
+                      float mscale, uint32_t flags, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                      int64_t T, int32_t H, int32_t D, int32_t R, gdn_dtype_t dtype, void* stream) {
+    gdn_status_t st = check_rotation(n_axes, axes, inv_freq, norm_w, nullptr, norm_eps, mscale, flags, T, H, D, R, dtype);
+    if (st != GDN_OK) return st;
+    if (T == 0) return GDN_OK;
+    if (x == nullptr || out == nullptr || positions == nullptr) return GDN_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(out) || !aligned_n(positions, 4)) return GDN_ERR_ALIGN;
+    if ((st = check_rows(x_token_stride, x_head_stride, T, H, dtype)) != GDN_OK ||
+        (st = check_rows(out_token_stride, out_head_stride, T, H, dtype)) != GDN_OK)
+        return st;
+    const int64_t ot = T > 1 ? out_token_stride : 0, oh = H > 1 ? out_head_stride : 0;
+    const int64_t xt = T > 1 ? x_token_stride : 0, xh = H > 1 ? x_head_stride : 0;
+    // rows of the output do not overlap, whichever of the two dims is the outer one
+    const bool heads_inside = (H == 1 || oh >= D) && (T == 1 || ot >= oh * (H - 1) + D);
+    const bool tokens_inside = (T == 1 || ot >= D) && (H == 1 || oh >= ot * (T - 1) + D);
+    if (!heads_inside && !tokens_inside) return GDN_ERR_INVALID_ARG;
+    if (x == out && (xt != ot || xh != oh)) return GDN_ERR_INVALID_ARG;
+    gdn::RopeArgs a;
+    fill_rotation(a, positions, n_axes, axes, inv_freq, norm_w, nullptr, norm_eps, mscale, flags, T, D, R);
+    a.q = x; a.q_tok = xt; a.q_head = xh; a.q_out = out; a.o_tok = ot; a.o_head = oh;
+    a.B = 1; a.H_q = H;
+    return cuda_status(gdn::launch_rope(a, dtype, (cudaStream_t)stream));
+}
+
+gdn_status_t gdn_rope_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                                int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                                int64_t v_head_stride, void* q_out, void* k_cache, void* v_cache,
+                                const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu_seqlens,
+                                const int32_t* positions, int32_t n_axes, const int32_t* axes, const float* inv_freq,
+                                const float* q_norm_w, const float* k_norm_w, float norm_eps, float mscale,
+                                uint32_t flags, int32_t B, int64_t T_tot, int32_t H_q, int32_t H_kv, int32_t D, int32_t R,
+                                int32_t page_size, int32_t n_pages, int32_t max_pages, gdn_dtype_t dtype, void* stream) {
+    gdn_status_t st = check_cache(H_kv, D, page_size, n_pages, max_pages, dtype);
+    if (st != GDN_OK) return st;
+    st = check_rotation(n_axes, axes, inv_freq, q_norm_w, k_norm_w, norm_eps, mscale, flags, T_tot, H_q, D, R, dtype);
+    if (st != GDN_OK) return st;
+    if (B < 0 || B > (1 << 24) || (positions == nullptr && n_axes != 1)) return GDN_ERR_INVALID_ARG;
+    if (T_tot == 0) return GDN_OK;
+    if (B == 0 || (cu_seqlens == nullptr && T_tot % B != 0)) return GDN_ERR_INVALID_ARG;
+    if (q == nullptr || k == nullptr || v == nullptr || q_out == nullptr || k_cache == nullptr || v_cache == nullptr ||
+        page_table == nullptr || seq_lens == nullptr)
+        return GDN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_cache) ||
+        !aligned16(v_cache) || !aligned_n(page_table, 4) || !aligned_n(seq_lens, 4) || !aligned_n(cu_seqlens, 4) ||
+        !aligned_n(positions, 4))
+        return GDN_ERR_ALIGN;
+    if ((st = check_rows(q_token_stride, q_head_stride, T_tot, H_q, dtype)) != GDN_OK ||
+        (st = check_rows(k_token_stride, k_head_stride, T_tot, H_kv, dtype)) != GDN_OK ||
+        (st = check_rows(v_token_stride, v_head_stride, T_tot, H_kv, dtype)) != GDN_OK)
+        return st;
+    gdn::RopeArgs a;
+    fill_rotation(a, positions, n_axes, axes, inv_freq, q_norm_w, k_norm_w, norm_eps, mscale, flags, T_tot, D, R);
+    const bool many = T_tot > 1;
+    a.q = q; a.q_tok = many ? q_token_stride : 0; a.q_head = H_q > 1 ? q_head_stride : 0;
+    a.k = k; a.k_tok = many ? k_token_stride : 0; a.k_head = H_kv > 1 ? k_head_stride : 0;
+    a.v = v; a.v_tok = many ? v_token_stride : 0; a.v_head = H_kv > 1 ? v_head_stride : 0;
+    a.q_out = q_out; a.o_tok = (int64_t)H_q * D; a.o_head = D;
+    if (q == q_out && ((many && a.q_tok != a.o_tok) || (H_q > 1 && a.q_head != a.o_head))) return GDN_ERR_INVALID_ARG;
+    a.k_cache = k_cache; a.v_cache = v_cache; a.table = page_table; a.lens = seq_lens; a.cu = cu_seqlens;
+    a.B = B; a.H_q = H_q; a.H_kv = H_kv; a.page_size = page_size; a.n_pages = n_pages; a.max_pages = max_pages;
+    return cuda_status(gdn::launch_rope(a, dtype, (cudaStream_t)stream));
 }
 
 size_t gdn_attn_decode_workspace_size(int32_t B, int32_t K, int32_t H_q, int32_t H_kv, int32_t D,

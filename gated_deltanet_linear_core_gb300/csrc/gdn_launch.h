@@ -196,6 +196,26 @@ struct KvAppendArgs {
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t s);
 
+// Head norm and rotary positions of q, and with a cache of k on the way into it beside v (gdn_rope,
+// gdn_rope_kv_append).  Strides in elements.
+struct RopeArgs {
+    const void *q, *k, *v;
+    int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head;
+    void* q_out;
+    int64_t o_tok, o_head;
+    void *k_cache, *v_cache;  // null: q alone
+    const int32_t *table, *lens;
+    const int32_t* cu;         // [B + 1] or null: T / B tokens each
+    const int32_t* positions;  // [n_axes, T] or null: the cache's
+    const int32_t* axes;       // [R / 2] or null: axis 0
+    const float* inv_freq;     // [R / 2]
+    const float *q_w, *k_w;    // [D] or null
+    float eps, mscale;
+    int64_t T;
+    int B, H_q, H_kv, D, R, n_axes, neighbours, page_size, max_pages, n_pages;
+};
+cudaError_t launch_rope(const RopeArgs& a, gdn_dtype_t dt, cudaStream_t s);
+
 // Acceptance of drafted tokens (gdn_draft_accept).
 struct DraftAcceptArgs {
     const void *p, *q;     // [B, K + 1, V], [B, K, V] or null

@@ -532,6 +532,54 @@ gdn_status_t gdn_kv_append(const void* k, const void* v, void* k_cache, void* v_
                            gdn_dtype_t dtype, void* stream);
 
 /*
+ * Rotary positions: with pair j of a head's first R dims -- dims (j, j + R/2), or
+ * (2j, 2j + 1) with GDN_ROPE_INTERLEAVED -- and the angle
+ * g = positions[axes[j]][t] inv_freq[j] of token t,
+ *   (x_a, x_b) <- mscale (x_a cos g - x_b sin g, x_b cos g + x_a sin g);
+ * dims from R on pass through.  With norm_w, before that,
+ *   x <- x / sqrt(mean_d x_d^2 + eps) norm_w   (over all D dims of the head).
+ * Several axes (time, height, width, ..) give images and video their positions:
+ * axes says which one each pair turns with, in any order.  Angles are exact to about
+ * 2^-50 of their size, however far the position is; arithmetic in f32, one rounding.
+ *   x          (device) [T, H, D] dtype, strides in elements between tokens and between heads
+ *              (multiples of 16 bytes, not negative; ignored where there is one token, one head);
+ *              the dims of a head are contiguous
+ *   positions  (device) [n_axes, T] int32, negative ones too
+ *   axes       (device) [R/2] int32, or NULL: axis 0.  Pairs of an axis outside [0, n_axes) have angle 0
+ *   inv_freq   (device) [R/2] f32
+ *   norm_w     (device) [D] f32, or NULL;  norm_eps > 0 where there is one
+ *   mscale     factor of the rotated dims, finite (1: none)
+ *   out        (device) like x with strides of its own, rows apart from one another; x itself (with x's strides)
+ *              or other memory
+ * R even, 2 <= R <= D;  D a multiple of 8 up to 256;  1 <= n_axes <= 16;  T < 2^31, H <= 65536.
+ */
+#define GDN_ROPE_INTERLEAVED 1u
+gdn_status_t gdn_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions,
+                      int32_t n_axes, const int32_t* axes, const float* inv_freq, const float* norm_w, float norm_eps,
+                      float mscale, uint32_t flags, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                      int64_t T, int32_t H, int32_t D, int32_t R, gdn_dtype_t dtype, void* stream);
+
+/*
+ * gdn_rope of new tokens' queries and keys, and gdn_kv_append of the keys and the
+ * values (copied bit for bit) in one pass.  Tokens, sequences, places and pages as
+ * gdn_kv_append.  A token outside every sequence is left out (its row of q_out
+ * too); one whose place or page does not exist has its query rotated, nothing else.
+ *   q, k, v    (device) [T_tot, H_q or H_kv, D] dtype, strides as gdn_rope's x
+ *   q_out      (device) [T_tot, H_q, D] dtype, dense, or q itself where that is dense; no other argument's memory
+ *   positions  (device) [n_axes, T_tot] int32, or NULL (n_axes 1): a token's place in its sequence
+ *   q_norm_w, k_norm_w (device) [D] f32, each or NULL
+ *   other arguments as gdn_rope's and gdn_kv_append's
+ */
+gdn_status_t gdn_rope_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                                int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                                int64_t v_head_stride, void* q_out, void* k_cache, void* v_cache,
+                                const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu_seqlens,
+                                const int32_t* positions, int32_t n_axes, const int32_t* axes, const float* inv_freq,
+                                const float* q_norm_w, const float* k_norm_w, float norm_eps, float mscale,
+                                uint32_t flags, int32_t B, int64_t T_tot, int32_t H_q, int32_t H_kv, int32_t D, int32_t R,
+                                int32_t page_size, int32_t n_pages, int32_t max_pages, gdn_dtype_t dtype, void* stream);
+
+/*
  * Attention of the K newest tokens of B sequences over the cache, which holds
  * their keys and values already (gdn_kv_append).  K = 1 is a decode step; K > 1 is
  * the verification pass (causal among the new tokens).  New token i of sequence b
