@@ -28,7 +28,8 @@ __all__ = [
     "gdn_layer_prefill_host", "gdn_decode_step", "gdn_decode_verify", "gdn_layer_prefill",
     "gdn_layer_prefill_workspace_size", "gdn_layer_prefill_launches", "gdn_chunk_prefill_norm",
     "HeadShard", "head_shard",
-    "gdn_layer_decode", "gdn_kv_append", "gdn_rope", "gdn_rope_kv_append", "gdn_attn_decode", "gdn_attn_decode_workspace_size", "gdn_draft_accept",
+    "gdn_layer_decode", "gdn_kv_append", "gdn_rope", "gdn_rope_kv_append", "gdn_attn_decode", "gdn_attn_decode_workspace_size",
+    "gdn_attn_decode_shared", "gdn_attn_decode_shared_workspace_size", "gdn_draft_accept",
     "library_path",
 ]
 
@@ -766,6 +767,66 @@ def gdn_attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=0.0, gate=N
         torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _lib.check(st, "gdn_attn_decode")
+    return (out, lse) if return_lse else out
+
+
+@lru_cache(maxsize=256)
+def _shared_workspace(B, K, H_q, H_kv, D, page_size, G, code):
+    return int(_lib.load().gdn_attn_decode_shared_workspace_size(B, K, H_q, H_kv, D, page_size, G, code))
+
+
+def gdn_attn_decode_shared_workspace_size(B: int, K: int, H_q: int, H_kv: int, D: int, page_size: int, dtype,
+                                          groups: int = 1) -> int:
+    return _shared_workspace(int(B), int(K), int(H_q), int(H_kv), int(D), int(page_size), int(groups),
+                             _lib.GDN_BF16 if dtype == torch.bfloat16 else _lib.GDN_F32)
+
+
+def gdn_attn_decode_shared(q, k_cache, v_cache, page_table, seq_lens, prefix_lens, cu_groups=None, scale=0.0, gate=None,
+                           out=None, lse=None, return_lse=False, workspace=None, stream=None):
+    """gdn_attn_decode of sequences in groups that share their first tokens, which are
+    attended to once per group: sequences cu_groups[g] .. cu_groups[g + 1] - 1 (int32
+    [G + 1]; None: one group of all) hold the same keys and values at their first
+    prefix_lens[g] (int32 [G]) positions.  seq_lens counts the prefix too, and the
+    page table holds its pages in every row; results are gdn_attn_decode's up to rounding."""
+    dt, i32, dev = q.dtype, torch.int32, q.get_device()
+    if _elsewhere(dev, stream):
+        return _on_stream(dev, stream, (q, k_cache, v_cache, page_table, seq_lens, prefix_lens, cu_groups, gate, out, lse,
+                                        workspace),
+                          lambda: gdn_attn_decode_shared(q, k_cache, v_cache, page_table, seq_lens, prefix_lens, cu_groups,
+                                                         scale, gate, out, lse, return_lse, workspace))
+    n_pages, H, ps, D, B, mp = _cache_dims(k_cache, v_cache, page_table, seq_lens)
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or shape[3] != D:
+        raise ValueError(f"q: shape {tuple(shape)}, expected [{B}, K, H_q, {D}]")
+    if prefix_lens.dim() != 1 or prefix_lens.shape[0] < 1 or (cu_groups is None and prefix_lens.shape[0] != 1):
+        raise ValueError(f"prefix_lens: shape {tuple(prefix_lens.shape)}, expected [G], [1] without cu_groups")
+    K, H_q, G = shape[1], shape[2], prefix_lens.shape[0]
+    code = _dtype_code(q)
+    p_q = _dptr(q, "q", dev, dt)
+    if out is None:
+        out = torch.empty_like(q)
+        p_o = out.data_ptr()
+    else:
+        p_o = _dptr(out, "out", dev, dt, shape)
+    if lse is None and return_lse:
+        lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
+        p_e = lse.data_ptr()
+    else:
+        p_e = _dptr(lse, "lse", dev, torch.float32, shape[:3])
+    if workspace is None:
+        nws = _shared_workspace(B, K, H_q, H, D, ps, G, code)
+        workspace = torch.empty(nws, dtype=torch.uint8, device=q.device)
+        p_w = workspace.data_ptr()
+    else:
+        p_w, nws = _dptr(workspace, "workspace", dev, None), workspace.numel() * workspace.element_size()
+    st = _lib.load().gdn_attn_decode_shared(
+        p_q, _dptr(k_cache, "k_cache", dev, dt), _dptr(v_cache, "v_cache", dev, dt),
+        _dptr(page_table, "page_table", dev, i32), _dptr(seq_lens, "seq_lens", dev, i32),
+        _dptr(prefix_lens, "prefix_lens", dev, i32), _dptr(cu_groups, "cu_groups", dev, i32, (G + 1,)), scale,
+        _dptr(gate, "gate", dev, dt, shape), p_o, p_e, B, K, H_q, H, D, ps, n_pages, mp, G, p_w, nws, code,
+        torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _lib.check(st, "gdn_attn_decode_shared")
     return (out, lse) if return_lse else out
 
 

@@ -83,6 +83,10 @@ SIGNATURES = {
     "gdn_attn_decode_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32, ST]),
     "gdn_attn_decode": (ST, [P, P, P, P, P, F32, P, P, P, I32, I32, I32, I32, I32, I32, I32, I32, P, SZ, ST, P]),
     "gdn_selftest_attn_decode": (ST, [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, I32, P, SZ, I32, P]),
+    "gdn_attn_decode_shared_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32, I32, ST]),
+    "gdn_attn_decode_shared": (ST, [P, P, P, P, P, P, P, F32, P, P, P, I32, I32, I32, I32, I32, I32, I32, I32, I32, P, SZ,
+                                    ST, P]),
+    "gdn_selftest_attn_decode_shared": (ST, [P, P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, I32, P, SZ, I32, P]),
     "gdn_draft_accept": (ST, [P, P, P, P, P, P, I32, I32, I32, P, P, P, ST, P]),
 }
 

@@ -31,6 +31,12 @@ __device__ __forceinline__ int clamped_len(const AttnArgs& a, int b) {
 }
 __device__ __forceinline__ int tiles_of(int len, int tile) { return len <= tile ? 1 : (len - 1) / tile + 1; }
 __device__ __forceinline__ int units_of(const AttnArgs& a, int len, int tile) { return a.setup + tiles_of(len, tile); }
+// Tokens of sequence b, of len, that the pass over the prefixes has taken (the bound holds for every call that keeps to
+// the rules; it keeps calls that share a workspace against them from reading out of bounds).
+template <bool SHARED>
+__device__ __forceinline__ int skip_of(const AttnArgs& a, int b, int len) {
+    return SHARED && len > 0 ? min(max(a.skip[b], 0), len - 1) & ~(kShareStep - 1) : 0;
+}
 
 // First unit of CTA c of n.
 __host__ __device__ __forceinline__ int64_t cta_begin(int64_t total, int c, int n) { return total * c / n; }
@@ -41,12 +47,14 @@ struct Place {
     int64_t total;  // units of the whole call
     int64_t first;  // first unit of sequence b's items
     int b, len;     // the sequence that holds the unit asked for, its clamped length
+    int skip;       // of which the pass over the prefixes has taken
 };
 
 // Units of the call and the sequence that holds the first unit of CTA c of the
 // n that take part (at most one per unit), by one warp: a lane adds up a 32nd of the sequences, then the warp searches the lane's
 // share that holds the unit.  (A block-wide scan saves loads but costs three
 // barriers, which at the start of a call is longer.)
+template <bool SHARED = false>
 __device__ __forceinline__ Place find_place(const AttnArgs& a, int tile, int c, int& n) {
     const int lane = threadIdx.x & 31;
     const int64_t mult = (int64_t)a.H_kv * a.n_rb;
@@ -55,7 +63,10 @@ __device__ __forceinline__ Place find_place(const AttnArgs& a, int tile, int c, 
 #pragma unroll 4
     for (int i = 0; i < per; ++i) {
         const int b = lane * per + i;
-        if (b < a.B) inc += units_of(a, clamped_len(a, b), tile);
+        if (b < a.B) {
+            const int len = clamped_len(a, b);
+            inc += units_of(a, len - skip_of<SHARED>(a, b, len), tile);
+        }
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -65,7 +76,7 @@ __device__ __forceinline__ Place find_place(const AttnArgs& a, int tile, int c, 
     Place p;
     p.total = __shfl_sync(0xffffffffu, inc, 31) * mult;
     p.first = 0;
-    p.b = p.len = 0;
+    p.b = p.len = p.skip = 0;
     if (n > p.total) n = (int)p.total;
     if (c >= n) return p;
     const int64_t want = cta_begin(p.total, c, n);
@@ -76,7 +87,8 @@ __device__ __forceinline__ Place find_place(const AttnArgs& a, int tile, int c, 
     for (int b0 = owner * per; b0 < end; b0 += 32) {
         const int b = b0 + lane;
         const int len = b < end ? clamped_len(a, b) : 0;
-        int sum = b < end ? units_of(a, len, tile) : 0;  // inclusive scan: 32 sequences' units fit 31 bits
+        const int skip = b < end ? skip_of<SHARED>(a, b, len) : 0;
+        int sum = b < end ? units_of(a, len - skip, tile) : 0;  // inclusive scan: 32 sequences' units fit 31 bits
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, sum, o);
@@ -88,6 +100,7 @@ __device__ __forceinline__ Place find_place(const AttnArgs& a, int tile, int c, 
             const int less = __shfl_sync(0xffffffffu, sum, l > 0 ? l - 1 : 0);
             p.b = b0 + l;
             p.len = __shfl_sync(0xffffffffu, len, l);
+            if (SHARED) p.skip = __shfl_sync(0xffffffffu, skip, l);
             if (l > 0) p.first += less * mult;
             break;
         }
@@ -100,20 +113,22 @@ __device__ __forceinline__ Place find_place(const AttnArgs& a, int tile, int c, 
 struct Segment {
     int b, h, rb, len;   // item
     int tile0, tile1;    // its tiles [tile0, tile1) of this segment
-    int tiles;           // tiles of the whole item
+    int tiles;           // tiles of the whole item; SHARED: how many CTAs' parts it has if this is the first, else 0
 };
+template <bool SHARED = false>
 struct Walk {
     int64_t at, end, item0;  // units; item0: first unit of sequence b's items
-    int b, len;
+    int b, len, skip;
     __device__ __forceinline__ Walk(const Place& p, int64_t lo, int64_t hi)
-        : at(lo), end(hi), item0(p.first), b(p.b), len(p.len) {}
+        : at(lo), end(hi), item0(p.first), b(p.b), len(p.len), skip(p.skip) {}
     __device__ __forceinline__ bool next(const AttnArgs& a, int tile, Segment& s) {
         while (at < end) {
-            int units = units_of(a, len, tile);
+            int units = units_of(a, len - skip, tile);
             while (at >= item0 + (int64_t)units * a.H_kv * a.n_rb) {
                 item0 += (int64_t)units * a.H_kv * a.n_rb;
                 len = clamped_len(a, ++b);
-                units = units_of(a, len, tile);
+                skip = skip_of<SHARED>(a, b, len);
+                units = units_of(a, len - skip, tile);
             }
             const int64_t off = at - item0;
             const int item = (int)(off / units);
@@ -125,6 +140,11 @@ struct Walk {
             s.tile0 = from > a.setup ? from - a.setup : 0;
             s.tile1 = upto - a.setup;
             s.tiles = units - a.setup;
+            if (SHARED) {  // (the parts are counted by the caller, where there are several)
+                s.tiles = s.tile0 > 0 ? 0 : upto == units ? 1 : 2;
+                s.tile0 += skip / tile;
+                s.tile1 += skip / tile;
+            }
             s.h = item / a.n_rb;
             s.rb = item - s.h * a.n_rb;
             s.b = b;
@@ -156,7 +176,7 @@ struct alignas(16) JoinTask {
 };
 __device__ __forceinline__ JoinTask* join_task(const AttnArgs& a, int c) { return reinterpret_cast<JoinTask*>(a.ws) + c; }
 // `first`: the CTA's first segment, just taken from its walk; null: it has none.
-__device__ __forceinline__ void write_join_task(const AttnArgs& a, const Place& p, const Walk& walk, const Segment* first,
+__device__ __forceinline__ void write_join_task(const AttnArgs& a, const Place& p, const Walk<>& walk, const Segment* first,
                                                 int c, int n) {
     JoinTask t;
     t.n = 0;
@@ -170,6 +190,14 @@ __device__ __forceinline__ void write_join_task(const AttnArgs& a, const Place& 
         t.rb = s.rb;
     }
     *join_task(a, c) = t;
+}
+
+// SHARED: the CTAs that work on the segment's item, whose first part the segment is.
+__device__ __forceinline__ int count_parts(const AttnArgs& a, const Place& p, const Walk<true>& walk, const Segment& s,
+                                           int tile, int c, int n) {
+    const int units = units_of(a, s.len - walk.skip, tile);
+    const int64_t last = walk.item0 + (int64_t)(s.h * a.n_rb + s.rb + 1) * units - 1;
+    return cta_of(p.total, last, n) - c + 1;
 }
 
 // A workspace slot: maxima (log2 domain) and sums of its rows, then their

@@ -5,6 +5,7 @@ namespace gdn {
 
 namespace {
 constexpr int kTcRows = 128;  // rows of a block, at most
+}  // namespace
 
 int attn_ctas() {
     int dev = 0, n = 0;
@@ -12,7 +13,6 @@ int attn_ctas() {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
     return n < kAttnMaxCtas ? n : kAttnMaxCtas;
 }
-}  // namespace
 
 size_t attn_plan(AttnArgs& a, gdn_dtype_t dt) {
     const int most = attn_tc_takes(a, dt) ? kTcRows : kAttnFfmaRows;

@@ -85,7 +85,7 @@ struct Ffma {
     static_assert(STAGE_FLOATS / NW >= R * NV * 128, "outputs fit the stages");
 };
 
-template <typename E, int R, int NV>
+template <typename E, int R, int NV, bool SHARED>
 __global__ void __launch_bounds__(Ffma<E, R, NV>::NT, 1) attn_ffma_kernel(AttnArgs a) {
     using G = Ffma<E, R, NV>;
     constexpr int T = G::T, NW = G::NW, S = G::S, PER = G::PER;
@@ -104,10 +104,10 @@ __global__ void __launch_bounds__(Ffma<E, R, NV>::NT, 1) attn_ffma_kernel(AttnAr
     pdl_wait();
     pdl_trigger();
     int n_cta = gridDim.x;
-    const Place place = find_place(a, TT, blockIdx.x, n_cta);
+    const Place place = find_place<SHARED>(a, TT, blockIdx.x, n_cta);
     const int64_t u0 = (int)blockIdx.x < n_cta ? cta_begin(place.total, blockIdx.x, n_cta) : 0;
     const int64_t u1 = (int)blockIdx.x < n_cta ? cta_begin(place.total, blockIdx.x + 1, n_cta) : 0;
-    Walk walk(place, u0, u1);
+    Walk<SHARED> walk(place, u0, u1);
     const E* kc = static_cast<const E*>(a.k_cache);
     const E* vc = static_cast<const E*>(a.v_cache);
     const bool has[2] = {lane * 4 < D, NV > 1 && (lane + 32) * 4 < D};
@@ -116,8 +116,11 @@ __global__ void __launch_bounds__(Ffma<E, R, NV>::NT, 1) attn_ffma_kernel(AttnAr
 
     Segment s;
     bool more = walk.next(a, TT, s);
-    if (tid == G::NT - 32) write_join_task(a, place, walk, more ? &s : nullptr, blockIdx.x, n_cta);
+    if constexpr (!SHARED)
+        if (tid == G::NT - 32) write_join_task(a, place, walk, more ? &s : nullptr, blockIdx.x, n_cta);
     for (; more; more = walk.next(a, TT, s)) {
+        if constexpr (SHARED)
+            if (s.tiles == 2) s.tiles = count_parts(a, place, walk, s, TT, blockIdx.x, n_cta);
         const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
         const int end = min(s.len, s.tile1 * TT);
         const int32_t* table = a.table + (int64_t)s.b * a.max_pages;
@@ -284,8 +287,8 @@ __global__ void __launch_bounds__(Ffma<E, R, NV>::NT, 1) attn_ffma_kernel(AttnAr
             for (int v = 0; v < NV; ++v)
                 if (has[v]) *reinterpret_cast<float4*>(o_w + r * D + (lane + 32 * v) * 4) = o[r][v];
         __syncthreads();
-        const bool whole = s.tile1 - s.tile0 == s.tiles;
-        float* slot = slot_ptr(a, part_slot(s));
+        const bool whole = !SHARED && s.tile1 - s.tile0 == s.tiles;
+        float* slot = slot_ptr(a, SHARED ? blockIdx.x : part_slot(s));
         for (int e = tid; e < nr * (D / 4); e += G::NT) {
             const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
             float top = kNone, sum = 0.f;
@@ -309,6 +312,12 @@ __global__ void __launch_bounds__(Ffma<E, R, NV>::NT, 1) attn_ffma_kernel(AttnAr
                 }
                 store4(static_cast<E*>(a.out) + row * D + d, y);
                 if (d == 0 && a.lse != nullptr) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            } else if (SHARED && s.tiles > 0) {
+                const int64_t row = row_index(a, s.b, s.h, r0 + r);
+                *reinterpret_cast<float4*>(a.part_o + row * D + d) = y;
+                if (d == 0)
+                    a.part_stat[row] = make_float4(top == kNone ? -INFINITY : top, sum, __int_as_float(blockIdx.x),
+                                                   __int_as_float(s.tiles));
             } else {
                 *reinterpret_cast<float4*>(slot + a.stat_floats + r * D + d) = y;
                 if (d == 0) {
@@ -442,20 +451,20 @@ __global__ void __launch_bounds__(JT) attn_join_kernel(AttnArgs a, int log_group
     }
 }
 
-template <typename E, int R, int NV>
+template <typename E, int R, int NV, bool SHARED>
 cudaError_t launch_ffma(const AttnArgs& a, int n_cta, cudaStream_t s) {
     using G = Ffma<E, R, NV>;
     const size_t smem = sizeof(float) * (G::STAGE_FLOATS + G::NW * (G::C + 2 * R) + R);
-    const cudaError_t e = cudaFuncSetAttribute(attn_ffma_kernel<E, R, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(attn_ffma_kernel<E, R, NV, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_ffma_kernel<E, R, NV>, dim3((unsigned)n_cta), dim3(G::NT), smem, s, a);
+    return launch_pdl(attn_ffma_kernel<E, R, NV, SHARED>, dim3((unsigned)n_cta), dim3(G::NT), smem, s, a);
 }
 
-template <typename E>
+template <typename E, bool SHARED>
 cudaError_t launch_ffma_rows(const AttnArgs& a, int n_cta, cudaStream_t s) {
-    if (a.D > 128) return a.rb_rows <= 4 ? launch_ffma<E, 4, 2>(a, n_cta, s) : launch_ffma<E, 8, 2>(a, n_cta, s);
-    return a.rb_rows <= 4 ? launch_ffma<E, 4, 1>(a, n_cta, s) : launch_ffma<E, 8, 1>(a, n_cta, s);
+    if (a.D > 128) return a.rb_rows <= 4 ? launch_ffma<E, 4, 2, SHARED>(a, n_cta, s) : launch_ffma<E, 8, 2, SHARED>(a, n_cta, s);
+    return a.rb_rows <= 4 ? launch_ffma<E, 4, 1, SHARED>(a, n_cta, s) : launch_ffma<E, 8, 1, SHARED>(a, n_cta, s);
 }
 
 }  // namespace
@@ -476,7 +485,10 @@ cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaS
 }
 
 cudaError_t launch_attn_ffma(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaStream_t s) {
-    const cudaError_t e = dt == GDN_BF16 ? launch_ffma_rows<bf16>(a, n_cta, s) : launch_ffma_rows<float>(a, n_cta, s);
+    if (a.skip != nullptr)
+        return dt == GDN_BF16 ? launch_ffma_rows<bf16, true>(a, n_cta, s) : launch_ffma_rows<float, true>(a, n_cta, s);
+    const cudaError_t e =
+        dt == GDN_BF16 ? launch_ffma_rows<bf16, false>(a, n_cta, s) : launch_ffma_rows<float, false>(a, n_cta, s);
     return e != cudaSuccess ? e : launch_attn_join(a, n_cta, dt, s);
 }
 

@@ -1,0 +1,516 @@
+// The pass over shared prefixes on tcgen05 tensor cores (bf16): a group's query
+// rows that share a key-value head, 128 at a time, over the prefix's tiles of 128 tokens.
+//
+// With hundreds of rows per cached token the products are the bound, not the
+// cache, so the query rows are the M = 128 side of the MMAs and the tokens the N side:
+//   S [128 rows x 128 tokens] = Q K^T    (Q and K tile in shared memory, both K-major)
+//   O [128 rows x D]         += P V      (P in tensor memory, V tile in shared memory, MN-major)
+// A softmax thread owns a row, so maxima and sums need no exchange between lanes, and
+// P goes back into the columns of S that it came from.  P is held as two bf16 (the value
+// cut to 8 bits and the rounded rest), as in attn_tc.cu: one alone would add an error of the size of the output's
+// own rounding.  Two buffers of S: while P V of a tile runs, the scores of the next are
+// turned into weights by the other warpgroup.  The two share a row's running maximum,
+// which is moved only when a score exceeds it by 2^8, and O is rescaled then.
+//
+// Warps: 0 walks the CTA's range, tells the others its segments, and loads K and V (of
+// every page piece the first 64 of 128 dims; warp 3 the others), 1 issues the MMAs,
+// 2 loads Q, 4 to 11 are the softmax.  Every wait is bounded (1 s): on a timeout the
+// roles run out without waiting, the copies in flight land, TMEM is freed and the error
+// word is set.
+#include "attn_shared.cuh"
+#include "attn_tc_common.cuh"
+
+namespace gdn {
+
+__device__ int g_prefix_error;  // bit 0: a bounded wait gave up
+
+namespace {
+
+using namespace attn;
+
+constexpr int ROWS = 128;
+constexpr int NT = 384;
+constexpr int NSOFT = 256;
+
+template <int NDB>
+struct Layout {
+    static constexpr int Q_BYTES = 2 * NDB * SLAB;
+    static constexpr int SMALL = 1024 + 4 * ROWS * 4;  // barriers and notes, a row's maximum, sums
+    static constexpr int FIT = (kSmemMax - Q_BYTES - SMALL) / SLOT;
+    static constexpr int NS = FIT < 6 ? FIT : 6;
+    static constexpr int O_Q = NS * SLOT;
+    static constexpr int O_BAR = O_Q + Q_BYTES;
+    static constexpr int O_SEG = O_BAR + 512;
+    static constexpr int O_M = O_BAR + 1024;   // [128] running maxima
+    static constexpr int O_L = O_M + ROWS * 4; // [2][128] the warpgroups' sums
+    static constexpr int SMEM = O_BAR + SMALL;
+    static constexpr int T_S = 0, T_O = 256, T_COLS = 512;
+    static constexpr int SEGS = 4;  // segments told ahead
+    static_assert(SMEM <= kSmemMax && NS >= 4, "shared memory");
+    // slots in the order K(0), K(1), V(0), K(2), V(1), .. of a segment's n tiles, from its first slot
+    __device__ static __forceinline__ int k_slot(int j) { return j == 0 ? 0 : NDB * (2 * j - 1); }
+    __device__ static __forceinline__ int v_slot(int j, int n) { return NDB * (j + 1 < n ? 2 * j + 2 : 2 * n - 1); }
+};
+static_assert(sizeof(PrefixSegment) == 32 && 4 * 32 <= 512, "notes");
+
+// D += A B with A in tensor memory (two bf16 per column), B by its descriptor's low word.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(hi)
+        : "memory");
+}
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+
+template <int NDB>
+__global__ void __launch_bounds__(NT, 1)
+attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, ShareArgs s,
+                      int piece) {
+    using L = Layout<NDB>;
+    constexpr int NS = L::NS;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const AttnArgs& a = s.a;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::O_BAR);
+    uint64_t* full = bars;            // [6] slot landed (TMA), told by both loading warps
+    uint64_t* empty = bars + 6;       // [6] slot consumed (commit)
+    uint64_t* s_full = bars + 12;     // [2] S of a tile done
+    uint64_t* p_full = bars + 14;     // [2] P of a tile written (4 warps)
+    uint64_t* pv_done = bars + 16;    // [2] P V of a tile done
+    uint64_t* q_full = bars + 18;     // a segment's Q written
+    uint64_t* q_empty = bars + 19;    // S of a segment's last tile done
+    uint64_t* seg_full = bars + 20;   // [4] a segment is told
+    uint64_t* seg_empty = bars + 24;  // [4] ... and taken note of
+    uint64_t* m_told = bars + 28;     // [4 lane quarters][2] running maxima up to a tile are decided
+    uint64_t* drained = bars + 36;    // every MMA issued is done (abort)
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 37);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+    volatile int* filled = reinterpret_cast<volatile int*>(bars + 38);  // [2 loading warps][6] loads into a slot
+    PrefixSegment* notes = reinterpret_cast<PrefixSegment*>(sm + L::O_SEG);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < 6; ++i) {
+            mbar_init(&full[i], 2);
+            mbar_init(&empty[i], 1);
+            filled[i] = filled[6 + i] = 0;
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&pv_done[i], 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        mbar_init(drained, 1);
+        for (int i = 0; i < L::SEGS; ++i) {
+            mbar_init(&seg_full[i], 1);
+            mbar_init(&seg_empty[i], 3 + NSOFT / 32);
+        }
+        for (int i = 0; i < 8; ++i) mbar_init(&m_told[i], 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+    }
+    if (warp == 1) {
+        tmem_alloc(tslot, L::T_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = *tslot;
+    pdl_wait();
+    pdl_trigger();
+
+    PrefixSegment g;
+    int sg = 0;  // segments told or taken note of
+    // The next segment, from warp 0: false at the end of the CTA's range.  `ok` turns false where the wait gave up.
+    auto heard = [&](bool& ok) -> bool {
+        ok = wait_or_abort(&seg_full[sg % L::SEGS], (uint32_t)((sg / L::SEGS) & 1), abort_flag);
+        if (!ok) return false;
+        g = notes[sg % L::SEGS];
+        ++sg;
+        return g.tile1 > 0;
+    };
+    auto took_note = [&] { mbar_arrive(&seg_empty[(sg - 1) % L::SEGS]); };  // one thread per warp, after heard()
+    const int nslab = (a.D + 63) / 64;  // 64-dim slabs of a cache row
+
+    // K and V of segment g, slab 0 or 1 of every 128 dims; lane p takes page piece p.
+    const int np = TILE / piece;
+    auto look_up = [&](int tile, int& y, int& z) {
+        z = a.n_pages;  // reads as zeros
+        y = 0;
+        if (lane < np) {
+            const int t = tile * TILE + lane * piece, pg = t / a.page_size;
+            const int page = a.table[(int64_t)g.leader * a.max_pages + pg];
+            if (page >= 0 && page < a.n_pages) z = page;
+            y = g.h * a.page_size + (t - pg * a.page_size);
+        }
+    };
+    auto load = [&](const CUtensorMap* map, int which, int y, int z, int sl) -> bool {  // into slots sl ..
+        for (int db = 0; db < NDB; ++db, ++sl) {
+            const int st = sl % NS;
+            if (sl >= NS && !__all_sync(0xffffffffu, wait_or_abort(&empty[st], (uint32_t)((sl / NS - 1) & 1), abort_flag)))
+                return false;
+            const int slab = 2 * db + which;
+            const bool real = slab < nslab;
+            if (lane == 0) {
+                if (real) mbar_arrive_expect_tx(&full[st], SLAB); else mbar_arrive(&full[st]);
+                filled[6 * which + st] = sl / NS + 1;
+            }
+            __syncwarp();
+            if (real && lane < np)
+                tma_load_3d(smem_u32(sm) + st * SLOT + which * SLAB + lane * piece * 128, map, &full[st], slab * 64, y, z);
+        }
+        return true;
+    };
+    auto load_segment = [&](int which, int& sl0) -> bool {
+        const int n = g.tile1 - g.tile0;
+        int yv = 0, zv = 0, yk = 0, zk = 0, yn = 0, zn = 0;  // pieces of tiles j, j + 1, and j + 2 looked up ahead
+        bool ok = true;
+        look_up(g.tile0, yk, zk);
+        for (int j = -1; ok && j < n; ++j) {  // K of tile j + 1, V of tile j
+            if (j + 2 < n) look_up(g.tile0 + j + 2, yn, zn);
+            if (j + 1 < n) ok = load(&kmap, which, yk, zk, sl0 + L::k_slot(j + 1));
+            if (j >= 0) ok = ok && load(&vmap, which, yv, zv, sl0 + L::v_slot(j, n));
+            yv = yk;
+            zv = zk;
+            yk = yn;
+            zk = zn;
+        }
+        sl0 += 2 * NDB * n;
+        return ok;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------ the walk; K and V, lower slabs
+        PrefixWalk walk(s, blockIdx.x, gridDim.x);
+        int sl0 = 0;  // slots before
+        bool ok = true, more = true;
+        while (ok && more) {
+            g.tile0 = g.tile1 = 0;
+            more = walk.next(s, TILE, g);
+            const int e = sg % L::SEGS;
+            if (sg >= L::SEGS)
+                ok = __all_sync(0xffffffffu, wait_or_abort(&seg_empty[e], (uint32_t)((sg / L::SEGS - 1) & 1), abort_flag));
+            if (!ok) break;
+            if (lane == 0) {
+                notes[e] = g;
+                mbar_arrive(&seg_full[e]);
+            }
+            ++sg;
+            if (more) ok = load_segment(0, sl0);
+        }
+    } else if (warp == 3) {
+        // ------------------------------------------------ K and V, upper slabs
+        int sl0 = 0;
+        bool ok = true;
+        for (;;) {
+            const bool more = heard(ok);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || !more) break;
+            if (lane == 0) took_note();
+            ok = load_segment(1, sl0);
+            if (!ok) break;
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMAs (lane 0)
+        if (lane == 0) {
+            const uint32_t base = smem_u32(sm);
+            const int ksteps = (a.D + 15) / 16;
+            int it = 0, seg = 0, sl0 = 0;  // tiles, segments and slots before
+            auto slot_full = [&](int k) { return wait_or_abort(&full[k % NS], (uint32_t)((k / NS) & 1), abort_flag); };
+            auto issue_s = [&](int t, int k0) -> bool {  // S of the CTA's tile t, its K from slot k0 on
+                for (int db = 0; db < NDB; ++db) {
+                    const int k = k0 + db;
+                    if (!slot_full(k)) return false;
+                    tc_fence_after();
+                    const int steps = ksteps - 8 * db;
+                    const uint32_t ka = desc_lo(base + (k % NS) * SLOT, 16);
+                    const uint32_t qa = desc_lo(base + L::O_Q + db * SLOT, 16);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (q < steps)
+                            mma_lo(tb + L::T_S + (t & 1) * TILE, qa + (((q >> 2) * SLAB + (q & 3) * 32) >> 4),
+                                   ka + (((q >> 2) * SLAB + (q & 3) * 32) >> 4), idesc_bf16_f32(ROWS, TILE, 0, 0),
+                                   db > 0 || q > 0);
+                    mma_commit(&empty[k % NS]);
+                }
+                mma_commit(&s_full[t & 1]);
+                return true;
+            };
+            bool ok = true;
+            while (ok && heard(ok)) {
+                took_note();
+                const int n = g.tile1 - g.tile0;
+                ok = wait_or_abort(q_full, (uint32_t)(seg & 1), abort_flag);
+                ++seg;
+                for (int j = -1; ok && j < n; ++j) {  // S of tile j + 1, then P V of tile j
+                    // (S of tile j + 1 overwrites P of tile j - 1, whose P V has been issued before it: MMAs of one
+                    // thread and shape run in order)
+                    if (j + 1 < n && !issue_s(it + (j < 0 ? 0 : 1), sl0 + L::k_slot(j + 1))) { ok = false; break; }
+                    if (j + 2 == n) mma_commit(q_empty);
+                    if (j < 0) continue;
+                    ok = it != a.stop_at;
+                    if (!ok) break;
+                    ok = wait_or_abort(&p_full[it & 1], (uint32_t)((it >> 1) & 1), abort_flag);
+                    if (!ok) break;
+                    for (int db = 0; db < NDB; ++db) {
+                        const int k = sl0 + L::v_slot(j, n) + db;
+                        if (!slot_full(k)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t va = desc_lo(base + (k % NS) * SLOT, SLAB);
+                        const uint32_t pa = tb + L::T_S + (it & 1) * TILE;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)  // 16 tokens: columns 8 (q % 2) of block q / 2's upper parts, then of its rests
+#pragma unroll
+                            for (int lo = 0; lo < 2; ++lo)
+                                mma_ts(tb + L::T_O + db * 128, pa + (q >> 1) * 32 + lo * 16 + (q & 1) * 8, va + q * (2048 >> 4),
+                                       idesc_bf16_f32(ROWS, 128, 0, 1), j > 0 || lo > 0 || q > 0);
+                        mma_commit(&empty[k % NS]);
+                    }
+                    if (!ok) break;
+                    mma_commit(&pv_done[it & 1]);
+                    ++it;
+                }
+                sl0 += 2 * NDB * n;
+            }
+            if (!ok) {  // MMAs that no commit above speaks of are waited for too
+                mma_commit(drained);
+                mbar_wait(drained, 0, kWaitNs);
+            }
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------ Q rows (zero beyond the block's rows and the head's dims)
+        int seg = 0;
+        bool ok = true;
+        for (;;) {
+            const bool more = heard(ok);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || !more) break;
+            if (lane == 0) took_note();
+            if (seg > 0) ok = __all_sync(0xffffffffu, wait_or_abort(q_empty, (uint32_t)((seg - 1) & 1), abort_flag));
+            if (!ok) break;
+            const uint32_t qs = smem_u32(sm) + L::O_Q;
+            for (int r1 = 0; r1 < ROWS; r1 += 32) {
+                // a lane finds its row, then the warp copies the 32 rows together
+                const int mine = r1 + lane;
+                const int64_t at = mine < g.nr ? prefix_row(a, g.seq0, g.h, g.r0 + mine) * a.D : -1;
+                constexpr int CH = 16 * NDB;  // pieces of 8 dims per row
+#pragma unroll 4
+                for (int e = lane; e < 32 * CH; e += 32) {
+                    const int r = e / CH, ch = e % CH;
+                    const int64_t from = __shfl_sync(0xffffffffu, at, r);
+                    const bool real = from >= 0 && ch * 8 < a.D;
+                    const bf16* src = static_cast<const bf16*>(a.q) + (real ? from + ch * 8 : 0);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     qs + (ch >> 3) * SLAB + sw128_off((uint32_t)(r1 + r), (uint32_t)(ch & 7) * 8)),
+                                 "l"(src), "r"(real ? 16 : 0)
+                                 : "memory");
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+            ++seg;
+        }
+    } else {
+        // ------------------------------------------------ softmax and outputs
+        const int wg = (warp - 4) >> 2, quad = warp & 3;
+        const int row = quad * 32 + lane;  // TMEM lane
+        const uint32_t tq = tb + ((uint32_t)(quad * 32) << 16);
+        float* m_s = reinterpret_cast<float*>(sm + L::O_M);
+        float* l_s = reinterpret_cast<float*>(sm + L::O_L);
+        int it = 0;        // tiles before
+        bool live = true;  // no wait gave up: outputs are written only then
+        auto wait = [&](uint64_t* bar, int k) {
+            live = __all_sync(0xffffffffu, live && wait_or_abort(bar, (uint32_t)(k & 1), abort_flag));
+        };
+        for (;;) {
+            bool ok;
+            const bool more = heard(ok);
+            if (softmax_any(!ok)) {  // the warps agree on a wait that gave up: they meet at barriers
+                live = false;
+                break;
+            }
+            if (!more) break;
+            if (lane == 0) took_note();
+            const int n = g.tile1 - g.tile0;
+            float l = 0.f, m_mine = kNone;  // sum of this warpgroup's tiles, and the maximum that it refers to
+            for (int j = 0; j < n; ++j, ++it) {
+                if ((it & 1) != wg) continue;
+                const uint32_t ts = tq + L::T_S + (it & 1) * TILE;
+                wait(&s_full[it & 1], it >> 1);
+                tc_fence_after();
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < TILE; c += 32) {
+                    float x[32];
+                    tmem_ld32(ts + c, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i]);
+                }
+                top *= a.scale_log2;
+                float m;
+                if (j == 0) {
+                    m = fmaxf(top, kNone);
+                } else {
+                    wait(&m_told[quad * 2 + ((it - 1) & 1)], (it - 1) >> 1);
+                    const float before = m_s[row];
+                    m = top > before + kSlack ? top : before;
+                    if (__any_sync(0xffffffffu, m != before)) {
+                        // ---- new maxima: the outputs so far are scaled to them
+                        const float f = ex2_approx(before - m);
+                        wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < 128 * NDB; c += 32) {
+                            float o[32];
+                            tmem_ld32(tq + L::T_O + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= f;
+                            tmem_st32(tq + L::T_O + c, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                m_s[row] = m;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m_told[quad * 2 + (it & 1)]);
+                if (m != m_mine) {
+                    l *= ex2_approx(m_mine - m);
+                    m_mine = m;
+                }
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int c = 0; c < TILE; c += 32) {
+                    float x[32];
+                    tmem_ld32(ts + c, x);
+                    tmem_wait_ld();
+                    uint32_t w[32];  // 16 columns of upper parts, 16 of rests
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 y = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]),
+                                                    make_float2(a.scale_log2, a.scale_log2), make_float2(-m, -m));
+                        const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                        sum = __fadd2_rn(sum, p);
+                        const uint32_t w0 = __float_as_uint(p.x), w1 = __float_as_uint(p.y);
+                        w[i] = __byte_perm(w0, w1, 0x7632);  // the upper halves: cut, not rounded
+                        // the rest, at least p's last bit: a rest of 0 would turn an infinite value into NaN
+                        const float2 rest = __fadd2_rn(make_float2(__uint_as_float(w0 | 1u), __uint_as_float(w1 | 1u)),
+                                                       make_float2(__uint_as_float((w0 & 0xffff0000u) | 0x80000000u),
+                                                                   __uint_as_float((w1 & 0xffff0000u) | 0x80000000u)));
+                        w[16 + i] = pack_bf16x2(rest.x, rest.y);
+                    }
+                    float st[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) st[i] = __uint_as_float(w[i]);
+                    tmem_st32(ts + c, st);
+                }
+                l += sum.x + sum.y;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[it & 1]);
+            }
+            // ---- sums and outputs of the segment
+            softmax_sync();
+            const float m = m_s[row];
+            l_s[wg * ROWS + row] = l * ex2_approx(m_mine - m);
+            wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
+            tc_fence_after();
+            softmax_sync();
+            const float sum = l_s[row] + l_s[ROWS + row];
+            const bool real = row < g.nr && live;
+            float *po, *slot = prefix_slot(s, blockIdx.x);
+            if (g.parts > 0) {
+                const int64_t at = real ? prefix_row(a, g.seq0, g.h, g.r0 + row) : 0;
+                po = s.pre_o + at * a.D;
+                if (real && wg == 0) s.pre_stat[at] = prefix_stat(m, sum, g.parts, row);
+            } else {
+                po = slot + 2 * ROWS + row * a.D;
+                if (real && wg == 0) {
+                    slot[row] = sum == 0.f ? -INFINITY : m;
+                    slot[ROWS + row] = sum;
+                }
+            }
+#pragma unroll 1
+            for (int c = wg * 64 * NDB; c < (wg + 1) * 64 * NDB; c += 32) {
+                float o[32];
+                tmem_ld32(tq + L::T_O + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    if (real && c + i < a.D) *reinterpret_cast<float4*>(po + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            }
+            tc_fence_before();
+            softmax_sync();  // O and the arrays are free
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && *abort_flag) {
+        for (int st = 0; st < NS; ++st) {  // let the copies in flight land before the CTA exits
+            const int n0 = filled[st], n1 = filled[6 + st];
+            if (n0 != n1) mbar_arrive(&full[st]);  // for the loading warp that gave up before this load
+            const int n = n0 > n1 ? n0 : n1;
+            if (n > 0) mbar_wait(&full[st], (uint32_t)((n - 1) & 1), kWaitNs);
+        }
+        atomicOr(&g_prefix_error, 1);
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tb, L::T_COLS);
+    }
+}
+
+template <int NDB>
+cudaError_t launch_ndb(const ShareArgs& s, int n_cta, int piece, cudaStream_t st) {
+    using L = Layout<NDB>;
+    CUtensorMap km, vm;
+    if (!encode_cache(&km, s.a.k_cache, s.a, piece) || !encode_cache(&vm, s.a.v_cache, s.a, piece)) return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(attn_prefix_tc_kernel<NDB>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attn_prefix_tc_kernel<NDB>, dim3((unsigned)n_cta), dim3(NT), L::SMEM, st, km, vm, s, piece);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_tc(const ShareArgs& s, int n_cta, cudaStream_t st) {
+    const int piece = page_piece(s.a.page_size);
+    return s.a.D <= 128 ? launch_ndb<1>(s, n_cta, piece, st) : launch_ndb<2>(s, n_cta, piece, st);
+}
+
+cudaError_t read_and_clear_prefix_error(cudaStream_t s, int* flags) {
+    int hf = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&hf, g_prefix_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return e;
+    *flags = hf;
+    if (hf != 0) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbolAsync(g_prefix_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    }
+    return e;
+}
+
+}  // namespace gdn

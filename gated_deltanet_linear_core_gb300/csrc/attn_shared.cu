@@ -1,0 +1,297 @@
+// gdn_attn_decode_shared: how a call is cut up, its plan and merge kernels.
+#include "attn_shared.cuh"
+#include "tc_ptx.cuh"
+
+namespace gdn {
+
+namespace {
+
+using namespace attn;
+
+constexpr int PT = 1024;  // threads of the plan
+constexpr int MT = 256;   // threads of a merge block
+
+// What every group shares in earnest, by one block: a warp (or, where there are few groups, several)
+// looks at a group's lengths.
+__global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
+    __shared__ int least_s[32], first_s[32], count_s[32], share_s[32];
+    const AttnArgs& a = s.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int32_t* skip = const_cast<int32_t*>(a.skip);
+    pdl_wait();
+    pdl_trigger();
+    for (int b = tid; b < a.B; b += PT) skip[b] = 0;  // of sequences in no group
+    __syncthreads();
+    const int per = s.G >= 32 ? 1 : 32 / s.G, at_once = 32 / per;  // warps per group, groups at once
+    int64_t before = 0;  // units of the groups before (warp 0)
+    for (int g0 = 0; g0 < s.G; g0 += at_once) {
+        const int mine = warp / per, g = g0 + mine;
+        const bool works = mine < at_once && g < s.G;
+        int lo = 0, hi = 0, least = INT32_MAX, first = INT32_MAX, count = 0;
+        if (works) {
+            group_bounds(s, g, lo, hi);
+#pragma unroll 4
+            for (int b = lo + (warp - mine * per) * 32 + lane; b < hi; b += per * 32) {
+                const int n = clamped_len(a, b);
+                if (n > 0) {  // sequences without a token see nothing and do not count
+                    least = min(least, n);
+                    first = min(first, b);
+                    ++count;
+                }
+            }
+        }
+        least = __reduce_min_sync(0xffffffffu, least);
+        first = __reduce_min_sync(0xffffffffu, first);
+        count = __reduce_add_sync(0xffffffffu, count);
+        if (lane == 0) {
+            least_s[warp] = least;
+            first_s[warp] = first;
+            count_s[warp] = count;
+        }
+        __syncthreads();
+        if (warp == 0) {  // lane i: group g0 + i
+            const int gi = g0 + lane;
+            int64_t units = 0;
+            if (lane < at_once && gi < s.G) {
+                least = first = INT32_MAX;
+                count = 0;
+                for (int w = lane * per; w < (lane + 1) * per; ++w) {
+                    least = min(least, least_s[w]);
+                    first = min(first, first_s[w]);
+                    count += count_s[w];
+                }
+                // less than the first new token of any sequence sees
+                int share = count > 1 ? min(s.prefix[gi], least - a.K) : 0;
+                share = share > 0 ? share / kShareStep * kShareStep : 0;
+                int seq0, seq1;
+                group_bounds(s, gi, seq0, seq1);
+                if (share > 0) units = group_blocks(s, seq1 - seq0) * a.H_kv * (s.setup + share / s.tile);
+                s.share[gi] = share_s[lane] = share;
+                s.leader[gi] = first == INT32_MAX ? 0 : first;
+            }
+            int64_t inc = units;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            if (lane < at_once && gi < s.G) s.unit0[gi] = before + inc - units;
+            before += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        __syncthreads();
+        if (works) {
+            const int share = share_s[mine];
+            if (share > 0)
+                for (int b = lo + (warp - mine * per) * 32 + lane; b < hi; b += per * 32)
+                    if (clamped_len(a, b) > 0) skip[b] = share;
+        }
+        __syncthreads();
+    }
+    if (tid == 0) s.unit0[s.G] = before;
+}
+
+struct Running {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    template <int U>
+    __device__ __forceinline__ void add(const float (&m1)[U], const float (&l1)[U], const float4 (&x)[U]) {
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < U; ++k) top = fmaxf(top, m1[k]);
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float f = tc::ex2_approx(m - ref);
+        m = top;
+        l *= f;
+        o.x *= f; o.y *= f; o.z *= f; o.w *= f;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const float w = tc::ex2_approx(m1[k] - ref);
+            l = fmaf(l1[k], w, l);
+            o.x = fmaf(x[k].x, w, o.x); o.y = fmaf(x[k].y, w, o.y);
+            o.z = fmaf(x[k].z, w, o.z); o.w = fmaf(x[k].w, w, o.w);
+        }
+    }
+};
+
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 ld4(const bf16* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 y) { *reinterpret_cast<float4*>(p) = y; }
+__device__ __forceinline__ void store4(bf16* p, float4 y) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+}
+
+// A row's parts: those of its own tokens, then the prefix's.
+struct Parts {
+    int n_own, n;       // CTAs
+    int c_own, c_pre;   // the first of each
+    int r_own, r_pre;   // the row in its blocks
+};
+
+// Puts a row's parts together: the running maximum, sum and output over the parts in CTA
+// order.  A group of threads (4 columns each) takes a row; where a row of the block has many
+// parts, the groups take each row together.
+template <typename T>
+__global__ void __launch_bounds__(MT) attn_merge_kernel(ShareArgs s) {
+    constexpr int U = 4;  // parts at once
+    constexpr int kSerial = 8;
+    __shared__ float4 o_s[MT];
+    __shared__ float2 ml_s[MT];
+    const AttnArgs& a = s.a;
+    const int ng = blockDim.x, groups = blockDim.y, g = threadIdx.y, tid = g * ng + threadIdx.x, d = threadIdx.x * 4;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t rows = (int64_t)a.B * a.K * a.H_q, row0 = (int64_t)blockIdx.x * groups;
+    auto parts_of = [&](int64_t row) -> Parts {
+        Parts p = {};
+        const int b = (int)(row / (a.K * a.H_q)), rest = (int)(row - (int64_t)b * a.K * a.H_q);
+        const int i = rest / a.H_q, hq = rest - i * a.H_q;
+        if (clamped_len(a, b) - (a.K - 1 - i) <= 0) return p;  // sees nothing
+        const float4 own = a.part_stat[row];
+        p.c_own = __float_as_int(own.z);
+        p.n_own = __float_as_int(own.w);
+        p.r_own = (i * a.group + hq % a.group) % a.rb_rows;
+        p.n = p.n_own;
+        if (a.skip[b] > 0) {
+            const float4 pre = s.pre_stat[row];
+            p.c_pre = __float_as_int(pre.z) & 0xffff;
+            p.r_pre = __float_as_int(pre.w);
+            p.n += __float_as_int(pre.z) >> 16;
+        }
+        // (the bounds hold for every call that keeps to the rules; they keep others' reads in bounds)
+        const int n_pre = p.n - p.n_own;
+        if ((unsigned)p.c_own >= kAttnMaxCtas || (unsigned)p.n_own > kAttnMaxCtas || p.c_own + p.n_own > kAttnMaxCtas ||
+            (unsigned)p.c_pre >= kAttnMaxCtas || (unsigned)n_pre > kAttnMaxCtas || p.c_pre + n_pre > kAttnMaxCtas ||
+            (unsigned)p.r_pre >= (unsigned)s.rows_per_block)
+            p.n = p.n_own = 0;
+        return p;
+    };
+    // parts from .. in steps of `step`
+    auto add_parts = [&](Running& run, const Parts& p, int64_t row, int from, int step) {
+#pragma unroll 1
+        for (int k0 = from; k0 < p.n; k0 += U * step) {
+            float m[U], l[U];
+            float4 x[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int part = k0 + k * step;
+                m[k] = -INFINITY;
+                l[k] = 0.f;
+                x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (part >= p.n) continue;
+                const bool own = part < p.n_own;
+                const int nth = own ? part : part - p.n_own;
+                if (nth == 0) {
+                    const float4 st = own ? a.part_stat[row] : s.pre_stat[row];
+                    m[k] = st.x;
+                    l[k] = st.y;
+                    x[k] = ld4((own ? a.part_o : s.pre_o) + row * a.D + d);
+                } else {
+                    const float* slot = own ? slot_ptr(a, p.c_own + nth) : prefix_slot(s, p.c_pre + nth);
+                    const int r = own ? p.r_own : p.r_pre, per = own ? a.rb_rows : s.rows_per_block;
+                    m[k] = slot[r];
+                    l[k] = slot[per + r];
+                    x[k] = ld4(slot + (own ? a.stat_floats : 2 * per) + r * a.D + d);
+                }
+            }
+            run.add(m, l, x);
+        }
+    };
+    auto write = [&](const Running& run, int64_t row) {
+        const int64_t at = row * a.D + d;
+        const float inv = run.l == 0.f ? 0.f : 1.0f / run.l;
+        float4 y = make_float4(run.o.x * inv, run.o.y * inv, run.o.z * inv, run.o.w * inv);
+        if (a.gate != nullptr && run.l != 0.f) {  // a row that sees nothing is 0 whatever its gate holds
+            const float4 gt = ld4(static_cast<const T*>(a.gate) + at);
+            y.x *= sigmoid_f(gt.x); y.y *= sigmoid_f(gt.y); y.z *= sigmoid_f(gt.z); y.w *= sigmoid_f(gt.w);
+        }
+        store4(static_cast<T*>(a.out) + at, y);
+        if (d == 0 && a.lse != nullptr) a.lse[row] = run.l == 0.f ? -INFINITY : (run.m + log2f(run.l)) * kLn2;
+    };
+    const int64_t mine = row0 + g;
+    Parts p = {};
+    if (mine < rows) p = parts_of(mine);
+    if (!__syncthreads_or(p.n > kSerial)) {
+        if (mine < rows) {
+            Running run;
+            add_parts(run, p, mine, 0, 1);
+            write(run, mine);
+        }
+        return;
+    }
+    for (int i = 0; i < groups && row0 + i < rows; ++i) {
+        const int64_t row = row0 + i;
+        const Parts q = parts_of(row);
+        Running run;
+        add_parts(run, q, row, g, groups);
+        o_s[tid] = run.o;
+        ml_s[tid] = make_float2(run.m, run.l);
+        __syncthreads();
+        if (g == i) {
+            run = Running();
+#pragma unroll 1
+            for (int k = 0; k < groups; ++k) {
+                const int t = k * ng + threadIdx.x;
+                const float m[1] = {ml_s[t].x}, l[1] = {ml_s[t].y};
+                const float4 x[1] = {o_s[t]};
+                run.add(m, l, x);
+            }
+            write(run, row);
+        }
+        __syncthreads();
+    }
+}
+
+size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace
+
+size_t attn_share_plan(ShareArgs& s, gdn_dtype_t dt, void* ws) {
+    AttnArgs& a = s.a;
+    attn_plan(a, dt);
+    const bool tc = attn_tc_takes(a, dt);
+    s.rows_per_block = tc ? 128 : kPrefixFfmaRows;
+    s.tile = tc ? 128 : 64;
+    s.setup = 1;
+    s.pre_slot_floats = 2 * s.rows_per_block + (int64_t)s.rows_per_block * a.D;
+    const size_t rows = (size_t)a.B * a.K * a.H_q;
+    char* base = reinterpret_cast<char*>(up(reinterpret_cast<size_t>(ws)));
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        char* p = base + at;
+        at += up(bytes);
+        return p;
+    };
+    a.ws = reinterpret_cast<float*>(take(kAttnMaxCtas * (sizeof(JoinTask) + (size_t)a.slot_floats * sizeof(float))));
+    s.pre_slots = reinterpret_cast<float*>(take(kAttnMaxCtas * (size_t)s.pre_slot_floats * sizeof(float)));
+    a.part_o = reinterpret_cast<float*>(take(rows * a.D * sizeof(float)));
+    s.pre_o = reinterpret_cast<float*>(take(rows * a.D * sizeof(float)));
+    a.part_stat = reinterpret_cast<float4*>(take(rows * sizeof(float4)));
+    s.pre_stat = reinterpret_cast<float4*>(take(rows * sizeof(float4)));
+    s.unit0 = reinterpret_cast<int64_t*>(take(((size_t)s.G + 1) * sizeof(int64_t)));
+    s.share = reinterpret_cast<int32_t*>(take((size_t)s.G * sizeof(int32_t)));
+    s.leader = reinterpret_cast<int32_t*>(take((size_t)s.G * sizeof(int32_t)));
+    a.skip = reinterpret_cast<int32_t*>(take((size_t)a.B * sizeof(int32_t)));
+    return at + 256;
+}
+
+cudaError_t launch_attn_shared(const ShareArgs& s, gdn_dtype_t dt, cudaStream_t st) {
+    const AttnArgs& a = s.a;
+    if (a.B == 0 || a.K == 0) return cudaSuccess;
+    const int n_cta = attn_ctas();
+    const bool tc = attn_tc_takes(a, dt);
+    cudaError_t e = launch_pdl(attn_share_plan_kernel, dim3(1), dim3(PT), 0, st, s);
+    if (e == cudaSuccess) e = tc ? launch_prefix_tc(s, n_cta, st) : launch_prefix_ffma(s, n_cta, dt, st);
+    if (e == cudaSuccess) e = tc ? launch_attn_tc(a, n_cta, st) : launch_attn_ffma(a, n_cta, dt, st);
+    if (e != cudaSuccess) return e;
+    const int ng = a.D / 4, groups = MT / ng;
+    const int64_t rows = (int64_t)a.B * a.K * a.H_q;
+    const dim3 grid((unsigned)((rows + groups - 1) / groups)), block((unsigned)ng, (unsigned)groups);
+    return dt == GDN_BF16 ? launch_pdl(attn_merge_kernel<bf16>, grid, block, 0, st, s)
+                          : launch_pdl(attn_merge_kernel<float>, grid, block, 0, st, s);
+}
+
+}  // namespace gdn

@@ -35,10 +35,7 @@
 // the outputs stand between two segments.  Every wait is bounded (1 s): on a
 // timeout the roles run out without waiting, the copies in flight land, TMEM is
 // freed and the error word is set.
-#include <cuda.h>
-
-#include "attn_common.cuh"
-#include "tc_ptx.cuh"
+#include "attn_tc_common.cuh"
 
 namespace gdn {
 
@@ -48,12 +45,6 @@ namespace {
 
 using namespace attn;
 using namespace tc;
-
-constexpr int TILE = 128;
-constexpr int SLAB = TILE * 128;      // bytes of 128 tokens x 64 dims
-constexpr int SLOT = 2 * SLAB;        // ... x 128 dims
-constexpr uint64_t kWaitNs = 1000000000ull;
-constexpr int kSmemMax = 232448;
 
 template <int N, int NDB>
 struct Layout {
@@ -124,22 +115,6 @@ struct alignas(16) SegmentNote {
 };
 static_assert(sizeof(SegmentNote) == 32, "notes");
 
-// Bounded wait; returns at once when another role has given up.
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    if (mbar_test(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_test(bar, parity)) return true;
-        if ((it & 31) == 0) {
-            if (*abort_flag) return false;
-            if (globaltimer_ns() - t0 > kWaitNs) {
-                *abort_flag = 1;
-                return false;
-            }
-        }
-    }
-}
-
 // The same for a slot's position counter to reach `pos`.
 __device__ __forceinline__ bool loaded_or_abort(volatile int* filled, int pos, volatile int* abort_flag) {
     if (*filled >= pos) return true;
@@ -156,13 +131,6 @@ __device__ __forceinline__ bool loaded_or_abort(volatile int* filled, int pos, v
     }
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
 template <int NTHR>
 __device__ __forceinline__ void softmax_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
@@ -218,21 +186,7 @@ __device__ __forceinline__ uint32_t zero_non_finite(uint32_t w) {
     return w;
 }
 
-// Operand descriptors by their low words (address and lbo in units of 16 bytes); the high word is the same for
-// all (sbo 1024, version, 128-byte swizzle: sdesc_sw128).
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
-__device__ __forceinline__ void mma_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
-    constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
-        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(hi)
-        : "memory");
-}
-
-template <int N, int NDB>
+template <int N, int NDB, bool SHARED>
 __global__ void __launch_bounds__(Layout<N, NDB>::NT, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a,
                int piece) {
@@ -348,14 +302,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     if (warp == 0) {
         // ------------------------------------------------ K and V
         int n_cta = gridDim.x;
-        const Place place = find_place(a, TILE, blockIdx.x, n_cta);
+        const Place place = find_place<SHARED>(a, TILE, blockIdx.x, n_cta);
         const bool works = (int)blockIdx.x < n_cta;
-        Walk walk(place, works ? cta_begin(place.total, blockIdx.x, n_cta) : 0,
+        Walk<SHARED> walk(place, works ? cta_begin(place.total, blockIdx.x, n_cta) : 0,
                   works ? cta_begin(place.total, blockIdx.x + 1, n_cta) : 0);
         int sl0 = 0;  // slots before
         bool ok = true, more = true;
         while (ok && more) {
             more = walk.next(a, TILE, s);
+            if constexpr (SHARED)
+                if (more && s.tiles == 2) s.tiles = count_parts(a, place, walk, s, TILE, blockIdx.x, n_cta);
             const int e = sg % L::SEGS;
             if (sg >= L::SEGS)
                 ok = __all_sync(0xffffffffu, wait_or_abort(&seg_empty[e], (uint32_t)((sg / L::SEGS - 1) & 1), abort_flag));
@@ -379,7 +335,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 zk = zn;
             }
             sl0 += 2 * NDB * n;
-            if (sg == 1 && lane == 0) write_join_task(a, place, walk, more ? &s : nullptr, blockIdx.x, n_cta);
+            if constexpr (!SHARED)
+                if (sg == 1 && lane == 0) write_join_task(a, place, walk, more ? &s : nullptr, blockIdx.x, n_cta);
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMAs (lane 0)
@@ -538,6 +495,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 if (!more) return false;
                 if (lane == 0) took_note();
                 if (s.len > 0) return true;
+                if (SHARED) continue;  // the merge's
                 const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
                 for (int e = st; e < nr * a.D; e += NSOFT) {
                     const int r = e / a.D, d = e - r * a.D;
@@ -550,7 +508,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         // Sums and outputs of a segment whose last tile is handed to the MMA warp.
         auto finish_segment = [&](const Segment& s, float (&l)[CPT]) {
             const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
-            const bool whole = s.tile1 - s.tile0 == s.tiles;
+            const bool whole = !SHARED && s.tile1 - s.tile0 == s.tiles;
             // sums over the tokens: the lanes, then the warps
             join_lanes<CPT>(l, lane, [](float x, float y) { return x + y; });
             // the output loop below has this many rounds per 128 dims; the gate's values are loaded two rounds ahead
@@ -575,7 +533,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             if constexpr (CPT == 64) *reinterpret_cast<float2*>(scr_w + 2 * lane) = make_float2(l[0], l[1]);
             else if (CPT == 32 || (lane & 1) == 0) scr_w[CPT == 32 ? lane : lane >> 1] = l[0];
             softmax_sync<NSOFT>();
-            float* slot = slot_ptr(a, part_slot(s));
+            float* slot = slot_ptr(a, SHARED ? blockIdx.x : part_slot(s));
             for (int c = st; c < nr; c += NSOFT) {
                 const float sum = (sum_s[c] + sum_s[N + c]) + (sum_s[2 * N + c] + sum_s[3 * N + c]);
                 const float m = -n_s[c];
@@ -584,6 +542,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     if (whole) {
                         if (a.lse != nullptr)
                             a.lse[out_row(c)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+                    } else if (SHARED && s.tiles > 0) {
+                        a.part_stat[out_row(c)] = make_float4(sum == 0.f ? -INFINITY : m, sum, __int_as_float(blockIdx.x),
+                                                              __int_as_float(s.tiles));
                     } else {
                         slot[c] = sum == 0.f ? -INFINITY : m;
                         slot[a.rb_rows + c] = sum;
@@ -653,7 +614,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         }
                         store16<bf16>(static_cast<bf16*>(a.out) + at, y);
                     } else {
-                        float* p = slot + a.stat_floats + r * a.D + d;
+                        float* p = SHARED && s.tiles > 0 ? a.part_o + out_row(r) * a.D + d : slot + a.stat_floats + r * a.D + d;
                         *reinterpret_cast<float4*>(p) = x0;
                         *reinterpret_cast<float4*>(p + 4) = x1;
                     }
@@ -831,51 +792,36 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     }
 }
 
-bool encode_cache(CUtensorMap* map, const void* base, const AttnArgs& a, int piece) {
-    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensormap_encoder();
-    if (enc == nullptr) return false;
-    cuuint64_t dim[3] = {(cuuint64_t)a.D, (cuuint64_t)a.H_kv * a.page_size, (cuuint64_t)a.n_pages};
-    cuuint64_t str[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.D * 2 * a.H_kv * a.page_size};
-    cuuint32_t box[3] = {64, (cuuint32_t)piece, 1};
-    cuuint32_t es[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dim, str, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <int N, int NDB>
+template <int N, int NDB, bool SHARED>
 cudaError_t launch_tc(const AttnArgs& a, int n_cta, int piece, cudaStream_t s) {
     using L = Layout<N, NDB>;
     CUtensorMap km, vm;
     if (!encode_cache(&km, a.k_cache, a, piece) || !encode_cache(&vm, a.v_cache, a, piece)) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<N, NDB>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<N, NDB, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_tc_kernel<N, NDB>, dim3((unsigned)n_cta), dim3(L::NT), L::SMEM, s, km, vm, a, piece);
+    return launch_pdl(attn_tc_kernel<N, NDB, SHARED>, dim3((unsigned)n_cta), dim3(L::NT), L::SMEM, s, km, vm, a, piece);
 }
 
-template <int NDB>
+template <int NDB, bool SHARED>
 cudaError_t launch_rows(const AttnArgs& a, int n_cta, int piece, cudaStream_t s) {
-    return a.rb_rows <= 16 ? launch_tc<16, NDB>(a, n_cta, piece, s)
-         : a.rb_rows <= 32 ? launch_tc<32, NDB>(a, n_cta, piece, s)
-         : a.rb_rows <= 64 ? launch_tc<64, NDB>(a, n_cta, piece, s) : launch_tc<128, NDB>(a, n_cta, piece, s);
-}
-
-// Rows of a page that one TMA box takes: the largest power of two that divides the page size, a tile at most.
-int page_piece(int page_size) {
-    const int p = page_size & -page_size;
-    return p < TILE ? p : TILE;
+    return a.rb_rows <= 16 ? launch_tc<16, NDB, SHARED>(a, n_cta, piece, s)
+         : a.rb_rows <= 32 ? launch_tc<32, NDB, SHARED>(a, n_cta, piece, s)
+         : a.rb_rows <= 64 ? launch_tc<64, NDB, SHARED>(a, n_cta, piece, s)
+                           : launch_tc<128, NDB, SHARED>(a, n_cta, piece, s);
 }
 
 }  // namespace
 
 bool attn_tc_takes(const AttnArgs& a, gdn_dtype_t dt) {
     // a lane loads one piece: 32 pieces of 4 tokens make a tile
-    return dt == GDN_BF16 && page_piece(a.page_size) >= TILE / 32;
+    return dt == GDN_BF16 && attn_tc_pages(a.page_size);
 }
+bool attn_tc_pages(int page_size) { return page_piece(page_size) >= TILE / 32; }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, int n_cta, cudaStream_t s) {
     const int piece = page_piece(a.page_size);
-    const cudaError_t e = a.D <= 128 ? launch_rows<1>(a, n_cta, piece, s) : launch_rows<2>(a, n_cta, piece, s);
+    if (a.skip != nullptr) return a.D <= 128 ? launch_rows<1, true>(a, n_cta, piece, s) : launch_rows<2, true>(a, n_cta, piece, s);
+    const cudaError_t e = a.D <= 128 ? launch_rows<1, false>(a, n_cta, piece, s) : launch_rows<2, false>(a, n_cta, piece, s);
     return e != cudaSuccess ? e : launch_attn_join(a, n_cta, GDN_BF16, s);
 }
 

@@ -120,12 +120,13 @@ gdn_status_t gdn_check_cu_seqlens(const int32_t* cu, int32_t n_seq, int64_t T, v
 }
 
 gdn_status_t gdn_sync_status(void* stream) {
-    int flags = 0, cflags = 0, aflags = 0;
+    int flags = 0, cflags = 0, aflags = 0, pflags = 0;
     cudaError_t e = gdn::read_and_clear_device_error((cudaStream_t)stream, &flags);
     if (e == cudaSuccess) e = gdn::read_and_clear_conv_error((cudaStream_t)stream, &cflags);
     if (e == cudaSuccess) e = gdn::read_and_clear_attn_error((cudaStream_t)stream, &aflags);
+    if (e == cudaSuccess) e = gdn::read_and_clear_prefix_error((cudaStream_t)stream, &pflags);
     if (e != cudaSuccess) return cuda_status(e);
-    return ((flags | cflags | aflags) & 1) ? GDN_ERR_TIMEOUT : GDN_OK;
+    return ((flags | cflags | aflags | pflags) & 1) ? GDN_ERR_TIMEOUT : GDN_OK;
 }
 
 size_t gdn_layer_prefill_host_workspace_size(int64_t T, gdn_dims_t dims, gdn_dtype_t dtype) {
@@ -820,6 +821,75 @@ gdn_status_t gdn_selftest_attn_decode(const void* q, const void* k_cache, const 
     if (page_size % 4 != 0) return GDN_ERR_UNSUPPORTED;  // the CUDA-core kernel waits for nothing
     return attn_decode(q, k_cache, v_cache, page_table, seq_lens, 0.f, nullptr, out, nullptr, B, K, H_q, H_kv, D,
                        page_size, n_pages, max_pages, workspace, ws_bytes, GDN_BF16, stop_at, stream);
+}
+
+namespace {
+gdn_status_t fill_shared(gdn::ShareArgs& s, int32_t B, int32_t K, int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size,
+                         int32_t n_pages, int32_t max_pages, int32_t G, gdn_dtype_t dt) {
+    memset(&s, 0, sizeof(s));
+    const gdn_status_t st = fill_attn(s.a, B, K, H_q, H_kv, D, page_size, n_pages, max_pages, dt);
+    if (st != GDN_OK) return st;
+    if (G < 1 || G > (1 << 24)) return GDN_ERR_INVALID_ARG;
+    if ((int64_t)B * K * H_q > (1 << 30)) return GDN_ERR_UNSUPPORTED;  // rows fit 31 bits
+    s.G = G;
+    return GDN_OK;
+}
+
+gdn_status_t attn_decode_shared(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                                const int32_t* seq_lens, const int32_t* prefix_lens, const int32_t* cu_groups, float scale,
+                                const void* gate, void* out, float* lse, int32_t B, int32_t K, int32_t H_q, int32_t H_kv,
+                                int32_t D, int32_t page_size, int32_t n_pages, int32_t max_pages, int32_t G, void* workspace,
+                                size_t ws_bytes, gdn_dtype_t dtype, int32_t stop_at, void* stream) {
+    gdn::ShareArgs s;
+    const gdn_status_t st = fill_shared(s, B, K, H_q, H_kv, D, page_size, n_pages, max_pages, G, dtype);
+    if (st != GDN_OK) return st;
+    if (!isfinite(scale) || scale < 0.f || (cu_groups == nullptr && G != 1)) return GDN_ERR_INVALID_ARG;
+    if (B == 0 || K == 0) return GDN_OK;
+    if (q == nullptr || k_cache == nullptr || v_cache == nullptr || page_table == nullptr || seq_lens == nullptr ||
+        prefix_lens == nullptr || out == nullptr)
+        return GDN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned_n(page_table, 4) ||
+        !aligned_n(seq_lens, 4) || !aligned_n(prefix_lens, 4) || !aligned_n(cu_groups, 4) || !aligned16(gate) ||
+        !aligned16(out) || !aligned_n(lse, 4) || !aligned16(workspace))
+        return GDN_ERR_ALIGN;
+    gdn::AttnArgs& a = s.a;
+    a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.table = page_table; a.lens = seq_lens;
+    a.gate = gate; a.out = out; a.lse = lse;
+    a.stop_at = stop_at;
+    a.scale_log2 = (scale == 0.f ? 1.0f / sqrtf((float)D) : scale) * 1.4426950408889634f;
+    s.prefix = prefix_lens; s.cu = cu_groups;
+    const size_t need = gdn::attn_share_plan(s, dtype, workspace);
+    if (workspace == nullptr || ws_bytes < need) return GDN_ERR_WORKSPACE;
+    return cuda_status(gdn::launch_attn_shared(s, dtype, (cudaStream_t)stream));
+}
+}  // namespace
+
+size_t gdn_attn_decode_shared_workspace_size(int32_t B, int32_t K, int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size,
+                                             int32_t G, gdn_dtype_t dtype) {
+    gdn::ShareArgs s;
+    if (fill_shared(s, B, K, H_q, H_kv, D, page_size, 1, 1, G, dtype) != GDN_OK || B == 0 || K == 0) return 0;
+    return gdn::attn_share_plan(s, dtype, nullptr);
+}
+
+gdn_status_t gdn_attn_decode_shared(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                                    const int32_t* seq_lens, const int32_t* prefix_lens, const int32_t* cu_groups,
+                                    float scale, const void* gate, void* out, float* lse, int32_t B, int32_t K, int32_t H_q,
+                                    int32_t H_kv, int32_t D, int32_t page_size, int32_t n_pages, int32_t max_pages, int32_t G,
+                                    void* workspace, size_t ws_bytes, gdn_dtype_t dtype, void* stream) {
+    return attn_decode_shared(q, k_cache, v_cache, page_table, seq_lens, prefix_lens, cu_groups, scale, gate, out, lse, B, K,
+                              H_q, H_kv, D, page_size, n_pages, max_pages, G, workspace, ws_bytes, dtype, -1, stream);
+}
+
+gdn_status_t gdn_selftest_attn_decode_shared(const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* page_table, const int32_t* seq_lens, const int32_t* prefix_lens,
+                                             void* out, int32_t B, int32_t K, int32_t H_q, int32_t H_kv, int32_t D,
+                                             int32_t page_size, int32_t n_pages, int32_t max_pages, void* workspace,
+                                             size_t ws_bytes, int32_t stop_at, void* stream) {
+    if (stop_at < 0) return GDN_ERR_INVALID_ARG;
+    if (page_size % 4 != 0) return GDN_ERR_UNSUPPORTED;  // the CUDA-core kernels wait for nothing
+    return attn_decode_shared(q, k_cache, v_cache, page_table, seq_lens, prefix_lens, nullptr, 0.f, nullptr, out, nullptr, B,
+                              K, H_q, H_kv, D, page_size, n_pages, max_pages, 1, workspace, ws_bytes, GDN_BF16, stop_at,
+                              stream);
 }
 
 gdn_status_t gdn_draft_accept(const void* p, const void* q, const int32_t* draft, const float* u,

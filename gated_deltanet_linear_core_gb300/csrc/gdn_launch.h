@@ -171,11 +171,16 @@ struct AttnArgs {
     int rb_rows, n_rb;     // rows per row block, row blocks
     int setup;             // units that starting an item counts as, beside its tiles
     int stop_at;           // self-test: the MMAs stop at a CTA's tile of this number (-1: never)
+    // behind shared prefixes (gdn_attn_decode_shared); null otherwise
+    const int32_t* skip;   // [B] tokens that the pass over the prefixes has taken, a multiple of kShareStep
+    float* part_o;         // [B, K, H_q, D] the items' first parts: unnormalised outputs,
+    float4* part_stat;     // [B, K, H_q] maximum, sum, first CTA, number of CTAs
 };
 constexpr int kAttnMaxK = 16;
 constexpr int kAttnMaxCtas = 152;  // CTAs of a call, at most: one per SM
 // Fills the derived fields from the sizes; returns the workspace bytes.
 size_t attn_plan(AttnArgs& a, gdn_dtype_t dt);
+int attn_ctas();
 cudaError_t launch_attn_decode(const AttnArgs& a, gdn_dtype_t dt, cudaStream_t s);
 constexpr int kAttnFfmaRows = 8;  // rows per block of launch_attn_ffma, at most
 cudaError_t launch_attn_ffma(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaStream_t s);
@@ -183,7 +188,31 @@ cudaError_t launch_attn_ffma(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaS
 bool attn_tc_takes(const AttnArgs& a, gdn_dtype_t dt);
 cudaError_t launch_attn_tc(const AttnArgs& a, int n_cta, cudaStream_t s);
 cudaError_t read_and_clear_attn_error(cudaStream_t s, int* flags);
+bool attn_tc_pages(int page_size);  // page sizes that its loads take
 cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaStream_t s);
+
+// Attention behind shared prefixes (gdn_attn_decode_shared): a pass over the prefixes, one over what
+// each sequence has of its own (the kernels above), and a merge of both (attn_shared.cuh).
+constexpr int kPrefixFfmaRows = 64;
+constexpr int kShareStep = 128;  // a prefix is shared down to a multiple of this many tokens
+struct ShareArgs {
+    AttnArgs a;                        // the sequences' own tokens
+    const int32_t *prefix, *cu;        // [G] tokens; [G + 1] sequences or null: one group
+    int G;
+    int rows_per_block, tile, setup;   // of the pass over the prefixes: rows and tokens per tile, units of an item's start
+    int32_t *share, *leader;           // [G] tokens that are shared in earnest; the sequence whose pages are read
+    int64_t* unit0;                    // [G + 1] first unit of the groups' items
+    float* pre_o;                      // [B, K, H_q, D], [B, K, H_q]: the prefix items' first parts, as a.part_o and a.part_stat
+    float4* pre_stat;
+    float* pre_slots;                  // per CTA: a part that starts inside an item
+    int64_t pre_slot_floats;
+};
+// Fills the derived fields from the sizes (and with a workspace the pointers into it); returns the workspace bytes.
+size_t attn_share_plan(ShareArgs& s, gdn_dtype_t dt, void* ws);
+cudaError_t launch_attn_shared(const ShareArgs& s, gdn_dtype_t dt, cudaStream_t st);
+cudaError_t launch_prefix_tc(const ShareArgs& s, int n_cta, cudaStream_t st);
+cudaError_t launch_prefix_ffma(const ShareArgs& s, int n_cta, gdn_dtype_t dt, cudaStream_t st);
+cudaError_t read_and_clear_prefix_error(cudaStream_t s, int* flags);
 
 // New keys and values into their pages (gdn_kv_append).
 struct KvAppendArgs {

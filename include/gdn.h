@@ -246,6 +246,12 @@ gdn_status_t gdn_selftest_attn_decode(const void* q, const void* k_cache, const 
                                       int32_t K, int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size,
                                       int32_t n_pages, int32_t max_pages, void* workspace, size_t ws_bytes,
                                       int32_t stop_at, void* stream);
+/* The same for gdn_attn_decode_shared with one group of all sequences. */
+gdn_status_t gdn_selftest_attn_decode_shared(const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* page_table, const int32_t* seq_lens, const int32_t* prefix_lens,
+                                             void* out, int32_t B, int32_t K, int32_t H_q, int32_t H_kv, int32_t D,
+                                             int32_t page_size, int32_t n_pages, int32_t max_pages, void* workspace,
+                                             size_t ws_bytes, int32_t stop_at, void* stream);
 
 /*
  * Number of kernel launches one gdn_chunk_prefill call with these sizes and
@@ -607,6 +613,33 @@ gdn_status_t gdn_attn_decode(const void* q, const void* k_cache, const void* v_c
                              int32_t B, int32_t K, int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size,
                              int32_t n_pages, int32_t max_pages, void* workspace, size_t ws_bytes,
                              gdn_dtype_t dtype, void* stream);
+
+/*
+ * gdn_attn_decode of a batch whose sequences share long prefixes (samples of one
+ * prompt, questions about one document): a group's common tokens are read, and
+ * attended to, once for all of its sequences.  Group g is the sequences
+ * cu_groups[g] .. cu_groups[g + 1] - 1; their first prefix_lens[g] positions hold the same
+ * keys and values (the same pages, or copies as where a prefix ends inside a page), which are read
+ * through the page table of one of them.  Definition, caches, lengths (seq_lens counts the
+ * prefix and the new tokens) and outputs are gdn_attn_decode's: sharing changes how
+ * sums are ordered, no result beyond rounding.  A prefix is shared down to a multiple of 128 tokens
+ * and as far as every new token of the group's sequences sees it (sequences of length 0 aside); a prefix
+ * length of 0 or less shares nothing, nor does a group of one sequence or a sequence of no group.
+ *   prefix_lens (device) [G] int32
+ *   cu_groups  (device) [G + 1] int32, not decreasing, or NULL: one group (G = 1) of all sequences
+ *   workspace  (device) >= gdn_attn_decode_shared_workspace_size bytes; calls that may
+ *              run at the same time need one each.  Its contents do not matter.
+ *   other arguments as gdn_attn_decode's;  B K H_q <= 2^30
+ * Nothing synchronises, and a captured call follows lengths, groups and prefix lengths.
+ * Results do not depend on timing.
+ */
+size_t gdn_attn_decode_shared_workspace_size(int32_t B, int32_t K, int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size,
+                                             int32_t G, gdn_dtype_t dtype);
+gdn_status_t gdn_attn_decode_shared(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                                    const int32_t* seq_lens, const int32_t* prefix_lens, const int32_t* cu_groups,
+                                    float scale, const void* gate, void* out, float* lse, int32_t B, int32_t K, int32_t H_q,
+                                    int32_t H_kv, int32_t D, int32_t page_size, int32_t n_pages, int32_t max_pages, int32_t G,
+                                    void* workspace, size_t ws_bytes, gdn_dtype_t dtype, void* stream);
 
 /*
  * Which of K drafted tokens hold, and the token after them, from given uniforms
