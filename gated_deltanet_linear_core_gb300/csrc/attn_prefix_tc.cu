@@ -5,8 +5,10 @@
 // cache, so the query rows are the M = 128 side of the MMAs and the tokens the N side:
 //   S [128 rows x 128 tokens] = Q K^T    (Q and K tile in shared memory, both K-major)
 //   O [128 rows x D]         += P V      (P in tensor memory, V tile in shared memory, MN-major)
-// A softmax thread owns a row, so maxima and sums need no exchange between lanes, and
-// P goes back into the columns of S that it came from.  P is held as two bf16 (the value
+// A softmax thread owns half a row of a tile (64 tokens), so maxima and sums need no exchange
+// between lanes, and P goes back into the columns of S that it came from.  A row's running maximum is moved
+// only when a score exceeds it by 2^8, which the two warps that share rows vote on; O is
+// rescaled then.  P is held as two bf16 (the value
 // cut to 8 bits and the rounded rest), as in attn_tc.cu: one alone would add an error of the size of the output's
 // own rounding.  Two buffers of S: while P V of a tile runs, the scores of the next are
 // turned into weights by the other warpgroup.  The two share a row's running maximum,
@@ -35,14 +37,14 @@ constexpr int NSOFT = 256;
 template <int NDB>
 struct Layout {
     static constexpr int Q_BYTES = 2 * NDB * SLAB;
-    static constexpr int SMALL = 1024 + 4 * ROWS * 4;  // barriers and notes, a row's maximum, sums
+    static constexpr int SMALL = 1024 + 4 * ROWS * 4;  // barriers and notes, the rows' maxima and sums
     static constexpr int FIT = (kSmemMax - Q_BYTES - SMALL) / SLOT;
     static constexpr int NS = FIT < 6 ? FIT : 6;
     static constexpr int O_Q = NS * SLOT;
     static constexpr int O_BAR = O_Q + Q_BYTES;
     static constexpr int O_SEG = O_BAR + 512;
-    static constexpr int O_M = O_BAR + 1024;   // [128] running maxima
-    static constexpr int O_L = O_M + ROWS * 4; // [2][128] the warpgroups' sums
+    static constexpr int O_M = O_BAR + 1024;
+    static constexpr int O_L = O_M + 2 * ROWS * 4;
     static constexpr int SMEM = O_BAR + SMALL;
     static constexpr int T_S = 0, T_O = 256, T_COLS = 512;
     static constexpr int SEGS = 4;  // segments told ahead
@@ -76,6 +78,19 @@ __device__ __forceinline__ bool softmax_any(bool x) {
     return r != 0;
 }
 
+// The two warps that share rows (named barriers 2 to 5).
+__device__ __forceinline__ void pair_sync(int quad) { asm volatile("bar.sync %0, 64;" ::"r"(2 + quad) : "memory"); }
+__device__ __forceinline__ bool pair_any(int quad, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(2 + quad)
+        : "memory");
+    return r != 0;
+}
+
 template <int NDB>
 __global__ void __launch_bounds__(NT, 1)
 attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, ShareArgs s,
@@ -88,13 +103,12 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     uint64_t* full = bars;            // [6] slot landed (TMA), told by both loading warps
     uint64_t* empty = bars + 6;       // [6] slot consumed (commit)
     uint64_t* s_full = bars + 12;     // [2] S of a tile done
-    uint64_t* p_full = bars + 14;     // [2] P of a tile written (4 warps)
+    uint64_t* p_full = bars + 14;     // [2] P of a tile written (softmax warps)
     uint64_t* pv_done = bars + 16;    // [2] P V of a tile done
     uint64_t* q_full = bars + 18;     // a segment's Q written
     uint64_t* q_empty = bars + 19;    // S of a segment's last tile done
     uint64_t* seg_full = bars + 20;   // [4] a segment is told
     uint64_t* seg_empty = bars + 24;  // [4] ... and taken note of
-    uint64_t* m_told = bars + 28;     // [4 lane quarters][2] running maxima up to a tile are decided
     uint64_t* drained = bars + 36;    // every MMA issued is done (abort)
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 37);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
@@ -110,7 +124,7 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[i], NSOFT / 32);
             mbar_init(&pv_done[i], 1);
         }
         mbar_init(q_full, 1);
@@ -120,7 +134,6 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             mbar_init(&seg_full[i], 1);
             mbar_init(&seg_empty[i], 3 + NSOFT / 32);
         }
-        for (int i = 0; i < 8; ++i) mbar_init(&m_told[i], 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&kmap);
@@ -335,8 +348,8 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
         const int wg = (warp - 4) >> 2, quad = warp & 3;
         const int row = quad * 32 + lane;  // TMEM lane
         const uint32_t tq = tb + ((uint32_t)(quad * 32) << 16);
-        float* m_s = reinterpret_cast<float*>(sm + L::O_M);
-        float* l_s = reinterpret_cast<float*>(sm + L::O_L);
+        float* t_s = reinterpret_cast<float*>(sm + L::O_M);  // [2][128] the warpgroups' maxima of a tile
+        float* l_s = reinterpret_cast<float*>(sm + L::O_L);  // [2][128] ... and sums
         int it = 0;        // tiles before
         bool live = true;  // no wait gave up: outputs are written only then
         auto wait = [&](uint64_t* bar, int k) {
@@ -352,36 +365,38 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             if (!more) break;
             if (lane == 0) took_note();
             const int n = g.tile1 - g.tile0;
-            float l = 0.f, m_mine = kNone;  // sum of this warpgroup's tiles, and the maximum that it refers to
+            float m = kNone;                      // the row's running maximum
+            float2 l = make_float2(0.f, 0.f);     // the sum of this warpgroup's tokens
             for (int j = 0; j < n; ++j, ++it) {
-                if ((it & 1) != wg) continue;
-                const uint32_t ts = tq + L::T_S + (it & 1) * TILE;
+                const uint32_t ts = tq + L::T_S + (it & 1) * TILE + wg * 64;
                 wait(&s_full[it & 1], it >> 1);
                 tc_fence_after();
-                float top = -INFINITY;
+                float x[64];
+                tmem_ld32(ts, x);
+                tmem_ld32(ts + 32, x + 32);
+                tmem_wait_ld();
+                float top = x[0], top2 = x[1];
 #pragma unroll
-                for (int c = 0; c < TILE; c += 32) {
-                    float x[32];
-                    tmem_ld32(ts + c, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i]);
+                for (int i = 2; i < 64; i += 4) {
+                    top = fmaxf(top, fmaxf(x[i], x[i + 1]));
+                    if (i + 3 < 64) top2 = fmaxf(top2, fmaxf(x[i + 2], x[i + 3]));
                 }
-                top *= a.scale_log2;
-                float m;
-                if (j == 0) {
-                    m = fmaxf(top, kNone);
-                } else {
-                    wait(&m_told[quad * 2 + ((it - 1) & 1)], (it - 1) >> 1);
-                    const float before = m_s[row];
-                    m = top > before + kSlack ? top : before;
-                    if (__any_sync(0xffffffffu, m != before)) {
-                        // ---- new maxima: the outputs so far are scaled to them
-                        const float f = ex2_approx(before - m);
+                top = fmaxf(top, top2) * a.scale_log2;
+                if (pair_any(quad, j == 0 || top > m + kSlack)) {
+                    // ---- new maxima; sums and outputs so far are scaled to them
+                    t_s[wg * ROWS + row] = top;
+                    pair_sync(quad);
+                    const float t = fmaxf(top, t_s[(wg ^ 1) * ROWS + row]);
+                    const float m1 = t > m + kSlack ? t : m;  // rows do not move with one another
+                    const float f = ex2_approx(m - m1);
+                    m = m1;
+                    l.x *= f;
+                    l.y *= f;
+                    if (j > 0) {
                         wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < 128 * NDB; c += 32) {
+                        for (int c = wg * 64 * NDB; c < (wg + 1) * 64 * NDB; c += 32) {
                             float o[32];
                             tmem_ld32(tq + L::T_O + c, o);
                             tmem_wait_ld();
@@ -389,52 +404,34 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                             for (int i = 0; i < 32; ++i) o[i] *= f;
                             tmem_st32(tq + L::T_O + c, o);
                         }
-                        tmem_wait_st();
                     }
                 }
-                m_s[row] = m;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&m_told[quad * 2 + (it & 1)]);
-                if (m != m_mine) {
-                    l *= ex2_approx(m_mine - m);
-                    m_mine = m;
-                }
-                float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int c = 0; c < TILE; c += 32) {
-                    float x[32];
-                    tmem_ld32(ts + c, x);
-                    tmem_wait_ld();
-                    uint32_t w[32];  // 16 columns of upper parts, 16 of rests
+                for (int c = 0; c < 64; c += 32) {
+                    float w[32];  // 16 columns of upper parts, 16 of rests
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float2 y = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]),
+                        const float2 y = __ffma2_rn(make_float2(x[c + 2 * i], x[c + 2 * i + 1]),
                                                     make_float2(a.scale_log2, a.scale_log2), make_float2(-m, -m));
                         const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-                        sum = __fadd2_rn(sum, p);
+                        l = __fadd2_rn(l, p);
                         const uint32_t w0 = __float_as_uint(p.x), w1 = __float_as_uint(p.y);
-                        w[i] = __byte_perm(w0, w1, 0x7632);  // the upper halves: cut, not rounded
-                        // the rest, at least p's last bit: a rest of 0 would turn an infinite value into NaN
-                        const float2 rest = __fadd2_rn(make_float2(__uint_as_float(w0 | 1u), __uint_as_float(w1 | 1u)),
+                        w[i] = __uint_as_float(__byte_perm(w0, w1, 0x7632));  // the upper halves: cut, not rounded
+                        // the rest, and p's last bit: a rest of 0 would turn an infinite value into NaN
+                        const float2 rest = __ffma2_rn(p, make_float2(1.0f + 0x1p-23f, 1.0f + 0x1p-23f),
                                                        make_float2(__uint_as_float((w0 & 0xffff0000u) | 0x80000000u),
                                                                    __uint_as_float((w1 & 0xffff0000u) | 0x80000000u)));
-                        w[16 + i] = pack_bf16x2(rest.x, rest.y);
+                        w[16 + i] = __uint_as_float(pack_bf16x2(rest.x, rest.y));
                     }
-                    float st[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) st[i] = __uint_as_float(w[i]);
-                    tmem_st32(ts + c, st);
+                    tmem_st32(ts + c, w);
                 }
-                l += sum.x + sum.y;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[it & 1]);
             }
             // ---- sums and outputs of the segment
-            softmax_sync();
-            const float m = m_s[row];
-            l_s[wg * ROWS + row] = l * ex2_approx(m_mine - m);
+            l_s[wg * ROWS + row] = l.x + l.y;
             wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
             tc_fence_after();
             softmax_sync();
@@ -462,7 +459,7 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                     if (real && c + i < a.D) *reinterpret_cast<float4*>(po + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
             }
             tc_fence_before();
-            softmax_sync();  // O and the arrays are free
+            softmax_sync();  // O and the sums are free
         }
     }
     tc_fence_before();

@@ -9,7 +9,7 @@ namespace {
 using namespace attn;
 
 constexpr int PT = 1024;  // threads of the plan
-constexpr int MT = 256;   // threads of a merge block
+constexpr int MT = 256;   // threads of a merge block that takes several rows
 
 // What every group shares in earnest, by one block: a warp (or, where there are few groups, several)
 // looks at a group's lengths.
@@ -124,125 +124,105 @@ __device__ __forceinline__ void store4(bf16* p, float4 y) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
 }
 
-// A row's parts: those of its own tokens, then the prefix's.
-struct Parts {
-    int n_own, n;       // CTAs
-    int c_own, c_pre;   // the first of each
-    int r_own, r_pre;   // the row in its blocks
-};
-
-// Puts a row's parts together: the running maximum, sum and output over the parts in CTA
-// order.  A group of threads (4 columns each) takes a row; where a row of the block has many
-// parts, the groups take each row together.
-template <typename T>
-__global__ void __launch_bounds__(MT) attn_merge_kernel(ShareArgs s) {
+// Puts a row's parts together: the running maximum, sum and output over the parts in a fixed
+// order.  A group of threads (blockDim.x, 4 columns each) takes a row, or where rows have many
+// parts (WIDE) the groups of a block take one row together.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? 1024 : MT) attn_merge_kernel(ShareArgs s) {
     constexpr int U = 4;  // parts at once
-    constexpr int kSerial = 8;
-    __shared__ float4 o_s[MT];
-    __shared__ float2 ml_s[MT];
+    extern __shared__ __align__(16) float4 o_s[];  // WIDE: the groups' outputs, then their maxima and sums
     const AttnArgs& a = s.a;
-    const int ng = blockDim.x, groups = blockDim.y, g = threadIdx.y, tid = g * ng + threadIdx.x, d = threadIdx.x * 4;
+    const int ng = blockDim.x, groups = blockDim.y, g = threadIdx.y, d = threadIdx.x * 4;
     pdl_wait();
     pdl_trigger();
-    const int64_t rows = (int64_t)a.B * a.K * a.H_q, row0 = (int64_t)blockIdx.x * groups;
-    auto parts_of = [&](int64_t row) -> Parts {
-        Parts p = {};
-        const int b = (int)(row / (a.K * a.H_q)), rest = (int)(row - (int64_t)b * a.K * a.H_q);
-        const int i = rest / a.H_q, hq = rest - i * a.H_q;
-        if (clamped_len(a, b) - (a.K - 1 - i) <= 0) return p;  // sees nothing
-        const float4 own = a.part_stat[row];
-        p.c_own = __float_as_int(own.z);
-        p.n_own = __float_as_int(own.w);
-        p.r_own = (i * a.group + hq % a.group) % a.rb_rows;
-        p.n = p.n_own;
-        if (a.skip[b] > 0) {
-            const float4 pre = s.pre_stat[row];
-            p.c_pre = __float_as_int(pre.z) & 0xffff;
-            p.r_pre = __float_as_int(pre.w);
-            p.n += __float_as_int(pre.z) >> 16;
-        }
-        // (the bounds hold for every call that keeps to the rules; they keep others' reads in bounds)
-        const int n_pre = p.n - p.n_own;
-        if ((unsigned)p.c_own >= kAttnMaxCtas || (unsigned)p.n_own > kAttnMaxCtas || p.c_own + p.n_own > kAttnMaxCtas ||
-            (unsigned)p.c_pre >= kAttnMaxCtas || (unsigned)n_pre > kAttnMaxCtas || p.c_pre + n_pre > kAttnMaxCtas ||
-            (unsigned)p.r_pre >= (unsigned)s.rows_per_block)
-            p.n = p.n_own = 0;
-        return p;
-    };
-    // parts from .. in steps of `step`
-    auto add_parts = [&](Running& run, const Parts& p, int64_t row, int from, int step) {
+    const int64_t rows = (int64_t)a.B * a.K * a.H_q, row = WIDE ? blockIdx.x : (int64_t)blockIdx.x * groups + g;
+    if (row >= rows) return;
+    const int b = (int)(row / (a.K * a.H_q)), rest = (int)(row - (int64_t)b * a.K * a.H_q);
+    const int i = rest / a.H_q, hq = rest - i * a.H_q;
+    const float4 own_stat = a.part_stat[row];
+    const float4 pre_stat = s.pre_stat[row];  // (of no meaning where nothing is shared)
+    const int len = clamped_len(a, b), shared = a.skip[b];
+    const int64_t at = row * a.D + d;
+    float4 gt = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.gate != nullptr && (!WIDE || g == 0)) gt = ld4(static_cast<const T*>(a.gate) + at);
+    // the row's parts: those of its own tokens (of the CTAs c_own ..), then the prefix's
+    const int c_own = __float_as_int(own_stat.z), c_pre = __float_as_int(pre_stat.z) & 0xffff;
+    const int r_own = (i * a.group + hq % a.group) % a.rb_rows, r_pre = __float_as_int(pre_stat.w);
+    int n_own = __float_as_int(own_stat.w), n_pre = shared > 0 ? __float_as_int(pre_stat.z) >> 16 : 0;
+    if (len - (a.K - 1 - i) <= 0) n_own = n_pre = 0;  // sees nothing
+    // (the bounds hold for every call that keeps to the rules; they keep others' reads in bounds)
+    if ((unsigned)n_own > kAttnMaxCtas || (n_own > 0 && ((unsigned)c_own >= kAttnMaxCtas || c_own + n_own > kAttnMaxCtas)))
+        n_own = 0;
+    if ((unsigned)n_pre > kAttnMaxCtas || (n_pre > 0 && (c_pre + n_pre > kAttnMaxCtas || (unsigned)r_pre >= (unsigned)s.rows_per_block)))
+        n_pre = 0;
+    const int n = n_own + n_pre;
+    Running run;
 #pragma unroll 1
-        for (int k0 = from; k0 < p.n; k0 += U * step) {
-            float m[U], l[U];
-            float4 x[U];
+    for (int k0 = WIDE ? g : 0; k0 < n; k0 += WIDE ? U * groups : U) {
+        float m[U], l[U];
+        float4 x[U];
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int part = k0 + k * step;
-                m[k] = -INFINITY;
-                l[k] = 0.f;
-                x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (part >= p.n) continue;
-                const bool own = part < p.n_own;
-                const int nth = own ? part : part - p.n_own;
-                if (nth == 0) {
-                    const float4 st = own ? a.part_stat[row] : s.pre_stat[row];
-                    m[k] = st.x;
-                    l[k] = st.y;
-                    x[k] = ld4((own ? a.part_o : s.pre_o) + row * a.D + d);
-                } else {
-                    const float* slot = own ? slot_ptr(a, p.c_own + nth) : prefix_slot(s, p.c_pre + nth);
-                    const int r = own ? p.r_own : p.r_pre, per = own ? a.rb_rows : s.rows_per_block;
-                    m[k] = slot[r];
-                    l[k] = slot[per + r];
-                    x[k] = ld4(slot + (own ? a.stat_floats : 2 * per) + r * a.D + d);
-                }
+        for (int k = 0; k < U; ++k) {
+            const int part = k0 + k * (WIDE ? groups : 1);
+            m[k] = -INFINITY;
+            l[k] = 0.f;
+            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (part >= n) continue;
+            const bool own = part < n_own;
+            const int nth = own ? part : part - n_own;
+            if (nth == 0) {
+                m[k] = own ? own_stat.x : pre_stat.x;
+                l[k] = own ? own_stat.y : pre_stat.y;
+                x[k] = ld4((own ? a.part_o : s.pre_o) + at);
+            } else {
+                const float* slot = own ? slot_ptr(a, c_own + nth) : prefix_slot(s, c_pre + nth);
+                const int r = own ? r_own : r_pre, per = own ? a.rb_rows : s.rows_per_block;
+                m[k] = slot[r];
+                l[k] = slot[per + r];
+                x[k] = ld4(slot + (own ? a.stat_floats : 2 * per) + r * a.D + d);
             }
+        }
+        run.add(m, l, x);
+    }
+    if (WIDE) {
+        float2* ml_s = reinterpret_cast<float2*>(o_s + ng * groups);
+        o_s[g * ng + threadIdx.x] = run.o;
+        if (threadIdx.x == 0) ml_s[g] = make_float2(run.m, run.l);
+        __syncthreads();
+        if (g > 0) return;
+#pragma unroll 4
+        for (int k = 1; k < groups; ++k) {
+            const float m[1] = {ml_s[k].x}, l[1] = {ml_s[k].y};
+            const float4 x[1] = {o_s[k * ng + threadIdx.x]};
             run.add(m, l, x);
         }
-    };
-    auto write = [&](const Running& run, int64_t row) {
-        const int64_t at = row * a.D + d;
-        const float inv = run.l == 0.f ? 0.f : 1.0f / run.l;
-        float4 y = make_float4(run.o.x * inv, run.o.y * inv, run.o.z * inv, run.o.w * inv);
-        if (a.gate != nullptr && run.l != 0.f) {  // a row that sees nothing is 0 whatever its gate holds
-            const float4 gt = ld4(static_cast<const T*>(a.gate) + at);
-            y.x *= sigmoid_f(gt.x); y.y *= sigmoid_f(gt.y); y.z *= sigmoid_f(gt.z); y.w *= sigmoid_f(gt.w);
-        }
-        store4(static_cast<T*>(a.out) + at, y);
-        if (d == 0 && a.lse != nullptr) a.lse[row] = run.l == 0.f ? -INFINITY : (run.m + log2f(run.l)) * kLn2;
-    };
-    const int64_t mine = row0 + g;
-    Parts p = {};
-    if (mine < rows) p = parts_of(mine);
-    if (!__syncthreads_or(p.n > kSerial)) {
-        if (mine < rows) {
-            Running run;
-            add_parts(run, p, mine, 0, 1);
-            write(run, mine);
-        }
-        return;
     }
-    for (int i = 0; i < groups && row0 + i < rows; ++i) {
-        const int64_t row = row0 + i;
-        const Parts q = parts_of(row);
-        Running run;
-        add_parts(run, q, row, g, groups);
-        o_s[tid] = run.o;
-        ml_s[tid] = make_float2(run.m, run.l);
-        __syncthreads();
-        if (g == i) {
-            run = Running();
-#pragma unroll 1
-            for (int k = 0; k < groups; ++k) {
-                const int t = k * ng + threadIdx.x;
-                const float m[1] = {ml_s[t].x}, l[1] = {ml_s[t].y};
-                const float4 x[1] = {o_s[t]};
-                run.add(m, l, x);
-            }
-            write(run, row);
-        }
-        __syncthreads();
+    const float inv = run.l == 0.f ? 0.f : 1.0f / run.l;
+    float4 y = make_float4(run.o.x * inv, run.o.y * inv, run.o.z * inv, run.o.w * inv);
+    if (a.gate != nullptr && run.l != 0.f) {  // a row that sees nothing is 0 whatever its gate holds
+        y.x *= sigmoid_f(gt.x); y.y *= sigmoid_f(gt.y); y.z *= sigmoid_f(gt.z); y.w *= sigmoid_f(gt.w);
     }
+    store4(static_cast<T*>(a.out) + at, y);
+    if (d == 0 && a.lse != nullptr) a.lse[row] = run.l == 0.f ? -INFINITY : (run.m + log2f(run.l)) * kLn2;
+}
+
+template <typename T>
+cudaError_t launch_merge(const ShareArgs& s, int n_cta, cudaStream_t st) {
+    const AttnArgs& a = s.a;
+    const int ng = a.D / 4;
+    const int64_t rows = (int64_t)a.B * a.K * a.H_q;
+    // parts that a row has if all sequences are one group, about; more groups have fewer
+    const int64_t items = a.H_kv * (((int64_t)a.B * a.rows + s.rows_per_block - 1) / s.rows_per_block);
+    const int64_t parts = 1 + (n_cta + items - 1) / items;
+    int groups = 1;
+    if (parts > 8) {
+        while (groups * 4 < parts && groups * 2 * ng <= 1024) groups *= 2;
+        const size_t smem = groups * (ng * sizeof(float4) + sizeof(float2));
+        return launch_pdl(attn_merge_kernel<T, true>, dim3((unsigned)rows), dim3((unsigned)ng, (unsigned)groups), smem, st, s);
+    }
+    groups = MT / ng;
+    return launch_pdl(attn_merge_kernel<T, false>, dim3((unsigned)((rows + groups - 1) / groups)),
+                      dim3((unsigned)ng, (unsigned)groups), 0, st, s);
 }
 
 size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -287,11 +267,7 @@ cudaError_t launch_attn_shared(const ShareArgs& s, gdn_dtype_t dt, cudaStream_t 
     if (e == cudaSuccess) e = tc ? launch_prefix_tc(s, n_cta, st) : launch_prefix_ffma(s, n_cta, dt, st);
     if (e == cudaSuccess) e = tc ? launch_attn_tc(a, n_cta, st) : launch_attn_ffma(a, n_cta, dt, st);
     if (e != cudaSuccess) return e;
-    const int ng = a.D / 4, groups = MT / ng;
-    const int64_t rows = (int64_t)a.B * a.K * a.H_q;
-    const dim3 grid((unsigned)((rows + groups - 1) / groups)), block((unsigned)ng, (unsigned)groups);
-    return dt == GDN_BF16 ? launch_pdl(attn_merge_kernel<bf16>, grid, block, 0, st, s)
-                          : launch_pdl(attn_merge_kernel<float>, grid, block, 0, st, s);
+    return dt == GDN_BF16 ? launch_merge<bf16>(s, n_cta, st) : launch_merge<float>(s, n_cta, st);
 }
 
 }  // namespace gdn
