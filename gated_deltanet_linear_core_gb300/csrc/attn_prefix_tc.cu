@@ -49,9 +49,6 @@ struct Layout {
     static constexpr int T_S = 0, T_O = 256, T_COLS = 512;
     static constexpr int SEGS = 4;  // segments told ahead
     static_assert(SMEM <= kSmemMax && NS >= 4, "shared memory");
-    // slots in the order K(0), K(1), V(0), K(2), V(1), .. of a segment's n tiles, from its first slot
-    __device__ static __forceinline__ int k_slot(int j) { return j == 0 ? 0 : NDB * (2 * j - 1); }
-    __device__ static __forceinline__ int v_slot(int j, int n) { return NDB * (j + 1 < n ? 2 * j + 2 : 2 * n - 1); }
 };
 static_assert(sizeof(PrefixSegment) == 32 && 4 * 32 <= 512, "notes");
 
@@ -65,6 +62,15 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(hi)
         : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}"
+        : "=r"(r)
+        :
+        : "memory");
+    return r != 0;
 }
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool softmax_any(bool x) {
@@ -175,45 +181,50 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             y = g.h * a.page_size + (t - pg * a.page_size);
         }
     };
-    auto load = [&](const CUtensorMap* map, int which, int y, int z, int sl) -> bool {  // into slots sl ..
-        for (int db = 0; db < NDB; ++db, ++sl) {
-            const int st = sl % NS;
-            if (sl >= NS && !__all_sync(0xffffffffu, wait_or_abort(&empty[st], (uint32_t)((sl / NS - 1) & 1), abort_flag)))
+    int slot_in = 0, loads = 0;  // the slot that is filled next, how often all were
+    auto load = [&](const CUtensorMap* map, int which, int y, int z) -> bool {  // into the next NDB slots
+#pragma unroll
+        for (int db = 0; db < NDB; ++db) {
+            const int st = slot_in;
+            if (loads > 0 && !__all_sync(0xffffffffu, wait_or_abort(&empty[st], (uint32_t)((loads - 1) & 1), abort_flag)))
                 return false;
             const int slab = 2 * db + which;
             const bool real = slab < nslab;
             if (lane == 0) {
                 if (real) mbar_arrive_expect_tx(&full[st], SLAB); else mbar_arrive(&full[st]);
-                filled[6 * which + st] = sl / NS + 1;
+                filled[6 * which + st] = loads + 1;
             }
             __syncwarp();
             if (real && lane < np)
                 tma_load_3d(smem_u32(sm) + st * SLOT + which * SLAB + lane * piece * 128, map, &full[st], slab * 64, y, z);
+            if (++slot_in == NS) {
+                slot_in = 0;
+                ++loads;
+            }
         }
         return true;
     };
-    auto load_segment = [&](int which, int& sl0) -> bool {
+    // K of a segment's first tile, then of tile j + 1 and V of tile j: the order in which the MMAs use them
+    auto load_segment = [&](int which) -> bool {
         const int n = g.tile1 - g.tile0;
         int yv = 0, zv = 0, yk = 0, zk = 0, yn = 0, zn = 0;  // pieces of tiles j, j + 1, and j + 2 looked up ahead
         bool ok = true;
         look_up(g.tile0, yk, zk);
-        for (int j = -1; ok && j < n; ++j) {  // K of tile j + 1, V of tile j
+        for (int j = -1; ok && j < n; ++j) {
             if (j + 2 < n) look_up(g.tile0 + j + 2, yn, zn);
-            if (j + 1 < n) ok = load(&kmap, which, yk, zk, sl0 + L::k_slot(j + 1));
-            if (j >= 0) ok = ok && load(&vmap, which, yv, zv, sl0 + L::v_slot(j, n));
+            if (j + 1 < n) ok = load(&kmap, which, yk, zk);
+            if (j >= 0) ok = ok && load(&vmap, which, yv, zv);
             yv = yk;
             zv = zk;
             yk = yn;
             zk = zn;
         }
-        sl0 += 2 * NDB * n;
         return ok;
     };
 
     if (warp == 0) {
         // ------------------------------------------------ the walk; K and V, lower slabs
         PrefixWalk walk(s, blockIdx.x, gridDim.x);
-        int sl0 = 0;  // slots before
         bool ok = true, more = true;
         while (ok && more) {
             g.tile0 = g.tile1 = 0;
@@ -227,86 +238,103 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                 mbar_arrive(&seg_full[e]);
             }
             ++sg;
-            if (more) ok = load_segment(0, sl0);
+            if (more) ok = load_segment(0);
         }
     } else if (warp == 3) {
         // ------------------------------------------------ K and V, upper slabs
-        int sl0 = 0;
         bool ok = true;
         for (;;) {
             const bool more = heard(ok);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || !more) break;
             if (lane == 0) took_note();
-            ok = load_segment(1, sl0);
+            ok = load_segment(1);
             if (!ok) break;
         }
     } else if (warp == 1) {
-        // ------------------------------------------------ MMAs (lane 0)
-        if (lane == 0) {
-            const uint32_t base = smem_u32(sm);
-            const int ksteps = (a.D + 15) / 16;
-            int it = 0, seg = 0, sl0 = 0;  // tiles, segments and slots before
-            auto slot_full = [&](int k) { return wait_or_abort(&full[k % NS], (uint32_t)((k / NS) & 1), abort_flag); };
-            auto issue_s = [&](int t, int k0) -> bool {  // S of the CTA's tile t, its K from slot k0 on
-                for (int db = 0; db < NDB; ++db) {
-                    const int k = k0 + db;
-                    if (!slot_full(k)) return false;
-                    tc_fence_after();
-                    const int steps = ksteps - 8 * db;
-                    const uint32_t ka = desc_lo(base + (k % NS) * SLOT, 16);
-                    const uint32_t qa = desc_lo(base + L::O_Q + db * SLOT, 16);
+        // ------------------------------------------------ MMAs
+        // The whole warp runs the loop and one elected lane issues: with addresses that are constants but for the slot
+        // and the buffer (the allocation is all of tensor memory, so it starts at 0), an MMA costs few instructions,
+        // which the warp has to get past two busy softmax warps of its scheduler.
+        const uint32_t base = smem_u32(sm);
+        const int ksteps = (a.D + 15) / 16;
+        int it = 0, seg = 0;        // tiles and segments before
+        int slot = 0;               // slots are used in the order they are filled
+        uint32_t phase = 0;
+        auto slot_full = [&] { return wait_or_abort(&full[slot], phase, abort_flag); };
+        auto slot_done = [&] {
+            if (++slot == NS) {
+                slot = 0;
+                phase ^= 1;
+            }
+        };
+        auto issue_s = [&](int t) -> bool {  // S of the CTA's tile t
+#pragma unroll
+            for (int db = 0; db < NDB; ++db) {
+                if (!slot_full()) return false;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t ka = desc_lo(base + slot * SLOT, 16), qa = desc_lo(base + L::O_Q + db * SLOT, 16);
+                    const uint32_t d = L::T_S + (t & 1) * TILE;
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        if (q < steps)
-                            mma_lo(tb + L::T_S + (t & 1) * TILE, qa + (((q >> 2) * SLAB + (q & 3) * 32) >> 4),
-                                   ka + (((q >> 2) * SLAB + (q & 3) * 32) >> 4), idesc_bf16_f32(ROWS, TILE, 0, 0),
-                                   db > 0 || q > 0);
-                    mma_commit(&empty[k % NS]);
+                        if (8 * db + q < ksteps)
+                            mma_lo(d, qa + (((q >> 2) * SLAB + (q & 3) * 32) >> 4), ka + (((q >> 2) * SLAB + (q & 3) * 32) >> 4),
+                                   idesc_bf16_f32(ROWS, TILE, 0, 0), db > 0 || q > 0);
+                    mma_commit(&empty[slot]);
+                    if (db + 1 == NDB) mma_commit(&s_full[t & 1]);
                 }
-                mma_commit(&s_full[t & 1]);
-                return true;
-            };
-            bool ok = true;
-            while (ok && heard(ok)) {
-                took_note();
-                const int n = g.tile1 - g.tile0;
-                ok = wait_or_abort(q_full, (uint32_t)(seg & 1), abort_flag);
-                ++seg;
-                for (int j = -1; ok && j < n; ++j) {  // S of tile j + 1, then P V of tile j
-                    // (S of tile j + 1 overwrites P of tile j - 1, whose P V has been issued before it: MMAs of one
-                    // thread and shape run in order)
-                    if (j + 1 < n && !issue_s(it + (j < 0 ? 0 : 1), sl0 + L::k_slot(j + 1))) { ok = false; break; }
-                    if (j + 2 == n) mma_commit(q_empty);
-                    if (j < 0) continue;
-                    ok = it != a.stop_at;
+                __syncwarp();
+                slot_done();
+            }
+            return true;
+        };
+        bool ok = true;
+        while (ok && heard(ok)) {
+            if (lane == 0) took_note();
+            const int n = g.tile1 - g.tile0;
+            ok = wait_or_abort(q_full, (uint32_t)(seg & 1), abort_flag);
+            ++seg;
+            for (int j = -1; ok && j < n; ++j) {  // S of tile j + 1, then P V of tile j
+                // (S of tile j + 1 overwrites P of tile j - 1, whose P V has been issued before it: MMAs of one
+                // thread and shape run in order)
+                if (j + 1 < n && !issue_s(it + (j < 0 ? 0 : 1))) { ok = false; break; }
+                if (j + 2 == n && elect_one()) mma_commit(q_empty);
+                __syncwarp();
+                if (j < 0) continue;
+                ok = it != a.stop_at;
+                if (!ok) break;
+                ok = wait_or_abort(&p_full[it & 1], (uint32_t)((it >> 1) & 1), abort_flag);
+                if (!ok) break;
+#pragma unroll
+                for (int db = 0; db < NDB; ++db) {
+                    ok = slot_full();
                     if (!ok) break;
-                    ok = wait_or_abort(&p_full[it & 1], (uint32_t)((it >> 1) & 1), abort_flag);
-                    if (!ok) break;
-                    for (int db = 0; db < NDB; ++db) {
-                        const int k = sl0 + L::v_slot(j, n) + db;
-                        if (!slot_full(k)) { ok = false; break; }
-                        tc_fence_after();
-                        const uint32_t va = desc_lo(base + (k % NS) * SLOT, SLAB);
-                        const uint32_t pa = tb + L::T_S + (it & 1) * TILE;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t va = desc_lo(base + slot * SLOT, SLAB);
+                        const uint32_t pa = L::T_S + (it & 1) * TILE;
 #pragma unroll
                         for (int q = 0; q < 8; ++q)  // 16 tokens: columns 8 (q % 2) of block q / 2's upper parts, then of its rests
 #pragma unroll
                             for (int lo = 0; lo < 2; ++lo)
-                                mma_ts(tb + L::T_O + db * 128, pa + (q >> 1) * 32 + lo * 16 + (q & 1) * 8, va + q * (2048 >> 4),
+                                mma_ts(L::T_O + db * 128, pa + (q >> 1) * 32 + lo * 16 + (q & 1) * 8, va + q * (2048 >> 4),
                                        idesc_bf16_f32(ROWS, 128, 0, 1), j > 0 || lo > 0 || q > 0);
-                        mma_commit(&empty[k % NS]);
+                        mma_commit(&empty[slot]);
+                        if (db + 1 == NDB) mma_commit(&pv_done[it & 1]);
                     }
-                    if (!ok) break;
-                    mma_commit(&pv_done[it & 1]);
-                    ++it;
+                    __syncwarp();
+                    slot_done();
                 }
-                sl0 += 2 * NDB * n;
+                if (!ok) break;
+                ++it;
             }
-            if (!ok) {  // MMAs that no commit above speaks of are waited for too
-                mma_commit(drained);
-                mbar_wait(drained, 0, kWaitNs);
-            }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {  // MMAs that no commit above speaks of are waited for too
+            if (elect_one()) mma_commit(drained);
+            __syncwarp();
+            mbar_wait(drained, 0, kWaitNs);
         }
     } else if (warp == 2) {
         // ------------------------------------------------ Q rows (zero beyond the block's rows and the head's dims)
