@@ -16,7 +16,7 @@
 //
 // Warps: 0 walks the CTA's range, tells the others its segments, and loads K and V (of
 // every page piece the first 64 of 128 dims; warp 3 the others), 1 issues the MMAs,
-// 2 loads Q, 4 to 11 are the softmax.  Every wait is bounded (1 s): on a timeout the
+// 4 to 11 load Q and are the softmax (warp 2 only fills the warpgroup).  Every wait is bounded (1 s): on a timeout the
 // roles run out without waiting, the copies in flight land, TMEM is freed and the error
 // word is set.
 #include "attn_shared.cuh"
@@ -36,7 +36,7 @@ constexpr int NSOFT = 256;
 
 template <int NDB>
 struct Layout {
-    static constexpr int Q_BYTES = 2 * NDB * SLAB;
+    static constexpr int Q_BYTES = 2 * NDB * SLAB;     // at a segment's end 4 KB per softmax warp for turning outputs into rows
     static constexpr int SMALL = 1024 + 4 * ROWS * 4;  // barriers and notes, the rows' maxima and sums
     static constexpr int FIT = (kSmemMax - Q_BYTES - SMALL) / SLOT;
     static constexpr int NS = FIT < 6 ? FIT : 6;
@@ -46,9 +46,12 @@ struct Layout {
     static constexpr int O_M = O_BAR + 1024;
     static constexpr int O_L = O_M + 2 * ROWS * 4;
     static constexpr int SMEM = O_BAR + SMALL;
-    static constexpr int T_S = 0, T_O = 256, T_COLS = 512;
+    // Tensor memory: buffers of S, then O.  S runs NB - 1 tiles ahead: with three buffers the scores of a tile wait
+    // while the weights of the one before are made (two leave no room for that, but D > 128 has twice the MMAs per tile).
+    static constexpr int NB = NDB == 1 ? 3 : 2, AHEAD = NB - 1;
+    static constexpr int T_S = 0, T_O = 512 - 128 * NDB, T_COLS = 512;
     static constexpr int SEGS = 4;  // segments told ahead
-    static_assert(SMEM <= kSmemMax && NS >= 4, "shared memory");
+    static_assert(SMEM <= kSmemMax && NS >= 4 && NB * TILE <= T_O && 8 * 4096 <= Q_BYTES, "memory");
 };
 static_assert(sizeof(PrefixSegment) == 32 && 4 * 32 <= 512, "notes");
 
@@ -108,13 +111,13 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::O_BAR);
     uint64_t* full = bars;            // [6] slot landed (TMA), told by both loading warps
     uint64_t* empty = bars + 6;       // [6] slot consumed (commit)
-    uint64_t* s_full = bars + 12;     // [2] S of a tile done
-    uint64_t* p_full = bars + 14;     // [2] P of a tile written (softmax warps)
-    uint64_t* pv_done = bars + 16;    // [2] P V of a tile done
-    uint64_t* q_full = bars + 18;     // a segment's Q written
-    uint64_t* q_empty = bars + 19;    // S of a segment's last tile done
-    uint64_t* seg_full = bars + 20;   // [4] a segment is told
-    uint64_t* seg_empty = bars + 24;  // [4] ... and taken note of
+    uint64_t* s_full = bars + 12;     // [3] S of a tile done
+    uint64_t* p_full = bars + 15;     // [3] P of a tile written (softmax warps)
+    uint64_t* pv_done = bars + 18;    // [3] P V of a tile done (where S runs two tiles ahead of P V, a softmax warp can be
+                                      // two tiles past the last P V: with two barriers it would take one phase for another)
+    uint64_t* q_full = bars + 21;     // a segment's Q written (softmax warps)
+    uint64_t* seg_full = bars + 22;   // [4] a segment is told
+    uint64_t* seg_empty = bars + 26;  // [4] ... and taken note of
     uint64_t* drained = bars + 36;    // every MMA issued is done (abort)
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 37);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
@@ -128,17 +131,16 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             mbar_init(&empty[i], 1);
             filled[i] = filled[6 + i] = 0;
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], NSOFT / 32);
             mbar_init(&pv_done[i], 1);
         }
-        mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
+        mbar_init(q_full, NSOFT / 32);
         mbar_init(drained, 1);
         for (int i = 0; i < L::SEGS; ++i) {
             mbar_init(&seg_full[i], 1);
-            mbar_init(&seg_empty[i], 3 + NSOFT / 32);
+            mbar_init(&seg_empty[i], 2 + NSOFT / 32);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -204,20 +206,22 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
         }
         return true;
     };
-    // K of a segment's first tile, then of tile j + 1 and V of tile j: the order in which the MMAs use them
+    // K of a segment's first tiles, then K of tile j + AHEAD and V of tile j: the order in which the MMAs use them
     auto load_segment = [&](int which) -> bool {
         const int n = g.tile1 - g.tile0;
-        int yv = 0, zv = 0, yk = 0, zk = 0, yn = 0, zn = 0;  // pieces of tiles j, j + 1, and j + 2 looked up ahead
+        int y[L::AHEAD + 2], z[L::AHEAD + 2];  // pieces of tiles j .. j + AHEAD, and of the next one, looked up ahead
+        look_up(g.tile0, y[L::AHEAD], z[L::AHEAD]);
         bool ok = true;
-        look_up(g.tile0, yk, zk);
-        for (int j = -1; ok && j < n; ++j) {
-            if (j + 2 < n) look_up(g.tile0 + j + 2, yn, zn);
-            if (j + 1 < n) ok = load(&kmap, which, yk, zk);
-            if (j >= 0) ok = ok && load(&vmap, which, yv, zv);
-            yv = yk;
-            zv = zk;
-            yk = yn;
-            zk = zn;
+        for (int j = -L::AHEAD; ok && j < n; ++j) {
+            const int t = j + L::AHEAD;
+            if (t + 1 < n) look_up(g.tile0 + t + 1, y[L::AHEAD + 1], z[L::AHEAD + 1]);
+            if (t < n) ok = load(&kmap, which, y[L::AHEAD], z[L::AHEAD]);
+            if (j >= 0) ok = ok && load(&vmap, which, y[0], z[0]);
+#pragma unroll
+            for (int i = 0; i <= L::AHEAD; ++i) {
+                y[i] = y[i + 1];
+                z[i] = z[i + 1];
+            }
         }
         return ok;
     };
@@ -256,64 +260,67 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
         // The whole warp runs the loop and one elected lane issues: with addresses that are constants but for the slot
         // and the buffer (the allocation is all of tensor memory, so it starts at 0), an MMA costs few instructions,
         // which the warp has to get past two busy softmax warps of its scheduler.
+        // (Its lanes agree on every wait: they meet at the elections.)
         const uint32_t base = smem_u32(sm);
         const int ksteps = (a.D + 15) / 16;
         int it = 0, seg = 0;        // tiles and segments before
         int slot = 0;               // slots are used in the order they are filled
         uint32_t phase = 0;
-        auto slot_full = [&] { return wait_or_abort(&full[slot], phase, abort_flag); };
+        int sb = 0, pb = 0;         // the buffers of the next S, of the next P
+        uint32_t p_phase = 0;
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag)); };
         auto slot_done = [&] {
             if (++slot == NS) {
                 slot = 0;
                 phase ^= 1;
             }
         };
-        auto issue_s = [&](int t) -> bool {  // S of the CTA's tile t
+        auto issue_s = [&]() -> bool {  // S of the next tile
 #pragma unroll
             for (int db = 0; db < NDB; ++db) {
-                if (!slot_full()) return false;
+                if (!wait(&full[slot], phase)) return false;
                 tc_fence_after();
                 if (elect_one()) {
                     const uint32_t ka = desc_lo(base + slot * SLOT, 16), qa = desc_lo(base + L::O_Q + db * SLOT, 16);
-                    const uint32_t d = L::T_S + (t & 1) * TILE;
+                    const uint32_t d = L::T_S + sb * TILE;
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
                         if (8 * db + q < ksteps)
                             mma_lo(d, qa + (((q >> 2) * SLAB + (q & 3) * 32) >> 4), ka + (((q >> 2) * SLAB + (q & 3) * 32) >> 4),
                                    idesc_bf16_f32(ROWS, TILE, 0, 0), db > 0 || q > 0);
                     mma_commit(&empty[slot]);
-                    if (db + 1 == NDB) mma_commit(&s_full[t & 1]);
+                    if (db + 1 == NDB) mma_commit(&s_full[sb]);
                 }
                 __syncwarp();
                 slot_done();
             }
+            sb = sb + 1 == L::NB ? 0 : sb + 1;
             return true;
         };
         bool ok = true;
-        while (ok && heard(ok)) {
+        for (;;) {
+            const bool more = heard(ok);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || !more) break;
             if (lane == 0) took_note();
             const int n = g.tile1 - g.tile0;
-            ok = wait_or_abort(q_full, (uint32_t)(seg & 1), abort_flag);
+            ok = wait(q_full, (uint32_t)(seg & 1));
             ++seg;
-            for (int j = -1; ok && j < n; ++j) {  // S of tile j + 1, then P V of tile j
-                // (S of tile j + 1 overwrites P of tile j - 1, whose P V has been issued before it: MMAs of one
-                // thread and shape run in order)
-                if (j + 1 < n && !issue_s(it + (j < 0 ? 0 : 1))) { ok = false; break; }
-                if (j + 2 == n && elect_one()) mma_commit(q_empty);
-                __syncwarp();
+            for (int j = -L::AHEAD; ok && j < n; ++j) {  // S of tile j + AHEAD, then P V of tile j
+                // (that S overwrites P of an earlier tile, whose P V has been issued before it: MMAs of one thread and
+                // shape run in order)
+                if (j + L::AHEAD < n && !issue_s()) { ok = false; break; }
                 if (j < 0) continue;
-                ok = it != a.stop_at;
-                if (!ok) break;
-                ok = wait_or_abort(&p_full[it & 1], (uint32_t)((it >> 1) & 1), abort_flag);
+                ok = it != a.stop_at && wait(&p_full[pb], p_phase);
                 if (!ok) break;
 #pragma unroll
                 for (int db = 0; db < NDB; ++db) {
-                    ok = slot_full();
+                    ok = wait(&full[slot], phase);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
                         const uint32_t va = desc_lo(base + slot * SLOT, SLAB);
-                        const uint32_t pa = L::T_S + (it & 1) * TILE;
+                        const uint32_t pa = L::T_S + pb * TILE;
 #pragma unroll
                         for (int q = 0; q < 8; ++q)  // 16 tokens: columns 8 (q % 2) of block q / 2's upper parts, then of its rests
 #pragma unroll
@@ -321,64 +328,36 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                                 mma_ts(L::T_O + db * 128, pa + (q >> 1) * 32 + lo * 16 + (q & 1) * 8, va + q * (2048 >> 4),
                                        idesc_bf16_f32(ROWS, 128, 0, 1), j > 0 || lo > 0 || q > 0);
                         mma_commit(&empty[slot]);
-                        if (db + 1 == NDB) mma_commit(&pv_done[it & 1]);
+                        if (db + 1 == NDB) mma_commit(&pv_done[pb]);
                     }
                     __syncwarp();
                     slot_done();
                 }
                 if (!ok) break;
                 ++it;
+                if (++pb == L::NB) {
+                    pb = 0;
+                    p_phase ^= 1;
+                }
             }
+            if (!ok) break;
         }
-        ok = __all_sync(0xffffffffu, ok);
         if (!ok) {  // MMAs that no commit above speaks of are waited for too
             if (elect_one()) mma_commit(drained);
             __syncwarp();
             mbar_wait(drained, 0, kWaitNs);
         }
-    } else if (warp == 2) {
-        // ------------------------------------------------ Q rows (zero beyond the block's rows and the head's dims)
-        int seg = 0;
-        bool ok = true;
-        for (;;) {
-            const bool more = heard(ok);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok || !more) break;
-            if (lane == 0) took_note();
-            if (seg > 0) ok = __all_sync(0xffffffffu, wait_or_abort(q_empty, (uint32_t)((seg - 1) & 1), abort_flag));
-            if (!ok) break;
-            const uint32_t qs = smem_u32(sm) + L::O_Q;
-            for (int r1 = 0; r1 < ROWS; r1 += 32) {
-                // a lane finds its row, then the warp copies the 32 rows together
-                const int mine = r1 + lane;
-                const int64_t at = mine < g.nr ? prefix_row(a, g.seq0, g.h, g.r0 + mine) * a.D : -1;
-                constexpr int CH = 16 * NDB;  // pieces of 8 dims per row
-#pragma unroll 4
-                for (int e = lane; e < 32 * CH; e += 32) {
-                    const int r = e / CH, ch = e % CH;
-                    const int64_t from = __shfl_sync(0xffffffffu, at, r);
-                    const bool real = from >= 0 && ch * 8 < a.D;
-                    const bf16* src = static_cast<const bf16*>(a.q) + (real ? from + ch * 8 : 0);
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                     qs + (ch >> 3) * SLAB + sw128_off((uint32_t)(r1 + r), (uint32_t)(ch & 7) * 8)),
-                                 "l"(src), "r"(real ? 16 : 0)
-                                 : "memory");
-                }
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
-            ++seg;
-        }
-    } else {
-        // ------------------------------------------------ softmax and outputs
+    } else if (warp >= 4) {
+        // ------------------------------------------------ Q, softmax and outputs
         const int wg = (warp - 4) >> 2, quad = warp & 3;
         const int row = quad * 32 + lane;  // TMEM lane
         const uint32_t tq = tb + ((uint32_t)(quad * 32) << 16);
         float* t_s = reinterpret_cast<float*>(sm + L::O_M);  // [2][128] the warpgroups' maxima of a tile
         float* l_s = reinterpret_cast<float*>(sm + L::O_L);  // [2][128] ... and sums
-        int it = 0;        // tiles before
+        int sb = 0;        // buffer of the next S
+        uint32_t s_phase = 0;
+        int last = 0;      // the buffer of the last tile
+        uint32_t last_phase = 0;
         bool live = true;  // no wait gave up: outputs are written only then
         auto wait = [&](uint64_t* bar, int k) {
             live = __all_sync(0xffffffffu, live && wait_or_abort(bar, (uint32_t)(k & 1), abort_flag));
@@ -392,12 +371,33 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             }
             if (!more) break;
             if (lane == 0) took_note();
+            // ---- Q (zero beyond the block's rows and the head's dims): a warp copies 16 rows
+            int64_t at = -1;  // a lane finds a row's elements
+            if (lane < 16 && (warp - 4) * 16 + lane < g.nr)
+                at = prefix_row(a, g.seq0, g.h, g.r0 + (warp - 4) * 16 + lane) * a.D;
+            constexpr int CH = 16 * NDB;  // pieces of 8 dims per row
+#pragma unroll 4
+            for (int e = lane; e < 16 * CH; e += 32) {
+                const int r = e / CH, ch = e % CH;
+                const int64_t from = __shfl_sync(0xffffffffu, at, r);
+                const bool real = from >= 0 && ch * 8 < a.D;
+                const bf16* src = static_cast<const bf16*>(a.q) + (real ? from + ch * 8 : 0);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 smem_u32(sm) + L::O_Q + (ch >> 3) * SLAB +
+                                 sw128_off((uint32_t)((warp - 4) * 16 + r), (uint32_t)(ch & 7) * 8)),
+                             "l"(src), "r"(real ? 16 : 0)
+                             : "memory");
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
             const int n = g.tile1 - g.tile0;
             float m = kNone;                      // the row's running maximum
             float2 l = make_float2(0.f, 0.f);     // the sum of this warpgroup's tokens
-            for (int j = 0; j < n; ++j, ++it) {
-                const uint32_t ts = tq + L::T_S + (it & 1) * TILE + wg * 64;
-                wait(&s_full[it & 1], it >> 1);
+            for (int j = 0; j < n; ++j) {
+                const uint32_t ts = tq + L::T_S + sb * TILE + wg * 64;
+                wait(&s_full[sb], s_phase);
                 tc_fence_after();
                 float x[64];
                 tmem_ld32(ts, x);
@@ -421,7 +421,7 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                     l.x *= f;
                     l.y *= f;
                     if (j > 0) {
-                        wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
+                        wait(&pv_done[last], last_phase);
                         tc_fence_after();
 #pragma unroll 1
                         for (int c = wg * 64 * NDB; c < (wg + 1) * 64 * NDB; c += 32) {
@@ -456,35 +456,55 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[it & 1]);
+                if (lane == 0) mbar_arrive(&p_full[sb]);
+                last = sb;
+                last_phase = s_phase;
+                if (++sb == L::NB) {
+                    sb = 0;
+                    s_phase ^= 1;
+                }
             }
             // ---- sums and outputs of the segment
             l_s[wg * ROWS + row] = l.x + l.y;
-            wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
+            wait(&pv_done[last], last_phase);
             tc_fence_after();
             softmax_sync();
             const float sum = l_s[row] + l_s[ROWS + row];
             const bool real = row < g.nr && live;
-            float *po, *slot = prefix_slot(s, blockIdx.x);
+            float *po = nullptr, *slot = prefix_slot(s, blockIdx.x);
             if (g.parts > 0) {
-                const int64_t at = real ? prefix_row(a, g.seq0, g.h, g.r0 + row) : 0;
-                po = s.pre_o + at * a.D;
-                if (real && wg == 0) s.pre_stat[at] = prefix_stat(m, sum, g.parts, row);
-            } else {
+                if (real) {
+                    const int64_t to = prefix_row(a, g.seq0, g.h, g.r0 + row);
+                    po = s.pre_o + to * a.D;
+                    if (wg == 0) s.pre_stat[to] = prefix_stat(m, sum, g.parts, row);
+                }
+            } else if (real) {
                 po = slot + 2 * ROWS + row * a.D;
-                if (real && wg == 0) {
+                if (wg == 0) {
                     slot[row] = sum == 0.f ? -INFINITY : m;
                     slot[ROWS + row] = sum;
                 }
             }
+            // outputs, 32 columns at a time, turned in Q's memory so that 8 lanes write 128 bytes of a row (a lane per
+            // row touches 32 lines at each store: 13 us a segment of head dim 256)
+            float4* o_s = reinterpret_cast<float4*>(sm + L::O_Q + (warp - 4) * 4096);
 #pragma unroll 1
-            for (int c = wg * 64 * NDB; c < (wg + 1) * 64 * NDB; c += 32) {
+            for (int c = wg * 64 * NDB; c < (wg + 1) * 64 * NDB && c < a.D; c += 32) {
                 float o[32];
                 tmem_ld32(tq + L::T_O + c, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    if (real && c + i < a.D) *reinterpret_cast<float4*>(po + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                for (int i = 0; i < 8; ++i)
+                    o_s[lane * 8 + (i ^ (lane & 7))] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 4 * i + (lane >> 3), d = c + (lane & 7) * 4;
+                    float* to = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(po), r));
+                    const float4 v = o_s[r * 8 + ((lane & 7) ^ (r & 7))];
+                    if (to != nullptr && d < a.D) *reinterpret_cast<float4*>(to + d) = v;
+                }
+                __syncwarp();
             }
             tc_fence_before();
             softmax_sync();  // O and the sums are free

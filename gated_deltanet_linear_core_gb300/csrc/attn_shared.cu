@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
         if (warp == 0) {  // lane i: group g0 + i
             const int gi = g0 + lane;
             int64_t units = 0;
+            PrefixGroup grp = {};
             if (lane < at_once && gi < s.G) {
                 least = first = INT32_MAX;
                 count = 0;
@@ -63,11 +64,13 @@ __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
                 // less than the first new token of any sequence sees
                 int share = count > 1 ? min(s.prefix[gi], least - a.K) : 0;
                 share = share > 0 ? share / kShareStep * kShareStep : 0;
-                int seq0, seq1;
-                group_bounds(s, gi, seq0, seq1);
-                if (share > 0) units = group_blocks(s, seq1 - seq0) * a.H_kv * (s.setup + share / s.tile);
-                s.share[gi] = share_s[lane] = share;
-                s.leader[gi] = first == INT32_MAX ? 0 : first;
+                int seq1;
+                group_bounds(s, gi, grp.seq0, seq1);
+                grp.seqs = seq1 - grp.seq0;
+                grp.blocks = (int)(((int64_t)grp.seqs * a.rows + s.rows_per_block - 1) / s.rows_per_block);
+                grp.share = share_s[lane] = share;
+                grp.leader = first == INT32_MAX ? 0 : first;
+                if (share > 0) units = (int64_t)grp.blocks * a.H_kv * (s.setup + share / s.tile);
             }
             int64_t inc = units;
 #pragma unroll
@@ -75,7 +78,8 @@ __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
                 const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += v;
             }
-            if (lane < at_once && gi < s.G) s.unit0[gi] = before + inc - units;
+            grp.unit0 = before + inc - units;
+            if (lane < at_once && gi < s.G) s.groups[gi] = grp;
             before += __shfl_sync(0xffffffffu, inc, 31);
         }
         __syncthreads();
@@ -87,7 +91,7 @@ __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
         }
         __syncthreads();
     }
-    if (tid == 0) s.unit0[s.G] = before;
+    if (tid == 0) s.groups[s.G].unit0 = before;
 }
 
 struct Running {
@@ -251,9 +255,7 @@ size_t attn_share_plan(ShareArgs& s, gdn_dtype_t dt, void* ws) {
     s.pre_o = reinterpret_cast<float*>(take(rows * a.D * sizeof(float)));
     a.part_stat = reinterpret_cast<float4*>(take(rows * sizeof(float4)));
     s.pre_stat = reinterpret_cast<float4*>(take(rows * sizeof(float4)));
-    s.unit0 = reinterpret_cast<int64_t*>(take(((size_t)s.G + 1) * sizeof(int64_t)));
-    s.share = reinterpret_cast<int32_t*>(take((size_t)s.G * sizeof(int32_t)));
-    s.leader = reinterpret_cast<int32_t*>(take((size_t)s.G * sizeof(int32_t)));
+    s.groups = reinterpret_cast<PrefixGroup*>(take(((size_t)s.G + 1) * sizeof(PrefixGroup)));
     a.skip = reinterpret_cast<int32_t*>(take((size_t)a.B * sizeof(int32_t)));
     return at + 256;
 }

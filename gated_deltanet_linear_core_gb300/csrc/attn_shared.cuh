@@ -25,11 +25,6 @@ __device__ __forceinline__ void group_bounds(const ShareArgs& s, int g, int& lo,
         hi = min(max(s.cu[g + 1], lo), s.a.B);
     }
 }
-// Row blocks of a group of `n` sequences.
-__device__ __forceinline__ int64_t group_blocks(const ShareArgs& s, int n) {
-    return ((int64_t)n * s.a.rows + s.rows_per_block - 1) / s.rows_per_block;
-}
-
 // A part of an item of the pass over the prefixes, worked on by one CTA.
 struct PrefixSegment {
     int tile0, tile1;  // its tiles; 0, 0: the CTA's range has ended
@@ -48,7 +43,7 @@ struct PrefixWalk {
     int64_t total, at, end;
     int c, n;  // the CTA, of how many that take part
     __device__ __forceinline__ PrefixWalk(const ShareArgs& s, int c_, int n_) : c(c_), n(n_) {
-        total = s.unit0[s.G];
+        total = s.groups[s.G].unit0;
         if (n > total) n = (int)total;
         at = c < n ? cta_begin(total, c, n) : 0;
         end = c < n ? cta_begin(total, c + 1, n) : 0;
@@ -58,13 +53,12 @@ struct PrefixWalk {
             int lo = 0, hi = s.G - 1;  // the last group that starts at or before the unit
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                if (s.unit0[mid] <= at) lo = mid; else hi = mid - 1;
+                if (s.groups[mid].unit0 <= at) lo = mid; else hi = mid - 1;
             }
-            int seq0, seq1;
-            group_bounds(s, lo, seq0, seq1);
-            const int rows = (seq1 - seq0) * s.a.rows, blocks = (int)group_blocks(s, seq1 - seq0);
-            const int units = s.setup + min(max(s.share[lo], 0), s.a.max_pages * s.a.page_size) / tile;
-            const int64_t off = at - s.unit0[lo];
+            const PrefixGroup grp = s.groups[lo];
+            const int rows = grp.seqs * s.a.rows;
+            const int units = s.setup + min(max(grp.share, 0), s.a.max_pages * s.a.page_size) / tile;
+            const int64_t off = at - grp.unit0;
             const int64_t item = off / units;
             const int from = (int)(off - item * units);
             const int64_t left = end - at;
@@ -75,11 +69,11 @@ struct PrefixWalk {
             g.tile0 = from > s.setup ? from - s.setup : 0;
             g.tile1 = upto - s.setup;
             g.parts = g.tile0 > 0 ? 0 : cta_of(total, last, n) - c + 1;
-            g.h = blocks > 0 ? (int)(item / blocks) : s.a.H_kv;
+            g.h = grp.blocks > 0 ? (int)(item / grp.blocks) : s.a.H_kv;
             if (g.h >= s.a.H_kv) return false;  // (never in a call that keeps to the rules)
-            g.seq0 = seq0;
-            g.leader = min(max(s.leader[lo], 0), s.a.B - 1);
-            g.r0 = (int)(item - (int64_t)g.h * blocks) * s.rows_per_block;
+            g.seq0 = grp.seq0;
+            g.leader = min(max(grp.leader, 0), s.a.B - 1);
+            g.r0 = (int)(item - (int64_t)g.h * grp.blocks) * s.rows_per_block;
             g.nr = min(s.rows_per_block, rows - g.r0);
             return true;
         }

@@ -195,13 +195,20 @@ cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaS
 // each sequence has of its own (the kernels above), and a merge of both (attn_shared.cuh).
 constexpr int kPrefixFfmaRows = 64;
 constexpr int kShareStep = 128;  // a prefix is shared down to a multiple of this many tokens
+struct alignas(16) PrefixGroup {
+    int64_t unit0;    // first unit of the group's items
+    int seq0, seqs;   // its sequences
+    int share;        // tokens that are shared in earnest
+    int leader;       // the sequence whose pages are read
+    int blocks;       // row blocks
+    int pad;
+};
 struct ShareArgs {
     AttnArgs a;                        // the sequences' own tokens
     const int32_t *prefix, *cu;        // [G] tokens; [G + 1] sequences or null: one group
     int G;
     int rows_per_block, tile, setup;   // of the pass over the prefixes: rows and tokens per tile, units of an item's start
-    int32_t *share, *leader;           // [G] tokens that are shared in earnest; the sequence whose pages are read
-    int64_t* unit0;                    // [G + 1] first unit of the groups' items
+    PrefixGroup* groups;               // [G + 1], the last one's unit0 all units
     float* pre_o;                      // [B, K, H_q, D], [B, K, H_q]: the prefix items' first parts, as a.part_o and a.part_stat
     float4* pre_stat;
     float* pre_slots;                  // per CTA: a part that starts inside an item
