@@ -257,10 +257,9 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMAs
-        // The whole warp runs the loop and one elected lane issues: with addresses that are constants but for the slot
-        // and the buffer (the allocation is all of tensor memory, so it starts at 0), an MMA costs few instructions,
+        // The whole warp runs the loop and one elected lane waits and issues: with addresses that are constants but for the
+        // slot and the buffer (the allocation is all of tensor memory, so it starts at 0), an MMA costs few instructions,
         // which the warp has to get past two busy softmax warps of its scheduler.
-        // (Its lanes agree on every wait: they meet at the elections.)
         const uint32_t base = smem_u32(sm);
         const int ksteps = (a.D + 15) / 16;
         int it = 0, seg = 0;        // tiles and segments before
@@ -268,34 +267,11 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
         uint32_t phase = 0;
         int sb = 0, pb = 0;         // the buffers of the next S, of the next P
         uint32_t p_phase = 0;
-        auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag)); };
-        auto slot_done = [&] {
-            if (++slot == NS) {
-                slot = 0;
-                phase ^= 1;
+        auto slot_done = [&](int& sl, uint32_t& ph) {
+            if (++sl == NS) {
+                sl = 0;
+                ph ^= 1;
             }
-        };
-        auto issue_s = [&]() -> bool {  // S of the next tile
-#pragma unroll
-            for (int db = 0; db < NDB; ++db) {
-                if (!wait(&full[slot], phase)) return false;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t ka = desc_lo(base + slot * SLOT, 16), qa = desc_lo(base + L::O_Q + db * SLOT, 16);
-                    const uint32_t d = L::T_S + sb * TILE;
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (8 * db + q < ksteps)
-                            mma_lo(d, qa + (((q >> 2) * SLAB + (q & 3) * 32) >> 4), ka + (((q >> 2) * SLAB + (q & 3) * 32) >> 4),
-                                   idesc_bf16_f32(ROWS, TILE, 0, 0), db > 0 || q > 0);
-                    mma_commit(&empty[slot]);
-                    if (db + 1 == NDB) mma_commit(&s_full[sb]);
-                }
-                __syncwarp();
-                slot_done();
-            }
-            sb = sb + 1 == L::NB ? 0 : sb + 1;
-            return true;
         };
         bool ok = true;
         for (;;) {
@@ -304,40 +280,69 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             if (!ok || !more) break;
             if (lane == 0) took_note();
             const int n = g.tile1 - g.tile0;
-            ok = wait(q_full, (uint32_t)(seg & 1));
+            ok = __all_sync(0xffffffffu, wait_or_abort(q_full, (uint32_t)(seg & 1), abort_flag));
             ++seg;
-            for (int j = -L::AHEAD; ok && j < n; ++j) {  // S of tile j + AHEAD, then P V of tile j
-                // (that S overwrites P of an earlier tile, whose P V has been issued before it: MMAs of one thread and
-                // shape run in order)
-                if (j + L::AHEAD < n && !issue_s()) { ok = false; break; }
-                if (j < 0) continue;
-                ok = it != a.stop_at && wait(&p_full[pb], p_phase);
-                if (!ok) break;
+            for (int j = -L::AHEAD; ok && j < n; ++j) {
+                // S of tile j + AHEAD, then P V of tile j (that S overwrites P of an earlier tile, whose P V has been issued
+                // before it: MMAs of one thread and shape run in order)
+                const bool has_s = j + L::AHEAD < n, has_pv = j >= 0;
+                if (elect_one()) {
+                    int sl = slot;
+                    uint32_t ph = phase;
+                    if (has_s) {
 #pragma unroll
-                for (int db = 0; db < NDB; ++db) {
-                    ok = wait(&full[slot], phase);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t va = desc_lo(base + slot * SLOT, SLAB);
-                        const uint32_t pa = L::T_S + pb * TILE;
+                        for (int db = 0; db < NDB; ++db) {
+                            ok = ok && wait_or_abort(&full[sl], ph, abort_flag);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t ka = desc_lo(base + sl * SLOT, 16), qa = desc_lo(base + L::O_Q + db * SLOT, 16);
+                            const uint32_t d = L::T_S + sb * TILE;
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)  // 16 tokens: columns 8 (q % 2) of block q / 2's upper parts, then of its rests
-#pragma unroll
-                            for (int lo = 0; lo < 2; ++lo)
-                                mma_ts(L::T_O + db * 128, pa + (q >> 1) * 32 + lo * 16 + (q & 1) * 8, va + q * (2048 >> 4),
-                                       idesc_bf16_f32(ROWS, 128, 0, 1), j > 0 || lo > 0 || q > 0);
-                        mma_commit(&empty[slot]);
-                        if (db + 1 == NDB) mma_commit(&pv_done[pb]);
+                            for (int q = 0; q < 8; ++q)
+                                if (8 * db + q < ksteps)
+                                    mma_lo(d, qa + (((q >> 2) * SLAB + (q & 3) * 32) >> 4),
+                                           ka + (((q >> 2) * SLAB + (q & 3) * 32) >> 4), idesc_bf16_f32(ROWS, TILE, 0, 0),
+                                           db > 0 || q > 0);
+                            mma_commit(&empty[sl]);
+                            if (db + 1 == NDB) mma_commit(&s_full[sb]);
+                            slot_done(sl, ph);
+                        }
                     }
-                    __syncwarp();
-                    slot_done();
+                    if (has_pv) {
+                        ok = ok && it != a.stop_at && wait_or_abort(&p_full[pb], p_phase, abort_flag);
+#pragma unroll
+                        for (int db = 0; db < NDB; ++db) {
+                            ok = ok && wait_or_abort(&full[sl], ph, abort_flag);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t va = desc_lo(base + sl * SLOT, SLAB);
+                            const uint32_t pa = L::T_S + pb * TILE;
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)  // 16 tokens: columns 8 (q % 2) of block q / 2's upper parts, then of its rests
+#pragma unroll
+                                for (int lo = 0; lo < 2; ++lo)
+                                    mma_ts(L::T_O + db * 128, pa + (q >> 1) * 32 + lo * 16 + (q & 1) * 8, va + q * (2048 >> 4),
+                                           idesc_bf16_f32(ROWS, 128, 0, 1), j > 0 || lo > 0 || q > 0);
+                            mma_commit(&empty[sl]);
+                            if (db + 1 == NDB) mma_commit(&pv_done[pb]);
+                            slot_done(sl, ph);
+                        }
+                    }
                 }
-                if (!ok) break;
-                ++it;
-                if (++pb == L::NB) {
-                    pb = 0;
-                    p_phase ^= 1;
+                ok = __all_sync(0xffffffffu, ok);
+                if (has_s) {
+                    sb = sb + 1 == L::NB ? 0 : sb + 1;
+#pragma unroll
+                    for (int db = 0; db < NDB; ++db) slot_done(slot, phase);
+                }
+                if (has_pv) {
+#pragma unroll
+                    for (int db = 0; db < NDB; ++db) slot_done(slot, phase);
+                    ++it;
+                    if (++pb == L::NB) {
+                        pb = 0;
+                        p_phase ^= 1;
+                    }
                 }
             }
             if (!ok) break;
