@@ -316,8 +316,8 @@ __global__ void __launch_bounds__(Ffma<E, R, NV>::NT, 1) attn_ffma_kernel(AttnAr
                 const int64_t row = row_index(a, s.b, s.h, r0 + r);
                 *reinterpret_cast<float4*>(a.part_o + row * D + d) = y;
                 if (d == 0)
-                    a.part_stat[row] = make_float4(top == kNone ? -INFINITY : top, sum, __int_as_float(blockIdx.x),
-                                                   __int_as_float(s.tiles));
+                    a.part_stat[row] = make_float4(top == kNone ? -INFINITY : top, sum,
+                                                   __int_as_float((int)blockIdx.x | s.tiles << 16), __int_as_float(r));
             } else {
                 *reinterpret_cast<float4*>(slot + a.stat_floats + r * D + d) = y;
                 if (d == 0) {

@@ -46,16 +46,16 @@ __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
     const int D = a.D, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     pdl_wait();
     pdl_trigger();
-    PrefixWalk walk(s, blockIdx.x, gridDim.x);
-    PrefixSegment g;
+    SharedWalk walk(s, blockIdx.x, gridDim.x);
+    SharedSegment g;
     const int fours = D / 4;
     for (int i = tid; i < 3 * 64 * QS; i += NT) sm[i] = 0.f;  // dims from D on stay zero
-    while (walk.next(s, TT, g)) {
+    while (walk.next(s, g)) {
         __syncthreads();
         for (int e = tid; e < ROWS * fours; e += NT) {
             const int r = e / fours, d = (e - r * fours) * 4;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < g.nr) x = ld4(static_cast<const E*>(a.q) + prefix_row(a, g.seq0, g.h, g.r0 + r) * D + d);
+            if (r < g.nr) x = ld4(static_cast<const E*>(a.q) + shared_row(a, g.seq0, g.h, g.r0 + r) * D + d);
             *reinterpret_cast<float4*>(q_s + r * QS + d) = x;
         }
         float m[4], l[4], o[4][4 * NC];
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
             __syncthreads();
         }
         // ---- the rows' part
-        float* slot = prefix_slot(s, blockIdx.x);
+        float* slot = shared_slot(s, blockIdx.x);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float sum = l[i];
@@ -164,9 +164,9 @@ __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
             if (r >= g.nr) continue;
             float* po;
             if (g.parts > 0) {
-                const int64_t at = prefix_row(a, g.seq0, g.h, g.r0 + r);
+                const int64_t at = shared_row(a, g.seq0, g.h, g.r0 + r);
                 po = s.pre_o + at * D;
-                if (tx == 0) s.pre_stat[at] = prefix_stat(m[i], sum, g.parts, r);
+                if (tx == 0) s.pre_stat[at] = part_stat(m[i], sum, g.parts, r);
             } else {
                 po = slot + 2 * ROWS + r * D;
                 if (tx == 0) {

@@ -15,6 +15,7 @@ constexpr int MT = 256;   // threads of a merge block that takes several rows
 // looks at a group's lengths.
 __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
     __shared__ int least_s[32], first_s[32], count_s[32], share_s[32];
+    __shared__ int64_t sums_s[32], before_s;
     const AttnArgs& a = s.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int32_t* skip = const_cast<int32_t*>(a.skip);
@@ -52,7 +53,7 @@ __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
         if (warp == 0) {  // lane i: group g0 + i
             const int gi = g0 + lane;
             int64_t units = 0;
-            PrefixGroup grp = {};
+            ShareRecord grp = {};
             if (lane < at_once && gi < s.G) {
                 least = first = INT32_MAX;
                 count = 0;
@@ -68,9 +69,10 @@ __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
                 group_bounds(s, gi, grp.seq0, seq1);
                 grp.seqs = seq1 - grp.seq0;
                 grp.blocks = (int)(((int64_t)grp.seqs * a.rows + s.rows_per_block - 1) / s.rows_per_block);
-                grp.share = share_s[lane] = share;
+                share_s[lane] = share;
+                grp.tiles = share / s.tile;
                 grp.leader = first == INT32_MAX ? 0 : first;
-                if (share > 0) units = (int64_t)grp.blocks * a.H_kv * (s.setup + share / s.tile);
+                if (share > 0) units = (int64_t)grp.blocks * a.H_kv * (s.setup + grp.tiles);
             }
             int64_t inc = units;
 #pragma unroll
@@ -79,7 +81,7 @@ __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
                 if (lane >= o) inc += v;
             }
             grp.unit0 = before + inc - units;
-            if (lane < at_once && gi < s.G) s.groups[gi] = grp;
+            if (lane < at_once && gi < s.G) s.rec[gi] = grp;
             before += __shfl_sync(0xffffffffu, inc, 31);
         }
         __syncthreads();
@@ -91,7 +93,40 @@ __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
         }
         __syncthreads();
     }
-    if (tid == 0) s.groups[s.G].unit0 = before;
+    // what the sequences have of their own
+    if (tid == 0) before_s = before;
+    __syncthreads();
+    const int blocks = (a.rows + s.rows_per_block - 1) / s.rows_per_block;
+    for (int b0 = 0; s.G + b0 < s.records; b0 += PT) {
+        const int b = b0 + tid;
+        ShareRecord own = {};
+        int64_t units = 0;
+        if (b < a.B) {
+            const int n = clamped_len(a, b);
+            own.seq0 = own.leader = b;
+            own.seqs = 1;
+            own.blocks = blocks;
+            own.tile0 = skip[b] / s.tile;
+            own.tiles = n > 0 ? (n - 1) / s.tile + 1 - own.tile0 : 0;
+            if (n > 0) units = (int64_t)blocks * a.H_kv * (s.setup + own.tiles);
+        }
+        int64_t inc = units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) sums_s[warp] = inc;
+        __syncthreads();
+        int64_t start = before_s;
+        for (int w = 0; w < warp; ++w) start += sums_s[w];
+        own.unit0 = start + inc - units;
+        if (b < a.B) s.rec[s.G + b] = own;
+        __syncthreads();
+        if (tid == PT - 1) before_s = start + inc;
+        __syncthreads();
+    }
+    if (tid == 0) s.rec[s.records].unit0 = before_s;
 }
 
 struct Running {
@@ -142,7 +177,7 @@ __global__ void __launch_bounds__(WIDE ? 1024 : MT) attn_merge_kernel(ShareArgs 
     const int64_t rows = (int64_t)a.B * a.K * a.H_q, row = WIDE ? blockIdx.x : (int64_t)blockIdx.x * groups + g;
     if (row >= rows) return;
     const int b = (int)(row / (a.K * a.H_q)), rest = (int)(row - (int64_t)b * a.K * a.H_q);
-    const int i = rest / a.H_q, hq = rest - i * a.H_q;
+    const int i = rest / a.H_q;
     const float4 own_stat = a.part_stat[row];
     const float4 pre_stat = s.pre_stat[row];  // (of no meaning where nothing is shared)
     const int len = clamped_len(a, b), shared = a.skip[b];
@@ -150,15 +185,15 @@ __global__ void __launch_bounds__(WIDE ? 1024 : MT) attn_merge_kernel(ShareArgs 
     float4 gt = make_float4(0.f, 0.f, 0.f, 0.f);
     if (a.gate != nullptr && (!WIDE || g == 0)) gt = ld4(static_cast<const T*>(a.gate) + at);
     // the row's parts: those of its own tokens (of the CTAs c_own ..), then the prefix's
-    const int c_own = __float_as_int(own_stat.z), c_pre = __float_as_int(pre_stat.z) & 0xffff;
-    const int r_own = (i * a.group + hq % a.group) % a.rb_rows, r_pre = __float_as_int(pre_stat.w);
-    int n_own = __float_as_int(own_stat.w), n_pre = shared > 0 ? __float_as_int(pre_stat.z) >> 16 : 0;
+    const bool one_kind = s.records > s.G;  // own tokens are records too, in the same slots
+    const int own_rows = one_kind ? s.rows_per_block : a.rb_rows;
+    const int c_own = __float_as_int(own_stat.z) & 0xffff, r_own = __float_as_int(own_stat.w);
+    const int c_pre = __float_as_int(pre_stat.z) & 0xffff, r_pre = __float_as_int(pre_stat.w);
+    int n_own = __float_as_int(own_stat.z) >> 16, n_pre = shared > 0 ? __float_as_int(pre_stat.z) >> 16 : 0;
     if (len - (a.K - 1 - i) <= 0) n_own = n_pre = 0;  // sees nothing
     // (the bounds hold for every call that keeps to the rules; they keep others' reads in bounds)
-    if ((unsigned)n_own > kAttnMaxCtas || (n_own > 0 && ((unsigned)c_own >= kAttnMaxCtas || c_own + n_own > kAttnMaxCtas)))
-        n_own = 0;
-    if ((unsigned)n_pre > kAttnMaxCtas || (n_pre > 0 && (c_pre + n_pre > kAttnMaxCtas || (unsigned)r_pre >= (unsigned)s.rows_per_block)))
-        n_pre = 0;
+    if (n_own < 0 || c_own + n_own > kAttnMaxCtas || (unsigned)r_own >= (unsigned)own_rows) n_own = 0;
+    if (n_pre < 0 || c_pre + n_pre > kAttnMaxCtas || (unsigned)r_pre >= (unsigned)s.rows_per_block) n_pre = 0;
     const int n = n_own + n_pre;
     Running run;
 #pragma unroll 1
@@ -179,11 +214,11 @@ __global__ void __launch_bounds__(WIDE ? 1024 : MT) attn_merge_kernel(ShareArgs 
                 l[k] = own ? own_stat.y : pre_stat.y;
                 x[k] = ld4((own ? a.part_o : s.pre_o) + at);
             } else {
-                const float* slot = own ? slot_ptr(a, c_own + nth) : prefix_slot(s, c_pre + nth);
-                const int r = own ? r_own : r_pre, per = own ? a.rb_rows : s.rows_per_block;
+                const float* slot = own && !one_kind ? slot_ptr(a, c_own + nth) : shared_slot(s, (own ? c_own : c_pre) + nth);
+                const int r = own ? r_own : r_pre, per = own ? own_rows : s.rows_per_block;
                 m[k] = slot[r];
                 l[k] = slot[per + r];
-                x[k] = ld4(slot + (own ? a.stat_floats : 2 * per) + r * a.D + d);
+                x[k] = ld4(slot + (own && !one_kind ? a.stat_floats : 2 * per) + r * a.D + d);
             }
         }
         run.add(m, l, x);
@@ -237,10 +272,11 @@ size_t attn_share_plan(ShareArgs& s, gdn_dtype_t dt, void* ws) {
     AttnArgs& a = s.a;
     attn_plan(a, dt);
     const bool tc = attn_tc_takes(a, dt);
+    s.records = s.G + (tc ? a.B : 0);
     s.rows_per_block = tc ? 128 : kPrefixFfmaRows;
     s.tile = tc ? 128 : 64;
     s.setup = 1;
-    s.pre_slot_floats = 2 * s.rows_per_block + (int64_t)s.rows_per_block * a.D;
+    s.slot_floats = 2 * s.rows_per_block + (int64_t)s.rows_per_block * a.D;
     const size_t rows = (size_t)a.B * a.K * a.H_q;
     char* base = reinterpret_cast<char*>(up(reinterpret_cast<size_t>(ws)));
     size_t at = 0;
@@ -249,13 +285,13 @@ size_t attn_share_plan(ShareArgs& s, gdn_dtype_t dt, void* ws) {
         at += up(bytes);
         return p;
     };
-    a.ws = reinterpret_cast<float*>(take(kAttnMaxCtas * (sizeof(JoinTask) + (size_t)a.slot_floats * sizeof(float))));
-    s.pre_slots = reinterpret_cast<float*>(take(kAttnMaxCtas * (size_t)s.pre_slot_floats * sizeof(float)));
+    if (!tc) a.ws = reinterpret_cast<float*>(take(kAttnMaxCtas * (sizeof(JoinTask) + (size_t)a.slot_floats * sizeof(float))));
+    s.slots = reinterpret_cast<float*>(take(kAttnMaxCtas * (size_t)s.slot_floats * sizeof(float)));
     a.part_o = reinterpret_cast<float*>(take(rows * a.D * sizeof(float)));
     s.pre_o = reinterpret_cast<float*>(take(rows * a.D * sizeof(float)));
     a.part_stat = reinterpret_cast<float4*>(take(rows * sizeof(float4)));
     s.pre_stat = reinterpret_cast<float4*>(take(rows * sizeof(float4)));
-    s.groups = reinterpret_cast<PrefixGroup*>(take(((size_t)s.G + 1) * sizeof(PrefixGroup)));
+    s.rec = reinterpret_cast<ShareRecord*>(take(((size_t)s.records + 1) * sizeof(ShareRecord)));
     a.skip = reinterpret_cast<int32_t*>(take((size_t)a.B * sizeof(int32_t)));
     return at + 256;
 }
@@ -266,8 +302,8 @@ cudaError_t launch_attn_shared(const ShareArgs& s, gdn_dtype_t dt, cudaStream_t 
     const int n_cta = attn_ctas();
     const bool tc = attn_tc_takes(a, dt);
     cudaError_t e = launch_pdl(attn_share_plan_kernel, dim3(1), dim3(PT), 0, st, s);
-    if (e == cudaSuccess) e = tc ? launch_prefix_tc(s, n_cta, st) : launch_prefix_ffma(s, n_cta, dt, st);
-    if (e == cudaSuccess) e = tc ? launch_attn_tc(a, n_cta, st) : launch_attn_ffma(a, n_cta, dt, st);
+    if (e == cudaSuccess) e = tc ? launch_shared_tc(s, n_cta, st) : launch_prefix_ffma(s, n_cta, dt, st);
+    if (e == cudaSuccess && !tc) e = launch_attn_ffma(a, n_cta, dt, st);
     if (e != cudaSuccess) return e;
     return dt == GDN_BF16 ? launch_merge<bf16>(s, n_cta, st) : launch_merge<float>(s, n_cta, st);
 }

@@ -24,7 +24,7 @@
 
 namespace gdn {
 
-__device__ int g_prefix_error;  // bit 0: a bounded wait gave up
+__device__ int g_shared_error;  // bit 0: a bounded wait gave up
 
 namespace {
 
@@ -53,7 +53,7 @@ struct Layout {
     static constexpr int SEGS = 4;  // segments told ahead
     static_assert(SMEM <= kSmemMax && NS >= 4 && NB * TILE <= T_O && 8 * 4096 <= Q_BYTES, "memory");
 };
-static_assert(sizeof(PrefixSegment) == 32 && 4 * 32 <= 512, "notes");
+static_assert(4 * sizeof(SharedSegment) <= 512, "notes");
 
 // D += A B with A in tensor memory (two bf16 per column), B by its descriptor's low word.
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
@@ -102,7 +102,7 @@ __device__ __forceinline__ bool pair_any(int quad, bool x) {
 
 template <int NDB>
 __global__ void __launch_bounds__(NT, 1)
-attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, ShareArgs s,
+attn_shared_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, ShareArgs s,
                       int piece) {
     using L = Layout<NDB>;
     constexpr int NS = L::NS;
@@ -122,7 +122,8 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 37);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     volatile int* filled = reinterpret_cast<volatile int*>(bars + 38);  // [2 loading warps][6] loads into a slot
-    PrefixSegment* notes = reinterpret_cast<PrefixSegment*>(sm + L::O_SEG);
+    volatile int* odd_v = reinterpret_cast<volatile int*>(bars + 44);   // a new token's value is not finite
+    SharedSegment* notes = reinterpret_cast<SharedSegment*>(sm + L::O_SEG);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
@@ -143,6 +144,7 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             mbar_init(&seg_empty[i], 2 + NSOFT / 32);
         }
         *abort_flag = 0;
+        *odd_v = 0;
         fence_mbar_init();
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
@@ -158,7 +160,7 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     pdl_wait();
     pdl_trigger();
 
-    PrefixSegment g;
+    SharedSegment g;
     int sg = 0;  // segments told or taken note of
     // The next segment, from warp 0: false at the end of the CTA's range.  `ok` turns false where the wait gave up.
     auto heard = [&](bool& ok) -> bool {
@@ -176,8 +178,9 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     auto look_up = [&](int tile, int& y, int& z) {
         z = a.n_pages;  // reads as zeros
         y = 0;
-        if (lane < np) {
-            const int t = tile * TILE + lane * piece, pg = t / a.page_size;
+        const int t = tile * TILE + lane * piece;
+        if (lane < np && (g.len == 0 || t < g.len)) {
+            const int pg = t / a.page_size;
             const int page = a.table[(int64_t)g.leader * a.max_pages + pg];
             if (page >= 0 && page < a.n_pages) z = page;
             y = g.h * a.page_size + (t - pg * a.page_size);
@@ -228,11 +231,11 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
 
     if (warp == 0) {
         // ------------------------------------------------ the walk; K and V, lower slabs
-        PrefixWalk walk(s, blockIdx.x, gridDim.x);
+        SharedWalk walk(s, blockIdx.x, gridDim.x);
         bool ok = true, more = true;
         while (ok && more) {
             g.tile0 = g.tile1 = 0;
-            more = walk.next(s, TILE, g);
+            more = walk.next(s, g);
             const int e = sg % L::SEGS;
             if (sg >= L::SEGS)
                 ok = __all_sync(0xffffffffu, wait_or_abort(&seg_empty[e], (uint32_t)((sg / L::SEGS - 1) & 1), abort_flag));
@@ -359,6 +362,8 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
         const uint32_t tq = tb + ((uint32_t)(quad * 32) << 16);
         float* t_s = reinterpret_cast<float*>(sm + L::O_M);  // [2][128] the warpgroups' maxima of a tile
         float* l_s = reinterpret_cast<float*>(sm + L::O_L);  // [2][128] ... and sums
+        const int st = tid - 128;  // softmax thread
+        int sl0 = 0;               // slots filled for the segments before
         int sb = 0;        // buffer of the next S
         uint32_t s_phase = 0;
         int last = 0;      // the buffer of the last tile
@@ -366,6 +371,33 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
         bool live = true;  // no wait gave up: outputs are written only then
         auto wait = [&](uint64_t* bar, int k) {
             live = __all_sync(0xffffffffu, live && wait_or_abort(bar, (uint32_t)(k & 1), abort_flag));
+        };
+        // V rows behind the sequence's end become zeros (whatever lies there times a weight of 0 could be NaN); so do
+        // non-finite values of the new tokens that not all rows see: the rows that do get them back at the end.
+        auto mend_v = [&](int j, int n, int t0) {
+            const int valid = min(TILE, g.len - t0), from = max(0, g.len - a.K + 1 - t0);
+#pragma unroll 1
+            for (int db = 0; db < NDB; ++db) {
+                const int k = sl0 + (min(j + L::AHEAD + 1, n) + j) * NDB + db, slot = k % NS, nth = k / NS;
+                // until a slot's load is issued its barrier's parity speaks of the load before last
+                live = __all_sync(0xffffffffu, live && loaded_or_abort(&filled[slot], nth + 1, abort_flag) &&
+                                                   loaded_or_abort(&filled[6 + slot], nth + 1, abort_flag));
+                wait(&full[slot], nth);
+                const int slabs = min(2, nslab - 2 * db);
+                for (int e = st; e < (TILE - from) * slabs * 8; e += NSOFT) {
+                    const int t = from + e / (slabs * 8), rest = e % (slabs * 8);
+                    uint4* p = reinterpret_cast<uint4*>(sm + slot * SLOT + (rest >> 3) * SLAB + t * 128 + (rest & 7) * 16);
+                    if (t >= valid) {
+                        *p = make_uint4(0u, 0u, 0u, 0u);
+                    } else {
+                        const uint4 v = *p;
+                        if (!finite_bf16x8(v)) {
+                            *odd_v = 1;
+                            *p = make_uint4(zero_non_finite(v.x), zero_non_finite(v.y), zero_non_finite(v.z), zero_non_finite(v.w));
+                        }
+                    }
+                }
+            }
         };
         for (;;) {
             bool ok;
@@ -379,7 +411,7 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             // ---- Q (zero beyond the block's rows and the head's dims): a warp copies 16 rows
             int64_t at = -1;  // a lane finds a row's elements
             if (lane < 16 && (warp - 4) * 16 + lane < g.nr)
-                at = prefix_row(a, g.seq0, g.h, g.r0 + (warp - 4) * 16 + lane) * a.D;
+                at = shared_row(a, g.seq0, g.h, g.r0 + (warp - 4) * 16 + lane) * a.D;
             constexpr int CH = 16 * NDB;  // pieces of 8 dims per row
 #pragma unroll 4
             for (int e = lane; e < 16 * CH; e += 32) {
@@ -398,6 +430,8 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
             const int n = g.tile1 - g.tile0;
+            // tokens that the row sees, and that the sequence's first new token does
+            const int vis = g.len > 0 ? g.len - (a.K - 1 - (g.r0 + row) / a.group) : 0, least = g.len - (a.K - 1);
             float m = kNone;                      // the row's running maximum
             float2 l = make_float2(0.f, 0.f);     // the sum of this warpgroup's tokens
             for (int j = 0; j < n; ++j) {
@@ -408,6 +442,14 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                 tmem_ld32(ts, x);
                 tmem_ld32(ts + 32, x + 32);
                 tmem_wait_ld();
+                const int t0 = (g.tile0 + j) * TILE;
+                const bool tail = g.len > 0 && t0 + TILE > least;
+                if (tail) {
+                    const int upto = vis - (t0 + wg * 64);
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        if (i >= upto) x[i] = -INFINITY;
+                }
                 float top = x[0], top2 = x[1];
 #pragma unroll
                 for (int i = 2; i < 64; i += 4) {
@@ -458,6 +500,10 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                     }
                     tmem_st32(ts + c, w);
                 }
+                if (tail) {
+                    mend_v(j, n, t0);
+                    fence_async_smem();
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -469,19 +515,21 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                     s_phase ^= 1;
                 }
             }
+            sl0 += 2 * NDB * n;
             // ---- sums and outputs of the segment
             l_s[wg * ROWS + row] = l.x + l.y;
             wait(&pv_done[last], last_phase);
             tc_fence_after();
             softmax_sync();
             const float sum = l_s[row] + l_s[ROWS + row];
+            const bool odd = *odd_v != 0;
             const bool real = row < g.nr && live;
-            float *po = nullptr, *slot = prefix_slot(s, blockIdx.x);
+            float *po = nullptr, *slot = shared_slot(s, blockIdx.x);
             if (g.parts > 0) {
                 if (real) {
-                    const int64_t to = prefix_row(a, g.seq0, g.h, g.r0 + row);
-                    po = s.pre_o + to * a.D;
-                    if (wg == 0) s.pre_stat[to] = prefix_stat(m, sum, g.parts, row);
+                    const int64_t to = shared_row(a, g.seq0, g.h, g.r0 + row);
+                    po = (g.len > 0 ? a.part_o : s.pre_o) + to * a.D;
+                    if (wg == 0) (g.len > 0 ? a.part_stat : s.pre_stat)[to] = part_stat(m, sum, g.parts, row);
                 }
             } else if (real) {
                 po = slot + 2 * ROWS + row * a.D;
@@ -498,6 +546,20 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                 float o[32];
                 tmem_ld32(tq + L::T_O + c, o);
                 tmem_wait_ld();
+                if (odd) {
+                    const int upto = min(min(g.len, g.tile1 * TILE), vis);
+#pragma unroll 1
+                    for (int t = max(g.tile0 * TILE, least); t < upto; ++t) {
+                        const int page = a.table[(int64_t)g.leader * a.max_pages + t / a.page_size];
+                        if (page < 0 || page >= a.n_pages) continue;
+                        const bf16* src = static_cast<const bf16*>(a.v_cache) +
+                                          (((int64_t)page * a.H_kv + g.h) * a.page_size + t % a.page_size) * a.D + c;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i < a.D && !isfinite(to_f(src[i]))) o[i] += to_f(src[i]);
+                    }
+                    __syncwarp();
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     o_s[lane * 8 + (i ^ (lane & 7))] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
@@ -511,6 +573,7 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                 }
                 __syncwarp();
             }
+            if (st == 0) *odd_v = 0;
             tc_fence_before();
             softmax_sync();  // O and the sums are free
         }
@@ -524,7 +587,7 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             const int n = n0 > n1 ? n0 : n1;
             if (n > 0) mbar_wait(&full[st], (uint32_t)((n - 1) & 1), kWaitNs);
         }
-        atomicOr(&g_prefix_error, 1);
+        atomicOr(&g_shared_error, 1);
     }
     if (warp == 1) {
         tc_fence_after();
@@ -537,27 +600,27 @@ cudaError_t launch_ndb(const ShareArgs& s, int n_cta, int piece, cudaStream_t st
     using L = Layout<NDB>;
     CUtensorMap km, vm;
     if (!encode_cache(&km, s.a.k_cache, s.a, piece) || !encode_cache(&vm, s.a.v_cache, s.a, piece)) return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(attn_prefix_tc_kernel<NDB>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(attn_shared_tc_kernel<NDB>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_prefix_tc_kernel<NDB>, dim3((unsigned)n_cta), dim3(NT), L::SMEM, st, km, vm, s, piece);
+    return launch_pdl(attn_shared_tc_kernel<NDB>, dim3((unsigned)n_cta), dim3(NT), L::SMEM, st, km, vm, s, piece);
 }
 
 }  // namespace
 
-cudaError_t launch_prefix_tc(const ShareArgs& s, int n_cta, cudaStream_t st) {
+cudaError_t launch_shared_tc(const ShareArgs& s, int n_cta, cudaStream_t st) {
     const int piece = page_piece(s.a.page_size);
     return s.a.D <= 128 ? launch_ndb<1>(s, n_cta, piece, st) : launch_ndb<2>(s, n_cta, piece, st);
 }
 
-cudaError_t read_and_clear_prefix_error(cudaStream_t s, int* flags) {
+cudaError_t read_and_clear_shared_error(cudaStream_t s, int* flags) {
     int hf = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&hf, g_prefix_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&hf, g_shared_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return e;
     *flags = hf;
     if (hf != 0) {
         const int zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_prefix_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+        e = cudaMemcpyToSymbolAsync(g_shared_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
         if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     }
     return e;

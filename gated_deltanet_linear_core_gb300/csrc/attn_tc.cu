@@ -115,22 +115,6 @@ struct alignas(16) SegmentNote {
 };
 static_assert(sizeof(SegmentNote) == 32, "notes");
 
-// The same for a slot's position counter to reach `pos`.
-__device__ __forceinline__ bool loaded_or_abort(volatile int* filled, int pos, volatile int* abort_flag) {
-    if (*filled >= pos) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (*filled >= pos) return true;
-        if ((it & 31) == 0) {
-            if (*abort_flag) return false;
-            if (globaltimer_ns() - t0 > kWaitNs) {
-                *abort_flag = 1;
-                return false;
-            }
-        }
-    }
-}
-
 template <int NTHR>
 __device__ __forceinline__ void softmax_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(NTHR) : "memory");
@@ -173,20 +157,7 @@ template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const float* v) {
     if constexpr (N == 16) tmem_st16(taddr, v); else tmem_st32(taddr, v);
 }
-__device__ __forceinline__ bool finite_bf16x8(uint4 u) {
-    bool ok = true;
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ok = ok && (w[i] & 0x7f80u) != 0x7f80u && (w[i] & 0x7f800000u) != 0x7f800000u;
-    return ok;
-}
-__device__ __forceinline__ uint32_t zero_non_finite(uint32_t w) {
-    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
-    return w;
-}
-
-template <int N, int NDB, bool SHARED>
+template <int N, int NDB>
 __global__ void __launch_bounds__(Layout<N, NDB>::NT, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a,
                int piece) {
@@ -302,16 +273,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     if (warp == 0) {
         // ------------------------------------------------ K and V
         int n_cta = gridDim.x;
-        const Place place = find_place<SHARED>(a, TILE, blockIdx.x, n_cta);
+        const Place place = find_place(a, TILE, blockIdx.x, n_cta);
         const bool works = (int)blockIdx.x < n_cta;
-        Walk<SHARED> walk(place, works ? cta_begin(place.total, blockIdx.x, n_cta) : 0,
+        Walk<> walk(place, works ? cta_begin(place.total, blockIdx.x, n_cta) : 0,
                   works ? cta_begin(place.total, blockIdx.x + 1, n_cta) : 0);
         int sl0 = 0;  // slots before
         bool ok = true, more = true;
         while (ok && more) {
             more = walk.next(a, TILE, s);
-            if constexpr (SHARED)
-                if (more && s.tiles == 2) s.tiles = count_parts(a, place, walk, s, TILE, blockIdx.x, n_cta);
             const int e = sg % L::SEGS;
             if (sg >= L::SEGS)
                 ok = __all_sync(0xffffffffu, wait_or_abort(&seg_empty[e], (uint32_t)((sg / L::SEGS - 1) & 1), abort_flag));
@@ -335,8 +304,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 zk = zn;
             }
             sl0 += 2 * NDB * n;
-            if constexpr (!SHARED)
-                if (sg == 1 && lane == 0) write_join_task(a, place, walk, more ? &s : nullptr, blockIdx.x, n_cta);
+            if (sg == 1 && lane == 0) write_join_task(a, place, walk, more ? &s : nullptr, blockIdx.x, n_cta);
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMAs (lane 0)
@@ -495,7 +463,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 if (!more) return false;
                 if (lane == 0) took_note();
                 if (s.len > 0) return true;
-                if (SHARED) continue;  // the merge's
                 const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
                 for (int e = st; e < nr * a.D; e += NSOFT) {
                     const int r = e / a.D, d = e - r * a.D;
@@ -508,7 +475,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         // Sums and outputs of a segment whose last tile is handed to the MMA warp.
         auto finish_segment = [&](const Segment& s, float (&l)[CPT]) {
             const int r0 = s.rb * a.rb_rows, nr = block_rows(a, s.rb);
-            const bool whole = !SHARED && s.tile1 - s.tile0 == s.tiles;
+            const bool whole = s.tile1 - s.tile0 == s.tiles;
             // sums over the tokens: the lanes, then the warps
             join_lanes<CPT>(l, lane, [](float x, float y) { return x + y; });
             // the output loop below has this many rounds per 128 dims; the gate's values are loaded two rounds ahead
@@ -533,7 +500,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             if constexpr (CPT == 64) *reinterpret_cast<float2*>(scr_w + 2 * lane) = make_float2(l[0], l[1]);
             else if (CPT == 32 || (lane & 1) == 0) scr_w[CPT == 32 ? lane : lane >> 1] = l[0];
             softmax_sync<NSOFT>();
-            float* slot = slot_ptr(a, SHARED ? blockIdx.x : part_slot(s));
+            float* slot = slot_ptr(a, part_slot(s));
             for (int c = st; c < nr; c += NSOFT) {
                 const float sum = (sum_s[c] + sum_s[N + c]) + (sum_s[2 * N + c] + sum_s[3 * N + c]);
                 const float m = -n_s[c];
@@ -542,9 +509,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     if (whole) {
                         if (a.lse != nullptr)
                             a.lse[out_row(c)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
-                    } else if (SHARED && s.tiles > 0) {
-                        a.part_stat[out_row(c)] = make_float4(sum == 0.f ? -INFINITY : m, sum, __int_as_float(blockIdx.x),
-                                                              __int_as_float(s.tiles));
                     } else {
                         slot[c] = sum == 0.f ? -INFINITY : m;
                         slot[a.rb_rows + c] = sum;
@@ -614,7 +578,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         }
                         store16<bf16>(static_cast<bf16*>(a.out) + at, y);
                     } else {
-                        float* p = SHARED && s.tiles > 0 ? a.part_o + out_row(r) * a.D + d : slot + a.stat_floats + r * a.D + d;
+                        float* p = slot + a.stat_floats + r * a.D + d;
                         *reinterpret_cast<float4*>(p) = x0;
                         *reinterpret_cast<float4*>(p + 4) = x1;
                     }
@@ -792,22 +756,21 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     }
 }
 
-template <int N, int NDB, bool SHARED>
+template <int N, int NDB>
 cudaError_t launch_tc(const AttnArgs& a, int n_cta, int piece, cudaStream_t s) {
     using L = Layout<N, NDB>;
     CUtensorMap km, vm;
     if (!encode_cache(&km, a.k_cache, a, piece) || !encode_cache(&vm, a.v_cache, a, piece)) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<N, NDB, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<N, NDB>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_tc_kernel<N, NDB, SHARED>, dim3((unsigned)n_cta), dim3(L::NT), L::SMEM, s, km, vm, a, piece);
+    return launch_pdl(attn_tc_kernel<N, NDB>, dim3((unsigned)n_cta), dim3(L::NT), L::SMEM, s, km, vm, a, piece);
 }
 
-template <int NDB, bool SHARED>
+template <int NDB>
 cudaError_t launch_rows(const AttnArgs& a, int n_cta, int piece, cudaStream_t s) {
-    return a.rb_rows <= 16 ? launch_tc<16, NDB, SHARED>(a, n_cta, piece, s)
-         : a.rb_rows <= 32 ? launch_tc<32, NDB, SHARED>(a, n_cta, piece, s)
-         : a.rb_rows <= 64 ? launch_tc<64, NDB, SHARED>(a, n_cta, piece, s)
-                           : launch_tc<128, NDB, SHARED>(a, n_cta, piece, s);
+    return a.rb_rows <= 16 ? launch_tc<16, NDB>(a, n_cta, piece, s)
+         : a.rb_rows <= 32 ? launch_tc<32, NDB>(a, n_cta, piece, s)
+         : a.rb_rows <= 64 ? launch_tc<64, NDB>(a, n_cta, piece, s) : launch_tc<128, NDB>(a, n_cta, piece, s);
 }
 
 }  // namespace
@@ -820,8 +783,7 @@ bool attn_tc_pages(int page_size) { return page_piece(page_size) >= TILE / 32; }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, int n_cta, cudaStream_t s) {
     const int piece = page_piece(a.page_size);
-    if (a.skip != nullptr) return a.D <= 128 ? launch_rows<1, true>(a, n_cta, piece, s) : launch_rows<2, true>(a, n_cta, piece, s);
-    const cudaError_t e = a.D <= 128 ? launch_rows<1, false>(a, n_cta, piece, s) : launch_rows<2, false>(a, n_cta, piece, s);
+    const cudaError_t e = a.D <= 128 ? launch_rows<1>(a, n_cta, piece, s) : launch_rows<2>(a, n_cta, piece, s);
     return e != cudaSuccess ? e : launch_attn_join(a, n_cta, GDN_BF16, s);
 }
 

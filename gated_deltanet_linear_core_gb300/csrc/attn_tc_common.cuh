@@ -1,4 +1,4 @@
-// What the tensor-core attention kernels (attn_tc.cu, attn_prefix_tc.cu) share: cache
+// What the tensor-core attention kernels (attn_tc.cu, attn_shared_tc.cu) share: cache
 // tiles of 128 tokens loaded by TMA in page pieces, bounded waits of their roles,
 // MMAs with 128-byte-swizzled operands.
 #pragma once
@@ -35,6 +35,22 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
     }
 }
 
+// The same for a slot's position counter to reach `pos`.
+__device__ __forceinline__ bool loaded_or_abort(volatile int* filled, int pos, volatile int* abort_flag) {
+    if (*filled >= pos) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (*filled >= pos) return true;
+        if ((it & 31) == 0) {
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 > kWaitNs) {
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
+
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -42,6 +58,19 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
+__device__ __forceinline__ bool finite_bf16x8(uint4 u) {
+    bool ok = true;
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ok = ok && (w[i] & 0x7f80u) != 0x7f80u && (w[i] & 0x7f800000u) != 0x7f800000u;
+    return ok;
+}
+__device__ __forceinline__ uint32_t zero_non_finite(uint32_t w) {
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+    return w;
+}
+
 // Operand descriptors by their low words (address and lbo in units of 16 bytes); the high word is the same for
 // all (sbo 1024, version, 128-byte swizzle: sdesc_sw128).
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }

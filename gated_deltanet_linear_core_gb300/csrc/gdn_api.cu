@@ -124,7 +124,7 @@ gdn_status_t gdn_sync_status(void* stream) {
     cudaError_t e = gdn::read_and_clear_device_error((cudaStream_t)stream, &flags);
     if (e == cudaSuccess) e = gdn::read_and_clear_conv_error((cudaStream_t)stream, &cflags);
     if (e == cudaSuccess) e = gdn::read_and_clear_attn_error((cudaStream_t)stream, &aflags);
-    if (e == cudaSuccess) e = gdn::read_and_clear_prefix_error((cudaStream_t)stream, &pflags);
+    if (e == cudaSuccess) e = gdn::read_and_clear_shared_error((cudaStream_t)stream, &pflags);
     if (e != cudaSuccess) return cuda_status(e);
     return ((flags | cflags | aflags | pflags) & 1) ? GDN_ERR_TIMEOUT : GDN_OK;
 }

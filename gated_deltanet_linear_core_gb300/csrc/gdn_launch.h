@@ -172,9 +172,9 @@ struct AttnArgs {
     int setup;             // units that starting an item counts as, beside its tiles
     int stop_at;           // self-test: the MMAs stop at a CTA's tile of this number (-1: never)
     // behind shared prefixes (gdn_attn_decode_shared); null otherwise
-    const int32_t* skip;   // [B] tokens that the pass over the prefixes has taken, a multiple of kShareStep
+    const int32_t* skip;   // [B] tokens of the shared prefix, a multiple of kShareStep
     float* part_o;         // [B, K, H_q, D] the items' first parts: unnormalised outputs,
-    float4* part_stat;     // [B, K, H_q] maximum, sum, first CTA, number of CTAs
+    float4* part_stat;     // [B, K, H_q] maximum, sum, first CTA | CTAs << 16, row in its block
 };
 constexpr int kAttnMaxK = 16;
 constexpr int kAttnMaxCtas = 152;  // CTAs of a call, at most: one per SM
@@ -191,35 +191,35 @@ cudaError_t read_and_clear_attn_error(cudaStream_t s, int* flags);
 bool attn_tc_pages(int page_size);  // page sizes that its loads take
 cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaStream_t s);
 
-// Attention behind shared prefixes (gdn_attn_decode_shared): a pass over the prefixes, one over what
-// each sequence has of its own (the kernels above), and a merge of both (attn_shared.cuh).
+// Attention behind shared prefixes (gdn_attn_decode_shared; attn_shared.cuh).
 constexpr int kPrefixFfmaRows = 64;
 constexpr int kShareStep = 128;  // a prefix is shared down to a multiple of this many tokens
-struct alignas(16) PrefixGroup {
-    int64_t unit0;    // first unit of the group's items
-    int seq0, seqs;   // its sequences
-    int share;        // tokens that are shared in earnest
-    int leader;       // the sequence whose pages are read
-    int blocks;       // row blocks
-    int pad;
+// Tokens that one or several sequences attend to through one page table.
+struct alignas(16) ShareRecord {
+    int64_t unit0;      // first unit of its items
+    int seq0, seqs;     // the sequences
+    int tile0, tiles;   // the tokens, in tiles
+    int leader;         // the sequence whose pages are read
+    int blocks;         // row blocks
 };
 struct ShareArgs {
-    AttnArgs a;                        // the sequences' own tokens
+    AttnArgs a;                        // (its work division holds for what the sequences have of their own on CUDA cores)
     const int32_t *prefix, *cu;        // [G] tokens; [G + 1] sequences or null: one group
     int G;
-    int rows_per_block, tile, setup;   // of the pass over the prefixes: rows and tokens per tile, units of an item's start
-    PrefixGroup* groups;               // [G + 1], the last one's unit0 all units
+    int records;                       // G prefixes, on tensor cores then B sequences' own tokens
+    int rows_per_block, tile, setup;   // rows and tokens per tile, units of an item's start
+    ShareRecord* rec;                  // [records + 1], the last one's unit0 all units
     float* pre_o;                      // [B, K, H_q, D], [B, K, H_q]: the prefix items' first parts, as a.part_o and a.part_stat
     float4* pre_stat;
-    float* pre_slots;                  // per CTA: a part that starts inside an item
-    int64_t pre_slot_floats;
+    float* slots;                      // per CTA: a part that starts inside an item
+    int64_t slot_floats;
 };
 // Fills the derived fields from the sizes (and with a workspace the pointers into it); returns the workspace bytes.
 size_t attn_share_plan(ShareArgs& s, gdn_dtype_t dt, void* ws);
 cudaError_t launch_attn_shared(const ShareArgs& s, gdn_dtype_t dt, cudaStream_t st);
-cudaError_t launch_prefix_tc(const ShareArgs& s, int n_cta, cudaStream_t st);
+cudaError_t launch_shared_tc(const ShareArgs& s, int n_cta, cudaStream_t st);
 cudaError_t launch_prefix_ffma(const ShareArgs& s, int n_cta, gdn_dtype_t dt, cudaStream_t st);
-cudaError_t read_and_clear_prefix_error(cudaStream_t s, int* flags);
+cudaError_t read_and_clear_shared_error(cudaStream_t s, int* flags);
 
 // New keys and values into their pages (gdn_kv_append).
 struct KvAppendArgs {
