@@ -9,124 +9,132 @@ namespace {
 using namespace attn;
 
 constexpr int PT = 1024;  // threads of the plan
+static_assert(PT == 32 * 32, "block_scan");
 constexpr int MT = 256;   // threads of a merge block that takes several rows
 
-// What every group shares in earnest, by one block: a warp (or, where there are few groups, several)
-// looks at a group's lengths.
+// Sum of x over the block's threads before this one, and `total` over all.
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t& total) {
+    __shared__ int64_t sums_s[PT / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) sums_s[warp] = inc;
+    __syncthreads();
+    int64_t w = sums_s[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += v;
+    }
+    total = __shfl_sync(0xffffffffu, w, 31);
+    const int64_t before = __shfl_sync(0xffffffffu, w, (warp - 1) & 31);
+    __syncthreads();
+    return inc - x + (warp > 0 ? before : 0);
+}
+
+// What every group shares in earnest, and the records, by one block.  Groups' least lengths, first
+// sequences and counts are gathered in shared memory, of many groups in the workspace.
+constexpr int kPlanGroups = 1024;  // groups in shared memory
 __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
-    __shared__ int least_s[32], first_s[32], count_s[32], share_s[32];
-    __shared__ int64_t sums_s[32], before_s;
+    __shared__ int first_s[kPlanGroups + 1], least_s[kPlanGroups], leader_s[kPlanGroups], count_s[kPlanGroups];
     const AttnArgs& a = s.a;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int32_t* skip = const_cast<int32_t*>(a.skip);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const bool few = s.G <= kPlanGroups;
+    int* least = few ? least_s : s.gather;
+    int* leader = few ? leader_s : s.gather + s.G;
+    int* count = few ? count_s : s.gather + 2 * (int64_t)s.G;
+    const int B = a.B;
     pdl_wait();
     pdl_trigger();
-    for (int b = tid; b < a.B; b += PT) skip[b] = 0;  // of sequences in no group
-    __syncthreads();
-    const int per = s.G >= 32 ? 1 : 32 / s.G, at_once = 32 / per;  // warps per group, groups at once
-    int64_t before = 0;  // units of the groups before (warp 0)
-    for (int g0 = 0; g0 < s.G; g0 += at_once) {
-        const int mine = warp / per, g = g0 + mine;
-        const bool works = mine < at_once && g < s.G;
-        int lo = 0, hi = 0, least = INT32_MAX, first = INT32_MAX, count = 0;
-        if (works) {
-            group_bounds(s, g, lo, hi);
-#pragma unroll 4
-            for (int b = lo + (warp - mine * per) * 32 + lane; b < hi; b += per * 32) {
-                const int n = clamped_len(a, b);
-                if (n > 0) {  // sequences without a token see nothing and do not count
-                    least = min(least, n);
-                    first = min(first, b);
-                    ++count;
-                }
-            }
+    int len0 = tid < B ? clamped_len(a, tid) : 0;  // of the first round's sequence
+    const int prefix0 = tid < s.G ? s.prefix[tid] : 0;
+    for (int g = tid; g <= s.G; g += PT) {
+        if (g < s.G) {
+            least[g] = leader[g] = INT32_MAX;
+            count[g] = 0;
         }
-        least = __reduce_min_sync(0xffffffffu, least);
-        first = __reduce_min_sync(0xffffffffu, first);
-        count = __reduce_add_sync(0xffffffffu, count);
-        if (lane == 0) {
-            least_s[warp] = least;
-            first_s[warp] = first;
-            count_s[warp] = count;
-        }
-        __syncthreads();
-        if (warp == 0) {  // lane i: group g0 + i
-            const int gi = g0 + lane;
-            int64_t units = 0;
-            ShareRecord grp = {};
-            if (lane < at_once && gi < s.G) {
-                least = first = INT32_MAX;
-                count = 0;
-                for (int w = lane * per; w < (lane + 1) * per; ++w) {
-                    least = min(least, least_s[w]);
-                    first = min(first, first_s[w]);
-                    count += count_s[w];
-                }
-                // less than the first new token of any sequence sees
-                int share = count > 1 ? min(s.prefix[gi], least - a.K) : 0;
-                share = share > 0 ? share / kShareStep * kShareStep : 0;
-                int seq1;
-                group_bounds(s, gi, grp.seq0, seq1);
-                grp.seqs = seq1 - grp.seq0;
-                grp.blocks = (int)(((int64_t)grp.seqs * a.rows + s.rows_per_block - 1) / s.rows_per_block);
-                share_s[lane] = share;
-                grp.tiles = share / s.tile;
-                grp.leader = first == INT32_MAX ? 0 : first;
-                if (share > 0) units = (int64_t)grp.blocks * a.H_kv * (s.setup + grp.tiles);
-            }
-            int64_t inc = units;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += v;
-            }
-            grp.unit0 = before + inc - units;
-            if (lane < at_once && gi < s.G) s.rec[gi] = grp;
-            before += __shfl_sync(0xffffffffu, inc, 31);
-        }
-        __syncthreads();
-        if (works) {
-            const int share = share_s[mine];
-            if (share > 0)
-                for (int b = lo + (warp - mine * per) * 32 + lane; b < hi; b += per * 32)
-                    if (clamped_len(a, b) > 0) skip[b] = share;
-        }
-        __syncthreads();
+        if (few) first_s[g] = s.cu != nullptr ? min(max(s.cu[g], 0), B) : g * B;
     }
-    // what the sequences have of their own
-    if (tid == 0) before_s = before;
     __syncthreads();
-    const int blocks = (a.rows + s.rows_per_block - 1) / s.rows_per_block;
-    for (int b0 = 0; s.G + b0 < s.records; b0 += PT) {
-        const int b = b0 + tid;
-        ShareRecord own = {};
+    auto first = [&](int g) -> int { return few ? first_s[g] : s.cu != nullptr ? min(max(s.cu[g], 0), B) : g * B; };
+    auto group_of = [&](int b) -> int {  // -1: none
+        int lo = 0, hi = s.G - 1;        // the last group that starts at or before the sequence
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (first(mid) <= b) lo = mid; else hi = mid - 1;
+        }
+        return first(lo) <= b && b < first(lo + 1) ? lo : -1;
+    };
+    int group0 = -1;
+    for (int b0 = 0; b0 < B; b0 += PT) {
+        const int b = b0 + tid, n = b0 == 0 ? len0 : b < B ? clamped_len(a, b) : 0;
+        const int g = b < B ? group_of(b) : -1;
+        if (b0 == 0) group0 = g;
+        // sequences without a token see nothing and do not count
+        const bool counts = g >= 0 && n > 0;
+        const int g1 = __shfl_sync(0xffffffffu, g, 0);
+        if (__all_sync(0xffffffffu, !counts || g == g1)) {  // a warp's sequences are mostly of one group
+            const int n1 = __reduce_min_sync(0xffffffffu, counts ? n : INT32_MAX);
+            const int b1 = __reduce_min_sync(0xffffffffu, counts ? b : INT32_MAX);
+            const int c1 = __popc(__ballot_sync(0xffffffffu, counts));
+            if (lane == 0 && c1 > 0) {
+                atomicMin(&least[g1], n1);
+                atomicMin(&leader[g1], b1);
+                atomicAdd(&count[g1], c1);
+            }
+        } else if (counts) {
+            atomicMin(&least[g], n);
+            atomicMin(&leader[g], b);
+            atomicAdd(&count[g], 1);
+        }
+    }
+    __syncthreads();
+    int64_t before = 0, total;  // units of the records before
+    for (int g0 = 0; g0 < s.G; g0 += PT) {
+        const int g = g0 + tid;
+        ShareRecord rec = {};
         int64_t units = 0;
-        if (b < a.B) {
-            const int n = clamped_len(a, b);
-            own.seq0 = own.leader = b;
-            own.seqs = 1;
-            own.blocks = blocks;
-            own.tile0 = skip[b] / s.tile;
-            own.tiles = n > 0 ? (n - 1) / s.tile + 1 - own.tile0 : 0;
-            if (n > 0) units = (int64_t)blocks * a.H_kv * (s.setup + own.tiles);
+        if (g < s.G) {
+            rec.seq0 = first(g);
+            rec.seqs = max(first(g + 1) - rec.seq0, 0);
+            rec.blocks = (int)(((int64_t)rec.seqs * a.rows + s.rows_per_block - 1) / s.rows_per_block);
+            // less than the first new token of any sequence sees
+            int share = count[g] > 1 ? min(g0 == 0 ? prefix0 : s.prefix[g], least[g] - a.K) : 0;
+            share = share > 0 ? share / kShareStep * kShareStep : 0;
+            rec.tiles = share / s.tile;
+            rec.leader = count[g] > 0 ? leader[g] : 0;
+            if (share > 0) units = (int64_t)rec.blocks * a.H_kv * (s.setup + rec.tiles);
+            least[g] = share;  // from here on
         }
-        int64_t inc = units;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        if (lane == 31) sums_s[warp] = inc;
-        __syncthreads();
-        int64_t start = before_s;
-        for (int w = 0; w < warp; ++w) start += sums_s[w];
-        own.unit0 = start + inc - units;
-        if (b < a.B) s.rec[s.G + b] = own;
-        __syncthreads();
-        if (tid == PT - 1) before_s = start + inc;
-        __syncthreads();
+        rec.unit0 = before + block_scan(units, total);
+        before += total;
+        if (g < s.G) s.rec[g] = rec;
     }
-    if (tid == 0) s.rec[s.records].unit0 = before_s;
+    int32_t* skip = const_cast<int32_t*>(a.skip);
+    const int blocks = (a.rows + s.rows_per_block - 1) / s.rows_per_block;
+    for (int b0 = 0; b0 < B; b0 += PT) {
+        const int b = b0 + tid;
+        const int n = b0 == 0 ? len0 : b < B ? clamped_len(a, b) : 0, g = b0 == 0 ? group0 : b < B ? group_of(b) : -1;
+        const int share = g >= 0 && n > 0 ? least[g] : 0;
+        if (b < B) skip[b] = share;
+        if (s.records == s.G) continue;
+        ShareRecord rec = {};
+        int64_t units = 0;
+        rec.seq0 = rec.leader = b;
+        rec.seqs = 1;
+        rec.blocks = blocks;
+        rec.tile0 = share / s.tile;
+        rec.tiles = n > 0 ? (n - 1) / s.tile + 1 - rec.tile0 : 0;
+        if (n > 0) units = (int64_t)blocks * a.H_kv * (s.setup + rec.tiles);
+        rec.unit0 = before + block_scan(units, total);
+        before += total;
+        if (b < B) s.rec[s.G + b] = rec;
+    }
+    if (tid == 0) s.rec[s.records].unit0 = before;
 }
 
 struct Running {
@@ -255,7 +263,9 @@ cudaError_t launch_merge(const ShareArgs& s, int n_cta, cudaStream_t st) {
     const int64_t parts = 1 + (n_cta + items - 1) / items;
     int groups = 1;
     if (parts > 8) {
-        while (groups * 4 < parts && groups * 2 * ng <= 1024) groups *= 2;
+        // more groups where there are few rows (us with 1, 2, 4, 8, 16: 1024 rows of 20 parts 67.9, 65.0, 65.6, 70.0, 79.2;
+        // 128 rows of 77 parts 124, 110, 103, 99, 98)
+        while (groups * 4 < parts && groups * 2 * ng <= 1024 && groups * 2 * ng * rows <= n_cta * 1024) groups *= 2;
         const size_t smem = groups * (ng * sizeof(float4) + sizeof(float2));
         return launch_pdl(attn_merge_kernel<T, true>, dim3((unsigned)rows), dim3((unsigned)ng, (unsigned)groups), smem, st, s);
     }
@@ -275,7 +285,10 @@ size_t attn_share_plan(ShareArgs& s, gdn_dtype_t dt, void* ws) {
     s.records = s.G + (tc ? a.B : 0);
     s.rows_per_block = tc ? 128 : kPrefixFfmaRows;
     s.tile = tc ? 128 : 64;
-    s.setup = 1;
+    // What starting an item costs, in tiles (of half the MMAs up to head dim 128): its first scores and weights and its
+    // outputs overlap with nothing.  us with 1, 2, 3, 4, 6 and 8: 64 sequences behind 32768 tokens (head dim 256) 85, 75,
+    // 70, 71, 74, 77; 32 with 16 new tokens behind 16384 (head dim 128) 279, 218, 181, 160, 158, 163.
+    s.setup = !tc ? 1 : a.D <= 128 ? 5 : 3;
     s.slot_floats = 2 * s.rows_per_block + (int64_t)s.rows_per_block * a.D;
     const size_t rows = (size_t)a.B * a.K * a.H_q;
     char* base = reinterpret_cast<char*>(up(reinterpret_cast<size_t>(ws)));
@@ -292,6 +305,7 @@ size_t attn_share_plan(ShareArgs& s, gdn_dtype_t dt, void* ws) {
     a.part_stat = reinterpret_cast<float4*>(take(rows * sizeof(float4)));
     s.pre_stat = reinterpret_cast<float4*>(take(rows * sizeof(float4)));
     s.rec = reinterpret_cast<ShareRecord*>(take(((size_t)s.records + 1) * sizeof(ShareRecord)));
+    s.gather = reinterpret_cast<int*>(take(s.G > kPlanGroups ? 3 * (size_t)s.G * sizeof(int) : 0));
     a.skip = reinterpret_cast<int32_t*>(take((size_t)a.B * sizeof(int32_t)));
     return at + 256;
 }

@@ -21,15 +21,6 @@
 namespace gdn {
 namespace attn {
 
-__device__ __forceinline__ void group_bounds(const ShareArgs& s, int g, int& lo, int& hi) {
-    lo = 0;
-    hi = s.a.B;
-    if (s.cu != nullptr) {
-        lo = min(max(s.cu[g], 0), s.a.B);
-        hi = min(max(s.cu[g + 1], lo), s.a.B);
-    }
-}
-
 // A part of an item, worked on by one CTA.
 struct alignas(16) SharedSegment {
     int tile0, tile1;  // its tiles; 0, 0: the CTA's range has ended

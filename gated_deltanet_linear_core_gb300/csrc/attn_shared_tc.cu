@@ -7,7 +7,7 @@
 //   O [128 rows x D]         += P V      (P in tensor memory, V tile in shared memory, MN-major)
 // A softmax thread owns half a row of a tile (64 tokens), so maxima and sums need no exchange
 // between lanes, and P goes back into the columns of S that it came from.  A row's running maximum is moved
-// only when a score exceeds it by 2^8, which the two warps that share rows vote on; O is
+// only when scores far above it make the weights' sum large, which the two warps that share rows vote on; O is
 // rescaled then.  P is held as two bf16 (the value
 // cut to 8 bits and the rounded rest), as in attn_tc.cu: one alone would add an error of the size of the output's
 // own rounding.  Two buffers of S: while P V of a tile runs, the scores of the next are
@@ -33,6 +33,9 @@ using namespace attn;
 constexpr int ROWS = 128;
 constexpr int NT = 384;
 constexpr int NSOFT = 256;
+// Half a tile's weights of a row add up to more than this where its running maximum is to be moved.  (The sum is there
+// anyway; looking for the largest score in each tile took a fifth of the arithmetic.)
+constexpr float kLarge = 4096.0f;
 
 template <int NDB>
 struct Layout {
@@ -430,6 +433,7 @@ attn_shared_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
             const int n = g.tile1 - g.tile0;
+            const bool works = quad * 32 < g.nr;  // else none of the warp's rows are real: its P and O may be anything
             // tokens that the row sees, and that the sequence's first new token does
             const int vis = g.len > 0 ? g.len - (a.K - 1 - (g.r0 + row) / a.group) : 0, least = g.len - (a.K - 1);
             float m = kNone;                      // the row's running maximum
@@ -438,73 +442,79 @@ attn_shared_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                 const uint32_t ts = tq + L::T_S + sb * TILE + wg * 64;
                 wait(&s_full[sb], s_phase);
                 tc_fence_after();
-                float x[64];
-                tmem_ld32(ts, x);
-                tmem_ld32(ts + 32, x + 32);
-                tmem_wait_ld();
                 const int t0 = (g.tile0 + j) * TILE;
                 const bool tail = g.len > 0 && t0 + TILE > least;
-                if (tail) {
-                    const int upto = vis - (t0 + wg * 64);
+                if (works) {
+                    float w[64];  // of every 32 tokens 16 columns of upper parts, 16 of rests
+                    float2 sum;
+                    for (bool fits = j > 0;;) {
+                        float x[64];
+                        tmem_ld32(ts, x);
+                        tmem_ld32(ts + 32, x + 32);
+                        tmem_wait_ld();
+                        if (tail) {
+                            const int upto = vis - (t0 + wg * 64);
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (i >= upto) x[i] = -INFINITY;
-                }
-                float top = x[0], top2 = x[1];
-#pragma unroll
-                for (int i = 2; i < 64; i += 4) {
-                    top = fmaxf(top, fmaxf(x[i], x[i + 1]));
-                    if (i + 3 < 64) top2 = fmaxf(top2, fmaxf(x[i + 2], x[i + 3]));
-                }
-                top = fmaxf(top, top2) * a.scale_log2;
-                if (pair_any(quad, j == 0 || top > m + kSlack)) {
-                    // ---- new maxima; sums and outputs so far are scaled to them
-                    t_s[wg * ROWS + row] = top;
-                    pair_sync(quad);
-                    const float t = fmaxf(top, t_s[(wg ^ 1) * ROWS + row]);
-                    const float m1 = t > m + kSlack ? t : m;  // rows do not move with one another
-                    const float f = ex2_approx(m - m1);
-                    m = m1;
-                    l.x *= f;
-                    l.y *= f;
-                    if (j > 0) {
-                        wait(&pv_done[last], last_phase);
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c = wg * 64 * NDB; c < (wg + 1) * 64 * NDB; c += 32) {
-                            float o[32];
-                            tmem_ld32(tq + L::T_O + c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] *= f;
-                            tmem_st32(tq + L::T_O + c, o);
+                            for (int i = 0; i < 64; ++i)
+                                if (i >= upto) x[i] = -INFINITY;
                         }
-                    }
-                }
+                        const bool sure = !fits;
+                        if (!fits) {
+                            // ---- new maxima; sums and outputs so far are scaled to them
+                            float top = x[0];
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    float w[32];  // 16 columns of upper parts, 16 of rests
+                            for (int i = 1; i < 64; ++i) top = fmaxf(top, x[i]);
+                            t_s[wg * ROWS + row] = top;
+                            pair_sync(quad);
+                            const float t = fmaxf(top, t_s[(wg ^ 1) * ROWS + row]) * a.scale_log2;
+                            const float m1 = t > m + kSlack ? t : m;  // rows do not move with one another
+                            const float f = ex2_approx(m - m1);
+                            m = m1;
+                            l.x *= f;
+                            l.y *= f;
+                            if (j > 0) {
+                                wait(&pv_done[last], last_phase);
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int c = wg * 64 * NDB; c < (wg + 1) * 64 * NDB; c += 32) {
+                                    float o[32];
+                                    tmem_ld32(tq + L::T_O + c, o);
+                                    tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 y = __ffma2_rn(make_float2(x[c + 2 * i], x[c + 2 * i + 1]),
-                                                    make_float2(a.scale_log2, a.scale_log2), make_float2(-m, -m));
-                        const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-                        l = __fadd2_rn(l, p);
-                        const uint32_t w0 = __float_as_uint(p.x), w1 = __float_as_uint(p.y);
-                        w[i] = __uint_as_float(__byte_perm(w0, w1, 0x7632));  // the upper halves: cut, not rounded
-                        // the rest, and p's last bit: a rest of 0 would turn an infinite value into NaN
-                        const float2 rest = __ffma2_rn(p, make_float2(1.0f + 0x1p-23f, 1.0f + 0x1p-23f),
-                                                       make_float2(__uint_as_float((w0 & 0xffff0000u) | 0x80000000u),
-                                                                   __uint_as_float((w1 & 0xffff0000u) | 0x80000000u)));
-                        w[16 + i] = __uint_as_float(pack_bf16x2(rest.x, rest.y));
+                                    for (int i = 0; i < 32; ++i) o[i] *= f;
+                                    tmem_st32(tq + L::T_O + c, o);
+                                }
+                            }
+                            fits = true;
+                        }
+                        sum = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float2 y = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]),
+                                                        make_float2(a.scale_log2, a.scale_log2), make_float2(-m, -m));
+                            const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                            sum = __fadd2_rn(sum, p);
+                            const uint32_t w0 = __float_as_uint(p.x), w1 = __float_as_uint(p.y);
+                            // the upper halves: cut, not rounded
+                            w[(i & 16) * 2 + (i & 15)] = __uint_as_float(__byte_perm(w0, w1, 0x7632));
+                            // the rest, and p's last bit: a rest of 0 would turn an infinite value into NaN
+                            const float2 rest = __ffma2_rn(p, make_float2(1.0f + 0x1p-23f, 1.0f + 0x1p-23f),
+                                                           make_float2(__uint_as_float((w0 & 0xffff0000u) | 0x80000000u),
+                                                                       __uint_as_float((w1 & 0xffff0000u) | 0x80000000u)));
+                            w[(i & 16) * 2 + 16 + (i & 15)] = __uint_as_float(pack_bf16x2(rest.x, rest.y));
+                        }
+                        if (sure || !pair_any(quad, sum.x + sum.y > kLarge)) break;
+                        fits = false;
                     }
-                    tmem_st32(ts + c, w);
+                    l = __fadd2_rn(l, sum);
+                    tmem_st32(ts, w);
+                    tmem_st32(ts + 32, w + 32);
+                    tmem_wait_st();
                 }
                 if (tail) {
                     mend_v(j, n, t0);
                     fence_async_smem();
                 }
-                tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[sb]);
@@ -542,7 +552,7 @@ attn_shared_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             // row touches 32 lines at each store: 13 us a segment of head dim 256)
             float4* o_s = reinterpret_cast<float4*>(sm + L::O_Q + (warp - 4) * 4096);
 #pragma unroll 1
-            for (int c = wg * 64 * NDB; c < (wg + 1) * 64 * NDB && c < a.D; c += 32) {
+            for (int c = wg * 64 * NDB; works && c < (wg + 1) * 64 * NDB && c < a.D; c += 32) {
                 float o[32];
                 tmem_ld32(tq + L::T_O + c, o);
                 tmem_wait_ld();

@@ -208,6 +208,7 @@ struct ShareArgs {
     int G;
     int records;                       // G prefixes, on tensor cores then B sequences' own tokens
     int rows_per_block, tile, setup;   // rows and tokens per tile, units of an item's start
+    int* gather;                       // [3 G] scratch of the plan where there are many groups
     ShareRecord* rec;                  // [records + 1], the last one's unit0 all units
     float* pre_o;                      // [B, K, H_q, D], [B, K, H_q]: the prefix items' first parts, as a.part_o and a.part_stat
     float4* pre_stat;

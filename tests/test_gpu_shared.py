@@ -333,3 +333,15 @@ def test_serving_samples_of_one_prompt():
         o, e = gdn.gdn_attn_decode(q, kc, vc, table, lens, gate=x["gate"], return_lse=True)
         # each is off by its own roundings: a step of bf16 in all
         assert bool(((out.double() - o.double()).abs() <= 2.0 ** -7 * o.double().abs() + 2.0 ** -13).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_more_sequences_and_groups_than_the_plan_holds_at_once(dtype):
+    """1100 groups of one to three sequences, 2200 sequences, some of them empty; then all in one group."""
+    g = torch.Generator().manual_seed(12)
+    groups = [(int(torch.randint(0, 300, (1,), generator=g)), [int(n) for n in torch.randint(-1, 20, (1 + i % 3,), generator=g)])
+              for i in range(1100)]
+    x = shared_inputs(groups, 1, 2, 1, 16, 16, dtype, 13)
+    check(x)
+    x = shared_inputs([(260, [1 + i % 7 if i % 11 else -1 for i in range(2100)])], 1, 2, 1, 16, 16, dtype, 14)
+    check(x)
