@@ -21,7 +21,7 @@ namespace gdn {
 namespace {
 
 constexpr int NT = 256;
-constexpr int kMaxTB = 32;
+constexpr int kMaxTB = 16;
 
 template <int BYTES> struct RawOf;
 template <> struct RawOf<16> { using type = uint4; };
@@ -68,9 +68,9 @@ __device__ __forceinline__ void narrow(const float (&x)[V], Vec<E, V>& v) {
 __device__ __forceinline__ bool find_token(const RopeArgs& a, int64_t t, int& b, int64_t& pos) {
     int64_t end;
     if (a.cu == nullptr) {
-        const int64_t per = a.T / a.B;
-        b = (int)(t / per);
-        end = (b + 1) * per;
+        const uint32_t per = (uint32_t)a.T / (uint32_t)a.B;  // T < 2^31
+        b = (int)((uint32_t)t / per);
+        end = (int64_t)(b + 1) * per;
     } else {
         int64_t start;
         b = seq_of_token(a.cu, a.B, t);
@@ -82,10 +82,12 @@ __device__ __forceinline__ bool find_token(const RopeArgs& a, int64_t t, int& b,
 }
 
 // V pairs per item, IT items per lane; NEIGHBOURS: pairs (2j, 2j + 1), else (j, j + R / 2).  2^log_lg lanes take a row,
-// `parts` groups of them share a token's heads.
+// `parts` groups of them share a token's rows: those of its query heads, key heads and value heads.  (One loop for the
+// three, whose sources, places and weights are picked per row: with a loop for each, a small call waited for its code,
+// 320 tokens 17.8 us.)
 template <typename E, int V, int IT, bool NEIGHBOURS>
-__global__ void __launch_bounds__(NT) rope_kernel(RopeArgs a, int tb, int log_lg, int parts) {
-    constexpr int U = IT > 1 ? 1 : sizeof(E) == 4 ? 2 : 4;  // rows in flight per lane
+__global__ void __launch_bounds__(NT, IT == 1 ? 3 : 2) rope_kernel(RopeArgs a, int tb, int log_lg, int parts) {
+    constexpr int U = IT > 1 ? 1 : 2;  // rows in flight per lane
     extern __shared__ __align__(16) float sm[];
     __shared__ int64_t row_s[kMaxTB];   // row of (page, head 0, position in page), -1: nowhere
     __shared__ int64_t pos_s[kMaxTB];   // place in the sequence
@@ -93,7 +95,8 @@ __global__ void __launch_bounds__(NT) rope_kernel(RopeArgs a, int tb, int log_lg
     const int half = a.R >> 1, tid = threadIdx.x;
     uint64_t* turn_s = reinterpret_cast<uint64_t*>(sm);  // [half] frequencies, 2^-64 turns per position
     float* odd_s = sm + 2 * half;                        // [half] 0, NaN where the frequency is not finite
-    float* cos_s = sm + ((3 * half + 3) & ~3);           // [tb][half]
+    float* w_s = sm + ((3 * half + 3) & ~3);             // [2][D] norm weights of queries and keys
+    float* cos_s = w_s + 2 * a.D;                        // [tb][half]
     float* sin_s = cos_s + ((tb * half + 3) & ~3);
     pdl_wait();
     pdl_trigger();
@@ -125,6 +128,10 @@ __global__ void __launch_bounds__(NT) rope_kernel(RopeArgs a, int tb, int log_lg
         const double part = fabs(c) - floor(fabs(c));
         const uint64_t turn = isfinite(c) ? (uint64_t)__double2ull_rn(part * 18446744073709551616.0) : 0;
         turn_s[tid] = c < 0 ? 0 - turn : turn;
+    }
+    if (tid < a.D) {
+        if (a.q_w != nullptr) w_s[tid] = a.q_w[tid];
+        if (a.k_w != nullptr) w_s[a.D + tid] = a.k_w[tid];
     }
     __syncthreads();
     for (int e = tid; e < n * half; e += NT) {
@@ -175,101 +182,110 @@ __global__ void __launch_bounds__(NT) rope_kernel(RopeArgs a, int tb, int log_lg
                 co[i][v] = cos_s[at];
                 si[i][v] = sin_s[at];
             }
-        // heads part, part + parts, .. of x, with norm weight w where it has one
-        auto rows = [&](const E* x, int64_t x_head, int H, const float* w, bool rotate, bool write, E* out, int64_t out_head) {
-            float wt[IT][2 * V];
-            if (w != nullptr)
+        const int64_t row = row_s[t], cache_head = (int64_t)a.page_size * a.D;
+        const int n_rows = a.H_q + (a.k_cache != nullptr ? 2 * a.H_kv : 0);
+#pragma unroll 1
+        for (int r0 = part; r0 - part < n_rows; r0 += U * parts) {
+            Vec<E, V> xa[U][IT], xb[U][IT];
+            E* to[U];
+            const float* w[U];
+            bool turn[U];
 #pragma unroll
-                for (int i = 0; i < IT; ++i)
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + u * parts, kind = r < a.H_q ? 0 : r < a.H_q + a.H_kv ? 1 : 2;
+                const int h = kind == 0 ? r : kind == 1 ? r - a.H_q : r - a.H_q - a.H_kv;
+                const E* x = kind == 0 ? static_cast<const E*>(a.q) + token * a.q_tok + h * a.q_head
+                           : kind == 1 ? static_cast<const E*>(a.k) + token * a.k_tok + h * a.k_head
+                                       : static_cast<const E*>(a.v) + token * a.v_tok + h * a.v_head;
+                const int64_t place = row * a.D + h * cache_head;
+                to[u] = kind == 0 ? static_cast<E*>(a.q_out) + token * a.o_tok + h * a.o_head
+                      : kind == 1 ? static_cast<E*>(a.k_cache) + place : static_cast<E*>(a.v_cache) + place;
+                w[u] = kind == 0 ? a.q_w : kind == 1 ? a.k_w : nullptr;
+                turn[u] = kind < 2;
+                if (!active || r >= n_rows || (kind > 0 && row < 0)) to[u] = nullptr;
 #pragma unroll
-                    for (int v = 0; v < 2 * V; ++v)
-                        wt[i][v] = has[i] ? __ldg(w + (v < V ? off_a[i] + v : off_b[i] + v - V)) : 0.f;
-            for (int h0 = part; h0 - part < H; h0 += U * parts) {
-                Vec<E, V> xa[U][IT], xb[U][IT];
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int i = 0; i < IT; ++i) {
-                        const int h = h0 + u * parts;
-                        if (write && has[i] && h < H) {
-                            xa[u][i].load(x + h * x_head + off_a[i]);
-                            xb[u][i].load(x + h * x_head + off_b[i]);
-                        } else {
-                            xa[u][i].raw = {};
-                            xb[u][i].raw = {};
-                        }
+                for (int i = 0; i < IT; ++i) {
+                    xa[u][i].raw = {};
+                    xb[u][i].raw = {};
+                    if (to[u] != nullptr && has[i]) {
+                        xa[u][i].load(x + off_a[i]);
+                        xb[u][i].load(x + off_b[i]);
                     }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int h = h0 + u * parts;
-                    const bool real = write && h < H;
-                    if (rotate) {
-                        float y[IT][2 * V];
-#pragma unroll
-                        for (int i = 0; i < IT; ++i) {
-                            float ya[V], yb[V];
-                            widen<E, V>(xa[u][i], ya);
-                            widen<E, V>(xb[u][i], yb);
-#pragma unroll
-                            for (int v = 0; v < V; ++v) {
-                                y[i][v] = ya[v];
-                                y[i][V + v] = yb[v];
-                            }
-                        }
-                        if (w != nullptr) {
-                            float sum = 0.f;
-#pragma unroll
-                            for (int i = 0; i < IT; ++i)
-#pragma unroll
-                                for (int v = 0; v < 2 * V; ++v) sum = fmaf(y[i][v], y[i][v], sum);
-                            for (int o = lg >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                            const float r = 1.0f / sqrtf(sum / (float)a.D + a.eps);
-#pragma unroll
-                            for (int i = 0; i < IT; ++i)
-#pragma unroll
-                                for (int v = 0; v < 2 * V; ++v) y[i][v] *= r * wt[i][v];
-                        }
-#pragma unroll
-                        for (int i = 0; i < IT; ++i) {
-                            if (turns[i]) {
-#pragma unroll
-                                for (int v = 0; v < V; ++v) {
-                                    float& p = y[i][NEIGHBOURS ? 2 * v : v];
-                                    float& q = y[i][NEIGHBOURS ? 2 * v + 1 : V + v];
-                                    const float p1 = p * co[i][v] - q * si[i][v], q1 = q * co[i][v] + p * si[i][v];
-                                    p = p1;
-                                    q = q1;
-                                }
-                            }
-                            if (w == nullptr && !turns[i]) continue;  // passes through bit for bit
-                            float ya[V], yb[V];
-#pragma unroll
-                            for (int v = 0; v < V; ++v) {
-                                ya[v] = y[i][v];
-                                yb[v] = y[i][V + v];
-                            }
-                            narrow<E, V>(ya, xa[u][i]);
-                            narrow<E, V>(yb, xb[u][i]);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < IT; ++i)
-                        if (real && has[i]) {
-                            xa[u][i].store(out + h * out_head + off_a[i]);
-                            xb[u][i].store(out + h * out_head + off_b[i]);
-                        }
                 }
             }
-        };
-        rows(static_cast<const E*>(a.q) + token * a.q_tok, a.q_head, a.H_q, a.q_w, true, active,
-             static_cast<E*>(a.q_out) + token * a.o_tok, a.o_head);
-        if (a.k_cache != nullptr) {
-            const int64_t row = row_s[t], cache_head = (int64_t)a.page_size * a.D;
-            const bool there = active && row >= 0;
-            rows(static_cast<const E*>(a.k) + token * a.k_tok, a.k_head, a.H_kv, a.k_w, true, there,
-                 static_cast<E*>(a.k_cache) + row * a.D, cache_head);
-            rows(static_cast<const E*>(a.v) + token * a.v_tok, a.v_head, a.H_kv, nullptr, false, there,
-                 static_cast<E*>(a.v_cache) + row * a.D, cache_head);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool norm = w[u] != nullptr;
+                float y[IT][2 * V], scale = 1.f;
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+                    float ya[V], yb[V];
+                    widen<E, V>(xa[u][i], ya);
+                    widen<E, V>(xb[u][i], yb);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        y[i][v] = ya[v];
+                        y[i][V + v] = yb[v];
+                    }
+                }
+                if (__any_sync(0xffffffffu, norm)) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int i = 0; i < IT; ++i)
+#pragma unroll
+                        for (int v = 0; v < 2 * V; ++v) sum = fmaf(y[i][v], y[i][v], sum);
+                    for (int o = lg >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    scale = rsqrtf(sum / (float)a.D + a.eps);
+                }
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+                    if (!has[i] || to[u] == nullptr) continue;
+                    if (norm) {
+                        const float* wr = w_s + (w[u] == a.q_w ? 0 : a.D);
+                        float wt[2 * V];
+                        if constexpr (V % 4 == 0) {
+#pragma unroll
+                            for (int v = 0; v < V; v += 4) {
+                                const float4 fa = *reinterpret_cast<const float4*>(wr + off_a[i] + v);
+                                const float4 fb = *reinterpret_cast<const float4*>(wr + off_b[i] + v);
+                                wt[v] = fa.x; wt[v + 1] = fa.y; wt[v + 2] = fa.z; wt[v + 3] = fa.w;
+                                wt[V + v] = fb.x; wt[V + v + 1] = fb.y; wt[V + v + 2] = fb.z; wt[V + v + 3] = fb.w;
+                            }
+                        } else {
+#pragma unroll
+                            for (int v = 0; v < V; ++v) {
+                                wt[v] = wr[off_a[i] + v];
+                                wt[V + v] = wr[off_b[i] + v];
+                            }
+                        }
+#pragma unroll
+                        for (int v = 0; v < 2 * V; ++v) y[i][v] *= scale * wt[v];
+                    }
+                    const bool turned = turn[u] && turns[i];
+                    if (turned) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            float& p = y[i][NEIGHBOURS ? 2 * v : v];
+                            float& q = y[i][NEIGHBOURS ? 2 * v + 1 : V + v];
+                            const float p1 = p * co[i][v] - q * si[i][v], q1 = q * co[i][v] + p * si[i][v];
+                            p = p1;
+                            q = q1;
+                        }
+                    }
+                    if (norm || turned) {  // what is neither passes through bit for bit
+                        float ya[V], yb[V];
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            ya[v] = y[i][v];
+                            yb[v] = y[i][V + v];
+                        }
+                        narrow<E, V>(ya, xa[u][i]);
+                        narrow<E, V>(yb, xb[u][i]);
+                    }
+                    xa[u][i].store(to[u] + off_a[i]);
+                    xb[u][i].store(to[u] + off_b[i]);
+                }
+            }
         }
     }
 }
@@ -281,12 +297,13 @@ cudaError_t launch_v(const RopeArgs& a, cudaStream_t s) {
     int log_lg = 0;
     while (log_lg < 5 && (1 << log_lg) < items) ++log_lg;
     const int ng = NT >> log_lg;
-    // enough blocks to fill the SMs several times; a group of lanes a token where there are many
-    int64_t tb = a.T / (152 * 6);
+    // small blocks, so that lookups and cosines overlap copies; a group of lanes a token where there are many
+    int64_t tb = a.T / (152 * 16);
     tb = tb < 1 ? 1 : (tb > kMaxTB ? kMaxTB : tb);
+    const int rows = a.H_q + 2 * a.H_kv;
     int parts = (int)(ng / tb);
-    parts = parts < 1 ? 1 : (parts > a.H_q ? a.H_q : parts);
-    const size_t smem = sizeof(float) * (((3 * half + 3) & ~3) + 2 * (((size_t)tb * half + 3) & ~(size_t)3));
+    parts = parts < 1 ? 1 : (parts > rows ? rows : parts);
+    const size_t smem = sizeof(float) * (((3 * half + 3) & ~3) + 2 * a.D + 2 * (((size_t)tb * half + 3) & ~(size_t)3));
     return launch_pdl(rope_kernel<E, V, IT, NEIGHBOURS>, dim3((unsigned)((a.T + tb - 1) / tb)), dim3(NT), smem, s, a, (int)tb,
                       log_lg, parts);
 }
