@@ -2,8 +2,9 @@
 // the tensor-core kernel's loads do not take.
 //
 // 64 query rows of a group that share a key-value head against tiles of 64 cached
-// tokens, all in shared memory as f32; a thread holds 4 x 4 scores, then 4 rows of D / 16
-// outputs.  Bound by the products (f32 fused multiply-adds).
+// tokens in shared memory; a thread holds 4 x 4 scores, then 4 rows of D / 16 outputs, a warp 8 rows (none of them
+// real: it computes nothing).  V of a tile lands beside its scores, K of the next one beside its
+// outputs.  Bound by the products (f32 fused multiply-adds) and what feeds them from shared memory.
 #include "attn_shared.cuh"
 #include "tc_ptx.cuh"
 
@@ -24,130 +25,152 @@ __device__ __forceinline__ float4 ld4(const bf16* p) {
     return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
                        __uint_as_float(u.y & 0xffff0000u));
 }
+__device__ __forceinline__ float2 ld2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 ld2(const bf16* p) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
 
-// NC blocks of 64 head dims.
+// NC blocks of 32 head dims.
 template <typename E, int NC>
 struct Tiles {
-    static constexpr int QS = NC * 64 + 4;  // floats per row: rows 16 bytes apart in the banks
-    static constexpr int FLOATS = 3 * 64 * QS + TT * PS;
+    static constexpr int QS = NC * 32 + 4;                     // floats per row of Q: rows 16 bytes apart in the banks
+    static constexpr int KS = NC * 32 + 16 / (int)sizeof(E);   // elements per row of K and V
+    static constexpr int BYTES = 4 * (ROWS * QS + TT * PS) + 2 * TT * KS * (int)sizeof(E);
 };
 
 template <typename E, int NC>
 __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
     using T = Tiles<E, NC>;
-    constexpr int QS = T::QS;
+    constexpr int QS = T::QS, KS = T::KS;
     extern __shared__ __align__(16) float sm[];
-    __shared__ int64_t off_s[TT];
+    __shared__ int64_t off_s[2][TT];
     float* q_s = sm;
-    float* k_s = q_s + 64 * QS;
-    float* v_s = k_s + 64 * QS;
-    float* p_s = v_s + 64 * QS;  // [token][row]
+    float* p_s = q_s + ROWS * QS;  // [token][row]
+    E* k_s = reinterpret_cast<E*>(p_s + TT * PS);
+    E* v_s = k_s + TT * KS;
     const AttnArgs& a = s.a;
     const int D = a.D, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     pdl_wait();
     pdl_trigger();
     SharedWalk walk(s, blockIdx.x, gridDim.x);
     SharedSegment g;
-    const int fours = D / 4;
-    for (int i = tid; i < 3 * 64 * QS; i += NT) sm[i] = 0.f;  // dims from D on stay zero
+    const int fours = D / 4, chunks = D * (int)sizeof(E) / 16;
+    for (int i = tid; i < T::BYTES / 4; i += NT) sm[i] = 0.f;  // dims from D on stay zero
+    auto place = [&](int j) {  // where the tokens of tile j lie
+        if (tid < TT) {
+            const int t = j * TT + tid, pg = t / a.page_size;
+            const int page = a.table[(int64_t)g.leader * a.max_pages + pg];
+            off_s[j & 1][tid] = page < 0 || page >= a.n_pages
+                                    ? -1
+                                    : (((int64_t)page * a.H_kv + g.h) * a.page_size + (t - pg * a.page_size)) * D;
+        }
+    };
+    auto copy = [&](E* to, const void* from, int j) {  // a tile's rows, zeros where there is no page
+        for (int e = tid; e < TT * chunks; e += NT) {
+            const int t = e / chunks, c = e - t * chunks;
+            const int64_t at = off_s[j & 1][t];
+            const E* src = static_cast<const E*>(from) + (at >= 0 ? at + c * (16 / (int)sizeof(E)) : 0);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             tc::smem_u32(to + t * KS + c * (16 / (int)sizeof(E)))),
+                         "l"(src), "r"(at >= 0 ? 16 : 0)
+                         : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     while (walk.next(s, g)) {
         __syncthreads();
+        place(g.tile0);
         for (int e = tid; e < ROWS * fours; e += NT) {
             const int r = e / fours, d = (e - r * fours) * 4;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < g.nr) x = ld4(static_cast<const E*>(a.q) + shared_row(a, g.seq0, g.h, g.r0 + r) * D + d);
             *reinterpret_cast<float4*>(q_s + r * QS + d) = x;
         }
-        float m[4], l[4], o[4][4 * NC];
+        __syncthreads();
+        copy(k_s, a.k_cache, g.tile0);
+        const bool works = (tid >> 5) * 8 < g.nr;  // the warp has real rows
+        float m[4], l[4];
+        float2 o[4][NC];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             m[i] = kNone;
             l[i] = 0.f;
 #pragma unroll
-            for (int c = 0; c < 4 * NC; ++c) o[i][c] = 0.f;
+            for (int c = 0; c < NC; ++c) o[i][c] = make_float2(0.f, 0.f);
         }
         for (int j = g.tile0; j < g.tile1; ++j) {
-            if (tid < TT) {
-                const int t = j * TT + tid, pg = t / a.page_size;
-                const int page = a.table[(int64_t)g.leader * a.max_pages + pg];
-                off_s[tid] = page < 0 || page >= a.n_pages
-                                 ? -1
-                                 : (((int64_t)page * a.H_kv + g.h) * a.page_size + (t - pg * a.page_size)) * D;
-            }
-            __syncthreads();
-            for (int e = tid; e < TT * fours; e += NT) {
-                const int t = e / fours, d = (e - t * fours) * 4;
-                const int64_t at = off_s[t];
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-                if (at >= 0) {
-                    x = ld4(static_cast<const E*>(a.k_cache) + at + d);
-                    y = ld4(static_cast<const E*>(a.v_cache) + at + d);
-                }
-                *reinterpret_cast<float4*>(k_s + t * QS + d) = x;
-                *reinterpret_cast<float4*>(v_s + t * QS + d) = y;
-            }
+            copy(v_s, a.v_cache, j);
+            if (j + 1 < g.tile1) place(j + 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncthreads();
             // ---- scores of rows 4 ty .., tokens tx + 16 ..
-            float2 acc[4][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) acc[i][k] = make_float2(0.f, 0.f);
-#pragma unroll 2
-            for (int d = 0; d < D; d += 4) {
-                float4 q[4], k[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    q[i] = *reinterpret_cast<const float4*>(q_s + (4 * ty + i) * QS + d);
-                    k[i] = *reinterpret_cast<const float4*>(k_s + (tx + 16 * i) * QS + d);
-                }
+            if (works) {
+                float2 acc[4][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        acc[i][t] = __ffma2_rn(make_float2(q[i].x, q[i].y), make_float2(k[t].x, k[t].y), acc[i][t]);
-                        acc[i][t] = __ffma2_rn(make_float2(q[i].z, q[i].w), make_float2(k[t].z, k[t].w), acc[i][t]);
-                    }
-            }
-            // ---- weights
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float x[4], top = -INFINITY;
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    x[t] = (acc[i][t].x + acc[i][t].y) * a.scale_log2;
-                    top = fmaxf(top, x[t]);
-                }
-#pragma unroll
-                for (int w = 1; w < 16; w *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-                if (top > m[i] + kSlack) {  // (the 16 threads of a row agree)
-                    const float f = tc::ex2_approx(m[i] - top);
-                    m[i] = top;
-                    l[i] *= f;
-#pragma unroll
-                    for (int c = 0; c < 4 * NC; ++c) o[i][c] *= f;
-                }
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const float p = tc::ex2_approx(x[t] - m[i]);
-                    l[i] += p;
-                    p_s[(tx + 16 * t) * PS + 4 * ty + i] = p;
-                }
-            }
-            __syncwarp();  // a row's weights are written and read by one warp
-            // ---- O += P V: rows 4 ty .., dims 4 tx + 64 ..
+                    for (int k = 0; k < 4; ++k) acc[i][k] = make_float2(0.f, 0.f);
 #pragma unroll 2
-            for (int t = 0; t < TT; ++t) {
-                const float4 p = *reinterpret_cast<const float4*>(p_s + t * PS + 4 * ty);
-                const float w[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const float4 v = *reinterpret_cast<const float4*>(v_s + t * QS + 64 * c + 4 * tx);
+                for (int d = 0; d < D; d += 4) {
+                    float4 q[4], k[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float2* y = reinterpret_cast<float2*>(&o[i][4 * c]);
-                        y[0] = __ffma2_rn(make_float2(w[i], w[i]), make_float2(v.x, v.y), y[0]);
-                        y[1] = __ffma2_rn(make_float2(w[i], w[i]), make_float2(v.z, v.w), y[1]);
+                        q[i] = ld4(q_s + (4 * ty + i) * QS + d);
+                        k[i] = ld4(k_s + (tx + 16 * i) * KS + d);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            acc[i][t] = __ffma2_rn(make_float2(q[i].x, q[i].y), make_float2(k[t].x, k[t].y), acc[i][t]);
+                            acc[i][t] = __ffma2_rn(make_float2(q[i].z, q[i].w), make_float2(k[t].z, k[t].w), acc[i][t]);
+                        }
+                }
+                // ---- weights
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float x[4], top = -INFINITY;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        x[t] = (acc[i][t].x + acc[i][t].y) * a.scale_log2;
+                        top = fmaxf(top, x[t]);
+                    }
+                    if (__any_sync(0xffffffffu, top > m[i] + kSlack)) {
+#pragma unroll
+                        for (int w = 1; w < 16; w *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                        if (top > m[i] + kSlack) {  // (the 16 threads of a row agree)
+                            const float f = tc::ex2_approx(m[i] - top);
+                            m[i] = top;
+                            l[i] *= f;
+#pragma unroll
+                            for (int c = 0; c < NC; ++c) o[i][c] = __fmul2_rn(o[i][c], make_float2(f, f));
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const float p = tc::ex2_approx(x[t] - m[i]);
+                        l[i] += p;
+                        p_s[(tx + 16 * t) * PS + 4 * ty + i] = p;
+                    }
+                }
+            }
+            __syncthreads();
+            if (j + 1 < g.tile1) copy(k_s, a.k_cache, j + 1);
+            else asm volatile("cp.async.commit_group;" ::: "memory");
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncthreads();
+            // ---- O += P V: rows 4 ty .., dims 2 tx + 32 ..
+            if (works) {
+#pragma unroll 4
+                for (int t = 0; t < TT; ++t) {
+                    const float4 p = ld4(p_s + t * PS + 4 * ty);
+                    const float w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        const float2 v = ld2(v_s + t * KS + 32 * c + 2 * tx);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[i][c] = __ffma2_rn(make_float2(w[i], w[i]), v, o[i][c]);
                     }
                 }
             }
@@ -176,24 +199,25 @@ __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
             }
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-                if (64 * c + 4 * tx < D)
-                    *reinterpret_cast<float4*>(po + 64 * c + 4 * tx) =
-                        make_float4(o[i][4 * c], o[i][4 * c + 1], o[i][4 * c + 2], o[i][4 * c + 3]);
+                if (32 * c + 2 * tx < D) *reinterpret_cast<float2*>(po + 32 * c + 2 * tx) = o[i][c];
         }
     }
 }
 
 template <typename E, int NC>
 cudaError_t launch_nc(const ShareArgs& s, int n_cta, cudaStream_t st) {
-    constexpr int smem = Tiles<E, NC>::FLOATS * (int)sizeof(float);
+    constexpr int smem = Tiles<E, NC>::BYTES;
     const cudaError_t e = cudaFuncSetAttribute(attn_prefix_ffma_kernel<E, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(attn_prefix_ffma_kernel<E, NC>, dim3((unsigned)n_cta), dim3(NT), smem, st, s);
 }
 template <typename E>
 cudaError_t launch_e(const ShareArgs& s, int n_cta, cudaStream_t st) {
-    if (s.a.D <= 64) return launch_nc<E, 1>(s, n_cta, st);
-    return s.a.D <= 128 ? launch_nc<E, 2>(s, n_cta, st) : launch_nc<E, 4>(s, n_cta, st);
+    const int D = s.a.D;
+    if (D <= 64) return launch_nc<E, 2>(s, n_cta, st);
+    if (D <= 96) return launch_nc<E, 3>(s, n_cta, st);
+    if (D <= 128) return launch_nc<E, 4>(s, n_cta, st);
+    return D <= 192 ? launch_nc<E, 6>(s, n_cta, st) : launch_nc<E, 8>(s, n_cta, st);
 }
 
 }  // namespace

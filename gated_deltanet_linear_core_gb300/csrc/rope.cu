@@ -3,11 +3,13 @@
 //
 // With f_j the frequency of pair j and p the token's position on the pair's axis,
 //   x <- x / sqrt(mean x^2 + eps) w,   (a, b) <- mscale (a cos p f_j - b sin p f_j, b cos p f_j + a sin p f_j)
-// A copy with some arithmetic on the way; HBM-bound.  A block takes TB tokens.  It first
-// makes their cosines and sines (once per token, whatever the number of heads) and looks up
-// where each goes in the cache; then groups of lanes take a (token, share of the heads)
-// each.  A lane holds both sides of its pairs, so a rotation needs no exchange, and its
-// cosines stay in registers over the heads.
+// A copy with some arithmetic on the way; HBM-bound.  Every warp works on its own, without barriers: it takes
+// a few tokens (or a share of one's rows), looks up where they go in the cache (a lane each), makes their cosines and
+// sines (a pair per lane, once for all heads), and copies their rows.  A lane holds both sides of
+// its pairs, so a rotation needs no exchange, and its cosines stay in registers over the
+// heads.  Rows come through shared memory, kStages steps ahead and across tokens (cp.async; a lane reads back what
+// it copied itself): with loads into registers, four rows at a time, 32768 prompt tokens into the cache took
+// 163 us, in blocks with barriers as well.
 //
 // The angle of a far position keeps no digits in f32: p f is held in turns, as a 64-bit
 // fraction of one turn (f / 2 pi in f64, times 2^64), whose product with the integer p drops whole
@@ -20,8 +22,10 @@ namespace gdn {
 
 namespace {
 
-constexpr int NT = 256;
-constexpr int kMaxTB = 16;
+constexpr int NT = 128;
+constexpr int NW = NT / 32;
+constexpr int kStages = 8;
+constexpr int kTokens = 4;  // of a warp at once, where there are many (one by one, looking up and the cosines took two thirds of the time)
 
 template <int BYTES> struct RawOf;
 template <> struct RawOf<16> { using type = uint4; };
@@ -36,31 +40,60 @@ struct Vec {
     union {
         Raw raw;
         E e[V];
+        uint32_t w[V * sizeof(E) >= 4 ? V * sizeof(E) / 4 : 1];
     };
     __device__ __forceinline__ Vec() {}
-    __device__ __forceinline__ void load(const E* p) { raw = __ldcs(reinterpret_cast<const Raw*>(p)); }
+    // copies to shared memory, there after the next wait (two bytes: at once)
+    __device__ __forceinline__ static void fetch(Raw* to, const E* p) {
+        if constexpr (sizeof(Raw) == 2) {
+            *to = *reinterpret_cast<const Raw*>(p);
+        } else {
+            const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+            if constexpr (sizeof(Raw) == 16)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(p) : "memory");
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(p), "n"(sizeof(Raw)) : "memory");
+        }
+    }
     __device__ __forceinline__ void store(E* p) const { *reinterpret_cast<Raw*>(p) = raw; }
 };
 
+// The 2 V elements of two vectors as V pairs of f32 (V = 1: one of each), and back.
 template <typename E, int V>
-__device__ __forceinline__ void widen(const Vec<E, V>& v, float (&x)[V]) {
-    if constexpr (V * sizeof(E) == 16) {
-        unpack16<E>(v.raw, x);
+__device__ __forceinline__ void widen(const Vec<E, V>& a, const Vec<E, V>& b, float2 (&z)[V]) {
+    if constexpr (V == 1) {
+        z[0] = make_float2(to_f(a.e[0]), to_f(b.e[0]));
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = to_f(v.e[i]);
+        for (int k = 0; k < V; ++k) {
+            const Vec<E, V>& x = k < V / 2 ? a : b;
+            const int at = k % (V / 2);
+            if constexpr (sizeof(E) == 2) {
+                const uint32_t w = x.w[at];
+                z[k] = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+            } else {
+                z[k] = make_float2(x.e[2 * at], x.e[2 * at + 1]);
+            }
+        }
     }
 }
 template <typename E, int V>
-__device__ __forceinline__ void narrow(const float (&x)[V], Vec<E, V>& v) {
-    if constexpr (sizeof(E) == 2 && V >= 2) {
-        uint32_t w[V / 2];
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-        memcpy(&v.raw, w, sizeof(v.raw));
+__device__ __forceinline__ void narrow(const float2 (&z)[V], Vec<E, V>& a, Vec<E, V>& b) {
+    if constexpr (V == 1) {
+        a.e[0] = from_f<E>(z[0].x);
+        b.e[0] = from_f<E>(z[0].y);
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v.e[i] = from_f<E>(x[i]);
+        for (int k = 0; k < V; ++k) {
+            Vec<E, V>& x = k < V / 2 ? a : b;
+            const int at = k % (V / 2);
+            if constexpr (sizeof(E) == 2) {
+                x.w[at] = pack_bf16x2(z[k].x, z[k].y);
+            } else {
+                x.e[2 * at] = z[k].x;
+                x.e[2 * at + 1] = z[k].y;
+            }
+        }
     }
 }
 
@@ -81,81 +114,49 @@ __device__ __forceinline__ bool find_token(const RopeArgs& a, int64_t t, int& b,
     return true;
 }
 
-// V pairs per item, IT items per lane; NEIGHBOURS: pairs (2j, 2j + 1), else (j, j + R / 2).  2^log_lg lanes take a row,
-// `parts` groups of them share a token's rows: those of its query heads, key heads and value heads.  (One loop for the
-// three, whose sources, places and weights are picked per row: with a loop for each, a small call waited for its code,
-// 320 tokens 17.8 us.)
-template <typename E, int V, int IT, bool NEIGHBOURS>
-__global__ void __launch_bounds__(NT, IT == 1 ? 3 : 2) rope_kernel(RopeArgs a, int tb, int log_lg, int parts) {
-    constexpr int U = IT > 1 ? 1 : 2;  // rows in flight per lane
+// V pairs per item, IT items per lane; NEIGHBOURS: pairs (2j, 2j + 1), else (j, j + R / 2).
+// `lg` lanes take a row (a power of two where a norm adds up over them), `tb` tokens at once or `parts` warps for a
+// token's rows: those of its query heads, key heads and value heads.  (One loop for the three, whose sources and places are picked per
+// row: with a loop for each, a small call waited for its code, 320 tokens 17.8 us.)
+template <typename E, int V, int IT, bool NEIGHBOURS, bool NORM>
+__global__ void __launch_bounds__(NT, NORM ? 4 : 5) rope_kernel(RopeArgs a, int lg, int tb, int parts) {
     extern __shared__ __align__(16) float sm[];
-    __shared__ int64_t row_s[kMaxTB];   // row of (page, head 0, position in page), -1: nowhere
-    __shared__ int64_t pos_s[kMaxTB];   // place in the sequence
-    __shared__ int in_s[kMaxTB];        // the token belongs to a sequence
-    const int half = a.R >> 1, tid = threadIdx.x;
+    const int half = a.R >> 1, tid = threadIdx.x, warp = tid >> 5;
     uint64_t* turn_s = reinterpret_cast<uint64_t*>(sm);  // [half] frequencies, 2^-64 turns per position
     float* odd_s = sm + 2 * half;                        // [half] 0, NaN where the frequency is not finite
-    float* w_s = sm + ((3 * half + 3) & ~3);             // [2][D] norm weights of queries and keys
-    float* cos_s = w_s + 2 * a.D;                        // [tb][half]
-    float* sin_s = cos_s + ((tb * half + 3) & ~3);
+    int* axis_s = reinterpret_cast<int*>(sm + 3 * half); // [half] axes, -1: none
+    float* w_s = sm + ((4 * half + 3) & ~3);             // [2][D] norm weights of queries and keys
+    using Raw = typename Vec<E, V>::Raw;
+    // the warp's stages [kStages][IT][a, b][32], of which a lane fills and reads its own
+    Raw* stage_s = reinterpret_cast<Raw*>(w_s + 2 * a.D) + warp * (kStages * IT * 64) + (tid & 31);
+    float* cos_s = reinterpret_cast<float*>(reinterpret_cast<Raw*>(w_s + 2 * a.D) + NW * (kStages * IT * 64)) +
+                   warp * (2 * tb * half);               // [tb][half] of the warp's tokens
+    float* sin_s = cos_s + tb * half;
     pdl_wait();
     pdl_trigger();
-    const int64_t t0 = (int64_t)blockIdx.x * tb;
-    const int n = (int)min((int64_t)tb, a.T - t0);
-    if (tid >= NT - kMaxTB) {
-        const int i = tid - (NT - kMaxTB);
-        if (i < n) {
-            int64_t row = -1, pos = 0;
-            bool in = true;
-            if (a.k_cache != nullptr) {
-                int b;
-                in = find_token(a, t0 + i, b, pos);
-                if (in && pos >= 0 && pos < (int64_t)a.max_pages * a.page_size) {
-                    const int pg = (int)(pos / a.page_size);
-                    const int page = a.table[(int64_t)b * a.max_pages + pg];
-                    if (page >= 0 && page < a.n_pages)
-                        row = (int64_t)page * a.H_kv * a.page_size + (pos - (int64_t)pg * a.page_size);
-                }
-            }
-            row_s[i] = row;
-            pos_s[i] = pos;
-            in_s[i] = in;
-        }
-    }
-    if (tid < half) {
+    if (tid < half) {  // (half is at most NT)
         double c = (double)a.inv_freq[tid] * 0.15915494309189533577;  // turns per position
         odd_s[tid] = (float)(c - c);
         const double part = fabs(c) - floor(fabs(c));
         const uint64_t turn = isfinite(c) ? (uint64_t)__double2ull_rn(part * 18446744073709551616.0) : 0;
         turn_s[tid] = c < 0 ? 0 - turn : turn;
+        const int ax = a.axes != nullptr ? a.axes[tid] : 0;
+        axis_s[tid] = ax >= 0 && ax < a.n_axes ? ax : -1;
     }
-    if (tid < a.D) {
-        if (a.q_w != nullptr) w_s[tid] = a.q_w[tid];
-        if (a.k_w != nullptr) w_s[a.D + tid] = a.k_w[tid];
-    }
-    __syncthreads();
-    for (int e = tid; e < n * half; e += NT) {
-        const int t = e / half, j = e - t * half;
-        const int ax = a.axes != nullptr ? a.axes[j] : 0;
-        const bool known = ax >= 0 && ax < a.n_axes;
-        int64_t p = 0;
-        if (known) p = a.positions == nullptr ? pos_s[t] : a.positions[ax * a.T + t0 + t];
-        const int32_t f = (int32_t)(((uint64_t)p * turn_s[j]) >> 32);
-        float s, c;
-        sincospif((float)f * 4.656612873077392578125e-10f + (known ? odd_s[j] : 0.f), &s, &c);  // 2^-31: half turns
-        cos_s[e] = c * a.mscale;
-        sin_s[e] = s * a.mscale;
+    for (int d = tid; NORM && d < a.D; d += NT) {
+        if (a.q_w != nullptr) w_s[d] = a.q_w[d];
+        if (a.k_w != nullptr) w_s[a.D + d] = a.k_w[d];
     }
     __syncthreads();
 
-    const int lg = 1 << log_lg, lane = tid & (lg - 1), ng = NT >> log_lg;
+    const int wl = tid & 31, rw = 32 / lg, grp = wl / lg, lane = wl - grp * lg;  // rows of a warp at once
     const int items = (a.D >> 1) / V;
     int off_a[IT], off_b[IT], pair[IT];
     bool has[IT], turns[IT];
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int it = lane + i * lg, p = it * V;
-        has[i] = it < items;
+        has[i] = it < items && grp < rw;
         turns[i] = has[i] && p < half;
         pair[i] = p;
         if (NEIGHBOURS) {
@@ -169,10 +170,105 @@ __global__ void __launch_bounds__(NT, IT == 1 ? 3 : 2) rope_kernel(RopeArgs a, i
             off_b[i] = p + (a.D >> 1);
         }
     }
-    for (int g0 = 0; g0 < n * parts; g0 += ng) {  // the lanes of a warp stay together (they share the norm's sums)
-        const int gi = g0 + (tid >> log_lg), t = gi < n * parts ? gi / parts : 0, part = gi - t * parts;
-        const bool active = gi < n * parts && in_s[t];
-        const int64_t token = t0 + t;
+    const int64_t cache_head = (int64_t)a.page_size * a.D;
+    const int step = parts * rw, kinds = a.k_cache != nullptr ? 3 : 1;
+    const int64_t all = (a.T + tb - 1) / tb * parts, stride = (int64_t)gridDim.x * NW;
+    auto split = [&](int64_t item, int64_t& token, int& h) {  // an item's first token and this lane's first head
+        const int64_t batch = parts == 1 ? item : (uint32_t)item / (uint32_t)parts;  // several parts: few tokens
+        token = batch * tb;
+        h = (int)(item - batch * parts) * rw + grp;
+    };
+    // the rows, those of an item's queries, keys and values after one another, kStages ahead
+    struct {
+        int64_t item, token, upto, skip;  // an item's tokens, elements between a lane's rows
+        const E* x;
+        int h0, h, heads, kind, stage;
+    } in;
+    in.item = (int64_t)blockIdx.x * NW + warp;
+    in.stage = 0;
+    auto enter = [&](int kind) {  // the token's rows of a kind
+        in.kind = kind;
+        in.h = in.h0;
+        in.heads = kind == 0 ? a.H_q : a.H_kv;
+        const int64_t tok = kind == 0 ? a.q_tok : kind == 1 ? a.k_tok : a.v_tok;
+        const int64_t head = kind == 0 ? a.q_head : kind == 1 ? a.k_head : a.v_head;
+        in.x = static_cast<const E*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + in.token * tok + in.h * head;
+        in.skip = step * head;
+    };
+    auto begin = [&] {
+        if (in.item >= all) return;
+        split(in.item, in.token, in.h0);
+        in.upto = min(in.token + tb, a.T);
+        enter(0);
+    };
+    begin();
+    auto fetch = [&] {
+        if (in.item < all) {
+            if (in.h < in.heads)
+#pragma unroll
+                for (int i = 0; i < IT; ++i)
+                    if (has[i]) {
+                        Vec<E, V>::fetch(stage_s + (in.stage * IT + i) * 64, in.x + off_a[i]);
+                        Vec<E, V>::fetch(stage_s + (in.stage * IT + i) * 64 + 32, in.x + off_b[i]);
+                    }
+            in.h += step;
+            in.x += in.skip;
+            if (in.h - grp >= in.heads) {  // (the lanes of a warp go on together)
+                if (in.kind + 1 < kinds) {
+                    enter(in.kind + 1);
+                } else if (++in.token < in.upto) {
+                    enter(0);
+                } else {
+                    in.item += stride;
+                    begin();
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        in.stage = (in.stage + 1) % kStages;
+    };
+#pragma unroll 1
+    for (int i = 0; i < kStages; ++i) fetch();
+    int stage = 0;
+    const float inv_d = 1.0f / (float)a.D;
+    const uint32_t per_half = (65536 + half - 1) / half;  // e / half = e per_half / 65536 for e < 65536 / half
+    for (int64_t item = (int64_t)blockIdx.x * NW + warp; item < all; item += stride) {
+        int64_t first;
+        int h0;
+        split(item, first, h0);
+        const int n = (int)min((int64_t)tb, a.T - first);
+        // lane i: token i's place in its sequence, and its row (page, head 0, position in page), -1: nowhere
+        int64_t its_row = -1, its_pos = 0;
+        bool its_member = true;
+        if (a.k_cache != nullptr && wl < n) {
+            int b;
+            its_member = find_token(a, first + wl, b, its_pos);
+            if (its_member && its_pos >= 0 && its_pos < (int64_t)a.max_pages * a.page_size) {
+                const int pg = (int)((uint32_t)its_pos / (uint32_t)a.page_size);
+                const int page = a.table[(int64_t)b * a.max_pages + pg];
+                if (page >= 0 && page < a.n_pages)
+                    its_row = (int64_t)page * a.H_kv * a.page_size + (its_pos - (int64_t)pg * a.page_size);
+            }
+        }
+        __syncwarp();  // the cosines before are read
+        for (int e0 = 0; e0 < n * half; e0 += 32) {
+            const int e = e0 + wl, t = min((int)((uint32_t)e * per_half >> 16), n - 1), j = e - t * half;
+            int64_t p = __shfl_sync(0xffffffffu, its_pos, t);
+            if (e < n * half) {
+                const int ax = axis_s[j];
+                if (a.positions != nullptr) p = ax >= 0 ? a.positions[ax * a.T + first + t] : 0;
+                const int32_t f = ax >= 0 ? (int32_t)(((uint64_t)p * turn_s[j]) >> 32) : 0;
+                float s, c;
+                sincospif((float)f * 4.656612873077392578125e-10f + (ax >= 0 ? odd_s[j] : 0.f), &s, &c);  // 2^-31: half turns
+                cos_s[e] = c * a.mscale;
+                sin_s[e] = s * a.mscale;
+            }
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int t = 0; t < n; ++t) {
+        const int64_t token = first + t, row = __shfl_sync(0xffffffffu, its_row, t);
+        const bool member = __shfl_sync(0xffffffffu, (int)its_member, t) != 0;
         float co[IT][V], si[IT][V];
 #pragma unroll
         for (int i = 0; i < IT; ++i)
@@ -182,110 +278,92 @@ __global__ void __launch_bounds__(NT, IT == 1 ? 3 : 2) rope_kernel(RopeArgs a, i
                 co[i][v] = cos_s[at];
                 si[i][v] = sin_s[at];
             }
-        const int64_t row = row_s[t], cache_head = (int64_t)a.page_size * a.D;
-        const int n_rows = a.H_q + (a.k_cache != nullptr ? 2 * a.H_kv : 0);
 #pragma unroll 1
-        for (int r0 = part; r0 - part < n_rows; r0 += U * parts) {
-            Vec<E, V> xa[U][IT], xb[U][IT];
-            E* to[U];
-            const float* w[U];
-            bool turn[U];
+        for (int kind = 0; kind < kinds; ++kind) {
+            const int heads = kind == 0 ? a.H_q : a.H_kv;
+            const int64_t head = kind == 0 ? a.o_head : cache_head;
+            E* to = kind == 0 ? static_cast<E*>(a.q_out) + token * a.o_tok
+                              : static_cast<E*>(kind == 1 ? a.k_cache : a.v_cache) + row * a.D;
+            to += h0 * head;
+            const int64_t skip = step * head;
+            const bool there = member && grp < rw && (kind == 0 || row >= 0);
+            const bool norm = (kind == 0 ? a.q_w : kind == 1 ? a.k_w : nullptr) != nullptr;
+            float2 wt[IT][V];
+            if (NORM && norm) {
+                const float* wr = w_s + (kind == 0 ? 0 : a.D);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int r = r0 + u * parts, kind = r < a.H_q ? 0 : r < a.H_q + a.H_kv ? 1 : 2;
-                const int h = kind == 0 ? r : kind == 1 ? r - a.H_q : r - a.H_q - a.H_kv;
-                const E* x = kind == 0 ? static_cast<const E*>(a.q) + token * a.q_tok + h * a.q_head
-                           : kind == 1 ? static_cast<const E*>(a.k) + token * a.k_tok + h * a.k_head
-                                       : static_cast<const E*>(a.v) + token * a.v_tok + h * a.v_head;
-                const int64_t place = row * a.D + h * cache_head;
-                to[u] = kind == 0 ? static_cast<E*>(a.q_out) + token * a.o_tok + h * a.o_head
-                      : kind == 1 ? static_cast<E*>(a.k_cache) + place : static_cast<E*>(a.v_cache) + place;
-                w[u] = kind == 0 ? a.q_w : kind == 1 ? a.k_w : nullptr;
-                turn[u] = kind < 2;
-                if (!active || r >= n_rows || (kind > 0 && row < 0)) to[u] = nullptr;
+                for (int i = 0; i < IT; ++i)
+                    if (has[i])
 #pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    xa[u][i].raw = {};
-                    xb[u][i].raw = {};
-                    if (to[u] != nullptr && has[i]) {
-                        xa[u][i].load(x + off_a[i]);
-                        xb[u][i].load(x + off_b[i]);
-                    }
-                }
+                        for (int k = 0; k < V; ++k) {
+                            const float* wa = wr + (V == 1 ? off_a[i] : k < V / 2 ? off_a[i] + 2 * k : off_b[i] + 2 * k - V);
+                            wt[i][k] = V == 1 ? make_float2(wa[0], wr[off_b[i]]) : *reinterpret_cast<const float2*>(wa);
+                        }
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const bool norm = w[u] != nullptr;
-                float y[IT][2 * V], scale = 1.f;
+#pragma unroll 1
+            for (int h = h0; h - grp < heads; h += step, to += skip) {
+                Vec<E, V> xa[IT], xb[IT];
+                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
 #pragma unroll
                 for (int i = 0; i < IT; ++i) {
-                    float ya[V], yb[V];
-                    widen<E, V>(xa[u][i], ya);
-                    widen<E, V>(xb[u][i], yb);
+                    xa[i].raw = stage_s[(stage * IT + i) * 64];
+                    xb[i].raw = stage_s[(stage * IT + i) * 64 + 32];
+                }
+                stage = (stage + 1) % kStages;
+                fetch();
+                if (kind < 2) {  // values are copied
+                    float2 z[IT][V];
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        y[i][v] = ya[v];
-                        y[i][V + v] = yb[v];
+                    for (int i = 0; i < IT; ++i) widen<E, V>(xa[i], xb[i], z[i]);
+                    if (NORM && norm) {
+                        float2 sq = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < IT; ++i)
+                            if (has[i])
+#pragma unroll
+                                for (int k = 0; k < V; ++k) sq = __ffma2_rn(z[i][k], z[i][k], sq);
+                        float sum = h < heads ? sq.x + sq.y : 0.f;
+                        for (int o = lg >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                        const float scale = rsqrtf(fmaf(sum, inv_d, a.eps));
+#pragma unroll
+                        for (int i = 0; i < IT; ++i) {
+                            if (!has[i]) continue;
+#pragma unroll
+                            for (int k = 0; k < V; ++k) z[i][k] = __fmul2_rn(__fmul2_rn(z[i][k], make_float2(scale, scale)), wt[i][k]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < IT; ++i) {
+                        if (turns[i]) {
+                            if constexpr (NEIGHBOURS || V == 1) {
+#pragma unroll
+                                for (int k = 0; k < V; ++k)
+                                    z[i][k] = __ffma2_rn(z[i][k], make_float2(co[i][k], co[i][k]),
+                                                         __fmul2_rn(make_float2(z[i][k].y, z[i][k].x),
+                                                                    make_float2(-si[i][k], si[i][k])));
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < V / 2; ++k) {
+                                    const float2 p = z[i][k], q = z[i][V / 2 + k];
+                                    const float2 c = make_float2(co[i][2 * k], co[i][2 * k + 1]);
+                                    const float2 sn = make_float2(si[i][2 * k], si[i][2 * k + 1]);
+                                    z[i][k] = __ffma2_rn(p, c, __fmul2_rn(q, make_float2(-sn.x, -sn.y)));
+                                    z[i][V / 2 + k] = __ffma2_rn(q, c, __fmul2_rn(p, sn));
+                                }
+                            }
+                        }
+                        if ((NORM && norm) || turns[i]) narrow<E, V>(z[i], xa[i], xb[i]);  // what is neither passes bit for bit
                     }
                 }
-                if (__any_sync(0xffffffffu, norm)) {
-                    float sum = 0.f;
+                if (there && h < heads)
 #pragma unroll
                     for (int i = 0; i < IT; ++i)
-#pragma unroll
-                        for (int v = 0; v < 2 * V; ++v) sum = fmaf(y[i][v], y[i][v], sum);
-                    for (int o = lg >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    scale = rsqrtf(sum / (float)a.D + a.eps);
-                }
-#pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    if (!has[i] || to[u] == nullptr) continue;
-                    if (norm) {
-                        const float* wr = w_s + (w[u] == a.q_w ? 0 : a.D);
-                        float wt[2 * V];
-                        if constexpr (V % 4 == 0) {
-#pragma unroll
-                            for (int v = 0; v < V; v += 4) {
-                                const float4 fa = *reinterpret_cast<const float4*>(wr + off_a[i] + v);
-                                const float4 fb = *reinterpret_cast<const float4*>(wr + off_b[i] + v);
-                                wt[v] = fa.x; wt[v + 1] = fa.y; wt[v + 2] = fa.z; wt[v + 3] = fa.w;
-                                wt[V + v] = fb.x; wt[V + v + 1] = fb.y; wt[V + v + 2] = fb.z; wt[V + v + 3] = fb.w;
-                            }
-                        } else {
-#pragma unroll
-                            for (int v = 0; v < V; ++v) {
-                                wt[v] = wr[off_a[i] + v];
-                                wt[V + v] = wr[off_b[i] + v];
-                            }
+                        if (has[i]) {
+                            xa[i].store(to + off_a[i]);
+                            xb[i].store(to + off_b[i]);
                         }
-#pragma unroll
-                        for (int v = 0; v < 2 * V; ++v) y[i][v] *= scale * wt[v];
-                    }
-                    const bool turned = turn[u] && turns[i];
-                    if (turned) {
-#pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            float& p = y[i][NEIGHBOURS ? 2 * v : v];
-                            float& q = y[i][NEIGHBOURS ? 2 * v + 1 : V + v];
-                            const float p1 = p * co[i][v] - q * si[i][v], q1 = q * co[i][v] + p * si[i][v];
-                            p = p1;
-                            q = q1;
-                        }
-                    }
-                    if (norm || turned) {  // what is neither passes through bit for bit
-                        float ya[V], yb[V];
-#pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            ya[v] = y[i][v];
-                            yb[v] = y[i][V + v];
-                        }
-                        narrow<E, V>(ya, xa[u][i]);
-                        narrow<E, V>(yb, xb[u][i]);
-                    }
-                    xa[u][i].store(to[u] + off_a[i]);
-                    xb[u][i].store(to[u] + off_b[i]);
-                }
             }
+        }
         }
     }
 }
@@ -294,18 +372,27 @@ template <typename E, int V, bool NEIGHBOURS>
 cudaError_t launch_v(const RopeArgs& a, cudaStream_t s) {
     constexpr int IT = V >= 4 ? 1 : 4 / V;  // 128 pairs at most
     const int items = (a.D >> 1) / V, half = a.R >> 1;
-    int log_lg = 0;
-    while (log_lg < 5 && (1 << log_lg) < items) ++log_lg;
-    const int ng = NT >> log_lg;
-    // small blocks, so that lookups and cosines overlap copies; a group of lanes a token where there are many
-    int64_t tb = a.T / (152 * 16);
-    tb = tb < 1 ? 1 : (tb > kMaxTB ? kMaxTB : tb);
-    const int rows = a.H_q + 2 * a.H_kv;
-    int parts = (int)(ng / tb);
-    parts = parts < 1 ? 1 : (parts > rows ? rows : parts);
-    const size_t smem = sizeof(float) * (((3 * half + 3) & ~3) + 2 * a.D + 2 * (((size_t)tb * half + 3) & ~(size_t)3));
-    return launch_pdl(rope_kernel<E, V, IT, NEIGHBOURS>, dim3((unsigned)((a.T + tb - 1) / tb)), dim3(NT), smem, s, a, (int)tb,
-                      log_lg, parts);
+    int lg = items;
+    if (a.q_w != nullptr || a.k_w != nullptr || items > 32) {
+        lg = 1;
+        while (lg < 32 && lg < items) lg *= 2;
+    }
+    const int rw = 32 / lg;
+    // few tokens: several warps share one's rows
+    const int most = (a.H_q + rw - 1) / rw;
+    int64_t parts = (2 * 152 * 4 * NW + a.T - 1) / a.T;
+    parts = parts < 1 ? 1 : (parts > most ? most : parts);
+    const bool norm = a.q_w != nullptr || a.k_w != nullptr;
+    const int ctas = 152 * (norm ? 4 : 5);  // resident at once: registers
+    const int tb = a.T < ctas * NW * kTokens ? 1 : kTokens;
+    int64_t blocks = ((a.T + tb - 1) / tb * parts + NW - 1) / NW;
+    blocks = blocks > ctas ? ctas : blocks;
+    const size_t smem = sizeof(float) * (((4 * half + 3) & ~3) + 2 * a.D + NW * 2 * tb * half) +
+                        (size_t)NW * kStages * IT * 64 * V * sizeof(E);
+    const auto kernel = norm ? rope_kernel<E, V, IT, NEIGHBOURS, true> : rope_kernel<E, V, IT, NEIGHBOURS, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(NT), smem, s, a, lg, tb, (int)parts);
 }
 
 template <typename E, bool NEIGHBOURS>
