@@ -24,7 +24,7 @@ namespace {
 
 constexpr int NT = 128;
 constexpr int NW = NT / 32;
-constexpr int kStages = 8;
+constexpr int kStages = 4;
 constexpr int kTokens = 4;  // of a warp at once, where there are many (one by one, looking up and the cosines took two thirds of the time)
 
 template <int BYTES> struct RawOf;
@@ -380,7 +380,7 @@ cudaError_t launch_v(const RopeArgs& a, cudaStream_t s) {
     const int rw = 32 / lg;
     // few tokens: several warps share one's rows
     const int most = (a.H_q + rw - 1) / rw;
-    int64_t parts = (2 * 152 * 4 * NW + a.T - 1) / a.T;
+    int64_t parts = 152 * 4 * NW / a.T;  // all warps at once
     parts = parts < 1 ? 1 : (parts > most ? most : parts);
     const bool norm = a.q_w != nullptr || a.k_w != nullptr;
     const int ctas = 152 * (norm ? 4 : 5);  // resident at once: registers
