@@ -20,6 +20,7 @@
 
 #include "gdn_common.cuh"
 #include "gdn_launch.h"
+#include "tc_ptx.cuh"
 
 namespace gdn {
 namespace attn {
@@ -231,6 +232,30 @@ __device__ __forceinline__ void join_lanes(float* v, int lane, F f) {
         }
     }
 }
+
+// Puts parts of a row together: the running maximum, sum and unnormalised output.
+struct Running {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    template <int U>
+    __device__ __forceinline__ void add(const float (&m1)[U], const float (&l1)[U], const float4 (&x)[U]) {
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < U; ++k) top = fmaxf(top, m1[k]);
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float f = tc::ex2_approx(m - ref);
+        m = top;
+        l *= f;
+        o.x *= f; o.y *= f; o.z *= f; o.w *= f;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const float w = tc::ex2_approx(m1[k] - ref);
+            l = fmaf(l1[k], w, l);
+            o.x = fmaf(x[k].x, w, o.x); o.y = fmaf(x[k].y, w, o.y);
+            o.z = fmaf(x[k].z, w, o.z); o.w = fmaf(x[k].w, w, o.w);
+        }
+    }
+};
 
 }  // namespace attn
 }  // namespace gdn

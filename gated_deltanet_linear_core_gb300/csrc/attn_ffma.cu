@@ -342,28 +342,6 @@ __global__ void __launch_bounds__(Ffma<E, R, NV>::NT, 1) attn_ffma_kernel(AttnAr
 // 16 new tokens 83 -> 79 us; one of 201 tokens 12.2 -> 10.2).
 constexpr int JT = 256;
 constexpr int kSerial = 8;
-struct Running {
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    template <int U>
-    __device__ __forceinline__ void add(const float (&m1)[U], const float (&l1)[U], const float4 (&x)[U]) {
-        float top = m;
-#pragma unroll
-        for (int k = 0; k < U; ++k) top = fmaxf(top, m1[k]);
-        const float ref = top == -INFINITY ? 0.f : top;
-        const float f = tc::ex2_approx(m - ref);
-        m = top;
-        l *= f;
-        o.x *= f; o.y *= f; o.z *= f; o.w *= f;
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const float w = tc::ex2_approx(m1[k] - ref);
-            l = fmaf(l1[k], w, l);
-            o.x = fmaf(x[k].x, w, o.x); o.y = fmaf(x[k].y, w, o.y);
-            o.z = fmaf(x[k].z, w, o.z); o.w = fmaf(x[k].w, w, o.w);
-        }
-    }
-};
 template <typename T>
 __device__ __forceinline__ float gate_of(float g) {
     return sizeof(T) == 2 ? __fdividef(1.0f, 1.0f + __expf(-g)) : sigmoid_f(g);

@@ -1,10 +1,12 @@
-// The pass over shared prefixes on CUDA cores: f32, and bf16 with page sizes that
-// the tensor-core kernel's loads do not take.
+// Attention behind shared prefixes on CUDA cores: f32, and bf16 with page sizes that the
+// tensor-core kernel's loads do not take.  The prefixes, and where a sequence has more rows per
+// key-value head than attn_ffma.cu takes at once what each has of its own too.
 //
 // 64 query rows of a group that share a key-value head against tiles of 64 cached
 // tokens in shared memory; a thread holds 4 x 4 scores, then 4 rows of D / 16 outputs, a warp 8 rows (none of them
 // real: it computes nothing).  V of a tile lands beside its scores, K of the next one beside its
-// outputs.  Bound by the products (f32 fused multiply-adds) and what feeds them from shared memory.
+// outputs.  Bound by the products (f32 fused multiply-adds) and what feeds them from shared memory: 9 sequences of 15
+// rows per head in 2 groups behind 100 to 5000 tokens 33 us (46 with the copies between the products and all rows computed).
 #include "attn_shared.cuh"
 #include "tc_ptx.cuh"
 
@@ -60,10 +62,12 @@ __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
     auto place = [&](int j) {  // where the tokens of tile j lie
         if (tid < TT) {
             const int t = j * TT + tid, pg = t / a.page_size;
-            const int page = a.table[(int64_t)g.leader * a.max_pages + pg];
-            off_s[j & 1][tid] = page < 0 || page >= a.n_pages
-                                    ? -1
-                                    : (((int64_t)page * a.H_kv + g.h) * a.page_size + (t - pg * a.page_size)) * D;
+            int64_t at = -1;
+            if (g.len == 0 || t < g.len) {
+                const int page = a.table[(int64_t)g.leader * a.max_pages + pg];
+                if (page >= 0 && page < a.n_pages) at = (((int64_t)page * a.H_kv + g.h) * a.page_size + (t - pg * a.page_size)) * D;
+            }
+            off_s[j & 1][tid] = at;
         }
     };
     auto copy = [&](E* to, const void* from, int j) {  // a tile's rows, zeros where there is no page
@@ -90,6 +94,11 @@ __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
         __syncthreads();
         copy(k_s, a.k_cache, g.tile0);
         const bool works = (tid >> 5) * 8 < g.nr;  // the warp has real rows
+        // tokens that the rows see, and that the sequence's first new token does
+        const int least = g.len - (a.K - 1);
+        int vis[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vis[i] = g.len - (a.K - 1 - (g.r0 + 4 * ty + i) / a.group);
         float m[4], l[4];
         float2 o[4][NC];
 #pragma unroll
@@ -104,6 +113,7 @@ __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
             if (j + 1 < g.tile1) place(j + 1);
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncthreads();
+            const bool tail = g.len > 0 && j * TT + TT > least;
             // ---- scores of rows 4 ty .., tokens tx + 16 ..
             if (works) {
                 float2 acc[4][4];
@@ -134,6 +144,7 @@ __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
                         x[t] = (acc[i][t].x + acc[i][t].y) * a.scale_log2;
+                        if (tail && j * TT + tx + 16 * t >= vis[i]) x[t] = -INFINITY;
                         top = fmaxf(top, x[t]);
                     }
                     if (__any_sync(0xffffffffu, top > m[i] + kSlack)) {
@@ -161,18 +172,23 @@ __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncthreads();
             // ---- O += P V: rows 4 ty .., dims 2 tx + 32 ..
-            if (works) {
-#pragma unroll 4
-                for (int t = 0; t < TT; ++t) {
-                    const float4 p = ld4(p_s + t * PS + 4 * ty);
-                    const float w[4] = {p.x, p.y, p.z, p.w};
+            auto outputs = [&](int t, bool tails) {
+                const float4 p = ld4(p_s + t * PS + 4 * ty);
+                const float w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        const float2 v = ld2(v_s + t * KS + 32 * c + 2 * tx);
+                for (int c = 0; c < NC; ++c) {
+                    const float2 v = ld2(v_s + t * KS + 32 * c + 2 * tx);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) o[i][c] = __ffma2_rn(make_float2(w[i], w[i]), v, o[i][c]);
-                    }
+                    for (int i = 0; i < 4; ++i)  // a hidden value may be anything: a weight of 0 must not meet it
+                        if (!tails || j * TT + t < vis[i]) o[i][c] = __ffma2_rn(make_float2(w[i], w[i]), v, o[i][c]);
                 }
+            };
+            if (works && tail) {
+#pragma unroll 1
+                for (int t = 0; t < min(TT, g.len - j * TT); ++t) outputs(t, true);
+            } else if (works) {
+#pragma unroll 4
+                for (int t = 0; t < TT; ++t) outputs(t, false);
             }
             __syncthreads();
         }
@@ -188,8 +204,8 @@ __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
             float* po;
             if (g.parts > 0) {
                 const int64_t at = shared_row(a, g.seq0, g.h, g.r0 + r);
-                po = s.pre_o + at * D;
-                if (tx == 0) s.pre_stat[at] = part_stat(m[i], sum, g.parts, r);
+                po = (g.len > 0 ? a.part_o : s.pre_o) + at * D;
+                if (tx == 0) (g.len > 0 ? a.part_stat : s.pre_stat)[at] = part_stat(m[i], sum, g.parts, r);
             } else {
                 po = slot + 2 * ROWS + r * D;
                 if (tx == 0) {

@@ -137,29 +137,6 @@ __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
     if (tid == 0) s.rec[s.records].unit0 = before;
 }
 
-struct Running {
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    template <int U>
-    __device__ __forceinline__ void add(const float (&m1)[U], const float (&l1)[U], const float4 (&x)[U]) {
-        float top = m;
-#pragma unroll
-        for (int k = 0; k < U; ++k) top = fmaxf(top, m1[k]);
-        const float ref = top == -INFINITY ? 0.f : top;
-        const float f = tc::ex2_approx(m - ref);
-        m = top;
-        l *= f;
-        o.x *= f; o.y *= f; o.z *= f; o.w *= f;
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const float w = tc::ex2_approx(m1[k] - ref);
-            l = fmaf(l1[k], w, l);
-            o.x = fmaf(x[k].x, w, o.x); o.y = fmaf(x[k].y, w, o.y);
-            o.z = fmaf(x[k].z, w, o.z); o.w = fmaf(x[k].w, w, o.w);
-        }
-    }
-};
-
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 ld4(const bf16* p) {
     const uint2 u = *reinterpret_cast<const uint2*>(p);
@@ -282,7 +259,11 @@ size_t attn_share_plan(ShareArgs& s, gdn_dtype_t dt, void* ws) {
     AttnArgs& a = s.a;
     attn_plan(a, dt);
     const bool tc = attn_tc_takes(a, dt);
-    s.records = s.G + (tc ? a.B : 0);
+    // On CUDA cores what sequences with few rows have of their own is gdn_attn_decode's kernel's, which spreads a tile's
+    // tokens over all warps (us with records, with that kernel: 5 sequences of up to 900 tokens, 48 rows, head dim 16 21.8,
+    // 53.7; 9 of 15 rows, head dim 80, 41, 49; 13 of 10 rows, head dim 256, 63, 54).
+    const bool own = tc || a.rows > (a.D <= 128 ? kAttnFfmaRows : 2 * kAttnFfmaRows);
+    s.records = s.G + (own ? a.B : 0);
     s.rows_per_block = tc ? 128 : kPrefixFfmaRows;
     s.tile = tc ? 128 : 64;
     // What starting an item costs, in tiles (of half the MMAs up to head dim 128): its first scores and weights and its
@@ -298,7 +279,7 @@ size_t attn_share_plan(ShareArgs& s, gdn_dtype_t dt, void* ws) {
         at += up(bytes);
         return p;
     };
-    if (!tc) a.ws = reinterpret_cast<float*>(take(kAttnMaxCtas * (sizeof(JoinTask) + (size_t)a.slot_floats * sizeof(float))));
+    if (!own) a.ws = reinterpret_cast<float*>(take(kAttnMaxCtas * (sizeof(JoinTask) + (size_t)a.slot_floats * sizeof(float))));
     s.slots = reinterpret_cast<float*>(take(kAttnMaxCtas * (size_t)s.slot_floats * sizeof(float)));
     a.part_o = reinterpret_cast<float*>(take(rows * a.D * sizeof(float)));
     s.pre_o = reinterpret_cast<float*>(take(rows * a.D * sizeof(float)));
@@ -317,7 +298,7 @@ cudaError_t launch_attn_shared(const ShareArgs& s, gdn_dtype_t dt, cudaStream_t 
     const bool tc = attn_tc_takes(a, dt);
     cudaError_t e = launch_pdl(attn_share_plan_kernel, dim3(1), dim3(PT), 0, st, s);
     if (e == cudaSuccess) e = tc ? launch_shared_tc(s, n_cta, st) : launch_prefix_ffma(s, n_cta, dt, st);
-    if (e == cudaSuccess && !tc) e = launch_attn_ffma(a, n_cta, dt, st);
+    if (e == cudaSuccess && s.records == s.G) e = launch_attn_ffma(a, n_cta, dt, st);
     if (e != cudaSuccess) return e;
     return dt == GDN_BF16 ? launch_merge<bf16>(s, n_cta, st) : launch_merge<float>(s, n_cta, st);
 }

@@ -7,9 +7,9 @@
 // sequence has of its own is never empty; a group of one sequence shares nothing
 // (attn_share_plan_kernel).
 //
-// The work is a list of records: the groups' prefixes, and on tensor cores what each sequence has of
-// its own, as the tiles behind its prefix.  (On CUDA cores, whose time goes by the rows, the latter is
-// gdn_attn_decode's kernel from a.skip[b] on.)  Items are (record, key-value head, row block) with `setup` units and
+// The work is a list of records: the groups' prefixes, then what each sequence has of its own, as
+// the tiles behind its prefix.  (On CUDA cores, whose time goes by the rows, the latter is
+// gdn_attn_decode's kernel from a.skip[b] on where there are few.)  Items are (record, key-value head, row block) with `setup` units and
 // one per tile; all units are cut into equal ranges, one per CTA, as attn_common.cuh
 // does.  A row's first part of a record goes to its place in a.part_o or s.pre_o, with how many
 // CTAs' parts there are beside it, and a part that starts inside an item to the

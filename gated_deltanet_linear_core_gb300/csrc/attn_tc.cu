@@ -777,9 +777,8 @@ cudaError_t launch_rows(const AttnArgs& a, int n_cta, int piece, cudaStream_t s)
 
 bool attn_tc_takes(const AttnArgs& a, gdn_dtype_t dt) {
     // a lane loads one piece: 32 pieces of 4 tokens make a tile
-    return dt == GDN_BF16 && attn_tc_pages(a.page_size);
+    return dt == GDN_BF16 && page_piece(a.page_size) >= TILE / 32;
 }
-bool attn_tc_pages(int page_size) { return page_piece(page_size) >= TILE / 32; }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, int n_cta, cudaStream_t s) {
     const int piece = page_piece(a.page_size);

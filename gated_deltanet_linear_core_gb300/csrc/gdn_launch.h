@@ -188,7 +188,6 @@ cudaError_t launch_attn_ffma(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaS
 bool attn_tc_takes(const AttnArgs& a, gdn_dtype_t dt);
 cudaError_t launch_attn_tc(const AttnArgs& a, int n_cta, cudaStream_t s);
 cudaError_t read_and_clear_attn_error(cudaStream_t s, int* flags);
-bool attn_tc_pages(int page_size);  // page sizes that its loads take
 cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaStream_t s);
 
 // Attention behind shared prefixes (gdn_attn_decode_shared; attn_shared.cuh).
@@ -206,7 +205,7 @@ struct ShareArgs {
     AttnArgs a;                        // (its work division holds for what the sequences have of their own on CUDA cores)
     const int32_t *prefix, *cu;        // [G] tokens; [G + 1] sequences or null: one group
     int G;
-    int records;                       // G prefixes, on tensor cores then B sequences' own tokens
+    int records;                       // G prefixes, then (unless launch_attn_ffma takes them) B sequences' own tokens
     int rows_per_block, tile, setup;   // rows and tokens per tile, units of an item's start
     int* gather;                       // [3 G] scratch of the plan where there are many groups
     ShareRecord* rec;                  // [records + 1], the last one's unit0 all units

@@ -11,6 +11,9 @@
 // it copied itself): with loads into registers, four rows at a time, 32768 prompt tokens into the cache took
 // 163 us, in blocks with barriers as well.
 //
+// Measured: those 132 us (691 MB, 77 % of the copy bandwidth; 80 M warp instructions, 55 % of the issue slots), without
+// norm and rotation 121; 32760 patches of 16 heads of 80 out of a fused projection 37 us (168 MB, 66 %; issue).
+//
 // The angle of a far position keeps no digits in f32: p f is held in turns, as a 64-bit
 // fraction of one turn (f / 2 pi in f64, times 2^64), whose product with the integer p drops whole
 // turns by itself.  The fraction is off by at most |p f| 2^-52 / 2 pi turns; its upper 32

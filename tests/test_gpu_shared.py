@@ -102,6 +102,9 @@ CASES = [
     ([(260 + 8 * i, [1 + i % 3] * (1 + i % 5)) for i in range(70)], 1, 4, 2, 64, 8, True),
     ([(2600, [9] * 20)], 8, 24, 8, 128, 40, True),
     ([(5000, [2, 3, 4]), (7000, [1] * 30)], 1, 40, 8, 104, 48, False),
+    ([(300, [9, 40, 300]), (100, [500])], 8, 48, 8, 16, 100, True),
+    ([(520, [3, 70, 131])], 3, 3, 1, 8, 4, True),
+    ([(400, [16, 700, 64])], 16, 66, 2, 128, 32, True),
 ]
 
 
