@@ -279,7 +279,8 @@ size_t attn_share_plan(ShareArgs& s, gdn_dtype_t dt, void* ws) {
         at += up(bytes);
         return p;
     };
-    if (!own) a.ws = reinterpret_cast<float*>(take(kAttnMaxCtas * (sizeof(JoinTask) + (size_t)a.slot_floats * sizeof(float))));
+    if (!tc)  // (used or not, so that more rows never need less)
+        a.ws = reinterpret_cast<float*>(take(kAttnMaxCtas * (sizeof(JoinTask) + (size_t)a.slot_floats * sizeof(float))));
     s.slots = reinterpret_cast<float*>(take(kAttnMaxCtas * (size_t)s.slot_floats * sizeof(float)));
     a.part_o = reinterpret_cast<float*>(take(rows * a.D * sizeof(float)));
     s.pre_o = reinterpret_cast<float*>(take(rows * a.D * sizeof(float)));
