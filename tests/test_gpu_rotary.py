@@ -276,3 +276,33 @@ def test_caches_and_inputs_past_32_bits_of_elements():
     assert torch.equal(out, gdn.gdn_rope(q.contiguous(), freqs(D), place))
     assert torch.equal(kc[-1].transpose(0, 1)[126:], gdn.gdn_rope(k, freqs(D), place))
     assert torch.equal(vc[-1].transpose(0, 1)[126:], v) and not bool(kc[:-1].any())
+
+
+def test_append_with_queries_in_place():
+    q, k, v, kc, vc, table, ln, cu = append_inputs([900, 300], [700, 299], 6, 2, 128, 16, BF, 21, fused=False)
+    f, w = freqs(96), (1 + 0.1 * torch.randn(128, generator=torch.Generator().manual_seed(1))).cuda()
+    k2, v2 = kc.clone(), vc.clone()
+    want = gdn.gdn_rope_kv_append(q, k, v, k2, v2, table, ln, f, q_norm_w=w, cu_seqlens=cu)
+    got = gdn.gdn_rope_kv_append(q, k, v, kc, vc, table, ln, f, q_norm_w=w, cu_seqlens=cu, q_out=q)
+    assert got is q and torch.equal(q, want) and torch.equal(kc, k2) and torch.equal(vc, v2)
+
+
+@pytest.mark.parametrize("T", [4000, 12000, 20001])
+def test_prompts_of_many_tokens(T):
+    """More tokens than warps: several of a warp at once, the last ones fewer."""
+    x, f, pos, axes, w = inputs(T, 3, 64, 32, 3, BF, 22, "gated", True)
+    rot.check_rope(gdn.gdn_rope(x, f, pos, axes=axes, norm_w=w), rot.rope(x, f, pos, axes, w), BF)
+    rot.check_rope(gdn.gdn_rope(x, f, pos, axes=axes), rot.rope(x, f, pos, axes), BF)
+    a = append_inputs([T // 2, T], [T // 2, T - T // 2], 2, 1, 64, 16, BF, 23)
+    check_append(a, f, pos, axes, w, None, False, BF, a[7].tolist())
+
+
+def test_the_binding_refuses_what_does_not_fit():
+    x, f, pos, axes, w = inputs(9, 4, 64, 32, 3, BF, 24)
+    for bad, error in ((dict(positions=pos[:, :5]), ValueError), (dict(positions=pos.long()), TypeError),
+                       (dict(inv_freq=f[:7]), ValueError), (dict(inv_freq=f.double()), TypeError), (dict(axes=axes[:3]), ValueError),
+                       (dict(norm_w=x[0, 0].float()[:9]), ValueError), (dict(out=x.float()), TypeError), (dict(x=x.half()), TypeError),
+                       (dict(x=x[:, :, ::2]), ValueError), (dict(norm_w=torch.ones(64, device="cuda"), norm_eps=0.0), gdn.GDNError),
+                       (dict(out=x[:, :, :].transpose(0, 1).contiguous().transpose(0, 1)[:, :2]), ValueError)):
+        with pytest.raises(error):
+            gdn.gdn_rope(**dict(dict(x=x, inv_freq=f, positions=pos, axes=axes), **bad))

@@ -348,3 +348,62 @@ def test_more_sequences_and_groups_than_the_plan_holds_at_once(dtype):
     check(x)
     x = shared_inputs([(260, [1 + i % 7 if i % 11 else -1 for i in range(2100)])], 1, 2, 1, 16, 16, dtype, 14)
     check(x)
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("K,hq,hkv,D,page", [(1, 16, 2, 256, 16), (16, 16, 1, 64, 8), (3, 4, 4, 8, 4)])
+def test_one_sequence(dtype, K, hq, hkv, D, page):
+    for n in (K, 130, 1000):
+        check(shared_inputs([(500, [n])], K, hq, hkv, D, page, dtype, 40 + n, True))
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_a_query_that_is_not_finite_spoils_its_own_row(dtype):
+    x = shared_inputs([(700, [9, 300, 30])], 2, 8, 2, 64, 16, dtype, 41)
+    want = gdn.gdn_attn_decode_shared(**x)
+    x["q"][1, 0, 3, 5] = NAN
+    out = gdn.gdn_attn_decode_shared(**x)
+    assert bool(torch.isnan(out[1, 0, 3]).all())
+    out[1, 0, 3] = want[1, 0, 3]
+    assert torch.equal(out, want)
+
+
+def test_two_graphs_of_one_batch():
+    """Captured with workspaces of their own, replayed in turns and beside one another."""
+    x = shared_inputs([(2000, [40] * 12)], 1, 16, 2, 256, 16, BF, 42, True)
+    y = dict(x, q=x["q"].flip(0).contiguous(), gate=None)
+    want = [gdn.gdn_attn_decode_shared(**x), gdn.gdn_attn_decode_shared(**y)]
+    s, graphs, outs = torch.cuda.Stream(), [], []
+    s.wait_stream(torch.cuda.current_stream())
+    for z in (x, y):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+            outs.append(gdn.gdn_attn_decode_shared(**z))
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, o, w in zip(graphs, outs, want):
+            o.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, w)
+    other = torch.cuda.Stream()
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    graphs[0].replay()
+    with torch.cuda.stream(other):
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+def test_the_binding_refuses_what_does_not_fit():
+    x = shared_inputs([(300, [9, 30])], 1, 8, 2, 64, 16, BF, 43)
+    for bad, error in ((dict(cu_groups=None, prefix_lens=x["prefix_lens"].repeat(2)), ValueError),
+                       (dict(cu_groups=x["cu_groups"][:1]), ValueError), (dict(prefix_lens=x["prefix_lens"].view(1, 1)), ValueError),
+                       (dict(prefix_lens=x["prefix_lens"].long()), TypeError), (dict(q=x["q"][:1]), ValueError),
+                       (dict(gate=x["q"][:, :, :4]), ValueError), (dict(workspace=torch.empty(64, dtype=torch.uint8, device="cuda")),
+                                                                   gdn.GDNError), (dict(scale=-1.0), gdn.GDNError)):
+        with pytest.raises(error):
+            gdn.gdn_attn_decode_shared(**dict(x, **bad))
