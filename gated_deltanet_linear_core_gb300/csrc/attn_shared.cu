@@ -8,11 +8,11 @@ namespace {
 
 using namespace attn;
 
-constexpr int PT = 1024;  // threads of the plan
-static_assert(PT == 32 * 32, "block_scan");
-constexpr int MT = 256;   // threads of a merge block that takes several rows
+constexpr int kPlanThreads = 1024, kPlanFew = 128;  // threads of the plan, which strides over sequences and groups; of one with few of both
+constexpr int MT = 256;  // threads of a merge block that takes several rows
 
 // Sum of x over the block's threads before this one, and `total` over all.
+template <int PT>
 __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t& total) {
     __shared__ int64_t sums_s[PT / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -24,7 +24,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t& total) {
     }
     if (lane == 31) sums_s[warp] = inc;
     __syncthreads();
-    int64_t w = sums_s[lane];
+    int64_t w = lane < PT / 32 ? sums_s[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t v = __shfl_up_sync(0xffffffffu, w, o);
@@ -39,6 +39,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t& total) {
 // What every group shares in earnest, and the records, by one block.  Groups' least lengths, first
 // sequences and counts are gathered in shared memory, of many groups in the workspace.
 constexpr int kPlanGroups = 1024;  // groups in shared memory
+template <int PT>
 __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
     __shared__ int first_s[kPlanGroups + 1], least_s[kPlanGroups], leader_s[kPlanGroups], count_s[kPlanGroups];
     const AttnArgs& a = s.a;
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
             if (share > 0) units = (int64_t)rec.blocks * a.H_kv * (s.setup + rec.tiles);
             least[g] = share;  // from here on
         }
-        rec.unit0 = before + block_scan(units, total);
+        rec.unit0 = before + block_scan<PT>(units, total);
         before += total;
         if (g < s.G) s.rec[g] = rec;
     }
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
         rec.tile0 = share / s.tile;
         rec.tiles = n > 0 ? (n - 1) / s.tile + 1 - rec.tile0 : 0;
         if (n > 0) units = (int64_t)blocks * a.H_kv * (s.setup + rec.tiles);
-        rec.unit0 = before + block_scan(units, total);
+        rec.unit0 = before + block_scan<PT>(units, total);
         before += total;
         if (b < B) s.rec[s.G + b] = rec;
     }
@@ -297,7 +298,11 @@ cudaError_t launch_attn_shared(const ShareArgs& s, gdn_dtype_t dt, cudaStream_t 
     if (a.B == 0 || a.K == 0) return cudaSuccess;
     const int n_cta = attn_ctas();
     const bool tc = attn_tc_takes(a, dt);
-    cudaError_t e = launch_pdl(attn_share_plan_kernel, dim3(1), dim3(PT), 0, st, s);
+    // a small block starts and scans sooner: 4 sequences behind 1000 tokens 17.3 -> 16.4 us a call, with SharedWalk's
+    // first step
+    cudaError_t e = a.B <= kPlanFew && s.G <= kPlanFew
+                        ? launch_pdl(attn_share_plan_kernel<kPlanFew>, dim3(1), dim3(kPlanFew), 0, st, s)
+                        : launch_pdl(attn_share_plan_kernel<kPlanThreads>, dim3(1), dim3(kPlanThreads), 0, st, s);
     if (e == cudaSuccess) e = tc ? launch_shared_tc(s, n_cta, st) : launch_prefix_ffma(s, n_cta, dt, st);
     if (e == cudaSuccess && s.records == s.G) e = launch_attn_ffma(a, n_cta, dt, st);
     if (e != cudaSuccess) return e;

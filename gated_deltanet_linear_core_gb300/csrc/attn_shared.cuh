@@ -41,17 +41,22 @@ __device__ __forceinline__ int64_t shared_row(const AttnArgs& a, int seq0, int h
 struct SharedWalk {
     int64_t total, at, end, rec_end;
     ShareRecord rec;
-    int r, c, n;  // the record; the CTA, of how many that take part
-    __device__ __forceinline__ SharedWalk(const ShareArgs& s, int c_, int n_) : rec_end(0), r(0), c(c_), n(n_) {
+    int r, len;  // the record, its sequence's length (a prefix: 0)
+    int c, n;    // the CTA, of how many that take part
+    __device__ __forceinline__ SharedWalk(const ShareArgs& s, int c_, int n_) : rec_end(0), r(0), len(0), c(c_), n(n_) {
+        // (the first step of find() needs nothing but the records: its loads go out with the total's)
+        const int step = (s.records + 31) >> 5, i = (threadIdx.x & 31) * step;
+        const int64_t mine = i < s.records ? s.rec[i].unit0 : INT64_MAX;
         total = s.rec[s.records].unit0;
         if (n > total) n = (int)total;
         at = c < n ? cta_begin(total, c, n) : 0;
         end = c < n ? cta_begin(total, c + 1, n) : 0;
+        r = (31 - __clz(__ballot_sync(0xffffffffu, mine <= at) | 1)) * step;
+        if (at < end) find(s, min(s.records, r + step));
     }
-    // The last record that starts at or before unit `at`, from record r on: 32 at a time.
-    __device__ __forceinline__ void find(const ShareArgs& s) {
+    // The last record before `hi` that starts at or before unit `at`, from record r on: 32 at a time.
+    __device__ __forceinline__ void find(const ShareArgs& s, int hi) {
         const int lane = threadIdx.x & 31;
-        int hi = s.records;
         while (hi - r > 1) {
             const int step = (hi - r + 31) >> 5, i = r + lane * step;
             const uint32_t past = __ballot_sync(0xffffffffu, i < hi && s.rec[i].unit0 <= at);
@@ -60,10 +65,11 @@ struct SharedWalk {
         }
         rec = s.rec[r];
         rec_end = s.rec[r + 1].unit0;
+        len = r < s.G ? 0 : clamped_len(s.a, r - s.G);
     }
     __device__ __forceinline__ bool next(const ShareArgs& s, SharedSegment& g) {
         while (at < end) {
-            if (at >= rec_end) find(s);
+            if (at >= rec_end) find(s, s.records);
             const int units = s.setup + rec.tiles;
             const int64_t off = at - rec.unit0;
             const int64_t item = off / units;
@@ -82,7 +88,7 @@ struct SharedWalk {
             g.leader = rec.leader;
             g.r0 = (int)(item - (int64_t)g.h * rec.blocks) * s.rows_per_block;
             g.nr = min(s.rows_per_block, rec.seqs * s.a.rows - g.r0);
-            g.len = r < s.G ? 0 : clamped_len(s.a, rec.leader);
+            g.len = len;
             return true;
         }
         return false;

@@ -407,3 +407,11 @@ def test_the_binding_refuses_what_does_not_fit():
                                                                    gdn.GDNError), (dict(scale=-1.0), gdn.GDNError)):
         with pytest.raises(error):
             gdn.gdn_attn_decode_shared(**dict(x, **bad))
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B", [127, 128, 129])
+def test_as_many_sequences_as_a_small_plan_takes(B, dtype):
+    """Three sequences to a group; 43 groups, the last of what is left."""
+    own = [[1 + (3 * i + j) % 20 for j in range(min(3, B - 3 * i))] for i in range(43)]
+    check(shared_inputs([(128 if i % 2 == 0 else 40, n) for i, n in enumerate(own)], 1, 4, 2, 64, 16, dtype, B))
