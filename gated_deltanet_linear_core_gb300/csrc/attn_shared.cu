@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
     const int B = a.B;
     pdl_wait();
     pdl_trigger();
-    int len0 = tid < B ? clamped_len(a, tid) : 0;  // of the first round's sequence
+    int len0 = tid < B ? clamped_len(a, tid) : 0;  // of the first sequence of the thread
     const int prefix0 = tid < s.G ? s.prefix[tid] : 0;
     for (int g = tid; g <= s.G; g += PT) {
         if (g < s.G) {

@@ -11,8 +11,9 @@
 // it copied itself): with loads into registers, four rows at a time, 32768 prompt tokens into the cache took
 // 163 us, in blocks with barriers as well.
 //
-// Measured: those 132 us (691 MB, 77 % of the copy bandwidth; 80 M warp instructions, 55 % of the issue slots), without
-// norm and rotation 121; 32760 patches of 16 heads of 80 out of a fused projection 37 us (168 MB, 66 %; issue).
+// Measured: those 121 us (691 MB, 84 % of the copy bandwidth; 76 M warp instructions; 131 with batches of tokens dealt to the
+// warps in turns, of which some got one more); 32760 patches of 16 heads of 80 out of a fused projection 34 us (168 MB,
+// 72 %; issue: 18 M warp instructions, 25 M and 37 us with the cache's part in the same code).
 //
 // The angle of a far position keeps no digits in f32: p f is held in turns, as a 64-bit
 // fraction of one turn (f / 2 pi in f64, times 2^64), whose product with the integer p drops whole
@@ -118,10 +119,10 @@ __device__ __forceinline__ bool find_token(const RopeArgs& a, int64_t t, int& b,
 }
 
 // V pairs per item, IT items per lane; NEIGHBOURS: pairs (2j, 2j + 1), else (j, j + R / 2).
-// `lg` lanes take a row (a power of two where a norm adds up over them), `tb` tokens at once or `parts` warps for a
-// token's rows: those of its query heads, key heads and value heads.  (One loop for the three, whose sources and places are picked per
+// `lg` lanes take a row (a power of two where a norm adds up over them), a warp `tb` tokens at once or one of `parts`
+// shares of a token's rows: those of its query heads, key heads and value heads.  (One loop for the three, whose sources and places are picked per
 // row: with a loop for each, a small call waited for its code, 320 tokens 17.8 us.)
-template <typename E, int V, int IT, bool NEIGHBOURS, bool NORM>
+template <typename E, int V, int IT, bool NEIGHBOURS, bool NORM, bool CACHE>
 __global__ void __launch_bounds__(NT, NORM ? 4 : 5) rope_kernel(RopeArgs a, int lg, int tb, int parts) {
     extern __shared__ __align__(16) float sm[];
     const int half = a.R >> 1, tid = threadIdx.x, warp = tid >> 5;
@@ -174,24 +175,29 @@ __global__ void __launch_bounds__(NT, NORM ? 4 : 5) rope_kernel(RopeArgs a, int 
         }
     }
     const int64_t cache_head = (int64_t)a.page_size * a.D;
-    const int step = parts * rw, kinds = a.k_cache != nullptr ? 3 : 1;
-    const int64_t all = (a.T + tb - 1) / tb * parts, stride = (int64_t)gridDim.x * NW;
-    auto split = [&](int64_t item, int64_t& token, int& h) {  // an item's first token and this lane's first head
-        const int64_t batch = parts == 1 ? item : (uint32_t)item / (uint32_t)parts;  // several parts: few tokens
-        token = batch * tb;
-        h = (int)(item - batch * parts) * rw + grp;
+    const int step = parts * rw;
+    constexpr int kinds = CACHE ? 3 : 1;
+    // the warp's items, shares of tokens: equal ranges, so that all warps end together
+    const uint32_t all = (uint32_t)(a.T * parts), warps = gridDim.x * NW, nth = blockIdx.x * NW + warp;  // T < 2^31
+    const uint32_t each = all / warps, more = all - each * warps;  // (several parts: few tokens)
+    const int64_t item0 = (int64_t)nth * each + min(nth, more), item1 = item0 + each + (nth < more ? 1 : 0);
+    auto split = [&](int64_t item, int64_t& token, int& h) {  // an item's token and this lane's first head
+        token = parts == 1 ? item : (uint32_t)item / (uint32_t)parts;  // several parts: few tokens
+        h = (int)(item - token * parts) * rw + grp;
     };
+    auto batch = [&](int64_t item) { return parts == 1 ? (int)min((int64_t)tb, item1 - item) : 1; };  // tokens at once
     // the rows, those of an item's queries, keys and values after one another, kStages ahead
     struct {
-        int64_t item, token, upto, skip;  // an item's tokens, elements between a lane's rows
+        int64_t item, token, skip;  // an item, its token, elements between a lane's rows
         const E* x;
         int h0, h, heads, kind, stage;
     } in;
-    in.item = (int64_t)blockIdx.x * NW + warp;
+    in.item = item0;
     in.stage = 0;
     auto enter = [&](int kind) {  // the token's rows of a kind
         in.kind = kind;
         in.h = in.h0;
+        if (!CACHE) kind = 0;
         in.heads = kind == 0 ? a.H_q : a.H_kv;
         const int64_t tok = kind == 0 ? a.q_tok : kind == 1 ? a.k_tok : a.v_tok;
         const int64_t head = kind == 0 ? a.q_head : kind == 1 ? a.k_head : a.v_head;
@@ -199,14 +205,13 @@ __global__ void __launch_bounds__(NT, NORM ? 4 : 5) rope_kernel(RopeArgs a, int 
         in.skip = step * head;
     };
     auto begin = [&] {
-        if (in.item >= all) return;
+        if (in.item >= item1) return;
         split(in.item, in.token, in.h0);
-        in.upto = min(in.token + tb, a.T);
         enter(0);
     };
     begin();
     auto fetch = [&] {
-        if (in.item < all) {
+        if (in.item < item1) {
             if (in.h < in.heads)
 #pragma unroll
                 for (int i = 0; i < IT; ++i)
@@ -217,12 +222,10 @@ __global__ void __launch_bounds__(NT, NORM ? 4 : 5) rope_kernel(RopeArgs a, int 
             in.h += step;
             in.x += in.skip;
             if (in.h - grp >= in.heads) {  // (the lanes of a warp go on together)
-                if (in.kind + 1 < kinds) {
+                if (CACHE && in.kind + 1 < kinds) {
                     enter(in.kind + 1);
-                } else if (++in.token < in.upto) {
-                    enter(0);
                 } else {
-                    in.item += stride;
+                    ++in.item;
                     begin();
                 }
             }
@@ -235,15 +238,16 @@ __global__ void __launch_bounds__(NT, NORM ? 4 : 5) rope_kernel(RopeArgs a, int 
     int stage = 0;
     const float inv_d = 1.0f / (float)a.D;
     const uint32_t per_half = (65536 + half - 1) / half;  // e / half = e per_half / 65536 for e < 65536 / half
-    for (int64_t item = (int64_t)blockIdx.x * NW + warp; item < all; item += stride) {
+    for (int64_t item = item0; item < item1;) {
         int64_t first;
         int h0;
         split(item, first, h0);
-        const int n = (int)min((int64_t)tb, a.T - first);
+        const int n = batch(item);
+        item += n;
         // lane i: token i's place in its sequence, and its row (page, head 0, position in page), -1: nowhere
         int64_t its_row = -1, its_pos = 0;
         bool its_member = true;
-        if (a.k_cache != nullptr && wl < n) {
+        if (CACHE && wl < n) {
             int b;
             its_member = find_token(a, first + wl, b, its_pos);
             if (its_member && its_pos >= 0 && its_pos < (int64_t)a.max_pages * a.page_size) {
@@ -256,7 +260,7 @@ __global__ void __launch_bounds__(NT, NORM ? 4 : 5) rope_kernel(RopeArgs a, int 
         __syncwarp();  // the cosines before are read
         for (int e0 = 0; e0 < n * half; e0 += 32) {
             const int e = e0 + wl, t = min((int)((uint32_t)e * per_half >> 16), n - 1), j = e - t * half;
-            int64_t p = __shfl_sync(0xffffffffu, its_pos, t);
+            int64_t p = CACHE ? __shfl_sync(0xffffffffu, its_pos, t) : 0;
             if (e < n * half) {
                 const int ax = axis_s[j];
                 if (a.positions != nullptr) p = ax >= 0 ? a.positions[ax * a.T + first + t] : 0;
@@ -270,8 +274,8 @@ __global__ void __launch_bounds__(NT, NORM ? 4 : 5) rope_kernel(RopeArgs a, int 
         __syncwarp();
 #pragma unroll 1
         for (int t = 0; t < n; ++t) {
-        const int64_t token = first + t, row = __shfl_sync(0xffffffffu, its_row, t);
-        const bool member = __shfl_sync(0xffffffffu, (int)its_member, t) != 0;
+        const int64_t token = first + t, row = CACHE ? __shfl_sync(0xffffffffu, its_row, t) : -1;
+        const bool member = !CACHE || __shfl_sync(0xffffffffu, (int)its_member, t) != 0;
         float co[IT][V], si[IT][V];
 #pragma unroll
         for (int i = 0; i < IT; ++i)
@@ -387,12 +391,15 @@ cudaError_t launch_v(const RopeArgs& a, cudaStream_t s) {
     parts = parts < 1 ? 1 : (parts > most ? most : parts);
     const bool norm = a.q_w != nullptr || a.k_w != nullptr;
     const int ctas = 152 * (norm ? 4 : 5);  // resident at once: registers
-    const int tb = a.T < ctas * NW * kTokens ? 1 : kTokens;
-    int64_t blocks = ((a.T + tb - 1) / tb * parts + NW - 1) / NW;
+    const int64_t each = (a.T + ctas * NW - 1) / (ctas * NW);  // tokens of a warp
+    const int tb = (int)(each < kTokens ? each : kTokens);
+    int64_t blocks = (a.T * parts + NW - 1) / NW;
     blocks = blocks > ctas ? ctas : blocks;
     const size_t smem = sizeof(float) * (((4 * half + 3) & ~3) + 2 * a.D + NW * 2 * tb * half) +
                         (size_t)NW * kStages * IT * 64 * V * sizeof(E);
-    const auto kernel = norm ? rope_kernel<E, V, IT, NEIGHBOURS, true> : rope_kernel<E, V, IT, NEIGHBOURS, false>;
+    const auto kernel = a.k_cache != nullptr
+                            ? (norm ? rope_kernel<E, V, IT, NEIGHBOURS, true, true> : rope_kernel<E, V, IT, NEIGHBOURS, false, true>)
+                            : (norm ? rope_kernel<E, V, IT, NEIGHBOURS, true, false> : rope_kernel<E, V, IT, NEIGHBOURS, false, false>);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3((unsigned)blocks), dim3(NT), smem, s, a, lg, tb, (int)parts);
