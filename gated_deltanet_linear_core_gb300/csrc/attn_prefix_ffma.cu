@@ -41,7 +41,7 @@ struct Tiles {
     static constexpr int BYTES = 4 * (ROWS * QS + TT * PS) + 2 * TT * KS * (int)sizeof(E);
 };
 
-template <typename E, int NC>
+template <typename E, int NC, bool FEW>
 __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
     using T = Tiles<E, NC>;
     constexpr int QS = T::QS, KS = T::KS;
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
     const int D = a.D, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     pdl_wait();
     pdl_trigger();
-    SharedWalk walk(s, blockIdx.x, gridDim.x);
+    SharedWalk<FEW> walk(s, blockIdx.x, gridDim.x);
     SharedSegment g;
     const int fours = D / 4, chunks = D * (int)sizeof(E) / 16;
     for (int i = tid; i < T::BYTES / 4; i += NT) sm[i] = 0.f;  // dims from D on stay zero
@@ -220,26 +220,27 @@ __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
     }
 }
 
-template <typename E, int NC>
+template <typename E, int NC, bool FEW>
 cudaError_t launch_nc(const ShareArgs& s, int n_cta, cudaStream_t st) {
     constexpr int smem = Tiles<E, NC>::BYTES;
-    const cudaError_t e = cudaFuncSetAttribute(attn_prefix_ffma_kernel<E, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(attn_prefix_ffma_kernel<E, NC, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_prefix_ffma_kernel<E, NC>, dim3((unsigned)n_cta), dim3(NT), smem, st, s);
+    return launch_pdl(attn_prefix_ffma_kernel<E, NC, FEW>, dim3((unsigned)n_cta), dim3(NT), smem, st, s);
 }
-template <typename E>
+template <typename E, bool FEW>
 cudaError_t launch_e(const ShareArgs& s, int n_cta, cudaStream_t st) {
     const int D = s.a.D;
-    if (D <= 64) return launch_nc<E, 2>(s, n_cta, st);
-    if (D <= 96) return launch_nc<E, 3>(s, n_cta, st);
-    if (D <= 128) return launch_nc<E, 4>(s, n_cta, st);
-    return D <= 192 ? launch_nc<E, 6>(s, n_cta, st) : launch_nc<E, 8>(s, n_cta, st);
+    if (D <= 64) return launch_nc<E, 2, FEW>(s, n_cta, st);
+    if (D <= 96) return launch_nc<E, 3, FEW>(s, n_cta, st);
+    if (D <= 128) return launch_nc<E, 4, FEW>(s, n_cta, st);
+    return D <= 192 ? launch_nc<E, 6, FEW>(s, n_cta, st) : launch_nc<E, 8, FEW>(s, n_cta, st);
 }
 
 }  // namespace
 
 cudaError_t launch_prefix_ffma(const ShareArgs& s, int n_cta, gdn_dtype_t dt, cudaStream_t st) {
-    return dt == GDN_BF16 ? launch_e<bf16>(s, n_cta, st) : launch_e<float>(s, n_cta, st);
+    if (s.few) return dt == GDN_BF16 ? launch_e<bf16, true>(s, n_cta, st) : launch_e<float, true>(s, n_cta, st);
+    return dt == GDN_BF16 ? launch_e<bf16, false>(s, n_cta, st) : launch_e<float, false>(s, n_cta, st);
 }
 
 }  // namespace gdn

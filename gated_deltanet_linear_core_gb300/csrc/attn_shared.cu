@@ -39,6 +39,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t& total) {
 // What every group shares in earnest, and the records, by one block.  Groups' least lengths, first
 // sequences and counts are gathered in shared memory, of many groups in the workspace.
 constexpr int kPlanGroups = 1024;  // groups in shared memory
+constexpr int kFewGroups = 8;  // groups that SharedWalk looks at one after another
 template <int PT>
 __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
     __shared__ int first_s[kPlanGroups + 1], least_s[kPlanGroups], leader_s[kPlanGroups], count_s[kPlanGroups];
@@ -58,10 +59,10 @@ __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
             least[g] = leader[g] = INT32_MAX;
             count[g] = 0;
         }
-        if (few) first_s[g] = s.cu != nullptr ? min(max(s.cu[g], 0), B) : g * B;
+        if (few) first_s[g] = group_begin(s, g);
     }
     __syncthreads();
-    auto first = [&](int g) -> int { return few ? first_s[g] : s.cu != nullptr ? min(max(s.cu[g], 0), B) : g * B; };
+    auto first = [&](int g) -> int { return few ? first_s[g] : group_begin(s, g); };
     auto group_of = [&](int b) -> int {  // -1: none
         int lo = 0, hi = s.G - 1;        // the last group that starts at or before the sequence
         while (lo < hi) {
@@ -100,15 +101,8 @@ __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
         ShareRecord rec = {};
         int64_t units = 0;
         if (g < s.G) {
-            rec.seq0 = first(g);
-            rec.seqs = max(first(g + 1) - rec.seq0, 0);
-            rec.blocks = (int)(((int64_t)rec.seqs * a.rows + s.rows_per_block - 1) / s.rows_per_block);
-            // less than the first new token of any sequence sees
-            int share = count[g] > 1 ? min(g0 == 0 ? prefix0 : s.prefix[g], least[g] - a.K) : 0;
-            share = share > 0 ? share / kShareStep * kShareStep : 0;
-            rec.tiles = share / s.tile;
-            rec.leader = count[g] > 0 ? leader[g] : 0;
-            if (share > 0) units = (int64_t)rec.blocks * a.H_kv * (s.setup + rec.tiles);
+            const int share = shared_tokens(a, g0 == 0 ? prefix0 : s.prefix[g], count[g], least[g]);
+            units = prefix_record(s, rec, first(g), first(g + 1), count[g] > 0 ? leader[g] : 0, share);
             least[g] = share;  // from here on
         }
         rec.unit0 = before + block_scan<PT>(units, total);
@@ -116,7 +110,6 @@ __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
         if (g < s.G) s.rec[g] = rec;
     }
     int32_t* skip = const_cast<int32_t*>(a.skip);
-    const int blocks = (a.rows + s.rows_per_block - 1) / s.rows_per_block;
     for (int b0 = 0; b0 < B; b0 += PT) {
         const int b = b0 + tid;
         const int n = b0 == 0 ? len0 : b < B ? clamped_len(a, b) : 0, g = b0 == 0 ? group0 : b < B ? group_of(b) : -1;
@@ -124,13 +117,7 @@ __global__ void __launch_bounds__(PT) attn_share_plan_kernel(ShareArgs s) {
         if (b < B) skip[b] = share;
         if (s.records == s.G) continue;
         ShareRecord rec = {};
-        int64_t units = 0;
-        rec.seq0 = rec.leader = b;
-        rec.seqs = 1;
-        rec.blocks = blocks;
-        rec.tile0 = share / s.tile;
-        rec.tiles = n > 0 ? (n - 1) / s.tile + 1 - rec.tile0 : 0;
-        if (n > 0) units = (int64_t)blocks * a.H_kv * (s.setup + rec.tiles);
+        const int64_t units = own_record(s, rec, b, n, share);
         rec.unit0 = before + block_scan<PT>(units, total);
         before += total;
         if (b < B) s.rec[s.G + b] = rec;
@@ -265,6 +252,7 @@ size_t attn_share_plan(ShareArgs& s, gdn_dtype_t dt, void* ws) {
     // 53.7; 9 of 15 rows, head dim 80, 41, 49; 13 of 10 rows, head dim 256, 63, 54).
     const bool own = tc || a.rows > (a.D <= 128 ? kAttnFfmaRows : 2 * kAttnFfmaRows);
     s.records = s.G + (own ? a.B : 0);
+    s.few = a.B + s.G <= 32 && s.G <= kFewGroups;
     s.rows_per_block = tc ? 128 : kPrefixFfmaRows;
     s.tile = tc ? 128 : 64;
     // What starting an item costs, in tiles (of half the MMAs up to head dim 128): its first scores and weights and its
@@ -298,9 +286,9 @@ cudaError_t launch_attn_shared(const ShareArgs& s, gdn_dtype_t dt, cudaStream_t 
     if (a.B == 0 || a.K == 0) return cudaSuccess;
     const int n_cta = attn_ctas();
     const bool tc = attn_tc_takes(a, dt);
-    // a small block starts and scans sooner: 4 sequences behind 1000 tokens 17.3 -> 16.4 us a call, with SharedWalk's
-    // first step
-    cudaError_t e = a.B <= kPlanFew && s.G <= kPlanFew
+    // (a small block starts and scans sooner: 1 us)
+    cudaError_t e = s.few ? cudaSuccess
+                    : a.B <= kPlanFew && s.G <= kPlanFew
                         ? launch_pdl(attn_share_plan_kernel<kPlanFew>, dim3(1), dim3(kPlanFew), 0, st, s)
                         : launch_pdl(attn_share_plan_kernel<kPlanThreads>, dim3(1), dim3(kPlanThreads), 0, st, s);
     if (e == cudaSuccess) e = tc ? launch_shared_tc(s, n_cta, st) : launch_prefix_ffma(s, n_cta, dt, st);

@@ -136,7 +136,7 @@ __device__ __forceinline__ bool pair_any(int quad, bool x) {
     return r != 0;
 }
 
-template <int NDB>
+template <int NDB, bool FEW>
 __global__ void __launch_bounds__(NT, 1)
 attn_shared_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, ShareArgs s,
                       int piece) {
@@ -267,7 +267,7 @@ attn_shared_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
 
     if (warp == 0) {
         // ------------------------------------------------ the walk; K and V, lower slabs
-        SharedWalk walk(s, blockIdx.x, gridDim.x);
+        SharedWalk<FEW> walk(s, blockIdx.x, gridDim.x);
         bool ok = true, more = true;
         while (ok && more) {
             g.tile0 = g.tile1 = 0;
@@ -636,21 +636,22 @@ attn_shared_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     }
 }
 
-template <int NDB>
+template <int NDB, bool FEW>
 cudaError_t launch_ndb(const ShareArgs& s, int n_cta, int piece, cudaStream_t st) {
     using L = Layout<NDB>;
     CUtensorMap km, vm;
     if (!encode_cache(&km, s.a.k_cache, s.a, piece) || !encode_cache(&vm, s.a.v_cache, s.a, piece)) return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(attn_shared_tc_kernel<NDB>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(attn_shared_tc_kernel<NDB, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_shared_tc_kernel<NDB>, dim3((unsigned)n_cta), dim3(NT), L::SMEM, st, km, vm, s, piece);
+    return launch_pdl(attn_shared_tc_kernel<NDB, FEW>, dim3((unsigned)n_cta), dim3(NT), L::SMEM, st, km, vm, s, piece);
 }
 
 }  // namespace
 
 cudaError_t launch_shared_tc(const ShareArgs& s, int n_cta, cudaStream_t st) {
     const int piece = page_piece(s.a.page_size);
-    return s.a.D <= 128 ? launch_ndb<1>(s, n_cta, piece, st) : launch_ndb<2>(s, n_cta, piece, st);
+    if (s.few) return s.a.D <= 128 ? launch_ndb<1, true>(s, n_cta, piece, st) : launch_ndb<2, true>(s, n_cta, piece, st);
+    return s.a.D <= 128 ? launch_ndb<1, false>(s, n_cta, piece, st) : launch_ndb<2, false>(s, n_cta, piece, st);
 }
 
 cudaError_t read_and_clear_shared_error(cudaStream_t s, int* flags) {

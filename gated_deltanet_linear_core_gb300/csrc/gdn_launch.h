@@ -206,6 +206,7 @@ struct ShareArgs {
     const int32_t *prefix, *cu;        // [G] tokens; [G + 1] sequences or null: one group
     int G;
     int records;                       // G prefixes, then (unless launch_attn_ffma takes them) B sequences' own tokens
+    int few;                           // a lane of a warp can hold each: every CTA makes the records for itself
     int rows_per_block, tile, setup;   // rows and tokens per tile, units of an item's start
     int* gather;                       // [3 G] scratch of the plan where there are many groups
     ShareRecord* rec;                  // [records + 1], the last one's unit0 all units

@@ -415,3 +415,19 @@ def test_as_many_sequences_as_a_small_plan_takes(B, dtype):
     """Three sequences to a group; 43 groups, the last of what is left."""
     own = [[1 + (3 * i + j) % 20 for j in range(min(3, B - 3 * i))] for i in range(43)]
     check(shared_inputs([(128 if i % 2 == 0 else 40, n) for i, n in enumerate(own)], 1, 4, 2, 64, 16, dtype, B))
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("i", range(len(CASES)))
+def test_padded_batches(i, dtype):
+    """The same with 32 empty sequences behind them, which make even a small batch one with a plan kernel; padded and
+    unpadded results are the same up to the order of their sums."""
+    groups, K, hq, hkv, D, page, gate = CASES[i]
+    check(shared_inputs(groups + [(0, [-1] * 32)], K, hq, hkv, D, page, dtype, 900 + i, gate))
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("G,B", [(1, 31), (1, 32), (7, 24), (8, 24), (8, 25), (9, 23), (9, 9), (31, 1), (8, 3)])
+def test_as_many_groups_and_sequences_as_a_warp_plans(G, B, dtype):
+    own = [[1 + (5 * g + j) % 30 for j in range((B * (g + 1)) // G - B * g // G)] for g in range(G)]
+    check(shared_inputs([(150 + 100 * (g % 3), n) for g, n in enumerate(own)], 2, 8, 2, 64, 16, dtype, 70 + G, True))
