@@ -8,7 +8,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int kPlanThreads = 1024, kPlanFew = 128;  // threads of the plan, which strides over sequences and groups; of one with few of both
+constexpr int kPlanThreads = 1024, kPlanFew = 128;  // threads of the plan; where there are at most 128 sequences and groups
 constexpr int MT = 256;  // threads of a merge block that takes several rows
 
 // Sum of x over the block's threads before this one, and `total` over all.

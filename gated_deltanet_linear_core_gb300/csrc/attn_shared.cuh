@@ -9,9 +9,9 @@
 //
 // The work is a list of records: the groups' prefixes, then what each sequence has of its own, as
 // the tiles behind its prefix.  (On CUDA cores, whose time goes by the rows, the latter is
-// gdn_attn_decode's kernel from a.skip[b] on where there are few.)  Items are (record, key-value head, row block) with `setup` units and
-// one per tile; all units are cut into equal ranges, one per CTA, as attn_common.cuh
-// does.  A row's first part of a record goes to its place in a.part_o or s.pre_o, with how many
+// gdn_attn_decode's kernel from a.skip[b] on where there are few.)  Items are (record, key-value
+// head, row block) with `setup` units and one per tile; all units are cut into equal ranges, one per
+// CTA, as attn_common.cuh does.  A row's first part of a record goes to its place in a.part_o or s.pre_o, with how many
 // CTAs' parts there are beside it, and a part that starts inside an item to the
 // CTA's one slot; attn_merge_kernel puts them together.
 #pragma once
@@ -49,7 +49,8 @@ __device__ __forceinline__ int64_t size_record(const ShareArgs& s, ShareRecord& 
     return rec.tiles > 0 ? (int64_t)rec.blocks * s.a.H_kv * (s.setup + rec.tiles) : 0;
 }
 // The record of a group's prefix, of what sequence b has of its own; their units.
-__device__ __forceinline__ int64_t prefix_record(const ShareArgs& s, ShareRecord& rec, int first, int behind, int leader, int share) {
+__device__ __forceinline__ int64_t prefix_record(const ShareArgs& s, ShareRecord& rec, int first, int behind, int leader,
+                                                 int share) {
     rec.seq0 = first;
     rec.seqs = max(behind - first, 0);
     rec.leader = leader;
@@ -78,7 +79,8 @@ struct SharedWalk {
     int c, n;    // the CTA, of how many that take part
     ShareRecord its;  // few: the lane's record, its sequence's length
     int its_len;
-    __device__ __forceinline__ SharedWalk(const ShareArgs& s, int c_, int n_) : rec_end(0), r(0), len(0), c(c_), n(n_), its_len(0) {
+    __device__ __forceinline__ SharedWalk(const ShareArgs& s, int c_, int n_)
+        : rec_end(0), r(0), len(0), c(c_), n(n_), its_len(0) {
         if (FEW) {
             plan(s);
             if (n > total) n = (int)total;
@@ -98,7 +100,9 @@ struct SharedWalk {
         if (at < end) find(s, min(s.records, r + step));
     }
     // The plan where there are few groups and sequences: lane g has group g, lane G + b sequence b.  (us a call with the
-    // plan in a kernel before this one, and here: 4 sequences behind 1000 tokens 16.4, 14.3; 8 behind 262000 95.7, 92.5.)  CTA 0 tells the kernels behind it what the sequences share.
+    // plan in a kernel before this one, and here: 4 sequences behind 1000 tokens 16.4, 14.3; 8 behind 262000 95.7, 92.5.
+    // With three records to a lane it took as long as that kernel: 64 sequences 63.5, 63.6.)  CTA 0 tells the kernels
+    // behind this one what the sequences share.
     __device__ __forceinline__ void plan(const ShareArgs& s) {
         const AttnArgs& a = s.a;
         const int lane = threadIdx.x & 31, b = lane - s.G;

@@ -29,7 +29,7 @@ namespace {
 constexpr int NT = 128;
 constexpr int NW = NT / 32;
 constexpr int kStages = 4;
-constexpr int kTokens = 4;  // of a warp at once, where there are many (one by one, looking up and the cosines took two thirds of the time)
+constexpr int kTokens = 4;  // of a warp at once (one by one, looking up and the cosines took two thirds of the time)
 
 template <int BYTES> struct RawOf;
 template <> struct RawOf<16> { using type = uint4; };
@@ -120,8 +120,8 @@ __device__ __forceinline__ bool find_token(const RopeArgs& a, int64_t t, int& b,
 
 // V pairs per item, IT items per lane; NEIGHBOURS: pairs (2j, 2j + 1), else (j, j + R / 2).
 // `lg` lanes take a row (a power of two where a norm adds up over them), a warp `tb` tokens at once or one of `parts`
-// shares of a token's rows: those of its query heads, key heads and value heads.  (One loop for the three, whose sources and places are picked per
-// row: with a loop for each, a small call waited for its code, 320 tokens 17.8 us.)
+// shares of a token's rows: those of its query heads, key heads and value heads.  (One loop for the three, whose sources
+// and places are picked per row: with a loop for each, a small call waited for its code, 320 tokens 17.8 us.)
 template <typename E, int V, int IT, bool NEIGHBOURS, bool NORM, bool CACHE>
 __global__ void __launch_bounds__(NT, NORM ? 4 : 5) rope_kernel(RopeArgs a, int lg, int tb, int parts) {
     extern __shared__ __align__(16) float sm[];

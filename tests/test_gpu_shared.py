@@ -419,15 +419,16 @@ def test_as_many_sequences_as_a_small_plan_takes(B, dtype):
 
 @pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
 @pytest.mark.parametrize("i", range(len(CASES)))
-def test_padded_batches(i, dtype):
-    """The same with 32 empty sequences behind them, which make even a small batch one with a plan kernel; padded and
-    unpadded results are the same up to the order of their sums."""
+@pytest.mark.parametrize("more", [32, 96])
+def test_padded_batches(more, i, dtype):
+    """The same with empty sequences behind them: batches of other sizes are planned in other ways."""
     groups, K, hq, hkv, D, page, gate = CASES[i]
-    check(shared_inputs(groups + [(0, [-1] * 32)], K, hq, hkv, D, page, dtype, 900 + i, gate))
+    check(shared_inputs(groups + [(0, [-1] * more)], K, hq, hkv, D, page, dtype, 900 + i, gate))
 
 
 @pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
-@pytest.mark.parametrize("G,B", [(1, 31), (1, 32), (7, 24), (8, 24), (8, 25), (9, 23), (9, 9), (31, 1), (8, 3)])
+@pytest.mark.parametrize("G,B", [(1, 31), (1, 32), (7, 24), (8, 24), (8, 25), (9, 23), (9, 9), (31, 1), (8, 3), (3, 62),
+                                  (2, 63), (1, 95), (1, 96), (8, 88), (8, 89)])
 def test_as_many_groups_and_sequences_as_a_warp_plans(G, B, dtype):
     own = [[1 + (5 * g + j) % 30 for j in range((B * (g + 1)) // G - B * g // G)] for g in range(G)]
     check(shared_inputs([(150 + 100 * (g % 3), n) for g, n in enumerate(own)], 2, 8, 2, 64, 16, dtype, 70 + G, True))
