@@ -122,8 +122,11 @@ __device__ __forceinline__ bool find_token(const RopeArgs& a, int64_t t, int& b,
 // `lg` lanes take a row (a power of two where a norm adds up over them), a warp `tb` tokens at once or one of `parts`
 // shares of a token's rows: those of its query heads, key heads and value heads.  (One loop for the three, whose sources
 // and places are picked per row: with a loop for each, a small call waited for its code, 320 tokens 17.8 us.)
+// CTAs per SM: as many as the registers allow without spills (norm, no cache, 33000 tokens of 8 heads of 128, us with 4
+// and 5: f32 53.7, 52.0, 16-byte bf16 accesses 30.9, 40.8).
+constexpr int rope_ctas(int V, bool norm, bool cache) { return norm && (cache || V == 8) ? 4 : 5; }
 template <typename E, int V, int IT, bool NEIGHBOURS, bool NORM, bool CACHE>
-__global__ void __launch_bounds__(NT, NORM ? 4 : 5) rope_kernel(RopeArgs a, int lg, int tb, int parts) {
+__global__ void __launch_bounds__(NT, rope_ctas(V, NORM, CACHE)) rope_kernel(RopeArgs a, int lg, int tb, int parts) {
     extern __shared__ __align__(16) float sm[];
     const int half = a.R >> 1, tid = threadIdx.x, warp = tid >> 5;
     uint64_t* turn_s = reinterpret_cast<uint64_t*>(sm);  // [half] frequencies, 2^-64 turns per position
@@ -238,6 +241,19 @@ __global__ void __launch_bounds__(NT, NORM ? 4 : 5) rope_kernel(RopeArgs a, int 
     int stage = 0;
     const float inv_d = 1.0f / (float)a.D;
     const uint32_t per_half = (65536 + half - 1) / half;  // e / half = e per_half / 65536 for e < 65536 / half
+    float2 wt[IT][V];  // the norm's weights of a lane's dims
+    auto weights = [&](int kind) {
+        const float* wr = w_s + (kind == 0 ? 0 : a.D);
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+            if (has[i])
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const float* wa = wr + (V == 1 ? off_a[i] : k < V / 2 ? off_a[i] + 2 * k : off_b[i] + 2 * k - V);
+                    wt[i][k] = V == 1 ? make_float2(wa[0], wr[off_b[i]]) : *reinterpret_cast<const float2*>(wa);
+                }
+    };
+    if (NORM && !CACHE) weights(0);
     for (int64_t item = item0; item < item1;) {
         int64_t first;
         int h0;
@@ -295,18 +311,7 @@ __global__ void __launch_bounds__(NT, NORM ? 4 : 5) rope_kernel(RopeArgs a, int 
             const int64_t skip = step * head;
             const bool there = member && grp < rw && (kind == 0 || row >= 0);
             const bool norm = (kind == 0 ? a.q_w : kind == 1 ? a.k_w : nullptr) != nullptr;
-            float2 wt[IT][V];
-            if (NORM && norm) {
-                const float* wr = w_s + (kind == 0 ? 0 : a.D);
-#pragma unroll
-                for (int i = 0; i < IT; ++i)
-                    if (has[i])
-#pragma unroll
-                        for (int k = 0; k < V; ++k) {
-                            const float* wa = wr + (V == 1 ? off_a[i] : k < V / 2 ? off_a[i] + 2 * k : off_b[i] + 2 * k - V);
-                            wt[i][k] = V == 1 ? make_float2(wa[0], wr[off_b[i]]) : *reinterpret_cast<const float2*>(wa);
-                        }
-            }
+            if (NORM && CACHE && norm) weights(kind);
 #pragma unroll 1
             for (int h = h0; h - grp < heads; h += step, to += skip) {
                 Vec<E, V> xa[IT], xb[IT];
@@ -390,7 +395,7 @@ cudaError_t launch_v(const RopeArgs& a, cudaStream_t s) {
     int64_t parts = 152 * 4 * NW / a.T;  // all warps at once
     parts = parts < 1 ? 1 : (parts > most ? most : parts);
     const bool norm = a.q_w != nullptr || a.k_w != nullptr;
-    const int ctas = 152 * (norm ? 4 : 5);  // resident at once: registers
+    const int ctas = 152 * rope_ctas(V, norm, a.k_cache != nullptr);  // resident at once
     const int64_t each = (a.T + ctas * NW - 1) / (ctas * NW);  // tokens of a warp
     const int tb = (int)(each < kTokens ? each : kTokens);
     int64_t blocks = (a.T * parts + NW - 1) / NW;
