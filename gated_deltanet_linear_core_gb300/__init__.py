@@ -630,13 +630,15 @@ def _rows(t, name, dev, dtype, T, D, H=None):
 
 def _rotation(inv_freq, positions, axes, T, D, dev):
     """Checked pointers of a rotation: (positions, n_axes, axes, inv_freq, R)."""
-    if inv_freq.dim() != 1 or not 1 <= inv_freq.shape[0] <= D // 2:
-        raise ValueError(f"inv_freq: shape {tuple(inv_freq.shape)}, expected [R / 2] with 2 <= R <= {D}")
-    half, n_axes = inv_freq.shape[0], 1
+    shape, n_axes = inv_freq.shape, 1
+    if len(shape) != 1 or not 1 <= shape[0] <= D // 2:
+        raise ValueError(f"inv_freq: shape {tuple(shape)}, expected [R / 2] with 2 <= R <= {D}")
+    half = shape[0]
     if positions is not None:
-        if positions.dim() not in (1, 2) or positions.shape[-1] != T:
-            raise ValueError(f"positions: shape {tuple(positions.shape)}, expected [{T}] or [n_axes, {T}]")
-        n_axes = positions.shape[0] if positions.dim() == 2 else 1
+        shape = positions.shape
+        if len(shape) not in (1, 2) or shape[-1] != T:
+            raise ValueError(f"positions: shape {tuple(shape)}, expected [{T}] or [n_axes, {T}]")
+        n_axes = shape[0] if len(shape) == 2 else 1
     return (_dptr(positions, "positions", dev, torch.int32), n_axes, _dptr(axes, "axes", dev, torch.int32, (half,)),
             _dptr(inv_freq, "inv_freq", dev, torch.float32), 2 * half)
 
@@ -653,17 +655,20 @@ def gdn_rope(x, inv_freq, positions, axes=None, norm_w=None, norm_eps=RMSNORM_EP
     if _elsewhere(dev, stream):
         return _on_stream(dev, stream, (x, inv_freq, positions, axes, norm_w, out),
                           lambda: gdn_rope(x, inv_freq, positions, axes, norm_w, norm_eps, mscale, interleaved, out))
-    if x.dim() != 3:
+    shape = x.shape
+    if len(shape) != 3:
         raise ValueError("x: expected [T, H, D]")
     if positions is None:
         raise ValueError("positions: needed")
-    T, H, D = x.shape
+    T, H, D = shape
     code = _dtype_code(x)
     p_x, x_tok, x_head = _rows(x, "x", dev, dt, T, D, H)
     p_pos, n_axes, p_axes, p_freq, R = _rotation(inv_freq, positions, axes, T, D, dev)
     if out is None:
-        out = torch.empty((T, H, D), dtype=dt, device=x.device)
-    p_out, o_tok, o_head = _rows(out, "out", dev, dt, T, D, H)
+        out = torch.empty(shape, dtype=dt, device=x.device)
+        p_out, o_tok, o_head = out.data_ptr(), H * D, D
+    else:
+        p_out, o_tok, o_head = _rows(out, "out", dev, dt, T, D, H)
     st = _lib.load().gdn_rope(
         p_x, x_tok, x_head, p_pos, n_axes, p_axes, p_freq, _dptr(norm_w, "norm_w", dev, torch.float32, (D,)), norm_eps,
         mscale, _lib.GDN_ROPE_INTERLEAVED if interleaved else 0, p_out, o_tok, o_head, T, H, D, R, code,
@@ -689,16 +694,17 @@ def gdn_rope_kv_append(q, k, v, k_cache, v_cache, page_table, seq_lens, inv_freq
                                                      axes, q_norm_w, k_norm_w, norm_eps, mscale, interleaved, cu_seqlens,
                                                      q_out))
     n_pages, H, ps, D, B, mp = _cache_dims(k_cache, v_cache, page_table, seq_lens)
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q: expected [T, H_q, D]")
-    T, H_q = q.shape[0], q.shape[1]
+    T, H_q = shape[0], shape[1]
     code = _dtype_code(q)
     p_q, q_tok, q_head = _rows(q, "q", dev, dt, T, D)
     p_k, k_tok, k_head = _rows(k, "k", dev, dt, T, D, H)
     p_v, v_tok, v_head = _rows(v, "v", dev, dt, T, D, H)
     p_pos, n_axes, p_axes, p_freq, R = _rotation(inv_freq, positions, axes, T, D, dev)
     if q_out is None:
-        q_out = torch.empty((T, H_q, D), dtype=dt, device=q.device)
+        q_out = torch.empty(shape, dtype=dt, device=q.device)
         p_o = q_out.data_ptr()
     else:
         p_o = _dptr(q_out, "q_out", dev, dt, (T, H_q, D))
@@ -798,9 +804,10 @@ def gdn_attn_decode_shared(q, k_cache, v_cache, page_table, seq_lens, prefix_len
     shape = q.shape
     if len(shape) != 4 or shape[0] != B or shape[3] != D:
         raise ValueError(f"q: shape {tuple(shape)}, expected [{B}, K, H_q, {D}]")
-    if prefix_lens.dim() != 1 or prefix_lens.shape[0] < 1 or (cu_groups is None and prefix_lens.shape[0] != 1):
-        raise ValueError(f"prefix_lens: shape {tuple(prefix_lens.shape)}, expected [G], [1] without cu_groups")
-    K, H_q, G = shape[1], shape[2], prefix_lens.shape[0]
+    ps_shape = prefix_lens.shape
+    if len(ps_shape) != 1 or ps_shape[0] < 1 or (cu_groups is None and ps_shape[0] != 1):
+        raise ValueError(f"prefix_lens: shape {tuple(ps_shape)}, expected [G], [1] without cu_groups")
+    K, H_q, G = shape[1], shape[2], ps_shape[0]
     code = _dtype_code(q)
     p_q = _dptr(q, "q", dev, dt)
     if out is None:
