@@ -614,9 +614,10 @@ attn_shared_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                 }
                 __syncwarp();
             }
-            if (st == 0) *odd_v = 0;
             tc_fence_before();
-            softmax_sync();  // O and the sums are free
+            softmax_sync();  // O, the sums and the flag are free
+            // (every warp has read the flag; none sets it again before it has met this thread at the next segment's barrier)
+            if (st == 0) *odd_v = 0;
         }
     }
     tc_fence_before();
