@@ -78,30 +78,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_
         "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(hi)
         : "memory");
 }
-// 64 consecutive columns, there when it returns: load and wait are one statement, because a register
-// that the compiler moved to memory between the two would not have its value yet.
-__device__ __forceinline__ void tmem_ld64_now(uint32_t taddr, float* v) {
-    uint32_t r[64];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
     asm volatile(
@@ -482,7 +458,7 @@ attn_shared_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                     float2 sum;
                     for (bool fits = j > 0;;) {
                         float x[64];
-                        tmem_ld64_now(ts, x);
+                        tmem_ld64(ts, x);
                         if (tail) {
                             const int upto = vis - (t0 + wg * 64);
 #pragma unroll
@@ -510,7 +486,6 @@ attn_shared_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                                 for (int c = wg * 64 * NDB; c < (wg + 1) * 64 * NDB; c += 32) {
                                     float o[32];
                                     tmem_ld32(tq + L::T_O + c, o);
-                                    tmem_wait_ld();
 #pragma unroll
                                     for (int i = 0; i < 32; ++i) o[i] *= f;
                                     tmem_st32(tq + L::T_O + c, o);
@@ -586,7 +561,6 @@ attn_shared_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             for (int c = wg * 64 * NDB; works && c < (wg + 1) * 64 * NDB && c < a.D; c += 32) {
                 float o[32];
                 tmem_ld32(tq + L::T_O + c, o);
-                tmem_wait_ld();
                 if (odd) {
                     const int upto = min(min(g.len, g.tile1 * TILE), vis);
 #pragma unroll 1

@@ -527,15 +527,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 for (int c = 0; c < CPT; c += CH) {
                     float o[CH];
                     const uint32_t to = tq + L::T_O + db * L::PARTS * N + c;
-                    tmem_ld<CH>(to, o);
                     if constexpr (L::PARTS == 2) {
                         float o2[CH];
-                        tmem_ld<CH>(to + N, o2);
-                        tmem_wait_ld();
+                        if constexpr (CH == 16) tmem_ld16_twice(to, o, to + N, o2); else tmem_ld32_twice(to, o, to + N, o2);
 #pragma unroll
                         for (int i = 0; i < CH; ++i) o[i] += o2[i];
                     } else {
-                        tmem_wait_ld();
+                        tmem_ld<CH>(to, o);
                     }
                     if (odd && db * 128 + row < a.D) {
                         const int t1 = min(s.len, s.tile1 * TILE);
@@ -615,7 +613,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     const uint32_t ts = tq + L::T_S + (it & 1) * N + c1;
                     float x[CH];  // scores in the log2 domain, less the running maximum
                     tmem_ld<CH>(ts, x);
-                    tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < CH; c += 4) {
                         const float4 n4 = *reinterpret_cast<const float4*>(n_s + c0 + c1 + c);
@@ -643,7 +640,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 #pragma unroll
                             for (int c = 0; c < CH; ++c) hidden |= (x[c] == -INFINITY ? 1u : 0u) << c;
                             tmem_ld<CH>(ts, x);
-                            tmem_wait_ld();
 #pragma unroll
                             for (int c = 0; c < CH; ++c) x[c] = hidden >> c & 1 ? -INFINITY : x[c] * a.scale_log2;
                         }
@@ -672,7 +668,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             for (int i = 0; i < NDB * L::PARTS; ++i) {
                                 float o[CH];
                                 tmem_ld<CH>(tq + L::T_O + i * N + c1, o);
-                                tmem_wait_ld();
 #pragma unroll
                                 for (int c = 0; c < CH; ++c) o[c] *= f_s[c0 + c1 + c];
                                 tmem_st<CH>(tq + L::T_O + i * N + c1, o);

@@ -591,18 +591,17 @@ chunk_intra_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         const bool isk = row < 64;
         const int i = row & 63, j0 = 32 * half;
         float d1[32];
-        tmem_ld32(tb + lo + TI_D1 + 32 * half, d1);
+        const uint32_t t1 = tb + lo + TI_D1 + 32 * half;
         // the warp whose 32 columns hold its rows' diagonal: l2-norm factors,
         // the row factors of W and the workspace vectors
         if (isk ? quarter == half : quarter - 2 == half) {
             float ss;
             if (isk) {
-                tmem_wait_ld();
+                tmem_ld32(t1, d1);
                 ss = select_lane(d1, lane);
             } else {
                 float dq[32];
-                tmem_ld32(tb + lo + TI_D1 + 64 + 32 * half, dq);
-                tmem_wait_ld();
+                tmem_ld32_twice(t1, d1, t1 + 64, dq);
                 ss = select_lane(dq, lane);
             }
             float f = isk ? 1.f : a.scale;
@@ -624,7 +623,7 @@ chunk_intra_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                 vec[i] = eg * f;
             }
         } else {
-            tmem_wait_ld();
+            tmem_ld32(t1, d1);
         }
         __syncthreads();
         {   // A (k rows -> shared, f32) and P (q rows -> workspace, fp16):
@@ -941,7 +940,6 @@ chunk_intra_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                 const int d0 = 32 * quarter + 16 * (q & 1), i0 = 32 * half + 16 * (q >> 1);
                 uint32_t r[8], p[4];
                 tmem_ld16x256b_x2(tb + ((uint32_t)d0 << 16) + col + 16 * (q >> 1), r);
-                tmem_wait_ld();
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     p[k] = acc == 0 ? pack_bf16x2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]))
@@ -1303,10 +1301,9 @@ chunk_chain_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
 #pragma unroll
                 for (int h16 = 0; h16 < CV; h16 += 16) {
                     float ws[16], up[16];
-                    tmem_ld16(tb + lo + Ly::T_QW + VS * b + c0 + h16, ws);
                     unpack8_h(*reinterpret_cast<const uint4*>(ut + sw128_off(j, cb + h16)), up);
                     unpack8_h(*reinterpret_cast<const uint4*>(ut + sw128_off(j, cb + h16 + 8)), up + 8);
-                    tmem_wait_ld();
+                    tmem_ld16(tb + lo + Ly::T_QW + VS * b + c0 + h16, ws);
 #pragma unroll
                     for (int q = 0; q < 16; ++q) up[q] -= ws[q];
                     store_row_h(up_op, j, cb + h16, up, 16);
@@ -1330,7 +1327,6 @@ chunk_chain_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                 }
                 float ds[CV];
                 tmem_ldn<CV>(tb + lo + Ly::T_DS + c0, ds);
-                tmem_wait_ld();
 #pragma unroll
                 for (int q = 0; q < CV; ++q) sv[q] = fmaf(eGn, sv[q], ds[q]);
                 store_row_bf16(s_op, lrow, cb, sv, CV);
@@ -1354,9 +1350,8 @@ chunk_chain_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
 #pragma unroll
                 for (int h16 = 0; h16 < CV; h16 += 16) {
                     float qs[16], po[16];
-                    tmem_ld16(tb + lo + Ly::T_QW + VS * b + c0 + h16, qs);
-                    tmem_ld16(tb + lo + Ly::T_OP + VS * (Ly::OPB == 2 ? b : 0) + c0 + h16, po);
-                    tmem_wait_ld();
+                    tmem_ld16_twice(tb + lo + Ly::T_QW + VS * b + c0 + h16, qs,
+                                    tb + lo + Ly::T_OP + VS * (Ly::OPB == 2 ? b : 0) + c0 + h16, po);
 #pragma unroll
                     for (int q = 0; q < 16; ++q) po[q] = fmaf(erq, qs[q], po[q]);
                     if (n == C) {

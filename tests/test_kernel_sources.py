@@ -22,3 +22,14 @@ def test_the_flag_of_odd_values_is_cleared_behind_a_barrier(name):
     assert len(reads) == 1 and len(clears) == 2  # the first clear comes before any segment
     assert clears[0] < reads[0] < clears[1]
     assert re.search(r"softmax_sync(<NSOFT>)?\(\);", text[reads[0]:clears[1]])
+
+
+@pytest.mark.parametrize("name", sorted(os.path.basename(p) for p in glob.glob(os.path.join(CSRC, "*.cu*"))))
+def test_loads_from_tensor_memory_wait_in_their_own_statement(name):
+    """Between two statements the compiler may move or use a register that does not have its value yet."""
+    for statement in re.findall(r"asm volatile\((.*?)\);", code(name), re.S):
+        loads = [m.start() for m in re.finditer(r"tcgen05\.ld\b", statement)]
+        waits = [m.start() for m in re.finditer(r"tcgen05\.wait::ld", statement)]
+        assert bool(loads) == bool(waits) and (not loads or loads[-1] < waits[-1])
+        if len(loads) > 1:  # a later load's address is not where an earlier one's values go
+            assert '"=&r"(r[0])' in statement
