@@ -545,8 +545,9 @@ gdn_status_t gdn_kv_append(const void* k, const void* v, void* k_cache, void* v_
  * dims from R on pass through.  With norm_w, before that,
  *   x <- x / sqrt(mean_d x_d^2 + eps) norm_w   (over all D dims of the head).
  * Several axes (time, height, width, ..) give images and video their positions:
- * axes says which one each pair turns with, in any order.  Angles are exact to about
- * 2^-50 of their size, however far the position is; arithmetic in f32, one rounding.
+ * axes says which one each pair turns with, in any order.  Before its cosine is taken in f32
+ * an angle p f is off by at most |p f| 2^-52 + |p| 2^-62 rad, however far the position is, and for
+ * bf16 by f32's rounding (2^-24 of what is left of it below half a turn); arithmetic in f32, one rounding.
  *   x          (device) [T, H, D] dtype, strides in elements between tokens and between heads
  *              (multiples of 16 bytes, not negative; ignored where there is one token, one head);
  *              the dims of a head are contiguous
