@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(NT, rope_ctas(V, NORM, CACHE)) rope_kernel(Rop
             in.h += step;
             in.x += in.skip;
             if (in.h - grp >= in.heads) {  // (the lanes of a warp go on together)
-                if (CACHE && in.kind + 1 < kinds) {
+                // (a share of a token's heads that has no key head has no rows of the later kinds: no stage, as below)
+                if (CACHE && in.kind + 1 < kinds && in.h0 - grp < a.H_kv) {
                     enter(in.kind + 1);
                 } else {
                     ++in.item;

@@ -77,3 +77,30 @@ def test_quarter_half_and_whole_turns(dtype):
     # (f32 frequencies are off the fractions by up to 2^-25 of them: the angles here are those of the f32 values)
     tol = 2.0 ** -22 + angle.abs() * 2.0 ** -51 + (2.0 ** -8 if dtype is BF else 0.0)
     assert bool(((s + torch.sin(angle)).abs() <= tol).all()) and bool(((c - torch.cos(angle)).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,D,R", [(16, 2, 256, 64), (7, 1, 72, 36), (5, 9, 24, 24), (64, 3, 16, 8)])
+def test_tokens_come_out_alike_however_many_warps_share_them(dtype, hq, hkv, D, R):
+    """A few tokens' heads are spread over warps, of which some have query heads and no key heads; of many
+    tokens a warp takes several whole ones: the same bits."""
+    g = torch.Generator().manual_seed(5)
+    most = 5000
+    q, k, v = (torch.randn((most, h, D), generator=g).to(dtype).cuda() for h in (hq, hkv, hkv))
+    w = [(1 + 0.1 * torch.randn(D, generator=g)).cuda() for _ in range(2)]
+    f = (1e4 ** (-torch.arange(R // 2, dtype=torch.float64) / (R // 2))).float().cuda()
+    pos = torch.arange(most, dtype=torch.int32, device="cuda") + 77
+    table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+
+    def run(T):
+        kc, vc = (torch.zeros((1, hkv, most, D), dtype=dtype, device="cuda") for _ in range(2))
+        lens = torch.tensor([T], dtype=torch.int32, device="cuda")
+        out = gdn.gdn_rope_kv_append(q[:T], k[:T], v[:T], kc, vc, table, lens, f, positions=pos[:T], q_norm_w=w[0], k_norm_w=w[1])
+        return out, kc, vc
+
+    out, kc, vc = run(most)
+    assert torch.equal(vc[0].transpose(0, 1), v)
+    for T in (1, 2, 3, 37, 151, 152, 153, 303, 608, 809, 1215, 1216, 1217, 2431, 2432, 2433, 3040, 3041):
+        o, kt, vt = run(T)
+        assert torch.equal(o, out[:T]) and torch.equal(kt[:, :, :T], kc[:, :, :T]) and torch.equal(vt[:, :, :T], vc[:, :, :T])
+        assert not kt[:, :, T:].any() and not vt[:, :, T:].any()
