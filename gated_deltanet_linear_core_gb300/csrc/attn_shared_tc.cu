@@ -45,6 +45,11 @@ constexpr int NSOFT = 256;
 // Half a tile's weights of a row add up to more than this where its running maximum is to be moved.  (The sum is there
 // anyway; looking for the largest score in each tile took a fifth of the arithmetic.)
 constexpr float kLarge = 4096.0f;
+// Scores of this size (log2) and beyond are a unit or more off by their own rounding, and so is a maximum of them: less it
+// in one multiply-add, scores as large as it would come out anywhere.  Rows with such a maximum take their scores rounded
+// as it is, at every tile.  (us before and with this: 64 sequences behind 32768 tokens 65.1, 64.4, 32 with 16 new tokens
+// behind 16384 154.4, 157.0; forms with fewer instructions per tile moved the two by as much, by the compiler's schedule.)
+constexpr float kHuge = 0x1p24f;
 
 template <int NDB>
 struct Layout {
@@ -447,6 +452,7 @@ attn_shared_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             const int vis = g.len > 0 ? g.len - (a.K - 1 - (g.r0 + row) / a.group) : 0, least = g.len - (a.K - 1);
             float m = kNone;                      // the row's running maximum
             float2 l = make_float2(0.f, 0.f);     // the sum of this warpgroup's tokens
+            bool plain = true;                    // none of the warp's rows has a huge maximum
             for (int j = 0; j < n; ++j) {
                 const uint32_t ts = tq + L::T_S + sb * TILE + wg * 64;
                 wait(&s_full[sb], s_phase);
@@ -456,7 +462,7 @@ attn_shared_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                 if (works) {
                     float w[64];  // of every 32 tokens 16 columns of upper parts, 16 of rests
                     float2 sum;
-                    for (bool fits = j > 0;;) {
+                    for (bool fits = j > 0 && plain;;) {
                         float x[64];
                         tmem_ld64(ts, x);
                         if (tail) {
@@ -479,6 +485,16 @@ attn_shared_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                             m = m1;
                             l.x *= f;
                             l.y *= f;
+                            plain = !__any_sync(0xffffffffu, fabsf(m) >= kHuge);  // (the same in the other warp)
+                            if (!plain) {
+                                l_s[wg * ROWS + row] = m;
+                                if (fabsf(m) >= kHuge) {
+                                    const float inv = 1.0f / a.scale_log2;
+#pragma unroll
+                                    for (int i = 0; i < 64; ++i) x[i] = (__fmul_rn(x[i], a.scale_log2) - m) * inv;
+                                    m = 0.f;  // until the weights are made
+                                }
+                            }
                             if (j > 0) {
                                 wait(&pv_done[last], last_phase);
                                 tc_fence_after();
@@ -512,6 +528,7 @@ attn_shared_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                         if (sure || !pair_any(quad, sum.x + sum.y > kLarge)) break;
                         fits = false;
                     }
+                    if (!plain) m = l_s[wg * ROWS + row];
                     l = __fadd2_rn(l, sum);
                     tmem_st32(ts, w);
                     tmem_st32(ts + 32, w + 32);

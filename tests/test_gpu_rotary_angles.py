@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import gated_deltanet_linear_core_gb300 as gdn
+import rotary_ref as rot
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +105,23 @@ def test_tokens_come_out_alike_however_many_warps_share_them(dtype, hq, hkv, D, 
         o, kt, vt = run(T)
         assert torch.equal(o, out[:T]) and torch.equal(kt[:, :, :T], kc[:, :, :T]) and torch.equal(vt[:, :, :T], vc[:, :, :T])
         assert not kt[:, :, T:].any() and not vt[:, :, T:].any()
+
+
+@pytest.mark.parametrize("T,H,D,R,n_axes,interleaved", [(130, 5, 72, 72, 3, False), (1000, 16, 80, 80, 3, False), (700, 3, 64, 64, 1, True),
+                                                        (99, 2, 128, 126, 2, True), (500, 4, 256, 64, 16, False), (9, 1, 8, 2, 1, False)])
+def test_f32_rotations_without_a_norm(T, H, D, R, n_axes, interleaved):
+    """The cosine and the sine are off by 1.5 steps of 2^-24 (see above) and are rounded once more with mscale; a
+    product and a sum round once each: (|a| + |b|) mscale 4.5 2^-24 in all, and the output is one of those roundings."""
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn((T, H, D), generator=g).cuda()
+    f = (1e4 ** (-torch.arange(R // 2, dtype=torch.float64) / (R // 2))).float().cuda()
+    pos = torch.randint(-30000, 30000, (n_axes, T), generator=g, dtype=torch.int32).cuda()
+    axes = torch.randint(0, n_axes, (R // 2,), generator=g, dtype=torch.int32).cuda()
+    for mscale in (1.0, 1.25, -0.7):
+        y = gdn.gdn_rope(x, f, pos, axes=axes, mscale=mscale, interleaved=interleaved).double()
+        want, _ = rot.rope(x, f, pos, axes, mscale=mscale, interleaved=interleaved)
+        j = torch.arange(R // 2, device="cuda")
+        a, b = (2 * j, 2 * j + 1) if interleaved else (j, j + R // 2)
+        size = (x[:, :, a].abs() + x[:, :, b].abs()).double() * abs(mscale) * 4.5 * 2.0 ** -24 + 1e-30
+        assert bool(((y - want)[:, :, a].abs() <= size).all()) and bool(((y - want)[:, :, b].abs() <= size).all())
+        assert torch.equal(y[:, :, R:], want[:, :, R:])

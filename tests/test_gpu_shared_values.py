@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import gated_deltanet_linear_core_gb300 as gdn
+import serving_ref as ref
 from test_gpu_shared import BF, F, INF, NAN, shared_inputs
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +36,44 @@ def test_non_finite_new_tokens_reach_every_row_that_sees_them(D, hkv):
         out = gdn.gdn_attn_decode_shared(**x)
         assert torch.equal(~torch.isfinite(out), want)
         assert torch.equal(out[~want], clean[~want])
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D,hq,hkv", [(64, 8, 2), (256, 16, 2), (128, 64, 4)])
+@pytest.mark.parametrize("low", [-INF, -1e30, -1e4])
+@pytest.mark.parametrize("pages,gone", [(64, 64), (64, 32), (64, 1), (1250, 700)])
+def test_keys_far_out_of_sight_leave_the_rest(pages, gone, low, D, hq, hkv, dtype):
+    """The first `gone` of the prefix's pages of 16 hold keys whose scores are -inf, or finite and so low that their
+    weights vanish in 64 bits as well: what remains is attention over the tokens behind them."""
+    x = shared_inputs([(16 * pages, [9, 60, 200, 140])], 2, hq, hkv, D, 16, dtype, 8)
+    x["q"] = x["q"].abs() + 0.5
+    x["k_cache"][x["page_table"][0, :gone].long()] = low
+    out, lse = gdn.gdn_attn_decode_shared(**x, return_lse=True)
+    rest = ref.attention(x["q"], x["k_cache"], x["v_cache"], x["page_table"][:, gone:].contiguous(), x["seq_lens"] - 16 * gone)
+    ref.check_attention(out, lse, rest, dtype)
+    del x["prefix_lens"], x["cu_groups"]
+    ref.check_attention(*gdn.gdn_attn_decode(**x, return_lse=True), rest, dtype)
+
+
+def alike(shift, dtype, n=20000):
+    """Inputs whose rows' scores are each the same number, the outputs and the log of the count, and what the outputs
+    may be off by.  (The queries are powers of two and one dim of the keys holds the number: the products are exact.)"""
+    x = shared_inputs([(n, [9, 60, 200, 140])], 3, 8, 2, 64, 16, dtype, 9)
+    x["k_cache"].zero_()
+    x["q"] = torch.pow(2.0, torch.randint(-3, 4, x["q"].shape, generator=torch.Generator().manual_seed(1)).float()).to(dtype).cuda()
+    want, count, _ = ref.attention(x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"])
+    x["k_cache"][..., 5] = shift
+    # the weights as in ref.attention(), where scores of 0 are exact: 2 (2^-21 + 2^-16 + (n / 128 + 256) 2^-24) |v|
+    err = 2 * (2.0 ** -21 + 2.0 ** -16 + (n / 128 + 258) * 2.0 ** -24) * x["v_cache"].double().nan_to_num().abs().max()
+    score = x["q"][..., 5].double() * x["k_cache"][0, 0, 0, 5].double() / 8
+    return x, want, score + count, ref.HALF_STEP[dtype] * want.abs() + err, 2.0 ** -20 * (1 + score.abs()) + 1e-4
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shift", [-3e35, -1e30, -1e12, -3e7, 1e5, 3e7, 1e12, 1e30, 3e35])
+def test_scores_that_are_alike_and_large(shift, dtype):
+    """However large: the weights are all 1 / n, over many tiles."""
+    x, want, want_lse, tol, lse_tol = alike(shift, dtype)
+    out, lse = gdn.gdn_attn_decode_shared(**x, return_lse=True)
+    assert bool(((out.double() - want).abs() <= tol).all())
+    assert bool(((lse.double() - want_lse).abs() <= lse_tol).all())
