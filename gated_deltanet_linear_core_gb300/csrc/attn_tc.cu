@@ -46,6 +46,11 @@ namespace {
 using namespace attn;
 using namespace tc;
 
+// A row's first scores are rounded before its maximum is taken off, later ones in the same multiply-add: that is a
+// difference of 2^-24 of the maximum, which for very large ones is more than the weights.  Rows with a maximum (log2) beyond
+// this take every tile's scores as the first's.
+constexpr float kHuge = 4096.0f;
+
 template <int N, int NDB>
 struct Layout {
     // Columns (rows of Q) per softmax thread and per TMEM access, chosen by time: 128 rows of head dim 256 took 222 us
@@ -601,6 +606,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             softmax_sync<NSOFT>();
 #pragma unroll
             for (int c = 0; c < CPT; ++c) l[c] = 0.f;
+            bool huge = false;  // a maximum is: scores as large as it, less it in one multiply-add, come out anywhere
             const int least = visible(a, s.len, r0);  // what the block's first row sees
             for (int j = s.tile0; j < s.tile1; ++j, ++it) {
                 const int t0 = j * TILE;
@@ -629,7 +635,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     float top = x[0];
 #pragma unroll
                     for (int c = 1; c < CH; ++c) top = fmaxf(top, x[c]);
-                    if (first || group_any(wg, top > kSlack)) {
+                    if (first || group_any(wg, top > kSlack || huge)) {
                         // ---- new maxima; sums and outputs so far are scaled to them
                         if (!first) wait(&pv_done[(it - 1) & 1], (it - 1) >> 1);
                         tc_fence_after();
@@ -660,7 +666,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         }
                         group_sync(wg);
 #pragma unroll
-                        for (int c = 0; c < CH; ++c) x[c] += n_s[c0 + c1 + c];
+                        for (int c = 0; c < CH; ++c) {
+                            const float n1 = n_s[c0 + c1 + c];
+                            huge = huge || (fabsf(n1) >= kHuge && n1 != -kNone);
+                            x[c] += n1;
+                        }
                         if (!first) {
 #pragma unroll
                             for (int c = 0; c < CH; ++c) l[c1 + c] *= f_s[c0 + c1 + c];

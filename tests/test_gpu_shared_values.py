@@ -71,9 +71,35 @@ def alike(shift, dtype, n=20000):
 
 @pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
 @pytest.mark.parametrize("shift", [-3e35, -1e30, -1e12, -3e7, 1e5, 3e7, 1e12, 1e30, 3e35])
-def test_scores_that_are_alike_and_large(shift, dtype):
-    """However large: the weights are all 1 / n, over many tiles."""
+@pytest.mark.parametrize("shared", [True, False])
+def test_scores_that_are_alike_and_large(shared, shift, dtype):
+    """However large: the weights are all 1 / n, over many tiles; and so in gdn_attn_decode."""
     x, want, want_lse, tol, lse_tol = alike(shift, dtype)
-    out, lse = gdn.gdn_attn_decode_shared(**x, return_lse=True)
+    if shared:
+        out, lse = gdn.gdn_attn_decode_shared(**x, return_lse=True)
+    else:
+        del x["prefix_lens"], x["cu_groups"]
+        out, lse = gdn.gdn_attn_decode(**x, return_lse=True)
     assert bool(((out.double() - want).abs() <= tol).all())
     assert bool(((lse.double() - want_lse).abs() <= lse_tol).all())
+
+
+@pytest.mark.parametrize("K,hq,hkv,D", [(1, 8, 8, 64), (3, 16, 2, 64), (8, 8, 2, 128), (16, 16, 2, 256), (16, 16, 2, 64), (1, 48, 1, 256)])
+@pytest.mark.parametrize("shift", [-1e30, 1e12, 1e30])
+def test_large_scores_at_every_number_of_rows(shift, K, hq, hkv, D):
+    """gdn_attn_decode's forms for 16 to 128 rows: alternate rows have huge scores that are alike, and ordinary ones."""
+    x = shared_inputs([(3000, [16, 60])], K, hq, hkv, D, 16, BF, 10, hidden=0.0)
+    del x["prefix_lens"], x["cu_groups"]
+    x["q"][:, :, ::2] = 0
+    x["q"][:, :, ::2, 5] = 2.0
+    x["k_cache"][..., 5] = 0
+    want, lse, bound = ref.attention(**{k: x[k] for k in ("q", "k_cache", "v_cache")}, table=x["page_table"], lens=x["seq_lens"])
+    x["q"][:, :, 1::2, 5] = 0
+    want[:, :, 1::2], lse[:, :, 1::2], bound[:, :, 1::2] = (
+        t[:, :, 1::2] for t in ref.attention(x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"]))
+    x["k_cache"][..., 5] = shift
+    score = torch.zeros_like(lse)
+    score[:, :, ::2] = 2 * x["k_cache"][0, 0, 0, 5].double() * D ** -0.5
+    out, e = gdn.gdn_attn_decode(**x, return_lse=True)
+    assert bool(((out.double() - want).abs() <= ref.HALF_STEP[BF] * want.abs() + bound).all())
+    assert bool(((e.double() - lse - score).abs() <= 2.0 ** -20 * (1 + score.abs() + lse.abs()) + 1e-4).all())
