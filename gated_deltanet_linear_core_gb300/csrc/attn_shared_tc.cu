@@ -646,18 +646,12 @@ cudaError_t launch_shared_tc(const ShareArgs& s, int n_cta, cudaStream_t st) {
     return s.a.D <= 128 ? launch_ndb<1, false>(s, n_cta, piece, st) : launch_ndb<2, false>(s, n_cta, piece, st);
 }
 
-cudaError_t read_and_clear_shared_error(cudaStream_t s, int* flags) {
-    int hf = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&hf, g_shared_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) return e;
-    *flags = hf;
-    if (hf != 0) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_shared_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    }
-    return e;
+cudaError_t copy_shared_error(cudaStream_t s, int* word) {
+    return cudaMemcpyFromSymbolAsync(word, g_shared_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+}
+cudaError_t clear_shared_error(cudaStream_t s) {
+    const int zero = 0;
+    return cudaMemcpyToSymbolAsync(g_shared_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
 }
 
 }  // namespace gdn

@@ -791,18 +791,12 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int n_cta, cudaStream_t s) {
     return e != cudaSuccess ? e : launch_attn_join(a, n_cta, GDN_BF16, s);
 }
 
-cudaError_t read_and_clear_attn_error(cudaStream_t s, int* flags) {
-    int hf = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&hf, g_attn_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) return e;
-    *flags = hf;
-    if (hf != 0) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_attn_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    }
-    return e;
+cudaError_t copy_attn_error(cudaStream_t s, int* word) {
+    return cudaMemcpyFromSymbolAsync(word, g_attn_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+}
+cudaError_t clear_attn_error(cudaStream_t s) {
+    const int zero = 0;
+    return cudaMemcpyToSymbolAsync(g_attn_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
 }
 
 }  // namespace gdn

@@ -1634,18 +1634,12 @@ cudaError_t launch_bounded_wait_selftest(uint64_t limit_ns, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t read_and_clear_device_error(cudaStream_t s, int* flags) {
-    int hf = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&hf, g_device_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) return e;
-    *flags = hf;
-    if (hf != 0) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_device_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    }
-    return e;
+cudaError_t copy_device_error(cudaStream_t s, int* word) {
+    return cudaMemcpyFromSymbolAsync(word, g_device_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+}
+cudaError_t clear_device_error(cudaStream_t s) {
+    const int zero = 0;
+    return cudaMemcpyToSymbolAsync(g_device_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
 }
 
 }  // namespace gdn

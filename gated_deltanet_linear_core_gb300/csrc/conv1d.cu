@@ -314,18 +314,12 @@ cudaError_t conv_fwd_t(const ConvArgs& args, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t read_and_clear_conv_error(cudaStream_t s, int* flags) {
-    int hf = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&hf, g_conv_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) return e;
-    *flags = hf;
-    if (hf != 0) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_conv_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    }
-    return e;
+cudaError_t copy_conv_error(cudaStream_t s, int* word) {
+    return cudaMemcpyFromSymbolAsync(word, g_conv_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+}
+cudaError_t clear_conv_error(cudaStream_t s) {
+    const int zero = 0;
+    return cudaMemcpyToSymbolAsync(g_conv_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
 }
 
 cudaError_t launch_conv1d_fwd(const ConvArgs& a, gdn_dtype_t dt, cudaStream_t s) {

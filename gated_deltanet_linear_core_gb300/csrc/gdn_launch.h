@@ -142,11 +142,13 @@ bool chunk_split_static_fits(int n_seq, int H_v);
 cudaError_t launch_chunk_split_static(const DeltaArgs& a, cudaStream_t s);
 
 // Reads (synchronising `s`) and clears the library's device error word.
-cudaError_t read_and_clear_device_error(cudaStream_t s, int* flags);
+cudaError_t copy_device_error(cudaStream_t s, int* word);
+cudaError_t clear_device_error(cudaStream_t s);
 // One CTA whose bounded wait runs out after limit_ns and sets the error word.
 cudaError_t launch_bounded_wait_selftest(uint64_t limit_ns, cudaStream_t s);
 // The same for the conv kernels' own error word.
-cudaError_t read_and_clear_conv_error(cudaStream_t s, int* flags);
+cudaError_t copy_conv_error(cudaStream_t s, int* word);
+cudaError_t clear_conv_error(cudaStream_t s);
 
 cudaError_t launch_rmsnorm_gated(const void* o, const void* z, const void* w, float eps, int64_t T,
                                  int H, int D, void* out, gdn_dtype_t dt, cudaStream_t s);
@@ -187,7 +189,8 @@ cudaError_t launch_attn_ffma(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaS
 // The tensor-core kernel: which calls it takes, and its launch with the join.
 bool attn_tc_takes(const AttnArgs& a, gdn_dtype_t dt);
 cudaError_t launch_attn_tc(const AttnArgs& a, int n_cta, cudaStream_t s);
-cudaError_t read_and_clear_attn_error(cudaStream_t s, int* flags);
+cudaError_t copy_attn_error(cudaStream_t s, int* word);
+cudaError_t clear_attn_error(cudaStream_t s);
 cudaError_t launch_attn_join(const AttnArgs& a, int n_cta, gdn_dtype_t dt, cudaStream_t s);
 
 // Attention behind shared prefixes (gdn_attn_decode_shared; attn_shared.cuh).
@@ -220,7 +223,8 @@ size_t attn_share_plan(ShareArgs& s, gdn_dtype_t dt, void* ws);
 cudaError_t launch_attn_shared(const ShareArgs& s, gdn_dtype_t dt, cudaStream_t st);
 cudaError_t launch_shared_tc(const ShareArgs& s, int n_cta, cudaStream_t st);
 cudaError_t launch_prefix_ffma(const ShareArgs& s, int n_cta, gdn_dtype_t dt, cudaStream_t st);
-cudaError_t read_and_clear_shared_error(cudaStream_t s, int* flags);
+cudaError_t copy_shared_error(cudaStream_t s, int* word);
+cudaError_t clear_shared_error(cudaStream_t s);
 
 // New keys and values into their pages (gdn_kv_append).
 struct KvAppendArgs {
