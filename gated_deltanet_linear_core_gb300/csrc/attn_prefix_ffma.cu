@@ -172,6 +172,14 @@ __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncthreads();
             // ---- O += P V: rows 4 ty .., dims 2 tx + 32 ..
+            // A tile's products are added up by themselves: one sum over the thousands of tokens that a CTA takes of a long
+            // prefix was 1.3e-6 off (rms; 8 key-value heads of 16 behind 105570 tokens), three times as far as the plain
+            // form's (9 sequences in 2 groups 38.5 -> 38.9 us).
+            float2 sum[4][NC];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) sum[i][c] = make_float2(0.f, 0.f);
             auto outputs = [&](int t, bool tails) {
                 const float4 p = ld4(p_s + t * PS + 4 * ty);
                 const float w[4] = {p.x, p.y, p.z, p.w};
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
                     const float2 v = ld2(v_s + t * KS + 32 * c + 2 * tx);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)  // a hidden value may be anything: a weight of 0 must not meet it
-                        if (!tails || j * TT + t < vis[i]) o[i][c] = __ffma2_rn(make_float2(w[i], w[i]), v, o[i][c]);
+                        if (!tails || j * TT + t < vis[i]) sum[i][c] = __ffma2_rn(make_float2(w[i], w[i]), v, sum[i][c]);
                 }
             };
             if (works && tail) {
@@ -190,6 +198,10 @@ __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
 #pragma unroll 4
                 for (int t = 0; t < TT; ++t) outputs(t, false);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) o[i][c] = __fadd2_rn(o[i][c], sum[i][c]);
             __syncthreads();
         }
         // ---- the rows' part

@@ -103,3 +103,16 @@ def test_large_scores_at_every_number_of_rows(shift, K, hq, hkv, D):
     out, e = gdn.gdn_attn_decode(**x, return_lse=True)
     assert bool(((out.double() - want).abs() <= ref.HALF_STEP[BF] * want.abs() + bound).all())
     assert bool(((e.double() - lse - score).abs() <= 2.0 ** -20 * (1 + score.abs() + lse.abs()) + 1e-4).all())
+
+
+@pytest.mark.parametrize("hq,hkv,D,n", [(16, 8, 16, 105570), (14, 7, 64, 90000), (8, 4, 128, 70000), (8, 2, 256, 60000)])
+def test_f32_sums_over_long_prefixes(hq, hkv, D, n):
+    """A rounding of f32 is off by 2.5e-8 of the value (rms).  A sum of n terms of either sign: 2.5e-8 sqrt(n / 2), as its
+    parts are smaller before.  Of a tile's 64 tokens 1.4e-7, of the up to 90 tiles that a CTA has 1.7e-7, of D products
+    in a score at most 2.8e-7 of it (D = 256; as many parts as a thread holds are added up apart), of sums of weights
+    below these; the weights' exponentials 5e-8, averaged over.  Together 3.6e-7; twice that."""
+    x = shared_inputs([(n, [9, 60, 200, 140, 33])], 1, hq, hkv, D, 16, F, 21)
+    out, lse = gdn.gdn_attn_decode_shared(**x, return_lse=True)
+    want, want_lse, _ = ref.attention(x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"])
+    assert float((out.double() - want).norm() / want.norm()) <= 7.2e-7
+    assert float((lse.double() - want_lse).norm() / want_lse.norm()) <= 2e-7
