@@ -5,8 +5,10 @@
 // 64 query rows of a group that share a key-value head against tiles of 64 cached
 // tokens in shared memory; a thread holds 4 x 4 scores, then 4 rows of D / 16 outputs, a warp 8 rows (none of them
 // real: it computes nothing).  V of a tile lands beside its scores, K of the next one beside its
-// outputs.  Bound by the products (f32 fused multiply-adds) and what feeds them from shared memory: 9 sequences of 15
-// rows per head in 2 groups behind 100 to 5000 tokens 33 us (46 with the copies between the products and all rows computed).
+// outputs.  Bound by latency: two warps per scheduler issue in 34 to 39 % of the clocks, 5 to 6 clocks a warp and
+// instruction, of which 1.5 are the pipes', 0.6 to 1.0 barriers, 0.7 reads of shared memory (whose path is 34 to 54 %
+// busy).  9 sequences of 15 rows per head in 2 groups behind 100 to 5000 tokens 39 us a call (the kernel 33 of
+// them before a tile's products had sums of their own, and 46 with the copies between the products and all rows computed).
 #include "attn_shared.cuh"
 #include "tc_ptx.cuh"
 
@@ -173,8 +175,8 @@ __global__ void __launch_bounds__(NT, 1) attn_prefix_ffma_kernel(ShareArgs s) {
             __syncthreads();
             // ---- O += P V: rows 4 ty .., dims 2 tx + 32 ..
             // A tile's products are added up by themselves: one sum over the thousands of tokens that a CTA takes of a long
-            // prefix was 1.3e-6 off (rms; 8 key-value heads of 16 behind 105570 tokens), three times as far as the plain
-            // form's (9 sequences in 2 groups 38.5 -> 38.9 us).
+            // prefix was 1.3e-6 off (rms; 8 key-value heads of 16 behind 105570 tokens), three times as far as a
+            // library's product in 32 bits (9 sequences in 2 groups 38.5 -> 38.9 us).
             float2 sum[4][NC];
 #pragma unroll
             for (int i = 0; i < 4; ++i)

@@ -249,7 +249,8 @@ size_t attn_share_plan(ShareArgs& s, gdn_dtype_t dt, void* ws) {
     const bool tc = attn_tc_takes(a, dt);
     // On CUDA cores what sequences with few rows have of their own is gdn_attn_decode's kernel's, which spreads a tile's
     // tokens over all warps (us with records, with that kernel: 5 sequences of up to 900 tokens, 48 rows, head dim 16 21.8,
-    // 53.7; 9 of 15 rows, head dim 80, 41, 49; 13 of 10 rows, head dim 256, 63, 54).
+    // 53.7; 9 of 15 rows, head dim 80, 41, 49; 13 of 10 rows, head dim 256, 63, 54; bf16 in pages of 18: 9 of 8 rows, head dim
+    // 128, 50, 48, of 24 rows 43, 50; 48 of 8 rows, head dim 256, 134, 105; 13 of 32 rows 74, 91).
     const bool own = tc || a.rows > (a.D <= 128 ? kAttnFfmaRows : 2 * kAttnFfmaRows);
     s.records = s.G + (own ? a.B : 0);
     s.few = a.B + s.G <= 32 && s.G <= kFewGroups;

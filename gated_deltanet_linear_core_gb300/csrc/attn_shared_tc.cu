@@ -17,10 +17,10 @@
 // of the output's own rounding, and without the second the call takes 7 % less.  S runs one
 // tile ahead of P V (two up to head dim 128), so the weights of a tile are made beside the products of another.
 //
-// Measured: 32 sequences with 16 new tokens (4096 rows per head, head dim 128) behind 16384 tokens 134 us, 2250 clocks
-// a tile where its MMAs take 1540 (the softmax, 1630 clocks a tile, half of them waits that its 8 warps spend together, and
-// the hand-overs); 64 sequences behind 32768 tokens (512 rows, head dim 256) 55 us, 18 tiles and 1.7 segments per
-// CTA of which the MMAs take 28.  Tried, no faster: the warpgroups on tiles in turns (164 and 76 us per call for 152 and 65),
+// Measured: 32 sequences with 16 new tokens (4096 rows per head, head dim 128) behind 16384 tokens 156 us a call, 147 of them
+// (cold, alone) this kernel, some 2250 clocks a tile where its MMAs take 1540 (the softmax, 1630 clocks a tile, half of them
+// waits that its 8 warps spend together, and the hand-overs); 64 sequences behind 32768 tokens (512 rows, head dim 256)
+// 64 us a call, 58 (cold) this kernel: 18 tiles and 1.7 segments per CTA, of which the MMAs take 28.  Tried, no faster: the warpgroups on tiles in turns (164 and 76 us per call for 152 and 65),
 // waits that sleep longer or poll, no search for the maximum.
 //
 // Warps: 0 walks the CTA's range, tells the others its segments, and loads K and V (of

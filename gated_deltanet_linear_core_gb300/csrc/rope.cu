@@ -12,8 +12,9 @@
 // 163 us, in blocks with barriers as well.
 //
 // Measured: those 121 us (691 MB, 84 % of the copy bandwidth; 76 M warp instructions; 131 with batches of tokens dealt to the
-// warps in turns, of which some got one more); 32760 patches of 16 heads of 80 out of a fused projection 34 us (168 MB,
-// 72 %; issue: 18 M warp instructions, 25 M and 37 us with the cache's part in the same code).
+// warps in turns, of which some got one more); 32760 patches of 16 heads of 80 out of a fused projection 35 us (168 MB,
+// 71 %; issue 52 %, 19 warps per SM that wait 2.1 of their 9.1 clocks an instruction for loads, positions among them, and 1.2 for
+// shared memory: none of the three is full; 18 M warp instructions, 25 M and 37 us with the cache's part in the same code).
 //
 // The angle of a far position keeps no digits in f32: p f is held in turns, as a 64-bit
 // fraction of one turn (f / 2 pi in f64, times 2^64), whose product with the integer p drops whole
